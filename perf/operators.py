@@ -247,7 +247,9 @@ def _prepare_bwd(case, g):
         s["w_absmax"] = 0.05 + 0.02 * torch.rand(nb, generator=g, device=DEV)
     keep = None
     if case["p"]:
-        keep = torch.rand((M, K), generator=g, device=DEV) >= case["p"]
+        # the mask of the forward's dropout (p, seed), as the forward stores it
+        s["seed"] = int(torch.randint(0, 1 << 62, (1,), generator=g, device=DEV))
+        keep = _keep(M * K, case["p"], s["seed"]).view(M, K)
         bit = torch.tensor([1 << i for i in range(8)], device=DEV, dtype=torch.int32)
         s["bits"] = (keep.view(-1, 8).int() * bit).sum(1).to(torch.uint8)
     # the forward's X A^T, from the input it had before the checkpoint
@@ -255,6 +257,25 @@ def _prepare_bwd(case, g):
     s["XA"] = (xd @ A.float().T).to(bf)
     s["codes"], s["scale"] = _act8(x)
     return s
+
+
+def _keep(n, p, seed):
+    """Keep flags of n elements (n % 4 == 0): Philox4x32-10 words of counters
+    0 .. n / 4 - 1 under the seed's two halves, kept at floor(p 2^32) or more."""
+    low = 0xFFFFFFFF
+    c0 = torch.arange(n // 4, device=DEV)
+    c1, c2, c3 = c0 >> 32, torch.zeros_like(c0), torch.zeros_like(c0)
+    c0, k0, k1 = c0 & low, seed & low, seed >> 32
+
+    def product(a, x):      # high and low 32 bits of a x, both below 2^32
+        return (a * (x >> 16) + ((a * (x & 0xFFFF)) >> 16)) >> 16, (a * x) & low
+
+    for _ in range(10):
+        h0, l0 = product(0xD2511F53, c0)
+        h1, l1 = product(0xCD9E8D57, c2)
+        c0, c1, c2, c3 = h1 ^ c1 ^ k0, l1, h0 ^ c3 ^ k1, l0
+        k0, k1 = (k0 + 0x9E3779B9) & low, (k1 + 0xBB67AE85) & low
+    return torch.stack((c0, c1, c2, c3), 1).view(-1) >= math.floor(p * 2 ** 32)
 
 
 def _diagonal(rows, r):
@@ -417,7 +438,7 @@ def _framework(s):
         else:
             dX, dA, dB = q.qlora_linear_bwd_act8(
                 W, a, s["A"], s["B"], s["alpha"], s["dY"], s["XA"], need_dx=c["dx"],
-                dropout=(c["p"], 0) if c["p"] else None, keep_bits=s.get("bits"))
+                dropout=(c["p"], s["seed"]) if c["p"] else None, keep_bits=s.get("bits"))
         return {"dA": dA, "dB": dB, "dX": dX} if c["dx"] else {"dA": dA, "dB": dB}
     if op == "logprob":
         if not c["grad"]:
