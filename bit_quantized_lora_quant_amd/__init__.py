@@ -8,6 +8,7 @@ every call raises.
 """
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -33,11 +34,18 @@ EXPORTS = [
     "qlora_adamw_step", "qlora_adamw8_step", "qlora_host_state_alloc", "qlora_host_state_free",
     "qlora_merge_workspace_bytes", "qlora_merge_requantize",
     "qlora_grouped_workspace_bytes", "qlora_grouped_fwd", "qlora_grouped_bwd",
+    "qlora_act8_quantize", "qlora_act8_dequantize", "qlora_linear_act8_workspace_bytes",
+    "qlora_linear_bwd_act8", "qlora_grouped_bwd_act8",
+    "qlora_loss_workspace_bytes", "qlora_token_logprobs", "qlora_token_logprobs_bwd",
+    "qlora_preference_loss", "qlora_policy_loss",
     "qlora_trace_begin", "qlora_trace_pause", "qlora_trace_end",
 ]
 KERNELS = {"fwd_gemm": 0, "dx_gemm": 1, "quantize": 2, "dequant": 3, "gemv": 4,
            "split_reduce": 5, "adamw": 6, "adamw8": 7}
 ADAMW8_BLOCK = 256
+ACT8_BLOCK = 64
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}      # QLORA_PREF_*
+POLICY_REDUCTIONS = {"token": 0, "sequence": 1}              # QLORA_POLICY_*
 
 
 class QloraError(RuntimeError):
@@ -76,6 +84,28 @@ class AdamW8Tensor(ctypes.Structure):
 class AdamWHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double)]
+
+
+class Act8Descriptor(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
+class LogitsDescriptor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("reserved", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("labels", ctypes.c_void_p)]
+
+
+class PreferenceParams(ctypes.Structure):
+    _fields_ = [("beta", ctypes.c_double), ("label_smoothing", ctypes.c_double),
+                ("kind", ctypes.c_int32), ("length_mean", ctypes.c_int32)]
+
+
+class PolicyParams(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+                ("kl_coef", ctypes.c_double), ("reduction", ctypes.c_int32),
+                ("token_advantages", ctypes.c_int32)]
 
 
 _lib = None
@@ -129,6 +159,22 @@ def lib():
         L.qlora_merge_workspace_bytes.restype = SZ
         L.qlora_merge_workspace_bytes.argtypes = [I64, I64]
         L.qlora_merge_requantize.argtypes = [D, P, P, I32, F, D, P, P, SZ, P]
+        A8 = ctypes.POINTER(Act8Descriptor)
+        Z = ctypes.POINTER(LogitsDescriptor)
+        L.qlora_act8_quantize.argtypes = [P, A8, P]
+        L.qlora_act8_dequantize.argtypes = [A8, ctypes.c_int, P, P]
+        L.qlora_linear_act8_workspace_bytes.argtypes = [I64, I64, I64, I32]
+        L.qlora_linear_act8_workspace_bytes.restype = SZ
+        L.qlora_linear_bwd_act8.argtypes = [D, A8, P, P, I32, F, P, P, P, P, P, P, P, P, SZ, P]
+        L.qlora_grouped_bwd_act8.argtypes = [D, A8, P, P, I32, I32, P, F, P, P, P, P, P, P, SZ, P]
+        L.qlora_loss_workspace_bytes.argtypes = [Z, I32]
+        L.qlora_loss_workspace_bytes.restype = SZ
+        L.qlora_token_logprobs.argtypes = [Z, P, P, P, SZ, P]
+        L.qlora_token_logprobs_bwd.argtypes = [Z, P, P, P, P, I64, P]
+        L.qlora_preference_loss.argtypes = [Z, I32, P, P, ctypes.POINTER(PreferenceParams), P, P,
+                                            P, P, P, P, P, I64, P, SZ, P]
+        L.qlora_policy_loss.argtypes = [Z, I32, P, P, P, P, ctypes.POINTER(PolicyParams), P, P, P,
+                                        P, P, I64, P, SZ, P]
         L.qlora_host_state_alloc.argtypes = [SZ, P]
         L.qlora_host_state_free.argtypes = [P]
         L.qlora_trace_begin.argtypes = [ctypes.c_uint32, I32]
@@ -675,6 +721,319 @@ def adamw8_states(numels, device, hbm_budget: int = None):
     return [AdamW8State(n, device, host=h) for n, h in zip(numels, host)]
 
 
+def _require(ok, what: str):
+    """Refuses arguments the library cannot check itself (a host tensor's
+    address, a tensor too short) the way it refuses the others."""
+    if not ok:
+        raise QloraError(QLORA_ERR_INVALID_ARG, what)
+
+
+def _on(what: str, first, *more):
+    """All given tensors are on one GPU; the calls run on that GPU's current
+    stream, whichever device is the current one."""
+    _require(first.is_cuda, what + ": tensors must be on a GPU")
+    for t in more:
+        _require(t is None or t.device == first.device, what + ": tensors on different devices")
+    return torch.cuda.device(first.device)
+
+
+class Act8Tensor:
+    """Activations [rows, cols] kept in 8 bits: int8 codes and a float32 scale
+    per 64 values of a row ([cols / 64, rows up to a multiple of 32]).  Buffers
+    owned by torch; existing ones can be handed in."""
+
+    def __init__(self, rows: int, cols: int, device=None, codes=None, scale=None):
+        _require(rows >= 0 and cols > 0 and cols % ACT8_BLOCK == 0,
+                 "Act8Tensor: cols must be a multiple of %d" % ACT8_BLOCK)
+        self.rows, self.cols = rows, cols
+        if codes is None:
+            codes = torch.empty((rows, cols), dtype=torch.int8, device=device)
+        kept = (cols // ACT8_BLOCK, (rows + 31) // 32 * 32)
+        if scale is None:
+            scale = torch.empty(kept, dtype=torch.float32, device=codes.device)
+        _require(codes.dtype == torch.int8 and codes.shape == (rows, cols) and
+                 codes.is_contiguous(), "Act8Tensor: codes must be contiguous int8 [rows, cols]")
+        _require(scale.dtype == torch.float32 and tuple(scale.shape) == kept and
+                 scale.is_contiguous() and scale.device == codes.device,
+                 "Act8Tensor: scale must be contiguous float32 [cols / 64, rows up to 32]")
+        self.codes, self.scale = codes, scale
+
+    def descriptor(self) -> Act8Descriptor:
+        return Act8Descriptor(self.rows, self.cols, self.codes.data_ptr(), self.scale.data_ptr())
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scale.numel()
+
+
+def qlora_act8_quantize(X, a: Act8Tensor = None) -> Act8Tensor:
+    """Checkpoint of the bf16 activations X [rows, cols] (cols a multiple of
+    64) in 8 bits."""
+    _require(X.dim() == 2 and X.dtype == torch.bfloat16 and X.is_contiguous(),
+             "qlora_act8_quantize: X must be contiguous bf16 [rows, cols]")
+    if a is None:
+        a = Act8Tensor(X.shape[0], X.shape[1], X.device)
+    _require((a.rows, a.cols) == tuple(X.shape), "qlora_act8_quantize: checkpoint of another shape")
+    with _on("qlora_act8_quantize", X, a.codes):
+        d = a.descriptor()
+        _check(lib().qlora_act8_quantize(_ptr(X), ctypes.byref(d), _stream()),
+               "qlora_act8_quantize")
+    return a
+
+
+def qlora_act8_dequantize(a: Act8Tensor, dtype=torch.bfloat16, out=None):
+    """The activations a checkpoint stands for, float32 or bf16 [rows, cols]."""
+    if out is None:
+        out = torch.empty((a.rows, a.cols), dtype=dtype, device=a.codes.device)
+    _require(out.dtype in (torch.bfloat16, torch.float32) and out.is_contiguous() and
+             out.shape == (a.rows, a.cols),
+             "qlora_act8_dequantize: out must be contiguous bf16 or float32 [rows, cols]")
+    with _on("qlora_act8_dequantize", a.codes, out):
+        d = a.descriptor()
+        code = QLORA_BF16 if out.dtype == torch.bfloat16 else QLORA_F32
+        _check(lib().qlora_act8_dequantize(ctypes.byref(d), code, _ptr(out), _stream()),
+               "qlora_act8_dequantize")
+    return out
+
+
+def qlora_linear_act8_workspace_bytes(M: int, N: int, K: int, r: int) -> int:
+    return int(lib().qlora_linear_act8_workspace_bytes(M, N, K, r))
+
+
+def _bwd_act8(what, q, a, A, B, R, dY, XA_in, need_dx, dX, dA, dB, ws):
+    """Checks and outputs the two backward calls from a checkpoint share."""
+    M, K, N = a.rows, a.cols, q.rows
+    for t, shape, name in ((A, (R, K), "A"), (B, (N, R), "B"), (dY, (M, N), "dY"),
+                           (XA_in, (M, R), "XA_in")):
+        _require(t.dtype == torch.bfloat16 and t.is_contiguous() and tuple(t.shape) == shape,
+                 "%s: %s must be contiguous bf16 %s" % (what, name, list(shape)))
+    _require(K == q.cols, what + ": checkpoint of another width than the weight")
+    dev = dY.device
+    if need_dx and dX is None:
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    if dA is None:
+        dA = torch.empty((R, K), dtype=torch.float32, device=dev)
+    if dB is None:
+        dB = torch.empty((N, R), dtype=torch.float32, device=dev)
+    for t, shape, dt, name in ((dX if need_dx else None, (M, K), torch.bfloat16, "dX"),
+                               (dA, (R, K), torch.float32, "dA"),
+                               (dB, (N, R), torch.float32, "dB")):
+        _require(t is None or (t.dtype == dt and t.is_contiguous() and tuple(t.shape) == shape),
+                 "%s: %s must be contiguous %s %s" % (what, name, dt, list(shape)))
+    if ws is None:
+        ws = workspace(qlora_linear_act8_workspace_bytes(M, N, K, R), dev)
+    return dX if need_dx else None, dA, dB, ws
+
+
+def qlora_linear_bwd_act8(q: NF4Tensor, a: Act8Tensor, A, B, alpha: float, dY, XA_in,
+                          need_dx: bool = True, dX=None, dA=None, dB=None, ws=None, dropout=None,
+                          keep_bits=None):
+    """qlora_linear_bwd with the input X as an 8-bit checkpoint; XA_in is the
+    forward's XA.  Returns (dX or None, dA float32 [r, K], dB float32 [N, r])."""
+    what = "qlora_linear_bwd_act8"
+    r = A.shape[0]
+    dX, dA, dB, ws = _bwd_act8(what, q, a, A, B, r, dY, XA_in, need_dx, dX, dA, dB, ws)
+    _require(keep_bits is None or (keep_bits.dtype == torch.uint8 and
+                                   keep_bits.numel() * 8 >= a.rows * a.cols),
+             what + ": keep_bits must be uint8 [M K / 8]")
+    with _on(what, dY, a.codes, q.codes, A, B, XA_in, dX, dA, dB, ws, keep_bits):
+        d, x8, dr = q.descriptor(), a.descriptor(), _dropout(dropout)
+        _check(lib().qlora_linear_bwd_act8(ctypes.byref(d), ctypes.byref(x8), _ptr(A), _ptr(B), r,
+                                           ctypes.c_float(alpha),
+                                           ctypes.byref(dr) if dr is not None else None,
+                                           _ptr(keep_bits) if dr is not None else None, _ptr(dY),
+                                           _ptr(XA_in), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws),
+                                           ws.numel(), _stream()), what)
+    return dX, dA, dB
+
+
+def qlora_grouped_bwd_act8(q: NF4Tensor, a: Act8Tensor, A, B, r: int, group_rows, alpha: float,
+                           dY, XA_in, need_dx: bool = True, dX=None, dA=None, dB=None, ws=None):
+    """qlora_grouped_bwd with the input X as an 8-bit checkpoint.  Returns (dX
+    or None, dA float32 [G r, K], dB float32 [N, G r] block-diagonal)."""
+    what = "qlora_grouped_bwd_act8"
+    G = len(group_rows)
+    dX, dA, dB, ws = _bwd_act8(what, q, a, A, B, G * r, dY, XA_in, need_dx, dX, dA, dB, ws)
+    with _on(what, dY, a.codes, q.codes, A, B, XA_in, dX, dA, dB, ws):
+        d, x8, rows = q.descriptor(), a.descriptor(), _rows_arg(group_rows)
+        _check(lib().qlora_grouped_bwd_act8(ctypes.byref(d), ctypes.byref(x8), _ptr(A), _ptr(B), r,
+                                            G, rows, ctypes.c_float(alpha), _ptr(dY), _ptr(XA_in),
+                                            _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(),
+                                            _stream()), what)
+    return dX, dA, dB
+
+
+def _logits(what, logits, labels):
+    """Descriptor of logits [rows, vocab] (bf16 or float32, rows of any stride)
+    and their int64 targets."""
+    _require(logits.dim() == 2 and logits.dtype in (torch.bfloat16, torch.float32) and
+             logits.shape[1] >= 1 and (logits.stride(1) == 1 or logits.shape[1] == 1),
+             what + ": logits must be bf16 or float32 [rows, vocab] with dense rows")
+    _require(labels.dtype == torch.int64 and labels.is_contiguous() and
+             labels.shape == (logits.shape[0],), what + ": labels must be int64 [rows]")
+    rows, vocab = logits.shape
+    ld = logits.stride(0) if rows > 1 else vocab
+    return LogitsDescriptor(logits.data_ptr(),
+                            QLORA_BF16 if logits.dtype == torch.bfloat16 else QLORA_F32, 0, rows,
+                            vocab, ld, labels.data_ptr())
+
+
+def _dlogits_like(what, logits, dlogits):
+    """The gradient buffer and its row stride: the logits' own stride where
+    none is given, so that rows start at the same alignment."""
+    rows, vocab = logits.shape
+    if dlogits is None:
+        ld = max(logits.stride(0), vocab) if rows > 1 else vocab
+        dlogits = torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
+    _require(dlogits.shape == logits.shape and dlogits.dtype == logits.dtype and
+             (dlogits.stride(1) == 1 or vocab == 1),
+             what + ": dlogits must have the logits' shape and type, with dense rows")
+    return dlogits, (dlogits.stride(0) if rows > 1 else vocab)
+
+
+def _rows_f32(what, rows, *named):
+    for t, name in named:
+        _require(t is None or (t.dtype == torch.float32 and t.is_contiguous() and
+                               t.numel() == rows), "%s: %s must be float32 of %d values"
+                 % (what, name, rows))
+
+
+def _sequences(what, cu_seqlens):
+    _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.is_contiguous() and
+             cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2,
+             what + ": cu_seqlens must be int32 [sequences + 1]")
+    return cu_seqlens.numel() - 1
+
+
+def qlora_loss_workspace_bytes(logits, labels, sequences: int = 0) -> int:
+    d = _logits("qlora_loss_workspace_bytes", logits, labels)
+    return int(lib().qlora_loss_workspace_bytes(ctypes.byref(d), sequences))
+
+
+def qlora_token_logprobs(logits, labels, logp=None, stats=None, ws=None,
+                         return_stats: bool = False):
+    """Log-probability of each row's target, float32 [rows] (0 where the label
+    is negative).  With return_stats also float32 [rows, 2] for the backward."""
+    what = "qlora_token_logprobs"
+    z = _logits(what, logits, labels)
+    dev = logits.device
+    if logp is None:
+        logp = torch.empty(z.rows, dtype=torch.float32, device=dev)
+    if return_stats and stats is None:
+        stats = torch.empty((z.rows, 2), dtype=torch.float32, device=dev)
+    _rows_f32(what, z.rows, (logp, "logp"))
+    _rows_f32(what, 2 * z.rows, (stats, "stats"))
+    if ws is None:
+        ws = workspace(lib().qlora_loss_workspace_bytes(ctypes.byref(z), 0), dev)
+    with _on(what, logits, labels, logp, stats, ws):
+        _check(lib().qlora_token_logprobs(ctypes.byref(z), _ptr(logp), _ptr(stats), _ptr(ws),
+                                          ws.numel(), _stream()), what)
+    return (logp, stats) if return_stats else logp
+
+
+def qlora_token_logprobs_bwd(logits, labels, stats, w, dlogits=None, grad_scale=None):
+    """Gradient of the logits for dLoss / dlogp = w [rows] (times the device
+    scalar grad_scale); dlogits may be the logits, overwritten in place."""
+    what = "qlora_token_logprobs_bwd"
+    z = _logits(what, logits, labels)
+    _rows_f32(what, 2 * z.rows, (stats, "stats"))
+    _rows_f32(what, z.rows, (w, "w"))
+    _rows_f32(what, 1, (grad_scale, "grad_scale"))
+    dlogits, ldd = _dlogits_like(what, logits, dlogits)
+    with _on(what, logits, labels, stats, w, grad_scale, dlogits):
+        _check(lib().qlora_token_logprobs_bwd(ctypes.byref(z), _ptr(stats), _ptr(w),
+                                              _ptr(grad_scale), _ptr(dlogits), ldd, _stream()),
+               what)
+    return dlogits
+
+
+class PreferenceLoss(NamedTuple):
+    loss: torch.Tensor                  # float32 scalar
+    seq_logp: torch.Tensor              # float32 [2 pairs]
+    rewards: torch.Tensor               # float32 [2 pairs]: beta times the log ratio
+    logp: torch.Tensor                  # float32 [rows]
+    dlogits: Optional[torch.Tensor]
+
+
+class PolicyLoss(NamedTuple):
+    loss: torch.Tensor                  # float32 scalar
+    kl: torch.Tensor                    # float32 scalar
+    clip_frac: torch.Tensor             # float32 scalar
+    logp: torch.Tensor                  # float32 [rows]
+    dlogits: Optional[torch.Tensor]
+
+
+def qlora_preference_loss(logits, labels, cu_seqlens, ref_logp=None, beta: float = 0.1,
+                          loss_type: str = "sigmoid", label_smoothing: float = 0.0,
+                          length_mean: bool = False, return_grad: bool = False, dlogits=None,
+                          stats=None, w=None, ws=None) -> PreferenceLoss:
+    """Preference loss over pairs of packed answers (sequences 2p and 2p + 1
+    are pair p's preferred and other answer) against reference token
+    log-probabilities ref_logp [rows] (None: 0).  With return_grad (or a
+    dlogits buffer, which may be the logits) the gradient of the logits comes
+    with it; stats [rows, 2] and w [rows] receive what
+    qlora_token_logprobs_bwd takes."""
+    what = "qlora_preference_loss"
+    z = _logits(what, logits, labels)
+    n = _sequences(what, cu_seqlens)
+    _require(n % 2 == 0, what + ": cu_seqlens must describe pairs")
+    _require(loss_type in PREFERENCE_KINDS, what + ": unknown loss_type")
+    _rows_f32(what, z.rows, (ref_logp, "ref_logp"), (w, "w"))
+    _rows_f32(what, 2 * z.rows, (stats, "stats"))
+    dev = logits.device
+    buf = torch.empty(2 * n + z.rows + 1, dtype=torch.float32, device=dev)
+    seq_logp, rewards, logp, loss = buf.split((n, n, z.rows, 1))
+    ldd = 0
+    if return_grad or dlogits is not None:
+        dlogits, ldd = _dlogits_like(what, logits, dlogits)
+    if ws is None:
+        ws = workspace(lib().qlora_loss_workspace_bytes(ctypes.byref(z), n), dev)
+    h = PreferenceParams(beta, label_smoothing, PREFERENCE_KINDS[loss_type], int(length_mean))
+    with _on(what, logits, labels, cu_seqlens, ref_logp, dlogits, stats, w, ws):
+        _check(lib().qlora_preference_loss(ctypes.byref(z), n // 2, _ptr(cu_seqlens),
+                                           _ptr(ref_logp), ctypes.byref(h), _ptr(loss),
+                                           _ptr(seq_logp), _ptr(rewards), _ptr(logp), _ptr(stats),
+                                           _ptr(w), _ptr(dlogits), ldd, _ptr(ws), ws.numel(),
+                                           _stream()), what)
+    return PreferenceLoss(loss[0], seq_logp, rewards, logp, dlogits)
+
+
+def qlora_policy_loss(logits, labels, cu_seqlens, advantages, old_logp=None, ref_logp=None,
+                      clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                      reduction: str = "token", token_advantages: bool = False,
+                      return_grad: bool = False, dlogits=None, stats=None, w=None,
+                      ws=None) -> PolicyLoss:
+    """Clipped policy loss with a KL term over packed answers: advantages
+    float32 [sequences] ([rows] with token_advantages), token log-probabilities of the
+    sampling policy (None: the current one) and of the reference (None: no KL
+    term).  reduction: mean over all targets ("token"), or over each
+    sequence's and then over sequences ("sequence").  return_grad, dlogits,
+    stats and w as in qlora_preference_loss."""
+    what = "qlora_policy_loss"
+    z = _logits(what, logits, labels)
+    n = _sequences(what, cu_seqlens)
+    _require(reduction in POLICY_REDUCTIONS, what + ": unknown reduction")
+    _rows_f32(what, z.rows if token_advantages else n, (advantages, "advantages"))
+    _rows_f32(what, z.rows, (old_logp, "old_logp"), (ref_logp, "ref_logp"), (w, "w"))
+    _rows_f32(what, 2 * z.rows, (stats, "stats"))
+    dev = logits.device
+    buf = torch.empty(3 + z.rows, dtype=torch.float32, device=dev)
+    out, logp = buf.split((3, z.rows))
+    ldd = 0
+    if return_grad or dlogits is not None:
+        dlogits, ldd = _dlogits_like(what, logits, dlogits)
+    if ws is None:
+        ws = workspace(lib().qlora_loss_workspace_bytes(ctypes.byref(z), n), dev)
+    h = PolicyParams(clip_low, clip_high, kl_coef, POLICY_REDUCTIONS[reduction],
+                     int(token_advantages))
+    with _on(what, logits, labels, cu_seqlens, advantages, old_logp, ref_logp, dlogits, stats, w,
+             ws):
+        _check(lib().qlora_policy_loss(ctypes.byref(z), n, _ptr(cu_seqlens), _ptr(advantages),
+                                       _ptr(old_logp), _ptr(ref_logp), ctypes.byref(h), _ptr(out),
+                                       _ptr(logp), _ptr(stats), _ptr(w), _ptr(dlogits), ldd,
+                                       _ptr(ws), ws.numel(), _stream()), what)
+    return PolicyLoss(out[0], out[1], out[2], logp, dlogits)
+
+
 def qlora_trace_begin(kernels, capacity: int = 4096):
     """Start timing launches of the named kernels (see KERNELS) with HIP events."""
     mask = 0
@@ -697,21 +1056,105 @@ def qlora_trace_end():
 
 
 class QLoRALinearFn(torch.autograd.Function):
-    """autograd wrapper: frozen NF4 weight, trainable bf16 adapters A and B."""
+    """autograd wrapper: frozen NF4 weight, trainable bf16 adapters A and B.
+    act8 keeps the input for the backward in 8 bits instead of bf16: True
+    makes a checkpoint of X, an Act8Tensor of X (shared by the projections
+    that read one input) is kept as it is."""
 
     @staticmethod
-    def forward(ctx, X, A, B, q, alpha, dropout=None):
+    def forward(ctx, X, A, B, q, alpha, dropout=None, act8=None):
         bits = keep_bits_buffer(X.shape[0], X.shape[1], X.device) if dropout else None
-        Y, XA = qlora_linear_fwd(q, X.contiguous(), A.contiguous(), B.contiguous(), alpha,
+        Xc = X.contiguous()
+        Y, XA = qlora_linear_fwd(q, Xc, A.contiguous(), B.contiguous(), alpha,
                                  return_xa=True, dropout=dropout, keep_bits=bits)
-        ctx.save_for_backward(X, A, B, XA)
+        if act8:
+            if act8 is True:
+                act8 = qlora_act8_quantize(Xc)
+            _require((act8.rows, act8.cols) == tuple(X.shape),
+                     "QLoRALinearFn: act8 is a checkpoint of another shape")
+            ctx.save_for_backward(act8.codes, A, B, XA, act8.scale)
+        else:
+            ctx.save_for_backward(X, A, B, XA)
         ctx.q, ctx.alpha, ctx.dropout, ctx.bits = q, alpha, dropout, bits
         return Y
 
     @staticmethod
     def backward(ctx, dY):
-        X, A, B, XA = ctx.saved_tensors
-        dX, dA, dB = qlora_linear_bwd(ctx.q, X, A, B, ctx.alpha, dY.contiguous(), XA_in=XA,
-                                      need_dx=ctx.needs_input_grad[0], dropout=ctx.dropout,
-                                      keep_bits=ctx.bits)
-        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None
+        X, A, B, XA, *scale = ctx.saved_tensors
+        if scale:
+            a = Act8Tensor(X.shape[0], X.shape[1], codes=X, scale=scale[0])
+            dX, dA, dB = qlora_linear_bwd_act8(ctx.q, a, A.contiguous(), B.contiguous(), ctx.alpha,
+                                               dY.contiguous(), XA,
+                                               need_dx=ctx.needs_input_grad[0],
+                                               dropout=ctx.dropout, keep_bits=ctx.bits)
+        else:
+            dX, dA, dB = qlora_linear_bwd(ctx.q, X, A, B, ctx.alpha, dY.contiguous(), XA_in=XA,
+                                          need_dx=ctx.needs_input_grad[0], dropout=ctx.dropout,
+                                          keep_bits=ctx.bits)
+        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None
+
+
+def _logits_grad(ctx, g, w):
+    logits, labels, stats = ctx.saved_tensors[:3]
+    g = g.to(torch.float32).reshape(1).contiguous() if g is not None else None
+    return qlora_token_logprobs_bwd(logits, labels, stats, w, grad_scale=g)
+
+
+class TokenLogprobsFn(torch.autograd.Function):
+    """autograd wrapper of qlora_token_logprobs(logits, labels)."""
+
+    @staticmethod
+    def forward(ctx, logits, labels):
+        logp, stats = qlora_token_logprobs(logits, labels, return_stats=True)
+        ctx.save_for_backward(logits, labels, stats)
+        return logp
+
+    @staticmethod
+    def backward(ctx, g):
+        return _logits_grad(ctx, None, g.to(torch.float32).contiguous()), None
+
+
+def _loss_buffers(logits):
+    rows = logits.shape[0]
+    return (torch.empty((rows, 2), dtype=torch.float32, device=logits.device),
+            torch.empty(rows, dtype=torch.float32, device=logits.device))
+
+
+class PreferenceLossFn(torch.autograd.Function):
+    """autograd wrapper of qlora_preference_loss: the loss, and (without
+    gradients) seq_logp and rewards."""
+
+    @staticmethod
+    def forward(ctx, logits, labels, cu_seqlens, ref_logp=None, beta=0.1, loss_type="sigmoid",
+                label_smoothing=0.0, length_mean=False):
+        stats, w = _loss_buffers(logits)
+        o = qlora_preference_loss(logits, labels, cu_seqlens, ref_logp, beta, loss_type,
+                                  label_smoothing, length_mean, stats=stats, w=w)
+        ctx.save_for_backward(logits, labels, stats, w)
+        ctx.mark_non_differentiable(o.seq_logp, o.rewards)
+        return o.loss.clone(), o.seq_logp, o.rewards
+
+    @staticmethod
+    def backward(ctx, g, *_):
+        return (_logits_grad(ctx, g, ctx.saved_tensors[3]),) + (None,) * 7
+
+
+class PolicyLossFn(torch.autograd.Function):
+    """autograd wrapper of qlora_policy_loss: the loss, and (without
+    gradients) the KL term and the clipped share."""
+
+    @staticmethod
+    def forward(ctx, logits, labels, cu_seqlens, advantages, old_logp=None, ref_logp=None,
+                clip_low=0.2, clip_high=0.2, kl_coef=0.0, reduction="token",
+                token_advantages=False):
+        stats, w = _loss_buffers(logits)
+        o = qlora_policy_loss(logits, labels, cu_seqlens, advantages, old_logp, ref_logp, clip_low,
+                              clip_high, kl_coef, reduction, token_advantages, stats=stats, w=w)
+        ctx.save_for_backward(logits, labels, stats, w)
+        kl, frac = o.kl.clone(), o.clip_frac.clone()
+        ctx.mark_non_differentiable(kl, frac)
+        return o.loss.clone(), kl, frac
+
+    @staticmethod
+    def backward(ctx, g, *_):
+        return (_logits_grad(ctx, g, ctx.saved_tensors[3]),) + (None,) * 10

@@ -124,6 +124,12 @@ LinearWs linear_layout(int64_t M, int64_t N, int64_t K, int r) {
   return w;
 }
 
+// What the backward from an 8-bit checkpoint needs behind that layout: the
+// float32 G^T [r, mp].
+size_t act8_bytes(const LinearWs& w, int r) {
+  return align_up((size_t)r * w.mp * sizeof(float));
+}
+
 template <typename T>
 T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
 
@@ -189,6 +195,17 @@ qlora_status check_linear(const qlora_nf4_tensor* W, const void* X, int64_t M, c
   if (!linear_fits(M, W->rows, W->cols)) return QLORA_ERR_UNSUPPORTED;
   if (!aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16)) return QLORA_ERR_INVALID_ARG;
   return QLORA_OK;
+}
+
+bool valid_act8(const qlora_act8* a) {
+  return a && a->rows >= 0 && a->cols >= 1 && a->cols <= INT64_MAX - kBlock &&
+         (a->rows == 0 || (a->codes && a->scale && aligned(a->codes, 16) && aligned(a->scale, 16)));
+}
+
+// Whole blocks, and at most 2^37 values of at most 2^26 to a row.
+bool act8_fits(const qlora_act8* a) {
+  return a->cols % kBlock == 0 && a->cols <= (int64_t)1 << 26 &&
+         a->rows <= (((int64_t)1 << 37) / a->cols);
 }
 
 // Kernel parameters of a dropout of an input with rows of K elements: keep
@@ -564,14 +581,15 @@ qlora_status qlora_linear_bwd(const qlora_nf4_tensor* W, const qlora_bf16* X, in
                                   ws_bytes, stream);
 }
 
-// The backward; `grp` (nullable) makes dB block-diagonal (grouped linear).
+// The backward; `grp` (nullable) makes dB block-diagonal (grouped linear), and
+// with `x8` (checked; XA_in then not null) dA reads the checkpoint, X its codes.
 static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16* X, int64_t M,
                                     const qlora_bf16* A, const qlora_bf16* B, int32_t r,
                                     float alpha, const qlora_dropout* drop,
                                     const uint8_t* keep_bits_in, const qlora_bf16* dY,
                                     const qlora_bf16* XA_in, qlora_bf16* dX, float* dA,
                                     float* dB, void* ws, size_t ws_bytes, void* stream,
-                                    const GradJob* grp) {
+                                    const GradJob* grp, const qlora_act8* x8 = nullptr) {
   qlora_status st = check_linear(W, X, M, A, B, r, alpha);
   if (st != QLORA_OK) return st;
   DropoutParams dp;
@@ -581,10 +599,13 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
   if (dX && !aligned(dX, 16)) return QLORA_ERR_INVALID_ARG;
   const int64_t N = W->rows, K = W->cols;
   const LinearWs L = linear_layout(M, N, K, r);
-  if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
+  const size_t gtf_at = L.total;   // x8: float32 G^T behind the plain layout
+  const size_t need = L.total + (x8 ? act8_bytes(L, r) : 0);
+  if (!ws || ws_bytes < need || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const float scale = alpha / (float)r;
   float* ahat_t = at<float>(ws, L.ahat_t);
+  float* gtf = at<float>(ws, gtf_at);
   uint16_t* bt = at<uint16_t>(ws, L.bt);
   uint16_t* gs = at<uint16_t>(ws, L.gs);
   uint16_t* gt = at<uint16_t>(ws, L.gt);
@@ -604,8 +625,9 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
   // without the forward's XA, X.A^T is recomputed beside it
   SkinnyJob sj[2];
   int nj = 0;
-  sj[nj++] = SkinnyJob{dY, N, N, bt, L.np, 0, 0, at<float>(ws, L.sk_n), scale, gs, nullptr, gt,
-                       L.mp};
+  sj[nj++] = SkinnyJob{dY, N, N, bt, L.np, 0, 0, at<float>(ws, L.sk_n), scale,
+                       x8 && !dX ? nullptr : gs, nullptr, x8 ? nullptr : gt, L.mp};
+  if (x8) sj[0].out_tf = gtf;
   if (!XA_in) {
     sj[nj++] = SkinnyJob{X, K, K, A, K, 0, 0, at<float>(ws, L.sk_k), 1.0f, nullptr, nullptr, xat,
                          L.mp};
@@ -632,6 +654,13 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
     gj[1].groups = grp->groups;
     gj[1].gr = grp->gr;
     for (int g = 0; g < kMaxGroups; ++g) gj[1].end[g] = grp->end[g];
+  }
+  if (x8) {
+    Act8GradJob aj{x8->codes, x8->scale, K, gtf, L.mp, scale, dA};
+    aj.drop = dp;
+    QL_TRY(launch_act8_grad(aj, M, r, s));
+    QL_TRY(launch_lora_grads(gj + 1, 1, M, r, s));
+    return QLORA_OK;
   }
   QL_TRY(launch_lora_grads(gj, 2, M, r, s));
 #undef QL_TRY
@@ -693,6 +722,66 @@ qlora_status qlora_grouped_bwd(const qlora_nf4_tensor* W, const qlora_bf16* X, i
   return linear_bwd_impl(W, X, M, A, B, groups * r, alpha * (float)groups, nullptr, nullptr, dY,
                          XA_in,
                          dX, dA, dB, ws, ws_bytes, stream, &g);
+}
+
+qlora_status qlora_act8_quantize(const qlora_bf16* X, const qlora_act8* a, void* stream) {
+  if (!valid_act8(a) || (a->rows > 0 && (!X || !aligned(X, 16)))) return QLORA_ERR_INVALID_ARG;
+  if (!act8_fits(a)) return QLORA_ERR_UNSUPPORTED;
+  if (a->rows == 0) return QLORA_OK;
+  return hip_status(launch_act8_quantize(X, a->rows, a->cols, a->codes, a->scale,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_act8_dequantize(const qlora_act8* a, qlora_dtype out_dtype, void* out,
+                                   void* stream) {
+  if (!valid_act8(a) || (a->rows > 0 && (!out || !aligned(out, 16)))) return QLORA_ERR_INVALID_ARG;
+  if (out_dtype != QLORA_F32 && out_dtype != QLORA_BF16) return QLORA_ERR_INVALID_ARG;
+  if (!act8_fits(a)) return QLORA_ERR_UNSUPPORTED;
+  if (a->rows == 0) return QLORA_OK;
+  return hip_status(launch_act8_dequantize(a->codes, a->scale, a->rows, a->cols,
+                                           out_dtype == QLORA_BF16, out,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_linear_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r) {
+  const size_t plain = qlora_linear_workspace_bytes(M, N, K, r);
+  return plain == 0 ? 0 : plain + act8_bytes(linear_layout(M, N, K, r), r);
+}
+
+// The checkpoint's own checks for a linear whose weight has `cols` columns.
+static qlora_status check_act8_linear(const qlora_nf4_tensor* W, const qlora_act8* X8,
+                                      const qlora_bf16* XA_in) {
+  if (!valid_tensor(W) || !valid_act8(X8) || X8->rows < 1 || !XA_in) return QLORA_ERR_INVALID_ARG;
+  if (X8->cols != W->cols) return QLORA_ERR_INVALID_ARG;
+  return act8_fits(X8) ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
+}
+
+qlora_status qlora_linear_bwd_act8(const qlora_nf4_tensor* W, const qlora_act8* X8,
+                                   const qlora_bf16* A, const qlora_bf16* B, int32_t r,
+                                   float alpha, const qlora_dropout* drop,
+                                   const uint8_t* keep_bits_in, const qlora_bf16* dY,
+                                   const qlora_bf16* XA_in, qlora_bf16* dX, float* dA, float* dB,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  const qlora_status st = check_act8_linear(W, X8, XA_in);
+  if (st != QLORA_OK) return st;
+  return linear_bwd_impl(W, reinterpret_cast<const qlora_bf16*>(X8->codes), X8->rows, A, B, r,
+                         alpha, drop, keep_bits_in, dY, XA_in, dX, dA, dB, ws, ws_bytes, stream,
+                         nullptr, X8);
+}
+
+qlora_status qlora_grouped_bwd_act8(const qlora_nf4_tensor* W, const qlora_act8* X8,
+                                    const qlora_bf16* A, const qlora_bf16* B, int32_t r,
+                                    int32_t groups, const int64_t* group_rows, float alpha,
+                                    const qlora_bf16* dY, const qlora_bf16* XA_in,
+                                    qlora_bf16* dX, float* dA, float* dB, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  const qlora_status st = check_act8_linear(W, X8, XA_in);
+  if (st != QLORA_OK) return st;
+  GradJob g{};
+  if (!grouping(W, r, groups, group_rows, &g)) return QLORA_ERR_INVALID_ARG;
+  return linear_bwd_impl(W, reinterpret_cast<const qlora_bf16*>(X8->codes), X8->rows, A, B,
+                         groups * r, alpha * (float)groups, nullptr, nullptr, dY, XA_in, dX, dA,
+                         dB, ws, ws_bytes, stream, &g, X8);
 }
 
 qlora_status qlora_dropout_mask(int64_t M, int64_t K, const qlora_dropout* drop, uint8_t* out,

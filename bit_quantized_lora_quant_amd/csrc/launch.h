@@ -105,6 +105,9 @@ struct SkinnyJob {
   // dropout of T (T = X only): dropped elements read as zero, sums times
   // drop.inv
   DropoutParams drop{};
+  // float32 P^T [r, ldo_t] (zero for m in [M, ldo_t)), beside or in place of
+  // out_t
+  float* out_tf = nullptr;
 };
 // Padded rank of the partial rows (16, 32, 64 or 128).
 int skinny_rpad(int r);
@@ -144,6 +147,27 @@ struct GradJob {
 int lora_grad_splits(int64_t M, int64_t P);
 // Both jobs' partial launch, then both reductions.
 hipError_t launch_lora_grads(const GradJob* jobs, int njobs, int64_t M, int r, hipStream_t s);
+
+// Checkpoints in 8 bits: codes int8 [rows, cols] and scales float32
+// [cols / 64][rows32] of X bf16 [rows, cols]; rows32 is rows up to 32.
+hipError_t launch_act8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes,
+                                float* scale, hipStream_t s);
+hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64_t rows,
+                                  int64_t cols, int bf16, void* out, hipStream_t s);
+// Adapter gradient from a checkpoint: out[j][k] = alpha sum_m G[j][m]
+// D(scale[k / 64][m] codes[m][k]), float32 [r][K]; G float32 [r, ldg] (zero
+// for m in [M, ldg)), ldg = M up to 32 is also the scales' row length.
+struct Act8GradJob {
+  const int8_t* codes;
+  const float* scale;
+  int64_t K;
+  const float* G;
+  int64_t ldg;
+  float alpha;
+  float* out;
+  DropoutParams drop{};
+};
+hipError_t launch_act8_grad(const Act8GradJob& job, int64_t M, int r, hipStream_t s);
 
 // The GEMMs split their inner loop into `splits` slices (one workgroup per
 // tile and slice) when the output tiles alone cannot fill the chip; with

@@ -53,9 +53,9 @@ __device__ __forceinline__ void recon_tile(const ReconJob& J, int64_t b,
 }
 
 
-// Row groups of a job: past M only when out_t needs zero padding.
+// Row groups of a job: past M only when out_t or out_tf needs zero padding.
 __device__ __host__ __forceinline__ int64_t skinny_rows(const SkinnyJob& J, int64_t M) {
-  return (J.ks == 1 && J.out_t && J.ldo_t > M) ? J.ldo_t : M;
+  return (J.ks == 1 && (J.out_t || J.out_tf) && J.ldo_t > M) ? J.ldo_t : M;
 }
 
 __device__ __forceinline__ int64_t skinny_blocks(const SkinnyJob& J, int64_t M) {
@@ -212,6 +212,8 @@ __device__ __forceinline__ void skinny2_slice(const SkinnyJob& J, int64_t M, int
       }
       if (J.out_t && j < r && m < J.ldo_t)
         J.out_t[(int64_t)j * J.ldo_t + m] = m < M ? to_bf16(sum) : 0;
+      if (J.out_tf && j < r && m < J.ldo_t)
+        J.out_tf[(int64_t)j * J.ldo_t + m] = m < M ? sum : 0.f;
     }
 }
 
@@ -241,7 +243,7 @@ __global__ __launch_bounds__(kSk2Waves * 64) void k_skinny2(SkinnyJob j0, Skinny
 // Thread per (row m, column j < r32) of one job: adds the slices in order.
 __device__ __forceinline__ void skinny_finish_elem(const SkinnyJob& J, int64_t M, int r, int r32,
                                                    int rpad, int64_t e) {
-  const int64_t rows = (J.out_t && J.ldo_t > M) ? J.ldo_t : M;
+  const int64_t rows = ((J.out_t || J.out_tf) && J.ldo_t > M) ? J.ldo_t : M;
   if (e >= rows * r32) return;
   const int64_t m = e / r32;
   const int j = (int)(e - m * r32);
@@ -255,13 +257,14 @@ __device__ __forceinline__ void skinny_finish_elem(const SkinnyJob& J, int64_t M
     if (J.out && j < r) J.out[m * r + j] = to_bf16(sum);
   }
   if (J.out_t && j < r && m < J.ldo_t) J.out_t[(int64_t)j * J.ldo_t + m] = m < M ? to_bf16(sum) : 0;
+  if (J.out_tf && j < r && m < J.ldo_t) J.out_tf[(int64_t)j * J.ldo_t + m] = m < M ? sum : 0.f;
 }
 
 // (jobs run as a single slice wrote their outputs directly: no finish)
 __device__ __host__ __forceinline__ int64_t finish_blocks(const SkinnyJob& J, int64_t M,
                                                           int r32) {
   if (J.ks == 1) return 0;
-  const int64_t rows = (J.out_t && J.ldo_t > M) ? J.ldo_t : M;
+  const int64_t rows = ((J.out_t || J.out_tf) && J.ldo_t > M) ? J.ldo_t : M;
   return ceil_div(rows * r32, 256);
 }
 

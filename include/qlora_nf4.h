@@ -473,6 +473,177 @@ qlora_status qlora_host_state_alloc(size_t bytes, void** ptr);
 qlora_status qlora_host_state_free(void* ptr);
 
 /* ------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits.  Activations are what is left of a
+ * finetune's memory once weights and statistics are small ("Fitting a
+ * fine-tune in 16 GB", on what still scales with batch and sequence length).
+ * Of its input X a frozen linear's backward reads only G^T . D(X), so X can
+ * be kept between the passes as int8 codes with one float32 scale per 64
+ * values of a row, 1 + 4/64 bytes a value instead of 2:
+ *     a = max |x| over the block,  code = rint(127 x / a),  scale = fl(a / 127),
+ *     x^ = fl(code * scale),
+ * rint half to even of the exact quotient, fl one rounding to float32.  A
+ * block of zeros has codes and scale 0.  A block that holds an infinity or a
+ * NaN has codes 0 and scale NaN, so all of it reads back as NaN.
+ * codes are [rows, cols] row-major; scale is [cols / 64][rows32], rows32 =
+ * rows rounded up to a multiple of 32 (the gradient reads it along tokens),
+ * zeros from rows to rows32.  Both 16-byte aligned, device memory owned by the
+ * caller; cols a multiple of 64 and at most 2^26, rows * cols at most 2^37,
+ * else QLORA_ERR_UNSUPPORTED.  rows 0 does nothing. */
+typedef struct {
+  int64_t rows, cols;
+  int8_t* codes;       /* [rows, cols] */
+  float* scale;        /* [cols / 64][rows32] */
+} qlora_act8;
+
+/* X bf16 [rows, cols], 16-byte aligned -> a's codes and scales (padding
+ * included). */
+qlora_status qlora_act8_quantize(const qlora_bf16* X, const qlora_act8* a, void* stream);
+/* a -> out [rows, cols] in float32 or bf16 (x^ rounded to nearest even),
+ * 16-byte aligned. */
+qlora_status qlora_act8_dequantize(const qlora_act8* a, qlora_dtype out_dtype, void* out,
+                                   void* stream);
+
+/* Bytes of workspace qlora_linear_bwd_act8 needs (and qlora_grouped_bwd_act8
+ * with r = groups * r); 0 for a shape qlora_linear_workspace_bytes refuses. */
+size_t qlora_linear_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r);
+
+/* qlora_linear_bwd_dropout whose input is a checkpoint of X [M, K], M =
+ * X8->rows: dA = s . G^T . D(x^) is formed from the codes, with G kept in
+ * float32 and its products with the scales in two bf16 parts, so dA has
+ * float32 accuracy for the given x^; dX and dB do not read X.  XA_in
+ * (required) is the forward's XA_out.  drop and keep_bits_in (both nullable)
+ * as there.  Same shapes, limits and errors, plus QLORA_ERR_INVALID_ARG for a
+ * checkpoint of another width or without rows, or XA_in NULL. */
+qlora_status qlora_linear_bwd_act8(const qlora_nf4_tensor* W, const qlora_act8* X8,
+                                   const qlora_bf16* A, const qlora_bf16* B, int32_t r,
+                                   float alpha, const qlora_dropout* drop,
+                                   const uint8_t* keep_bits_in, const qlora_bf16* dY,
+                                   const qlora_bf16* XA_in, qlora_bf16* dX, float* dA, float* dB,
+                                   void* ws, size_t ws_bytes, void* stream);
+/* qlora_grouped_bwd from a checkpoint, likewise. */
+qlora_status qlora_grouped_bwd_act8(const qlora_nf4_tensor* W, const qlora_act8* X8,
+                                    const qlora_bf16* A, const qlora_bf16* B, int32_t r,
+                                    int32_t groups, const int64_t* group_rows, float alpha,
+                                    const qlora_bf16* dY, const qlora_bf16* XA_in,
+                                    qlora_bf16* dX, float* dA, float* dB, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Losses on the logits of packed sequences: the step that turns an adapted
+ * model's outputs into the gradient the linears' backward starts from.
+ * Row t of the logits z [rows, vocab] predicts labels[t] (already shifted by
+ * the caller); a negative label means no target: its logp is 0, its gradient
+ * row zero, and the row is not read.  A label >= vocab gives logp NaN, which
+ * reaches the loss and the gradient.  For a row with target y
+ *     logp = z_y - m - log sum_v exp(z_v - m),   m = max_v z_v,
+ * the sum over v in float32, the logarithm and what follows it in float64
+ * (logp is rounded once when it is stored); a logit of -inf has probability 0, a row of nothing else (or with +inf or NaN) logp
+ * NaN.  Results are identical run to run (fixed orders, no float atomics).
+ *
+ * The logits are described by a host struct: bf16 or float32, row stride
+ * ld >= vocab values, aligned to their type (16-byte row starts are fastest).
+ * Gradient outputs have the logits' type and a row stride of their own (ldd);
+ * they may be the logits themselves (then ldd == ld), overwritten in place.
+ *
+ * Sequence i of a packed batch is rows cu_seqlens[i] .. cu_seqlens[i+1] - 1
+ * (int32 [sequences + 1], device, ascending from >= 0 to <= rows; a value
+ * outside is clamped).  Empty sequences are allowed.  Rows in no sequence
+ * (padding before the first or behind the last) count as rows without target,
+ * whatever their label: their logp is 0 and their gradient zero. */
+typedef struct {
+  const void* data;        /* device, [rows] x ld; may be NULL when rows == 0 */
+  qlora_dtype dtype;       /* QLORA_F32 or QLORA_BF16 */
+  int32_t reserved;        /* must be 0 */
+  int64_t rows, vocab, ld; /* 0 <= rows < 2^24, 1 <= vocab < 2^30 */
+  const int64_t* labels;   /* device, [rows] */
+} qlora_logits;
+
+/* Bytes of workspace the four calls below need for these logits and this
+ * number of sequences (token_logprobs: 0); 0 for sizes they refuse. */
+size_t qlora_loss_workspace_bytes(const qlora_logits* z, int32_t sequences);
+
+/* Log-probabilities of the targets: logp float32 [rows].  stats (nullable)
+ * float32 [rows][2] receives each row's m and sum_v exp(z_v - m) (0, 0
+ * without target) for the backward.  Every row with a label >= 0 counts, in any sequence. */
+qlora_status qlora_token_logprobs(const qlora_logits* z, float* logp, float* stats, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* Backward of the above for weights w float32 [rows] (dLoss / dlogp):
+ *     dlogits[t][v] = g w[t] (1[v == y_t] - exp(z_tv - m_t) / sum_t),
+ * g = grad_scale[0] (device; NULL = 1).  A row without target, or with
+ * w == 0, gets zeros and is not read. */
+qlora_status qlora_token_logprobs_bwd(const qlora_logits* z, const float* stats, const float* w,
+                                      const float* grad_scale, void* dlogits, int64_t ldd,
+                                      void* stream);
+
+/* Preference loss over pairs of answers: sequence 2p is pair p's preferred
+ * answer, 2p + 1 the other.  With the log ratio of a sequence against the
+ * reference policy, lr_i = sum_t (logp_t - ref_logp_t) (divided by the
+ * sequence's targets with length_mean), and h = lr_2p - lr_(2p+1):
+ *     SIGMOID  -(1 - e) log sigmoid(beta h) - e log sigmoid(-beta h)
+ *     HINGE    max(0, 1 - beta h)
+ *     IPO      (h - 1 / (2 beta))^2
+ * averaged over the pairs; e = label_smoothing.  Log ratios and losses are
+ * summed in float64. */
+#define QLORA_PREF_SIGMOID 0
+#define QLORA_PREF_HINGE 1
+#define QLORA_PREF_IPO 2
+typedef struct {
+  double beta;             /* > 0 */
+  double label_smoothing;  /* in [0, 0.5]; 0 unless SIGMOID */
+  int32_t kind;            /* QLORA_PREF_* */
+  int32_t length_mean;     /* 0 or 1 */
+} qlora_preference_params;
+
+/*   ref_logp  float32 [rows] token log-probabilities of the reference policy
+ *             (qlora_token_logprobs with the adapters off), or NULL: 0.
+ *   loss      float32 [1].
+ *   seq_logp  float32 [2 pairs] (nullable): sum (mean) of logp per sequence.
+ *   rewards   float32 [2 pairs] (nullable): beta lr.
+ *   logp      float32 [rows], stats float32 [rows][2] (as above) and
+ *             w float32 [rows], dLoss / dlogp: what qlora_token_logprobs_bwd
+ *             takes.  Each nullable.
+ *   dlogits   (nullable) the gradient for an upstream gradient of 1, written
+ *             in the same call.
+ * pairs >= 1. */
+qlora_status qlora_preference_loss(const qlora_logits* z, int32_t pairs, const int32_t* cu_seqlens,
+                                   const float* ref_logp, const qlora_preference_params* h,
+                                   float* loss, float* seq_logp, float* rewards, float* logp,
+                                   float* stats, float* w, void* dlogits, int64_t ldd, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Clipped policy loss with a KL term over sampled answers:
+ *     r = exp(logp - old_logp),  A the answer's (or token's) advantage,
+ *     term = max(-A r, -A clamp(r, 1 - clip_low, 1 + clip_high))
+ *            + kl_coef (exp(d) - d - 1),   d = ref_logp - logp,
+ * averaged over all targets (TOKEN) or over each sequence's targets and then
+ * over the sequences that have any (SEQUENCE).  No gradient flows through
+ * the clamp where it is the larger.  0 when there is no target.  Terms in
+ * float64. */
+#define QLORA_POLICY_TOKEN 0
+#define QLORA_POLICY_SEQUENCE 1
+typedef struct {
+  double clip_low, clip_high;   /* clip_low in [0, 1], clip_high >= 0 */
+  double kl_coef;               /* >= 0 */
+  int32_t reduction;            /* QLORA_POLICY_* */
+  int32_t token_advantages;     /* 0: advantages [sequences]; 1: [rows] */
+} qlora_policy_params;
+
+/*   advantages float32 [sequences] or [rows];  old_logp float32 [rows] or
+ *              NULL (logp itself: r = 1);  ref_logp float32 [rows] or NULL
+ *              (no KL term; required when kl_coef > 0).
+ *   out        float32 [3]: the loss, the mean (as reduced) of
+ *              exp(d) - d - 1, and the share of targets whose clamped term is
+ *              the larger.
+ *   logp, stats, w, dlogits as in qlora_preference_loss.  sequences >= 1. */
+qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
+                               const int32_t* cu_seqlens, const float* advantages,
+                               const float* old_logp, const float* ref_logp,
+                               const qlora_policy_params* h, float* out, float* logp,
+                               float* stats, float* w, void* dlogits, int64_t ldd, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Kernel timing (benchmark instrumentation; not part of the method).
  * Between qlora_trace_begin and qlora_trace_end, every launch of a kernel whose
  * bit is set in `kernel_mask` (1 << qlora_kernel) records its own start and end

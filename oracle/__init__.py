@@ -4,7 +4,7 @@ TEST INFRASTRUCTURE ONLY: the parity reference for the GPU library.  Only the
 tests, ``__graft_entry__.smoke()`` and the benchmark's ``cpu_baseline`` leg may
 import it.  It shares no code with the GPU library and never calls it.
 
-Four parts:
+Six parts:
   * ``nf4_oracle.c`` (wrapped here): codebook, blockwise absmax quantisation,
     double quantisation of the constants, dequantisation, bf16 rounding.
   * ``linear.py``: the forward and backward of
@@ -14,6 +14,9 @@ Four parts:
     W' + (alpha / r) . B . A.
   * ``dropout.py``: the keep mask of that dropout (Philox4x32-10).
   * ``adamw.py``: the AdamW step on the adapters.
+  * ``act8.py``: activation checkpoints in 8 bits.
+  * ``loss.py``: token log-probabilities, the preference loss and the clipped
+    policy loss on packed logits, with their gradients.
 
 Pins (tests/test_oracle_*.py) tie every function here to something other than
 itself: scipy's normal quantile, printed figures from the pages, closed forms,
@@ -29,6 +32,7 @@ from .linear import (linear_fwd, linear_bwd, adapter_grads, lora_scale,  # noqa:
                      merge_adapter)
 from . import dropout  # noqa: F401
 from . import adamw  # noqa: F401
+from . import act8, loss  # noqa: F401
 
 NF4_BLOCK = 64
 DQ_BLOCK = 256
