@@ -148,24 +148,220 @@ __global__ __launch_bounds__(256) void k_act8_dequantize(const int8_t* __restric
   }
 }
 
-// Thread per column p and eight rank indices: dA[j][p] = scale inv sum_m
-// G[j][m] keep(m, p) scale[m] code[m][p].
+// ------------------------------------------------ adapter gradient from codes
+//     partial[j][k] = sum_m (G[j][m] scale[kb][m]) code[m][k]
+// on the matrix cores.  A code is exact in bf16, so the scale goes to the side
+// of G: per block of 64 columns the 16 RT rows of G are multiplied by it
+// instead of the 64 columns (less work up to rank 64), and only that product
+// needs more than 8 bits.  It is cut into three bf16 parts by truncation,
+// which together are the float32 value, and each part meets the same codes:
+// three MFMAs where one would leave dA with bf16 errors.
+//
+// A workgroup takes 128 columns (two blocks) of a token slice; its 4 waves take
+// interleaved 32-token steps.  Lane (i16, g) loads, for rows m = 8 g .. 8 g + 7
+// of a step, the 4 codes of columns 4 i16 .. 4 i16 + 3 of either block: MFMA
+// (h, t) handles columns 64 h + 4 i + t, one scale block each, and converting
+// byte t of the eight rows is the transpose.  The next step's loads are in
+// flight under a step's work.  The waves' sums are added in wave order through
+// LDS, 16 rank indices at a time, and leave as rows of 128 columns.
+constexpr int kGradCols = 128;
+
+template <int RT>
+struct GradStep {
+  uint32_t code[2][8];
+  uint8_t keep[2][8];      // dropout's stored bits, unused without
+  float4 scale[2][2];
+  float4 g[RT][2];
+};
+
+__device__ __forceinline__ float elem(const float4 (&v)[2], int e) {
+  const float4& q = v[e >> 2];
+  return (e & 3) == 0 ? q.x : (e & 3) == 1 ? q.y : (e & 3) == 2 ? q.z : q.w;
+}
+
+// high halves of two words: b's above a's
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
+
+__device__ __forceinline__ uint32_t nibble_mask(uint32_t n) {   // 4 keep bits -> 4 bytes
+  return (((n & 1u) | ((n & 2u) << 7) | ((n & 4u) << 14) | ((n & 8u) << 21))) * 0xFFu;
+}
+
+template <int RT, bool DROP>
 __global__ __launch_bounds__(256) void k_act8_grad(Act8GradJob J, int64_t M, int r) {
-  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int j0 = blockIdx.y * 8;
-  if (p >= J.K) return;
-  float acc[8] = {};
-  for (int64_t m = 0; m < M; ++m) {
-    float v = (float)J.codes[m * J.K + p] * J.scale[(p / kBlock) * J.ldg + m];
-    if (J.drop.thr != 0) {
-      const uint64_t e = (uint64_t)(m * J.K + p);
-      v = (dropout_byte(e & ~7ull, J.drop) >> (e & 7)) & 1u ? v : 0.f;
-    }
-    for (int j = 0; j < 8; ++j)
-      if (j0 + j < r) acc[j] = __builtin_fmaf(J.G[(int64_t)(j0 + j) * J.ldg + m], v, acc[j]);
+  __shared__ float red[4][16][kGradCols + 4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i16 = lane & 15, g = lane >> 4;
+  const int split = (int)(blockIdx.x % J.splits);
+  const int64_t p0 = (int64_t)(blockIdx.x / J.splits) * kGradCols;
+  const int64_t mchunk = ceil_div(ceil_div(M, J.splits), 128) * 128;
+  const int64_t mbeg = (int64_t)split * mchunk;
+  int64_t mend = mbeg + mchunk;
+  mend = mend < M ? mend : M;
+  // a last workgroup of one block reads it twice and drops the second
+  const int64_t blk[2] = {p0 / kBlock, p0 + kBlock < J.K ? p0 / kBlock + 1 : p0 / kBlock};
+
+  f32x4_t acc[2][4][RT];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int jt = 0; jt < RT; ++jt) acc[h][t][jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  const bool bits = DROP && J.drop.bits;
+  // a rank row past r feeds only rows of the partial that are never stored
+  const float* grow[RT];
+#pragma unroll
+  for (int jt = 0; jt < RT; ++jt) {
+    const int u = jt * 16 + i16;
+    grow[jt] = J.G + (int64_t)(u < r ? u : r - 1) * J.ldg + 8 * g;
   }
-  for (int j = 0; j < 8; ++j)
-    if (j0 + j < r) J.out[(int64_t)(j0 + j) * J.K + p] = J.alpha * (J.drop.inv * acc[j]);
+  // rows past M are clamped copies that meet G = 0 and scale = 0; mb + 31 is
+  // inside ldg, a multiple of 32
+  auto load = [&](int64_t mb, GradStep<RT>& s) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      int64_t m = mb + 8 * g + e;
+      m = m < M ? m : M - 1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = m * J.K + blk[h] * kBlock + 4 * i16;
+        s.code[h][e] = *reinterpret_cast<const uint32_t*>(J.codes + at);
+        if constexpr (DROP)
+          if (bits) s.keep[h][e] = J.drop.bits[at >> 3];
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4* p = reinterpret_cast<const float4*>(J.scale + blk[h] * J.ldg + mb + 8 * g);
+      s.scale[h][0] = p[0];
+      s.scale[h][1] = p[1];
+    }
+#pragma unroll
+    for (int jt = 0; jt < RT; ++jt) {
+      const float4* p = reinterpret_cast<const float4*>(grow[jt] + mb);
+      s.g[jt][0] = p[0];
+      s.g[jt][1] = p[1];
+    }
+  };
+  auto work = [&](int64_t mb, GradStep<RT>& s) {
+    if constexpr (DROP) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        int64_t m = mb + 8 * g + e;
+        m = m < M ? m : M - 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t at = (uint64_t)(m * J.K + blk[h] * kBlock + 4 * i16);
+          const uint32_t n = bits ? (uint32_t)s.keep[h][e] >> (at & 4)
+                                  : keep_nibble(dropout_words(at >> 2, J.drop), J.drop.thr);
+          s.code[h][e] &= nibble_mask(n);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 a[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        uint32_t f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          f[e] = __builtin_bit_cast(uint32_t,
+                                    (float)((int)(s.code[h][e] << (24 - 8 * t)) >> 24));
+        a[t] = make_uint4(high_halves(f[0], f[1]), high_halves(f[2], f[3]),
+                          high_halves(f[4], f[5]), high_halves(f[6], f[7]));
+      }
+#pragma unroll
+      for (int jt = 0; jt < RT; ++jt) {
+        uint32_t p1[8], p2[8], p3[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = elem(s.g[jt], e) * elem(s.scale[h], e);
+          p1[e] = __builtin_bit_cast(uint32_t, v);
+          const float rest = v - __builtin_bit_cast(float, p1[e] & 0xFFFF0000u);
+          p2[e] = __builtin_bit_cast(uint32_t, rest);
+          p3[e] = __builtin_bit_cast(uint32_t,
+                                     rest - __builtin_bit_cast(float, p2[e] & 0xFFFF0000u));
+        }
+        auto operand = [](const uint32_t (&p)[8]) {
+          return make_uint4(high_halves(p[0], p[1]), high_halves(p[2], p[3]),
+                            high_halves(p[4], p[5]), high_halves(p[6], p[7]));
+        };
+        const uint4 b1 = operand(p1), b2 = operand(p2), b3 = operand(p3);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          acc[h][t][jt] = mfma16x16x32(a[t], b3, acc[h][t][jt]);
+          acc[h][t][jt] = mfma16x16x32(a[t], b2, acc[h][t][jt]);
+          acc[h][t][jt] = mfma16x16x32(a[t], b1, acc[h][t][jt]);
+        }
+      }
+    }
+  };
+  const int64_t first = mbeg + 32 * wv;
+  const int64_t cnt = first < mend ? (mend - first + 127) / 128 : 0;
+  if constexpr (RT <= 4) {
+    if (cnt > 0) {
+      GradStep<RT> s0, s1;
+      load(first, s0);
+      int64_t i = 0;
+      for (; i + 1 < cnt; i += 2) {
+        load(first + 128 * (i + 1), s1);
+        __builtin_amdgcn_sched_barrier(0);
+        work(first + 128 * i, s0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 2 < cnt) load(first + 128 * (i + 2), s0);
+        __builtin_amdgcn_sched_barrier(0);
+        work(first + 128 * (i + 1), s1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (i < cnt) work(first + 128 * i, s0);
+    }
+  } else {
+    for (int64_t i = 0; i < cnt; ++i) {   // ranks above 64 fill the registers with sums
+      GradStep<RT> s0;
+      load(first + 128 * i, s0);
+      work(first + 128 * i, s0);
+    }
+  }
+  // D[i = 4 g + v][j16] of MFMA (h, t): column 64 h + 16 g + 4 v + t
+  float* base = J.partial + (int64_t)split * r * J.K + p0;
+#pragma unroll
+  for (int jt = 0; jt < RT; ++jt) {
+    if (jt > 0) __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        *reinterpret_cast<float4*>(&red[wv][i16][64 * h + 16 * g + 4 * v]) =
+            make_float4(acc[h][0][jt][v], acc[h][1][jt][v], acc[h][2][jt][v], acc[h][3][jt][v]);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int j = (tid >> 5) + 8 * q, p = 4 * (tid & 31);
+      float4 s = *reinterpret_cast<const float4*>(&red[0][j][p]);
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const float4 o = *reinterpret_cast<const float4*>(&red[w][j][p]);
+        s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
+      }
+      if constexpr (DROP) {
+        s.x *= J.drop.inv; s.y *= J.drop.inv; s.z *= J.drop.inv; s.w *= J.drop.inv;
+      }
+      if (jt * 16 + j < r && p0 + p < J.K)
+        *reinterpret_cast<float4*>(base + (int64_t)(jt * 16 + j) * J.K + p) = s;
+    }
+  }
+}
+
+template <int RT>
+hipError_t act8_grad_rt(const Act8GradJob& job, int64_t M, int r, hipStream_t s) {
+  const int64_t blocks = ceil_div(job.K, kGradCols) * job.splits;
+  return launch_kernel(job.drop.thr != 0 ? k_act8_grad<RT, true> : k_act8_grad<RT, false>,
+                       dim3((unsigned)blocks), dim3(256), s, job, M, r);
 }
 
 }  // namespace
@@ -187,9 +383,21 @@ hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64
                        rows, rows32, kb, tk, out);
 }
 
+// About two workgroups for each CU, at least one 32-token step for each wave.
+int act8_grad_splits(int64_t M, int64_t K) {
+  int64_t splits = ceil_div(512, ceil_div(K, kGradCols));
+  const int64_t maxs = ceil_div(M, 128);
+  if (splits > maxs) splits = maxs;
+  return (int)(splits < 1 ? 1 : splits);
+}
+
 hipError_t launch_act8_grad(const Act8GradJob& job, int64_t M, int r, hipStream_t s) {
-  return launch_kernel(k_act8_grad, dim3((unsigned)ceil_div(job.K, 256), (unsigned)ceil_div(r, 8)),
-                       dim3(256), s, job, M, r);
+  switch (skinny_rpad(r)) {
+    case 16: return act8_grad_rt<1>(job, M, r, s);
+    case 32: return act8_grad_rt<2>(job, M, r, s);
+    case 64: return act8_grad_rt<4>(job, M, r, s);
+    default: return act8_grad_rt<8>(job, M, r, s);
+  }
 }
 
 }  // namespace qnf4

@@ -125,9 +125,13 @@ LinearWs linear_layout(int64_t M, int64_t N, int64_t K, int r) {
 }
 
 // What the backward from an 8-bit checkpoint needs behind that layout: the
-// float32 G^T [r, mp].
-size_t act8_bytes(const LinearWs& w, int r) {
+// float32 G^T [r, mp], then dA's partials.
+size_t act8_g_bytes(const LinearWs& w, int r) {
   return align_up((size_t)r * w.mp * sizeof(float));
+}
+size_t act8_bytes(const LinearWs& w, int64_t M, int64_t K, int r) {
+  return act8_g_bytes(w, r) +
+         align_up((size_t)act8_grad_splits(M, K) * r * (size_t)K * sizeof(float));
 }
 
 template <typename T>
@@ -599,13 +603,12 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
   if (dX && !aligned(dX, 16)) return QLORA_ERR_INVALID_ARG;
   const int64_t N = W->rows, K = W->cols;
   const LinearWs L = linear_layout(M, N, K, r);
-  const size_t gtf_at = L.total;   // x8: float32 G^T behind the plain layout
-  const size_t need = L.total + (x8 ? act8_bytes(L, r) : 0);
+  const size_t need = L.total + (x8 ? act8_bytes(L, M, K, r) : 0);
   if (!ws || ws_bytes < need || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const float scale = alpha / (float)r;
   float* ahat_t = at<float>(ws, L.ahat_t);
-  float* gtf = at<float>(ws, gtf_at);
+  float* gtf = at<float>(ws, L.total);   // x8
   uint16_t* bt = at<uint16_t>(ws, L.bt);
   uint16_t* gs = at<uint16_t>(ws, L.gs);
   uint16_t* gt = at<uint16_t>(ws, L.gt);
@@ -656,10 +659,13 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
     for (int g = 0; g < kMaxGroups; ++g) gj[1].end[g] = grp->end[g];
   }
   if (x8) {
-    Act8GradJob aj{x8->codes, x8->scale, K, gtf, L.mp, scale, dA};
+    gj[0].splits = act8_grad_splits(M, K);
+    gj[0].partial = at<float>(ws, L.total + act8_g_bytes(L, r));
+    Act8GradJob aj{x8->codes, x8->scale, K, gtf, L.mp, gj[0].splits, gj[0].partial};
     aj.drop = dp;
     QL_TRY(launch_act8_grad(aj, M, r, s));
-    QL_TRY(launch_lora_grads(gj + 1, 1, M, r, s));
+    QL_TRY(launch_lora_grad_partials(gj + 1, 1, M, r, s));
+    QL_TRY(launch_lora_grad_reduce(gj, 2, r, s));
     return QLORA_OK;
   }
   QL_TRY(launch_lora_grads(gj, 2, M, r, s));
@@ -745,7 +751,7 @@ qlora_status qlora_act8_dequantize(const qlora_act8* a, qlora_dtype out_dtype, v
 
 size_t qlora_linear_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r) {
   const size_t plain = qlora_linear_workspace_bytes(M, N, K, r);
-  return plain == 0 ? 0 : plain + act8_bytes(linear_layout(M, N, K, r), r);
+  return plain == 0 ? 0 : plain + act8_bytes(linear_layout(M, N, K, r), M, K, r);
 }
 
 // The checkpoint's own checks for a linear whose weight has `cols` columns.

@@ -147,6 +147,10 @@ struct GradJob {
 int lora_grad_splits(int64_t M, int64_t P);
 // Both jobs' partial launch, then both reductions.
 hipError_t launch_lora_grads(const GradJob* jobs, int njobs, int64_t M, int r, hipStream_t s);
+// The two launches apart.
+hipError_t launch_lora_grad_partials(const GradJob* jobs, int njobs, int64_t M, int r,
+                                     hipStream_t s);
+hipError_t launch_lora_grad_reduce(const GradJob* jobs, int njobs, int r, hipStream_t s);
 
 // Checkpoints in 8 bits: codes int8 [rows, cols] and scales float32
 // [cols / 64][rows32] of X bf16 [rows, cols]; rows32 is rows up to 32.
@@ -154,19 +158,21 @@ hipError_t launch_act8_quantize(const uint16_t* x, int64_t rows, int64_t cols, i
                                 float* scale, hipStream_t s);
 hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64_t rows,
                                   int64_t cols, int bf16, void* out, hipStream_t s);
-// Adapter gradient from a checkpoint: out[j][k] = alpha sum_m G[j][m]
-// D(scale[k / 64][m] codes[m][k]), float32 [r][K]; G float32 [r, ldg] (zero
-// for m in [M, ldg)), ldg = M up to 32 is also the scales' row length.
+// Partials of the adapter gradient from a checkpoint: partial[split][j][k] =
+// sum over the split's tokens of G[j][m] D(scale[k / 64][m] codes[m][k]); G
+// float32 [r, ldg] (zero for m in [M, ldg)), ldg = M up to 32 is also the
+// scales' row length.  The reduction is launch_lora_grad_reduce's.
 struct Act8GradJob {
   const int8_t* codes;
   const float* scale;
   int64_t K;
   const float* G;
   int64_t ldg;
-  float alpha;
-  float* out;
+  int splits;
+  float* partial;
   DropoutParams drop{};
 };
+int act8_grad_splits(int64_t M, int64_t K);
 hipError_t launch_act8_grad(const Act8GradJob& job, int64_t M, int r, hipStream_t s);
 
 // The GEMMs split their inner loop into `splits` slices (one workgroup per

@@ -742,21 +742,27 @@ int lora_grad_splits(int64_t M, int64_t P) {
   return (int)splits;
 }
 
-hipError_t launch_lora_grads(const GradJob* jobs, int nj, int64_t M, int r, hipStream_t s) {
-  hipError_t e;
-  const int rpad = skinny_rpad(r);
-  switch (rpad) {
-    case 16: e = grads_rt<1>(jobs, nj, M, r, s); break;
-    case 32: e = grads_rt<2>(jobs, nj, M, r, s); break;
-    case 64: e = grads_rt<4>(jobs, nj, M, r, s); break;
-    default: e = grads_rt<8>(jobs, nj, M, r, s); break;
+hipError_t launch_lora_grad_partials(const GradJob* jobs, int nj, int64_t M, int r,
+                                     hipStream_t s) {
+  switch (skinny_rpad(r)) {
+    case 16: return grads_rt<1>(jobs, nj, M, r, s);
+    case 32: return grads_rt<2>(jobs, nj, M, r, s);
+    case 64: return grads_rt<4>(jobs, nj, M, r, s);
+    default: return grads_rt<8>(jobs, nj, M, r, s);
   }
-  if (e != hipSuccess) return e;
+}
+
+hipError_t launch_lora_grad_reduce(const GradJob* jobs, int nj, int r, hipStream_t s) {
   int64_t blocks = 0;
   for (int i = 0; i < nj; ++i) blocks += grad_reduce_blocks(jobs[i], r, grad_vec4(jobs[i], r));
   hipLaunchKernelGGL(k_lora_grad_reduce, dim3((unsigned)blocks), dim3(256), 0, s, jobs[0],
                      nj > 1 ? jobs[1] : jobs[0], nj, r);
   return hipGetLastError();
+}
+
+hipError_t launch_lora_grads(const GradJob* jobs, int nj, int64_t M, int r, hipStream_t s) {
+  const hipError_t e = launch_lora_grad_partials(jobs, nj, M, r, s);
+  return e == hipSuccess ? launch_lora_grad_reduce(jobs, nj, r, s) : e;
 }
 
 }  // namespace qnf4
