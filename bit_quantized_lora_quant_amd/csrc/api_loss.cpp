@@ -27,6 +27,9 @@ qlora_status check_sizes(const qlora_logits* z) {
   if (z->rows < 0 || z->vocab < 1 || z->ld < z->vocab) return QLORA_ERR_INVALID_ARG;
   if (z->rows >= kMaxRows || z->vocab >= kMaxVocab || z->ld >= kMaxVocab)
     return QLORA_ERR_UNSUPPORTED;
+  // the gradient launch's workgroups of 256 threads, in one grid dimension
+  if (z->rows * row_grad_slices(z->vocab, z->dtype == QLORA_BF16) >= kMaxRows)
+    return QLORA_ERR_UNSUPPORTED;
   return QLORA_OK;
 }
 
@@ -44,20 +47,27 @@ bool valid_grad(const qlora_logits* z, const void* dz, int64_t ldd) {
   return dz != z->data || ldd == z->ld;
 }
 
-// Scratch of one call: what the caller does not take of the rows' outputs, and
-// the sums of the sequences.
+LogitsView view(const qlora_logits* z, const int32_t* cu, int32_t nseq) {
+  return LogitsView{z->data, z->dtype == QLORA_BF16, z->rows, z->vocab, z->ld, z->labels, cu, nseq};
+}
+
+// Scratch of one call: what the caller does not take of the rows' outputs,
+// their slices, the sums of the sequences and the counter.
 struct LossWs {
-  size_t logp, stats, w, count, sums, total;
+  size_t logp, stats, w, part, count, sums, ticket, total;
 };
 LossWs loss_layout(const qlora_logits* z, int32_t sequences) {
   LossWs L;
   size_t off = 0;
   const size_t rows = (size_t)z->rows, seqs = (size_t)sequences;
-  L.logp = off;  off = align_up(off + rows * sizeof(float));
-  L.stats = off; off = align_up(off + rows * 2 * sizeof(float));
-  L.w = off;     off = align_up(off + rows * sizeof(float));
-  L.count = off; off = align_up(off + seqs * sizeof(int));
-  L.sums = off;  off = align_up(off + seqs * 4 * sizeof(double));
+  const int slices = row_slices(view(z, nullptr, 0));
+  L.logp = off;   off = align_up(off + rows * sizeof(float));
+  L.stats = off;  off = align_up(off + rows * sizeof(MaxSum));
+  L.w = off;      off = align_up(off + rows * sizeof(float));
+  L.part = off;   off = align_up(off + (slices > 1 ? rows * slices : 0) * sizeof(MaxSum));
+  L.count = off;  off = align_up(off + seqs * sizeof(int));
+  L.sums = off;   off = align_up(off + seqs * 3 * sizeof(double));
+  L.ticket = off; off = align_up(off + sizeof(uint32_t));
   L.total = off;
   return L;
 }
@@ -65,8 +75,10 @@ LossWs loss_layout(const qlora_logits* z, int32_t sequences) {
 template <typename T>
 T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
 
-LogitsView view(const qlora_logits* z, const int32_t* cu, int32_t nseq) {
-  return LogitsView{z->data, z->dtype == QLORA_BF16, z->rows, z->vocab, z->ld, z->labels, cu, nseq};
+RowOut row_out(void* ws, const LossWs& L, float* logp, float* stats, float* w) {
+  return RowOut{logp ? logp : at<float>(ws, L.logp),
+                stats ? reinterpret_cast<MaxSum*>(stats) : at<MaxSum>(ws, L.stats),
+                w ? w : at<float>(ws, L.w), at<MaxSum>(ws, L.part), at<uint32_t>(ws, L.ticket)};
 }
 
 bool opt4(const void* p) { return aligned(p, 4); }   // NULL passes
@@ -88,8 +100,8 @@ qlora_status qlora_token_logprobs(const qlora_logits* z, float* logp, float* sta
   if (z->rows == 0) return QLORA_OK;
   const LossWs L = loss_layout(z, 0);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
-  const RowOut o{logp, stats ? stats : at<float>(ws, L.stats), nullptr};
-  return hip_status(launch_row_stats(view(z, nullptr, 0), o, static_cast<hipStream_t>(stream)));
+  return hip_status(launch_row_logp(view(z, nullptr, 0), row_out(ws, L, logp, stats, nullptr),
+                                    static_cast<hipStream_t>(stream)));
 }
 
 qlora_status qlora_token_logprobs_bwd(const qlora_logits* z, const float* stats, const float* w,
@@ -101,8 +113,9 @@ qlora_status qlora_token_logprobs_bwd(const qlora_logits* z, const float* stats,
     return QLORA_ERR_INVALID_ARG;
   if (z->rows == 0) return QLORA_OK;
   if (!stats || !w || !dlogits) return QLORA_ERR_INVALID_ARG;
-  return hip_status(launch_row_grad(view(z, nullptr, 0), stats, w, grad_scale, dlogits, ldd,
-                                    static_cast<hipStream_t>(stream)));
+  return hip_status(launch_row_grad(view(z, nullptr, 0),
+                                    reinterpret_cast<const MaxSum*>(stats), w, grad_scale, dlogits,
+                                    ldd, static_cast<hipStream_t>(stream)));
 }
 
 qlora_status qlora_preference_loss(const qlora_logits* z, int32_t pairs, const int32_t* cu_seqlens,
@@ -127,8 +140,7 @@ qlora_status qlora_preference_loss(const qlora_logits* z, int32_t pairs, const i
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const LogitsView v = view(z, cu_seqlens, 2 * pairs);
-  const RowOut o{logp ? logp : at<float>(ws, L.logp), stats ? stats : at<float>(ws, L.stats),
-                 w ? w : at<float>(ws, L.w)};
+  const RowOut o = row_out(ws, L, logp, stats, w);
   const PreferenceArgs a{pairs,          ref_logp, h->beta,  h->label_smoothing, h->kind,
                          h->length_mean, loss,     seq_logp, rewards,            at<double>(ws, L.sums)};
   hipError_t e = launch_preference(v, o, a, s);
@@ -161,8 +173,7 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const LogitsView v = view(z, cu_seqlens, sequences);
-  const RowOut o{logp ? logp : at<float>(ws, L.logp), stats ? stats : at<float>(ws, L.stats),
-                 w ? w : at<float>(ws, L.w)};
+  const RowOut o = row_out(ws, L, logp, stats, w);
   const PolicyArgs a{advantages,          old_logp, ref_logp, 1 - h->clip_low, 1 + h->clip_high,
                      h->kl_coef,          h->reduction, h->token_advantages, out,
                      at<int>(ws, L.count), at<double>(ws, L.sums)};

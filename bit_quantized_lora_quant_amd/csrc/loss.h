@@ -16,11 +16,19 @@ struct LogitsView {
   int nseq;
 };
 
-// What a loss writes for each row: logp, stats (m, sum) and w = dLoss / dlogp.
+// Maximum m and sum of exp(z - m) of a row, or of a slice of one.
+struct MaxSum {
+  float m, s;
+};
+
+// What a loss writes for each row (logp, stats, w = dLoss / dlogp) and its
+// scratch: the slices' statistics [rows][row_slices] and a counter.
 struct RowOut {
   float* logp;
-  float* stats;
+  MaxSum* stats;
   float* w;
+  MaxSum* part;
+  uint32_t* ticket;
 };
 
 struct PreferenceArgs {
@@ -42,15 +50,20 @@ struct PolicyArgs {
   int reduction, token_adv;
   float* out;             // [3]
   int* count;             // scratch [nseq]: targets of each sequence
-  double* sums;           // scratch [nseq][4]: loss, kl, clipped, targets
+  double* sums;           // scratch [nseq][3]: loss, kl, clipped
 };
 
-hipError_t launch_row_stats(const LogitsView& v, const RowOut& o, hipStream_t s);
+// Slices of a row in the statistics launch.
+int row_slices(const LogitsView& v);
+// Workgroups of a row in the gradient launch.
+int64_t row_grad_slices(int64_t vocab, int bf16);
+// stats and logp of every row with a target
+hipError_t launch_row_logp(const LogitsView& v, const RowOut& o, hipStream_t s);
 hipError_t launch_preference(const LogitsView& v, const RowOut& o, const PreferenceArgs& a,
                              hipStream_t s);
 hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs& a, hipStream_t s);
 // dlogits = g w (1[y] - exp(z - m) / sum), row stride ldd
-hipError_t launch_row_grad(const LogitsView& v, const float* stats, const float* w,
+hipError_t launch_row_grad(const LogitsView& v, const MaxSum* stats, const float* w,
                            const float* g, void* dz, int64_t ldd, hipStream_t s);
 
 }  // namespace qnf4

@@ -1,5 +1,12 @@
 // Losses on packed logits: token log-probabilities, the preference loss over
-// pairs and the clipped policy loss, with the gradient of the logits.
+// pairs and the clipped policy loss, with the gradient of the logits.  The
+// logits are all of the work: a few bytes of loss per row of a vocabulary's
+// length, so every kernel that reads them is a stream bound by HBM, and the
+// arithmetic between the streams (float64, per row or sequence) is kept to
+// one small launch.
+//
+//     logp = z_y - m - log s,   m = max z,   s = sum exp(z - m)
+//     dz_v = w (1[v == y] - exp(z_v - m) / s),   w = dLoss / dlogp
 #include <cmath>
 
 #include "loss.h"
@@ -8,8 +15,19 @@
 namespace qnf4 {
 namespace {
 
-constexpr int kT = 256;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kT = 256;          // threads of a workgroup
+constexpr int kBatch = 8;        // 16-byte loads a thread has in flight
+constexpr float kInf = __builtin_inff();
+
+// log2(e) in two parts: the float32 nearest, and what it lacks.  Without the
+// second every exponential is off by 1.3e-8 of its argument to the same side,
+// which a sequence's sum of log ratios adds up.
+constexpr float kL2e = 0x1.715476p+0f;
+constexpr float kL2eLow = 0x1.4ae0bep-26f;
+// exp(d), d <= 0 or NaN
+__device__ __forceinline__ float exp_f32(float d) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kL2eLow, d * kL2e));
+}
 
 template <typename T>
 __device__ __forceinline__ float ld1(const T* p) {
@@ -21,116 +39,336 @@ __device__ __forceinline__ void st1(T* p, float v) {
   if constexpr (sizeof(T) == 2) *p = to_bf16(v);
   else *p = v;
 }
+template <typename T>
+constexpr int vec() { return 16 / (int)sizeof(T); }   // values of a 16-byte chunk
 
-__device__ __forceinline__ float exp2_f32(float x) { return __builtin_amdgcn_exp2f(x); }
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& q, float (&f)[vec<T>()]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      f[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+      f[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+    } else {
+      f[i] = __builtin_bit_cast(float, w[i]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&f)[vec<T>()]) {
+  if constexpr (sizeof(T) == 2)
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  else
+    return __builtin_bit_cast(uint4, f32x4_t{f[0], f[1], f[2], f[3]});
+}
+// a chunk of -inf: what stands in for values past a row's end
+template <typename T>
+__device__ __forceinline__ uint4 no_values() {
+  const uint32_t w = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+  return make_uint4(w, w, w, w);
+}
+
+// A row of any alignment: `head` values up to the first 16-byte boundary, `nb`
+// whole chunks from there, and a tail; head and tail (at most 14 values) are
+// the edge, one value to a thread.
+template <typename T>
+struct Row {
+  const T* z;
+  int head, edge;
+  int64_t nb, vocab;
+  __device__ __forceinline__ Row(const LogitsView& v, int64_t t) {
+    z = static_cast<const T*>(v.z) + t * v.ld;
+    vocab = v.vocab;
+    const int64_t off = (int64_t)((uintptr_t)z & 15) / (int64_t)sizeof(T);
+    const int64_t h = off ? vec<T>() - off : 0;
+    head = (int)(h < vocab ? h : vocab);
+    nb = (vocab - head) / vec<T>();
+    edge = (int)(vocab - nb * vec<T>());
+  }
+  __device__ __forceinline__ const uint4* body() const {
+    return reinterpret_cast<const uint4*>(z + head);
+  }
+  // value index of edge element k
+  __device__ __forceinline__ int64_t edge_at(int k) const {
+    return k < head ? k : nb * vec<T>() + k;
+  }
+};
 
 // sequence bounds, clamped to the rows there are
 __device__ __forceinline__ int64_t cu_at(const LogitsView& v, int i) {
   const int64_t c = v.cu[i];
   return c < 0 ? 0 : c > v.rows ? v.rows : c;
 }
-__device__ __forceinline__ bool has_target(const LogitsView& v, int64_t t) {
-  if (v.labels[t] < 0) return false;
-  return !v.cu || (t >= cu_at(v, 0) && t < cu_at(v, v.nseq));
+__device__ __forceinline__ bool outside(const LogitsView& v, int64_t t) {
+  return v.cu && (t < cu_at(v, 0) || t >= cu_at(v, v.nseq));
 }
 
-// (maximum, sum of exp(z - maximum)) of two parts of a row
-struct MaxSum {
-  float m, s;
-};
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
-  const float m = fmaxf(a.m, b.m);
-  if (m == -__builtin_inff()) return MaxSum{m, a.s + b.s};
-  return MaxSum{m, a.s * exp2_f32((a.m - m) * kLog2e) + b.s * exp2_f32((b.m - m) * kLog2e)};
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) x = fmaxf(x, __shfl_xor(x, k));
+  return x;
 }
-
-template <typename T>
-__global__ __launch_bounds__(kT) void k_row_stats(LogitsView v, RowOut o) {
-  __shared__ MaxSum red[kT];
-  const int64_t t = blockIdx.x;
-  const int64_t y = v.labels[t];
-  if (!has_target(v, t) || y >= v.vocab) {
-    if (threadIdx.x == 0) {
-      const float bad = has_target(v, t) ? __builtin_nanf("") : 0.f;
-      o.stats[2 * t] = 0.f;
-      o.stats[2 * t + 1] = bad;
-      o.logp[t] = bad;
-    }
-    return;
-  }
-  const T* z = static_cast<const T*>(v.z) + t * v.ld;
-  MaxSum a{-__builtin_inff(), 0.f};
-  for (int64_t e = threadIdx.x; e < v.vocab; e += kT) {
-    const float x = ld1(z + e);
-    if (x != x) a.s = x;                               // NaN: the row's sum is NaN
-    else if (x != -__builtin_inff()) a = join(a, MaxSum{x, 1.f});
-  }
-  red[threadIdx.x] = a;
-  __syncthreads();
-  for (int k = kT / 2; k > 0; k >>= 1) {
-    if ((int)threadIdx.x < k) red[threadIdx.x] = join(red[threadIdx.x], red[threadIdx.x + k]);
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    a = red[0];
-    o.stats[2 * t] = a.m;
-    o.stats[2 * t + 1] = a.s;
-    o.logp[t] = (float)((double)ld1(z + y) - (double)a.m - std::log((double)a.s));
-  }
-}
-
-template <typename T>
-__global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const float* stats, const float* w,
-                                                 const float* g, T* dz, int64_t ldd) {
-  const int64_t t = blockIdx.x;
-  const int64_t y = v.labels[t];
-  const float c = has_target(v, t) ? w[t] * (g ? *g : 1.f) : 0.f;
-  const T* z = static_cast<const T*>(v.z) + t * v.ld;
-  T* d = dz + t * ldd;
-  if (c == 0.f) {
-    for (int64_t e = threadIdx.x; e < v.vocab; e += kT) d[e] = 0;
-    return;
-  }
-  const float m = stats[2 * t], sum = stats[2 * t + 1];
-  for (int64_t e = threadIdx.x; e < v.vocab; e += kT) {
-    const float p = exp2_f32((ld1(z + e) - m) * kLog2e) / sum;
-    st1(d + e, e == y ? c * (1.f - p) : -c * p);
-  }
-}
-
-// sum over the workgroup, in a fixed order; the result in every thread
-__device__ __forceinline__ double wg_sum(double x, double* red) {
-  red[threadIdx.x] = x;
-  __syncthreads();
-  for (int k = kT / 2; k > 0; k >>= 1) {
-    if ((int)threadIdx.x < k) red[threadIdx.x] += red[threadIdx.x + k];
-    __syncthreads();
-  }
-  x = red[0];
-  __syncthreads();
+template <typename F>
+__device__ __forceinline__ F wave_sum(F x) {
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) x += __shfl_xor(x, k);
   return x;
 }
 
+// Joins the threads' parts of a row in a fixed order; the result in every
+// thread.  red: 2 floats for each wave.
+template <int W>
+__device__ __forceinline__ MaxSum wg_join(MaxSum a, float (*red)[2]) {
+  const int wv = threadIdx.x >> 6;
+  float m = wave_max(a.m);
+  if ((threadIdx.x & 63) == 0) red[wv][0] = m;
+  __syncthreads();
+  m = red[0][0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) m = fmaxf(m, red[w][0]);
+  // a thread without values has m = -inf and s = 0 (or NaN, which stays)
+  const float s = wave_sum(a.m == m ? a.s : a.s * exp_f32(a.m - m));
+  if ((threadIdx.x & 63) == 0) red[wv][1] = s;
+  __syncthreads();
+  float t = red[0][1];
+#pragma unroll
+  for (int w = 1; w < W; ++w) t += red[w][1];
+  return MaxSum{m, t};
+}
+
+// Adds a batch of chunks to a thread's part: the maximum first, so that the
+// sum is rescaled once a batch.
+template <typename T, int N>
+__device__ __forceinline__ void add_batch(MaxSum& a, const uint4 (&q)[N]) {
+  float m = a.m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float f[vec<T>()];
+    unpack<T>(q[i], f);
+#pragma unroll
+    for (int e = 0; e < vec<T>(); ++e) m = fmaxf(m, f[e]);
+  }
+  if (m > a.m) {
+    a.s *= exp_f32(a.m - m);
+    a.m = m;
+  }
+  const float ref = m == -kInf ? 0.f : m;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float f[vec<T>()];
+    unpack<T>(q[i], f);
+#pragma unroll
+    for (int e = 0; e < vec<T>(); ++e) s += exp_f32(f[e] - ref);
+  }
+  a.s += s;
+}
+__device__ __forceinline__ void add_value(MaxSum& a, float x) {
+  if (x > a.m) {
+    a.s *= exp_f32(a.m - x);
+    a.m = x;
+  }
+  a.s += exp_f32(x - (a.m == -kInf ? 0.f : a.m));
+}
+
+// ------------------------------------------------------------ row statistics
+// Workgroup (row, slice of its chunks); 8 loads a thread in flight.  One slice
+// writes the row's result, several their parts.
 template <typename T>
-__device__ __forceinline__ double row_logp(const LogitsView& v, const float* stats, int64_t t) {
+__global__ __launch_bounds__(kT) void k_row_stats(LogitsView v, RowOut o, int slices) {
+  __shared__ float red[kT / 64][2];
+  if (blockIdx.x == 0 && threadIdx.x == 0 && o.ticket) *o.ticket = 0;
+  const int64_t t = blockIdx.x / (unsigned)slices;
+  const int sl = (int)(blockIdx.x - t * slices);
+  if (t >= v.rows) return;
   const int64_t y = v.labels[t];
-  const float sum = stats[2 * t + 1];
-  if (y >= v.vocab) return (double)__builtin_nanf("");
+  if (y < 0 || y >= v.vocab || outside(v, t)) {
+    if (sl == 0 && threadIdx.x == 0) {
+      const float none = y < v.vocab || outside(v, t) ? 0.f : __builtin_nanf("");
+      o.stats[t] = MaxSum{0.f, none};
+      o.logp[t] = none;
+    }
+    return;
+  }
+  const Row<T> r(v, t);
+  const int64_t per = ceil_div(r.nb, slices);
+  const int64_t c0 = sl * per, c1 = c0 + per < r.nb ? c0 + per : r.nb;
+  const uint4* b = r.body();
+  MaxSum a{-kInf, 0.f};
+  int64_t c = c0 + threadIdx.x;
+  for (; c0 < c1 && c - threadIdx.x + kT * kBatch <= c1; c += kT * kBatch) {
+    uint4 q[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) q[i] = b[c + kT * i];
+    add_batch<T>(a, q);
+  }
+  if (c - threadIdx.x < c1) {
+    uint4 q[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      q[i] = c + kT * i < c1 ? b[c + kT * i] : no_values<T>();
+    add_batch<T>(a, q);
+  }
+  if (sl == 0 && (int)threadIdx.x < r.edge) add_value(a, ld1(r.z + r.edge_at(threadIdx.x)));
+  a = wg_join<kT / 64>(a, red);
+  if (threadIdx.x != 0) return;
+  if (slices > 1) {
+    o.part[t * slices + sl] = a;
+  } else {
+    o.stats[t] = a;
+    o.logp[t] = (float)((double)ld1(r.z + y) - (double)a.m - std::log((double)a.s));
+  }
+}
+
+// The statistics of row t, joined from its slices in their order if there are
+// several (and then stored with logp).  Rows with a target only.
+template <typename T>
+__device__ __forceinline__ double row_logp(const LogitsView& v, const RowOut& o, int slices,
+                                           int64_t t) {
+  const int64_t y = v.labels[t];
+  if (y >= v.vocab) return (double)__builtin_nanf("");   // written with the statistics
+  MaxSum a;
+  if (slices > 1) {
+    const MaxSum* p = o.part + t * slices;
+    float m = -kInf;
+    for (int i = 0; i < slices; ++i) m = fmaxf(m, p[i].m);
+    float s = 0.f;
+    for (int i = 0; i < slices; ++i) s += p[i].m == m ? p[i].s : p[i].s * exp_f32(p[i].m - m);
+    a = MaxSum{m, s};
+    o.stats[t] = a;
+  } else {
+    a = o.stats[t];
+  }
   const float zy = ld1(static_cast<const T*>(v.z) + t * v.ld + y);
-  return (double)zy - (double)stats[2 * t] - std::log((double)sum);
+  const double l = (double)zy - (double)a.m - std::log((double)a.s);
+  if (slices > 1) o.logp[t] = (float)l;
+  return l;
 }
 
 template <typename T>
-__global__ __launch_bounds__(kT) void k_preference(LogitsView v, RowOut o, PreferenceArgs a) {
-  __shared__ double red[kT];
+__global__ __launch_bounds__(kT) void k_row_join(LogitsView v, RowOut o, int slices) {
+  const int64_t t = (int64_t)blockIdx.x * kT + threadIdx.x;
+  if (t < v.rows && v.labels[t] >= 0) row_logp<T>(v, o, slices, t);
+}
+
+// --------------------------------------------------------------- row gradient
+// Workgroup (row, 256 x 8 chunks): loads, then the same chunks' stores.  Rows
+// go from the last to the first: the statistics launch left the last ones in
+// the Infinity Cache.  A row of weight 0 is written and not read.
+template <typename T>
+__global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const MaxSum* stats, const float* w,
+                                                 const float* g, T* dz, int64_t ldd, int slices) {
+  const int64_t tr = blockIdx.x / (unsigned)slices;
+  const int sl = (int)(blockIdx.x - tr * slices);
+  const int64_t t = v.rows - 1 - tr;
+  const int64_t y = v.labels[t];
+  const float c = y < 0 ? 0.f : w[t] * (g ? *g : 1.f);
+  const Row<T> r(v, t);
+  T* const d = dz + t * ldd;
+  const bool even = (((uintptr_t)d ^ (uintptr_t)r.z) & 15) == 0;   // 16-byte stores fit
+  const int64_t c0 = (int64_t)sl * kT * kBatch + threadIdx.x;
+  const uint4* b = r.body();
+  uint4* const db = reinterpret_cast<uint4*>(d + r.head);
+  auto store = [&](int64_t k, const uint4& q) {
+    if (even) {
+      __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, q),
+                                  reinterpret_cast<u32x4_t*>(db + k));
+    } else {
+      float f[vec<T>()];
+      unpack<T>(q, f);
+#pragma unroll
+      for (int e = 0; e < vec<T>(); ++e) st1(d + r.head + k * vec<T>() + e, f[e]);
+    }
+  };
+  const bool at_edge = sl == 0 && (int)threadIdx.x < r.edge;
+  if (c == 0.f) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (c0 + kT * i < r.nb) store(c0 + kT * i, make_uint4(0u, 0u, 0u, 0u));
+    if (at_edge) d[r.edge_at(threadIdx.x)] = 0;
+    return;
+  }
+  uint4 q[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    if (c0 + kT * i < r.nb) q[i] = b[c0 + kT * i];
+  const MaxSum a = stats[t];
+  const float k = -c / a.s;
+  const int64_t yb = y - r.head;
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int64_t at = c0 + kT * i;
+    if (at >= r.nb) continue;
+    float f[vec<T>()];
+    unpack<T>(q[i], f);
+#pragma unroll
+    for (int e = 0; e < vec<T>(); ++e) f[e] = k * exp_f32(f[e] - a.m);
+    if ((uint64_t)(yb - at * vec<T>()) < (uint64_t)vec<T>()) {
+#pragma unroll
+      for (int e = 0; e < vec<T>(); ++e) f[e] += at * vec<T>() + e == yb ? c : 0.f;
+    }
+    store(at, pack<T>(f));
+  }
+  if (at_edge) {
+    const int64_t at = r.edge_at(threadIdx.x);
+    st1(d + at, k * exp_f32(ld1(r.z + at) - a.m) + (at == y ? c : 0.f));
+  }
+}
+
+// ------------------------------------------------------- between the streams
+// Sum over the workgroup in a fixed order, the result in every thread; red: a
+// double for each wave.
+__device__ __forceinline__ double wg_sum(double x, double* red) {
+  x = wave_sum(x);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = red[0];
+#pragma unroll
+  for (int w = 1; w < kT / 64; ++w) x += red[w];
+  return x;
+}
+
+// Whether this workgroup is the last of n to come here.  What each wrote
+// through thread 0 before is then visible to the last one's device_load.
+__device__ __forceinline__ bool last_of(uint32_t* ticket, uint32_t n) {
+  __shared__ uint32_t k;
+  if (threadIdx.x == 0)
+    k = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return k == n - 1;
+}
+__device__ __forceinline__ double device_load(const double* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void device_store(double* p, double v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// w of the rows in no sequence, shared out over the workgroups
+__device__ __forceinline__ void zero_outside(const LogitsView& v, float* w) {
+  const int64_t b = cu_at(v, 0), e = cu_at(v, v.nseq);
+  const int64_t step = (int64_t)gridDim.x * kT, at = (int64_t)blockIdx.x * kT + threadIdx.x;
+  for (int64_t t = at; t < b; t += step) w[t] = 0.f;
+  for (int64_t t = e + at; t < v.rows; t += step) w[t] = 0.f;
+}
+
+// Workgroup per pair; the last one adds the pairs' losses in their order.
+template <typename T>
+__global__ __launch_bounds__(kT) void k_preference(LogitsView v, RowOut o, PreferenceArgs a,
+                                                   int slices) {
+  __shared__ double red[kT / 64];
   const int p = blockIdx.x;
   double lr[2], n[2];
+  zero_outside(v, o.w);
   for (int i = 0; i < 2; ++i) {
     const int64_t b = cu_at(v, 2 * p + i), e = cu_at(v, 2 * p + i + 1);
     double lp = 0, rf = 0, cnt = 0;
     for (int64_t t = b + threadIdx.x; t < e; t += kT) {
       if (v.labels[t] < 0) continue;
-      const double l = row_logp<T>(v, o.stats, t);
+      const double l = row_logp<T>(v, o, slices, t);
       lp += l;
       rf += l - (a.ref ? (double)a.ref[t] : 0.0);
       cnt += 1;
@@ -148,13 +386,12 @@ __global__ __launch_bounds__(kT) void k_preference(LogitsView v, RowOut o, Prefe
   const double h = lr[0] - lr[1], x = a.beta * h;
   double loss, dh;
   if (a.kind == 0) {
-    // log(1 + exp(-x)) and log(1 + exp(x)) without overflow
-    const double u = std::log1p(std::exp(-std::fabs(x)));
+    // log(1 + exp(-x)), log(1 + exp(x)) and both sigmoids without overflow
+    const double ex = std::exp(-std::fabs(x)), u = std::log1p(ex);
     const double ln = u + (x < 0 ? -x : 0), lp = u + (x > 0 ? x : 0);
+    const double sp = x >= 0 ? 1 / (1 + ex) : ex / (1 + ex);
+    const double sn = x >= 0 ? ex / (1 + ex) : 1 / (1 + ex);
     loss = (1 - a.smooth) * ln + a.smooth * lp;
-    const double ex = std::exp(-std::fabs(x));
-    const double sp = x >= 0 ? 1 / (1 + ex) : ex / (1 + ex);     // sigmoid(x)
-    const double sn = x >= 0 ? ex / (1 + ex) : 1 / (1 + ex);     // sigmoid(-x)
     dh = -a.beta * ((1 - a.smooth) * sn - a.smooth * sp);
     if (x != x) loss = dh = x;
   } else if (a.kind == 1) {
@@ -165,30 +402,21 @@ __global__ __launch_bounds__(kT) void k_preference(LogitsView v, RowOut o, Prefe
     loss = d * d;
     dh = 2 * d;
   }
-  if (threadIdx.x == 0) a.pair_loss[p] = loss;
   for (int i = 0; i < 2; ++i) {
     const int64_t b = cu_at(v, 2 * p + i), e = cu_at(v, 2 * p + i + 1);
     const float wt = (float)((i ? -dh : dh) / n[i] / a.pairs);
     for (int64_t t = b + threadIdx.x; t < e; t += kT) o.w[t] = v.labels[t] < 0 ? 0.f : wt;
   }
-}
-
-// rows in no sequence
-__global__ __launch_bounds__(kT) void k_outside(LogitsView v, RowOut o) {
-  const int64_t t = (int64_t)blockIdx.x * kT + threadIdx.x;
-  if (t < v.rows && (t < cu_at(v, 0) || t >= cu_at(v, v.nseq))) o.w[t] = 0.f;
-}
-
-__global__ __launch_bounds__(kT) void k_preference_mean(PreferenceArgs a) {
-  __shared__ double red[kT];
-  double x = 0;
-  for (int p = threadIdx.x; p < a.pairs; p += kT) x += a.pair_loss[p];
-  x = wg_sum(x, red);
-  if (threadIdx.x == 0) *a.loss = (float)(x / a.pairs);
+  if (threadIdx.x == 0) device_store(a.pair_loss + p, loss);
+  if (!last_of(o.ticket, gridDim.x)) return;
+  double tot = 0;
+  for (int k = threadIdx.x; k < a.pairs; k += kT) tot += device_load(a.pair_loss + k);
+  tot = wg_sum(tot, red);
+  if (threadIdx.x == 0) *a.loss = (float)(tot / a.pairs);
 }
 
 __global__ __launch_bounds__(kT) void k_policy_count(LogitsView v, PolicyArgs a) {
-  __shared__ double red[kT];
+  __shared__ double red[kT / 64];
   const int i = blockIdx.x;
   double n = 0;
   for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += kT) n += v.labels[t] >= 0;
@@ -196,109 +424,148 @@ __global__ __launch_bounds__(kT) void k_policy_count(LogitsView v, PolicyArgs a)
   if (threadIdx.x == 0) a.count[i] = (int)n;
 }
 
-template <typename T>
-__global__ __launch_bounds__(kT) void k_policy(LogitsView v, RowOut o, PolicyArgs a) {
-  __shared__ double red[kT];
-  const int i = blockIdx.x;
-  double tot = 0, filled = 0;
-  for (int j = threadIdx.x; j < v.nseq; j += kT) {
-    tot += a.count[j];
-    filled += a.count[j] > 0;
+// All targets, and the sequences that have any.
+struct Totals {
+  double targets, filled;
+};
+__device__ __forceinline__ Totals totals(const PolicyArgs& a, int nseq, double* red) {
+  double n = 0, f = 0;
+  for (int j = threadIdx.x; j < nseq; j += kT) {
+    n += a.count[j];
+    f += a.count[j] > 0;
   }
-  tot = wg_sum(tot, red);
-  filled = wg_sum(filled, red);
-  const double share = a.reduction == 0 ? (tot > 0 ? 1 / tot : 0)
-                                        : (a.count[i] > 0 ? 1 / (a.count[i] * filled) : 0);
-  double loss = 0, kls = 0, hits = 0;
+  n = wg_sum(n, red);
+  return Totals{n, wg_sum(f, red)};
+}
+// weight of one target of sequence i in the mean
+__device__ __forceinline__ double share_of(const PolicyArgs& a, const Totals& n, int i) {
+  if (a.reduction == 0) return n.targets > 0 ? 1 / n.targets : 0;
+  return a.count[i] > 0 ? 1 / (a.count[i] * n.filled) : 0;
+}
+
+struct Term {
+  double loss, kl, clipped, dlogp;
+};
+__device__ __forceinline__ Term policy_term(const PolicyArgs& a, double l, double A, int64_t t) {
+  const double r = a.old_logp ? std::exp(l - (double)a.old_logp[t]) : (l == l ? 1.0 : l);
+  const double u = -A * r, c = -A * (r < a.lo ? a.lo : r > a.hi ? a.hi : r);
+  const bool cut = c > u;
+  Term x{cut ? c : u, 0.0, cut ? 1.0 : 0.0, cut ? 0.0 : u};
+  if (a.ref) {
+    const double d = (double)a.ref[t] - l, em = std::expm1(d);
+    x.kl = em - d;
+    x.loss += a.kl_coef * x.kl;
+    x.dlogp -= a.kl_coef * em;
+  }
+  return x;
+}
+
+// Workgroup per sequence; the last one adds the sequences' sums in their order.
+template <typename T>
+__global__ __launch_bounds__(kT) void k_policy(LogitsView v, RowOut o, PolicyArgs a, int slices) {
+  __shared__ double red[kT / 64];
+  const int i = blockIdx.x;
+  zero_outside(v, o.w);
+  const Totals n = totals(a, v.nseq, red);
+  const double share = share_of(a, n, i);
+  double loss = 0, kl = 0, cut = 0;
   for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += kT) {
     if (v.labels[t] < 0) {
       o.w[t] = 0.f;
       continue;
     }
-    const double l = row_logp<T>(v, o.stats, t);
     const double A = (double)(a.token_adv ? a.adv[t] : a.adv[i]);
-    const double r = std::exp(l - (a.old_logp ? (double)a.old_logp[t] : l));
-    const double u = -A * r, c = -A * (r < a.lo ? a.lo : r > a.hi ? a.hi : r);
-    const bool cut = c > u;
-    double term = cut ? c : u, dterm = cut ? 0.0 : u;
-    if (a.ref) {
-      const double d = (double)a.ref[t] - l, em = std::expm1(d), kl = em - d;
-      term += a.kl_coef * kl;
-      dterm -= a.kl_coef * em;
-      kls += kl;
-    }
-    loss += term;
-    hits += cut;
-    o.w[t] = (float)(share * dterm);
+    const Term x = policy_term(a, row_logp<T>(v, o, slices, t), A, t);
+    loss += x.loss;
+    kl += x.kl;
+    cut += x.clipped;
+    o.w[t] = (float)(share * x.dlogp);
   }
   loss = wg_sum(loss, red);
-  kls = wg_sum(kls, red);
-  hits = wg_sum(hits, red);
+  kl = wg_sum(kl, red);
+  cut = wg_sum(cut, red);
   if (threadIdx.x == 0) {
-    a.sums[4 * i] = share * loss;
-    a.sums[4 * i + 1] = share * kls;
-    a.sums[4 * i + 2] = hits;
-    a.sums[4 * i + 3] = tot;
+    device_store(a.sums + 3 * i, share * loss);
+    device_store(a.sums + 3 * i + 1, share * kl);
+    device_store(a.sums + 3 * i + 2, cut);
   }
-}
-
-__global__ __launch_bounds__(kT) void k_policy_sum(int nseq, PolicyArgs a) {
-  __shared__ double red[kT];
+  if (!last_of(o.ticket, gridDim.x)) return;
   double x[3] = {0, 0, 0};
-  for (int i = threadIdx.x; i < nseq; i += kT)
-    for (int k = 0; k < 3; ++k) x[k] += a.sums[4 * i + k];
+  for (int j = threadIdx.x; j < v.nseq; j += kT)
+    for (int k = 0; k < 3; ++k) x[k] += device_load(a.sums + 3 * j + k);
   for (int k = 0; k < 3; ++k) x[k] = wg_sum(x[k], red);
   if (threadIdx.x == 0) {
     a.out[0] = (float)x[0];
     a.out[1] = (float)x[1];
-    a.out[2] = (float)(x[2] / fmax(a.sums[3], 1.0));
+    a.out[2] = (float)(x[2] / (n.targets > 0 ? n.targets : 1));
   }
+}
+
+// 16-byte chunks of a row, at most (one that starts between boundaries has fewer)
+int64_t row_chunks(int64_t vocab, int bf16) { return ceil_div(vocab, bf16 ? 8 : 4); }
+
+hipError_t row_stats(const LogitsView& v, const RowOut& o, int slices, hipStream_t s) {
+  const int64_t blocks = v.rows > 0 ? v.rows * slices : 1;   // one sets the counter
+  return launch_kernel(v.bf16 ? k_row_stats<uint16_t> : k_row_stats<float>,
+                       dim3((unsigned)blocks), dim3(kT), s, v, o, slices);
 }
 
 }  // namespace
 
-hipError_t launch_row_stats(const LogitsView& v, const RowOut& o, hipStream_t s) {
-  if (v.rows == 0) return hipSuccess;
-  return launch_kernel(v.bf16 ? k_row_stats<uint16_t> : k_row_stats<float>,
-                       dim3((unsigned)v.rows), dim3(kT), s, v, o);
+// Enough workgroups to fill the chip where the rows alone do not, each with a
+// batch of loads for every thread.
+int row_slices(const LogitsView& v) {
+  if (v.rows == 0) return 1;
+  const int64_t chunks = row_chunks(v.vocab, v.bf16);
+  int64_t n = ceil_div(1024, v.rows);
+  const int64_t most = ceil_div(chunks, (int64_t)kT * kBatch / 2);
+  if (n > most) n = most;
+  return (int)(n < 1 ? 1 : n);
 }
 
-hipError_t launch_row_grad(const LogitsView& v, const float* stats, const float* w,
+int64_t row_grad_slices(int64_t vocab, int bf16) {
+  return ceil_div(row_chunks(vocab, bf16), (int64_t)kT * kBatch);
+}
+
+hipError_t launch_row_logp(const LogitsView& v, const RowOut& o, hipStream_t s) {
+  const int slices = row_slices(v);
+  hipError_t e = row_stats(v, o, slices, s);
+  if (e == hipSuccess && slices > 1)
+    e = launch_kernel(v.bf16 ? k_row_join<uint16_t> : k_row_join<float>,
+                      dim3((unsigned)ceil_div(v.rows, kT)), dim3(kT), s, v, o, slices);
+  return e;
+}
+
+hipError_t launch_row_grad(const LogitsView& v, const MaxSum* stats, const float* w,
                            const float* g, void* dz, int64_t ldd, hipStream_t s) {
   if (v.rows == 0) return hipSuccess;
+  const int slices = (int)row_grad_slices(v.vocab, v.bf16);
+  const dim3 grid((unsigned)(v.rows * slices));
   if (v.bf16)
-    return launch_kernel(k_row_grad<uint16_t>, dim3((unsigned)v.rows), dim3(kT), s, v, stats, w, g,
-                         static_cast<uint16_t*>(dz), ldd);
-  return launch_kernel(k_row_grad<float>, dim3((unsigned)v.rows), dim3(kT), s, v, stats, w, g,
-                       static_cast<float*>(dz), ldd);
-}
-
-static hipError_t launch_outside(const LogitsView& v, const RowOut& o, hipStream_t s) {
-  if (v.rows == 0) return hipSuccess;
-  return launch_kernel(k_outside, dim3((unsigned)ceil_div(v.rows, kT)), dim3(kT), s, v, o);
+    return launch_kernel(k_row_grad<uint16_t>, grid, dim3(kT), s, v, stats, w, g,
+                         static_cast<uint16_t*>(dz), ldd, slices);
+  return launch_kernel(k_row_grad<float>, grid, dim3(kT), s, v, stats, w, g,
+                       static_cast<float*>(dz), ldd, slices);
 }
 
 hipError_t launch_preference(const LogitsView& v, const RowOut& o, const PreferenceArgs& a,
                              hipStream_t s) {
-  hipError_t e = launch_row_stats(v, o, s);
-  if (e == hipSuccess) e = launch_outside(v, o, s);
-  if (e == hipSuccess)
-    e = launch_kernel(v.bf16 ? k_preference<uint16_t> : k_preference<float>,
-                      dim3((unsigned)a.pairs), dim3(kT), s, v, o, a);
-  if (e == hipSuccess) e = launch_kernel(k_preference_mean, dim3(1), dim3(kT), s, a);
-  return e;
+  const int slices = row_slices(v);
+  const hipError_t e = row_stats(v, o, slices, s);
+  if (e != hipSuccess) return e;
+  return launch_kernel(v.bf16 ? k_preference<uint16_t> : k_preference<float>,
+                       dim3((unsigned)a.pairs), dim3(kT), s, v, o, a, slices);
 }
 
 hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs& a,
                          hipStream_t s) {
-  hipError_t e = launch_row_stats(v, o, s);
-  if (e == hipSuccess) e = launch_outside(v, o, s);
+  const int slices = row_slices(v);
+  hipError_t e = row_stats(v, o, slices, s);
   if (e == hipSuccess)
     e = launch_kernel(k_policy_count, dim3((unsigned)v.nseq), dim3(kT), s, v, a);
   if (e == hipSuccess)
     e = launch_kernel(v.bf16 ? k_policy<uint16_t> : k_policy<float>, dim3((unsigned)v.nseq),
-                      dim3(kT), s, v, o, a);
-  if (e == hipSuccess) e = launch_kernel(k_policy_sum, dim3(1), dim3(kT), s, v.nseq, a);
+                      dim3(kT), s, v, o, a, slices);
   return e;
 }
 

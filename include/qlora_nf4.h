@@ -554,7 +554,7 @@ typedef struct {
   const void* data;        /* device, [rows] x ld; may be NULL when rows == 0 */
   qlora_dtype dtype;       /* QLORA_F32 or QLORA_BF16 */
   int32_t reserved;        /* must be 0 */
-  int64_t rows, vocab, ld; /* 0 <= rows < 2^24, 1 <= vocab < 2^30 */
+  int64_t rows, vocab, ld; /* rows * ceil(row bytes / 32 KB) < 2^24, vocab < 2^30 */
   const int64_t* labels;   /* device, [rows] */
 } qlora_logits;
 
