@@ -19,15 +19,32 @@ constexpr int kT = 256;          // threads of a workgroup
 constexpr int kBatch = 8;        // 16-byte loads a thread has in flight
 constexpr float kInf = __builtin_inff();
 
-// log2(e) in two parts: the float32 nearest, and what it lacks.  Without the
-// second every exponential is off by 1.3e-8 of its argument to the same side,
-// which a sequence's sum of log ratios adds up.
-constexpr float kL2e = 0x1.715476p+0f;
-constexpr float kL2eLow = 0x1.4ae0bep-26f;
-// exp(d), d <= 0 or NaN
+// exp(d), d <= 0 or NaN; log2(e) as the nearest float32 and what that lacks
+constexpr float kL2e = 0x1.715476p+0f, kL2eLow = 0x1.4ae0bep-26f;
 __device__ __forceinline__ float exp_f32(float d) {
   return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kL2eLow, d * kL2e));
 }
+
+// The same to within v_exp_f32's own error, whatever the argument's size: what
+// the product d log2(e) was rounded by comes back as a factor.
+__device__ __forceinline__ float exp_exact(float d) {
+  const float t = d * kL2e, x = __builtin_amdgcn_exp2f(t);
+  const float rest = __builtin_fmaf(d, kL2eLow, __builtin_fmaf(d, kL2e, -t));
+  return d > -200.f ? __builtin_fmaf(x, 0.6931472f * rest, x) : x;
+}
+
+// A row's sum is taken over 2^(z H - R), H the 16 leading bits of log2(e) and R
+// an integer near the maximum's: for a bf16 z that argument is exact wherever
+// |z| is of the maximum's size, so the exponentials that make up the sum carry
+// v_exp_f32's own error only (2.6e-8, mean -3e-9).  With the rounded argument
+// of exp_f32 the few hundred values a bf16 takes there leave every row's sum
+// 6e-8 too large, which a sequence's sum of log ratios adds up.  What H lacks
+// is first order: 2^(z D) = 2^(m D) (1 + (z - m) D ln 2), from sum v z.
+// x y with 0 times anything 0 (v_mul_legacy_f32): a masked logit's x is 0
+__device__ float mul_zero(float x, float y) __asm("llvm.amdgcn.fmul.legacy");
+
+constexpr float kH = 0x1.7154p+0f;
+constexpr float kDLn2 = 0x1.480fb6p-18f;   // (log2(e) - kH) ln 2
 
 template <typename T>
 __device__ __forceinline__ float ld1(const T* p) {
@@ -129,7 +146,7 @@ __device__ __forceinline__ MaxSum wg_join(MaxSum a, float (*red)[2]) {
 #pragma unroll
   for (int w = 1; w < W; ++w) m = fmaxf(m, red[w][0]);
   // a thread without values has m = -inf and s = 0 (or NaN, which stays)
-  const float s = wave_sum(a.m == m ? a.s : a.s * exp_f32(a.m - m));
+  const float s = wave_sum(a.m == m ? a.s : a.s * exp_exact(a.m - m));
   if ((threadIdx.x & 63) == 0) red[wv][1] = s;
   __syncthreads();
   float t = red[0][1];
@@ -151,26 +168,43 @@ __device__ __forceinline__ void add_batch(MaxSum& a, const uint4 (&q)[N]) {
     for (int e = 0; e < vec<T>(); ++e) m = fmaxf(m, f[e]);
   }
   if (m > a.m) {
-    a.s *= exp_f32(a.m - m);
+    a.s *= exp_exact(a.m - m);
     a.m = m;
   }
-  const float ref = m == -kInf ? 0.f : m;
-  float s = 0.f;
+  if (__builtin_fabsf(m) < 0x1p20f) {
+    const float R = __builtin_rintf(m * kH);
+    float s = 0.f, sz = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float f[vec<T>()];
-    unpack<T>(q[i], f);
+    for (int i = 0; i < N; ++i) {
+      float f[vec<T>()];
+      unpack<T>(q[i], f);
 #pragma unroll
-    for (int e = 0; e < vec<T>(); ++e) s += exp_f32(f[e] - ref);
+      for (int e = 0; e < vec<T>(); ++e) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(f[e], kH, -R));
+        s += x;
+        sz += mul_zero(x, f[e]);
+      }
+    }
+    // relative to the maximum itself: 2^(R - m H)
+    a.s += __builtin_fmaf(kDLn2, __builtin_fmaf(-m, s, sz), s) *
+           __builtin_amdgcn_exp2f(__builtin_fmaf(-m, kH, R));
+  } else {   // no value yet, or of a size (or an infinity) the above cannot scale
+    const float ref = m == -kInf ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float f[vec<T>()];
+      unpack<T>(q[i], f);
+#pragma unroll
+      for (int e = 0; e < vec<T>(); ++e) a.s += exp_f32(f[e] - ref);
+    }
   }
-  a.s += s;
 }
 __device__ __forceinline__ void add_value(MaxSum& a, float x) {
   if (x > a.m) {
-    a.s *= exp_f32(a.m - x);
+    a.s *= exp_exact(a.m - x);
     a.m = x;
   }
-  a.s += exp_f32(x - (a.m == -kInf ? 0.f : a.m));
+  a.s += exp_exact(x - (a.m == -kInf ? 0.f : a.m));
 }
 
 // ------------------------------------------------------------ row statistics
@@ -235,7 +269,7 @@ __device__ __forceinline__ double row_logp(const LogitsView& v, const RowOut& o,
     float m = -kInf;
     for (int i = 0; i < slices; ++i) m = fmaxf(m, p[i].m);
     float s = 0.f;
-    for (int i = 0; i < slices; ++i) s += p[i].m == m ? p[i].s : p[i].s * exp_f32(p[i].m - m);
+    for (int i = 0; i < slices; ++i) s += p[i].m == m ? p[i].s : p[i].s * exp_exact(p[i].m - m);
     a = MaxSum{m, s};
     o.stats[t] = a;
   } else {
