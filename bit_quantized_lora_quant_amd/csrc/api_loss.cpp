@@ -54,7 +54,7 @@ LogitsView view(const qlora_logits* z, const int32_t* cu, int32_t nseq) {
 // Scratch of one call: what the caller does not take of the rows' outputs,
 // their slices, the sums of the sequences and the counter.
 struct LossWs {
-  size_t logp, stats, w, part, count, sums, ticket, total;
+  size_t logp, stats, w, zy, part, count, seq, sums, ticket, total;
 };
 LossWs loss_layout(const qlora_logits* z, int32_t sequences) {
   LossWs L;
@@ -64,8 +64,10 @@ LossWs loss_layout(const qlora_logits* z, int32_t sequences) {
   L.logp = off;   off = align_up(off + rows * sizeof(float));
   L.stats = off;  off = align_up(off + rows * sizeof(MaxSum));
   L.w = off;      off = align_up(off + rows * sizeof(float));
+  L.zy = off;     off = align_up(off + rows * sizeof(float));
   L.part = off;   off = align_up(off + (slices > 1 ? rows * slices : 0) * sizeof(MaxSum));
   L.count = off;  off = align_up(off + seqs * sizeof(int));
+  L.seq = off;    off = align_up(off + (seqs > 0 ? rows : 0) * sizeof(int));
   L.sums = off;   off = align_up(off + seqs * 3 * sizeof(double));
   L.ticket = off; off = align_up(off + sizeof(uint32_t));
   L.total = off;
@@ -78,7 +80,8 @@ T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws)
 RowOut row_out(void* ws, const LossWs& L, float* logp, float* stats, float* w) {
   return RowOut{logp ? logp : at<float>(ws, L.logp),
                 stats ? reinterpret_cast<MaxSum*>(stats) : at<MaxSum>(ws, L.stats),
-                w ? w : at<float>(ws, L.w), at<MaxSum>(ws, L.part), at<uint32_t>(ws, L.ticket)};
+                w ? w : at<float>(ws, L.w), at<float>(ws, L.zy), at<MaxSum>(ws, L.part),
+                at<uint32_t>(ws, L.ticket)};
 }
 
 bool opt4(const void* p) { return aligned(p, 4); }   // NULL passes
@@ -176,10 +179,8 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
   const RowOut o = row_out(ws, L, logp, stats, w);
   const PolicyArgs a{advantages,          old_logp, ref_logp, 1 - h->clip_low, 1 + h->clip_high,
                      h->kl_coef,          h->reduction, h->token_advantages, out,
-                     at<int>(ws, L.count), at<double>(ws, L.sums)};
-  hipError_t e = launch_policy(v, o, a, s);
-  if (e == hipSuccess && dlogits) e = launch_row_grad(v, o.stats, o.w, nullptr, dlogits, ldd, s);
-  return hip_status(e);
+                     at<int>(ws, L.count), at<int>(ws, L.seq), at<double>(ws, L.sums)};
+  return hip_status(launch_policy(v, o, a, dlogits, ldd, s));
 }
 
 }  // extern "C"

@@ -22,11 +22,13 @@ struct MaxSum {
 };
 
 // What a loss writes for each row (logp, stats, w = dLoss / dlogp) and its
-// scratch: the slices' statistics [rows][row_slices] and a counter.
+// scratch: the target's logit (the logits may be overwritten by the gradient
+// before the sums), the slices' statistics [rows][row_slices] and a counter.
 struct RowOut {
   float* logp;
   MaxSum* stats;
   float* w;
+  float* zy;
   MaxSum* part;
   uint32_t* ticket;
 };
@@ -50,6 +52,7 @@ struct PolicyArgs {
   int reduction, token_adv;
   float* out;             // [3]
   int* count;             // scratch [nseq]: targets of each sequence
+  int* seq;               // scratch [rows]: sequence of each row in one
   double* sums;           // scratch [nseq][3]: loss, kl, clipped
 };
 
@@ -61,7 +64,9 @@ int64_t row_grad_slices(int64_t vocab, int bf16);
 hipError_t launch_row_logp(const LogitsView& v, const RowOut& o, hipStream_t s);
 hipError_t launch_preference(const LogitsView& v, const RowOut& o, const PreferenceArgs& a,
                              hipStream_t s);
-hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs& a, hipStream_t s);
+// with the gradient in dz (nullable, row stride ldd)
+hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs& a, void* dz,
+                         int64_t ldd, hipStream_t s);
 // dlogits = g w (1[y] - exp(z - m) / sum), row stride ldd
 hipError_t launch_row_grad(const LogitsView& v, const MaxSum* stats, const float* w,
                            const float* g, void* dz, int64_t ldd, hipStream_t s);

@@ -25,6 +25,11 @@ __device__ __forceinline__ float exp_f32(float d) {
   return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kL2eLow, d * kL2e));
 }
 
+// exp(d) of either sign
+__device__ __forceinline__ float exp_any(float d) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kL2eLow, d * kL2e));
+}
+
 // The same to within v_exp_f32's own error, whatever the argument's size: what
 // the product d log2(e) was rounded by comes back as a factor.
 __device__ __forceinline__ float exp_exact(float d) {
@@ -80,6 +85,12 @@ __device__ __forceinline__ uint4 pack(const float (&f)[vec<T>()]) {
   else
     return __builtin_bit_cast(uint4, f32x4_t{f[0], f[1], f[2], f[3]});
 }
+// Keeps what was unpacked from a chunk from living on to its next use, and the
+// chunks' work in order: 16 bytes of a row stay, not 8 floats.
+__device__ __forceinline__ void forget(uint4& q) {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" : "+v"(q.x), "+v"(q.y), "+v"(q.z), "+v"(q.w));
+}
 // a chunk of -inf: what stands in for values past a row's end
 template <typename T>
 __device__ __forceinline__ uint4 no_values() {
@@ -93,22 +104,24 @@ __device__ __forceinline__ uint4 no_values() {
 template <typename T>
 struct Row {
   const T* z;
-  int head, edge;
-  int64_t nb, vocab;
+  int head, edge, nb, vocab;
   __device__ __forceinline__ Row(const LogitsView& v, int64_t t) {
     z = static_cast<const T*>(v.z) + t * v.ld;
-    vocab = v.vocab;
-    const int64_t off = (int64_t)((uintptr_t)z & 15) / (int64_t)sizeof(T);
-    const int64_t h = off ? vec<T>() - off : 0;
-    head = (int)(h < vocab ? h : vocab);
+    vocab = (int)v.vocab;
+    const int off = (int)((uintptr_t)z & 15) / (int)sizeof(T);
+    const int h = off ? vec<T>() - off : 0;
+    head = h < vocab ? h : vocab;
     nb = (vocab - head) / vec<T>();
-    edge = (int)(vocab - nb * vec<T>());
+    edge = vocab - nb * vec<T>();
   }
-  __device__ __forceinline__ const uint4* body() const {
-    return reinterpret_cast<const uint4*>(z + head);
+  // chunk k: a row is uniform in a workgroup, so its base stays in scalar
+  // registers and a lane has a 32-bit offset
+  __device__ __forceinline__ uint4 chunk(int k) const {
+    return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(z + head) +
+                                           (uint32_t)k * 16u);
   }
   // value index of edge element k
-  __device__ __forceinline__ int64_t edge_at(int k) const {
+  __device__ __forceinline__ int edge_at(int k) const {
     return k < head ? k : nb * vec<T>() + k;
   }
 };
@@ -155,14 +168,46 @@ __device__ __forceinline__ MaxSum wg_join(MaxSum a, float (*red)[2]) {
   return MaxSum{m, t};
 }
 
+// What turns a logit into its gradient: k exp(z - m), k = -w / sum, and + w at
+// the target.  A bf16 gradient takes k into the exponent (one multiply-add; its
+// argument's rounding, a few 2^-24, is far below half a bf16 step), a float32
+// one keeps the exponential apart.
+template <typename T>
+struct GradOf {
+  float m, w, k, flip;     // bf16: k = log2 |w / sum|, flip: the sign of -w
+  __device__ __forceinline__ GradOf(const MaxSum& a, float w_) : m(a.m), w(w_), k(-w_ / a.s) {
+    flip = __builtin_copysignf(1.f, -w_);
+    if constexpr (sizeof(T) == 2) k = __builtin_amdgcn_logf(__builtin_fabsf(w_ / a.s));
+  }
+  __device__ __forceinline__ float operator()(float z) const {
+    if constexpr (sizeof(T) == 2)
+      return flip * __builtin_amdgcn_exp2f(__builtin_fmaf(z - m, kL2e, k));
+    else
+      return k * exp_f32(z - m);
+  }
+  // chunk `at` of a row whose target is body value yb
+  __device__ __forceinline__ uint4 chunk(const uint4& q, int at, int yb) const {
+    float f[vec<T>()];
+    unpack<T>(q, f);
+#pragma unroll
+    for (int e = 0; e < vec<T>(); ++e) f[e] = (*this)(f[e]);
+    if ((unsigned)(yb - at * vec<T>()) < (unsigned)vec<T>()) {
+#pragma unroll
+      for (int e = 0; e < vec<T>(); ++e) f[e] += at * vec<T>() + e == yb ? w : 0.f;
+    }
+    return pack<T>(f);
+  }
+};
+
 // Adds a batch of chunks to a thread's part: the maximum first, so that the
 // sum is rescaled once a batch.
 template <typename T, int N>
-__device__ __forceinline__ void add_batch(MaxSum& a, const uint4 (&q)[N]) {
+__device__ __forceinline__ void add_batch(MaxSum& a, uint4 (&q)[N]) {
   float m = a.m;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     float f[vec<T>()];
+    forget(q[i]);
     unpack<T>(q[i], f);
 #pragma unroll
     for (int e = 0; e < vec<T>(); ++e) m = fmaxf(m, f[e]);
@@ -177,6 +222,7 @@ __device__ __forceinline__ void add_batch(MaxSum& a, const uint4 (&q)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float f[vec<T>()];
+      forget(q[i]);
       unpack<T>(q[i], f);
 #pragma unroll
       for (int e = 0; e < vec<T>(); ++e) {
@@ -193,6 +239,7 @@ __device__ __forceinline__ void add_batch(MaxSum& a, const uint4 (&q)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float f[vec<T>()];
+      forget(q[i]);
       unpack<T>(q[i], f);
 #pragma unroll
       for (int e = 0; e < vec<T>(); ++e) a.s += exp_f32(f[e] - ref);
@@ -227,38 +274,39 @@ __global__ __launch_bounds__(kT) void k_row_stats(LogitsView v, RowOut o, int sl
     return;
   }
   const Row<T> r(v, t);
-  const int64_t per = ceil_div(r.nb, slices);
-  const int64_t c0 = sl * per, c1 = c0 + per < r.nb ? c0 + per : r.nb;
-  const uint4* b = r.body();
+  const int per = (r.nb + slices - 1) / slices;
+  const int c0 = sl * per < r.nb ? sl * per : r.nb, c1 = c0 + per < r.nb ? c0 + per : r.nb;
   MaxSum a{-kInf, 0.f};
-  int64_t c = c0 + threadIdx.x;
-  for (; c0 < c1 && c - threadIdx.x + kT * kBatch <= c1; c += kT * kBatch) {
+  const int tid = threadIdx.x;
+  int c = c0 + tid;
+  for (; c - tid + kT * kBatch <= c1; c += kT * kBatch) {
     uint4 q[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) q[i] = b[c + kT * i];
+    for (int i = 0; i < kBatch; ++i) q[i] = r.chunk(c + kT * i);
     add_batch<T>(a, q);
   }
-  if (c - threadIdx.x < c1) {
+  if (c - tid < c1) {
     uint4 q[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      q[i] = c + kT * i < c1 ? b[c + kT * i] : no_values<T>();
+      q[i] = c + kT * i < c1 ? r.chunk(c + kT * i) : no_values<T>();
     add_batch<T>(a, q);
   }
   if (sl == 0 && (int)threadIdx.x < r.edge) add_value(a, ld1(r.z + r.edge_at(threadIdx.x)));
   a = wg_join<kT / 64>(a, red);
   if (threadIdx.x != 0) return;
+  const float zy = ld1(r.z + y);
+  if (sl == 0) o.zy[t] = zy;
   if (slices > 1) {
     o.part[t * slices + sl] = a;
   } else {
     o.stats[t] = a;
-    o.logp[t] = (float)((double)ld1(r.z + y) - (double)a.m - std::log((double)a.s));
+    o.logp[t] = (float)((double)zy - (double)a.m - std::log((double)a.s));
   }
 }
 
 // The statistics of row t, joined from its slices in their order if there are
 // several (and then stored with logp).  Rows with a target only.
-template <typename T>
 __device__ __forceinline__ double row_logp(const LogitsView& v, const RowOut& o, int slices,
                                            int64_t t) {
   const int64_t y = v.labels[t];
@@ -275,16 +323,14 @@ __device__ __forceinline__ double row_logp(const LogitsView& v, const RowOut& o,
   } else {
     a = o.stats[t];
   }
-  const float zy = ld1(static_cast<const T*>(v.z) + t * v.ld + y);
-  const double l = (double)zy - (double)a.m - std::log((double)a.s);
-  if (slices > 1) o.logp[t] = (float)l;
+  const double l = (double)o.zy[t] - (double)a.m - std::log((double)a.s);
+  if (slices != 1) o.logp[t] = (float)l;
   return l;
 }
 
-template <typename T>
 __global__ __launch_bounds__(kT) void k_row_join(LogitsView v, RowOut o, int slices) {
   const int64_t t = (int64_t)blockIdx.x * kT + threadIdx.x;
-  if (t < v.rows && v.labels[t] >= 0) row_logp<T>(v, o, slices, t);
+  if (t < v.rows && v.labels[t] >= 0) row_logp(v, o, slices, t);
 }
 
 // --------------------------------------------------------------- row gradient
@@ -302,13 +348,12 @@ __global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const MaxSum* sta
   const Row<T> r(v, t);
   T* const d = dz + t * ldd;
   const bool even = (((uintptr_t)d ^ (uintptr_t)r.z) & 15) == 0;   // 16-byte stores fit
-  const int64_t c0 = (int64_t)sl * kT * kBatch + threadIdx.x;
-  const uint4* b = r.body();
-  uint4* const db = reinterpret_cast<uint4*>(d + r.head);
-  auto store = [&](int64_t k, const uint4& q) {
+  const int c0 = sl * kT * kBatch + (int)threadIdx.x;
+  char* const db = reinterpret_cast<char*>(d + r.head);
+  auto store = [&](int k, const uint4& q) {
     if (even) {
       __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, q),
-                                  reinterpret_cast<u32x4_t*>(db + k));
+                                  reinterpret_cast<u32x4_t*>(db + (uint32_t)k * 16u));
     } else {
       float f[vec<T>()];
       unpack<T>(q, f);
@@ -327,33 +372,26 @@ __global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const MaxSum* sta
   uint4 q[kBatch];
 #pragma unroll
   for (int i = 0; i < kBatch; ++i)
-    if (c0 + kT * i < r.nb) q[i] = b[c0 + kT * i];
-  const MaxSum a = stats[t];
-  const float k = -c / a.s;
-  const int64_t yb = y - r.head;
+    if (c0 + kT * i < r.nb) q[i] = r.chunk(c0 + kT * i);
+  const GradOf<T> grad(stats[t], c);
+  const int yb = y < v.vocab ? (int)y - r.head : -vec<T>();
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
-    const int64_t at = c0 + kT * i;
+    const int at = c0 + kT * i;
     if (at >= r.nb) continue;
-    float f[vec<T>()];
-    unpack<T>(q[i], f);
-#pragma unroll
-    for (int e = 0; e < vec<T>(); ++e) f[e] = k * exp_f32(f[e] - a.m);
-    if ((uint64_t)(yb - at * vec<T>()) < (uint64_t)vec<T>()) {
-#pragma unroll
-      for (int e = 0; e < vec<T>(); ++e) f[e] += at * vec<T>() + e == yb ? c : 0.f;
-    }
-    store(at, pack<T>(f));
+    forget(q[i]);
+    store(at, grad.chunk(q[i], at, yb));
   }
   if (at_edge) {
-    const int64_t at = r.edge_at(threadIdx.x);
-    st1(d + at, k * exp_f32(ld1(r.z + at) - a.m) + (at == y ? c : 0.f));
+    const int at = r.edge_at(threadIdx.x);
+    st1(d + at, grad(ld1(r.z + at)) + (at == y ? c : 0.f));
   }
 }
 
 // ------------------------------------------------------- between the streams
 // Sum over the workgroup in a fixed order, the result in every thread; red: a
 // double for each wave.
+template <int NT>
 __device__ __forceinline__ double wg_sum(double x, double* red) {
   x = wave_sum(x);
   __syncthreads();
@@ -361,7 +399,7 @@ __device__ __forceinline__ double wg_sum(double x, double* red) {
   __syncthreads();
   x = red[0];
 #pragma unroll
-  for (int w = 1; w < kT / 64; ++w) x += red[w];
+  for (int w = 1; w < NT / 64; ++w) x += red[w];
   return x;
 }
 
@@ -384,36 +422,43 @@ __device__ __forceinline__ void device_store(double* p, double v) {
 // w of the rows in no sequence, shared out over the workgroups
 __device__ __forceinline__ void zero_outside(const LogitsView& v, float* w) {
   const int64_t b = cu_at(v, 0), e = cu_at(v, v.nseq);
-  const int64_t step = (int64_t)gridDim.x * kT, at = (int64_t)blockIdx.x * kT + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   for (int64_t t = at; t < b; t += step) w[t] = 0.f;
   for (int64_t t = e + at; t < v.rows; t += step) w[t] = 0.f;
 }
 
-// Workgroup per pair; the last one adds the pairs' losses in their order.
-template <typename T>
-__global__ __launch_bounds__(kT) void k_preference(LogitsView v, RowOut o, PreferenceArgs a,
-                                                   int slices) {
-  __shared__ double red[kT / 64];
+// Workgroup per pair, its two sequences in one pass; the last one adds the
+// pairs' losses in their order.
+constexpr int kSeqT = 1024;
+
+__global__ __launch_bounds__(kSeqT) void k_preference(LogitsView v, RowOut o, PreferenceArgs a,
+                                                      int slices) {
+  __shared__ double red[kSeqT / 64];
   const int p = blockIdx.x;
-  double lr[2], n[2];
+  const int64_t b = cu_at(v, 2 * p), mid = cu_at(v, 2 * p + 1), e = cu_at(v, 2 * p + 2);
+  double lp[2] = {0, 0}, lr[2] = {0, 0}, n[2] = {0, 0};
   zero_outside(v, o.w);
+  for (int64_t t = b + threadIdx.x; t < e; t += kSeqT) {
+    if (v.labels[t] < 0) continue;
+    const double l = row_logp(v, o, slices, t);
+    const double d = l - (a.ref ? (double)a.ref[t] : 0.0);
+    const bool second = t >= mid;
+    lp[0] += second ? 0.0 : l;
+    lr[0] += second ? 0.0 : d;
+    n[0] += second ? 0.0 : 1.0;
+    lp[1] += second ? l : 0.0;
+    lr[1] += second ? d : 0.0;
+    n[1] += second ? 1.0 : 0.0;
+  }
   for (int i = 0; i < 2; ++i) {
-    const int64_t b = cu_at(v, 2 * p + i), e = cu_at(v, 2 * p + i + 1);
-    double lp = 0, rf = 0, cnt = 0;
-    for (int64_t t = b + threadIdx.x; t < e; t += kT) {
-      if (v.labels[t] < 0) continue;
-      const double l = row_logp<T>(v, o, slices, t);
-      lp += l;
-      rf += l - (a.ref ? (double)a.ref[t] : 0.0);
-      cnt += 1;
-    }
-    lp = wg_sum(lp, red);
-    lr[i] = wg_sum(rf, red);
-    n[i] = wg_sum(cnt, red);
+    lp[i] = wg_sum<kSeqT>(lp[i], red);
+    lr[i] = wg_sum<kSeqT>(lr[i], red);
+    n[i] = wg_sum<kSeqT>(n[i], red);
     if (!a.length_mean || n[i] < 1) n[i] = 1;
     lr[i] /= n[i];
     if (threadIdx.x == 0) {
-      if (a.seq_logp) a.seq_logp[2 * p + i] = (float)(lp / n[i]);
+      if (a.seq_logp) a.seq_logp[2 * p + i] = (float)(lp[i] / n[i]);
       if (a.rewards) a.rewards[2 * p + i] = (float)(a.beta * lr[i]);
     }
   }
@@ -436,25 +481,28 @@ __global__ __launch_bounds__(kT) void k_preference(LogitsView v, RowOut o, Prefe
     loss = d * d;
     dh = 2 * d;
   }
-  for (int i = 0; i < 2; ++i) {
-    const int64_t b = cu_at(v, 2 * p + i), e = cu_at(v, 2 * p + i + 1);
-    const float wt = (float)((i ? -dh : dh) / n[i] / a.pairs);
-    for (int64_t t = b + threadIdx.x; t < e; t += kT) o.w[t] = v.labels[t] < 0 ? 0.f : wt;
-  }
+  const float w0 = (float)(dh / n[0] / a.pairs), w1 = (float)(-dh / n[1] / a.pairs);
+  for (int64_t t = b + threadIdx.x; t < e; t += kSeqT)
+    o.w[t] = v.labels[t] < 0 ? 0.f : t < mid ? w0 : w1;
   if (threadIdx.x == 0) device_store(a.pair_loss + p, loss);
   if (!last_of(o.ticket, gridDim.x)) return;
   double tot = 0;
-  for (int k = threadIdx.x; k < a.pairs; k += kT) tot += device_load(a.pair_loss + k);
-  tot = wg_sum(tot, red);
+  for (int k = threadIdx.x; k < a.pairs; k += kSeqT) tot += device_load(a.pair_loss + k);
+  tot = wg_sum<kSeqT>(tot, red);
   if (threadIdx.x == 0) *a.loss = (float)(tot / a.pairs);
 }
 
-__global__ __launch_bounds__(kT) void k_policy_count(LogitsView v, PolicyArgs a) {
-  __shared__ double red[kT / 64];
+// Workgroup per sequence: its targets, and its rows' sequence.
+__global__ __launch_bounds__(kSeqT) void k_policy_count(LogitsView v, RowOut o, PolicyArgs a) {
+  __shared__ double red[kSeqT / 64];
   const int i = blockIdx.x;
+  if (i == 0 && threadIdx.x == 0) *o.ticket = 0;
   double n = 0;
-  for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += kT) n += v.labels[t] >= 0;
-  n = wg_sum(n, red);
+  for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += kSeqT) {
+    n += v.labels[t] >= 0;
+    a.seq[t] = i;
+  }
+  n = wg_sum<kSeqT>(n, red);
   if (threadIdx.x == 0) a.count[i] = (int)n;
 }
 
@@ -462,14 +510,15 @@ __global__ __launch_bounds__(kT) void k_policy_count(LogitsView v, PolicyArgs a)
 struct Totals {
   double targets, filled;
 };
+template <int NT>
 __device__ __forceinline__ Totals totals(const PolicyArgs& a, int nseq, double* red) {
   double n = 0, f = 0;
-  for (int j = threadIdx.x; j < nseq; j += kT) {
+  for (int j = threadIdx.x; j < nseq; j += NT) {
     n += a.count[j];
     f += a.count[j] > 0;
   }
-  n = wg_sum(n, red);
-  return Totals{n, wg_sum(f, red)};
+  n = wg_sum<NT>(n, red);
+  return Totals{n, wg_sum<NT>(f, red)};
 }
 // weight of one target of sequence i in the mean
 __device__ __forceinline__ double share_of(const PolicyArgs& a, const Totals& n, int i) {
@@ -495,29 +544,28 @@ __device__ __forceinline__ Term policy_term(const PolicyArgs& a, double l, doubl
 }
 
 // Workgroup per sequence; the last one adds the sequences' sums in their order.
-template <typename T>
-__global__ __launch_bounds__(kT) void k_policy(LogitsView v, RowOut o, PolicyArgs a, int slices) {
-  __shared__ double red[kT / 64];
+__global__ __launch_bounds__(kSeqT) void k_policy(LogitsView v, RowOut o, PolicyArgs a, int slices) {
+  __shared__ double red[kSeqT / 64];
   const int i = blockIdx.x;
   zero_outside(v, o.w);
-  const Totals n = totals(a, v.nseq, red);
+  const Totals n = totals<kSeqT>(a, v.nseq, red);
   const double share = share_of(a, n, i);
   double loss = 0, kl = 0, cut = 0;
-  for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += kT) {
+  for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += kSeqT) {
     if (v.labels[t] < 0) {
       o.w[t] = 0.f;
       continue;
     }
     const double A = (double)(a.token_adv ? a.adv[t] : a.adv[i]);
-    const Term x = policy_term(a, row_logp<T>(v, o, slices, t), A, t);
+    const Term x = policy_term(a, row_logp(v, o, slices, t), A, t);
     loss += x.loss;
     kl += x.kl;
     cut += x.clipped;
     o.w[t] = (float)(share * x.dlogp);
   }
-  loss = wg_sum(loss, red);
-  kl = wg_sum(kl, red);
-  cut = wg_sum(cut, red);
+  loss = wg_sum<kSeqT>(loss, red);
+  kl = wg_sum<kSeqT>(kl, red);
+  cut = wg_sum<kSeqT>(cut, red);
   if (threadIdx.x == 0) {
     device_store(a.sums + 3 * i, share * loss);
     device_store(a.sums + 3 * i + 1, share * kl);
@@ -525,13 +573,129 @@ __global__ __launch_bounds__(kT) void k_policy(LogitsView v, RowOut o, PolicyArg
   }
   if (!last_of(o.ticket, gridDim.x)) return;
   double x[3] = {0, 0, 0};
-  for (int j = threadIdx.x; j < v.nseq; j += kT)
+  for (int j = threadIdx.x; j < v.nseq; j += kSeqT)
     for (int k = 0; k < 3; ++k) x[k] += device_load(a.sums + 3 * j + k);
-  for (int k = 0; k < 3; ++k) x[k] = wg_sum(x[k], red);
+  for (int k = 0; k < 3; ++k) x[k] = wg_sum<kSeqT>(x[k], red);
   if (threadIdx.x == 0) {
     a.out[0] = (float)x[0];
     a.out[1] = (float)x[1];
     a.out[2] = (float)(x[2] / (n.targets > 0 ? n.targets : 1));
+  }
+}
+
+// ------------------------------------------- policy loss in one pass
+// The weight of a row hangs on that row's logp and on counts known from the
+// labels, so a workgroup can hold its row in registers from the maximum to the
+// gradient: the logits are read once where the statistics and the gradient as
+// two launches read them twice.  A row of up to NT x NC chunks goes to NT
+// threads, NC 16-byte chunks each (1024 x 16 holds 131,072 bf16 in half of a
+// CU's registers).  The workgroups are persistent and the memory never waits
+// for arithmetic: as a chunk's gradient is stored its registers take the same
+// chunk of the workgroup's next row, and the sums run over four chunks at a
+// time as they arrive.  The weight is formed in float32 here (the logits'
+// gradient has no more); logp and the loss come from the statistics after.
+template <typename T, int NT, int NC>
+__global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, PolicyArgs a, T* dz,
+                                                    int64_t ldd) {
+  __shared__ float red[NT / 64][2];
+  __shared__ double dred[NT / 64];
+  constexpr int kSum = 4;                       // chunks summed at a time
+  const Totals n = totals<NT>(a, v.nseq, dred);
+  const int64_t step = gridDim.x;
+  auto has_target = [&](int64_t t) {
+    const int64_t y = v.labels[t];
+    return y >= 0 && y < v.vocab && !outside(v, t);
+  };
+  auto next_target = [&](int64_t t) {
+    while (t < v.rows && !has_target(t)) t += step;
+    return t;
+  };
+  auto store = [&](T* d, int head, int k, const uint4& q) {
+    __builtin_nontemporal_store(
+        __builtin_bit_cast(u32x4_t, q),
+        reinterpret_cast<u32x4_t*>(reinterpret_cast<char*>(d + head) + (uint32_t)k * 16u));
+  };
+  // the workgroup's rows without a target: zeros (NaN for a label out of range)
+  for (int64_t t = blockIdx.x; t < v.rows; t += step) {
+    if (has_target(t)) continue;
+    const Row<T> r(v, t);
+    T* const d = dz + t * ldd;
+    const float none = v.labels[t] >= v.vocab && !outside(v, t) ? __builtin_nanf("") : 0.f;
+    uint4 q;
+    if constexpr (sizeof(T) == 2) q.x = pack_bf16x2(none, none);
+    else q.x = __builtin_bit_cast(uint32_t, none);
+    q.y = q.z = q.w = q.x;
+    for (int k = threadIdx.x; k < r.nb; k += NT) store(d, r.head, k, q);
+    if ((int)threadIdx.x < r.edge) st1(d + r.edge_at(threadIdx.x), none);
+    if (threadIdx.x == 0) {
+      o.stats[t] = MaxSum{0.f, none};
+      o.logp[t] = none;
+    }
+  }
+  int64_t t = next_target(blockIdx.x);
+  if (t >= v.rows) return;
+  uint4 q[NC];
+  float ze, zy;
+  auto load_edge = [&](const Row<T>& r, int64_t row, int tid) {
+    ze = tid < r.edge ? ld1(r.z + r.edge_at(tid)) : -kInf;
+    zy = ld1(r.z + v.labels[row]);
+  };
+  {
+    const Row<T> r(v, t);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int k = (int)threadIdx.x + NT * i;
+      q[i] = k < r.nb ? r.chunk(k) : no_values<T>();
+    }
+    load_edge(r, t, threadIdx.x);
+  }
+  while (t < v.rows) {
+    // (opaque, or the chunks' offsets are kept in registers over the rows)
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int64_t tn = next_target(t + step);
+    const Row<T> r(v, t), rn(v, tn < v.rows ? tn : t);
+    const int nbn = tn < v.rows ? rn.nb : 0;    // chunks of the next row, none without one
+    const int64_t y = v.labels[t];
+    const int sq = a.seq[t];
+    const float A = a.token_adv ? a.adv[t] : a.adv[sq];
+    const float share = (float)share_of(a, n, sq);
+    const float old_logp = a.old_logp ? a.old_logp[t] : 0.f, ref = a.ref ? a.ref[t] : 0.f;
+    MaxSum s{-kInf, 0.f};
+#pragma unroll
+    for (int i = 0; i < NC; i += kSum)
+      add_batch<T>(s, *reinterpret_cast<uint4(*)[kSum]>(&q[i]));
+    if (tid < r.edge) add_value(s, ze);
+    s = wg_join<NT / 64>(s, red);
+    if (tid == 0) {
+      o.stats[t] = s;
+      o.zy[t] = zy;
+    }
+    const float l = (zy - s.m) - 0.6931472f * __builtin_amdgcn_logf(s.s);
+    const float ratio = a.old_logp ? exp_any(l - old_logp) : (l == l ? 1.f : l);
+    const float lo = (float)a.lo, hi = (float)a.hi;
+    const float u = -A * ratio, c = -A * (ratio < lo ? lo : ratio > hi ? hi : ratio);
+    float w = c > u ? 0.f : u;
+    if (a.ref) w -= (float)a.kl_coef * (exp_any(ref - l) - 1.f);
+    w *= share;
+    const GradOf<T> grad(s, w);
+    const int yb = (int)y - r.head;
+    T* const d = dz + t * ldd;
+    const float zt = ze;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int at = tid + NT * i;
+      forget(q[i]);
+      if (at < r.nb)
+        store(d, r.head, at, w == 0.f ? make_uint4(0u, 0u, 0u, 0u) : grad.chunk(q[i], at, yb));
+      q[i] = at < nbn ? rn.chunk(at) : no_values<T>();
+    }
+    if (tid < r.edge) {
+      const int at = r.edge_at(tid);
+      st1(d + at, w == 0.f ? 0.f : grad(zt) + (at == y ? w : 0.f));
+    }
+    if (tn < v.rows) load_edge(rn, tn, tid);
+    t = tn;
   }
 }
 
@@ -565,8 +729,7 @@ hipError_t launch_row_logp(const LogitsView& v, const RowOut& o, hipStream_t s) 
   const int slices = row_slices(v);
   hipError_t e = row_stats(v, o, slices, s);
   if (e == hipSuccess && slices > 1)
-    e = launch_kernel(v.bf16 ? k_row_join<uint16_t> : k_row_join<float>,
-                      dim3((unsigned)ceil_div(v.rows, kT)), dim3(kT), s, v, o, slices);
+    e = launch_kernel(k_row_join, dim3((unsigned)ceil_div(v.rows, kT)), dim3(kT), s, v, o, slices);
   return e;
 }
 
@@ -587,19 +750,51 @@ hipError_t launch_preference(const LogitsView& v, const RowOut& o, const Prefere
   const int slices = row_slices(v);
   const hipError_t e = row_stats(v, o, slices, s);
   if (e != hipSuccess) return e;
-  return launch_kernel(v.bf16 ? k_preference<uint16_t> : k_preference<float>,
-                       dim3((unsigned)a.pairs), dim3(kT), s, v, o, a, slices);
+  return launch_kernel(k_preference, dim3((unsigned)a.pairs), dim3(kSeqT), s, v, o, a, slices);
 }
 
-hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs& a,
-                         hipStream_t s) {
-  const int slices = row_slices(v);
-  hipError_t e = row_stats(v, o, slices, s);
+template <typename T, int NT, int NC>
+static hipError_t policy_rows(const LogitsView& v, const RowOut& o, const PolicyArgs& a, void* dz,
+                              int64_t ldd, hipStream_t s) {
+  const int64_t most = 256 * (1024 / NT);       // what the CUs hold at a time
+  return launch_kernel(k_policy_rows<T, NT, NC>, dim3((unsigned)(v.rows < most ? v.rows : most)),
+                       dim3(NT), s, v, o, a, static_cast<T*>(dz), ldd);
+}
+
+// The one-pass form where a row fits in registers, the rows fill the chip and
+// the gradient's rows start where the logits' do between 16-byte boundaries.
+template <typename T>
+static hipError_t policy_rows_of(const LogitsView& v, const RowOut& o, const PolicyArgs& a,
+                                 void* dz, int64_t ldd, hipStream_t s) {
+  const int64_t chunks = row_chunks(v.vocab, v.bf16);
+  if (chunks <= 256 * 4) return policy_rows<T, 256, 4>(v, o, a, dz, ldd, s);
+  if (chunks <= 256 * 16) return policy_rows<T, 256, 16>(v, o, a, dz, ldd, s);
+  if (chunks <= 512 * 16) return policy_rows<T, 512, 16>(v, o, a, dz, ldd, s);
+  return policy_rows<T, 1024, 16>(v, o, a, dz, ldd, s);
+}
+static bool one_pass(const LogitsView& v, const void* dz, int64_t ldd) {
+  const int64_t chunks = row_chunks(v.vocab, v.bf16);
+  const uintptr_t apart = ((uintptr_t)dz - (uintptr_t)v.z) | (uintptr_t)((ldd - v.ld) * (v.bf16 ? 2 : 4));
+  return chunks <= 1024 * 16 && v.rows >= 256 && (apart & 15) == 0;
+}
+
+hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs& a, void* dz,
+                         int64_t ldd, hipStream_t s) {
+  const bool fused = dz && one_pass(v, dz, ldd);
+  // (0 slices: the statistics are there, logp is not)
+  const int slices = fused ? 0 : row_slices(v);
+  hipError_t e =
+      launch_kernel(k_policy_count, dim3((unsigned)v.nseq), dim3(kSeqT), s, v, o, a);
+  if (e != hipSuccess) return e;
+  if (fused)
+    e = v.bf16 ? policy_rows_of<uint16_t>(v, o, a, dz, ldd, s)
+               : policy_rows_of<float>(v, o, a, dz, ldd, s);
+  else
+    e = row_stats(v, o, slices, s);
   if (e == hipSuccess)
-    e = launch_kernel(k_policy_count, dim3((unsigned)v.nseq), dim3(kT), s, v, a);
-  if (e == hipSuccess)
-    e = launch_kernel(v.bf16 ? k_policy<uint16_t> : k_policy<float>, dim3((unsigned)v.nseq),
-                      dim3(kT), s, v, o, a, slices);
+    e = launch_kernel(k_policy, dim3((unsigned)v.nseq), dim3(kSeqT), s, v, o, a, slices);
+  if (e == hipSuccess && dz && !fused)
+    e = launch_row_grad(v, o.stats, o.w, nullptr, dz, ldd, s);
   return e;
 }
 

@@ -155,7 +155,8 @@ PACKS = [  # lengths, rows before, rows behind, V, dtype
     ([1, 1], 0, 0, 50, BF), ([5, 3], 0, 2, 1000, BF), ([7, 0, 1, 9], 3, 4, 333, F32),
     ([40, 25, 60, 31], 0, 0, 2003, BF), ([300, 280], 0, 10, 515, BF), ([4] * 64, 1, 0, 129, F32),
     ([90, 61, 0, 0, 75, 80], 2, 5, 4100, BF), ([6, 5], 0, 0, 128256, BF), ([3, 4], 1, 1, 140000, F32),
-    ([70, 66, 51, 80], 0, 3, 33001, BF),
+    ([70, 66, 51, 80], 0, 3, 33001, BF), ([150, 128], 1, 2, 70001, BF), ([140, 0, 3, 160], 0, 2, 20011, BF),
+    ([131, 130], 0, 4, 20003, F32), ([129, 128], 2, 0, 40001, F32),
 ]
 
 
