@@ -54,7 +54,7 @@ LogitsView view(const qlora_logits* z, const int32_t* cu, int32_t nseq) {
 // Scratch of one call: what the caller does not take of the rows' outputs,
 // their slices, the sums of the sequences and the counter.
 struct LossWs {
-  size_t logp, stats, w, zy, part, count, seq, sums, ticket, total;
+  size_t logp, stats, w, zy, part, count, seq, list, sums, ticket, total;
 };
 LossWs loss_layout(const qlora_logits* z, int32_t sequences) {
   LossWs L;
@@ -68,6 +68,7 @@ LossWs loss_layout(const qlora_logits* z, int32_t sequences) {
   L.part = off;   off = align_up(off + (slices > 1 ? rows * slices : 0) * sizeof(MaxSum));
   L.count = off;  off = align_up(off + seqs * sizeof(int));
   L.seq = off;    off = align_up(off + (seqs > 0 ? rows : 0) * sizeof(int));
+  L.list = off;   off = align_up(off + (seqs > 0 ? rows + 1 : 0) * sizeof(int));
   L.sums = off;   off = align_up(off + seqs * 3 * sizeof(double));
   L.ticket = off; off = align_up(off + sizeof(uint32_t));
   L.total = off;
@@ -179,7 +180,8 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
   const RowOut o = row_out(ws, L, logp, stats, w);
   const PolicyArgs a{advantages,          old_logp, ref_logp, 1 - h->clip_low, 1 + h->clip_high,
                      h->kl_coef,          h->reduction, h->token_advantages, out,
-                     at<int>(ws, L.count), at<int>(ws, L.seq), at<double>(ws, L.sums)};
+                     at<int>(ws, L.count), at<int>(ws, L.seq), at<int>(ws, L.list),
+                     at<double>(ws, L.sums)};
   return hip_status(launch_policy(v, o, a, dlogits, ldd, s));
 }
 

@@ -53,6 +53,7 @@ struct PolicyArgs {
   float* out;             // [3]
   int* count;             // scratch [nseq]: targets of each sequence
   int* seq;               // scratch [rows]: sequence of each row in one
+  int* list;              // scratch [rows + 1]: the rows with a target, their number last
   double* sums;           // scratch [nseq][3]: loss, kl, clipped
 };
 

@@ -45,9 +45,6 @@ __device__ __forceinline__ float exp_exact(float d) {
 // of exp_f32 the few hundred values a bf16 takes there leave every row's sum
 // 6e-8 too large, which a sequence's sum of log ratios adds up.  What H lacks
 // is first order: 2^(z D) = 2^(m D) (1 + (z - m) D ln 2), from sum v z.
-// x y with 0 times anything 0 (v_mul_legacy_f32): a masked logit's x is 0
-__device__ float mul_zero(float x, float y) __asm("llvm.amdgcn.fmul.legacy");
-
 constexpr float kH = 0x1.7154p+0f;
 constexpr float kDLn2 = 0x1.480fb6p-18f;   // (log2(e) - kH) ln 2
 
@@ -90,12 +87,6 @@ __device__ __forceinline__ uint4 pack(const float (&f)[vec<T>()]) {
 __device__ __forceinline__ void forget(uint4& q) {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("" : "+v"(q.x), "+v"(q.y), "+v"(q.z), "+v"(q.w));
-}
-// a chunk of -inf: what stands in for values past a row's end
-template <typename T>
-__device__ __forceinline__ uint4 no_values() {
-  const uint32_t w = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-  return make_uint4(w, w, w, w);
 }
 
 // A row of any alignment: `head` values up to the first 16-byte boundary, `nb`
@@ -174,35 +165,48 @@ __device__ __forceinline__ MaxSum wg_join(MaxSum a, float (*red)[2]) {
 // one keeps the exponential apart.
 template <typename T>
 struct GradOf {
-  float m, w, k, flip;     // bf16: k = log2 |w / sum|, flip: the sign of -w
+  float m, w, k;
+  uint32_t flip;           // bf16: k = log2 |w / sum|, flip: the sign of -w
   __device__ __forceinline__ GradOf(const MaxSum& a, float w_) : m(a.m), w(w_), k(-w_ / a.s) {
-    flip = __builtin_copysignf(1.f, -w_);
+    flip = w_ > 0.f ? 0x80008000u : 0u;
     if constexpr (sizeof(T) == 2) k = __builtin_amdgcn_logf(__builtin_fabsf(w_ / a.s));
   }
-  __device__ __forceinline__ float operator()(float z) const {
+  // bf16: its magnitude
+  __device__ __forceinline__ float value(float z) const {
     if constexpr (sizeof(T) == 2)
-      return flip * __builtin_amdgcn_exp2f(__builtin_fmaf(z - m, kL2e, k));
+      return __builtin_amdgcn_exp2f(__builtin_fmaf(z - m, kL2e, k));
     else
       return k * exp_f32(z - m);
+  }
+  __device__ __forceinline__ float signed_value(float z) const {
+    const float x = value(z);
+    return sizeof(T) == 2 && flip ? -x : x;
   }
   // chunk `at` of a row whose target is body value yb
   __device__ __forceinline__ uint4 chunk(const uint4& q, int at, int yb) const {
     float f[vec<T>()];
     unpack<T>(q, f);
 #pragma unroll
-    for (int e = 0; e < vec<T>(); ++e) f[e] = (*this)(f[e]);
+    for (int e = 0; e < vec<T>(); ++e) f[e] = value(f[e]);
     if ((unsigned)(yb - at * vec<T>()) < (unsigned)vec<T>()) {
+      const float add = sizeof(T) == 2 ? -__builtin_fabsf(w) : w;
 #pragma unroll
-      for (int e = 0; e < vec<T>(); ++e) f[e] += at * vec<T>() + e == yb ? w : 0.f;
+      for (int e = 0; e < vec<T>(); ++e) f[e] += at * vec<T>() + e == yb ? add : 0.f;
     }
-    return pack<T>(f);
+    uint4 o = pack<T>(f);
+    if constexpr (sizeof(T) == 2) {
+      o.x ^= flip; o.y ^= flip; o.z ^= flip; o.w ^= flip;
+    }
+    return o;
   }
 };
 
-// Adds a batch of chunks to a thread's part: the maximum first, so that the
-// sum is rescaled once a batch.
-template <typename T, int N>
-__device__ __forceinline__ void add_batch(MaxSum& a, uint4 (&q)[N]) {
+// Adds a batch of chunks to a thread's part: the maximum first, so that the sum
+// is rescaled once a batch.  Of a batch that is not FULL the first n chunks
+// count and the others repeat one of them: that leaves the maximum alone, and a
+// select keeps them out of the sums without a branch.
+template <typename T, bool FULL, int N>
+__device__ __forceinline__ void add_batch(MaxSum& a, uint4 (&q)[N], int n) {
   float m = a.m;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -216,34 +220,44 @@ __device__ __forceinline__ void add_batch(MaxSum& a, uint4 (&q)[N]) {
     a.s *= exp_exact(a.m - m);
     a.m = m;
   }
-  if (__builtin_fabsf(m) < 0x1p20f) {
-    const float R = __builtin_rintf(m * kH);
-    float s = 0.f, sz = 0.f;
+  const float R = __builtin_rintf(m * kH);
+  float s = 0.f, sz = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float f[vec<T>()];
-      forget(q[i]);
-      unpack<T>(q[i], f);
+  for (int i = 0; i < N; ++i) {
+    float f[vec<T>()];
+    forget(q[i]);
+    unpack<T>(q[i], f);
+    float c = 0.f, cz = 0.f;
 #pragma unroll
-      for (int e = 0; e < vec<T>(); ++e) {
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(f[e], kH, -R));
-        s += x;
-        sz += mul_zero(x, f[e]);
-      }
+    for (int e = 0; e < vec<T>(); ++e) {
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(f[e], kH, -R));
+      c += x;
+      cz = __builtin_fmaf(x, f[e], cz);
     }
-    // relative to the maximum itself: 2^(R - m H)
-    a.s += __builtin_fmaf(kDLn2, __builtin_fmaf(-m, s, sz), s) *
-           __builtin_amdgcn_exp2f(__builtin_fmaf(-m, kH, R));
-  } else {   // no value yet, or of a size (or an infinity) the above cannot scale
-    const float ref = m == -kInf ? 0.f : m;
+    s += FULL || i < n ? c : 0.f;
+    sz += FULL || i < n ? cz : 0.f;
+  }
+  // relative to the maximum itself: 2^(R - m H)
+  s = __builtin_fmaf(kDLn2, __builtin_fmaf(-m, s, sz), s) *
+      __builtin_amdgcn_exp2f(__builtin_fmaf(-m, kH, R));
+  a.s += s;
+}
+// Whether a thread's part has to be summed again: a -inf (0 times it above), a
+// NaN, or logits of a size H cannot scale.
+__device__ __forceinline__ bool failed(const MaxSum& a) {
+  return !(a.s < kInf) || (__builtin_fabsf(a.m) > 0x1p20f && a.m != -kInf);
+}
+// The sum of chunks c, c + step, .. below c1, against a maximum that is known.
+template <typename T>
+__device__ __forceinline__ void sum_again(MaxSum& a, const Row<T>& r, int c, int c1, int step) {
+  const float ref = a.m == -kInf ? 0.f : a.m;
+  a.s = 0.f;
+#pragma unroll 1
+  for (; c < c1; c += step) {
+    float f[vec<T>()];
+    unpack<T>(r.chunk(c), f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float f[vec<T>()];
-      forget(q[i]);
-      unpack<T>(q[i], f);
-#pragma unroll
-      for (int e = 0; e < vec<T>(); ++e) a.s += exp_f32(f[e] - ref);
-    }
+    for (int e = 0; e < vec<T>(); ++e) a.s += exp_exact(f[e] - ref);
   }
 }
 __device__ __forceinline__ void add_value(MaxSum& a, float x) {
@@ -283,16 +297,17 @@ __global__ __launch_bounds__(kT) void k_row_stats(LogitsView v, RowOut o, int sl
     uint4 q[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) q[i] = r.chunk(c + kT * i);
-    add_batch<T>(a, q);
+    add_batch<T, true>(a, q, kBatch);
   }
-  if (c - tid < c1) {
+  if (c < c1) {
     uint4 q[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      q[i] = c + kT * i < c1 ? r.chunk(c + kT * i) : no_values<T>();
-    add_batch<T>(a, q);
+      q[i] = r.chunk(c + kT * i < c1 ? c + kT * i : c);
+    add_batch<T, false>(a, q, (c1 - c + kT - 1) / kT);
   }
-  if (sl == 0 && (int)threadIdx.x < r.edge) add_value(a, ld1(r.z + r.edge_at(threadIdx.x)));
+  if (failed(a)) sum_again<T>(a, r, c0 + tid, c1, kT);
+  if (sl == 0 && tid < r.edge) add_value(a, ld1(r.z + r.edge_at(tid)));
   a = wg_join<kT / 64>(a, red);
   if (threadIdx.x != 0) return;
   const float zy = ld1(r.z + y);
@@ -384,23 +399,29 @@ __global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const MaxSum* sta
   }
   if (at_edge) {
     const int at = r.edge_at(threadIdx.x);
-    st1(d + at, grad(ld1(r.z + at)) + (at == y ? c : 0.f));
+    st1(d + at, grad.signed_value(ld1(r.z + at)) + (at == y ? c : 0.f));
   }
 }
 
 // ------------------------------------------------------- between the streams
-// Sum over the workgroup in a fixed order, the result in every thread; red: a
-// double for each wave.
-template <int NT>
-__device__ __forceinline__ double wg_sum(double x, double* red) {
-  x = wave_sum(x);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-  __syncthreads();
-  x = red[0];
+// Sums over the workgroup in a fixed order, the results in every thread; red: N
+// doubles for each wave.
+template <int NT, int N>
+__device__ __forceinline__ void wg_sum(double (&x)[N], double (*red)[N]) {
 #pragma unroll
-  for (int w = 1; w < NT / 64; ++w) x += red[w];
-  return x;
+  for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[threadIdx.x >> 6][i] = x[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = red[0][i];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) x[i] += red[w][i];
+  }
 }
 
 // Whether this workgroup is the last of n to come here.  What each wrote
@@ -430,35 +451,34 @@ __device__ __forceinline__ void zero_outside(const LogitsView& v, float* w) {
 
 // Workgroup per pair, its two sequences in one pass; the last one adds the
 // pairs' losses in their order.
-constexpr int kSeqT = 1024;
+constexpr int kSeqT = 512;
 
 __global__ __launch_bounds__(kSeqT) void k_preference(LogitsView v, RowOut o, PreferenceArgs a,
                                                       int slices) {
-  __shared__ double red[kSeqT / 64];
+  __shared__ double red[kSeqT / 64][6];
   const int p = blockIdx.x;
   const int64_t b = cu_at(v, 2 * p), mid = cu_at(v, 2 * p + 1), e = cu_at(v, 2 * p + 2);
-  double lp[2] = {0, 0}, lr[2] = {0, 0}, n[2] = {0, 0};
+  double sum[6] = {0, 0, 0, 0, 0, 0};   // logp, log ratio, targets of either
   zero_outside(v, o.w);
   for (int64_t t = b + threadIdx.x; t < e; t += kSeqT) {
     if (v.labels[t] < 0) continue;
     const double l = row_logp(v, o, slices, t);
     const double d = l - (a.ref ? (double)a.ref[t] : 0.0);
     const bool second = t >= mid;
-    lp[0] += second ? 0.0 : l;
-    lr[0] += second ? 0.0 : d;
-    n[0] += second ? 0.0 : 1.0;
-    lp[1] += second ? l : 0.0;
-    lr[1] += second ? d : 0.0;
-    n[1] += second ? 1.0 : 0.0;
+    sum[0] += second ? 0.0 : l;
+    sum[1] += second ? 0.0 : d;
+    sum[2] += second ? 0.0 : 1.0;
+    sum[3] += second ? l : 0.0;
+    sum[4] += second ? d : 0.0;
+    sum[5] += second ? 1.0 : 0.0;
   }
+  wg_sum<kSeqT, 6>(sum, red);
+  double lr[2], n[2];
   for (int i = 0; i < 2; ++i) {
-    lp[i] = wg_sum<kSeqT>(lp[i], red);
-    lr[i] = wg_sum<kSeqT>(lr[i], red);
-    n[i] = wg_sum<kSeqT>(n[i], red);
-    if (!a.length_mean || n[i] < 1) n[i] = 1;
-    lr[i] /= n[i];
+    n[i] = a.length_mean && sum[3 * i + 2] > 1 ? sum[3 * i + 2] : 1;
+    lr[i] = sum[3 * i + 1] / n[i];
     if (threadIdx.x == 0) {
-      if (a.seq_logp) a.seq_logp[2 * p + i] = (float)(lp[i] / n[i]);
+      if (a.seq_logp) a.seq_logp[2 * p + i] = (float)(sum[3 * i] / n[i]);
       if (a.rewards) a.rewards[2 * p + i] = (float)(a.beta * lr[i]);
     }
   }
@@ -486,24 +506,53 @@ __global__ __launch_bounds__(kSeqT) void k_preference(LogitsView v, RowOut o, Pr
     o.w[t] = v.labels[t] < 0 ? 0.f : t < mid ? w0 : w1;
   if (threadIdx.x == 0) device_store(a.pair_loss + p, loss);
   if (!last_of(o.ticket, gridDim.x)) return;
-  double tot = 0;
-  for (int k = threadIdx.x; k < a.pairs; k += kSeqT) tot += device_load(a.pair_loss + k);
-  tot = wg_sum<kSeqT>(tot, red);
-  if (threadIdx.x == 0) *a.loss = (float)(tot / a.pairs);
+  __shared__ double last[kSeqT / 64][1];
+  double tot[1] = {0};
+  for (int k = threadIdx.x; k < a.pairs; k += kSeqT) tot[0] += device_load(a.pair_loss + k);
+  wg_sum<kSeqT, 1>(tot, last);
+  if (threadIdx.x == 0) *a.loss = (float)(tot[0] / a.pairs);
 }
 
-// Workgroup per sequence: its targets, and its rows' sequence.
+__device__ __forceinline__ void list_targets(const LogitsView& v, int* list) {
+  __shared__ int count[2][kSeqT / 64];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  int n = 0;
+  auto label = [&](int64_t t) { return t < v.rows ? v.labels[t] : -1; };
+  int64_t y = label(threadIdx.x);
+  for (int64_t t0 = 0, k = 0; t0 < v.rows; t0 += kSeqT, k ^= 1) {
+    const int64_t t = t0 + threadIdx.x;
+    const bool yes = y >= 0 && y < v.vocab && !outside(v, t);
+    y = label(t + kSeqT);                       // the next rows', in flight
+    const uint64_t in = __ballot(yes);
+    if (lane == 0) count[k][wv] = __popcll(in);
+    __syncthreads();
+    int at = n + __popcll(in & ((1ull << lane) - 1));
+    for (int w = 0; w < kSeqT / 64; ++w) {
+      at += w < wv ? count[k][w] : 0;
+      n += count[k][w];
+    }
+    if (yes) list[at] = (int)t;
+  }
+  if (threadIdx.x == 0) list[v.rows] = n;
+}
+
+// Workgroup per sequence: its targets, and its rows' sequence.  One more lists
+// all rows with a target, in order, where the one-pass form shares them out.
 __global__ __launch_bounds__(kSeqT) void k_policy_count(LogitsView v, RowOut o, PolicyArgs a) {
-  __shared__ double red[kSeqT / 64];
+  __shared__ double red[kSeqT / 64][1];
   const int i = blockIdx.x;
   if (i == 0 && threadIdx.x == 0) *o.ticket = 0;
-  double n = 0;
+  if (i == v.nseq) {
+    list_targets(v, a.list);
+    return;
+  }
+  double n[1] = {0};
   for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += kSeqT) {
-    n += v.labels[t] >= 0;
+    n[0] += v.labels[t] >= 0;
     a.seq[t] = i;
   }
-  n = wg_sum<kSeqT>(n, red);
-  if (threadIdx.x == 0) a.count[i] = (int)n;
+  wg_sum<kSeqT, 1>(n, red);
+  if (threadIdx.x == 0) a.count[i] = (int)n[0];
 }
 
 // All targets, and the sequences that have any.
@@ -511,14 +560,14 @@ struct Totals {
   double targets, filled;
 };
 template <int NT>
-__device__ __forceinline__ Totals totals(const PolicyArgs& a, int nseq, double* red) {
-  double n = 0, f = 0;
+__device__ __forceinline__ Totals totals(const PolicyArgs& a, int nseq, double (*red)[2]) {
+  double n[2] = {0, 0};
   for (int j = threadIdx.x; j < nseq; j += NT) {
-    n += a.count[j];
-    f += a.count[j] > 0;
+    n[0] += a.count[j];
+    n[1] += a.count[j] > 0;
   }
-  n = wg_sum<NT>(n, red);
-  return Totals{n, wg_sum<NT>(f, red)};
+  wg_sum<NT, 2>(n, red);
+  return Totals{n[0], n[1]};
 }
 // weight of one target of sequence i in the mean
 __device__ __forceinline__ double share_of(const PolicyArgs& a, const Totals& n, int i) {
@@ -545,12 +594,12 @@ __device__ __forceinline__ Term policy_term(const PolicyArgs& a, double l, doubl
 
 // Workgroup per sequence; the last one adds the sequences' sums in their order.
 __global__ __launch_bounds__(kSeqT) void k_policy(LogitsView v, RowOut o, PolicyArgs a, int slices) {
-  __shared__ double red[kSeqT / 64];
+  __shared__ double tred[kSeqT / 64][2], red[kSeqT / 64][3];
   const int i = blockIdx.x;
   zero_outside(v, o.w);
-  const Totals n = totals<kSeqT>(a, v.nseq, red);
+  const Totals n = totals<kSeqT>(a, v.nseq, tred);
   const double share = share_of(a, n, i);
-  double loss = 0, kl = 0, cut = 0;
+  double sum[3] = {0, 0, 0};            // loss, kl, clipped
   for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += kSeqT) {
     if (v.labels[t] < 0) {
       o.w[t] = 0.f;
@@ -558,24 +607,22 @@ __global__ __launch_bounds__(kSeqT) void k_policy(LogitsView v, RowOut o, Policy
     }
     const double A = (double)(a.token_adv ? a.adv[t] : a.adv[i]);
     const Term x = policy_term(a, row_logp(v, o, slices, t), A, t);
-    loss += x.loss;
-    kl += x.kl;
-    cut += x.clipped;
+    sum[0] += x.loss;
+    sum[1] += x.kl;
+    sum[2] += x.clipped;
     o.w[t] = (float)(share * x.dlogp);
   }
-  loss = wg_sum<kSeqT>(loss, red);
-  kl = wg_sum<kSeqT>(kl, red);
-  cut = wg_sum<kSeqT>(cut, red);
+  wg_sum<kSeqT, 3>(sum, red);
   if (threadIdx.x == 0) {
-    device_store(a.sums + 3 * i, share * loss);
-    device_store(a.sums + 3 * i + 1, share * kl);
-    device_store(a.sums + 3 * i + 2, cut);
+    device_store(a.sums + 3 * i, share * sum[0]);
+    device_store(a.sums + 3 * i + 1, share * sum[1]);
+    device_store(a.sums + 3 * i + 2, sum[2]);
   }
   if (!last_of(o.ticket, gridDim.x)) return;
   double x[3] = {0, 0, 0};
   for (int j = threadIdx.x; j < v.nseq; j += kSeqT)
     for (int k = 0; k < 3; ++k) x[k] += device_load(a.sums + 3 * j + k);
-  for (int k = 0; k < 3; ++k) x[k] = wg_sum<kSeqT>(x[k], red);
+  wg_sum<kSeqT, 3>(x, red);
   if (threadIdx.x == 0) {
     a.out[0] = (float)x[0];
     a.out[1] = (float)x[1];
@@ -598,7 +645,7 @@ template <typename T, int NT, int NC>
 __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, PolicyArgs a, T* dz,
                                                     int64_t ldd) {
   __shared__ float red[NT / 64][2];
-  __shared__ double dred[NT / 64];
+  __shared__ double dred[NT / 64][2];
   constexpr int kSum = 4;                       // chunks summed at a time
   const Totals n = totals<NT>(a, v.nseq, dred);
   const int64_t step = gridDim.x;
@@ -606,10 +653,9 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
     const int64_t y = v.labels[t];
     return y >= 0 && y < v.vocab && !outside(v, t);
   };
-  auto next_target = [&](int64_t t) {
-    while (t < v.rows && !has_target(t)) t += step;
-    return t;
-  };
+  // every step-th of the rows with a target: as many for each workgroup, to one
+  const int rows_with = a.list[v.rows];
+  auto listed = [&](int64_t k) { return k < rows_with ? (int64_t)a.list[k] : v.rows; };
   auto store = [&](T* d, int head, int k, const uint4& q) {
     __builtin_nontemporal_store(
         __builtin_bit_cast(u32x4_t, q),
@@ -632,7 +678,7 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
       o.logp[t] = none;
     }
   }
-  int64_t t = next_target(blockIdx.x);
+  int64_t k0 = blockIdx.x, t = listed(k0);
   if (t >= v.rows) return;
   uint4 q[NC];
   float ze, zy;
@@ -645,7 +691,7 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int k = (int)threadIdx.x + NT * i;
-      q[i] = k < r.nb ? r.chunk(k) : no_values<T>();
+      q[i] = r.chunk(k < r.nb ? k : r.nb - 1);
     }
     load_edge(r, t, threadIdx.x);
   }
@@ -653,18 +699,23 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
     // (opaque, or the chunks' offsets are kept in registers over the rows)
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
-    const int64_t tn = next_target(t + step);
+    k0 += step;
+    const int64_t tn = listed(k0);
     const Row<T> r(v, t), rn(v, tn < v.rows ? tn : t);
-    const int nbn = tn < v.rows ? rn.nb : 0;    // chunks of the next row, none without one
+    const int nbn = tn < v.rows ? rn.nb : 1;    // (without a next row one chunk, unused)
     const int64_t y = v.labels[t];
     const int sq = a.seq[t];
     const float A = a.token_adv ? a.adv[t] : a.adv[sq];
     const float share = (float)share_of(a, n, sq);
     const float old_logp = a.old_logp ? a.old_logp[t] : 0.f, ref = a.ref ? a.ref[t] : 0.f;
+    // this thread's chunks; loads past a row's end repeat its last one
+    const int mine = (r.nb - tid + NT - 1) / NT;
     MaxSum s{-kInf, 0.f};
 #pragma unroll
     for (int i = 0; i < NC; i += kSum)
-      add_batch<T>(s, *reinterpret_cast<uint4(*)[kSum]>(&q[i]));
+      add_batch<T, false>(s, *reinterpret_cast<uint4(*)[kSum]>(&q[i]), mine - i);
+    if (mine <= 0) s = MaxSum{-kInf, 0.f};
+    if (failed(s)) sum_again<T>(s, r, tid, r.nb, NT);
     if (tid < r.edge) add_value(s, ze);
     s = wg_join<NT / 64>(s, red);
     if (tid == 0) {
@@ -688,11 +739,11 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
       forget(q[i]);
       if (at < r.nb)
         store(d, r.head, at, w == 0.f ? make_uint4(0u, 0u, 0u, 0u) : grad.chunk(q[i], at, yb));
-      q[i] = at < nbn ? rn.chunk(at) : no_values<T>();
+      q[i] = rn.chunk(at < nbn ? at : nbn - 1);
     }
     if (tid < r.edge) {
       const int at = r.edge_at(tid);
-      st1(d + at, w == 0.f ? 0.f : grad(zt) + (at == y ? w : 0.f));
+      st1(d + at, w == 0.f ? 0.f : grad.signed_value(zt) + (at == y ? w : 0.f));
     }
     if (tn < v.rows) load_edge(rn, tn, tid);
     t = tn;
@@ -761,13 +812,13 @@ static hipError_t policy_rows(const LogitsView& v, const RowOut& o, const Policy
                        dim3(NT), s, v, o, a, static_cast<T*>(dz), ldd);
 }
 
-// The one-pass form where a row fits in registers, the rows fill the chip and
-// the gradient's rows start where the logits' do between 16-byte boundaries.
+// The one-pass form where a row fits in registers and is long enough to be worth
+// a workgroup (16 KB), the rows fill the chip, and the gradient's rows start
+// where the logits' do between 16-byte boundaries.
 template <typename T>
 static hipError_t policy_rows_of(const LogitsView& v, const RowOut& o, const PolicyArgs& a,
                                  void* dz, int64_t ldd, hipStream_t s) {
   const int64_t chunks = row_chunks(v.vocab, v.bf16);
-  if (chunks <= 256 * 4) return policy_rows<T, 256, 4>(v, o, a, dz, ldd, s);
   if (chunks <= 256 * 16) return policy_rows<T, 256, 16>(v, o, a, dz, ldd, s);
   if (chunks <= 512 * 16) return policy_rows<T, 512, 16>(v, o, a, dz, ldd, s);
   return policy_rows<T, 1024, 16>(v, o, a, dz, ldd, s);
@@ -775,7 +826,7 @@ static hipError_t policy_rows_of(const LogitsView& v, const RowOut& o, const Pol
 static bool one_pass(const LogitsView& v, const void* dz, int64_t ldd) {
   const int64_t chunks = row_chunks(v.vocab, v.bf16);
   const uintptr_t apart = ((uintptr_t)dz - (uintptr_t)v.z) | (uintptr_t)((ldd - v.ld) * (v.bf16 ? 2 : 4));
-  return chunks <= 1024 * 16 && v.rows >= 256 && (apart & 15) == 0;
+  return chunks >= 1024 && chunks <= 1024 * 16 && v.rows >= 256 && (apart & 15) == 0;
 }
 
 hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs& a, void* dz,
@@ -784,7 +835,8 @@ hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs&
   // (0 slices: the statistics are there, logp is not)
   const int slices = fused ? 0 : row_slices(v);
   hipError_t e =
-      launch_kernel(k_policy_count, dim3((unsigned)v.nseq), dim3(kSeqT), s, v, o, a);
+      launch_kernel(k_policy_count, dim3((unsigned)v.nseq + (fused ? 1 : 0)), dim3(kSeqT), s, v, o,
+                    a);
   if (e != hipSuccess) return e;
   if (fused)
     e = v.bf16 ? policy_rows_of<uint16_t>(v, o, a, dz, ldd, s)
