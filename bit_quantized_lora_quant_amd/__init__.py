@@ -6,6 +6,7 @@ memory and the current HIP stream, every step of the computation runs in the
 library's HIP kernels.  There is no CPU fallback: if the library is missing,
 every call raises.
 """
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -201,8 +202,14 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a torch.cuda.Stream around it
+# (0.1 us against 2.8: what a small call costs the host counts).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
 
 
 def qlora_nf4_codebook():
@@ -721,20 +728,24 @@ def adamw8_states(numels, device, hbm_budget: int = None):
     return [AdamW8State(n, device, host=h) for n, h in zip(numels, host)]
 
 
-def _require(ok, what: str):
+def _require(ok, what: str, detail: str = "", *args):
     """Refuses arguments the library cannot check itself (a host tensor's
     address, a tensor too short) the way it refuses the others."""
     if not ok:
-        raise QloraError(QLORA_ERR_INVALID_ARG, what)
+        raise QloraError(QLORA_ERR_INVALID_ARG, what + (": " + detail % args if detail else ""))
+
+
+_HERE_ALREADY = contextlib.nullcontext()
 
 
 def _on(what: str, first, *more):
     """All given tensors are on one GPU; the calls run on that GPU's current
     stream, whichever device is the current one."""
-    _require(first.is_cuda, what + ": tensors must be on a GPU")
+    _require(first.is_cuda, what, "tensors must be on a GPU")
+    d = first.device
     for t in more:
-        _require(t is None or t.device == first.device, what + ": tensors on different devices")
-    return torch.cuda.device(first.device)
+        _require(t is None or t.device == d, what, "tensors on different devices")
+    return _HERE_ALREADY if d.index == torch.cuda.current_device() else torch.cuda.device(d)
 
 
 class Act8Tensor:
@@ -743,8 +754,8 @@ class Act8Tensor:
     owned by torch; existing ones can be handed in."""
 
     def __init__(self, rows: int, cols: int, device=None, codes=None, scale=None):
-        _require(rows >= 0 and cols > 0 and cols % ACT8_BLOCK == 0,
-                 "Act8Tensor: cols must be a multiple of %d" % ACT8_BLOCK)
+        _require(rows >= 0 and cols > 0 and cols % ACT8_BLOCK == 0, "Act8Tensor",
+                 "cols must be a multiple of %d", ACT8_BLOCK)
         self.rows, self.cols = rows, cols
         if codes is None:
             codes = torch.empty((rows, cols), dtype=torch.int8, device=device)
@@ -804,9 +815,9 @@ def _bwd_act8(what, q, a, A, B, R, dY, XA_in, need_dx, dX, dA, dB, ws):
     M, K, N = a.rows, a.cols, q.rows
     for t, shape, name in ((A, (R, K), "A"), (B, (N, R), "B"), (dY, (M, N), "dY"),
                            (XA_in, (M, R), "XA_in")):
-        _require(t.dtype == torch.bfloat16 and t.is_contiguous() and tuple(t.shape) == shape,
-                 "%s: %s must be contiguous bf16 %s" % (what, name, list(shape)))
-    _require(K == q.cols, what + ": checkpoint of another width than the weight")
+        _require(t.dtype == torch.bfloat16 and t.is_contiguous() and t.shape == shape, what,
+                 "%s must be contiguous bf16 %s", name, shape)
+    _require(K == q.cols, what, "checkpoint of another width than the weight")
     dev = dY.device
     if need_dx and dX is None:
         dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
@@ -817,8 +828,8 @@ def _bwd_act8(what, q, a, A, B, R, dY, XA_in, need_dx, dX, dA, dB, ws):
     for t, shape, dt, name in ((dX if need_dx else None, (M, K), torch.bfloat16, "dX"),
                                (dA, (R, K), torch.float32, "dA"),
                                (dB, (N, R), torch.float32, "dB")):
-        _require(t is None or (t.dtype == dt and t.is_contiguous() and tuple(t.shape) == shape),
-                 "%s: %s must be contiguous %s %s" % (what, name, dt, list(shape)))
+        _require(t is None or (t.dtype == dt and t.is_contiguous() and t.shape == shape), what,
+                 "%s must be contiguous %s %s", name, dt, shape)
     if ws is None:
         ws = workspace(qlora_linear_act8_workspace_bytes(M, N, K, R), dev)
     return dX if need_dx else None, dA, dB, ws
@@ -834,7 +845,7 @@ def qlora_linear_bwd_act8(q: NF4Tensor, a: Act8Tensor, A, B, alpha: float, dY, X
     dX, dA, dB, ws = _bwd_act8(what, q, a, A, B, r, dY, XA_in, need_dx, dX, dA, dB, ws)
     _require(keep_bits is None or (keep_bits.dtype == torch.uint8 and
                                    keep_bits.numel() * 8 >= a.rows * a.cols),
-             what + ": keep_bits must be uint8 [M K / 8]")
+             what, "keep_bits must be uint8 [M K / 8]")
     with _on(what, dY, a.codes, q.codes, A, B, XA_in, dX, dA, dB, ws, keep_bits):
         d, x8, dr = q.descriptor(), a.descriptor(), _dropout(dropout)
         _check(lib().qlora_linear_bwd_act8(ctypes.byref(d), ctypes.byref(x8), _ptr(A), _ptr(B), r,
@@ -867,9 +878,9 @@ def _logits(what, logits, labels):
     and their int64 targets."""
     _require(logits.dim() == 2 and logits.dtype in (torch.bfloat16, torch.float32) and
              logits.shape[1] >= 1 and (logits.stride(1) == 1 or logits.shape[1] == 1),
-             what + ": logits must be bf16 or float32 [rows, vocab] with dense rows")
+             what, "logits must be bf16 or float32 [rows, vocab] with dense rows")
     _require(labels.dtype == torch.int64 and labels.is_contiguous() and
-             labels.shape == (logits.shape[0],), what + ": labels must be int64 [rows]")
+             labels.shape == logits.shape[:1], what, "labels must be int64 [rows]")
     rows, vocab = logits.shape
     ld = logits.stride(0) if rows > 1 else vocab
     return LogitsDescriptor(logits.data_ptr(),
@@ -883,24 +894,26 @@ def _dlogits_like(what, logits, dlogits):
     rows, vocab = logits.shape
     if dlogits is None:
         ld = max(logits.stride(0), vocab) if rows > 1 else vocab
-        dlogits = torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
+        dlogits = torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)
+        if ld != vocab:
+            dlogits = dlogits[:, :vocab]
     _require(dlogits.shape == logits.shape and dlogits.dtype == logits.dtype and
              (dlogits.stride(1) == 1 or vocab == 1),
-             what + ": dlogits must have the logits' shape and type, with dense rows")
+             what, "dlogits must have the logits' shape and type, with dense rows")
     return dlogits, (dlogits.stride(0) if rows > 1 else vocab)
 
 
 def _rows_f32(what, rows, *named):
     for t, name in named:
         _require(t is None or (t.dtype == torch.float32 and t.is_contiguous() and
-                               t.numel() == rows), "%s: %s must be float32 of %d values"
-                 % (what, name, rows))
+                               t.numel() == rows), what, "%s must be float32 of %d values", name,
+                 rows)
 
 
 def _sequences(what, cu_seqlens):
     _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.is_contiguous() and
              cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2,
-             what + ": cu_seqlens must be int32 [sequences + 1]")
+             what, "cu_seqlens must be int32 [sequences + 1]")
     return cu_seqlens.numel() - 1
 
 
@@ -975,13 +988,14 @@ def qlora_preference_loss(logits, labels, cu_seqlens, ref_logp=None, beta: float
     what = "qlora_preference_loss"
     z = _logits(what, logits, labels)
     n = _sequences(what, cu_seqlens)
-    _require(n % 2 == 0, what + ": cu_seqlens must describe pairs")
-    _require(loss_type in PREFERENCE_KINDS, what + ": unknown loss_type")
+    _require(n % 2 == 0, what, "cu_seqlens must describe pairs")
+    _require(loss_type in PREFERENCE_KINDS, what, "unknown loss_type")
     _rows_f32(what, z.rows, (ref_logp, "ref_logp"), (w, "w"))
     _rows_f32(what, 2 * z.rows, (stats, "stats"))
     dev = logits.device
-    buf = torch.empty(2 * n + z.rows + 1, dtype=torch.float32, device=dev)
-    seq_logp, rewards, logp, loss = buf.split((n, n, z.rows, 1))
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    seq_logp, rewards = torch.empty((2, n), dtype=torch.float32, device=dev).unbind()
+    logp = torch.empty(z.rows, dtype=torch.float32, device=dev)
     ldd = 0
     if return_grad or dlogits is not None:
         dlogits, ldd = _dlogits_like(what, logits, dlogits)
@@ -994,7 +1008,7 @@ def qlora_preference_loss(logits, labels, cu_seqlens, ref_logp=None, beta: float
                                            _ptr(seq_logp), _ptr(rewards), _ptr(logp), _ptr(stats),
                                            _ptr(w), _ptr(dlogits), ldd, _ptr(ws), ws.numel(),
                                            _stream()), what)
-    return PreferenceLoss(loss[0], seq_logp, rewards, logp, dlogits)
+    return PreferenceLoss(loss, seq_logp, rewards, logp, dlogits)
 
 
 def qlora_policy_loss(logits, labels, cu_seqlens, advantages, old_logp=None, ref_logp=None,
@@ -1011,13 +1025,13 @@ def qlora_policy_loss(logits, labels, cu_seqlens, advantages, old_logp=None, ref
     what = "qlora_policy_loss"
     z = _logits(what, logits, labels)
     n = _sequences(what, cu_seqlens)
-    _require(reduction in POLICY_REDUCTIONS, what + ": unknown reduction")
+    _require(reduction in POLICY_REDUCTIONS, what, "unknown reduction")
     _rows_f32(what, z.rows if token_advantages else n, (advantages, "advantages"))
     _rows_f32(what, z.rows, (old_logp, "old_logp"), (ref_logp, "ref_logp"), (w, "w"))
     _rows_f32(what, 2 * z.rows, (stats, "stats"))
     dev = logits.device
-    buf = torch.empty(3 + z.rows, dtype=torch.float32, device=dev)
-    out, logp = buf.split((3, z.rows))
+    out = torch.empty(3, dtype=torch.float32, device=dev)
+    logp = torch.empty(z.rows, dtype=torch.float32, device=dev)
     ldd = 0
     if return_grad or dlogits is not None:
         dlogits, ldd = _dlogits_like(what, logits, dlogits)
@@ -1031,7 +1045,7 @@ def qlora_policy_loss(logits, labels, cu_seqlens, advantages, old_logp=None, ref
                                        _ptr(old_logp), _ptr(ref_logp), ctypes.byref(h), _ptr(out),
                                        _ptr(logp), _ptr(stats), _ptr(w), _ptr(dlogits), ldd,
                                        _ptr(ws), ws.numel(), _stream()), what)
-    return PolicyLoss(out[0], out[1], out[2], logp, dlogits)
+    return PolicyLoss(*out.unbind(), logp, dlogits)
 
 
 def qlora_trace_begin(kernels, capacity: int = 4096):
@@ -1132,7 +1146,7 @@ class PreferenceLossFn(torch.autograd.Function):
                                   label_smoothing, length_mean, stats=stats, w=w)
         ctx.save_for_backward(logits, labels, stats, w)
         ctx.mark_non_differentiable(o.seq_logp, o.rewards)
-        return o.loss.clone(), o.seq_logp, o.rewards
+        return o.loss, o.seq_logp, o.rewards
 
     @staticmethod
     def backward(ctx, g, *_):

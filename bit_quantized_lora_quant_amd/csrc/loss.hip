@@ -18,6 +18,10 @@ namespace {
 constexpr int kT = 256;          // threads of a workgroup
 constexpr int kBatch = 8;        // 16-byte loads a thread has in flight
 constexpr float kInf = __builtin_inff();
+// Bytes of the last rows that the statistics launch loads to stay cached (of the
+// 256 MB Infinity Cache), for the gradient launch, which begins with them; the
+// rows before go through without displacing them.
+constexpr int64_t kKept = (int64_t)160 << 20;
 
 // exp(d), d <= 0 or NaN; log2(e) as the nearest float32 and what that lacks
 constexpr float kL2e = 0x1.715476p+0f, kL2eLow = 0x1.4ae0bep-26f;
@@ -108,8 +112,15 @@ struct Row {
   // chunk k: a row is uniform in a workgroup, so its base stays in scalar
   // registers and a lane has a 32-bit offset
   __device__ __forceinline__ uint4 chunk(int k) const {
-    return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(z + head) +
-                                           (uint32_t)k * 16u);
+    return *reinterpret_cast<const uint4*>(at(k));
+  }
+  // the same, not to be kept by the caches
+  __device__ __forceinline__ uint4 chunk_once(int k) const {
+    return __builtin_bit_cast(
+        uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(at(k))));
+  }
+  __device__ __forceinline__ const char* at(int k) const {
+    return reinterpret_cast<const char*>(z + head) + (uint32_t)k * 16u;
   }
   // value index of edge element k
   __device__ __forceinline__ int edge_at(int k) const {
@@ -293,10 +304,16 @@ __global__ __launch_bounds__(kT) void k_row_stats(LogitsView v, RowOut o, int sl
   MaxSum a{-kInf, 0.f};
   const int tid = threadIdx.x;
   int c = c0 + tid;
+  const bool keep = (v.rows - t) * v.ld * (int64_t)sizeof(T) < kKept;
   for (; c - tid + kT * kBatch <= c1; c += kT * kBatch) {
     uint4 q[kBatch];
+    if (keep) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) q[i] = r.chunk(c + kT * i);
+      for (int i = 0; i < kBatch; ++i) q[i] = r.chunk(c + kT * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) q[i] = r.chunk_once(c + kT * i);
+    }
     add_batch<T, true>(a, q, kBatch);
   }
   if (c < c1) {
@@ -387,7 +404,7 @@ __global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const MaxSum* sta
   uint4 q[kBatch];
 #pragma unroll
   for (int i = 0; i < kBatch; ++i)
-    if (c0 + kT * i < r.nb) q[i] = r.chunk(c0 + kT * i);
+    if (c0 + kT * i < r.nb) q[i] = r.chunk_once(c0 + kT * i);
   const GradOf<T> grad(stats[t], c);
   const int yb = y < v.vocab ? (int)y - r.head : -vec<T>();
 #pragma unroll
@@ -691,7 +708,7 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int k = (int)threadIdx.x + NT * i;
-      q[i] = r.chunk(k < r.nb ? k : r.nb - 1);
+      q[i] = r.chunk_once(k < r.nb ? k : r.nb - 1);
     }
     load_edge(r, t, threadIdx.x);
   }
@@ -739,7 +756,7 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
       forget(q[i]);
       if (at < r.nb)
         store(d, r.head, at, w == 0.f ? make_uint4(0u, 0u, 0u, 0u) : grad.chunk(q[i], at, yb));
-      q[i] = rn.chunk(at < nbn ? at : nbn - 1);
+      q[i] = rn.chunk_once(at < nbn ? at : nbn - 1);
     }
     if (tid < r.edge) {
       const int at = r.edge_at(tid);
