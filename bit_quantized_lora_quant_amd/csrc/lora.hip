@@ -31,21 +31,47 @@ __device__ __forceinline__ int64_t recon_blocks(const ReconJob& J) {
   return ceil_div(J.N, kReconTile) * ceil_div(J.KB, kReconTile);
 }
 
+// NT: threads of the workgroup.  All of a thread's loads are issued before the
+// first is used (clamped to the table, so no branch stands between them): one
+// at a time their latency is the launch's time.
+template <int NT>
 __device__ __forceinline__ void recon_tile(const ReconJob& J, int64_t b,
                                            float (*tile)[kReconTile + 1]) {
+  constexpr int kPer = kReconTile * kReconTile / NT;
   const int64_t tiles_kb = ceil_div(J.KB, kReconTile);
   const int64_t n0 = (b / tiles_kb) * kReconTile, kb0 = (b % tiles_kb) * kReconTile;
-  const float mu = J.f32 ? 0.f : *J.mean;
-  for (int idx = threadIdx.x; idx < kReconTile * kReconTile; idx += blockDim.x) {
-    const int nl = idx / kReconTile, kl = idx % kReconTile;
-    const int64_t n = n0 + nl, kb = kb0 + kl;
-    if (n < J.N && kb < J.KB) {
-      const int64_t e = n * J.KB + kb;
-      tile[kl][nl] = J.f32 ? J.f32[e] : absmax_recon(J.q, J.scale, mu, e);
+  auto at = [&](int u) {
+    const int idx = (int)threadIdx.x + NT * u;
+    int64_t n = n0 + idx / kReconTile, kb = kb0 + idx % kReconTile;
+    n = n < J.N ? n : J.N - 1;
+    kb = kb < J.KB ? kb : J.KB - 1;
+    return n * J.KB + kb;
+  };
+  float v[kPer];
+  if (J.f32) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) v[u] = J.f32[at(u)];
+  } else {
+    const float mu = *J.mean;
+    int8_t q[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int64_t e = at(u);
+      q[u] = J.q[e];
+      v[u] = J.scale[e / kDqBlock];
     }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) v[u] = __builtin_fmaf((float)q[u], v[u], mu);
+  }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int idx = (int)threadIdx.x + NT * u;
+    tile[idx % kReconTile][idx / kReconTile] = v[u];
   }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < kReconTile * kReconTile; idx += blockDim.x) {
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int idx = (int)threadIdx.x + NT * u;
     const int kl = idx / kReconTile, nl = idx % kReconTile;
     const int64_t n = n0 + nl, kb = kb0 + kl;
     if (n < J.N && kb < J.KB) J.out[kb * J.N + n] = tile[kl][nl];
@@ -78,7 +104,7 @@ __global__ __launch_bounds__(sk_waves<RT>() * 64) void k_skinny_slices(SkinnyJob
   }
   if (has_rc) {
     __shared__ float tile[kReconTile][kReconTile + 1];
-    recon_tile(rc, b, tile);
+    recon_tile<sk_waves<RT>() * 64>(rc, b, tile);
   }
 }
 
@@ -237,7 +263,8 @@ __global__ __launch_bounds__(kSk2Waves * 64) void k_skinny2(SkinnyJob j0, Skinny
     if (b < b1) { skinny2_slice<RT, DROP>(j1, M, r, r32, b, arena); return; }
     b -= b1;
   }
-  if (has_rc) recon_tile(rc, b, reinterpret_cast<float (*)[kReconTile + 1]>(arena));
+  if (has_rc)
+    recon_tile<kSk2Waves * 64>(rc, b, reinterpret_cast<float (*)[kReconTile + 1]>(arena));
 }
 
 // Thread per (row m, column j < r32) of one job: adds the slices in order.
@@ -279,28 +306,42 @@ __global__ __launch_bounds__(256) void k_skinny_finish(SkinnyJob j0, SkinnyJob j
 
 // ------------------------------------------------------------------ prep
 // bf16 transpose [rows, cols] -> [cols, ldo] (zero for i in [rows, ldo)), a
-// 64 x 64 tile per workgroup through LDS: rows of the input are read along
-// cols, rows of the output written along i, both coalesced.
-constexpr int kTrTile = 64;
-
-__device__ __forceinline__ int64_t transpose_blocks(const TransposeJob& J) {
-  return ceil_div(J.ldo, kTrTile) * ceil_div(J.cols, kTrTile);
+// tile of 4096 values per workgroup through LDS: rows of the input are read
+// along cols, rows of the output written along i, both coalesced.  The tile is
+// 64 x 64, or as narrow as an adapter of rank 32 or 16 with more rows.  As
+// above, a thread's 16 loads are all in flight together.
+constexpr int kTrTile = 4096;
+__device__ __host__ __forceinline__ int tr_shift(const TransposeJob& J) {
+  return J.cols <= 16 ? 4 : J.cols <= 32 ? 5 : 6;
+}
+__device__ __host__ __forceinline__ int64_t transpose_blocks(const TransposeJob& J) {
+  const int sh = tr_shift(J);
+  return ceil_div(J.ldo, kTrTile >> sh) * ceil_div(J.cols, (int64_t)1 << sh);
 }
 
-__device__ __forceinline__ void transpose_tile(const TransposeJob& J, int64_t b,
-                                               uint16_t (*tile)[kTrTile + 2]) {
-  const int64_t tiles_j = ceil_div(J.cols, kTrTile);
-  const int64_t i0 = (b / tiles_j) * kTrTile, j0 = (b % tiles_j) * kTrTile;
-  for (int idx = threadIdx.x; idx < kTrTile * kTrTile; idx += blockDim.x) {
-    const int il = idx / kTrTile, jl = idx % kTrTile;
-    const int64_t i = i0 + il, j = j0 + jl;
-    if (j < J.cols) tile[jl][il] = i < J.rows ? J.in[i * J.cols + j] : (uint16_t)0;
+__device__ __forceinline__ void transpose_tile(const TransposeJob& J, int64_t b, uint16_t* tile) {
+  const int sh = tr_shift(J), ti = kTrTile >> sh, tj = 1 << sh, ld = ti + 2;
+  const int64_t tiles_j = ceil_div(J.cols, tj);
+  const int64_t i0 = (b / tiles_j) * ti, j0 = (b % tiles_j) * tj;
+  uint16_t v[16];
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const int idx = (int)threadIdx.x + 256 * u;
+    const int64_t i = i0 + (idx >> sh), j = j0 + (idx & (tj - 1));
+    v[u] = J.in[(i < J.rows ? i : J.rows - 1) * J.cols + (j < J.cols ? j : J.cols - 1)];
+  }
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const int idx = (int)threadIdx.x + 256 * u, il = idx >> sh;
+    tile[(idx & (tj - 1)) * ld + il] = i0 + il < J.rows ? v[u] : (uint16_t)0;
   }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < kTrTile * kTrTile; idx += blockDim.x) {
-    const int jl = idx / kTrTile, il = idx % kTrTile;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const int idx = (int)threadIdx.x + 256 * u;
+    const int jl = idx >> (12 - sh), il = idx & (ti - 1);
     const int64_t i = i0 + il, j = j0 + jl;
-    if (j < J.cols && i < J.ldo) J.out[j * J.ldo + i] = tile[jl][il];
+    if (j < J.cols && i < J.ldo) J.out[j * J.ldo + i] = tile[jl * ld + il];
   }
 }
 
@@ -308,7 +349,7 @@ __global__ __launch_bounds__(256) void k_prep(TransposeJob t0, TransposeJob t1, 
                                               ReconJob rc, int has_rc) {
   __shared__ float lds[kReconTile * (kReconTile + 1)];
   int64_t b = blockIdx.x;
-  auto tr = reinterpret_cast<uint16_t (*)[kTrTile + 2]>(lds);
+  auto tr = reinterpret_cast<uint16_t*>(lds);
   if (nt > 0) {
     const int64_t n0 = transpose_blocks(t0);
     if (b < n0) { transpose_tile(t0, b, tr); return; }
@@ -319,7 +360,7 @@ __global__ __launch_bounds__(256) void k_prep(TransposeJob t0, TransposeJob t1, 
     if (b < n1) { transpose_tile(t1, b, tr); return; }
     b -= n1;
   }
-  if (has_rc) recon_tile(rc, b, reinterpret_cast<float (*)[kReconTile + 1]>(lds));
+  if (has_rc) recon_tile<256>(rc, b, reinterpret_cast<float (*)[kReconTile + 1]>(lds));
 }
 
 // ------------------------------------------------------- adapter gradients
@@ -550,6 +591,7 @@ __device__ __forceinline__ void grad_reduce_vec4(const GradJob& J, int r, int64_
     return;
   }
   float4 s = *reinterpret_cast<const float4*>(J.partial + idx);
+#pragma unroll 8
   for (int k = 1; k < J.splits; ++k) {
     const float4 v = *reinterpret_cast<const float4*>(J.partial + (int64_t)k * stride + idx);
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
@@ -721,7 +763,7 @@ hipError_t launch_skinny(const SkinnyJob* jobs, int nj, int64_t M, int r, int r3
 
 hipError_t launch_prep(const TransposeJob* t, int nt, const ReconJob* recon, hipStream_t s) {
   int64_t blocks = 0;
-  for (int i = 0; i < nt; ++i) blocks += ceil_div(t[i].ldo, kTrTile) * ceil_div(t[i].cols, kTrTile);
+  for (int i = 0; i < nt; ++i) blocks += transpose_blocks(t[i]);
   blocks += recon ? ceil_div(recon->N, kReconTile) * ceil_div(recon->KB, kReconTile) : 0;
   if (blocks == 0) return hipSuccess;
   const TransposeJob tn{};
