@@ -157,20 +157,22 @@ __global__ __launch_bounds__(256) void k_act8_dequantize(const int8_t* __restric
 // which together are the float32 value, and each part meets the same codes:
 // three MFMAs where one would leave dA with bf16 errors.
 //
-// A workgroup takes 128 columns (two blocks) of a token slice; its 4 waves take
-// interleaved 32-token steps.  Lane (i16, g) loads, for rows m = 8 g .. 8 g + 7
-// of a step, the 4 codes of columns 4 i16 .. 4 i16 + 3 of either block: MFMA
-// (h, t) handles columns 64 h + 4 i + t, one scale block each, and converting
-// byte t of the eight rows is the transpose.  The next step's loads are in
-// flight under a step's work.  The waves' sums are added in wave order through
-// LDS, 16 rank indices at a time, and leave as rows of 128 columns.
-constexpr int kGradCols = 128;
+// A workgroup takes 128 columns (two blocks) of a token slice: waves 0 and 1 the
+// even 32-token steps, waves 2 and 3 the odd ones, the second of each pair the
+// second block (the pair reads the same rows of G, once from the L2).  Lane
+// (i16, g) loads, for rows m = 8 g .. 8 g + 7 of a step, the 4 codes of columns
+// 4 i16 .. 4 i16 + 3: MFMA t handles columns 4 i + t, and converting byte t of
+// the eight rows is the transpose.  The next step's loads are in flight under a
+// step's work; 64 columns a wave keep that within two waves' registers up to
+// rank 64.  The token halves are added in order through LDS, 16 rank indices at
+// a time, and leave as rows of 128 columns.
+constexpr int kGradCols = 128, kGradTokens = 64;   // a workgroup's, per pass
 
 template <int RT>
 struct GradStep {
-  uint32_t code[2][8];
-  uint8_t keep[2][8];      // dropout's stored bits, unused without
-  float4 scale[2][2];
+  uint32_t code[8];
+  uint8_t keep[8];         // dropout's stored bits, unused without
+  float4 scale[2];
   float4 g[RT][2];
 };
 
@@ -189,165 +191,152 @@ __device__ __forceinline__ uint32_t nibble_mask(uint32_t n) {   // 4 keep bits -
 }
 
 template <int RT, bool DROP>
-__global__ __launch_bounds__(256) void k_act8_grad(Act8GradJob J, int64_t M, int r) {
-  __shared__ float red[4][16][kGradCols + 4];
+__global__ __launch_bounds__(256, 2) void k_act8_grad(Act8GradJob J, int64_t M, int r) {
+  __shared__ float red[2][16][kGradCols + 4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = wv >> 1, side = wv & 1;
   const int i16 = lane & 15, g = lane >> 4;
   const int split = (int)(blockIdx.x % J.splits);
   const int64_t p0 = (int64_t)(blockIdx.x / J.splits) * kGradCols;
-  const int64_t mchunk = ceil_div(ceil_div(M, J.splits), 128) * 128;
+  const int64_t mchunk = ceil_div(ceil_div(M, J.splits), kGradTokens) * kGradTokens;
   const int64_t mbeg = (int64_t)split * mchunk;
   int64_t mend = mbeg + mchunk;
   mend = mend < M ? mend : M;
   // a last workgroup of one block reads it twice and drops the second
-  const int64_t blk[2] = {p0 / kBlock, p0 + kBlock < J.K ? p0 / kBlock + 1 : p0 / kBlock};
+  const int64_t blk = p0 / kBlock + (side && p0 + kBlock < J.K ? 1 : 0);
 
-  f32x4_t acc[2][4][RT];
+  f32x4_t acc[4][RT];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int t = 0; t < 4; ++t)
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int jt = 0; jt < RT; ++jt) acc[h][t][jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int jt = 0; jt < RT; ++jt) acc[t][jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const bool bits = DROP && J.drop.bits;
-  // a rank row past r feeds only rows of the partial that are never stored
-  const float* grow[RT];
-#pragma unroll
-  for (int jt = 0; jt < RT; ++jt) {
-    const int u = jt * 16 + i16;
-    grow[jt] = J.G + (int64_t)(u < r ? u : r - 1) * J.ldg + 8 * g;
-  }
+  const uint32_t K = (uint32_t)J.K;
   // rows past M are clamped copies that meet G = 0 and scale = 0; mb + 31 is
   // inside ldg, a multiple of 32
   auto load = [&](int64_t mb, GradStep<RT>& s) {
+    const int8_t* base = J.codes + mb * J.K + blk * kBlock;     // uniform
+    const int64_t first = mb * J.K + blk * kBlock;
+    const int left = (int)(M - 1 - mb < 31 ? M - 1 - mb : 31);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      int64_t m = mb + 8 * g + e;
-      m = m < M ? m : M - 1;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t at = m * J.K + blk[h] * kBlock + 4 * i16;
-        s.code[h][e] = *reinterpret_cast<const uint32_t*>(J.codes + at);
-        if constexpr (DROP)
-          if (bits) s.keep[h][e] = J.drop.bits[at >> 3];
-      }
+      const int row = 8 * g + e < left ? 8 * g + e : left;
+      const uint32_t at = (uint32_t)row * K + 4 * i16;
+      s.code[e] = *reinterpret_cast<const uint32_t*>(base + at);
+      if constexpr (DROP)
+        if (bits) s.keep[e] = J.drop.bits[(first + at) >> 3];
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4* p = reinterpret_cast<const float4*>(J.scale + blk[h] * J.ldg + mb + 8 * g);
-      s.scale[h][0] = p[0];
-      s.scale[h][1] = p[1];
-    }
+    const float4* p = reinterpret_cast<const float4*>(J.scale + blk * J.ldg + mb) + 2 * g;
+    s.scale[0] = p[0];
+    s.scale[1] = p[1];
+    // (a rank index past r feeds only rows of the partial that are never stored)
+    const float4* q = reinterpret_cast<const float4*>(J.G) + (mb >> 5) * (RT * 128);
 #pragma unroll
     for (int jt = 0; jt < RT; ++jt) {
-      const float4* p = reinterpret_cast<const float4*>(grow[jt] + mb);
-      s.g[jt][0] = p[0];
-      s.g[jt][1] = p[1];
+      s.g[jt][0] = q[(2 * jt) * 64 + lane];
+      s.g[jt][1] = q[(2 * jt + 1) * 64 + lane];
     }
   };
   auto work = [&](int64_t mb, GradStep<RT>& s) {
     if constexpr (DROP) {
+      const int64_t first = mb * J.K + blk * kBlock;
+      const int left = (int)(M - 1 - mb < 31 ? M - 1 - mb : 31);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        int64_t m = mb + 8 * g + e;
-        m = m < M ? m : M - 1;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint64_t at = (uint64_t)(m * J.K + blk[h] * kBlock + 4 * i16);
-          const uint32_t n = bits ? (uint32_t)s.keep[h][e] >> (at & 4)
-                                  : keep_nibble(dropout_words(at >> 2, J.drop), J.drop.thr);
-          s.code[h][e] &= nibble_mask(n);
-        }
+        const int row = 8 * g + e < left ? 8 * g + e : left;
+        const uint64_t at = (uint64_t)(first + (uint32_t)row * K + 4 * i16);
+        const uint32_t n = bits ? (uint32_t)s.keep[e] >> (at & 4)
+                                : keep_nibble(dropout_words(at >> 2, J.drop), J.drop.thr);
+        s.code[e] &= nibble_mask(n);
       }
     }
+    uint4 a[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 a[4];
+    for (int t = 0; t < 4; ++t) {
+      uint32_t f[8];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        uint32_t f[8];
+      for (int e = 0; e < 8; ++e)
+        f[e] = __builtin_bit_cast(uint32_t, (float)((int)(s.code[e] << (24 - 8 * t)) >> 24));
+      a[t] = make_uint4(high_halves(f[0], f[1]), high_halves(f[2], f[3]),
+                        high_halves(f[4], f[5]), high_halves(f[6], f[7]));
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          f[e] = __builtin_bit_cast(uint32_t,
-                                    (float)((int)(s.code[h][e] << (24 - 8 * t)) >> 24));
-        a[t] = make_uint4(high_halves(f[0], f[1]), high_halves(f[2], f[3]),
-                          high_halves(f[4], f[5]), high_halves(f[6], f[7]));
+    for (int jt = 0; jt < RT; ++jt) {
+      uint32_t p1[8], p2[8], p3[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = elem(s.g[jt], e) * elem(s.scale, e);
+        p1[e] = __builtin_bit_cast(uint32_t, v);
+        const float rest = v - __builtin_bit_cast(float, p1[e] & 0xFFFF0000u);
+        p2[e] = __builtin_bit_cast(uint32_t, rest);
+        p3[e] = __builtin_bit_cast(uint32_t,
+                                   rest - __builtin_bit_cast(float, p2[e] & 0xFFFF0000u));
       }
+      auto operand = [](const uint32_t (&p)[8]) {
+        return make_uint4(high_halves(p[0], p[1]), high_halves(p[2], p[3]),
+                          high_halves(p[4], p[5]), high_halves(p[6], p[7]));
+      };
+      const uint4 b1 = operand(p1), b2 = operand(p2), b3 = operand(p3);
 #pragma unroll
-      for (int jt = 0; jt < RT; ++jt) {
-        uint32_t p1[8], p2[8], p3[8];
+      for (int t = 0; t < 4; ++t) acc[t][jt] = mfma16x16x32(a[t], b3, acc[t][jt]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = elem(s.g[jt], e) * elem(s.scale[h], e);
-          p1[e] = __builtin_bit_cast(uint32_t, v);
-          const float rest = v - __builtin_bit_cast(float, p1[e] & 0xFFFF0000u);
-          p2[e] = __builtin_bit_cast(uint32_t, rest);
-          p3[e] = __builtin_bit_cast(uint32_t,
-                                     rest - __builtin_bit_cast(float, p2[e] & 0xFFFF0000u));
-        }
-        auto operand = [](const uint32_t (&p)[8]) {
-          return make_uint4(high_halves(p[0], p[1]), high_halves(p[2], p[3]),
-                            high_halves(p[4], p[5]), high_halves(p[6], p[7]));
-        };
-        const uint4 b1 = operand(p1), b2 = operand(p2), b3 = operand(p3);
+      for (int t = 0; t < 4; ++t) acc[t][jt] = mfma16x16x32(a[t], b2, acc[t][jt]);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          acc[h][t][jt] = mfma16x16x32(a[t], b3, acc[h][t][jt]);
-          acc[h][t][jt] = mfma16x16x32(a[t], b2, acc[h][t][jt]);
-          acc[h][t][jt] = mfma16x16x32(a[t], b1, acc[h][t][jt]);
-        }
-      }
+      for (int t = 0; t < 4; ++t) acc[t][jt] = mfma16x16x32(a[t], b1, acc[t][jt]);
+    }
+    // one rank tile's matrix instructions between the next one's arithmetic
+    __builtin_amdgcn_sched_group_barrier(0x2, 100, 0);
+#pragma unroll
+    for (int k = 0; k < 12 * RT; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
     }
   };
-  const int64_t first = mbeg + 32 * wv;
-  const int64_t cnt = first < mend ? (mend - first + 127) / 128 : 0;
+  const int64_t first = mbeg + 32 * half;
+  const int64_t cnt = first < mend ? (mend - first + kGradTokens - 1) / kGradTokens : 0;
+  auto step = [&](int64_t i) { return first + kGradTokens * i; };
   if constexpr (RT <= 4) {
     if (cnt > 0) {
       GradStep<RT> s0, s1;
       load(first, s0);
       int64_t i = 0;
       for (; i + 1 < cnt; i += 2) {
-        load(first + 128 * (i + 1), s1);
+        load(step(i + 1), s1);
         __builtin_amdgcn_sched_barrier(0);
-        work(first + 128 * i, s0);
+        work(step(i), s0);
         __builtin_amdgcn_sched_barrier(0);
-        if (i + 2 < cnt) load(first + 128 * (i + 2), s0);
+        load(step(i + 2 < cnt ? i + 2 : i), s0);   // (after the last step: unused)
         __builtin_amdgcn_sched_barrier(0);
-        work(first + 128 * (i + 1), s1);
+        work(step(i + 1), s1);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (i < cnt) work(first + 128 * i, s0);
+      if (i < cnt) work(step(i), s0);
     }
   } else {
     for (int64_t i = 0; i < cnt; ++i) {   // ranks above 64 fill the registers with sums
       GradStep<RT> s0;
-      load(first + 128 * i, s0);
-      work(first + 128 * i, s0);
+      load(step(i), s0);
+      work(step(i), s0);
     }
   }
-  // D[i = 4 g + v][j16] of MFMA (h, t): column 64 h + 16 g + 4 v + t
+  // D[i = 4 g + v][j16] of MFMA t: column 16 g + 4 v + t of the wave's block
   float* base = J.partial + (int64_t)split * r * J.K + p0;
 #pragma unroll
   for (int jt = 0; jt < RT; ++jt) {
     if (jt > 0) __syncthreads();
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        *reinterpret_cast<float4*>(&red[wv][i16][64 * h + 16 * g + 4 * v]) =
-            make_float4(acc[h][0][jt][v], acc[h][1][jt][v], acc[h][2][jt][v], acc[h][3][jt][v]);
+    for (int v = 0; v < 4; ++v)
+      *reinterpret_cast<float4*>(&red[half][i16][64 * side + 16 * g + 4 * v]) =
+          make_float4(acc[0][jt][v], acc[1][jt][v], acc[2][jt][v], acc[3][jt][v]);
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int j = (tid >> 5) + 8 * q, p = 4 * (tid & 31);
       float4 s = *reinterpret_cast<const float4*>(&red[0][j][p]);
-#pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const float4 o = *reinterpret_cast<const float4*>(&red[w][j][p]);
-        s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
-      }
+      const float4 o = *reinterpret_cast<const float4*>(&red[1][j][p]);
+      s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
       if constexpr (DROP) {
         s.x *= J.drop.inv; s.y *= J.drop.inv; s.z *= J.drop.inv; s.w *= J.drop.inv;
       }
@@ -383,12 +372,24 @@ hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64
                        rows, rows32, kb, tk, out);
 }
 
-// About two workgroups for each CU, at least one 32-token step for each wave.
+// The split of the tokens with the least rounds x passes: the CUs hold 512
+// workgroups at once, so 3 slices of 172 column groups (516) take two rounds of
+// the length 5 slices (860) fill far better.  A slice more costs its partial's
+// way to memory and back, about K / 18000 passes.  4096 x 22016 at rank 64: 78
+// us with 2 slices (one round, a third of it empty), 81 with 3, 51 with 5.
 int act8_grad_splits(int64_t M, int64_t K) {
-  int64_t splits = ceil_div(512, ceil_div(K, kGradCols));
-  const int64_t maxs = ceil_div(M, 128);
-  if (splits > maxs) splits = maxs;
-  return (int)(splits < 1 ? 1 : splits);
+  const int64_t groups = ceil_div(K, kGradCols), passes = ceil_div(M, kGradTokens);
+  int64_t best = 1;
+  double least = 1e300;
+  for (int64_t s = 1; s <= 16 && s <= ceil_div(passes, 2); ++s) {
+    const double cost = (double)ceil_div(groups * s, 512) * (double)ceil_div(passes, s) +
+                        (double)s * (double)K / 18000.0;
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return (int)best;
 }
 
 hipError_t launch_act8_grad(const Act8GradJob& job, int64_t M, int r, hipStream_t s) {

@@ -108,8 +108,8 @@ LinearWs linear_layout(int64_t M, int64_t N, int64_t K, int r) {
   w.gemv_part = off; off = align_up(off + (size_t)w.gemv_splits * M * N * sizeof(float));
   w.bt = off;        off = align_up(off + (size_t)r * w.np * 2);
   w.gs = off;        off = align_up(off + (size_t)M * w.r32 * 2);
-  w.gt = off;        off = align_up(off + (size_t)r * w.mp * 2);
-  w.xat = off;       off = align_up(off + (size_t)r * w.mp * 2);
+  w.gt = off;        off = align_up(off + (size_t)skinny_rpad(r) * w.mp * 2);
+  w.xat = off;       off = align_up(off + (size_t)skinny_rpad(r) * w.mp * 2);
   w.part_a = off;    off = align_up(off + (size_t)w.sa * r * K * sizeof(float));
   w.part_b = off;    off = align_up(off + (size_t)w.sb * N * r * sizeof(float));
   const size_t gp = std::max((size_t)(w.sf > 1 ? w.sf : 0) * M * N,
@@ -125,9 +125,9 @@ LinearWs linear_layout(int64_t M, int64_t N, int64_t K, int r) {
 }
 
 // What the backward from an 8-bit checkpoint needs behind that layout: the
-// float32 G^T [r, mp], then dA's partials.
+// float32 G^T [rpad, mp], then dA's partials.
 size_t act8_g_bytes(const LinearWs& w, int r) {
-  return align_up((size_t)r * w.mp * sizeof(float));
+  return align_up((size_t)skinny_rpad(r) * w.mp * sizeof(float));
 }
 size_t act8_bytes(const LinearWs& w, int64_t M, int64_t K, int r) {
   return act8_g_bytes(w, r) +
@@ -615,12 +615,12 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
   uint16_t* xat = at<uint16_t>(ws, L.xat);
   hipError_t e;
 #define QL_TRY(call) do { e = (call); if (e != hipSuccess) return QLORA_ERR_HIP; } while (0)
-  // one launch: B^T [r, N128] for G = dY.B; XA^T [r, M32] for dB from the
-  // forward's copy; the block constants for the dX GEMM
+  // one launch: B^T [r, N128] for G = dY.B; XA^T for dB from the forward's
+  // copy; the block constants for the dX GEMM
   TransposeJob tj[2];
   int nt = 0;
   tj[nt++] = TransposeJob{B, N, r, bt, L.np};
-  if (XA_in) tj[nt++] = TransposeJob{XA_in, M, r, xat, L.mp};
+  if (XA_in) tj[nt++] = TransposeJob{XA_in, M, r, xat, L.mp, skinny_rpad(r) / 16};
   const ReconJob rc{W->absmax_q, W->absmax_scale, W->absmax_mean, N, K / kBlock, ahat_t,
                     f32_consts(W)};
   QL_TRY(launch_prep(tj, nt, dX ? &rc : nullptr, s));
@@ -650,8 +650,8 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
   }
   // dA = s . G^T X  (reduce over tokens into [r, K]);  dB = s . dY^T XA  ([N, r])
   GradJob gj[2] = {
-      GradJob{X, K, gt, L.mp, L.sa, at<float>(ws, L.part_a), scale, 1, dA},
-      GradJob{dY, N, xat, L.mp, L.sb, at<float>(ws, L.part_b), scale, 0, dB}};
+      GradJob{X, K, gt, L.sa, at<float>(ws, L.part_a), scale, 1, dA},
+      GradJob{dY, N, xat, L.sb, at<float>(ws, L.part_b), scale, 0, dB}};
   gj[0].drop = dp;   // dA reads D(X)
   if (grp) {
     gj[1].groups = grp->groups;

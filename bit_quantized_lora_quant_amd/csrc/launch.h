@@ -73,12 +73,31 @@ struct ReconJob {
   float* out;
   const float* f32;
 };
-// bf16 transpose [rows, cols] -> [cols, ldo], zero for i in [rows, ldo)
+// The adapter gradients read their rank-side operand U [r][tokens] as MFMA
+// fragments: 16 rank indices j x 32 tokens m, lane (j % 16, (m / 8) % 4) with 8
+// consecutive tokens.  Stored in that order, 16 bytes a lane and the lanes in a
+// row, a fragment is one contiguous load; as rows of tokens each lane's 16 bytes
+// lie in a line of their own, and it is the cache's accesses that bound the
+// kernel.  rt: rank tiles, skinny_rpad(r) / 16.
+__host__ __device__ __forceinline__ int64_t frag_at(int64_t m, int j, int rt) {
+  return ((((m >> 5) * rt + (j >> 4)) * 64 + ((m >> 3) & 3) * 16 + (j & 15)) << 3) + (m & 7);
+}
+// float32: two loads of 16 bytes a lane, tokens 0-3 and 4-7 of its 8
+__host__ __device__ __forceinline__ int64_t frag32_at(int64_t m, int j, int rt) {
+  return (((((m >> 5) * rt + (j >> 4)) * 2 + ((m >> 2) & 1)) * 64 + ((m >> 3) & 3) * 16 +
+           (j & 15))
+          << 2) +
+         (m & 3);
+}
+
+// bf16 transpose [rows, cols] -> [cols, ldo], zero for i in [rows, ldo); with
+// rt > 0 in fragment order (frag_at(i, col, rt))
 struct TransposeJob {
   const uint16_t* in;
   int64_t rows, cols;
   uint16_t* out;
   int64_t ldo;
+  int rt = 0;
 };
 // Skinny product P = T . U^T over the inner dim kin: T [M, kin] (row stride
 // ldt), U [r, kin] (row stride ldu).  The inner dim is cut into `ks` slices
@@ -86,7 +105,7 @@ struct TransposeJob {
 // them in slice order and writes (each output nullable)
 //   out_s  bf16(scale * P) [M, r32]   (zero columns r..r32)
 //   out    bf16(P)         [M, r]
-//   out_t  bf16(P)^T       [r, ldo_t] (zero for m in [M, ldo_t))
+//   out_t  bf16(P)^T in fragment order, m < ldo_t (zero from M on)
 struct SkinnyJob {
   const uint16_t* T;
   int64_t kin, ldt;
@@ -105,8 +124,7 @@ struct SkinnyJob {
   // dropout of T (T = X only): dropped elements read as zero, sums times
   // drop.inv
   DropoutParams drop{};
-  // float32 P^T [r, ldo_t] (zero for m in [M, ldo_t)), beside or in place of
-  // out_t
+  // float32 P^T likewise (frag32_at), beside or in place of out_t
   float* out_tf = nullptr;
 };
 // Padded rank of the partial rows (16, 32, 64 or 128).
@@ -123,14 +141,13 @@ hipError_t launch_skinny(const SkinnyJob* jobs, int njobs, int64_t M, int r, int
 hipError_t launch_prep(const TransposeJob* t, int nt, const ReconJob* recon, hipStream_t s);
 
 // Adapter gradient: out = scale * sum_m T[m][p] U[j][m], T [M, P] (row stride
-// P), U [r, ldu] (zero for m in [M, ldu)).  Token range cut into `splits`
+// P), U in fragment order (zero from M to the next multiple of 32).  Token range cut into `splits`
 // slices with float32 partials [splits][P][r]; out is [r][P] when
 // `transposed`, else [P][r].
 struct GradJob {
   const uint16_t* T;
   int64_t P;
   const uint16_t* U;
-  int64_t ldu;
   int splits;
   float* partial;
   float scale;
@@ -160,7 +177,7 @@ hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64
                                   int64_t cols, int bf16, void* out, hipStream_t s);
 // Partials of the adapter gradient from a checkpoint: partial[split][j][k] =
 // sum over the split's tokens of G[j][m] D(scale[k / 64][m] codes[m][k]); G
-// float32 [r, ldg] (zero for m in [M, ldg)), ldg = M up to 32 is also the
+// float32 in fragment order (zero for m in [M, ldg)), ldg = M up to 32 the
 // scales' row length.  The reduction is launch_lora_grad_reduce's.
 struct Act8GradJob {
   const int8_t* codes;

@@ -237,9 +237,9 @@ __device__ __forceinline__ void skinny2_slice(const SkinnyJob& J, int64_t M, int
         if (J.out && j < r) J.out[m * r + j] = to_bf16(sum);
       }
       if (J.out_t && j < r && m < J.ldo_t)
-        J.out_t[(int64_t)j * J.ldo_t + m] = m < M ? to_bf16(sum) : 0;
+        J.out_t[frag_at(m, j, RT)] = m < M ? to_bf16(sum) : 0;
       if (J.out_tf && j < r && m < J.ldo_t)
-        J.out_tf[(int64_t)j * J.ldo_t + m] = m < M ? sum : 0.f;
+        J.out_tf[frag32_at(m, j, RT)] = m < M ? sum : 0.f;
     }
 }
 
@@ -283,8 +283,10 @@ __device__ __forceinline__ void skinny_finish_elem(const SkinnyJob& J, int64_t M
     if (J.out_s) J.out_s[m * r32 + j] = to_bf16(j < r ? J.scale * sum : 0.f);
     if (J.out && j < r) J.out[m * r + j] = to_bf16(sum);
   }
-  if (J.out_t && j < r && m < J.ldo_t) J.out_t[(int64_t)j * J.ldo_t + m] = m < M ? to_bf16(sum) : 0;
-  if (J.out_tf && j < r && m < J.ldo_t) J.out_tf[(int64_t)j * J.ldo_t + m] = m < M ? sum : 0.f;
+  if (J.out_t && j < r && m < J.ldo_t)
+    J.out_t[frag_at(m, j, rpad / 16)] = m < M ? to_bf16(sum) : 0;
+  if (J.out_tf && j < r && m < J.ldo_t)
+    J.out_tf[frag32_at(m, j, rpad / 16)] = m < M ? sum : 0.f;
 }
 
 // (jobs run as a single slice wrote their outputs directly: no finish)
@@ -339,9 +341,12 @@ __device__ __forceinline__ void transpose_tile(const TransposeJob& J, int64_t b,
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
     const int idx = (int)threadIdx.x + 256 * u;
-    const int jl = idx >> (12 - sh), il = idx & (ti - 1);
+    // consecutive threads along i, or in a fragment's order: 8 of i, then j
+    const int jl = J.rt ? (idx >> 3) & (tj - 1) : idx >> (12 - sh);
+    const int il = J.rt ? ((idx >> (3 + sh)) << 3) + (idx & 7) : idx & (ti - 1);
     const int64_t i = i0 + il, j = j0 + jl;
-    if (j < J.cols && i < J.ldo) J.out[j * J.ldo + i] = tile[jl * ld + il];
+    if (j < J.cols && i < J.ldo)
+      J.out[J.rt ? frag_at(i, (int)j, J.rt) : j * J.ldo + i] = tile[jl * ld + il];
   }
 }
 
@@ -394,21 +399,13 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
     for (int jt = 0; jt < RT; ++jt) acc[t][jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const bool fast = pv && p0 + 128 <= J.P;   // workgroup-uniform
-  // this lane's rows of U, clamped: a row past r feeds only output column
-  // j >= r, which is never stored (no branch or select around the loads, which
-  // would cost the two-steps-in-flight schedule)
-  const uint16_t* urow[RT];
-#pragma unroll
-  for (int jt = 0; jt < RT; ++jt) {
-    const int u = jt * 16 + i16;
-    urow[jt] = J.U + (int64_t)(u < r ? u : r - 1) * J.ldu;
-  }
-  // step mb: rows mb + 8g + e of T (clamped below M; U is zero there) and
-  // columns mb + 8g .. + 7 of U (within ldu, a multiple of 32)
+  // step mb: rows mb + 8g + e of T (clamped below M; U is zero there) and the
+  // fragments of U.  A rank index past r feeds only output column j >= r, which
+  // is never stored, so what its slots hold does not matter.
   auto load_u = [&](int64_t mb, uint4 (&bu)[RT]) {
 #pragma unroll
     for (int jt = 0; jt < RT; ++jt)
-      bu[jt] = *reinterpret_cast<const uint4*>(urow[jt] + mb + 8 * g);
+      bu[jt] = *reinterpret_cast<const uint4*>(J.U + ((mb >> 5) * RT + jt) * 512 + lane * 8);
   };
   auto load_step = [&](int64_t mb, uint4 (&rows)[8], uint4 (&bu)[RT]) {   // 128 columns in range
 #pragma unroll
@@ -468,24 +465,22 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
   // through buffer views (fixed byte offsets per lane, the step's base as the
   // uniform offset), two steps in flight: the next step's loads are issued
   // before this step's MFMAs.
-  const int64_t tbytes = M * J.P * 2, ubytes = (int64_t)r * J.ldu * 2;
+  const int64_t tbytes = M * J.P * 2, ubytes = ceil_div(M, 32) * RT * 1024;
   const bool bufs = fast && RT <= 4 && tbytes <= kBufferMax && ubytes <= kBufferMax;
   const int64_t cnt_fast = bufs && first + 32 <= mend ? (mend - first - 32) / 128 + 1 : 0;
   if (cnt_fast > 0) {
     const __amdgpu_buffer_rsrc_t tview = buffer_view(J.T, tbytes);
     const __amdgpu_buffer_rsrc_t uview = buffer_view(J.U, ubytes);
-    uint32_t roff[8], uoff[RT];
+    uint32_t roff[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) roff[e] = (uint32_t)((8 * g + e) * J.P + pc) * 2;
-#pragma unroll
-    for (int jt = 0; jt < RT; ++jt) uoff[jt] = (uint32_t)((urow[jt] - J.U) + 8 * g) * 2;
     auto load_fast = [&](int64_t i, uint4 (&rows)[8], uint4 (&bu)[RT]) {
       const int64_t mb = first + 128 * i;
-      const uint32_t tb = (uint32_t)(mb * J.P) * 2, ub = (uint32_t)mb * 2;
+      const uint32_t tb = (uint32_t)(mb * J.P) * 2, ub = (uint32_t)(mb >> 5) * (RT * 1024);
 #pragma unroll
       for (int e = 0; e < 8; ++e) rows[e] = buffer_load16(tview, roff[e], tb);
 #pragma unroll
-      for (int jt = 0; jt < RT; ++jt) bu[jt] = buffer_load16(uview, uoff[jt], ub);
+      for (int jt = 0; jt < RT; ++jt) bu[jt] = buffer_load16(uview, lane * 16 + jt * 1024, ub);
     };
     uint4 r0[8], u0[RT], r1[8], u1[RT];
     load_fast(0, r0, u0);

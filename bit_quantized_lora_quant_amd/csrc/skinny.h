@@ -221,9 +221,9 @@ __device__ __forceinline__ void skinny_slice(const SkinnyJob& J, int64_t M, int 
         if (J.out && j < r) J.out[m * r + j] = to_bf16(sum);
       }
       if (J.out_t && j < r && m < J.ldo_t)
-        J.out_t[(int64_t)j * J.ldo_t + m] = m < M ? to_bf16(sum) : 0;
+        J.out_t[frag_at(m, j, RT)] = m < M ? to_bf16(sum) : 0;
       if (J.out_tf && j < r && m < J.ldo_t)
-        J.out_tf[(int64_t)j * J.ldo_t + m] = m < M ? sum : 0.f;
+        J.out_tf[frag32_at(m, j, RT)] = m < M ? sum : 0.f;
     }
   if (J.ks == 1 && !J.part_only && J.out_s) {   // padding columns of out_s past the tiles
     for (int j = RT * 16 + j16; j < r32; j += 16)
