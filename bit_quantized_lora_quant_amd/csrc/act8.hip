@@ -8,7 +8,7 @@
 // of a 15-bit by an 8-bit integer is never nearer than 2^-17 of itself to a
 // half-integer unless it is one, so the code is the rounding (half to even)
 // of the exact quotient whichever correctly rounded division forms it.
-#include "skinny.h"
+#include "grads.h"
 
 namespace qnf4 {
 namespace {
@@ -191,14 +191,15 @@ __device__ __forceinline__ uint32_t nibble_mask(uint32_t n) {   // 4 keep bits -
 }
 
 template <int RT, bool DROP>
-__global__ __launch_bounds__(256, 2) void k_act8_grad(Act8GradJob J, int64_t M, int r) {
+__device__ __forceinline__ void act8_grad_slice(const Act8GradJob& J, int64_t M, int r,
+                                                int64_t block) {
   __shared__ float red[2][16][kGradCols + 4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = wv >> 1, side = wv & 1;
   const int i16 = lane & 15, g = lane >> 4;
-  const int split = (int)(blockIdx.x % J.splits);
-  const int64_t p0 = (int64_t)(blockIdx.x / J.splits) * kGradCols;
+  const int split = (int)(block % J.splits);
+  const int64_t p0 = (block / J.splits) * kGradCols;
   const int64_t mchunk = ceil_div(ceil_div(M, J.splits), kGradTokens) * kGradTokens;
   const int64_t mbeg = (int64_t)split * mchunk;
   int64_t mend = mbeg + mchunk;
@@ -346,11 +347,30 @@ __global__ __launch_bounds__(256, 2) void k_act8_grad(Act8GradJob J, int64_t M, 
   }
 }
 
+// dA from the codes and dB from dY in one launch: neither needs the other, and
+// one's last workgroups run beside the other's first.  Above rank 32 dB's sums
+// take registers that would leave dA one wave a SIMD instead of two, and the
+// two are launches of their own.
+template <int RT, bool DROP>
+__global__ __launch_bounds__(256, 2) void k_act8_grads(Act8GradJob a, GradJob b, int64_t M,
+                                                      int r) {
+  const int64_t na = ceil_div(a.K, kGradCols) * a.splits;
+  if ((int64_t)blockIdx.x < na) {
+    act8_grad_slice<RT, DROP>(a, M, r, blockIdx.x);
+    return;
+  }
+  if constexpr (RT <= 2) grad_slice<RT, false>(b, M, r, blockIdx.x - na);
+}
+
 template <int RT>
-hipError_t act8_grad_rt(const Act8GradJob& job, int64_t M, int r, hipStream_t s) {
-  const int64_t blocks = ceil_div(job.K, kGradCols) * job.splits;
-  return launch_kernel(job.drop.thr != 0 ? k_act8_grad<RT, true> : k_act8_grad<RT, false>,
-                       dim3((unsigned)blocks), dim3(256), s, job, M, r);
+hipError_t act8_grads_rt(const Act8GradJob& a, const GradJob& b, int64_t M, int r,
+                         hipStream_t s) {
+  const int64_t blocks =
+      ceil_div(a.K, kGradCols) * a.splits + (RT <= 2 ? grad_blocks(b) : 0);
+  const hipError_t e =
+      launch_kernel(a.drop.thr != 0 ? k_act8_grads<RT, true> : k_act8_grads<RT, false>,
+                    dim3((unsigned)blocks), dim3(256), s, a, b, M, r);
+  return RT <= 2 || e != hipSuccess ? e : launch_lora_grad_partials(&b, 1, M, r, s);
 }
 
 }  // namespace
@@ -392,12 +412,13 @@ int act8_grad_splits(int64_t M, int64_t K) {
   return (int)best;
 }
 
-hipError_t launch_act8_grad(const Act8GradJob& job, int64_t M, int r, hipStream_t s) {
+hipError_t launch_act8_grads(const Act8GradJob& a, const GradJob& b, int64_t M, int r,
+                             hipStream_t s) {
   switch (skinny_rpad(r)) {
-    case 16: return act8_grad_rt<1>(job, M, r, s);
-    case 32: return act8_grad_rt<2>(job, M, r, s);
-    case 64: return act8_grad_rt<4>(job, M, r, s);
-    default: return act8_grad_rt<8>(job, M, r, s);
+    case 16: return act8_grads_rt<1>(a, b, M, r, s);
+    case 32: return act8_grads_rt<2>(a, b, M, r, s);
+    case 64: return act8_grads_rt<4>(a, b, M, r, s);
+    default: return act8_grads_rt<8>(a, b, M, r, s);
   }
 }
 

@@ -663,8 +663,7 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
     gj[0].partial = at<float>(ws, L.total + act8_g_bytes(L, r));
     Act8GradJob aj{x8->codes, x8->scale, K, gtf, L.mp, gj[0].splits, gj[0].partial};
     aj.drop = dp;
-    QL_TRY(launch_act8_grad(aj, M, r, s));
-    QL_TRY(launch_lora_grad_partials(gj + 1, 1, M, r, s));
+    QL_TRY(launch_act8_grads(aj, gj[1], M, r, s));
     QL_TRY(launch_lora_grad_reduce(gj, 2, r, s));
     return QLORA_OK;
   }

@@ -190,7 +190,9 @@ struct Act8GradJob {
   DropoutParams drop{};
 };
 int act8_grad_splits(int64_t M, int64_t K);
-hipError_t launch_act8_grad(const Act8GradJob& job, int64_t M, int r, hipStream_t s);
+// a's partials and those of b (dB).
+hipError_t launch_act8_grads(const Act8GradJob& a, const GradJob& b, int64_t M, int r,
+                             hipStream_t s);
 
 // The GEMMs split their inner loop into `splits` slices (one workgroup per
 // tile and slice) when the output tiles alone cannot fill the chip; with
