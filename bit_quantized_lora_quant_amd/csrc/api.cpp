@@ -125,13 +125,16 @@ LinearWs linear_layout(int64_t M, int64_t N, int64_t K, int r) {
 }
 
 // What the backward from an 8-bit checkpoint needs behind that layout: the
-// float32 G^T [rpad, mp], then dA's partials.
+// float32 G^T [rpad, mp], then dA's partials, then (rank <= 16) G's.
 size_t act8_g_bytes(const LinearWs& w, int r) {
   return align_up((size_t)skinny_rpad(r) * w.mp * sizeof(float));
 }
-size_t act8_bytes(const LinearWs& w, int64_t M, int64_t K, int r) {
-  return act8_g_bytes(w, r) +
-         align_up((size_t)act8_grad_splits(M, K) * r * (size_t)K * sizeof(float));
+size_t act8_a_bytes(int64_t M, int64_t K, int r) {
+  return align_up((size_t)act8_grad_splits(M, K) * r * (size_t)K * sizeof(float));
+}
+size_t act8_bytes(const LinearWs& w, int64_t M, int64_t N, int64_t K, int r) {
+  return act8_g_bytes(w, r) + act8_a_bytes(M, K, r) +
+         (r <= 16 ? align_up(skinny_staged16_floats(M, N) * sizeof(float)) : 0);
 }
 
 template <typename T>
@@ -603,7 +606,7 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
   if (dX && !aligned(dX, 16)) return QLORA_ERR_INVALID_ARG;
   const int64_t N = W->rows, K = W->cols;
   const LinearWs L = linear_layout(M, N, K, r);
-  const size_t need = L.total + (x8 ? act8_bytes(L, M, K, r) : 0);
+  const size_t need = L.total + (x8 ? act8_bytes(L, M, N, K, r) : 0);
   if (!ws || ws_bytes < need || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const float scale = alpha / (float)r;
@@ -630,7 +633,13 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
   int nj = 0;
   sj[nj++] = SkinnyJob{dY, N, N, bt, L.np, 0, 0, at<float>(ws, L.sk_n), scale,
                        x8 && !dX ? nullptr : gs, nullptr, x8 ? nullptr : gt, L.mp};
-  if (x8) sj[0].out_tf = gtf;
+  if (x8) {
+    sj[0].out_tf = gtf;
+    if (r <= 16 && !dX) {   // (with dX, G is summed as the plain backward sums it)
+      sj[0].stage16 = true;
+      sj[0].part = at<float>(ws, L.total + act8_g_bytes(L, r) + act8_a_bytes(M, K, r));
+    }
+  }
   if (!XA_in) {
     sj[nj++] = SkinnyJob{X, K, K, A, K, 0, 0, at<float>(ws, L.sk_k), 1.0f, nullptr, nullptr, xat,
                          L.mp};
@@ -750,7 +759,7 @@ qlora_status qlora_act8_dequantize(const qlora_act8* a, qlora_dtype out_dtype, v
 
 size_t qlora_linear_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r) {
   const size_t plain = qlora_linear_workspace_bytes(M, N, K, r);
-  return plain == 0 ? 0 : plain + act8_bytes(linear_layout(M, N, K, r), M, K, r);
+  return plain == 0 ? 0 : plain + act8_bytes(linear_layout(M, N, K, r), M, N, K, r);
 }
 
 // The checkpoint's own checks for a linear whose weight has `cols` columns.

@@ -339,15 +339,23 @@ __device__ __forceinline__ void transpose_tile(const TransposeJob& J, int64_t b,
     tile[(idx & (tj - 1)) * ld + il] = i0 + il < J.rows ? v[u] : (uint16_t)0;
   }
   __syncthreads();
+  if (J.rt) {   // a lane's 8 of i are 16 bytes of a fragment
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int c = (int)threadIdx.x + 256 * u, jl = c & (tj - 1), il = (c >> sh) * 8;
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(tile + jl * ld + il);
+      if (j0 + jl < J.cols && i0 + il < J.ldo)
+        *reinterpret_cast<uint4*>(J.out + frag_at(i0 + il, (int)(j0 + jl), J.rt)) =
+            make_uint4(p[0], p[1], p[2], p[3]);
+    }
+    return;
+  }
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
     const int idx = (int)threadIdx.x + 256 * u;
-    // consecutive threads along i, or in a fragment's order: 8 of i, then j
-    const int jl = J.rt ? (idx >> 3) & (tj - 1) : idx >> (12 - sh);
-    const int il = J.rt ? ((idx >> (3 + sh)) << 3) + (idx & 7) : idx & (ti - 1);
+    const int jl = idx >> (12 - sh), il = idx & (ti - 1);
     const int64_t i = i0 + il, j = j0 + jl;
-    if (j < J.cols && i < J.ldo)
-      J.out[J.rt ? frag_at(i, (int)j, J.rt) : j * J.ldo + i] = tile[jl * ld + il];
+    if (j < J.cols && i < J.ldo) J.out[j * J.ldo + i] = tile[jl * ld + il];
   }
 }
 
@@ -486,10 +494,11 @@ hipError_t grads_rt(const GradJob* jobs, int nj, int64_t M, int r, hipStream_t s
 
 int skinny_rpad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
-// The LDS-staged form: ranks 17..64, whole 64-wide steps, 16-byte rows.
+// The LDS-staged form: ranks 17..64 (below where asked), whole 64-wide steps,
+// 16-byte rows.
 static bool skinny_staged(const SkinnyJob& j, int r) {
   const int rp = skinny_rpad(r);
-  return (rp == 32 || rp == 64) && j.kin % kSk2Step == 0 && j.ldt % 8 == 0 &&
+  return (rp == 32 || rp == 64 || (rp == 16 && j.stage16)) && j.kin % kSk2Step == 0 && j.ldt % 8 == 0 &&
          j.ldu % 8 == 0 && (reinterpret_cast<uintptr_t>(j.T) & 15) == 0 &&
          (reinterpret_cast<uintptr_t>(j.U) & 15) == 0;
 }
@@ -532,6 +541,12 @@ size_t skinny_part_floats(int64_t M, int64_t kin, int r) {
   return (size_t)skinny_slices(M, kin, r) * (size_t)M * (size_t)skinny_rpad(r);
 }
 
+size_t skinny_staged16_floats(int64_t M, int64_t kin) {
+  const int s1 = skinny1_slices(M, kin);
+  const int s2 = kin % kSk2Step == 0 ? skinny2_slices(M, kin) : 1;
+  return (size_t)(s1 > s2 ? s1 : s2) * (size_t)M * 16;
+}
+
 void skinny_plan(SkinnyJob* j, int64_t M, int r) {
   j->staged = skinny_staged(*j, r) ? 1 : 0;
   const int ks = j->staged ? skinny2_slices(M, j->kin) : skinny1_slices(M, j->kin);
@@ -550,8 +565,9 @@ hipError_t launch_skinny(const SkinnyJob* jobs, int nj, int64_t M, int r, int r3
   for (int i = 0; i < nj; ++i) (jobs[i].staged ? st[ns++] : pl[np++]) = jobs[i];
   hipError_t e = hipSuccess;
   if (ns > 0) {
-    e = rpad == 32 ? skinny2_rt<2>(st, ns, M, r, r32, recon, s)
-                   : skinny2_rt<4>(st, ns, M, r, r32, recon, s);
+    e = rpad == 16   ? skinny2_rt<1>(st, ns, M, r, r32, recon, s)
+        : rpad == 32 ? skinny2_rt<2>(st, ns, M, r, r32, recon, s)
+                     : skinny2_rt<4>(st, ns, M, r, r32, recon, s);
     if (e != hipSuccess) return e;
     recon = nullptr;
   }
