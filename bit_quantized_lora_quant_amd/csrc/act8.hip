@@ -163,8 +163,8 @@ __global__ __launch_bounds__(256) void k_act8_dequantize(const int8_t* __restric
 // (i16, g) loads, for rows m = 8 g .. 8 g + 7 of a step, the 4 codes of columns
 // 4 i16 .. 4 i16 + 3: MFMA t handles columns 4 i + t, and converting byte t of
 // the eight rows is the transpose.  The next step's loads are in flight under a
-// step's work; 64 columns a wave keep that within two waves' registers up to
-// rank 64.  The token halves are added in order through LDS, 16 rank indices at
+// step's work; 64 columns a wave keep that within two waves' registers at four
+// rank tiles, and ranks above 64 are two slices' work.  The token halves are added in order through LDS, 16 rank indices at
 // a time, and leave as rows of 128 columns.
 constexpr int kGradCols = 128, kGradTokens = 64;   // a workgroup's, per pass
 
@@ -192,7 +192,7 @@ __device__ __forceinline__ uint32_t nibble_mask(uint32_t n) {   // 4 keep bits -
 
 template <int RT, bool DROP>
 __device__ __forceinline__ void act8_grad_slice(const Act8GradJob& J, int64_t M, int r,
-                                                int64_t block) {
+                                                int64_t block, int jt0, int rt) {
   __shared__ float red[2][16][kGradCols + 4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -233,7 +233,7 @@ __device__ __forceinline__ void act8_grad_slice(const Act8GradJob& J, int64_t M,
     s.scale[0] = p[0];
     s.scale[1] = p[1];
     // (a rank index past r feeds only rows of the partial that are never stored)
-    const float4* q = reinterpret_cast<const float4*>(J.G) + (mb >> 5) * (RT * 128);
+    const float4* q = reinterpret_cast<const float4*>(J.G) + ((mb >> 5) * rt + jt0) * 128;
 #pragma unroll
     for (int jt = 0; jt < RT; ++jt) {
       s.g[jt][0] = q[(2 * jt) * 64 + lane];
@@ -298,29 +298,21 @@ __device__ __forceinline__ void act8_grad_slice(const Act8GradJob& J, int64_t M,
   const int64_t first = mbeg + 32 * half;
   const int64_t cnt = first < mend ? (mend - first + kGradTokens - 1) / kGradTokens : 0;
   auto step = [&](int64_t i) { return first + kGradTokens * i; };
-  if constexpr (RT <= 4) {
-    if (cnt > 0) {
-      GradStep<RT> s0, s1;
-      load(first, s0);
-      int64_t i = 0;
-      for (; i + 1 < cnt; i += 2) {
-        load(step(i + 1), s1);
-        __builtin_amdgcn_sched_barrier(0);
-        work(step(i), s0);
-        __builtin_amdgcn_sched_barrier(0);
-        load(step(i + 2 < cnt ? i + 2 : i), s0);   // (after the last step: unused)
-        __builtin_amdgcn_sched_barrier(0);
-        work(step(i + 1), s1);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (i < cnt) work(step(i), s0);
-    }
-  } else {
-    for (int64_t i = 0; i < cnt; ++i) {   // ranks above 64 fill the registers with sums
-      GradStep<RT> s0;
-      load(step(i), s0);
+  if (cnt > 0) {
+    GradStep<RT> s0, s1;
+    load(first, s0);
+    int64_t i = 0;
+    for (; i + 1 < cnt; i += 2) {
+      load(step(i + 1), s1);
+      __builtin_amdgcn_sched_barrier(0);
       work(step(i), s0);
+      __builtin_amdgcn_sched_barrier(0);
+      load(step(i + 2 < cnt ? i + 2 : i), s0);   // (after the last step: unused)
+      __builtin_amdgcn_sched_barrier(0);
+      work(step(i + 1), s1);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if (i < cnt) work(step(i), s0);
   }
   // D[i = 4 g + v][j16] of MFMA t: column 16 g + 4 v + t of the wave's block
   float* base = J.partial + (int64_t)split * r * J.K + p0;
@@ -341,8 +333,9 @@ __device__ __forceinline__ void act8_grad_slice(const Act8GradJob& J, int64_t M,
       if constexpr (DROP) {
         s.x *= J.drop.inv; s.y *= J.drop.inv; s.z *= J.drop.inv; s.w *= J.drop.inv;
       }
-      if (jt * 16 + j < r && p0 + p < J.K)
-        *reinterpret_cast<float4*>(base + (int64_t)(jt * 16 + j) * J.K + p) = s;
+      const int rank = (jt0 + jt) * 16 + j;
+      if (rank < r && p0 + p < J.K)
+        *reinterpret_cast<float4*>(base + (int64_t)rank * J.K + p) = s;
     }
   }
 }
@@ -355,8 +348,14 @@ template <int RT, bool DROP>
 __global__ __launch_bounds__(256, 2) void k_act8_grads(Act8GradJob a, GradJob b, int64_t M,
                                                       int r) {
   const int64_t na = ceil_div(a.K, kGradCols) * a.splits;
+  if constexpr (RT == 4) {
+    const int parts = grad_parts(r);
+    const int64_t block = blockIdx.x / parts;
+    act8_grad_slice<RT, DROP>(a, M, r, block, (int)(blockIdx.x - block * parts) * RT, RT * parts);
+    return;
+  }
   if ((int64_t)blockIdx.x < na) {
-    act8_grad_slice<RT, DROP>(a, M, r, blockIdx.x);
+    act8_grad_slice<RT, DROP>(a, M, r, blockIdx.x, 0, RT);
     return;
   }
   if constexpr (RT <= 2) grad_slice<RT, false>(b, M, r, blockIdx.x - na);
@@ -365,8 +364,8 @@ __global__ __launch_bounds__(256, 2) void k_act8_grads(Act8GradJob a, GradJob b,
 template <int RT>
 hipError_t act8_grads_rt(const Act8GradJob& a, const GradJob& b, int64_t M, int r,
                          hipStream_t s) {
-  const int64_t blocks =
-      ceil_div(a.K, kGradCols) * a.splits + (RT <= 2 ? grad_blocks(b) : 0);
+  const int64_t blocks = ceil_div(a.K, kGradCols) * a.splits * grad_parts(r) +
+                         (RT <= 2 ? grad_blocks(b) : 0);
   const hipError_t e =
       launch_kernel(a.drop.thr != 0 ? k_act8_grads<RT, true> : k_act8_grads<RT, false>,
                     dim3((unsigned)blocks), dim3(256), s, a, b, M, r);
@@ -417,8 +416,7 @@ hipError_t launch_act8_grads(const Act8GradJob& a, const GradJob& b, int64_t M, 
   switch (skinny_rpad(r)) {
     case 16: return act8_grads_rt<1>(a, b, M, r, s);
     case 32: return act8_grads_rt<2>(a, b, M, r, s);
-    case 64: return act8_grads_rt<4>(a, b, M, r, s);
-    default: return act8_grads_rt<8>(a, b, M, r, s);
+    default: return act8_grads_rt<4>(a, b, M, r, s);
   }
 }
 

@@ -125,7 +125,7 @@ LinearWs linear_layout(int64_t M, int64_t N, int64_t K, int r) {
 }
 
 // What the backward from an 8-bit checkpoint needs behind that layout: the
-// float32 G^T [rpad, mp], then dA's partials, then (rank <= 16) G's.
+// float32 G^T [rpad, mp], then dA's partials, then G's.
 size_t act8_g_bytes(const LinearWs& w, int r) {
   return align_up((size_t)skinny_rpad(r) * w.mp * sizeof(float));
 }
@@ -134,7 +134,7 @@ size_t act8_a_bytes(int64_t M, int64_t K, int r) {
 }
 size_t act8_bytes(const LinearWs& w, int64_t M, int64_t N, int64_t K, int r) {
   return act8_g_bytes(w, r) + act8_a_bytes(M, K, r) +
-         (r <= 16 ? align_up(skinny_staged16_floats(M, N) * sizeof(float)) : 0);
+         align_up(skinny_staged_floats(M, N, r) * sizeof(float));
 }
 
 template <typename T>
@@ -635,8 +635,8 @@ static qlora_status linear_bwd_impl(const qlora_nf4_tensor* W, const qlora_bf16*
                        x8 && !dX ? nullptr : gs, nullptr, x8 ? nullptr : gt, L.mp};
   if (x8) {
     sj[0].out_tf = gtf;
-    if (r <= 16 && !dX) {   // (with dX, G is summed as the plain backward sums it)
-      sj[0].stage16 = true;
+    if (!dX) {   // (with dX, G is summed as the plain backward sums it)
+      sj[0].stage_any = true;
       sj[0].part = at<float>(ws, L.total + act8_g_bytes(L, r) + act8_a_bytes(M, K, r));
     }
   }

@@ -14,8 +14,12 @@ namespace qnf4 {
 // in wave order through LDS, one MFMA column t at a time.  With DROP, a job
 // whose J.drop is set reads T = X through the dropout mask and scales its
 // partials by J.drop.inv.
+// RT rank tiles from tile jt0 on, of rt in all: above rank 64 the tiles are two
+// slices' work (both read T; one slice of 8 tiles has no registers left to keep
+// a step's loads in flight: 2048 x 4096 at rank 128 31 us against GR128).
 template <int RT, bool DROP>
-__device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, int64_t b) {
+__device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, int64_t b,
+                                           int jt0 = 0, int rt = RT) {
   __shared__ float red[4][RT][4][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);   // wave-uniform
@@ -42,7 +46,7 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
   auto load_u = [&](int64_t mb, uint4 (&bu)[RT]) {
 #pragma unroll
     for (int jt = 0; jt < RT; ++jt)
-      bu[jt] = *reinterpret_cast<const uint4*>(J.U + ((mb >> 5) * RT + jt) * 512 + lane * 8);
+      bu[jt] = *reinterpret_cast<const uint4*>(J.U + ((mb >> 5) * rt + jt0 + jt) * 512 + lane * 8);
   };
   auto load_step = [&](int64_t mb, uint4 (&rows)[8], uint4 (&bu)[RT]) {   // 128 columns in range
 #pragma unroll
@@ -102,8 +106,8 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
   // through buffer views (fixed byte offsets per lane, the step's base as the
   // uniform offset), two steps in flight: the next step's loads are issued
   // before this step's MFMAs.
-  const int64_t tbytes = M * J.P * 2, ubytes = ceil_div(M, 32) * RT * 1024;
-  const bool bufs = fast && RT <= 4 && tbytes <= kBufferMax && ubytes <= kBufferMax;
+  const int64_t tbytes = M * J.P * 2, ubytes = ceil_div(M, 32) * rt * 1024;
+  const bool bufs = fast && tbytes <= kBufferMax && ubytes <= kBufferMax;
   const int64_t cnt_fast = bufs && first + 32 <= mend ? (mend - first - 32) / 128 + 1 : 0;
   if (cnt_fast > 0) {
     const __amdgpu_buffer_rsrc_t tview = buffer_view(J.T, tbytes);
@@ -113,11 +117,11 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
     for (int e = 0; e < 8; ++e) roff[e] = (uint32_t)((8 * g + e) * J.P + pc) * 2;
     auto load_fast = [&](int64_t i, uint4 (&rows)[8], uint4 (&bu)[RT]) {
       const int64_t mb = first + 128 * i;
-      const uint32_t tb = (uint32_t)(mb * J.P) * 2, ub = (uint32_t)(mb >> 5) * (RT * 1024);
+      const uint32_t tb = (uint32_t)(mb * J.P) * 2, ub = (uint32_t)(mb >> 5) * (rt * 1024);
 #pragma unroll
       for (int e = 0; e < 8; ++e) rows[e] = buffer_load16(tview, roff[e], tb);
 #pragma unroll
-      for (int jt = 0; jt < RT; ++jt) bu[jt] = buffer_load16(uview, lane * 16 + jt * 1024, ub);
+      for (int jt = 0; jt < RT; ++jt) bu[jt] = buffer_load16(uview, lane * 16 + (jt0 + jt) * 1024, ub);
     };
     uint4 r0[8], u0[RT], r1[8], u1[RT];
     load_fast(0, r0, u0);
@@ -175,7 +179,7 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
           for (int w = 1; w < 4; ++w) s += red[w][jt][v][lane];
           if constexpr (DROP) s *= J.drop.inv;
           const int64_t p = p0 + 8 * (4 * g + v) + t;
-          const int j = jt * 16 + i16;
+          const int j = (jt0 + jt) * 16 + i16;
           // partials in the output's own layout, so the reduce reads them
           // contiguously
           if (p < J.P && j < r) base[J.transposed ? (int64_t)j * J.P + p : p * r + j] = s;
@@ -184,6 +188,9 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
     __syncthreads();
   }
 }
+
+// Slices' worth of rank tiles.
+__host__ __device__ __forceinline__ int grad_parts(int r) { return r > 64 ? 2 : 1; }
 
 __host__ __device__ __forceinline__ int64_t grad_blocks(const GradJob& J) {
   return ceil_div(J.P, 128) * J.splits;

@@ -126,17 +126,18 @@ struct SkinnyJob {
   DropoutParams drop{};
   // float32 P^T likewise (frag32_at), beside or in place of out_t
   float* out_tf = nullptr;
-  // the LDS-staged kernel at ranks <= 16 too, `part` then sized by
-  // skinny_staged16_floats: whole 128-byte lines of T where the per-wave form
-  // takes 64-byte pieces of 16 rows (2048 x 14336: 10 us against 15.5)
-  bool stage16 = false;
+  // the LDS-staged kernel at every rank, `part` then sized by
+  // skinny_staged_floats: whole 128-byte lines of T where the per-wave form
+  // takes 64-byte pieces of 16 rows (2048 x 14336 at rank 16 10 us against
+  // 15.5, 2048 x 4096 at rank 128 SK128 against 42)
+  bool stage_any = false;
 };
 // Padded rank of the partial rows (16, 32, 64 or 128).
 int skinny_rpad(int r);
 int skinny_slices(int64_t M, int64_t kin, int r);
 // Floats of `part` a job with these sizes needs.
 size_t skinny_part_floats(int64_t M, int64_t kin, int r);
-size_t skinny_staged16_floats(int64_t M, int64_t kin);
+size_t skinny_staged_floats(int64_t M, int64_t kin, int r);
 // Fills ks / kslice of each job from its kin.
 void skinny_plan(SkinnyJob* j, int64_t M, int r);
 // Slice launch (jobs + optional recon), then the finish launch.

@@ -381,10 +381,12 @@ __global__ __launch_bounds__(256) void k_prep(TransposeJob t0, TransposeJob t1, 
 template <int RT, bool DROP>
 __global__ __launch_bounds__(256) void k_lora_grads(GradJob j0, GradJob j1, int nj, int64_t M,
                                                     int r) {
-  int64_t b = blockIdx.x;
+  const int parts = grad_parts(r);
+  const int64_t b = blockIdx.x / parts;
+  const int jt0 = (int)(blockIdx.x - b * parts) * RT, rt = RT * parts;
   const int64_t b0 = grad_blocks(j0);
-  if (b < b0) { grad_slice<RT, DROP>(j0, M, r, b); return; }
-  if (nj > 1) grad_slice<RT, DROP>(j1, M, r, b - b0);
+  if (b < b0) { grad_slice<RT, DROP>(j0, M, r, b, jt0, rt); return; }
+  if (nj > 1) grad_slice<RT, DROP>(j1, M, r, b - b0, jt0, rt);
 }
 
 __device__ __forceinline__ void grad_reduce_elem(const GradJob& J, int r, int64_t idx) {
@@ -481,7 +483,8 @@ hipError_t skinny2_rt(const SkinnyJob* jobs, int nj, int64_t M, int r, int r32,
 template <int RT>
 hipError_t grads_rt(const GradJob* jobs, int nj, int64_t M, int r, hipStream_t s) {
   int64_t blocks = 0;
-  for (int i = 0; i < nj; ++i) blocks += ceil_div(jobs[i].P, 128) * jobs[i].splits;
+  for (int i = 0; i < nj; ++i) blocks += grad_blocks(jobs[i]);
+  blocks *= grad_parts(r);
   bool drop = false;
   for (int i = 0; i < nj; ++i) drop |= jobs[i].drop.thr != 0;
   const auto kern = drop ? k_lora_grads<RT, true> : k_lora_grads<RT, false>;
@@ -498,7 +501,7 @@ int skinny_rpad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128
 // 16-byte rows.
 static bool skinny_staged(const SkinnyJob& j, int r) {
   const int rp = skinny_rpad(r);
-  return (rp == 32 || rp == 64 || (rp == 16 && j.stage16)) && j.kin % kSk2Step == 0 && j.ldt % 8 == 0 &&
+  return (rp == 32 || rp == 64 || j.stage_any) && j.kin % kSk2Step == 0 && j.ldt % 8 == 0 &&
          j.ldu % 8 == 0 && (reinterpret_cast<uintptr_t>(j.T) & 15) == 0 &&
          (reinterpret_cast<uintptr_t>(j.U) & 15) == 0;
 }
@@ -541,10 +544,10 @@ size_t skinny_part_floats(int64_t M, int64_t kin, int r) {
   return (size_t)skinny_slices(M, kin, r) * (size_t)M * (size_t)skinny_rpad(r);
 }
 
-size_t skinny_staged16_floats(int64_t M, int64_t kin) {
+size_t skinny_staged_floats(int64_t M, int64_t kin, int r) {
   const int s1 = skinny1_slices(M, kin);
   const int s2 = kin % kSk2Step == 0 ? skinny2_slices(M, kin) : 1;
-  return (size_t)(s1 > s2 ? s1 : s2) * (size_t)M * 16;
+  return (size_t)(s1 > s2 ? s1 : s2) * (size_t)M * (size_t)skinny_rpad(r);
 }
 
 void skinny_plan(SkinnyJob* j, int64_t M, int r) {
@@ -567,7 +570,8 @@ hipError_t launch_skinny(const SkinnyJob* jobs, int nj, int64_t M, int r, int r3
   if (ns > 0) {
     e = rpad == 16   ? skinny2_rt<1>(st, ns, M, r, r32, recon, s)
         : rpad == 32 ? skinny2_rt<2>(st, ns, M, r, r32, recon, s)
-                     : skinny2_rt<4>(st, ns, M, r, r32, recon, s);
+        : rpad == 64 ? skinny2_rt<4>(st, ns, M, r, r32, recon, s)
+                     : skinny2_rt<8>(st, ns, M, r, r32, recon, s);
     if (e != hipSuccess) return e;
     recon = nullptr;
   }
@@ -626,8 +630,7 @@ hipError_t launch_lora_grad_partials(const GradJob* jobs, int nj, int64_t M, int
   switch (skinny_rpad(r)) {
     case 16: return grads_rt<1>(jobs, nj, M, r, s);
     case 32: return grads_rt<2>(jobs, nj, M, r, s);
-    case 64: return grads_rt<4>(jobs, nj, M, r, s);
-    default: return grads_rt<8>(jobs, nj, M, r, s);
+    default: return grads_rt<4>(jobs, nj, M, r, s);
   }
 }
 
