@@ -341,35 +341,24 @@ __device__ __forceinline__ void act8_grad_slice(const Act8GradJob& J, int64_t M,
 }
 
 // dA from the codes and dB from dY in one launch: neither needs the other, and
-// one's last workgroups run beside the other's first.  Above rank 32 dB's sums
-// take registers that would leave dA one wave a SIMD instead of two, and the
-// two are launches of their own.
+// one's last workgroups run beside the other's first.
 template <int RT, bool DROP>
 __global__ __launch_bounds__(256, 2) void k_act8_grads(Act8GradJob a, GradJob b, int64_t M,
                                                       int r) {
-  const int64_t na = ceil_div(a.K, kGradCols) * a.splits;
-  if constexpr (RT == 4) {
-    const int parts = grad_parts(r);
-    const int64_t block = blockIdx.x / parts;
-    act8_grad_slice<RT, DROP>(a, M, r, block, (int)(blockIdx.x - block * parts) * RT, RT * parts);
-    return;
-  }
-  if ((int64_t)blockIdx.x < na) {
-    act8_grad_slice<RT, DROP>(a, M, r, blockIdx.x, 0, RT);
-    return;
-  }
-  if constexpr (RT <= 2) grad_slice<RT, false>(b, M, r, blockIdx.x - na);
+  const int parts = grad_parts(r);
+  const int64_t block = blockIdx.x / parts, na = ceil_div(a.K, kGradCols) * a.splits;
+  const int jt0 = (int)(blockIdx.x - block * parts) * RT, rt = RT * parts;
+  if (block < na) act8_grad_slice<RT, DROP>(a, M, r, block, jt0, rt);
+  else grad_slice<RT, false>(b, M, r, block - na, jt0, rt);
 }
 
 template <int RT>
 hipError_t act8_grads_rt(const Act8GradJob& a, const GradJob& b, int64_t M, int r,
                          hipStream_t s) {
-  const int64_t blocks = ceil_div(a.K, kGradCols) * a.splits * grad_parts(r) +
-                         (RT <= 2 ? grad_blocks(b) : 0);
-  const hipError_t e =
-      launch_kernel(a.drop.thr != 0 ? k_act8_grads<RT, true> : k_act8_grads<RT, false>,
-                    dim3((unsigned)blocks), dim3(256), s, a, b, M, r);
-  return RT <= 2 || e != hipSuccess ? e : launch_lora_grad_partials(&b, 1, M, r, s);
+  const int64_t blocks =
+      (ceil_div(a.K, kGradCols) * a.splits + grad_blocks(b)) * grad_parts(r);
+  return launch_kernel(a.drop.thr != 0 ? k_act8_grads<RT, true> : k_act8_grads<RT, false>,
+                       dim3((unsigned)blocks), dim3(256), s, a, b, M, r);
 }
 
 }  // namespace
