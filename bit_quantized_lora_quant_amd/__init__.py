@@ -815,8 +815,8 @@ def _bwd_act8(what, q, a, A, B, R, dY, XA_in, need_dx, dX, dA, dB, ws):
     M, K, N = a.rows, a.cols, q.rows
     for t, shape, name in ((A, (R, K), "A"), (B, (N, R), "B"), (dY, (M, N), "dY"),
                            (XA_in, (M, R), "XA_in")):
-        _require(t.dtype == torch.bfloat16 and t.is_contiguous() and t.shape == shape, what,
-                 "%s must be contiguous bf16 %s", name, shape)
+        _require(t is not None and t.dtype == torch.bfloat16 and t.is_contiguous() and
+                 t.shape == shape, what, "%s must be contiguous bf16 %s", name, shape)
     _require(K == q.cols, what, "checkpoint of another width than the weight")
     dev = dY.device
     if need_dx and dX is None:

@@ -380,24 +380,16 @@ hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64
                        rows, rows32, kb, tk, out);
 }
 
-// The split of the tokens with the least rounds x passes: the CUs hold 512
-// workgroups at once, so 3 slices of 172 column groups (516) take two rounds of
-// the length 5 slices (860) fill far better.  A slice more costs its partial's
-// way to memory and back, about K / 18000 passes.  4096 x 22016 at rank 64: 78
-// us with 2 slices (one round, a third of it empty), 81 with 3, 51 with 5.
+// About 192 workgroups (dB's fill the rest of the chip), at least two 32-token
+// steps a wave.  More slices shorten the launch until the chip is full and then
+// only add partials: with the reduction, 2048 x 4096 at rank 48 takes 40, 26,
+// 20 and 22 us with 1, 2, 4 and 8 slices, 4096 x 22016 at rank 64 75, 73, 74
+// and 82.
 int act8_grad_splits(int64_t M, int64_t K) {
-  const int64_t groups = ceil_div(K, kGradCols), passes = ceil_div(M, kGradTokens);
-  int64_t best = 1;
-  double least = 1e300;
-  for (int64_t s = 1; s <= 16 && s <= ceil_div(passes, 2); ++s) {
-    const double cost = (double)ceil_div(groups * s, 512) * (double)ceil_div(passes, s) +
-                        (double)s * (double)K / 18000.0;
-    if (cost < least) {
-      least = cost;
-      best = s;
-    }
-  }
-  return (int)best;
+  int64_t splits = ceil_div(192, ceil_div(K, kGradCols));
+  const int64_t maxs = ceil_div(M, 2 * kGradTokens);
+  if (splits > maxs) splits = maxs;
+  return (int)splits;
 }
 
 hipError_t launch_act8_grads(const Act8GradJob& a, const GradJob& b, int64_t M, int r,

@@ -14,6 +14,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxRows = (int64_t)1 << 24, kMaxVocab = (int64_t)1 << 30;
+constexpr int32_t kMaxSequences = 1 << 22;   // a workgroup of 512 threads each, in one dimension
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -92,7 +93,7 @@ bool opt4(const void* p) { return aligned(p, 4); }   // NULL passes
 extern "C" {
 
 size_t qlora_loss_workspace_bytes(const qlora_logits* z, int32_t sequences) {
-  if (check_sizes(z) != QLORA_OK || sequences < 0 || sequences >= (1 << 24)) return 0;
+  if (check_sizes(z) != QLORA_OK || sequences < 0 || sequences >= kMaxSequences) return 0;
   return loss_layout(z, sequences).total;
 }
 
@@ -139,7 +140,7 @@ qlora_status qlora_preference_loss(const qlora_logits* z, int32_t pairs, const i
       h->kind > QLORA_PREF_IPO || (h->kind != QLORA_PREF_SIGMOID && h->label_smoothing != 0) ||
       (h->length_mean != 0 && h->length_mean != 1))
     return QLORA_ERR_INVALID_ARG;
-  if (pairs >= (1 << 23)) return QLORA_ERR_UNSUPPORTED;
+  if (pairs >= kMaxSequences / 2) return QLORA_ERR_UNSUPPORTED;
   const LossWs L = loss_layout(z, 2 * pairs);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -172,7 +173,7 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
       (h->reduction != QLORA_POLICY_TOKEN && h->reduction != QLORA_POLICY_SEQUENCE) ||
       (h->token_advantages != 0 && h->token_advantages != 1))
     return QLORA_ERR_INVALID_ARG;
-  if (sequences >= (1 << 24)) return QLORA_ERR_UNSUPPORTED;
+  if (sequences >= kMaxSequences) return QLORA_ERR_UNSUPPORTED;
   const LossWs L = loss_layout(z, sequences);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -29,12 +29,12 @@ __device__ __forceinline__ uint2 load4_bf16(const uint16_t* __restrict__ p, int6
 // operands of 4 MFMAs: MFMA t handles p = p0 + 4 i + t, so the transpose of T
 // costs one 16-bit regroup per pair of rows, no LDS.  64 columns leave two
 // waves a SIMD their registers with two steps in flight each (128 columns left
-// one: 4096 x 8192 at rank 64 27 us against GR64).  Wave partials are added in
+// one: 4096 x 8192 at rank 64 27 us, now 22.6).  Wave partials are added in
 // wave order through LDS, one MFMA column t at a time.  With DROP, a job whose
 // J.drop is set reads T = X through the dropout mask and scales its partials by
 // J.drop.inv.
 // RT rank tiles from tile jt0 on, of rt in all: above rank 64 the tiles are two
-// slices' work (2048 x 4096 at rank 128 31 us as one slice of eight tiles).
+// slices' work (2048 x 4096 at rank 128 21 us, 31 as one slice of eight tiles).
 template <int RT, bool DROP>
 __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, int64_t b,
                                            int jt0 = 0, int rt = RT) {

@@ -129,7 +129,8 @@ struct SkinnyJob {
   // the LDS-staged kernel at every rank, `part` then sized by
   // skinny_staged_floats: whole 128-byte lines of T where the per-wave form
   // takes 64-byte pieces of 16 rows (2048 x 14336 at rank 16 10 us against
-  // 15.5, 2048 x 4096 at rank 128 SK128 against 42)
+  // 15.5, 2048 x 4096 at rank 128 10 us
+  // against 42)
   bool stage_any = false;
 };
 // Padded rank of the partial rows (16, 32, 64 or 128).
@@ -170,9 +171,7 @@ struct GradJob {
 int lora_grad_splits(int64_t M, int64_t P);
 // Both jobs' partial launch, then both reductions.
 hipError_t launch_lora_grads(const GradJob* jobs, int njobs, int64_t M, int r, hipStream_t s);
-// The two launches apart.
-hipError_t launch_lora_grad_partials(const GradJob* jobs, int njobs, int64_t M, int r,
-                                     hipStream_t s);
+// The reductions alone.
 hipError_t launch_lora_grad_reduce(const GradJob* jobs, int njobs, int r, hipStream_t s);
 
 // Checkpoints in 8 bits: codes int8 [rows, cols] and scales float32

@@ -625,7 +625,7 @@ hipError_t launch_lora_grad_reduce(const GradJob* jobs, int nj, int r, hipStream
   return hipGetLastError();
 }
 
-hipError_t launch_lora_grad_partials(const GradJob* jobs, int nj, int64_t M, int r,
+static hipError_t lora_grad_partials(const GradJob* jobs, int nj, int64_t M, int r,
                                      hipStream_t s) {
   switch (skinny_rpad(r)) {
     case 16: return grads_rt<1>(jobs, nj, M, r, s);
@@ -635,7 +635,7 @@ hipError_t launch_lora_grad_partials(const GradJob* jobs, int nj, int64_t M, int
 }
 
 hipError_t launch_lora_grads(const GradJob* jobs, int nj, int64_t M, int r, hipStream_t s) {
-  const hipError_t e = launch_lora_grad_partials(jobs, nj, M, r, s);
+  const hipError_t e = lora_grad_partials(jobs, nj, M, r, s);
   return e == hipSuccess ? launch_lora_grad_reduce(jobs, nj, r, s) : e;
 }
 

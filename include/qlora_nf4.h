@@ -547,7 +547,7 @@ qlora_status qlora_grouped_bwd_act8(const qlora_nf4_tensor* W, const qlora_act8*
  *
  * Sequence i of a packed batch is rows cu_seqlens[i] .. cu_seqlens[i+1] - 1
  * (int32 [sequences + 1], device, ascending from >= 0 to <= rows; a value
- * outside is clamped).  Empty sequences are allowed.  Rows in no sequence
+ * outside is clamped), fewer than 2^22 of them.  Empty sequences are allowed.  Rows in no sequence
  * (padding before the first or behind the last) count as rows without target,
  * whatever their label: their logp is 0 and their gradient zero. */
 typedef struct {
@@ -558,8 +558,9 @@ typedef struct {
   const int64_t* labels;   /* device, [rows] */
 } qlora_logits;
 
-/* Bytes of workspace the four calls below need for these logits and this
- * number of sequences (token_logprobs: 0); 0 for sizes they refuse. */
+/* Bytes of workspace the calls below need for these logits and this number of
+ * sequences (token_logprobs: 0; its backward needs none); 0 for sizes they
+ * refuse. */
 size_t qlora_loss_workspace_bytes(const qlora_logits* z, int32_t sequences);
 
 /* Log-probabilities of the targets: logp float32 [rows].  stats (nullable)

@@ -98,5 +98,5 @@ def test_binding_refusals():
     _raises(q.qlora_linear_bwd_act8, **good)                       # on the host
     for name, v in (("A", b(8, 64)), ("B", b(256, 4)), ("dY", b(5, 256)), ("XA_in", b(4, 4)),
                     ("dY", b(4, 512)[:, ::2]), ("dA", b(8, 128)), ("dX", torch.zeros(4, 128)),
-                    ("keep_bits", torch.zeros(3, dtype=torch.uint8))):
+                    ("keep_bits", torch.zeros(3, dtype=torch.uint8)), ("XA_in", None)):
         _raises(q.qlora_linear_bwd_act8, **{**good, name: v})

@@ -81,7 +81,8 @@ def test_preference_refusals():
                dict(smooth=0.6), dict(smooth=nan), dict(kind=3), dict(kind=-1),
                dict(kind=1, smooth=0.1), dict(mean=2), dict(dz=FAKE, ldd=99), dict(ref=FAKE + 1)):
         assert _pref(_z(), **kw) == bad, kw
-    assert _pref(_z(), pairs=1 << 23) == q.QLORA_ERR_UNSUPPORTED
+    for pairs in (1 << 21, 1 << 23):
+        assert _pref(_z(), pairs=pairs) == q.QLORA_ERR_UNSUPPORTED
     z = _z()
     need = q.lib().qlora_loss_workspace_bytes(ctypes.byref(z), 4)
     assert need > 0 and _pref(z, ws_bytes=need - 1) == q.QLORA_ERR_WORKSPACE
@@ -94,7 +95,8 @@ def test_policy_refusals():
                dict(lo=1.5), dict(hi=-0.1), dict(hi=inf), dict(kl=-1.0, ref=FAKE),
                dict(kl=nan, ref=FAKE), dict(kl=0.1), dict(red=2), dict(tok=2), dict(old=FAKE + 2)):
         assert _pol(_z(), **kw) == bad, kw
-    assert _pol(_z(), n=1 << 24) == q.QLORA_ERR_UNSUPPORTED
+    for n in (1 << 22, 1 << 24):
+        assert _pol(_z(), n=n) == q.QLORA_ERR_UNSUPPORTED
     z = _z()
     need = q.lib().qlora_loss_workspace_bytes(ctypes.byref(z), 2)
     assert _pol(z, ws_bytes=need - 1) == q.QLORA_ERR_WORKSPACE
