@@ -474,23 +474,54 @@ void k_qlora_fwd_nt(const FwdGemmJob j0, const FwdGemmJob j1, int64_t tn_split, 
 // the starting value of the accumulators that the frozen product's MFMAs then
 // add to (nothing is added to them by VALU afterwards).  The product runs as
 // the unmasked tail does: per 32 adapter indices, A's B operands once and all
-// 16 row tiles' (s.G) loads in flight together.  Where the forward stored the
-// keep bits they are read: the wave's 256 rows x 64 columns are 8 bytes a row,
-// four loads a lane, and go through the wave's 2 KB at `lds` to the lanes that
-// need them (each takes a byte of 64 rows, which straight from memory are 64
-// scattered loads).  Without them they come from the generator, one block per
-// row and 4 consecutive columns, with the round loop rolled over 4 blocks at a
-// time (fully unrolled, the 16 row tiles exceed the unroller's budget and the
-// accumulators fall into scratch): 64 blocks a lane.  The bits make the dX
-// launch 28.5 us instead of 39 at 331 x 1024 x 1024 and 81 instead of 88 at
-// 2048 x 4096 x 4096.  The workgroup synchronises before it uses `lds` for
-// anything else.
+// 16 row tiles' (s.G) loads in flight together.  The keep bits of the wave's 256
+// rows x 64 columns are gathered first, before the accumulators are live: 8
+// bytes a row into the wave's 2 KB at `lds`, read where the forward stored
+// them (four loads a lane; straight from memory each lane would need a byte of
+// 64 rows), else drawn (64 generator blocks a lane, eight at a time).  Both then
+// mask alike, so no 256 accumulators live across a branch: with the generator
+// between the product and the mask, beside the path of the bits, 110 registers
+// spill and drawing costs 20 us more.  dX at 331 x 1024 x 1024 takes 24 us
+// without dropout, 30 with stored bits and 38 drawn; 2048 x 4096 x 4096 75, 77
+// and 87, 2048 x 4096 x 14336 217, 228 and 246.
+// The workgroup synchronises before it uses `lds` for anything else.
 __device__ __forceinline__ void dropout_lora_init(f32x4_t (&acc)[16][4],
                                                   const uint16_t* __restrict__ gs,
                                                   const uint16_t* __restrict__ A, int r, int r32,
                                                   int64_t M, int64_t K, int64_t m0, int64_t kcl,
                                                   int j16, int g, const DropoutParams& d,
                                                   void* lds) {
+  // keep bits of rows 64 i + lane, the wave's 64 columns (K % 64 == 0; past K
+  // they repeat the last 64, which are never stored)
+  uint2* const kept = static_cast<uint2*>(lds) + (threadIdx.x >> 6) * 256;
+  const int64_t kw = __builtin_amdgcn_readfirstlane((int)(kcl / kBlock)) * (int64_t)kBlock;
+  const int lane = threadIdx.x & 63;
+  if (d.bits) {
+    uint2 kr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int64_t m = m0 + 64 * i + lane;
+      m = m < M ? m : M - 1;
+      __builtin_memcpy(&kr[i], d.bits + ((m * K + kw) >> 3), 8);   // of any alignment
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) kept[64 * i + lane] = kr[i];
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      int64_t m = m0 + 64 * i + lane;
+      m = m < M ? m : M - 1;
+      const uint64_t c0 = (uint64_t)(m * K + kw) >> 2;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t b = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          b |= keep_nibble(dropout_words(c0 + 8 * h + q, d), d.thr) << (4 * q);
+        reinterpret_cast<uint32_t*>(kept + 64 * i + lane)[h] = b;
+      }
+    }
+  }
 #pragma unroll
   for (int mt = 0; mt < 16; ++mt)
 #pragma unroll
@@ -531,53 +562,21 @@ __device__ __forceinline__ void dropout_lora_init(f32x4_t (&acc)[16][4],
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[mt][t] = mfma16x16x32(a[mt], bb[t], acc[mt][t]);
   }
-  // kn: keep bits of rows v = 0..3 of row tile mt, columns kc .. kc + 3
-  auto mask = [&](int mt, const uint32_t (&kn)[4]) {
+  // (the wave reads what its own lanes wrote)
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  // keep bits of rows 16 mt + 4 g + v, columns kc .. kc + 3
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(kept) + 32 * g + ((kcl & 63) >> 3);
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        acc[mt][t][v] = ((kn[v] >> t) & 1u) ? d.inv * acc[mt][t][v] : 0.f;
-  };
-  if (d.bits) {
-    // rows 64 i + lane of the wave's 64 columns (K % 64 == 0; past K it repeats
-    // the last 64, which are never stored)
-    uint2* const kept = static_cast<uint2*>(lds) + (threadIdx.x >> 6) * 256;
-    const int64_t kw = __builtin_amdgcn_readfirstlane((int)(kcl / kBlock)) * (int64_t)kBlock;
-    uint2 kr[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      int64_t m = m0 + 64 * i + (threadIdx.x & 63);
-      m = m < M ? m : M - 1;
-      __builtin_memcpy(&kr[i], d.bits + ((m * K + kw) >> 3), 8);   // of any alignment
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) kept[64 * i + (threadIdx.x & 63)] = kr[i];
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(kept) + 32 * g + ((kcl & 63) >> 3);
-#pragma unroll
-    for (int mt = 0; mt < 16; ++mt) {
-      uint32_t kn[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) kn[v] = (uint32_t)p[128 * mt + 8 * v] >> (kcl & 4);
-      mask(mt, kn);
-    }
-    return;
-  }
-#pragma unroll
-  for (int mt = 0; mt < 16; ++mt) {
-    uint32_t kn[4];
-    uint4 wd[4];
+  for (int mt = 0; mt < 16; ++mt)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const uint64_t c =
-          ((uint64_t)(m0 + mt * 16 + 4 * g + v) * (uint64_t)K + (uint64_t)kcl) >> 2;
-      wd[v] = make_uint4((uint32_t)c, (uint32_t)(c >> 32), 0u, 0u);
-    }
-    philox4x32_10_rolled<4>(wd, d.k0, d.k1);
+      const uint32_t kn = (uint32_t)p[128 * mt + 8 * v] >> (kcl & 4);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) kn[v] = keep_nibble(wd[v], d.thr);
-    mask(mt, kn);
-  }
+      for (int t = 0; t < 4; ++t)
+        acc[mt][t][v] = ((kn >> t) & 1u) ? d.inv * acc[mt][t][v] : 0.f;
+    }
 }
 
 // dX tile 256 (rows m) x 256 (cols k); inner loop over n in steps of 64.

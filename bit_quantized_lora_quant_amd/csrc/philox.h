@@ -52,25 +52,6 @@ __device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1
   return c;
 }
 
-// N blocks at once with the round loop kept rolled: the rounds of the N
-// independent blocks interleave, and the code stays small enough to sit in a
-// fully unrolled loop over register-resident tiles.
-template <int N>
-__device__ __forceinline__ void philox4x32_10_rolled(uint4 (&c)[N], uint32_t k0, uint32_t k1) {
-#pragma unroll 1
-  for (int round = 0; round < 10; ++round) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint64_t p0 = (uint64_t)0xD2511F53u * c[i].x;
-      const uint64_t p1 = (uint64_t)0xCD9E8D57u * c[i].z;
-      c[i] = make_uint4((uint32_t)(p1 >> 32) ^ c[i].y ^ k0, (uint32_t)p1,
-                        (uint32_t)(p0 >> 32) ^ c[i].w ^ k1, (uint32_t)p0);
-    }
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
-  }
-}
-
 // The four output words of block c (elements 4c .. 4c + 3).
 __device__ __forceinline__ uint4 dropout_words(uint64_t c, const DropoutParams& d) {
   return philox4x32_10(make_uint4((uint32_t)c, (uint32_t)(c >> 32), 0u, 0u), d.k0, d.k1);
