@@ -14,11 +14,12 @@ namespace qnf4 {
 namespace {
 
 // Both directions move about three bytes a value with little to compute and
-// are bound by HBM: 4096 x 22016 there and back in 91 us, 6.1 TB/s.  A workgroup takes 32 rows x 256 columns: 32 lanes hold a
-// row's 256 values, 16 bytes each, so every load and store instruction covers
-// whole 256- to 1024-byte runs of two rows, a lane has its four rows' loads
-// in flight together, and 8 neighbouring lanes hold one block, whose maximum
-// is three DPP steps on packed 16-bit magnitudes.  32 rows are what makes the
+// are bound by HBM: 4096 x 22016 there and back in 91 us, 6.1 TB/s.  A
+// workgroup takes 32 rows x 256 columns: 32 lanes hold a row's 256 values, 16
+// bytes each, so every load and store instruction covers whole 256- to
+// 1024-byte runs of two rows, a lane has its four rows' loads in flight
+// together, and 8 neighbouring lanes hold one block, whose maximum is three DPP
+// steps on packed 16-bit magnitudes.  32 rows are what makes the
 // scales, which run along rows, whole 128-byte lines.
 constexpr int kTileRows = 32, kTileCols = 256, kTileKb = kTileCols / kBlock;
 constexpr int kRowsPerStep = 8;                     // 256 threads / 32 lanes a row
@@ -158,8 +159,8 @@ __global__ __launch_bounds__(256) void k_act8_dequantize(const int8_t* __restric
 // three MFMAs where one would leave dA with bf16 errors (relative error 2e-7
 // against 2e-3).  Bound by issue: 6.5 operations for each product of G and a
 // scale and three MFMAs for each 16 x 16 x 32; at rank 16 the codes' way from
-// memory shows first.  With dB in the same launch 4096 x 22016 x 8192 at rank 64
-// takes 64 us, 2048 x 4096 x 14336 at rank 16 12.5.
+// memory shows first.  With dB in the same launch, codes of 4096 x 22016 and dY of
+// 4096 x 8192 at rank 64 take 64 us, 2048 x 4096 and 2048 x 14336 at rank 16 13.5.
 //
 // A workgroup takes 128 columns (two blocks) of a token slice: waves 0 and 1 the
 // even 32-token steps, waves 2 and 3 the odd ones, the second of each pair the
@@ -168,8 +169,9 @@ __global__ __launch_bounds__(256) void k_act8_dequantize(const int8_t* __restric
 // 4 i16 .. 4 i16 + 3: MFMA t handles columns 4 i + t, and converting byte t of
 // the eight rows is the transpose.  The next step's loads are in flight under a
 // step's work; 64 columns a wave keep that within two waves' registers at four
-// rank tiles, and ranks above 64 are two slices' work.  The token halves are added in order through LDS, 16 rank indices at
-// a time, and leave as rows of 128 columns.
+// rank tiles, and ranks above 64 are two slices' work.  The token halves are
+// added in order through LDS, 16 rank indices at a time, and leave as rows of
+// 128 columns.
 constexpr int kGradCols = 128, kGradTokens = 64;   // a workgroup's, per pass
 
 template <int RT>

@@ -129,8 +129,7 @@ struct SkinnyJob {
   // the LDS-staged kernel at every rank, `part` then sized by
   // skinny_staged_floats: whole 128-byte lines of T where the per-wave form
   // takes 64-byte pieces of 16 rows (2048 x 14336 at rank 16 10 us against
-  // 15.5, 2048 x 4096 at rank 128 10 us
-  // against 42)
+  // 15.5, 2048 x 4096 at rank 128 10 us against 42)
   bool stage_any = false;
 };
 // Padded rank of the partial rows (16, 32, 64 or 128).
@@ -148,9 +147,9 @@ hipError_t launch_skinny(const SkinnyJob* jobs, int njobs, int64_t M, int r, int
 hipError_t launch_prep(const TransposeJob* t, int nt, const ReconJob* recon, hipStream_t s);
 
 // Adapter gradient: out = scale * sum_m T[m][p] U[j][m], T [M, P] (row stride
-// P), U in fragment order (zero from M to the next multiple of 32).  Token range cut into `splits`
-// slices with float32 partials [splits][P][r]; out is [r][P] when
-// `transposed`, else [P][r].
+// P), U in fragment order (zero from M to the next multiple of 32).  Token
+// range cut into `splits` slices with float32 partials [splits][P][r]; out is
+// [r][P] when `transposed`, else [P][r].
 struct GradJob {
   const uint16_t* T;
   int64_t P;

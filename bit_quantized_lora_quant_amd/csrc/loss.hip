@@ -835,11 +835,7 @@ static hipError_t policy_rows(const LogitsView& v, const RowOut& o, const Policy
                        dim3(NT), s, v, o, a, static_cast<T*>(dz), ldd);
 }
 
-// The one-pass form where a row fits in registers and is long enough to be worth
-// a workgroup (16 KB), the rows fill the chip, and the gradient's rows start
-// where the logits' do between 16-byte boundaries.  Whole calls over 128,256
-// bf16 logits, one pass against two: 43 and 38 us at 128 rows, 48 and 54 at 256,
-// 206 and 251 at 2048; over 32,000 26 and 29, 28 and 35, 64 and 78.
+// threads that hold the row in 16 chunks each at most
 template <typename T>
 static hipError_t policy_rows_of(const LogitsView& v, const RowOut& o, const PolicyArgs& a,
                                  void* dz, int64_t ldd, hipStream_t s) {
@@ -848,9 +844,15 @@ static hipError_t policy_rows_of(const LogitsView& v, const RowOut& o, const Pol
   if (chunks <= 512 * 16) return policy_rows<T, 512, 16>(v, o, a, dz, ldd, s);
   return policy_rows<T, 1024, 16>(v, o, a, dz, ldd, s);
 }
+// The one-pass form where a row fits in registers and is long enough to be worth
+// a workgroup (16 KB), the rows fill the chip, and the gradient's rows start
+// where the logits' do between 16-byte boundaries.  Whole calls over 128,256
+// bf16 logits, one pass against two: 43 and 38 us at 128 rows, 48 and 54 at 256,
+// 206 and 251 at 2048; over 32,000 26 and 29, 28 and 35, 64 and 78.
 static bool one_pass(const LogitsView& v, const void* dz, int64_t ldd) {
   const int64_t chunks = row_chunks(v.vocab, v.bf16);
-  const uintptr_t apart = ((uintptr_t)dz - (uintptr_t)v.z) | (uintptr_t)((ldd - v.ld) * (v.bf16 ? 2 : 4));
+  const uintptr_t apart =
+      ((uintptr_t)dz - (uintptr_t)v.z) | (uintptr_t)((ldd - v.ld) * (v.bf16 ? 2 : 4));
   return chunks >= 1024 && chunks <= 1024 * 16 && v.rows >= 256 && (apart & 15) == 0;
 }
 

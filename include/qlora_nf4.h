@@ -509,7 +509,7 @@ size_t qlora_linear_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_
 
 /* qlora_linear_bwd_dropout whose input is a checkpoint of X [M, K], M =
  * X8->rows: dA = s . G^T . D(x^) is formed from the codes, with G kept in
- * float32 and its products with the scales in two bf16 parts, so dA has
+ * float32 and its products with the scales in three bf16 parts, so dA has
  * float32 accuracy for the given x^; dX and dB do not read X.  XA_in
  * (required) is the forward's XA_out.  drop and keep_bits_in (both nullable)
  * as there.  Same shapes, limits and errors, plus QLORA_ERR_INVALID_ARG for a
@@ -537,8 +537,9 @@ qlora_status qlora_grouped_bwd_act8(const qlora_nf4_tensor* W, const qlora_act8*
  * reaches the loss and the gradient.  For a row with target y
  *     logp = z_y - m - log sum_v exp(z_v - m),   m = max_v z_v,
  * the sum over v in float32, the logarithm and what follows it in float64
- * (logp is rounded once when it is stored); a logit of -inf has probability 0, a row of nothing else (or with +inf or NaN) logp
- * NaN.  Results are identical run to run (fixed orders, no float atomics).
+ * (logp is rounded once when it is stored); a logit of -inf has probability 0,
+ * a row of nothing else (or with +inf or NaN) logp NaN.  Results are identical
+ * run to run (fixed orders, no float atomics).
  *
  * The logits are described by a host struct: bf16 or float32, row stride
  * ld >= vocab values, aligned to their type (16-byte row starts are fastest).
@@ -547,9 +548,10 @@ qlora_status qlora_grouped_bwd_act8(const qlora_nf4_tensor* W, const qlora_act8*
  *
  * Sequence i of a packed batch is rows cu_seqlens[i] .. cu_seqlens[i+1] - 1
  * (int32 [sequences + 1], device, ascending from >= 0 to <= rows; a value
- * outside is clamped), fewer than 2^22 of them.  Empty sequences are allowed.  Rows in no sequence
- * (padding before the first or behind the last) count as rows without target,
- * whatever their label: their logp is 0 and their gradient zero. */
+ * outside is clamped), fewer than 2^22 of them.  Empty sequences are allowed.
+ * Rows in no sequence (padding before the first or behind the last) count as
+ * rows without target, whatever their label: their logp is 0 and their gradient
+ * zero. */
 typedef struct {
   const void* data;        /* device, [rows] x ld; may be NULL when rows == 0 */
   qlora_dtype dtype;       /* QLORA_F32 or QLORA_BF16 */
@@ -565,7 +567,8 @@ size_t qlora_loss_workspace_bytes(const qlora_logits* z, int32_t sequences);
 
 /* Log-probabilities of the targets: logp float32 [rows].  stats (nullable)
  * float32 [rows][2] receives each row's m and sum_v exp(z_v - m) (0, 0
- * without target) for the backward.  Every row with a label >= 0 counts, in any sequence. */
+ * without target) for the backward.  Every row with a label >= 0 counts: there
+ * are no sequences here. */
 qlora_status qlora_token_logprobs(const qlora_logits* z, float* logp, float* stats, void* ws,
                                   size_t ws_bytes, void* stream);
 
@@ -619,8 +622,11 @@ qlora_status qlora_preference_loss(const qlora_logits* z, int32_t pairs, const i
  *            + kl_coef (exp(d) - d - 1),   d = ref_logp - logp,
  * averaged over all targets (TOKEN) or over each sequence's targets and then
  * over the sequences that have any (SEQUENCE).  No gradient flows through
- * the clamp where it is the larger.  0 when there is no target.  Terms in
- * float64. */
+ * the clamp where it is the larger.  0 when there is no target.  Terms and
+ * their means are float64; a row's weight dLoss / dlogp is float64 too, rounded
+ * once, except where a call with dlogits reads the logits only once (many rows
+ * of a vocabulary's length that fits a workgroup's registers): there it is
+ * formed in float32. */
 #define QLORA_POLICY_TOKEN 0
 #define QLORA_POLICY_SEQUENCE 1
 typedef struct {
