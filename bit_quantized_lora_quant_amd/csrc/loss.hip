@@ -350,10 +350,24 @@ __device__ __forceinline__ double row_logp(const LogitsView& v, const RowOut& o,
   MaxSum a;
   if (slices > 1) {
     const MaxSum* p = o.part + t * slices;
-    float m = -kInf;
-    for (int i = 0; i < slices; ++i) m = fmaxf(m, p[i].m);
-    float s = 0.f;
-    for (int i = 0; i < slices; ++i) s += p[i].m == m ? p[i].s : p[i].s * exp_exact(p[i].m - m);
+    // (a thread has this to itself: its loads go out 16 at a time)
+    MaxSum q[16];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) q[i] = p[i0 + i < slices ? i0 + i : slices - 1];
+    };
+    float m = -kInf, s = 0.f;
+    for (int i0 = 0; i0 < slices; i0 += 16) {
+      load(i0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = fmaxf(m, q[i].m);
+    }
+    for (int i0 = 0; i0 < slices; i0 += 16) {
+      if (slices > 16) load(i0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        s += i0 + i >= slices ? 0.f : q[i].m == m ? q[i].s : q[i].s * exp_exact(q[i].m - m);
+    }
     a = MaxSum{m, s};
     o.stats[t] = a;
   } else {
