@@ -34,6 +34,11 @@ qlora_status check_sizes(const qlora_logits* z) {
   return QLORA_OK;
 }
 
+// (the statistics launch has a workgroup for each of both)
+bool too_many(const qlora_logits* z, int64_t sequences) {
+  return sequences >= kMaxSequences || z->rows + sequences >= kMaxRows;
+}
+
 qlora_status check_logits(const qlora_logits* z) {
   const qlora_status st = check_sizes(z);
   if (st != QLORA_OK) return st;
@@ -93,7 +98,7 @@ bool opt4(const void* p) { return aligned(p, 4); }   // NULL passes
 extern "C" {
 
 size_t qlora_loss_workspace_bytes(const qlora_logits* z, int32_t sequences) {
-  if (check_sizes(z) != QLORA_OK || sequences < 0 || sequences >= kMaxSequences) return 0;
+  if (check_sizes(z) != QLORA_OK || sequences < 0 || too_many(z, sequences)) return 0;
   return loss_layout(z, sequences).total;
 }
 
@@ -140,7 +145,7 @@ qlora_status qlora_preference_loss(const qlora_logits* z, int32_t pairs, const i
       h->kind > QLORA_PREF_IPO || (h->kind != QLORA_PREF_SIGMOID && h->label_smoothing != 0) ||
       (h->length_mean != 0 && h->length_mean != 1))
     return QLORA_ERR_INVALID_ARG;
-  if (pairs >= kMaxSequences / 2) return QLORA_ERR_UNSUPPORTED;
+  if (too_many(z, 2 * (int64_t)pairs)) return QLORA_ERR_UNSUPPORTED;
   const LossWs L = loss_layout(z, 2 * pairs);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -173,7 +178,7 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
       (h->reduction != QLORA_POLICY_TOKEN && h->reduction != QLORA_POLICY_SEQUENCE) ||
       (h->token_advantages != 0 && h->token_advantages != 1))
     return QLORA_ERR_INVALID_ARG;
-  if (sequences >= kMaxSequences) return QLORA_ERR_UNSUPPORTED;
+  if (too_many(z, sequences)) return QLORA_ERR_UNSUPPORTED;
   const LossWs L = loss_layout(z, sequences);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);

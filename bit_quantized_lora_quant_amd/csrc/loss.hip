@@ -281,17 +281,61 @@ __device__ __forceinline__ void add_value(MaxSum& a, float x) {
   a.s += exp_exact(x - (a.m == -kInf ? 0.f : a.m));
 }
 
+// Sums over the workgroup in a fixed order, the results in every thread; red: N
+// doubles for each wave.
+template <int NT, int N>
+__device__ __forceinline__ void wg_sum(double (&x)[N], double (*red)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[threadIdx.x >> 6][i] = x[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = red[0][i];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) x[i] += red[w][i];
+  }
+}
+
+// The targets of sequence i, and its rows' sequence.
+template <int NT>
+__device__ __forceinline__ void count_sequence(const LogitsView& v, int i, int* count, int* seq,
+                                               double (*red)[1]) {
+  double n[1] = {0};
+  for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += NT) {
+    n[0] += v.labels[t] >= 0;
+    seq[t] = i;
+  }
+  wg_sum<NT, 1>(n, red);
+  if (threadIdx.x == 0) count[i] = (int)n[0];
+}
+
 // ------------------------------------------------------------ row statistics
 // Workgroup (row, slice of its chunks); 8 loads a thread in flight.  One slice
-// writes the row's result, several their parts.  Bound by HBM, with the
+// writes the row's result, several their parts.  With `count` the first nseq
+// workgroups count the sequences' targets instead.  Bound by HBM, with the
 // exponentials close behind (9 operations a value, one of quarter rate): 0.80 GB
 // of targets' rows in 131 us, 6.1 TB/s.
-template <typename T>
-__global__ __launch_bounds__(kT) void k_row_stats(LogitsView v, RowOut o, int slices) {
-  __shared__ float red[kT / 64][2];
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void k_row_stats(LogitsView v, RowOut o, int slices,
+                                                  int* count, int* seq) {
+  __shared__ float red[NT / 64][2];
   if (blockIdx.x == 0 && threadIdx.x == 0 && o.ticket) *o.ticket = 0;
-  const int64_t t = blockIdx.x / (unsigned)slices;
-  const int sl = (int)(blockIdx.x - t * slices);
+  unsigned b = blockIdx.x;
+  if (count) {
+    if (b < (unsigned)v.nseq) {
+      __shared__ double n[NT / 64][1];
+      count_sequence<NT>(v, (int)b, count, seq, n);
+      return;
+    }
+    b -= v.nseq;
+  }
+  const int64_t t = b / (unsigned)slices;
+  const int sl = (int)(b - t * slices);
   if (t >= v.rows) return;
   const int64_t y = v.labels[t];
   if (y < 0 || y >= v.vocab || outside(v, t)) {
@@ -309,14 +353,14 @@ __global__ __launch_bounds__(kT) void k_row_stats(LogitsView v, RowOut o, int sl
   const int tid = threadIdx.x;
   int c = c0 + tid;
   const bool keep = (v.rows - t) * v.ld * (int64_t)sizeof(T) < kKept;
-  for (; c - tid + kT * kBatch <= c1; c += kT * kBatch) {
+  for (; c - tid + NT * kBatch <= c1; c += NT * kBatch) {
     uint4 q[kBatch];
     if (keep) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) q[i] = r.chunk(c + kT * i);
+      for (int i = 0; i < kBatch; ++i) q[i] = r.chunk(c + NT * i);
     } else {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) q[i] = r.chunk_once(c + kT * i);
+      for (int i = 0; i < kBatch; ++i) q[i] = r.chunk_once(c + NT * i);
     }
     add_batch<T, true>(a, q, kBatch);
   }
@@ -324,12 +368,12 @@ __global__ __launch_bounds__(kT) void k_row_stats(LogitsView v, RowOut o, int sl
     uint4 q[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      q[i] = r.chunk(c + kT * i < c1 ? c + kT * i : c);
-    add_batch<T, false>(a, q, (c1 - c + kT - 1) / kT);
+      q[i] = r.chunk(c + NT * i < c1 ? c + NT * i : c);
+    add_batch<T, false>(a, q, (c1 - c + NT - 1) / NT);
   }
-  if (failed(a)) sum_again<T>(a, r, c0 + tid, c1, kT);
+  if (failed(a)) sum_again<T>(a, r, c0 + tid, c1, NT);
   if (sl == 0 && tid < r.edge) add_value(a, ld1(r.z + r.edge_at(tid)));
-  a = wg_join<kT / 64>(a, red);
+  a = wg_join<NT / 64>(a, red);
   if (threadIdx.x != 0) return;
   const float zy = ld1(r.z + y);
   if (sl == 0) o.zy[t] = zy;
@@ -440,26 +484,6 @@ __global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const MaxSum* sta
 }
 
 // ------------------------------------------------------- between the streams
-// Sums over the workgroup in a fixed order, the results in every thread; red: N
-// doubles for each wave.
-template <int NT, int N>
-__device__ __forceinline__ void wg_sum(double (&x)[N], double (*red)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[threadIdx.x >> 6][i] = x[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] = red[0][i];
-#pragma unroll
-    for (int w = 1; w < NT / 64; ++w) x[i] += red[w][i];
-  }
-}
-
 // Whether this workgroup is the last of n to come here.  What each wrote
 // through thread 0 before is then visible to the last one's device_load.
 __device__ __forceinline__ bool last_of(uint32_t* ticket, uint32_t n) {
@@ -572,8 +596,8 @@ __device__ __forceinline__ void list_targets(const LogitsView& v, int* list) {
   if (threadIdx.x == 0) list[v.rows] = n;
 }
 
-// Workgroup per sequence: its targets, and its rows' sequence.  One more lists
-// all rows with a target, in order, where the one-pass form shares them out.
+// Before the one-pass form: a workgroup per sequence counts its targets, and one
+// more lists all rows with a target, in order, to be shared out.
 __global__ __launch_bounds__(kSeqT) void k_policy_count(LogitsView v, RowOut o, PolicyArgs a) {
   __shared__ double red[kSeqT / 64][1];
   const int i = blockIdx.x;
@@ -582,13 +606,7 @@ __global__ __launch_bounds__(kSeqT) void k_policy_count(LogitsView v, RowOut o, 
     list_targets(v, a.list);
     return;
   }
-  double n[1] = {0};
-  for (int64_t t = cu_at(v, i) + threadIdx.x; t < cu_at(v, i + 1); t += kSeqT) {
-    n[0] += v.labels[t] >= 0;
-    a.seq[t] = i;
-  }
-  wg_sum<kSeqT, 1>(n, red);
-  if (threadIdx.x == 0) a.count[i] = (int)n[0];
+  count_sequence<kSeqT>(v, i, a.count, a.seq, red);
 }
 
 // All targets, and the sequences that have any.
@@ -790,10 +808,12 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
 // 16-byte chunks of a row, at most (one that starts between boundaries has fewer)
 int64_t row_chunks(int64_t vocab, int bf16) { return ceil_div(vocab, bf16 ? 8 : 4); }
 
-hipError_t row_stats(const LogitsView& v, const RowOut& o, int slices, hipStream_t s) {
-  const int64_t blocks = v.rows > 0 ? v.rows * slices : 1;   // one sets the counter
-  return launch_kernel(v.bf16 ? k_row_stats<uint16_t> : k_row_stats<float>,
-                       dim3((unsigned)blocks), dim3(kT), s, v, o, slices);
+hipError_t row_stats(const LogitsView& v, const RowOut& o, int slices, hipStream_t s,
+                     int* count = nullptr, int* seq = nullptr) {
+  // (one at least, which sets the counter)
+  const int64_t blocks = (v.rows > 0 ? v.rows * slices : 1) + (count ? v.nseq : 0);
+  return launch_kernel(v.bf16 ? k_row_stats<uint16_t, kT> : k_row_stats<float, kT>,
+                       dim3((unsigned)blocks), dim3(kT), s, v, o, slices, count, seq);
 }
 
 }  // namespace
@@ -813,7 +833,20 @@ int64_t row_grad_slices(int64_t vocab, int bf16) {
   return ceil_div(row_chunks(vocab, bf16), (int64_t)kT * kBatch);
 }
 
+// Rows that half fill the chip or fill it twice go whole to workgroups of 1024
+// threads, not in slices that a second launch joins: 256 rows of 32000 bf16 in
+// 8.0 us against 13.0, 512 in 12.2 against 13.4, 256 of 128256 in 15.3 against
+// 20.1.  With 16 rows of 128256 a workgroup is too slow for a row (10.5 against
+// 7.0); rows of less than two loads a thread (9000 bf16) lose as much as they
+// gain, and so do the losses, whose own launch joins the slices.
+static bool whole_rows(const LogitsView& v) {
+  return v.rows >= 128 && v.rows <= 512 && row_chunks(v.vocab, v.bf16) >= 2048;
+}
+
 hipError_t launch_row_logp(const LogitsView& v, const RowOut& o, hipStream_t s) {
+  if (whole_rows(v))
+    return launch_kernel(v.bf16 ? k_row_stats<uint16_t, 1024> : k_row_stats<float, 1024>,
+                         dim3((unsigned)v.rows), dim3(1024), s, v, o, 1, nullptr, nullptr);
   const int slices = row_slices(v);
   hipError_t e = row_stats(v, o, slices, s);
   if (e == hipSuccess && slices > 1)
@@ -859,15 +892,16 @@ static hipError_t policy_rows_of(const LogitsView& v, const RowOut& o, const Pol
   return policy_rows<T, 1024, 16>(v, o, a, dz, ldd, s);
 }
 // The one-pass form where a row fits in registers and is long enough to be worth
-// a workgroup (16 KB), the rows fill the chip, and the gradient's rows start
-// where the logits' do between 16-byte boundaries.  Whole calls over 128,256
-// bf16 logits, one pass against two: 43 and 38 us at 128 rows, 48 and 54 at 256,
-// 206 and 251 at 2048; over 32,000 26 and 29, 28 and 35, 64 and 78.
+// a workgroup (32 KB), the rows fill the chip, and the gradient's rows start
+// where the logits' do between 16-byte boundaries.  Whole calls, one pass against
+// two: over 128,256 bf16 logits 42 and 34 us at 128 rows, 48 and 50 at 256, 208
+// and 249 at 2048; over 32,000 26 and 23, 28 and 31, 65 and 74; over 9,000 25 and
+// 23 at 256 rows, 42 and 40 at 2048.
 static bool one_pass(const LogitsView& v, const void* dz, int64_t ldd) {
   const int64_t chunks = row_chunks(v.vocab, v.bf16);
   const uintptr_t apart =
       ((uintptr_t)dz - (uintptr_t)v.z) | (uintptr_t)((ldd - v.ld) * (v.bf16 ? 2 : 4));
-  return chunks >= 1024 && chunks <= 1024 * 16 && v.rows >= 256 && (apart & 15) == 0;
+  return chunks >= 2048 && chunks <= 1024 * 16 && v.rows >= 256 && (apart & 15) == 0;
 }
 
 hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs& a, void* dz,
@@ -875,15 +909,15 @@ hipError_t launch_policy(const LogitsView& v, const RowOut& o, const PolicyArgs&
   const bool fused = dz && one_pass(v, dz, ldd);
   // (0 slices: the statistics are there, logp is not)
   const int slices = fused ? 0 : row_slices(v);
-  hipError_t e =
-      launch_kernel(k_policy_count, dim3((unsigned)v.nseq + (fused ? 1 : 0)), dim3(kSeqT), s, v, o,
-                    a);
-  if (e != hipSuccess) return e;
-  if (fused)
-    e = v.bf16 ? policy_rows_of<uint16_t>(v, o, a, dz, ldd, s)
-               : policy_rows_of<float>(v, o, a, dz, ldd, s);
-  else
-    e = row_stats(v, o, slices, s);
+  hipError_t e;
+  if (fused) {
+    e = launch_kernel(k_policy_count, dim3((unsigned)v.nseq + 1), dim3(kSeqT), s, v, o, a);
+    if (e == hipSuccess)
+      e = v.bf16 ? policy_rows_of<uint16_t>(v, o, a, dz, ldd, s)
+                 : policy_rows_of<float>(v, o, a, dz, ldd, s);
+  } else {
+    e = row_stats(v, o, slices, s, a.count, a.seq);
+  }
   if (e == hipSuccess)
     e = launch_kernel(k_policy, dim3((unsigned)v.nseq), dim3(kSeqT), s, v, o, a, slices);
   if (e == hipSuccess && dz && !fused)

@@ -548,10 +548,10 @@ qlora_status qlora_grouped_bwd_act8(const qlora_nf4_tensor* W, const qlora_act8*
  *
  * Sequence i of a packed batch is rows cu_seqlens[i] .. cu_seqlens[i+1] - 1
  * (int32 [sequences + 1], device, ascending from >= 0 to <= rows; a value
- * outside is clamped), fewer than 2^22 of them.  Empty sequences are allowed.
- * Rows in no sequence (padding before the first or behind the last) count as
- * rows without target, whatever their label: their logp is 0 and their gradient
- * zero. */
+ * outside is clamped), fewer than 2^22 of them and with the rows fewer than
+ * 2^24.  Empty sequences are allowed.  Rows in no sequence (padding before the
+ * first or behind the last) count as rows without target, whatever their label:
+ * their logp is 0 and their gradient zero. */
 typedef struct {
   const void* data;        /* device, [rows] x ld; may be NULL when rows == 0 */
   qlora_dtype dtype;       /* QLORA_F32 or QLORA_BF16 */

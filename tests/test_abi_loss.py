@@ -130,3 +130,11 @@ def test_binding_refusals():
     _raises(q.qlora_policy_loss, z, y, cu, torch.zeros(4))          # per token only when asked
     _raises(q.qlora_policy_loss, z, y, cu, torch.zeros(2), token_advantages=True)
     _raises(q.qlora_policy_loss, z, y, cu, torch.zeros(2), reduction="mean")
+
+
+def test_rows_and_sequences_share_a_grid():
+    z = _z(rows=(1 << 24) - 2)
+    want = q.QLORA_ERR_UNSUPPORTED
+    assert _pref(z, pairs=1) == want and _pol(z, n=2) == want
+    assert q.lib().qlora_loss_workspace_bytes(ctypes.byref(z), 2) == 0
+    assert q.lib().qlora_loss_workspace_bytes(ctypes.byref(z), 1) > 0

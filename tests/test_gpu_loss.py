@@ -86,6 +86,26 @@ def test_token_logprobs_and_backward(T, V, dtype, pad):
     assert torch.equal(d, q.qlora_token_logprobs_bwd(z, y, stats, w, grad_scale=g))
 
 
+@pytest.mark.parametrize("T,V,dtype,pad", [
+    (128, 16385, BF, 0), (200, 16391, BF, 1), (127, 16384, BF, 0), (512, 17000, BF, 0),
+    (513, 16384, BF, 0), (129, 8193, F32, 0), (256, 32003, F32, 5), (140, 131073, BF, 2)])
+def test_rows_given_whole_to_a_workgroup(T, V, dtype, pad):
+    say("whole rows T=%d V=%d %s pad=%d" % (T, V, dtype, pad))
+    z, y = _logits(T + V, T, V, dtype, pad)
+    z[3, : V // 2] = -math.inf
+    z[5] = -math.inf
+    z[7, V - 1] = math.nan
+    y[3], y[5], y[7], y[9] = V - 1, 1, 2, V
+    logp, stats = q.qlora_token_logprobs(z, y, return_stats=True)
+    ref, _ = oloss.token_logprobs(_np(z), _np(y).astype(int))
+    _check_logp(logp, ref, V)
+    assert torch.isnan(logp[[5, 7, 9]]).all()
+    # the launch that a loss makes of the same rows
+    cu = torch.tensor([0, T // 2, T], dtype=torch.int32, device=DEV)
+    o = q.qlora_preference_loss(z, y, cu, stats=torch.empty_like(stats))
+    _check_logp(o.logp, ref, V)
+
+
 @pytest.mark.parametrize("dtype,V", [(BF, 1000), (BF, 1003), (F32, 999)])
 def test_gradient_in_place_and_with_another_stride(dtype, V):
     say("dlogits in place, V=%d %s" % (V, dtype))
@@ -454,3 +474,42 @@ def test_a_training_step_end_to_end():
     q.qlora_adamw_step(masters, 1, 1e-2)
     assert all(not torch.equal(u, v.detach()) for u, v in zip(before, (a, b)))
     assert all(torch.isfinite(v).all() for v in (a, b))
+
+
+@pytest.mark.parametrize("lens,lead,tail,V,dtype", [
+    ([131, 0, 127], 0, 3, 12003, F32), ([150, 107], 1, 0, 16384, BF), ([150, 107], 0, 0, 16376, BF)])
+@pytest.mark.parametrize("reduction,kl,token_adv,old", [("token", 0.05, True, True),
+                                                        ("sequence", 0.0, False, False)])
+def test_policy_where_one_pass_begins(lens, lead, tail, V, dtype, reduction, kl, token_adv, old):
+    test_policy(lens, lead, tail, V, dtype, reduction, kl, token_adv, old)
+
+
+def test_policy_in_one_pass_replayed():
+    say("policy loss in one pass: graph")
+    T, V = 300, 17000
+    z, y, cu = _packed(9, [T // 2, 0, T // 2], 0, 0, V, BF)
+    adv = torch.tensor([0.5, 1.0, -1.5], device=DEV)
+    lp = q.qlora_token_logprobs(z, y)
+
+    def step():
+        b = q.qlora_policy_loss(z, y, cu, adv, lp + 0.1, lp - 0.2, kl_coef=0.1, return_grad=True)
+        return [b.loss, b.kl, b.clip_frac, b.logp, b.dlogits]
+
+    want = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step()
+    side.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(want, got))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for _ in range(3):
+        for t in out:
+            t.fill_(7)
+        torch.randn(1 << 18, device=DEV).sum().item()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(want, out))
+        assert all(torch.equal(u, v) for u, v in zip(want, step()))
