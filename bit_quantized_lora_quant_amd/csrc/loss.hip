@@ -152,24 +152,28 @@ __device__ __forceinline__ F wave_sum(F x) {
 }
 
 // Joins the threads' parts of a row in a fixed order; the result in every
-// thread.  red: 2 floats for each wave.
-template <int W>
-__device__ __forceinline__ MaxSum wg_join(MaxSum a, float (*red)[2]) {
+// thread, its sum also in float64 (`sum`): what is rounded once a thread comes
+// out in the mean, what the last few additions round does not, and a sequence's
+// log ratio or a KL term is small against its rows' logp.  S: float where
+// the registers are short.
+template <int W, typename S = double>
+__device__ __forceinline__ MaxSum wg_join(MaxSum a, S (*red)[2], S* sum = nullptr) {
   const int wv = threadIdx.x >> 6;
   float m = wave_max(a.m);
   if ((threadIdx.x & 63) == 0) red[wv][0] = m;
   __syncthreads();
-  m = red[0][0];
+  m = (float)red[0][0];
 #pragma unroll
-  for (int w = 1; w < W; ++w) m = fmaxf(m, red[w][0]);
+  for (int w = 1; w < W; ++w) m = fmaxf(m, (float)red[w][0]);
   // a thread without values has m = -inf and s = 0 (or NaN, which stays)
-  const float s = wave_sum(a.m == m ? a.s : a.s * exp_exact(a.m - m));
+  const S s = wave_sum((S)(a.m == m ? a.s : a.s * exp_exact(a.m - m)));
   if ((threadIdx.x & 63) == 0) red[wv][1] = s;
   __syncthreads();
-  float t = red[0][1];
+  S t = red[0][1];
 #pragma unroll
   for (int w = 1; w < W; ++w) t += red[w][1];
-  return MaxSum{m, t};
+  if (sum) *sum = t;
+  return MaxSum{m, (float)t};
 }
 
 // What turns a logit into its gradient: k exp(z - m), k = -w / sum, and + w at
@@ -323,7 +327,7 @@ __device__ __forceinline__ void count_sequence(const LogitsView& v, int i, int* 
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void k_row_stats(LogitsView v, RowOut o, int slices,
                                                   int* count, int* seq) {
-  __shared__ float red[NT / 64][2];
+  __shared__ double red[NT / 64][2];
   if (blockIdx.x == 0 && threadIdx.x == 0 && o.ticket) *o.ticket = 0;
   unsigned b = blockIdx.x;
   if (count) {
@@ -373,7 +377,8 @@ __global__ __launch_bounds__(NT) void k_row_stats(LogitsView v, RowOut o, int sl
   }
   if (failed(a)) sum_again<T>(a, r, c0 + tid, c1, NT);
   if (sl == 0 && tid < r.edge) add_value(a, ld1(r.z + r.edge_at(tid)));
-  a = wg_join<NT / 64>(a, red);
+  double sum;
+  a = wg_join<NT / 64>(a, red, &sum);
   if (threadIdx.x != 0) return;
   const float zy = ld1(r.z + y);
   if (sl == 0) o.zy[t] = zy;
@@ -381,7 +386,7 @@ __global__ __launch_bounds__(NT) void k_row_stats(LogitsView v, RowOut o, int sl
     o.part[t * slices + sl] = a;
   } else {
     o.stats[t] = a;
-    o.logp[t] = (float)((double)zy - (double)a.m - std::log((double)a.s));
+    o.logp[t] = (float)((double)zy - (double)a.m - std::log(sum));
   }
 }
 
@@ -392,6 +397,7 @@ __device__ __forceinline__ double row_logp(const LogitsView& v, const RowOut& o,
   const int64_t y = v.labels[t];
   if (y >= v.vocab) return (double)__builtin_nanf("");   // written with the statistics
   MaxSum a;
+  double s = 0;
   if (slices > 1) {
     const MaxSum* p = o.part + t * slices;
     // (a thread has this to itself: its loads go out 16 at a time)
@@ -400,7 +406,7 @@ __device__ __forceinline__ double row_logp(const LogitsView& v, const RowOut& o,
 #pragma unroll
       for (int i = 0; i < 16; ++i) q[i] = p[i0 + i < slices ? i0 + i : slices - 1];
     };
-    float m = -kInf, s = 0.f;
+    float m = -kInf;
     for (int i0 = 0; i0 < slices; i0 += 16) {
       load(i0);
 #pragma unroll
@@ -412,12 +418,13 @@ __device__ __forceinline__ double row_logp(const LogitsView& v, const RowOut& o,
       for (int i = 0; i < 16; ++i)
         s += i0 + i >= slices ? 0.f : q[i].m == m ? q[i].s : q[i].s * exp_exact(q[i].m - m);
     }
-    a = MaxSum{m, s};
+    a = MaxSum{m, (float)s};
     o.stats[t] = a;
   } else {
     a = o.stats[t];
+    s = a.s;
   }
-  const double l = (double)o.zy[t] - (double)a.m - std::log((double)a.s);
+  const double l = (double)o.zy[t] - (double)a.m - std::log(s);
   if (slices != 1) o.logp[t] = (float)l;
   return l;
 }
@@ -772,7 +779,7 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
     if (mine <= 0) s = MaxSum{-kInf, 0.f};
     if (failed(s)) sum_again<T>(s, r, tid, r.nb, NT);
     if (tid < r.edge) add_value(s, ze);
-    s = wg_join<NT / 64>(s, red);
+    s = wg_join<NT / 64, float>(s, red);
     if (tid == 0) {
       o.stats[t] = s;
       o.zy[t] = zy;
