@@ -700,7 +700,7 @@ __global__ __launch_bounds__(kSeqT) void k_policy(LogitsView v, RowOut o, Policy
 // CU's registers).  The workgroups are persistent and the memory never waits
 // for arithmetic: as a chunk's gradient is stored its registers take the same
 // chunk of the workgroup's next row, and the sums run over four chunks at a
-// time as they arrive.  1.85 GB in 365 us (4096 x 128256), 5.0 TB/s; as two
+// time as they arrive.  1.85 GB in 370 us (4096 x 128256), 5.0 TB/s; as two
 // launches 445.  The weight is formed in float32 here (the logits'
 // gradient has no more); logp and the loss come from the statistics after.
 template <typename T, int NT, int NC>
