@@ -31,11 +31,6 @@ __device__ __forceinline__ float exp_f32(float d) {
   return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kL2eLow, d * kL2e));
 }
 
-// exp(d) of either sign
-__device__ __forceinline__ float exp_any(float d) {
-  return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kL2eLow, d * kL2e));
-}
-
 // The same to within v_exp_f32's own error, whatever the argument's size: what
 // the product d log2(e) was rounded by comes back as a factor.
 __device__ __forceinline__ float exp_exact(float d) {
@@ -639,18 +634,29 @@ __device__ __forceinline__ double share_of(const PolicyArgs& a, const Totals& n,
 struct Term {
   double loss, kl, clipped, dlogp;
 };
-__device__ __forceinline__ Term policy_term(const PolicyArgs& a, double l, double A, int64_t t) {
-  const double r = a.old_logp ? std::exp(l - (double)a.old_logp[t]) : (l == l ? 1.0 : l);
+// The exponents of the ratio and of the KL term, logp = l.
+struct Exponents {
+  double ratio, kl;
+};
+__device__ __forceinline__ Exponents policy_exponents(const PolicyArgs& a, double l, int64_t t) {
+  return Exponents{a.old_logp ? l - (double)a.old_logp[t] : (l == l ? 0.0 : l),
+                   a.ref ? (double)a.ref[t] - l : 0.0};
+}
+// The term of a target, from its exponents x and r = exp(x.ratio), e = exp(x.kl).
+// e - 1 is off by 2^-53, far less than e moves by with what logp is off by (3e-8),
+// however small x.kl is.
+__device__ __forceinline__ Term policy_term(const PolicyArgs& a, double A, const Exponents& x,
+                                            double r, double e) {
   const double u = -A * r, c = -A * (r < a.lo ? a.lo : r > a.hi ? a.hi : r);
   const bool cut = c > u;
-  Term x{cut ? c : u, 0.0, cut ? 1.0 : 0.0, cut ? 0.0 : u};
+  Term y{cut ? c : u, 0.0, cut ? 1.0 : 0.0, cut ? 0.0 : u};
   if (a.ref) {
-    const double d = (double)a.ref[t] - l, em = std::expm1(d);
-    x.kl = em - d;
-    x.loss += a.kl_coef * x.kl;
-    x.dlogp -= a.kl_coef * em;
+    const double em = e - 1;
+    y.kl = em - x.kl;
+    y.loss += a.kl_coef * y.kl;
+    y.dlogp -= a.kl_coef * em;
   }
-  return x;
+  return y;
 }
 
 // Workgroup per sequence; the last one adds the sequences' sums in their order.
@@ -667,7 +673,8 @@ __global__ __launch_bounds__(kSeqT) void k_policy(LogitsView v, RowOut o, Policy
       continue;
     }
     const double A = (double)(a.token_adv ? a.adv[t] : a.adv[i]);
-    const Term x = policy_term(a, row_logp(v, o, slices, t), A, t);
+    const Exponents d = policy_exponents(a, row_logp(v, o, slices, t), t);
+    const Term x = policy_term(a, A, d, std::exp(d.ratio), std::exp(d.kl));
     sum[0] += x.loss;
     sum[1] += x.kl;
     sum[2] += x.clipped;
@@ -691,6 +698,17 @@ __global__ __launch_bounds__(kSeqT) void k_policy(LogitsView v, RowOut o, Policy
   }
 }
 
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ float uniform(float x) {
+  return __builtin_bit_cast(float, uniform(__builtin_bit_cast(int, x)));
+}
+__device__ __forceinline__ double uniform(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint64_t lo = (uint32_t)uniform((int)(uint32_t)b), hi = (uint32_t)uniform((int)(b >> 32));
+  return __builtin_bit_cast(double, hi << 32 | lo);
+}
+
 // ------------------------------------------- policy loss in one pass
 // The weight of a row hangs on that row's logp and on counts known from the
 // labels, so a workgroup can hold its row in registers from the maximum to the
@@ -701,23 +719,29 @@ __global__ __launch_bounds__(kSeqT) void k_policy(LogitsView v, RowOut o, Policy
 // for arithmetic: as a chunk's gradient is stored its registers take the same
 // chunk of the workgroup's next row, and the sums run over four chunks at a
 // time as they arrive.  1.85 GB in 370 us (4096 x 128256), 5.0 TB/s; as two
-// launches 445.  The weight is formed in float32 here (the logits'
-// gradient has no more); logp and the loss come from the statistics after.
+// launches 445.  logp, weight and loss are formed after, from the same
+// statistics; here one wave forms the weight for the gradient, with the same
+// float64 operations, so that both say of a ratio next to a border whether it is
+// clipped.  What is the same in all lanes is kept in scalar registers: a row's
+// float64 constants beside it would spill (22 registers), and with more than 128
+// a CU would hold fewer workgroups (64,000 bf16 logits, 512 threads: 132 us
+// instead of 115 at 2048 rows).
 template <typename T, int NT, int NC>
-__global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, PolicyArgs a, T* dz,
-                                                    int64_t ldd) {
-  __shared__ float red[NT / 64][2];
+__global__ __launch_bounds__(NT, 4) void k_policy_rows(LogitsView v, RowOut o, PolicyArgs a, T* dz,
+                                                       int64_t ldd) {
+  __shared__ float red[NT / 64][2], row_w;
   __shared__ double dred[NT / 64][2];
   constexpr int kSum = 4;                       // chunks summed at a time
-  const Totals n = totals<NT>(a, v.nseq, dred);
+  Totals n = totals<NT>(a, v.nseq, dred);
+  n = Totals{uniform(n.targets), uniform(n.filled)};
   const int64_t step = gridDim.x;
   auto has_target = [&](int64_t t) {
     const int64_t y = v.labels[t];
     return y >= 0 && y < v.vocab && !outside(v, t);
   };
   // every step-th of the rows with a target: as many for each workgroup, to one
-  const int rows_with = a.list[v.rows];
-  auto listed = [&](int64_t k) { return k < rows_with ? (int64_t)a.list[k] : v.rows; };
+  const int rows_with = uniform(a.list[v.rows]);
+  auto listed = [&](int64_t k) { return k < rows_with ? (int64_t)uniform(a.list[k]) : v.rows; };
   auto store = [&](T* d, int head, int k, const uint4& q) {
     __builtin_nontemporal_store(
         __builtin_bit_cast(u32x4_t, q),
@@ -765,11 +789,10 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
     const int64_t tn = listed(k0);
     const Row<T> r(v, t), rn(v, tn < v.rows ? tn : t);
     const int nbn = tn < v.rows ? rn.nb : 1;    // (without a next row one chunk, unused)
-    const int64_t y = v.labels[t];
-    const int sq = a.seq[t];
-    const float A = a.token_adv ? a.adv[t] : a.adv[sq];
-    const float share = (float)share_of(a, n, sq);
-    const float old_logp = a.old_logp ? a.old_logp[t] : 0.f, ref = a.ref ? a.ref[t] : 0.f;
+    const int64_t y = uniform((int)v.labels[t]);
+    const int sq = uniform(a.seq[t]);
+    const double A = (double)uniform(a.token_adv ? a.adv[t] : a.adv[sq]);
+    const double share = uniform(share_of(a, n, sq));
     // this thread's chunks; loads past a row's end repeat its last one
     const int mine = (r.nb - tid + NT - 1) / NT;
     MaxSum s{-kInf, 0.f};
@@ -780,17 +803,22 @@ __global__ __launch_bounds__(NT) void k_policy_rows(LogitsView v, RowOut o, Poli
     if (failed(s)) sum_again<T>(s, r, tid, r.nb, NT);
     if (tid < r.edge) add_value(s, ze);
     s = wg_join<NT / 64, float>(s, red);
+    s = MaxSum{uniform(s.m), uniform(s.s)};
     if (tid == 0) {
       o.stats[t] = s;
       o.zy[t] = zy;
     }
-    const float l = (zy - s.m) - 0.6931472f * __builtin_amdgcn_logf(s.s);
-    const float ratio = a.old_logp ? exp_any(l - old_logp) : (l == l ? 1.f : l);
-    const float lo = (float)a.lo, hi = (float)a.hi;
-    const float u = -A * ratio, c = -A * (ratio < lo ? lo : ratio > hi ? hi : ratio);
-    float w = c > u ? 0.f : u;
-    if (a.ref) w -= (float)a.kl_coef * (exp_any(ref - l) - 1.f);
-    w *= share;
+    // the weight as k_policy forms it after this launch, from the same statistics;
+    // two lanes of a wave take an exponential each
+    if (tid < 64) {
+      const Exponents x =
+          policy_exponents(a, (double)zy - (double)s.m - std::log((double)s.s), t);
+      const double e = std::exp(tid & 1 ? x.kl : x.ratio);
+      const Term term = policy_term(a, A, x, __shfl(e, 0), __shfl(e, 1));
+      if (tid == 0) row_w = (float)(share * term.dlogp);
+    }
+    __syncthreads();
+    const float w = uniform(row_w);
     const GradOf<T> grad(s, w);
     const int yb = (int)y - r.head;
     T* const d = dz + t * ldd;

@@ -623,10 +623,8 @@ qlora_status qlora_preference_loss(const qlora_logits* z, int32_t pairs, const i
  * averaged over all targets (TOKEN) or over each sequence's targets and then
  * over the sequences that have any (SEQUENCE).  No gradient flows through
  * the clamp where it is the larger.  0 when there is no target.  Terms and
- * their means are float64; a row's weight dLoss / dlogp is float64 too, rounded
- * once, except where a call with dlogits reads the logits only once (many rows
- * of a vocabulary's length that fits a workgroup's registers): there it is
- * formed in float32. */
+ * their means are float64, and a row's weight dLoss / dlogp is float64 too,
+ * rounded once: dlogits has the weights that w receives. */
 #define QLORA_POLICY_TOKEN 0
 #define QLORA_POLICY_SEQUENCE 1
 typedef struct {
