@@ -644,17 +644,21 @@ __device__ __forceinline__ Exponents policy_exponents(const PolicyArgs& a, doubl
 }
 // The term of a target, from its exponents x and r = exp(x.ratio), e = exp(x.kl).
 // e - 1 is off by 2^-53, far less than e moves by with what logp is off by (3e-8),
-// however small x.kl is.
+// however small x.kl is.  An advantage or coefficient of 0 adds 0 to an infinite
+// ratio or divergence too (a masked target has logp -inf).
 __device__ __forceinline__ Term policy_term(const PolicyArgs& a, double A, const Exponents& x,
                                             double r, double e) {
-  const double u = -A * r, c = -A * (r < a.lo ? a.lo : r > a.hi ? a.hi : r);
+  const double u = A == 0 && r == r ? 0.0 : -A * r;
+  const double c = -A * (r < a.lo ? a.lo : r > a.hi ? a.hi : r);
   const bool cut = c > u;
   Term y{cut ? c : u, 0.0, cut ? 1.0 : 0.0, cut ? 0.0 : u};
   if (a.ref) {
     const double em = e - 1;
-    y.kl = em - x.kl;
-    y.loss += a.kl_coef * y.kl;
-    y.dlogp -= a.kl_coef * em;
+    y.kl = em < (double)kInf ? em - x.kl : em;   // (NaN stays)
+    if (a.kl_coef > 0) {
+      y.loss += a.kl_coef * y.kl;
+      y.dlogp -= a.kl_coef * em;
+    }
   }
   return y;
 }

@@ -622,7 +622,8 @@ qlora_status qlora_preference_loss(const qlora_logits* z, int32_t pairs, const i
  *            + kl_coef (exp(d) - d - 1),   d = ref_logp - logp,
  * averaged over all targets (TOKEN) or over each sequence's targets and then
  * over the sequences that have any (SEQUENCE).  No gradient flows through
- * the clamp where it is the larger.  0 when there is no target.  Terms and
+ * the clamp where it is the larger.  0 when there is no target.  An advantage or
+ * kl_coef of 0 adds 0, also to an infinite ratio or divergence.  Terms and
  * their means are float64, and a row's weight dLoss / dlogp is float64 too,
  * rounded once: dlogits has the weights that w receives. */
 #define QLORA_POLICY_TOKEN 0

@@ -1,0 +1,59 @@
+"""Losses whose log-probabilities are infinite, in a term that the call leaves
+out (a coefficient, smoothing or advantage of zero), and other products with
+zero: what is left out adds nothing."""
+import math
+
+import pytest
+import torch
+
+from gpu_common import DEV, say
+
+import bit_quantized_lora_quant_amd as q
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _rows(T, V, dtype):
+    g = torch.Generator().manual_seed(T + V)
+    z = (2 * torch.randn((T, V), generator=g)).to(dtype).to(DEV)
+    return z, torch.randint(0, V, (T,), generator=g).to(DEV)
+
+
+# two launches, and one pass over the rows
+FORMS = [(40, 500, F32), (40, 501, BF), (300, 16500, BF), (270, 9001, F32)]
+
+
+@pytest.mark.parametrize("T,V,dtype", FORMS)
+@pytest.mark.parametrize("low", [-math.inf, None])
+def test_policy_with_a_masked_target_and_a_reference_that_is_only_watched(T, V, dtype, low):
+    say("policy, masked target, kl_coef 0, T=%d V=%d %s" % (T, V, dtype))
+    z, y = _rows(T, V, dtype)
+    cu = torch.tensor([0, T // 2, T], dtype=torch.int32, device=DEV)
+    adv = torch.tensor([1.0, -0.5], device=DEV)
+    old = q.qlora_token_logprobs(z, y)
+    for t in (3, T - 2):
+        z[t, y[t]] = torch.finfo(dtype).min if low is None else low
+    w, alone = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    want = q.qlora_policy_loss(z, y, cu, adv, old, return_grad=True, w=alone)
+    assert math.isfinite(float(want.loss))
+    o = q.qlora_policy_loss(z, y, cu, adv, old, old, kl_coef=0.0, return_grad=True, w=w)
+    assert torch.equal(o.loss, want.loss) and torch.equal(w, alone)
+    assert torch.equal(o.dlogits, want.dlogits) and bool(torch.isfinite(o.dlogits).all())
+    assert float(o.kl) == math.inf
+    # and where the term counts it is infinite, not undefined
+    assert float(q.qlora_policy_loss(z, y, cu, adv, old, old, kl_coef=0.1).loss) == math.inf
+
+
+@pytest.mark.parametrize("T,V,dtype", FORMS)
+def test_policy_without_advantage_of_a_token_its_sampler_ruled_out(T, V, dtype):
+    say("policy, advantage 0, infinite ratio, T=%d V=%d %s" % (T, V, dtype))
+    z, y = _rows(T, V, dtype)
+    cu = torch.tensor([0, T // 2, T], dtype=torch.int32, device=DEV)
+    old = q.qlora_token_logprobs(z, y)
+    old[5] = -math.inf
+    o = q.qlora_policy_loss(z, y, cu, torch.tensor([0.0, 0.0], device=DEV), old, return_grad=True)
+    assert float(o.loss) == 0 and not o.dlogits.any()
+    # a positive advantage meets the upper clip
+    o = q.qlora_policy_loss(z, y, cu, torch.tensor([1.0, 0.0], device=DEV), old, return_grad=True)
+    assert math.isfinite(float(o.loss)) and not o.dlogits[5].any() and o.dlogits[4].any()
