@@ -552,7 +552,8 @@ __global__ __launch_bounds__(kSeqT) void k_preference(LogitsView v, RowOut o, Pr
     const double ln = u + (x < 0 ? -x : 0), lp = u + (x > 0 ? x : 0);
     const double sp = x >= 0 ? 1 / (1 + ex) : ex / (1 + ex);
     const double sn = x >= 0 ? ex / (1 + ex) : 1 / (1 + ex);
-    loss = (1 - a.smooth) * ln + a.smooth * lp;
+    // (without smoothing, a pair won by infinity has no loss)
+    loss = (1 - a.smooth) * ln + (a.smooth > 0 ? a.smooth * lp : 0.0);
     dh = -a.beta * ((1 - a.smooth) * sn - a.smooth * sp);
     if (x != x) loss = dh = x;
   } else if (a.kind == 1) {

@@ -57,3 +57,26 @@ def test_policy_without_advantage_of_a_token_its_sampler_ruled_out(T, V, dtype):
     # a positive advantage meets the upper clip
     o = q.qlora_policy_loss(z, y, cu, torch.tensor([1.0, 0.0], device=DEV), old, return_grad=True)
     assert math.isfinite(float(o.loss)) and not o.dlogits[5].any() and o.dlogits[4].any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge"])
+def test_preference_without_smoothing_of_an_answer_ruled_out(dtype, kind):
+    """The other answer of pair 0 holds a masked token: its log ratio is -inf, the
+    pair is won, its loss and gradient 0."""
+    say("preference, infinite log ratio, %s %s" % (kind, dtype))
+    z, y = _rows(24, 700, dtype)
+    cu = torch.tensor([0, 6, 12, 18, 24], dtype=torch.int32, device=DEV)
+    ref = q.qlora_token_logprobs(z, y)
+    half = q.qlora_preference_loss(z[12:], y[12:], cu[:3], ref[12:], 0.2, kind, return_grad=True)
+    z[8, y[8]] = -math.inf
+    o = q.qlora_preference_loss(z, y, cu, ref, 0.2, kind, return_grad=True)
+    assert float(o.loss) == pytest.approx(float(half.loss) / 2, rel=2.0 ** -22)
+    assert not o.dlogits[:12].any() and o.dlogits[12:].any()
+    assert bool(torch.isfinite(o.dlogits).all()) and float(o.rewards[1]) == -math.inf
+    # the pair lost, and the pair won with smoothing: infinite, not undefined
+    swap = torch.cat((torch.arange(6, 12), torch.arange(6), torch.arange(12, 24))).to(DEV)
+    lost = q.qlora_preference_loss(z[swap], y[swap], cu, ref[swap], 0.2, kind)
+    assert float(lost.loss) == math.inf
+    if kind == "sigmoid":
+        assert float(q.qlora_preference_loss(z, y, cu, ref, 0.2, kind, 0.1).loss) == math.inf
