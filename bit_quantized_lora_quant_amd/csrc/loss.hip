@@ -171,17 +171,20 @@ __device__ __forceinline__ MaxSum wg_join(MaxSum a, S (*red)[2], S* sum = nullpt
   return MaxSum{m, (float)t};
 }
 
-// What turns a logit into its gradient: k exp(z - m), k = -w / sum, and + w at
-// the target.  A bf16 gradient takes k into the exponent (one multiply-add; its
-// argument's rounding, a few 2^-24, is far below half a bf16 step), a float32
-// one keeps the exponential apart.
+// What turns a logit into its gradient: k exp(z - m), k = -w / sum.  A bf16
+// gradient takes k into the exponent (one multiply-add; its argument is of the
+// size of 20 at most where the value is not small, and its rounding then 2^-20,
+// against a half bf16 step of 2^-8), a float32 one keeps the exponential apart.
+// The target's is w (1 - p), formed as (w / sum) (sum - exp(z - m)): the
+// difference is exact where p is next to 1 and what it leaves is small, so all of
+// its error is the sum's own, where w - w p would bring p's rounding with it.
 template <typename T>
 struct GradOf {
-  float m, w, k;
-  uint32_t flip;           // bf16: k = log2 |w / sum|, flip: the sign of -w
-  __device__ __forceinline__ GradOf(const MaxSum& a, float w_) : m(a.m), w(w_), k(-w_ / a.s) {
-    flip = w_ > 0.f ? 0x80008000u : 0u;
-    if constexpr (sizeof(T) == 2) k = __builtin_amdgcn_logf(__builtin_fabsf(w_ / a.s));
+  float m, s, ws, k;       // ws = w / sum
+  uint32_t flip;           // bf16: k = log2 |ws|, flip: the sign of -w
+  __device__ __forceinline__ GradOf(const MaxSum& a, float w) : m(a.m), s(a.s), ws(w / a.s), k(-ws) {
+    flip = w > 0.f ? 0x80008000u : 0u;
+    if constexpr (sizeof(T) == 2) k = __builtin_amdgcn_logf(__builtin_fabsf(ws));
   }
   // bf16: its magnitude
   __device__ __forceinline__ float value(float z) const {
@@ -190,20 +193,24 @@ struct GradOf {
     else
       return k * exp_f32(z - m);
   }
+  // the target's
+  __device__ __forceinline__ float target(float z) const { return ws * (s - exp_exact(z - m)); }
   __device__ __forceinline__ float signed_value(float z) const {
     const float x = value(z);
     return sizeof(T) == 2 && flip ? -x : x;
   }
-  // chunk `at` of a row whose target is body value yb
-  __device__ __forceinline__ uint4 chunk(const uint4& q, int at, int yb) const {
+  // chunk `at` of a row whose target is body value yb; ty() its gradient
+  template <typename F>
+  __device__ __forceinline__ uint4 chunk(const uint4& q, int at, int yb, F ty) const {
     float f[vec<T>()];
     unpack<T>(q, f);
 #pragma unroll
     for (int e = 0; e < vec<T>(); ++e) f[e] = value(f[e]);
     if ((unsigned)(yb - at * vec<T>()) < (unsigned)vec<T>()) {
-      const float add = sizeof(T) == 2 ? -__builtin_fabsf(w) : w;
+      float t = ty();
+      if (sizeof(T) == 2 && flip) t = -t;        // (flipped back below)
 #pragma unroll
-      for (int e = 0; e < vec<T>(); ++e) f[e] += at * vec<T>() + e == yb ? add : 0.f;
+      for (int e = 0; e < vec<T>(); ++e) f[e] = at * vec<T>() + e == yb ? t : f[e];
     }
     uint4 o = pack<T>(f);
     if constexpr (sizeof(T) == 2) {
@@ -477,11 +484,18 @@ __global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const MaxSum* sta
     const int at = c0 + kT * i;
     if (at >= r.nb) continue;
     forget(q[i]);
-    store(at, grad.chunk(q[i], at, yb));
+    store(at, grad.chunk(q[i], at, yb, [&] {   // (z_y is in this chunk; the row may be gone)
+      float f[vec<T>()], zy = 0.f;
+      unpack<T>(q[i], f);
+#pragma unroll
+      for (int e = 0; e < vec<T>(); ++e) zy = at * vec<T>() + e == yb ? f[e] : zy;
+      return grad.target(zy);
+    }));
   }
   if (at_edge) {
     const int at = r.edge_at(threadIdx.x);
-    st1(d + at, grad.signed_value(ld1(r.z + at)) + (at == y ? c : 0.f));
+    const float z = ld1(r.z + at);
+    st1(d + at, at == y ? grad.target(z) : grad.signed_value(z));
   }
 }
 
@@ -825,6 +839,7 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(LogitsView v, RowOut o, P
     __syncthreads();
     const float w = uniform(row_w);
     const GradOf<T> grad(s, w);
+    const float ty = uniform(grad.target(zy));
     const int yb = (int)y - r.head;
     T* const d = dz + t * ldd;
     const float zt = ze;
@@ -833,12 +848,13 @@ __global__ __launch_bounds__(NT, 4) void k_policy_rows(LogitsView v, RowOut o, P
       const int at = tid + NT * i;
       forget(q[i]);
       if (at < r.nb)
-        store(d, r.head, at, w == 0.f ? make_uint4(0u, 0u, 0u, 0u) : grad.chunk(q[i], at, yb));
+        store(d, r.head, at, w == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                                      : grad.chunk(q[i], at, yb, [&] { return ty; }));
       q[i] = rn.chunk_once(at < nbn ? at : nbn - 1);
     }
     if (tid < r.edge) {
       const int at = r.edge_at(tid);
-      st1(d + at, w == 0.f ? 0.f : grad.signed_value(zt) + (at == y ? w : 0.f));
+      st1(d + at, w == 0.f ? 0.f : at == y ? ty : grad.signed_value(zt));
     }
     if (tn < v.rows) load_edge(rn, tn, tid);
     t = tn;
