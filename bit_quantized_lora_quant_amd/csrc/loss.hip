@@ -448,7 +448,8 @@ __global__ __launch_bounds__(kT) void k_row_grad(LogitsView v, const MaxSum* sta
   const int sl = (int)(blockIdx.x - tr * slices);
   const int64_t t = v.rows - 1 - tr;
   const int64_t y = v.labels[t];
-  const float c = y < 0 ? 0.f : w[t] * (g ? *g : 1.f);
+  const float wt = y < 0 ? 0.f : w[t];
+  const float c = wt == 0.f ? 0.f : wt * (g ? *g : 1.f);   // (0 whatever g is)
   const Row<T> r(v, t);
   T* const d = dz + t * ldd;
   const bool even = (((uintptr_t)d ^ (uintptr_t)r.z) & 15) == 0;   // 16-byte stores fit

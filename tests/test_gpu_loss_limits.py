@@ -80,3 +80,24 @@ def test_preference_without_smoothing_of_an_answer_ruled_out(dtype, kind):
     assert float(lost.loss) == math.inf
     if kind == "sigmoid":
         assert float(q.qlora_preference_loss(z, y, cu, ref, 0.2, kind, 0.1).loss) == math.inf
+
+
+@pytest.mark.parametrize("scale", [math.inf, math.nan])
+def test_rows_of_weight_zero_under_an_overflowed_upstream_gradient(scale):
+    say("weight 0, upstream gradient %s" % scale)
+    for V, dtype in ((700, BF), (701, F32)):
+        z, y = _rows(20, V, dtype)
+        z[3] = math.nan                                # not read
+        y[5], y[6] = -100, -1
+        _, stats = q.qlora_token_logprobs(z, y, return_stats=True)
+        w = torch.linspace(0.5, 1.0, 20, device=DEV)
+        w[[0, 3, 19]] = 0
+        d = q.qlora_token_logprobs_bwd(z, y, stats, w, grad_scale=torch.tensor([scale], device=DEV))
+        assert not d[[0, 3, 5, 6, 19]].any()
+        assert bool((~torch.isfinite(d[1])).any())
+        # padding rows of a loss, whose weights are zero
+        cu = torch.tensor([2, 9, 16], dtype=torch.int32, device=DEV)
+        leaf = torch.where(torch.isnan(z), 0, z).requires_grad_()
+        loss, _, _ = q.PreferenceLossFn.apply(leaf, y, cu)
+        (loss * scale).backward()
+        assert not leaf.grad[:2].any() and not leaf.grad[16:].any()
