@@ -369,21 +369,23 @@ hipError_t act8_grads_rt(const Act8GradJob& a, const GradJob& b, int64_t M, int 
 
 }  // namespace
 
+int64_t act8_tiles(int64_t rows, int64_t cols) {
+  return ceil_div(rows, kTileRows) * ceil_div(cols, kTileCols);
+}
+
 hipError_t launch_act8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes,
                                 float* scale, hipStream_t s) {
   const int64_t kb = cols / kBlock, rows32 = ceil_div(rows, 32) * 32;
-  const int64_t tk = ceil_div(cols, kTileCols);
-  return launch_kernel(k_act8_quantize, dim3((unsigned)(tk * (rows32 / kTileRows))), dim3(256), s,
-                       x, rows, rows32, kb, tk, codes, scale);
+  return launch_kernel(k_act8_quantize, dim3((unsigned)act8_tiles(rows, cols)), dim3(256), s, x,
+                       rows, rows32, kb, ceil_div(cols, kTileCols), codes, scale);
 }
 
 hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64_t rows,
                                   int64_t cols, int bf16, void* out, hipStream_t s) {
   const int64_t kb = cols / kBlock, rows32 = ceil_div(rows, 32) * 32;
-  const int64_t tk = ceil_div(cols, kTileCols);
   return launch_kernel(bf16 ? k_act8_dequantize<true> : k_act8_dequantize<false>,
-                       dim3((unsigned)(tk * (rows32 / kTileRows))), dim3(256), s, codes, scale,
-                       rows, rows32, kb, tk, out);
+                       dim3((unsigned)act8_tiles(rows, cols)), dim3(256), s, codes, scale, rows,
+                       rows32, kb, ceil_div(cols, kTileCols), out);
 }
 
 // About 192 workgroups (dB's fill the rest of the chip), at least two 32-token

@@ -209,10 +209,11 @@ bool valid_act8(const qlora_act8* a) {
          (a->rows == 0 || (a->codes && a->scale && aligned(a->codes, 16) && aligned(a->scale, 16)));
 }
 
-// Whole blocks, and at most 2^37 values of at most 2^26 to a row.
+// Whole blocks, at most 2^37 values of at most 2^26 to a row, and tiles that one
+// grid dimension holds.
 bool act8_fits(const qlora_act8* a) {
   return a->cols % kBlock == 0 && a->cols <= (int64_t)1 << 26 &&
-         a->rows <= (((int64_t)1 << 37) / a->cols);
+         a->rows <= (((int64_t)1 << 37) / a->cols) && act8_tiles(a->rows, a->cols) < (1 << 24);
 }
 
 // Kernel parameters of a dropout of an input with rows of K elements: keep

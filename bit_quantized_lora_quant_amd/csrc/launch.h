@@ -174,7 +174,10 @@ hipError_t launch_lora_grads(const GradJob* jobs, int njobs, int64_t M, int r, h
 hipError_t launch_lora_grad_reduce(const GradJob* jobs, int njobs, int r, hipStream_t s);
 
 // Checkpoints in 8 bits: codes int8 [rows, cols] and scales float32
-// [cols / 64][rows32] of X bf16 [rows, cols]; rows32 is rows up to 32.
+// [cols / 64][rows32] of X bf16 [rows, cols]; rows32 is rows up to 32.  A
+// workgroup of 256 threads per tile of act8_tiles, in one grid dimension: fewer
+// than 2^24.
+int64_t act8_tiles(int64_t rows, int64_t cols);
 hipError_t launch_act8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes,
                                 float* scale, hipStream_t s);
 hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64_t rows,

@@ -487,8 +487,9 @@ qlora_status qlora_host_state_free(void* ptr);
  * codes are [rows, cols] row-major; scale is [cols / 64][rows32], rows32 =
  * rows rounded up to a multiple of 32 (the gradient reads it along tokens),
  * zeros from rows to rows32.  Both 16-byte aligned, device memory owned by the
- * caller; cols a multiple of 64 and at most 2^26, rows * cols at most 2^37,
- * else QLORA_ERR_UNSUPPORTED.  rows 0 does nothing. */
+ * caller; cols a multiple of 64 and at most 2^26, rows * cols at most 2^37, and
+ * fewer than 2^24 tiles of 32 rows x 256 columns (rows below 2^29 - 31 for up to
+ * 256 columns), else QLORA_ERR_UNSUPPORTED.  rows 0 does nothing. */
 typedef struct {
   int64_t rows, cols;
   int8_t* codes;       /* [rows, cols] */

@@ -100,3 +100,16 @@ def test_binding_refusals():
                     ("dY", b(4, 512)[:, ::2]), ("dA", b(8, 128)), ("dX", torch.zeros(4, 128)),
                     ("keep_bits", torch.zeros(3, dtype=torch.uint8)), ("XA_in", None)):
         _raises(q.qlora_linear_bwd_act8, **{**good, name: v})
+
+
+@pytest.mark.parametrize("rows,cols", [(1 << 29, 64), ((1 << 29) - 31, 64), (1 << 29, 256),
+                                       (1 << 28, 320), (1 << 28, 512), (1 << 31, 64)])
+def test_checkpoints_of_more_tiles_than_a_launch_has(rows, cols):
+    # below the limit of values, but 2^24 or more tiles of 32 rows x 256 columns,
+    # a workgroup of 256 threads each: refused, where a launch would fail
+    assert rows * cols <= 1 << 37
+    a = _a8(rows=rows, cols=cols)
+    assert q.lib().qlora_act8_quantize(P(FAKE), ctypes.byref(a), None) == q.QLORA_ERR_UNSUPPORTED
+    for out in (q.QLORA_BF16, q.QLORA_F32):
+        assert q.lib().qlora_act8_dequantize(ctypes.byref(a), out, P(FAKE), None) == \
+            q.QLORA_ERR_UNSUPPORTED
