@@ -8,6 +8,7 @@ every call raises.
 """
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -1069,6 +1070,36 @@ def qlora_trace_end():
     return {name: (int(n[i]), float(ms[i])) for name, i in KERNELS.items() if n[i] > 0}
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """A gradient as it is; differentiating it raises."""
+
+    @staticmethod
+    def forward(ctx, d, *sources):
+        return d.view_as(d)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("this gradient has no derivative: the backward runs in the library's "
+                           "kernels")
+
+
+def _first_order(backward):
+    """For a backward that autograd cannot see into: with create_graph its
+    results hang on what they were formed from, so that a second derivative
+    raises and is not taken for zero."""
+    @functools.wraps(backward)
+    def wrapped(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if torch.is_grad_enabled():
+            on = [t for t in (*ctx.saved_tensors, *grads) if t is not None and t.requires_grad]
+            if on:
+                out = tuple(_NoSecondDerivative.apply(d, *on) if d is not None else None
+                            for d in out)
+        return out
+    return wrapped
+
+
 class QLoRALinearFn(torch.autograd.Function):
     """autograd wrapper: frozen NF4 weight, trainable bf16 adapters A and B.
     act8 keeps the input for the backward in 8 bits instead of bf16: True
@@ -1093,6 +1124,7 @@ class QLoRALinearFn(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @_first_order
     def backward(ctx, dY):
         X, A, B, XA, *scale = ctx.saved_tensors
         if scale:
@@ -1124,6 +1156,7 @@ class TokenLogprobsFn(torch.autograd.Function):
         return logp
 
     @staticmethod
+    @_first_order
     def backward(ctx, g):
         return _logits_grad(ctx, None, g.to(torch.float32).contiguous()), None
 
@@ -1149,6 +1182,7 @@ class PreferenceLossFn(torch.autograd.Function):
         return o.loss, o.seq_logp, o.rewards
 
     @staticmethod
+    @_first_order
     def backward(ctx, g, *_):
         return (_logits_grad(ctx, g, ctx.saved_tensors[3]),) + (None,) * 7
 
@@ -1170,5 +1204,6 @@ class PolicyLossFn(torch.autograd.Function):
         return o.loss.clone(), kl, frac
 
     @staticmethod
+    @_first_order
     def backward(ctx, g, *_):
         return (_logits_grad(ctx, g, ctx.saved_tensors[3]),) + (None,) * 10
