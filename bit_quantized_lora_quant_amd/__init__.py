@@ -890,11 +890,13 @@ def _logits(what, logits, labels):
 
 
 def _dlogits_like(what, logits, dlogits):
-    """The gradient buffer and its row stride: the logits' own stride where
-    none is given, so that rows start at the same alignment."""
+    """The gradient buffer and its row stride: where none is given, the least
+    that starts rows at the same alignment as the logits' rows."""
     rows, vocab = logits.shape
     if dlogits is None:
-        ld = max(logits.stride(0), vocab) if rows > 1 else vocab
+        ld = vocab
+        if rows > 1:
+            ld += (logits.stride(0) - vocab) % (16 // logits.element_size())
         dlogits = torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)
         if ld != vocab:
             dlogits = dlogits[:, :vocab]
