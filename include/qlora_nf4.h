@@ -511,7 +511,8 @@ size_t qlora_linear_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_
 /* qlora_linear_bwd_dropout whose input is a checkpoint of X [M, K], M =
  * X8->rows: dA = s . G^T . D(x^) is formed from the codes, with G kept in
  * float32 and its products with the scales in three bf16 parts, so dA has
- * float32 accuracy for the given x^; dX and dB do not read X.  XA_in
+ * float32 accuracy for the given x^; dX and dB do not read X.  A block whose
+ * scale is NaN makes its 64 columns of dA NaN, under dropout too.  XA_in
  * (required) is the forward's XA_out.  drop and keep_bits_in (both nullable)
  * as there.  Same shapes, limits and errors, plus QLORA_ERR_INVALID_ARG for a
  * checkpoint of another width or without rows, or XA_in NULL. */
@@ -557,7 +558,7 @@ typedef struct {
   const void* data;        /* device, [rows] x ld; may be NULL when rows == 0 */
   qlora_dtype dtype;       /* QLORA_F32 or QLORA_BF16 */
   int32_t reserved;        /* must be 0 */
-  int64_t rows, vocab, ld; /* rows * ceil(row bytes / 32 KB) < 2^24, vocab < 2^30 */
+  int64_t rows, vocab, ld; /* rows * ceil(row bytes / 32 KB) < 2^24; vocab, ld < 2^30 */
   const int64_t* labels;   /* device, [rows] */
 } qlora_logits;
 

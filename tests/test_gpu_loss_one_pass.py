@@ -143,3 +143,84 @@ def test_weights_against_the_oracle(T, V, dtype, pad, kl):
     half = torch.finfo(dtype).eps / 2
     bound = (half * np.abs(r["dlogits"]) + (tol + np.abs(r["w"]) * (e + 2.0 ** -20))[:, None])
     assert np.all(np.abs(_np(o.dlogits) - r["dlogits"]) <= bound)
+
+
+# more rows with a target than the launch has workgroups, so that each takes a
+# second row and a third
+LOOPS = [(2700, 16411, BF, 2, 1024), (1500, 33003, BF, 5, 512), (900, 70001, BF, 0, 256),
+         (820, 66003, BF, 4, 256), (1700, 8203, F32, 0, 1024), (1600, 17001, F32, 1, 512),
+         (760, 40001, F32, 2, 256)]
+
+
+@pytest.mark.parametrize("T,V,dtype,pad,groups", LOOPS)
+def test_workgroups_that_take_row_after_row(T, V, dtype, pad, groups):
+    """Rows of changing alignment: a workgroup's next row has a head, an edge and
+    chunks of its own.  logp within a row's float32 sum of float64 (each
+    exponential off by 2^-22, a thread adding V / 256 + 64 terms at most), the
+    weights one rounding from the statistics', the gradient theirs."""
+    say("one pass, many rows T=%d V=%d %s pad=%d" % (T, V, dtype, pad))
+    g, z, y, cu, lp = _case(T, V, dtype, pad)
+    y[7], y[T // 2 + 1] = V, V + 5                    # labels out of the vocabulary between
+    old = lp - 0.3 * torch.randn(T, generator=g).to(DEV)
+    ref = lp + 0.2 * torch.randn(T, generator=g).to(DEV)
+    adv = torch.randn(T, generator=g).to(DEV)
+    kw = dict(kl_coef=0.05, token_advantages=True)
+    o, stats, w = _nan_run(z, y, cu, adv, old, ref, **kw)
+    inside = torch.zeros(T, dtype=torch.bool, device=DEV)
+    inside[int(cu[0]):int(cu[-1])] = True
+    use, bad = inside & (y >= 0) & (y < V), inside & (y >= V)
+    assert int(use.sum()) > groups
+    zd = z.double()
+    zy = torch.gather(zd, 1, y.clamp(0, V - 1)[:, None])[:, 0]
+    want = torch.where(use, zy - torch.logsumexp(zd, 1), 0.0)
+    e = 2.0 ** -22 + (V / 256 + 64) * 2.0 ** -24
+    assert bool(((o.logp.double() - want).abs() <= e + 2.0 ** -24 * want.abs())[~bad].all())
+    assert bool(torch.isnan(o.logp[bad]).all()) and bool(torch.isnan(o.dlogits[bad]).all())
+    l = zy - stats[:, 0].double() - stats[:, 1].double().log()
+    r, k = torch.exp(l - old.double()), torch.exp(ref.double() - l)
+    u, c = -adv.double() * r, -adv.double() * r.clamp(0.8, 1.2)
+    share = 1 / int((inside & (y >= 0)).sum())
+    want = share * (torch.where(c > u, 0.0, u) - 0.05 * (k - 1))
+    err, tol = (w.double() - want).abs(), 2.0 ** -23 * want.abs() + 1e-13 * share
+    border = ((l - old.double()).exp() - 0.8).abs().minimum((r - 1.2).abs()) < 1e-12
+    assert bool((err <= tol)[use & ~border].all())
+    # in place, where a row's stores follow the next row's loads
+    t = z.clone() if z.is_contiguous() else torch.empty((T, V + pad), dtype=dtype, device=DEV)[:, :V]
+    t.copy_(z)
+    b = q.qlora_policy_loss(t, y, cu, adv, old, ref, dlogits=t, **kw)
+    assert b.dlogits is t and torch.equal(torch.nan_to_num(t, 7.0), torch.nan_to_num(o.dlogits, 7.0))
+    assert torch.equal(torch.nan_to_num(b.logp, 7.0), torch.nan_to_num(o.logp, 7.0))
+
+
+def _nan_run(z, y, cu, *args, **kw):
+    """_run for batches with labels out of the vocabulary, whose rows are NaN."""
+    T = len(y)
+    stats, w = torch.empty((T, 2), device=DEV), torch.empty(T, device=DEV)
+    o = q.qlora_policy_loss(z, y, cu, *args, return_grad=True, stats=stats, w=w, **kw)
+    inside = torch.zeros(T, dtype=torch.bool, device=DEV)
+    inside[int(cu[0]):int(cu[-1])] = True
+    d = q.qlora_token_logprobs_bwd(z, torch.where(inside, y, -1), stats, w)
+    assert torch.equal(torch.nan_to_num(o.dlogits, 7.0), torch.nan_to_num(d, 7.0))
+    return o, stats, w
+
+
+@pytest.mark.parametrize("T,V,dtype", [(512, 32000, BF), (512, 128256, BF), (600, 32000, BF),
+                                       (512, 32003, F32)])
+def test_sums_have_no_bias(T, V, dtype):
+    """Over many rows the sums' relative errors average out: rounded once they are
+    within 2^-24 with mean 0 (1.5e-9 over 512 rows), and what the exponentials add
+    is under 2^-25 in the mean.  A bias adds up over a sequence's log ratio."""
+    say("bias of the sums T=%d V=%d %s" % (T, V, dtype))
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = (torch.randn((T, V), generator=g, device=DEV) * 2.5).to(dtype)
+    y = torch.randint(0, V, (T,), generator=g, device=DEV)
+    cu = torch.tensor([0, T // 2, T], dtype=torch.int32, device=DEV)
+    stats = torch.empty((3, T, 2), device=DEV)
+    q.qlora_token_logprobs(z, y, stats=stats[0])
+    q.qlora_preference_loss(z, y, cu, stats=stats[1])
+    q.qlora_policy_loss(z, y, cu, torch.ones(2, device=DEV), return_grad=True, stats=stats[2])
+    for s in stats:
+        exact = torch.exp(z.double() - s[:, :1].double()).sum(1)
+        rel = s[:, 1].double() / exact - 1
+        assert abs(float(rel.mean())) <= 2.0 ** -25, float(rel.mean())
+        assert float(rel.square().mean().sqrt()) <= 2.0 ** -23
