@@ -48,7 +48,10 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
   const int64_t mbeg = (int64_t)split * mchunk;
   int64_t mend = mbeg + mchunk;
   mend = mend < M ? mend : M;
-  const int64_t pc = p0 + 4 * i16;
+  // rows of whole groups of 4 columns are read as such, a last tile's lanes past
+  // them repeating the row's last group: what they make is never stored
+  const bool fast = (J.P % 4) == 0;
+  const int64_t pc = fast && p0 + 4 * i16 >= J.P ? J.P - 4 : p0 + 4 * i16;
 
   f32x4_t acc[4][RT];
 #pragma unroll
@@ -56,7 +59,6 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
 #pragma unroll
     for (int jt = 0; jt < RT; ++jt) acc[t][jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  const bool fast = (J.P % 4) == 0 && p0 + kGradP <= J.P;   // workgroup-uniform
   // step mb: rows mb + 8g + e of T (clamped below M; U is zero there) and the
   // fragments of U.  A rank index past r feeds only output column j >= r, which
   // is never stored, so what its slots hold does not matter.
@@ -113,7 +115,7 @@ __device__ __forceinline__ void grad_slice(const GradJob& J, int64_t M, int r, i
   // this wave's steps: mb = first + 128 i, i < cnt
   const int64_t first = mbeg + 32 * wv;
   const int64_t cnt = first < mend ? (mend - first + 127) / 128 : 0;
-  // Steps of 32 whole rows with 64 columns in range read through buffer views
+  // Steps of 32 whole rows of such groups read through buffer views
   // (fixed byte offsets per lane, the step's base as the uniform offset), two
   // steps in flight: the next step's loads are issued before this step's MFMAs.
   const int64_t tbytes = M * J.P * 2, ubytes = ceil_div(M, 32) * rt * 1024;
