@@ -109,7 +109,8 @@ __global__ __launch_bounds__(sk_waves<RT>() * 64) void k_skinny_slices(SkinnyJob
 }
 
 // ------------------------------------------------ skinny NT, LDS-staged
-// For ranks 17..64 (RT = 2, 4) over an inner dimension that is a multiple of
+// For ranks 17..64 (RT = 2, 4), and for any rank where a job asks for it
+// (stage_any; without dropout), over an inner dimension that is a multiple of
 // 64: a workgroup of 8 waves takes 128 rows of T (16 per wave) and one inner
 // slice.  Per 64-wide step both tiles stream into LDS by DMA, three stages
 // deep: T [128 rows][64] (16 KB) and U [16 RT rows][64] (2 RT KB), 16-byte
@@ -474,7 +475,12 @@ hipError_t skinny2_rt(const SkinnyJob* jobs, int nj, int64_t M, int r, int r32,
   const ReconJob none{};
   bool drop = false;
   for (int i = 0; i < nj; ++i) drop |= jobs[i].drop.thr != 0;
-  const auto kern = drop ? k_skinny2<RT, true> : k_skinny2<RT, false>;
+  auto kern = k_skinny2<RT, false>;
+  if constexpr (RT == 2 || RT == 4) {
+    if (drop) kern = k_skinny2<RT, true>;
+  } else if (drop) {
+    return hipErrorInvalidValue;   // (skinny_staged keeps these out)
+  }
   hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kSk2Waves * 64), 0, s, jobs[0],
                      nj > 1 ? jobs[1] : jobs[0], nj, M, r, r32, rc ? *rc : none, rc ? 1 : 0);
   return hipGetLastError();
@@ -497,12 +503,13 @@ hipError_t grads_rt(const GradJob* jobs, int nj, int64_t M, int r, hipStream_t s
 
 int skinny_rpad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
-// The LDS-staged form: ranks 17..64 (below where asked), whole 64-wide steps,
-// 16-byte rows.
+// The LDS-staged form: ranks 17..64 (any where asked, without dropout), whole
+// 64-wide steps, 16-byte rows.
 static bool skinny_staged(const SkinnyJob& j, int r) {
   const int rp = skinny_rpad(r);
-  return (rp == 32 || rp == 64 || j.stage_any) && j.kin % kSk2Step == 0 && j.ldt % 8 == 0 &&
-         j.ldu % 8 == 0 && (reinterpret_cast<uintptr_t>(j.T) & 15) == 0 &&
+  return (rp == 32 || rp == 64 || (j.stage_any && j.drop.thr == 0)) &&
+         j.kin % kSk2Step == 0 && j.ldt % 8 == 0 && j.ldu % 8 == 0 &&
+         (reinterpret_cast<uintptr_t>(j.T) & 15) == 0 &&
          (reinterpret_cast<uintptr_t>(j.U) & 15) == 0;
 }
 
@@ -607,8 +614,8 @@ hipError_t launch_prep(const TransposeJob* t, int nt, const ReconJob* recon, hip
 }
 
 int lora_grad_splits(int64_t M, int64_t P) {
-  // about 256 workgroups over the chip per job, at least 512 tokens per split
-  // (four steps per wave)
+  // about 512 workgroups of 64 columns per job, twice the CUs (above rank 64
+  // twice that), at least 512 tokens per split (four steps per wave)
   const int64_t groups = ceil_div(P, 128);
   int64_t splits = ceil_div(256, groups);
   const int64_t maxs = ceil_div(M, 512);
