@@ -80,11 +80,6 @@ __device__ __forceinline__ uint4 byte_mask8(uint32_t b) {
                     ((b & 64u) ? 0xFFFFu : 0u) | ((b & 128u) ? 0xFFFF0000u : 0u));
 }
 
-// And-masks for the 8 bf16 of elements e .. e + 7 of X (e % 8 == 0).
-__device__ __forceinline__ uint4 dropout_keep8(uint64_t e, const DropoutParams& d) {
-  return byte_mask8(dropout_byte(e, d));
-}
-
 __device__ __forceinline__ uint4 and4(uint4 v, uint4 m) {
   return make_uint4(v.x & m.x, v.y & m.y, v.z & m.z, v.w & m.w);
 }
