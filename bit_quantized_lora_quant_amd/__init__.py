@@ -1086,15 +1086,17 @@ class _NoSecondDerivative(torch.autograd.Function):
 
 
 def _first_order(backward):
-    """For a backward that autograd cannot see into: with create_graph its
-    results hang on what they were formed from, so that a second derivative
-    raises and is not taken for zero."""
+    """For a backward that autograd cannot see into, given its saved tensors
+    (read once: a hook may recompute them): with create_graph its results hang on
+    what they were formed from, so that a second derivative raises and is not
+    taken for zero."""
     @functools.wraps(backward)
     def wrapped(ctx, *grads):
+        saved = ctx.saved_tensors
         with torch.no_grad():
-            out = backward(ctx, *grads)
+            out = backward(ctx, saved, *grads)
         if torch.is_grad_enabled():
-            on = [t for t in (*ctx.saved_tensors, *grads) if t is not None and t.requires_grad]
+            on = [t for t in (*saved, *grads) if t is not None and t.requires_grad]
             if on:
                 out = tuple(_NoSecondDerivative.apply(d, *on) if d is not None else None
                             for d in out)
@@ -1127,8 +1129,8 @@ class QLoRALinearFn(torch.autograd.Function):
 
     @staticmethod
     @_first_order
-    def backward(ctx, dY):
-        X, A, B, XA, *scale = ctx.saved_tensors
+    def backward(ctx, saved, dY):
+        X, A, B, XA, *scale = saved
         if scale:
             a = Act8Tensor(X.shape[0], X.shape[1], codes=X, scale=scale[0])
             dX, dA, dB = qlora_linear_bwd_act8(ctx.q, a, A.contiguous(), B.contiguous(), ctx.alpha,
@@ -1142,8 +1144,8 @@ class QLoRALinearFn(torch.autograd.Function):
         return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None
 
 
-def _logits_grad(ctx, g, w):
-    logits, labels, stats = ctx.saved_tensors[:3]
+def _logits_grad(saved, g, w):
+    logits, labels, stats = saved[:3]
     g = g.to(torch.float32).reshape(1).contiguous() if g is not None else None
     return qlora_token_logprobs_bwd(logits, labels, stats, w, grad_scale=g)
 
@@ -1159,8 +1161,8 @@ class TokenLogprobsFn(torch.autograd.Function):
 
     @staticmethod
     @_first_order
-    def backward(ctx, g):
-        return _logits_grad(ctx, None, g.to(torch.float32).contiguous()), None
+    def backward(ctx, saved, g):
+        return _logits_grad(saved, None, g.to(torch.float32).contiguous()), None
 
 
 def _loss_buffers(logits):
@@ -1185,8 +1187,8 @@ class PreferenceLossFn(torch.autograd.Function):
 
     @staticmethod
     @_first_order
-    def backward(ctx, g, *_):
-        return (_logits_grad(ctx, g, ctx.saved_tensors[3]),) + (None,) * 7
+    def backward(ctx, saved, g, *_):
+        return (_logits_grad(saved, g, saved[3]),) + (None,) * 7
 
 
 class PolicyLossFn(torch.autograd.Function):
@@ -1207,5 +1209,5 @@ class PolicyLossFn(torch.autograd.Function):
 
     @staticmethod
     @_first_order
-    def backward(ctx, g, *_):
-        return (_logits_grad(ctx, g, ctx.saved_tensors[3]),) + (None,) * 10
+    def backward(ctx, saved, g, *_):
+        return (_logits_grad(saved, g, saved[3]),) + (None,) * 10
