@@ -844,9 +844,9 @@ def qlora_linear_bwd_act8(q: NF4Tensor, a: Act8Tensor, A, B, alpha: float, dY, X
     what = "qlora_linear_bwd_act8"
     r = A.shape[0]
     dX, dA, dB, ws = _bwd_act8(what, q, a, A, B, r, dY, XA_in, need_dx, dX, dA, dB, ws)
-    _require(keep_bits is None or (keep_bits.dtype == torch.uint8 and
+    _require(keep_bits is None or (keep_bits.dtype == torch.uint8 and keep_bits.is_contiguous() and
                                    keep_bits.numel() * 8 >= a.rows * a.cols),
-             what, "keep_bits must be uint8 [M K / 8]")
+             what, "keep_bits must be contiguous uint8 [M K / 8]")
     with _on(what, dY, a.codes, q.codes, A, B, XA_in, dX, dA, dB, ws, keep_bits):
         d, x8, dr = q.descriptor(), a.descriptor(), _dropout(dropout)
         _check(lib().qlora_linear_bwd_act8(ctypes.byref(d), ctypes.byref(x8), _ptr(A), _ptr(B), r,

@@ -113,3 +113,12 @@ def test_checkpoints_of_more_tiles_than_a_launch_has(rows, cols):
     for out in (q.QLORA_BF16, q.QLORA_F32):
         assert q.lib().qlora_act8_dequantize(ctypes.byref(a), out, P(FAKE), None) == \
             q.QLORA_ERR_UNSUPPORTED
+
+
+def test_strided_keep_bits_are_refused():
+    W, a = q.NF4Tensor(256, 128, "cpu"), q.Act8Tensor(4, 128, "cpu")
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    for bits in (torch.zeros(128, dtype=torch.uint8)[::2], torch.zeros(1, dtype=torch.uint8).expand(64)):
+        with pytest.raises(q.QloraError, match="keep_bits"):
+            q.qlora_linear_bwd_act8(W, a, b(8, 128), b(256, 8), 1.0, b(4, 256), b(4, 8),
+                                    dropout=(0.1, 1), keep_bits=bits)
