@@ -266,7 +266,10 @@ __device__ __forceinline__ void add_batch(MaxSum& a, uint4 (&q)[N], int n) {
 __device__ __forceinline__ bool failed(const MaxSum& a) {
   return !(a.s < kInf) || (__builtin_fabsf(a.m) > 0x1p20f && a.m != -kInf);
 }
-// The sum of chunks c, c + step, .. below c1, against a maximum that is known.
+// The sum of chunks c, c + step, .. below c1, against a maximum that is known.  A
+// -inf sends its thread here: logp of 4096 x 128256 takes 189 us with the last 256
+// columns masked by it and 283 with half of them (141 without, and with the type's
+// lowest value in its place).
 template <typename T>
 __device__ __forceinline__ void sum_again(MaxSum& a, const Row<T>& r, int c, int c1, int step) {
   const float ref = a.m == -kInf ? 0.f : a.m;
@@ -738,8 +741,8 @@ __device__ __forceinline__ double uniform(double x) {
 // CU's registers).  The workgroups are persistent and the memory never waits
 // for arithmetic: as a chunk's gradient is stored its registers take the same
 // chunk of the workgroup's next row, and the sums run over four chunks at a
-// time as they arrive.  1.85 GB in 370 us (4096 x 128256), 5.0 TB/s; as two
-// launches 445.  logp, weight and loss are formed after, from the same
+// time as they arrive.  1.85 GB in 379 us (4096 x 128256), 4.9 TB/s; as two
+// launches 456.  logp, weight and loss are formed after, from the same
 // statistics; here one wave forms the weight for the gradient, with the same
 // float64 operations, so that both say of a ratio next to a border whether it is
 // clipped.  What is the same in all lanes is kept in scalar registers: a row's
@@ -951,9 +954,9 @@ static hipError_t policy_rows_of(const LogitsView& v, const RowOut& o, const Pol
 // The one-pass form where a row fits in registers and is long enough to be worth
 // a workgroup (32 KB), the rows fill the chip, and the gradient's rows start
 // where the logits' do between 16-byte boundaries.  Whole calls, one pass against
-// two: over 128,256 bf16 logits 42 and 34 us at 128 rows, 48 and 50 at 256, 208
-// and 249 at 2048; over 32,000 26 and 23, 28 and 31, 65 and 74; over 9,000 25 and
-// 23 at 256 rows, 42 and 40 at 2048.
+// two: over 128,256 bf16 logits 38 and 31 us at 128 rows, 43 and 46 at 256, 130
+// and 125 at 1024, 220 and 240 at 2048, 398 and 460 at 4096; over 32,000 25 and 28
+// at 256 rows, 66 and 69 at 2048; over 9,000 25 and 25 at 256, 40 and 36 at 2048.
 static bool one_pass(const LogitsView& v, const void* dz, int64_t ldd) {
   const int64_t chunks = row_chunks(v.vocab, v.bf16);
   const uintptr_t apart =
