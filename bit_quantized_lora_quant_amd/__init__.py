@@ -40,6 +40,8 @@ EXPORTS = [
     "qlora_linear_bwd_act8", "qlora_grouped_bwd_act8",
     "qlora_loss_workspace_bytes", "qlora_token_logprobs", "qlora_token_logprobs_bwd",
     "qlora_preference_loss", "qlora_policy_loss",
+    "qlora_head_workspace_bytes", "qlora_head_logprobs", "qlora_head_logprobs_bwd",
+    "qlora_head_cross_entropy",
     "qlora_trace_begin", "qlora_trace_pause", "qlora_trace_end",
 ]
 KERNELS = {"fwd_gemm": 0, "dx_gemm": 1, "quantize": 2, "dequant": 3, "gemv": 4,
@@ -48,6 +50,7 @@ ADAMW8_BLOCK = 256
 ACT8_BLOCK = 64
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}      # QLORA_PREF_*
 POLICY_REDUCTIONS = {"token": 0, "sequence": 1}              # QLORA_POLICY_*
+HEAD_REDUCTIONS = {"mean": 0, "sum": 1}                      # QLORA_HEAD_MEAN, _SUM
 
 
 class QloraError(RuntimeError):
@@ -108,6 +111,13 @@ class PolicyParams(ctypes.Structure):
     _fields_ = [("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
                 ("kl_coef", ctypes.c_double), ("reduction", ctypes.c_int32),
                 ("token_advantages", ctypes.c_int32)]
+
+
+class HeadDescriptor(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_void_p), ("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("ld_hidden", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("vocab", ctypes.c_int64), ("ld_weight", ctypes.c_int64),
+                ("labels", ctypes.c_void_p)]
 
 
 _lib = None
@@ -177,6 +187,12 @@ def lib():
                                             P, P, P, P, P, I64, P, SZ, P]
         L.qlora_policy_loss.argtypes = [Z, I32, P, P, P, P, ctypes.POINTER(PolicyParams), P, P, P,
                                         P, P, I64, P, SZ, P]
+        H = ctypes.POINTER(HeadDescriptor)
+        L.qlora_head_workspace_bytes.argtypes = [H, I32]
+        L.qlora_head_workspace_bytes.restype = SZ
+        L.qlora_head_logprobs.argtypes = [H, P, P, P, SZ, P]
+        L.qlora_head_logprobs_bwd.argtypes = [H, P, P, P, P, I64, P, I64, P, SZ, P]
+        L.qlora_head_cross_entropy.argtypes = [H, I32, P, P, P, I64, P, I64, P, SZ, P]
         L.qlora_host_state_alloc.argtypes = [SZ, P]
         L.qlora_host_state_free.argtypes = [P]
         L.qlora_trace_begin.argtypes = [ctypes.c_uint32, I32]
@@ -1051,6 +1067,121 @@ def qlora_policy_loss(logits, labels, cu_seqlens, advantages, old_logp=None, ref
     return PolicyLoss(*out.unbind(), logp, dlogits)
 
 
+def _dense_rows(t):
+    return t.dim() == 2 and t.dtype == torch.bfloat16 and (t.stride(1) == 1 or t.shape[1] == 1)
+
+
+def _head(what, hidden, weight, labels):
+    """Descriptor of hidden states [rows, dim], the head's weight [vocab, dim]
+    (both bf16, rows of any stride that is a multiple of 8) and int64 targets."""
+    _require(_dense_rows(hidden), what, "hidden must be bf16 [rows, dim] with dense rows")
+    _require(_dense_rows(weight) and weight.shape[1] == hidden.shape[1], what,
+             "weight must be bf16 [vocab, %d] with dense rows", hidden.shape[1])
+    _require(labels.dtype == torch.int64 and labels.is_contiguous() and
+             labels.shape == hidden.shape[:1], what, "labels must be int64 [rows]")
+    (rows, dim), vocab = hidden.shape, weight.shape[0]
+    return HeadDescriptor(hidden.data_ptr(), rows, dim, hidden.stride(0) if rows > 1 else dim,
+                          weight.data_ptr(), vocab, weight.stride(0) if vocab > 1 else dim,
+                          labels.data_ptr())
+
+
+def _head_grad(what, like, wanted, d, name):
+    """A gradient's buffer and row stride, (None, 0) where it is not asked for."""
+    if not wanted and d is None:
+        return None, 0
+    if d is None:
+        d = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+    _require(_dense_rows(d) and d.shape == like.shape, what,
+             "%s must be bf16 %s with dense rows", name, tuple(like.shape))
+    return d, d.stride(0) if d.shape[0] > 1 else d.shape[1]
+
+
+def _head_ws(h, dh, dw, ws, dev):
+    if ws is None:
+        ws = workspace(lib().qlora_head_workspace_bytes(
+            ctypes.byref(h), (dh is not None) + 2 * (dw is not None)), dev)
+    return ws
+
+
+def qlora_head_workspace_bytes(hidden, weight, labels, dhidden: bool = False,
+                               dweight: bool = False) -> int:
+    h = _head("qlora_head_workspace_bytes", hidden, weight, labels)
+    return int(lib().qlora_head_workspace_bytes(ctypes.byref(h), int(dhidden) + 2 * int(dweight)))
+
+
+def qlora_head_logprobs(hidden, weight, labels, logp=None, stats=None, ws=None,
+                        return_stats: bool = False):
+    """Log-probability of each row's target under the logits hidden . weight^T,
+    which are not written: float32 [rows] (0 where the label is negative).  With
+    return_stats also float32 [rows, 2] for the backward."""
+    what = "qlora_head_logprobs"
+    h = _head(what, hidden, weight, labels)
+    dev = hidden.device
+    if logp is None:
+        logp = torch.empty(h.rows, dtype=torch.float32, device=dev)
+    if return_stats and stats is None:
+        stats = torch.empty((h.rows, 2), dtype=torch.float32, device=dev)
+    _rows_f32(what, h.rows, (logp, "logp"))
+    _rows_f32(what, 2 * h.rows, (stats, "stats"))
+    ws = _head_ws(h, None, None, ws, dev)
+    with _on(what, hidden, weight, labels, logp, stats, ws):
+        _check(lib().qlora_head_logprobs(ctypes.byref(h), _ptr(logp), _ptr(stats), _ptr(ws),
+                                         ws.numel(), _stream()), what)
+    return (logp, stats) if return_stats else logp
+
+
+def qlora_head_logprobs_bwd(hidden, weight, labels, stats, w, need_dhidden: bool = True,
+                            need_dweight: bool = False, dhidden=None, dweight=None,
+                            grad_scale=None, ws=None):
+    """Gradients of hidden and weight (bf16) for dLoss / dlogp = w [rows] (times
+    the device scalar grad_scale): (dhidden or None, dweight or None).  dhidden may
+    be hidden, overwritten in place."""
+    what = "qlora_head_logprobs_bwd"
+    h = _head(what, hidden, weight, labels)
+    _rows_f32(what, 2 * h.rows, (stats, "stats"))
+    _rows_f32(what, h.rows, (w, "w"))
+    _rows_f32(what, 1, (grad_scale, "grad_scale"))
+    dhidden, ldd = _head_grad(what, hidden, need_dhidden, dhidden, "dhidden")
+    dweight, ldo = _head_grad(what, weight, need_dweight, dweight, "dweight")
+    ws = _head_ws(h, dhidden, dweight, ws, hidden.device)
+    with _on(what, hidden, weight, labels, stats, w, grad_scale, dhidden, dweight, ws):
+        _check(lib().qlora_head_logprobs_bwd(ctypes.byref(h), _ptr(stats), _ptr(w),
+                                             _ptr(grad_scale), _ptr(dhidden), ldd, _ptr(dweight),
+                                             ldo, _ptr(ws), ws.numel(), _stream()), what)
+    return dhidden, dweight
+
+
+class HeadLoss(NamedTuple):
+    loss: torch.Tensor                  # float32 scalar
+    logp: torch.Tensor                  # float32 [rows]
+    dhidden: Optional[torch.Tensor]
+    dweight: Optional[torch.Tensor]
+
+
+def qlora_head_cross_entropy(hidden, weight, labels, reduction: str = "mean",
+                             return_grad: bool = False, need_dweight: bool = False, dhidden=None,
+                             dweight=None, ws=None) -> HeadLoss:
+    """Softmax cross entropy of hidden . weight^T [rows, vocab] against labels
+    (negative: no target), the mean or sum over the targets, without the logits.
+    With return_grad (or a dhidden buffer, which may be hidden) the gradient of
+    hidden comes with it, with need_dweight (or a dweight buffer) weight's."""
+    what = "qlora_head_cross_entropy"
+    h = _head(what, hidden, weight, labels)
+    _require(reduction in HEAD_REDUCTIONS, what, "unknown reduction")
+    dev = hidden.device
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    logp = torch.empty(h.rows, dtype=torch.float32, device=dev)
+    dhidden, ldd = _head_grad(what, hidden, return_grad, dhidden, "dhidden")
+    dweight, ldo = _head_grad(what, weight, need_dweight, dweight, "dweight")
+    ws = _head_ws(h, dhidden, dweight, ws, dev)
+    with _on(what, hidden, weight, labels, dhidden, dweight, ws):
+        _check(lib().qlora_head_cross_entropy(ctypes.byref(h), HEAD_REDUCTIONS[reduction],
+                                              _ptr(loss), _ptr(logp), _ptr(dhidden), ldd,
+                                              _ptr(dweight), ldo, _ptr(ws), ws.numel(),
+                                              _stream()), what)
+    return HeadLoss(loss, logp, dhidden, dweight)
+
+
 def qlora_trace_begin(kernels, capacity: int = 4096):
     """Start timing launches of the named kernels (see KERNELS) with HIP events."""
     mask = 0
@@ -1211,3 +1342,56 @@ class PolicyLossFn(torch.autograd.Function):
     @_first_order
     def backward(ctx, saved, g, *_):
         return (_logits_grad(saved, g, saved[3]),) + (None,) * 10
+
+
+class HeadLogprobsFn(torch.autograd.Function):
+    """autograd wrapper of qlora_head_logprobs(hidden, weight, labels); the
+    backward forms the logits again."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, labels):
+        logp, stats = qlora_head_logprobs(hidden, weight, labels, return_stats=True)
+        ctx.save_for_backward(hidden, weight, labels, stats)
+        return logp
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, saved, g):
+        hidden, weight, labels, stats = saved
+        dh, dw = qlora_head_logprobs_bwd(hidden, weight, labels, stats,
+                                         g.to(torch.float32).contiguous(),
+                                         need_dhidden=ctx.needs_input_grad[0],
+                                         need_dweight=ctx.needs_input_grad[1])
+        return dh, dw, None
+
+
+def _scaled(d, g):
+    """bf16 d times a float32 device scalar, rounded once (g itself is not
+    rounded to bf16), a piece at a time."""
+    out = torch.empty_like(d)
+    g = g.to(torch.float32).reshape(1)
+    step = max(1, (1 << 26) // max(1, d.shape[1]))
+    for i in range(0, d.shape[0], step):
+        out[i:i + step] = d[i:i + step] * g
+    return out
+
+
+class HeadCrossEntropyFn(torch.autograd.Function):
+    """autograd wrapper of qlora_head_cross_entropy: the loss, and (without
+    gradients) logp.  The gradients are formed in the forward, beside the loss,
+    where any is needed; the backward multiplies them by the upstream gradient."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, labels, reduction="mean"):
+        o = qlora_head_cross_entropy(hidden, weight, labels, reduction,
+                                     return_grad=ctx.needs_input_grad[0],
+                                     need_dweight=ctx.needs_input_grad[1])
+        # (the inputs only so that a second derivative hangs on them)
+        ctx.save_for_backward(o.dhidden, o.dweight, hidden, weight)
+        ctx.mark_non_differentiable(o.logp)
+        return o.loss, o.logp
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, saved, g, _):
+        return tuple(_scaled(d, g) if d is not None else None for d in saved[:2]) + (None, None)

@@ -1,0 +1,89 @@
+// Internal launcher interface of the language-model head: log-probabilities and
+// cross entropy straight from hidden states.
+#pragma once
+
+#include "launch.h"
+
+namespace qnf4 {
+
+// What the forward leaves of a row for its gradient: log sum_v exp(z_v), and
+// 1 - p of the target (what is left beside a nearly certain target, which
+// 1 - exp(logp) would not have).
+struct HeadStat {
+  float lse, rest;
+};
+// A slice's maximum and sum of exp(z - m), the target left out of both.
+struct HeadPart {
+  float m, s;
+};
+
+// Rows with a target, packed: hidden [up to a tile's rows][D], their source rows and
+// labels (-1: past the vocabulary) and, for the backward, lse / rest / weight.
+struct HeadRows {
+  uint16_t* h;
+  int32_t* src;
+  int32_t* y;
+  int32_t* n;         // [1] how many
+  HeadStat* stat;
+  float* w;
+};
+
+struct HeadPackArgs {
+  const uint16_t* hidden;
+  int64_t ldh, rows;
+  int dim;
+  int64_t vocab;
+  const int64_t* labels;
+  const float* w;          // nullable: rows of weight 0 count as without target
+  const float* w_scale;    // nullable, [1]
+  const HeadStat* stat;    // with w
+  HeadRows to;
+  // rows without a target, each nullable
+  float* logp;
+  HeadStat* stat_out;
+  uint16_t* dh;
+  int64_t ldd;
+};
+hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t s);
+
+// One panel of packed rows [row0, row0 + rows) (as many as there are), rows a
+// multiple of the tile.
+struct HeadPanel {
+  HeadRows r;
+  int64_t row0;
+  int rows;
+  int dim;
+  const uint16_t* weight;
+  int64_t ldw, vocab;
+  HeadPart* part;      // [vocab tiles * 2][rows]
+  float* zy;           // [rows] the target's logit
+  uint16_t* e;         // [rows][head_cols(vocab)] exponentials (fp16), then dz (bf16)
+};
+// Columns of a panel's row.
+__host__ __device__ inline int64_t head_cols(int64_t vocab) { return ceil_div(vocab, 256) * 256; }
+// Rows of tokens per workgroup tile (64, 128 or 256) for a call of this many rows.
+int head_tile(int64_t rows);
+
+// HEAD_STATS: part and zy; HEAD_EXP: these and e; HEAD_DZ: dz from r.stat and r.w
+enum { HEAD_STATS = 0, HEAD_EXP = 1, HEAD_DZ = 2 };
+hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, hipStream_t s);
+// Joins the slices: logp and stat of the rows (nullable, by source row).
+// From HEAD_LOSS on the packed rows' logp in lp; with HEAD_GRAD_* also r.stat and
+// r.w = -1 (sum) or -1 / n (mean).
+enum { HEAD_SCORE = 0, HEAD_LOSS = 1, HEAD_GRAD_SUM = 2, HEAD_GRAD_MEAN = 3 };
+hipError_t launch_head_join(const HeadPanel& p, int kind, double* lp, float* logp, HeadStat* stat,
+                            hipStream_t s);
+hipError_t launch_head_loss(const int32_t* n, const double* lp, int mean, float* loss,
+                            hipStream_t s);
+// e -> dz in place
+hipError_t launch_head_dz(const HeadPanel& p, hipStream_t s);
+// dh = dz . W by source row; part: head_dh_floats floats
+size_t head_dh_floats(int64_t rows, int dim, int64_t vocab, int tile);
+hipError_t launch_head_dh(const HeadPanel& p, int tile, float* part, uint16_t* dh, int64_t ldd,
+                          hipStream_t s);
+// dw = dz^T . h (bf16, row stride ldo), or with acc [vocab][dim] over several
+// panels: added to it (stored where first), and only the last writes dw.
+hipError_t launch_head_dw(const HeadPanel& p, float* acc, int first, int last, uint16_t* dw,
+                          int64_t ldo, hipStream_t s);
+
+}  // namespace qnf4

@@ -1,0 +1,828 @@
+// The language-model head without its logits: log-probabilities and cross entropy
+// from hidden states h [rows, D] and the head's weight W [V, D], both bf16.
+//
+//   z_t = W h_t,  logp_t = z_ty - log sum_v exp(z_tv)
+//   dz_tv = w_t (1[v = y_t] - p_tv),  dh = dz W,  dW = dz^T h
+//
+// Rows with a target are packed first, so prompts and padding cost nothing and
+// whatever they hold reaches no sum.  The packed rows go through in panels of at
+// most 2^29 row x vocabulary elements: the product's tiles leave a maximum and a
+// sum per row and 128 vocabulary entries and, where a gradient follows in the
+// same call, exp(z - m) of the slice in fp16 (11 bits below the slice's own
+// maximum; the next kernel rounds dz to bf16, the matrix cores' type, once).  The
+// target is left out of its slice: its exponential is kept apart, so that
+// 1 - p of a nearly certain target is a sum of what is left and not 1 minus
+// something rounded.
+//
+// All three products share one tile loop, bound by the matrix cores: 256 values of
+// the output's contiguous index (MFMA rows: a lane then holds eight
+// neighbours of one output row, a 16-byte store) x 64 to 256 of its rows, 64 inner
+// indices a step, four waves of 128 x half the rows.  Accumulators stay in AGPRs;
+// both tiles stream into LDS by DMA while the step before them is multiplied, and
+// operands are read half a step ahead.  Operands whose inner index is not
+// contiguous (W in dh, both in dW) are transposed by the LDS reads themselves.
+#include "head.h"
+
+namespace qnf4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStep = 64;               // inner indices per step
+constexpr int kTileA = 256;             // values of the output's contiguous index
+constexpr int kMaxSlots = 1024;         // partial tiles of dh
+constexpr int kMaxSplits = 64;
+constexpr float kLog2e = 1.4426950408889634f;
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float exp_diff(float z, float m) {
+  return __builtin_amdgcn_exp2f((z - m) * kLog2e);
+}
+
+// ---------------------------------------------------------------- packing rows
+// Workgroup b looks after rows [b R, (b + 1) R): it counts the targets before
+// them, copies its rows that have one to their places and clears what the call
+// returns for the others.  Labels are few (8 bytes a row, against 2 D), so
+// every workgroup counts for itself and one launch does.
+__global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t per) {
+  __shared__ int wave_count[4];
+  __shared__ int place[kThreads];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int64_t first = blockIdx.x * per;
+  const int64_t end = first + per < a.rows ? first + per : a.rows;
+  auto has = [&](int64_t t) { return a.labels[t] >= 0 && (!a.w || a.w[t] != 0.f); };
+  int c = 0;
+#pragma unroll 8
+  for (int64_t t = tid; t < first; t += kThreads) c += has(t);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) c += __shfl_xor(c, d);
+  if (lane == 0) wave_count[wv] = c;
+  __syncthreads();
+  int at = wave_count[0] + wave_count[1] + wave_count[2] + wave_count[3];
+  const float scale = a.w && a.w_scale ? a.w_scale[0] : 1.f;
+  const int chunks = a.dim / 8;
+  for (int64_t t0 = first; t0 < end; t0 += kThreads) {
+    const int64_t t = t0 + tid;
+    const bool mine = t < end && has(t);
+    const uint64_t m = __builtin_amdgcn_ballot_w64(mine);
+    __syncthreads();                       // the counts and places read before
+    if (lane == 0) wave_count[wv] = __popcll(m);
+    __syncthreads();
+    int p = at + __popcll(m & ((1ull << lane) - 1));
+    for (int w = 0; w < wv; ++w) p += wave_count[w];
+    place[tid] = mine ? p : -1;
+    if (mine) {
+      const int64_t y = a.labels[t];
+      a.to.src[p] = (int32_t)t;
+      a.to.y[p] = y < a.vocab ? (int32_t)y : -1;
+      if (a.w) {
+        a.to.w[p] = scale * a.w[t];
+        a.to.stat[p] = a.stat[t];
+      }
+    } else if (t < end) {
+      if (a.logp) a.logp[t] = 0.f;
+      if (a.stat_out) a.stat_out[t] = HeadStat{0.f, 0.f};
+    }
+    __syncthreads();
+    const int n = end - t0 < kThreads ? (int)(end - t0) : kThreads;
+    for (int i = wv; i < n; i += 4) {
+      const int q = place[i];
+      const uint4* in = reinterpret_cast<const uint4*>(a.hidden + (t0 + i) * a.ldh);
+      if (q >= 0) {
+        uint4* out = reinterpret_cast<uint4*>(a.to.h + (int64_t)q * a.dim);
+#pragma unroll 4
+        for (int k = lane; k < chunks; k += 64) out[k] = in[k];
+      } else if (a.dh) {
+        uint4* out = reinterpret_cast<uint4*>(a.dh + (t0 + i) * a.ldd);
+        for (int k = lane; k < chunks; k += 64) out[k] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    at += wave_count[0] + wave_count[1] + wave_count[2] + wave_count[3];
+  }
+  if (blockIdx.x != gridDim.x - 1) return;
+  if (tid == 0) *a.to.n = at;
+  // zeros up to a whole step: inner indices of dW
+  for (int64_t q = at + wv; q < ceil_div(at, kStep) * kStep; q += 4) {
+    uint4* out = reinterpret_cast<uint4*>(a.to.h + q * a.dim);
+    for (int k = lane; k < chunks; k += 64) out[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// ----------------------------------------------------------------- tile loop
+__device__ __forceinline__ void mfma_acc(f32x4_t& acc, const u32x4_t& a, const u32x4_t& b) {
+  // (results in AGPRs by hand: with 256 of them in use the allocator otherwise
+  // moves tiles to VGPRs and back every step)
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7"); }
+
+template <int N>
+__device__ __forceinline__ void wait_vmem() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
+// 16 bytes a lane from base + off to LDS address lds + 16 lane (as dma16, with the
+// lane's part of the address in 32 bits)
+__device__ __forceinline__ void dma16_at(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "m0", "memory");
+}
+
+// An operand: element (index, inner) at p[index * ld + inner] (TR false) or
+// p[inner * ld + index] (TR true); indices past `count` repeat the last ones
+// (their outputs are not stored), inner indices past `inner` the last one (the
+// other operand is zero there).  TR: count % 8 == 0.
+struct Operand {
+  const uint16_t* p;
+  int64_t ld;
+  int64_t count, inner;
+};
+
+// LDS of a step.  TR false: [R][64] values, 128 bytes a row, 16-byte chunk c of row
+// r at c ^ hash(r); TR true: [64][R], 2 R bytes an inner index k, chunk c at
+// c ^ hash(k).  The hashes put the addresses that a read's lanes use together on
+// different banks: A's MFMA row 4 q + v of tile (i, h) is index 32 i + 8 q + 4 h + v
+// (so that a lane's results of h = 0, 1 are neighbours), B's is in order.
+template <int R, bool TR, bool IS_A>
+struct Tile {
+  static constexpr int kBytes = R * kStep * 2;
+  static constexpr int kLoads = kBytes / 1024 / 4;     // per wave and step
+  static constexpr int kRowChunks = TR ? R / 8 : 8;
+  uint32_t off[kLoads];
+  uint32_t krow[TR ? kLoads : 1];
+  const uint16_t* base;
+  uint32_t ld2;
+  int64_t inner;
+
+  __device__ static __forceinline__ int hash(int r) {
+    if (TR) return IS_A ? (r & 1) | ((r & 2) << 1) : (r & 3) << 1;
+    return IS_A ? (r & 3) | (((r >> 3) & 1) << 2) : r & 7;
+  }
+  __device__ __forceinline__ void init(const Operand& o, int64_t first, int lane, int wv) {
+    ld2 = (uint32_t)(o.ld * 2);
+    inner = o.inner;
+    base = TR ? o.p + first : o.p + first * o.ld;
+    const int64_t left = o.count - first;      // > 0
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int chunk = (kLoads * wv + q) * 64 + lane;
+      const int row = chunk / kRowChunks;
+      const int c = (chunk % kRowChunks) ^ hash(row);
+      if (TR) {
+        krow[q] = row;
+        const int64_t col = 8 * c < left ? 8 * c : left - 8;
+        off[q] = (uint32_t)(col * 2);
+      } else {
+        const int64_t r = row < left ? row : left - 1;
+        off[q] = (uint32_t)r * ld2 + 16 * c;
+      }
+    }
+  }
+  // load q of step k0 / 64
+  __device__ __forceinline__ void load(int q, int64_t k0, uint32_t lds, int wv) const {
+    const uint32_t to = lds + (kLoads * wv + q) * 1024;
+    if (TR) {
+      const int64_t left = inner - 1 - k0;
+      const uint32_t k = (int64_t)krow[q] < left ? krow[q] : (uint32_t)left;
+      dma16_at(base + k0 * (ld2 / 2), off[q] + __umul24(k, ld2), to);
+    } else {
+      dma16_at(base + k0, off[q], to);
+    }
+  }
+  // Lane's addresses within a stage: kBases of them, a tile's at one of them plus a
+  // constant.
+  static constexpr int kBases = TR ? 4 : 2;
+  __device__ static __forceinline__ void bases(uint32_t (&b)[kBases], int first, int lane) {
+    const int j = lane & 15, g = lane >> 4;
+    if (!TR) {
+      const int row = IS_A ? 8 * (j >> 2) + (j & 3) : j;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        b[s] = (first + row) * 128 + (((4 * s + g) ^ hash(row)) << 4);
+    } else {
+      // this lane hands in 8 bytes of inner index 8 g + j / 4, piece j % 4 of 16 columns
+      const int k = 8 * g + (j >> 2), p = j & 3;
+      const uint32_t row = k * R * 2;
+      if (IS_A) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {   // u = (i & 1) * 2 + h
+          const int i = u >> 1, h = u & 1;
+          b[u] = row + (((first / 8 + 4 * i + p) ^ hash(k)) << 4) + 8 * (h ^ (p & 1));
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)     // u = tile & 3
+          b[u] = row + (((first / 8 + 2 * u + (p >> 1)) ^ hash(k)) << 4) + 8 * (p & 1);
+      }
+    }
+  }
+  // MFMA operand of tile t (A: t = 2 i + h), inner half s of the stage at `lds`
+  __device__ static __forceinline__ u32x4_t read(const char* lds, const uint32_t (&b)[kBases],
+                                                 int t, int s) {
+    if (!TR) {
+      const int c = IS_A ? (t >> 1) * 4096 + (t & 1) * 512 : t * 2048;
+      return *reinterpret_cast<const u32x4_t*>(lds + b[s] + c);
+    }
+    // (tile t + 4 is 64 columns on: the hash does not reach that bit of the chunk)
+    const uint32_t at = b[t & 3] + (t >> 2) * 128 + s * 32 * R * 2;
+    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds + at));
+    const i16x4_t hi =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds + at + 4 * R * 2));
+    const uint2 l = __builtin_bit_cast(uint2, lo), u = __builtin_bit_cast(uint2, hi);
+    return u32x4_t{l.x, l.y, u.x, u.y};
+  }
+};
+
+template <int TN>
+struct Shape {
+  static constexpr int kStages = TN == 256 ? 2 : 3;
+  static constexpr int kTilesB = TN / 32;          // MFMA tiles of a wave's half
+  static constexpr int kStageBytes = (kTileA + TN) * kStep * 2;
+  static constexpr int kLds = kStages * kStageBytes;
+};
+
+// acc[ta][tb] += A . B^T over steps [s0, s1) (s0 < s1).  Wave (wm, wn): A's values
+// 128 wm .. and B's rows TN / 2 wn ...  Step k's DMA was issued stages - 1 / 2 steps
+// ahead; one barrier a step, in its middle: by then every wave has read the
+// step's second half, so its stage takes the DMA of step k + stages, and step
+// k + 1's tiles have landed (an exact vmcnt: every wave issues the same loads
+// each step, past the end the last step's again).
+template <int TN, bool ATR, bool BTR>
+__device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 32], char* lds, const Operand& A,
+                                          int64_t a0, const Operand& B, int64_t b0, int64_t s0,
+                                          int64_t s1) {
+  using S = Shape<TN>;
+  using TA = Tile<kTileA, ATR, true>;
+  using TB = Tile<TN, BTR, false>;
+  constexpr int NB = S::kTilesB, NS = S::kStages;
+  constexpr int kDma = TA::kLoads + TB::kLoads;
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv & 1, wn = wv >> 1;
+  TA ta;
+  TB tb;
+  ta.init(A, a0, lane, wv);
+  tb.init(B, b0, lane, wv);
+  uint32_t ab[TA::kBases], bb[TB::kBases];
+  TA::bases(ab, 128 * wm, lane);
+  TB::bases(bb, TN / 2 * wn, lane);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void_t*)lds;
+
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int t = 0; t < NB; ++t) {
+      acc[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      asm volatile("" : "+a"(acc[i][t]));
+    }
+  mfma_settle();
+
+  auto load = [&](int q, int64_t step, uint32_t stage) {
+    const int64_t k0 = (step < s1 ? step : s1 - 1) * kStep;
+    if (q < TA::kLoads) ta.load(q, k0, lds0 + stage, wv);
+    else tb.load(q - TA::kLoads, k0, lds0 + stage + TA::kBytes, wv);
+  };
+#pragma unroll
+  for (int st = 0; st < NS; ++st)
+#pragma unroll
+    for (int q = 0; q < kDma; ++q) load(q, s0 + st, st * S::kStageBytes);
+  wait_vmem<(NS - 1) * kDma>();
+  __syncthreads();
+
+  u32x4_t fa[2][8], fb[2][NB];
+  auto fetch = [&](int r, const char* stage, int s) {   // operand r of half s
+    if (r < 8) fa[s][r] = TA::read(stage, ab, r, s);
+    else fb[s][r - 8] = TB::read(stage + TA::kBytes, bb, r - 8, s);
+  };
+#pragma unroll
+  for (int r = 0; r < 8 + NB; ++r) fetch(r, lds, 0);
+
+  uint32_t cur = 0;
+  constexpr int M = 8 * NB, R = 8 + NB, RM = M * 3 / 4, DM = M / 2;
+  for (int64_t k = s0; k < s1; ++k) {
+    const uint32_t nxt = cur + S::kStageBytes < S::kLds ? cur + S::kStageBytes : 0;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      mfma_acc(acc[i & 7][i >> 3], fa[0][i & 7], fb[0][i >> 3]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int r = i * R / RM; r < (i + 1) * R / RM && r < R; ++r) fetch(r, lds + cur, 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_vmem<(NS - 2) * kDma>();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      mfma_acc(acc[i & 7][i >> 3], fa[1][i & 7], fb[1][i >> 3]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = i * kDma / DM; q < (i + 1) * kDma / DM && q < kDma; ++q) load(q, k + NS, cur);
+#pragma unroll
+      for (int r = i * R / RM; r < (i + 1) * R / RM && r < R; ++r) fetch(r, lds + nxt, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    cur = nxt;
+  }
+  wait_vmem<0>();   // nothing left in flight into LDS at exit
+  mfma_settle();
+}
+
+// Tile of workgroup `id` among na x nb (A tiles, B tiles): workgroups go to the
+// eight XCDs in turn, so each XCD takes a contiguous run of the order "eight A
+// tiles, then the next B tile", where 32 neighbours (its CUs) share 8 + 4 tiles.
+__device__ __forceinline__ bool tile_of(int64_t id, int64_t na, int64_t nb, int64_t& ta,
+                                        int64_t& tb) {
+  const int64_t total = na * nb, per = ceil_div(total, 8);
+  const int64_t loc = id >> 3, l = (id & 7) * per + loc;
+  if (loc >= per || l >= total) return false;
+  const int64_t grp = l / (8 * nb), left = na - 8 * grp;
+  const int64_t rem = l - grp * 8 * nb, ga = left < 8 ? left : 8;
+  tb = rem / ga;
+  ta = 8 * grp + rem % ga;
+  return true;
+}
+
+__device__ __forceinline__ int panel_rows(const HeadPanel& p) {
+  const int64_t n = __builtin_amdgcn_readfirstlane(*p.r.n) - p.row0;
+  return n < 0 ? 0 : n < p.rows ? (int)n : p.rows;
+}
+
+// -------------------------------------------------------------------- logits
+// A = W (the vocabulary along a lane's registers: a row's statistics are sums in the
+// lane, then over the four lanes of its column), B = rows.
+template <int TN, int MODE>
+__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
+                          amdgpu_waves_per_eu(1, 1)))
+void k_head_logits(HeadPanel p) {
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
+  constexpr int NB = TN / 32;
+  const int n = panel_rows(p);
+  int64_t tv, tt;
+  if (!tile_of(blockIdx.x, ceil_div(p.vocab, kTileA), ceil_div(n, TN), tv, tt)) return;
+  const Operand A{p.weight, p.ldw, p.vocab, p.dim};
+  const Operand B{p.r.h + p.row0 * p.dim, p.dim, n, p.dim};
+  f32x4_t acc[8][NB];
+  tile_loop<TN, false, false>(acc, lds, A, tv * kTileA, B, tt * TN, 0, p.dim / kStep);
+
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv & 1, wn = wv >> 1;
+  const int64_t v0 = tv * kTileA + 128 * wm;       // of this wave's slice
+  const int64_t cols = head_cols(p.vocab);
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+    const int row = (int)(tt * TN) + TN / 2 * wn + 16 * t + j;
+    const bool valid = row < n;
+    const int64_t q = p.row0 + (valid ? row : 0);
+    const int64_t rel = valid ? (int64_t)p.r.y[q] - v0 - 8 * g : -1;   // in this lane: 32 i + 4 h + v
+    float z[32];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) z[4 * i + v] = acc[i][t][v];
+    if (v0 + 128 > p.vocab) {   // the vocabulary's last tile
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (v0 + 32 * (i >> 3) + 8 * g + (i & 7) >= p.vocab) z[i] = -INFINITY;
+    }
+    uint16_t* out = p.e + (int64_t)row * cols + v0 + 8 * g;
+    if (MODE == HEAD_DZ) {
+      const HeadStat st = p.r.stat[q];
+      const float w = p.r.w[q];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = -w * exp_diff(z[i], st.lse);
+      if (__builtin_amdgcn_ballot_w64(rel >= 0 && rel < 128)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (rel == 32 * (i >> 3) + (i & 7)) z[i] = w * st.rest;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 o = make_uint4(pack_bf16x2(z[8 * i], z[8 * i + 1]),
+                             pack_bf16x2(z[8 * i + 2], z[8 * i + 3]),
+                             pack_bf16x2(z[8 * i + 4], z[8 * i + 5]),
+                             pack_bf16x2(z[8 * i + 6], z[8 * i + 7]));
+        // (rows behind the last are inner indices of dW, whatever h holds there)
+        if (!valid) o = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(out + 32 * i) = o;
+      }
+      continue;
+    }
+    if (__builtin_amdgcn_ballot_w64(rel >= 0 && rel < 128)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (rel == 32 * (i >> 3) + (i & 7)) {
+          p.zy[row] = z[i];
+          z[i] = -INFINITY;
+        }
+    }
+    float m = z[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) m = fmaxf(m, z[i]);
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const float from = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      z[i] = exp_diff(z[i], from);
+      s += z[i];
+    }
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (valid && g == 0) p.part[(2 * tv + wm) * p.rows + row] = HeadPart{m, s};
+    if (MODE == HEAD_EXP && valid) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = __builtin_bit_cast(uint32_t, half2_t{(_Float16)z[8 * i + 2 * k],
+                                                      (_Float16)z[8 * i + 2 * k + 1]});
+        *reinterpret_cast<uint4*>(out + 32 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- join
+// A workgroup joins the slices of 64 rows (a lane each), 16 waves every sixteenth
+// slice: the maximum first, then the sums in float64.
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(64 * kJoinWaves)
+void k_head_join(HeadPanel p, int kind, double* lp, float* logp, HeadStat* stat) {
+  __shared__ float ms[kJoinWaves][64];
+  __shared__ double ss[kJoinWaves][64];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int n = panel_rows(p);
+  const int row = blockIdx.x * 64 + lane;
+  if ((int)blockIdx.x * 64 >= n) return;
+  const int rr = row < n ? row : n - 1;
+  const int64_t slices = 2 * ceil_div(p.vocab, kTileA);
+  const HeadPart* part = p.part + rr;
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int64_t k = wv; k < slices; k += kJoinWaves) m = fmaxf(m, part[k * p.rows].m);
+  ms[wv][lane] = m;
+  __syncthreads();
+  const int32_t y = p.r.y[p.row0 + rr];
+  const float zy = y >= 0 ? p.zy[rr] : NAN;
+  m = zy;
+#pragma unroll
+  for (int k = 0; k < kJoinWaves; ++k) m = fmaxf(m, ms[k][lane]);
+  double s = 0;
+#pragma unroll 4
+  for (int64_t k = wv; k < slices; k += kJoinWaves) {
+    const HeadPart e = part[k * p.rows];
+    if (e.m != -INFINITY || !(e.s == 0.f)) s += (double)e.s * exp_diff(e.m, m);
+  }
+  ss[wv][lane] = s;
+  __syncthreads();
+  if (wv != 0 || row >= n) return;
+  s = 0;
+#pragma unroll
+  for (int k = 0; k < kJoinWaves; ++k) s += ss[k][lane];
+  const double ey = exp((double)zy - (double)m);
+  const double all = s + ey, lg = log(all);
+  double l = (double)zy - (double)m - lg;
+  HeadStat st{(float)((double)m + lg), (float)(s / all)};
+  if (y < 0) {
+    l = NAN;
+    st = HeadStat{NAN, NAN};
+  }
+  const int64_t q = p.row0 + row;
+  const int32_t src = p.r.src[q];
+  if (logp) logp[src] = (float)l;
+  if (stat) stat[src] = st;
+  if (kind >= HEAD_LOSS) lp[q] = l;
+  if (kind >= HEAD_GRAD_SUM) {
+    p.r.stat[q] = st;
+    p.r.w[q] = kind == HEAD_GRAD_MEAN ? (float)(-1.0 / *p.r.n) : -1.f;
+  }
+}
+
+// loss = -(sum of logp), over the number of targets
+__global__ __launch_bounds__(1024) void k_head_loss(const int32_t* n, const double* lp, int mean,
+                                                    float* loss) {
+  __shared__ double ss[16];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, rows = *n;
+  double s = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < rows; i += 1024) s += lp[i];
+#pragma unroll
+  for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+  if (lane == 0) ss[wv] = s;
+  __syncthreads();
+  if (threadIdx.x) return;
+  s = 0;
+  for (int k = 0; k < 16; ++k) s += ss[k];
+  *loss = (float)(rows == 0 ? 0.0 : mean ? -s / rows : -s);
+}
+
+// ------------------------------------------------------------------------ dz
+// In place, a thread 8 columns of 8 rows: HBM-bound.  dz = -w exp(m - lse) e, the
+// target's w (1 - p); zeros in the rows up to a whole step of dW.
+constexpr int kDzRows = 8;
+__global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
+  const int n = panel_rows(p);
+  const int64_t cols = head_cols(p.vocab);
+  const int64_t c = (int64_t)blockIdx.y * kThreads * 8 + threadIdx.x * 8;
+  const int r0 = blockIdx.x * kDzRows;
+  if (c >= cols || r0 >= (int)ceil_div(n, kStep) * kStep) return;
+  uint4 e[kDzRows];
+  uint4* at = reinterpret_cast<uint4*>(p.e + (int64_t)r0 * cols + c);
+#pragma unroll
+  for (int r = 0; r < kDzRows; ++r)
+    e[r] = r0 + r < n ? at[r * (cols / 8)] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int r = 0; r < kDzRows; ++r) {
+    uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    if (r0 + r < n) {
+      const int64_t q = p.row0 + r0 + r;
+      const HeadStat st = p.r.stat[q];
+      const float w = p.r.w[q], m = p.part[(c >> 7) * p.rows + r0 + r].m;
+      const float f = m == -INFINITY ? 0.f : -w * exp_diff(m, st.lse);
+      float d[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const half2_t h = __builtin_bit_cast(half2_t, (&e[r].x)[k]);
+        d[2 * k] = f * (float)h[0];
+        d[2 * k + 1] = f * (float)h[1];
+      }
+      const int64_t rel = p.r.y[q] - c;
+      if (rel >= 0 && rel < 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (rel == k) d[k] = w * st.rest;
+      }
+      o = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
+                     pack_bf16x2(d[6], d[7]));
+    }
+    at[r * (cols / 8)] = o;
+  }
+}
+
+// ------------------------------------------------------------------------ dh
+// The inner index is the vocabulary, long: with fewer tiles than CUs it is cut
+// into the number of slices that fills whole rounds best, which hangs on how
+// many rows there are and so is found here.  A slice's epilogue and its part of
+// the sum that follows cost about as much as 24 steps.
+__host__ __device__ inline int dh_splits(int64_t tiles, int64_t steps) {
+  int best = 1;
+  int64_t least = -1;
+  for (int s = 1; s <= kMaxSplits && tiles * s <= kMaxSlots; ++s) {
+    const int64_t each = ceil_div(steps, s);
+    if (s > 1 && each < 6) break;
+    const int64_t cost = ceil_div(tiles * s, 256) * (each + (s > 1 ? 24 : 4));
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+__device__ __forceinline__ void dh_plan(const HeadPanel& p, int n, int TN, int64_t& ta, int64_t& tb,
+                                        int& splits) {
+  ta = ceil_div(p.dim, kTileA);
+  tb = ceil_div(n, TN);
+  splits = dh_splits(ta * tb, ceil_div(p.vocab, kStep));
+}
+
+// Eight neighbouring values of a lane: tiles (i, 0) and (i, 1), in the order the
+// transposing read has them (odd lane groups the other way round).
+template <int NB>
+__device__ __forceinline__ void eight(const f32x4_t (&acc)[8][NB], int i, int t, int g,
+                                      float (&o)[8]) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const float a = acc[2 * i][t][v], b = acc[2 * i + 1][t][v];
+    o[v] = (g & 1) ? b : a;
+    o[4 + v] = (g & 1) ? a : b;
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&o)[8]) {
+  return make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                    pack_bf16x2(o[6], o[7]));
+}
+
+template <int TN>
+__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
+                          amdgpu_waves_per_eu(1, 1)))
+void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
+  constexpr int NB = TN / 32;
+  const int n = panel_rows(p);
+  int64_t na, nb, td, tt;
+  int splits;
+  dh_plan(p, n, TN, na, nb, splits);
+  const int64_t slot = blockIdx.x;       // tiles of a slice together
+  const int64_t per8 = ceil_div(na * nb, 8) * 8;
+  const int64_t sl = per8 ? slot / per8 : 0;
+  if (sl >= splits || !tile_of(slot - sl * per8, na, nb, td, tt)) return;
+  const int64_t steps = ceil_div(p.vocab, kStep), each = ceil_div(steps, splits);
+  const int64_t s0 = sl * each, s1 = s0 + each < steps ? s0 + each : steps;
+  const int64_t cols = head_cols(p.vocab);
+  const Operand A{p.weight, p.ldw, p.dim, p.vocab};
+  const Operand B{p.e, cols, n, cols};
+  f32x4_t acc[8][NB];
+  // (a cut that leaves the last slice empty is left out by the rows above: each >= 1)
+  tile_loop<TN, true, false>(acc, lds, A, td * kTileA, B, tt * TN, s0 < steps ? s0 : steps - 1, s1);
+
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv & 1, wn = wv >> 1;
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+    const int in = TN / 2 * wn + 16 * t + j, row = (int)(tt * TN) + in;
+    if (row >= n) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t col = td * kTileA + 128 * wm + 32 * i + 8 * g;
+      float o[8];
+      eight<NB>(acc, i, t, g, o);
+      if (splits > 1) {
+        if (s0 >= steps) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = 0.f;
+        }
+        float4* to = reinterpret_cast<float4*>(part + ((sl * na + td) * nb + tt) * (TN * kTileA) +
+                                               in * kTileA + 128 * wm + 32 * i + 8 * g);
+        to[0] = make_float4(o[0], o[1], o[2], o[3]);
+        to[1] = make_float4(o[4], o[5], o[6], o[7]);
+      } else if (col < p.dim) {
+        *reinterpret_cast<uint4*>(dh + p.r.src[p.row0 + row] * ldd + col) = pack8(o);
+      }
+    }
+  }
+}
+
+// Adds the slices in order and rounds once; a thread 8 values of a row.
+__global__ __launch_bounds__(kThreads) void k_head_dh_sum(HeadPanel p, int TN, const float* part,
+                                                          uint16_t* dh, int64_t ldd) {
+  const int n = panel_rows(p);
+  int64_t na, nb;
+  int splits;
+  dh_plan(p, n, TN, na, nb, splits);
+  const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int per = p.dim / 8;
+  const int64_t row = k / per;
+  const int col = (int)(k - row * per) * 8;
+  if (splits == 1 || row >= n) return;
+  const float* from = part + ((col / kTileA) * nb + row / TN) * (TN * kTileA) +
+                      (row % TN) * kTileA + col % kTileA;
+  const int64_t step = na * nb * (TN * kTileA);
+  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 a = *reinterpret_cast<const float4*>(from + s * step);
+    const float4 b = *reinterpret_cast<const float4*>(from + s * step + 4);
+    o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
+    o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
+  }
+  *reinterpret_cast<uint4*>(dh + p.r.src[p.row0 + row] * ldd + col) = pack8(o);
+}
+
+// ------------------------------------------------------------------------ dW
+// A = h (transposed by the reads), B = dz (likewise); inner index the rows.
+__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
+                          amdgpu_waves_per_eu(1, 1)))
+void k_head_dw(HeadPanel p, float* sum, int first, int last, uint16_t* dw, int64_t ldo) {
+  constexpr int TN = 256, NB = TN / 32;
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
+  const int n = panel_rows(p);
+  int64_t td, tv;
+  if (!tile_of(blockIdx.x, ceil_div(p.dim, kTileA), ceil_div(p.vocab, TN), td, tv)) return;
+  const int64_t cols = head_cols(p.vocab), steps = ceil_div(n, kStep);
+  const Operand A{p.r.h + p.row0 * p.dim, p.dim, p.dim, steps * kStep};
+  const Operand B{p.e, cols, cols, steps * kStep};
+  f32x4_t acc[8][NB];
+  if (steps > 0) {
+    tile_loop<TN, true, true>(acc, lds, A, td * kTileA, B, tv * TN, 0, steps);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int t = 0; t < NB; ++t) {
+        acc[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        asm volatile("" : "+a"(acc[i][t]));
+      }
+    mfma_settle();
+  }
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv & 1, wn = wv >> 1;
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+    const int64_t v = tv * TN + TN / 2 * wn + 16 * t + j;
+    if (v >= p.vocab) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t col = td * kTileA + 128 * wm + 32 * i + 8 * g;
+      if (col >= p.dim) continue;
+      float o[8];
+      eight<NB>(acc, i, t, g, o);
+      if (sum) {
+        float4* at = reinterpret_cast<float4*>(sum + v * p.dim + col);
+        if (!first) {
+          const float4 a = at[0], b = at[1];
+          o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
+          o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
+        }
+        if (!last) {
+          at[0] = make_float4(o[0], o[1], o[2], o[3]);
+          at[1] = make_float4(o[4], o[5], o[6], o[7]);
+        }
+      }
+      if (last) *reinterpret_cast<uint4*>(dw + v * ldo + col) = pack8(o);
+    }
+  }
+}
+
+unsigned grid8(int64_t tiles) { return (unsigned)(ceil_div(tiles, 8) * 8); }
+
+template <int TN>
+hipError_t launch_logits(const HeadPanel& p, int mode, hipStream_t s) {
+  const dim3 grid(grid8(ceil_div(p.vocab, kTileA) * ceil_div(p.rows, TN)));
+  if (mode == HEAD_STATS)
+    return launch_kernel(k_head_logits<TN, HEAD_STATS>, grid, dim3(kThreads), s, p);
+  if (mode == HEAD_EXP) return launch_kernel(k_head_logits<TN, HEAD_EXP>, grid, dim3(kThreads), s, p);
+  return launch_kernel(k_head_logits<TN, HEAD_DZ>, grid, dim3(kThreads), s, p);
+}
+
+// Workgroups of dh, and tiles of its partial sums, that any number of rows up to
+// the panel's can ask for.
+struct DhSize {
+  int64_t grid, slots;
+};
+DhSize dh_size(int64_t rows, int dim, int64_t vocab, int tile) {
+  const int64_t na = ceil_div(dim, kTileA), steps = ceil_div(vocab, kStep);
+  const int64_t all = ceil_div(rows, tile);
+  DhSize d{ceil_div(na * all, 8) * 8, 0};   // uncut
+  for (int64_t nb = 1; nb <= all && na * nb <= kMaxSlots; ++nb) {
+    const int64_t sp = dh_splits(na * nb, steps);
+    if (ceil_div(na * nb, 8) * 8 * sp > d.grid) d.grid = ceil_div(na * nb, 8) * 8 * sp;
+    if (sp > 1 && na * nb * sp > d.slots) d.slots = na * nb * sp;
+  }
+  return d;
+}
+
+}  // namespace
+
+int head_tile(int64_t rows) { return rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+
+hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t s) {
+  // (a workgroup also without rows: it writes how many there are)
+  const int64_t per = a.rows > 512 ? ceil_div(a.rows, 512) : 1;
+  const int64_t groups = a.rows > 0 ? ceil_div(a.rows, per) : 1;
+  return launch_kernel(k_head_pack, dim3((unsigned)groups), dim3(kThreads), s, a, per);
+}
+
+hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, hipStream_t s) {
+  return tile == 64 ? launch_logits<64>(p, mode, s)
+                    : tile == 128 ? launch_logits<128>(p, mode, s) : launch_logits<256>(p, mode, s);
+}
+
+hipError_t launch_head_join(const HeadPanel& p, int kind, double* lp, float* logp, HeadStat* stat,
+                            hipStream_t s) {
+  return launch_kernel(k_head_join, dim3((unsigned)ceil_div(p.rows, 64)), dim3(64 * kJoinWaves), s,
+                       p, kind, lp, logp, stat);
+}
+
+hipError_t launch_head_loss(const int32_t* n, const double* lp, int mean, float* loss,
+                            hipStream_t s) {
+  return launch_kernel(k_head_loss, dim3(1), dim3(1024), s, n, lp, mean, loss);
+}
+
+hipError_t launch_head_dz(const HeadPanel& p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.rows / kDzRows),
+                  (unsigned)ceil_div(head_cols(p.vocab), kThreads * 8));
+  return launch_kernel(k_head_dz, grid, dim3(kThreads), s, p);
+}
+
+size_t head_dh_floats(int64_t rows, int dim, int64_t vocab, int tile) {
+  return (size_t)dh_size(rows, dim, vocab, tile).slots * tile * kTileA;
+}
+
+hipError_t launch_head_dh(const HeadPanel& p, int tile, float* part, uint16_t* dh, int64_t ldd,
+                          hipStream_t s) {
+  const DhSize d = dh_size(p.rows, p.dim, p.vocab, tile);
+  const dim3 grid((unsigned)d.grid);
+  hipError_t e = tile == 64 ? launch_kernel(k_head_dh<64>, grid, dim3(kThreads), s, p, part, dh, ldd)
+                 : tile == 128
+                     ? launch_kernel(k_head_dh<128>, grid, dim3(kThreads), s, p, part, dh, ldd)
+                     : launch_kernel(k_head_dh<256>, grid, dim3(kThreads), s, p, part, dh, ldd);
+  if (e != hipSuccess || d.slots == 0) return e;
+  return launch_kernel(k_head_dh_sum, dim3((unsigned)ceil_div((int64_t)p.rows * p.dim / 8, kThreads)),
+                       dim3(kThreads), s, p, tile, part, dh, ldd);
+}
+
+hipError_t launch_head_dw(const HeadPanel& p, float* acc, int first, int last, uint16_t* dw,
+                          int64_t ldo, hipStream_t s) {
+  const dim3 grid(grid8(ceil_div(p.dim, kTileA) * ceil_div(p.vocab, 256)));
+  return launch_kernel(k_head_dw, grid, dim3(kThreads), s, p, acc, first, last, dw, ldo);
+}
+
+}  // namespace qnf4

@@ -652,6 +652,71 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
                                size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The language-model head without its logits: the log-probabilities above and
+ * the softmax cross entropy straight from hidden states h [rows, dim] and the
+ * head's weight W [vocab, dim] (both bf16), z_t = W h_t in float32.  The logits
+ * of a step are its largest tensor; here they are never written.  At most
+ * 2^29 row x vocabulary elements (at least 256 rows) are in work at a time,
+ * and of those a call that returns gradients keeps 16-bit exponentials.
+ *
+ * Rows, labels and their refusals follow qlora_logits: a negative label means
+ * no target (logp 0, gradient row zero; whatever the hidden row holds, NaN
+ * included, reaches nothing, and the row costs no product), a label >= vocab
+ * gives logp NaN, which reaches the loss, the row's gradient and all of dW.
+ * Sums over the vocabulary are float32 in a tile and float64 between tiles and
+ * after the logarithm.  dz is rounded to bf16 (the matrix cores' type) once
+ * before the products that give dh and dW, whose sums are float32 and rounded
+ * once to bf16.  Results are identical run to run. */
+typedef struct {
+  const qlora_bf16* hidden;  /* device, [rows] x ld_hidden; may be NULL when rows == 0 */
+  int64_t rows;              /* < 2^24 */
+  int64_t dim;               /* a multiple of 64, <= 65536 */
+  int64_t ld_hidden;         /* row strides: multiples of 8, >= dim, < 2^22 */
+  const qlora_bf16* weight;  /* device, [vocab] x ld_weight */
+  int64_t vocab;             /* <= 2^22 */
+  int64_t ld_weight;
+  const int64_t* labels;     /* device, [rows] */
+} qlora_head;
+/* hidden and weight are 16-byte aligned, as are the gradients; a gradient's row
+ * stride (ldd, ldo) is a multiple of 8, >= dim, < 2^22.  dhidden may be hidden
+ * itself (then ldd == ld_hidden), overwritten in place; nothing else may overlap. */
+#define QLORA_HEAD_DHIDDEN 1
+#define QLORA_HEAD_DWEIGHT 2
+#define QLORA_HEAD_MEAN 0
+#define QLORA_HEAD_SUM 1
+
+/* Bytes of workspace the calls below need; grads: the gradients the call
+ * returns, QLORA_HEAD_DHIDDEN | QLORA_HEAD_DWEIGHT (0: none).  0 for sizes they
+ * refuse. */
+size_t qlora_head_workspace_bytes(const qlora_head* h, int32_t grads);
+
+/* Log-probabilities of the targets: logp float32 [rows].  stats (nullable)
+ * float32 [rows][2] receives each row's log sum_v exp(z_v) and the target's
+ * 1 - p (0, 0 without target) for the backward. */
+qlora_status qlora_head_logprobs(const qlora_head* h, float* logp, float* stats, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* Backward of the above for weights w float32 [rows] (dLoss / dlogp, as the
+ * preference and policy losses give them), g = grad_scale[0] (device; NULL = 1):
+ *     dz_tv = g w_t (1[v == y_t] - p_tv),
+ *     dhidden = dz . W [rows, dim],   dweight = dz^T . h [vocab, dim]   (bf16,
+ * each nullable, not both).  The logits are formed again.  A row without target,
+ * or with w == 0, gets zeros and is not read. */
+qlora_status qlora_head_logprobs_bwd(const qlora_head* h, const float* stats, const float* w,
+                                     const float* grad_scale, qlora_bf16* dhidden, int64_t ldd,
+                                     qlora_bf16* dweight, int64_t ldo, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* Cross entropy: loss float32 [1] = -(sum of logp) over the targets, divided by
+ * their number with QLORA_HEAD_MEAN (0 when there is none); logp (nullable) float32
+ * [rows].  dhidden and dweight (each nullable) receive the gradients for an
+ * upstream gradient of 1, from one product of h and W. */
+qlora_status qlora_head_cross_entropy(const qlora_head* h, int32_t reduction, float* loss,
+                                      float* logp, qlora_bf16* dhidden, int64_t ldd,
+                                      qlora_bf16* dweight, int64_t ldo, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/* ------------------------------------------------------------------------
  * Kernel timing (benchmark instrumentation; not part of the method).
  * Between qlora_trace_begin and qlora_trace_end, every launch of a kernel whose
  * bit is set in `kernel_mask` (1 << qlora_kernel) records its own start and end
