@@ -42,6 +42,7 @@ EXPORTS = [
     "qlora_preference_loss", "qlora_policy_loss",
     "qlora_head_workspace_bytes", "qlora_head_logprobs", "qlora_head_logprobs_bwd",
     "qlora_head_cross_entropy",
+    "qlora_muon_workspace_bytes", "qlora_orthogonalize", "qlora_muon_step",
     "qlora_trace_begin", "qlora_trace_pause", "qlora_trace_end",
 ]
 KERNELS = {"fwd_gemm": 0, "dx_gemm": 1, "quantize": 2, "dequant": 3, "gemv": 4,
@@ -50,6 +51,8 @@ ADAMW8_BLOCK = 256
 ACT8_BLOCK = 64
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}      # QLORA_PREF_*
 POLICY_REDUCTIONS = {"token": 0, "sequence": 1}              # QLORA_POLICY_*
+MUON_ADJUST = {None: 0, "shape": 1, "rms": 2}                # QLORA_MUON_*
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
 HEAD_REDUCTIONS = {"mean": 0, "sum": 1}                      # QLORA_HEAD_MEAN, _SUM
 
 
@@ -118,6 +121,32 @@ class HeadDescriptor(ctypes.Structure):
                 ("ld_hidden", ctypes.c_int64), ("weight", ctypes.c_void_p),
                 ("vocab", ctypes.c_int64), ("ld_weight", ctypes.c_int64),
                 ("labels", ctypes.c_void_p)]
+
+
+class NewtonSchulz(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double),
+                ("eps", ctypes.c_double), ("steps", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class OrthoMatrix(ctypes.Structure):
+    _fields_ = [("input", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld_in", ctypes.c_int64), ("ld_out", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("reserved", ctypes.c_int32)]
+
+
+class MuonTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("momentum", ctypes.c_void_p), ("param_bf16", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld_param", ctypes.c_int64),
+                ("ld_grad", ctypes.c_int64), ("ld_momentum", ctypes.c_int64),
+                ("ld_bf16", ctypes.c_int64), ("grad_dtype", ctypes.c_int),
+                ("reserved", ctypes.c_int32)]
+
+
+class MuonHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("ns", NewtonSchulz),
+                ("nesterov", ctypes.c_int32), ("adjust", ctypes.c_int32)]
 
 
 _lib = None
@@ -193,6 +222,10 @@ def lib():
         L.qlora_head_logprobs.argtypes = [H, P, P, P, SZ, P]
         L.qlora_head_logprobs_bwd.argtypes = [H, P, P, P, P, I64, P, I64, P, SZ, P]
         L.qlora_head_cross_entropy.argtypes = [H, I32, P, P, P, I64, P, I64, P, SZ, P]
+        L.qlora_muon_workspace_bytes.argtypes = [P, P, I32]
+        L.qlora_muon_workspace_bytes.restype = SZ
+        L.qlora_orthogonalize.argtypes = [ctypes.POINTER(NewtonSchulz), P, I32, P, SZ, P]
+        L.qlora_muon_step.argtypes = [ctypes.POINTER(MuonHparams), P, I32, P, SZ, P]
         L.qlora_host_state_alloc.argtypes = [SZ, P]
         L.qlora_host_state_free.argtypes = [P]
         L.qlora_trace_begin.argtypes = [ctypes.c_uint32, I32]
@@ -763,6 +796,136 @@ def _on(what: str, first, *more):
     for t in more:
         _require(t is None or t.device == d, what, "tensors on different devices")
     return _HERE_ALREADY if d.index == torch.cuda.current_device() else torch.cuda.device(d)
+
+
+def _matrix(what, t, dtypes, shape, name):
+    """Row stride of a 2-D tensor with dense rows of one of the dtypes."""
+    _require(t.dim() == 2 and t.dtype in dtypes and (shape is None or t.shape == shape) and
+             (t.stride(1) == 1 or t.shape[1] <= 1), what,
+             "%s must be a matrix of %s with dense rows", name, dtypes)
+    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+
+
+def qlora_muon_workspace_bytes(shapes) -> int:
+    """Workspace bytes for matrices of these (rows, cols)."""
+    shapes = list(shapes)
+    rows = (ctypes.c_int64 * max(len(shapes), 1))(*[r for r, _ in shapes])
+    cols = (ctypes.c_int64 * max(len(shapes), 1))(*[c for _, c in shapes])
+    return int(lib().qlora_muon_workspace_bytes(rows, cols, len(shapes)))
+
+
+def _newton_schulz(what, coefficients, steps, eps):
+    _require(len(coefficients) == 3, what, "three coefficients")
+    return NewtonSchulz(*coefficients, eps, steps, 0)
+
+
+def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_SCHULZ,
+                        eps: float = 1e-7, ws=None):
+    """Each float32 or bf16 matrix (shorter side <= 128, rows of any stride) moved
+    towards singular values of 1 by Newton-Schulz steps.  Returns the list of
+    results, in `out` (which may be the matrices) or new tensors."""
+    what = "qlora_orthogonalize"
+    matrices = list(matrices)
+    ns = _newton_schulz(what, coefficients, steps, eps)
+    if out is None:
+        out = [torch.empty(m.shape, dtype=m.dtype, device=m.device) for m in matrices]
+    out = list(out)
+    _require(len(out) == len(matrices), what, "as many outputs as matrices")
+    if not matrices:
+        return out
+    arr = (OrthoMatrix * len(matrices))()
+    for a, m, o in zip(arr, matrices, out):
+        ld = _matrix(what, m, (torch.float32, torch.bfloat16), None, "each")
+        a.ld_in, a.ld_out = ld, _matrix(what, o, (m.dtype,), m.shape, "its output")
+        a.input, a.out, (a.rows, a.cols) = m.data_ptr(), o.data_ptr(), m.shape
+        a.dtype = QLORA_BF16 if m.dtype == torch.bfloat16 else QLORA_F32
+    dev = matrices[0].device
+    if ws is None:
+        ws = workspace(qlora_muon_workspace_bytes([m.shape for m in matrices]), dev)
+    with _on(what, matrices[0], ws, *matrices[1:], *out):
+        _check(lib().qlora_orthogonalize(ctypes.byref(ns), arr, len(matrices), _ptr(ws),
+                                         ws.numel(), _stream()), what)
+    return out
+
+
+class MuonPlan:
+    """The tensors of a qlora_muon_step and its workspace, checked and laid out
+    once: a list of (param, grad, momentum, param_bf16 or None), matrices whose
+    shorter side is <= 128, rows of any stride; param and momentum float32, grad
+    float32 or bf16.  The plan holds the tensors and finds their memory anew each
+    step; gradients that are other tensors every time go to the step itself.  Steps
+    that share a plan must be ordered on one stream."""
+
+    def __init__(self, tensors):
+        what = "MuonPlan"
+        self.tensors = [tuple(t) for t in tensors]
+        self.array = (MuonTensor * max(len(self.tensors), 1))()
+        f32 = (torch.float32,)
+        shapes = []
+        for a, t in zip(self.array, self.tensors):
+            _require(len(t) == 4, what, "(param, grad, momentum, param_bf16) tuples")
+            p, g, m, pb = t
+            a.ld_param = _matrix(what, p, f32, None, "param")
+            a.ld_grad = _matrix(what, g, (torch.float32, torch.bfloat16), p.shape, "grad")
+            a.ld_momentum = _matrix(what, m, f32, p.shape, "momentum")
+            if pb is not None:
+                a.ld_bf16 = _matrix(what, pb, (torch.bfloat16,), p.shape, "param_bf16")
+            a.rows, a.cols = p.shape
+            a.grad_dtype = QLORA_BF16 if g.dtype == torch.bfloat16 else QLORA_F32
+            shapes.append(tuple(p.shape))
+        self._collect()
+        self._layout = [(x.dtype, x.shape, x.stride(), x.device) for x in self._flat]
+        self.ws = None
+        if self._flat:
+            with _on(what, *self._flat):
+                pass
+            need = qlora_muon_workspace_bytes(shapes)
+            _require(need > 0 or all(0 in s for s in shapes), what,
+                     "a matrix's shorter side is above %d", MAX_RANK)
+            self.ws = workspace(need, self._flat[0].device)
+
+    def _collect(self):
+        self._flat = [x for t in self.tensors for x in t if x is not None]
+        self._at = None
+
+    def _bind(self, what, grads):
+        """The tensors' addresses as they are now."""
+        if grads is not None:
+            grads = list(grads)
+            _require(len(grads) == len(self.tensors), what, "as many gradients as tensors")
+            if any(t[1] is not g for t, g in zip(self.tensors, grads)):
+                self.tensors = [(t[0], g, *t[2:]) for t, g in zip(self.tensors, grads)]
+                self._collect()
+        at = [x.data_ptr() for x in self._flat]
+        if at == self._at:
+            return
+        for x, kept in zip(self._flat, self._layout):
+            _require((x.dtype, x.shape, x.stride(), x.device) == kept, what,
+                     "a tensor of another type, shape, stride or device than the plan's")
+        for a, (p, g, m, pb) in zip(self.array, self.tensors):
+            a.param, a.grad, a.momentum = p.data_ptr(), g.data_ptr(), m.data_ptr()
+            a.param_bf16 = None if pb is None else pb.data_ptr()
+        self._at = at
+
+
+def qlora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool = True,
+                    weight_decay: float = 0.0, adjust: Optional[str] = "shape", steps: int = 5,
+                    coefficients=NEWTON_SCHULZ, eps: float = 1e-7, grads=None):
+    """One step of the orthogonalised update on a MuonPlan (or the list it is made
+    of).  grads: this step's gradients in place of the plan's, of the same types,
+    shapes and strides (kept until others come).  adjust: the step's factor, "shape" sqrt(max(1, rows / cols)), "rms"
+    0.2 sqrt(max(rows, cols)) or None."""
+    what = "qlora_muon_step"
+    plan = tensors if isinstance(tensors, MuonPlan) else MuonPlan(tensors)
+    _require(adjust in MUON_ADJUST, what, "unknown adjust")
+    h = MuonHparams(lr, momentum, weight_decay, _newton_schulz(what, coefficients, steps, eps),
+                    int(nesterov), MUON_ADJUST[adjust])
+    if not plan._flat:
+        return
+    plan._bind(what, grads)
+    with _on(what, plan.ws):
+        _check(lib().qlora_muon_step(ctypes.byref(h), plan.array, len(plan.tensors),
+                                     _ptr(plan.ws), plan.ws.numel(), _stream()), what)
 
 
 class Act8Tensor:

@@ -1,0 +1,60 @@
+// Launcher interface of the orthogonalised update (Newton-Schulz products).
+#pragma once
+
+#include "nf4_common.h"
+
+namespace qnf4 {
+
+// One matrix: `in` is the gradient (of a step) or the update itself; m the momentum
+// (null: none); `out` the parameter of a step, with its bf16 copy pb (nullable), or
+// what receives the orthogonalised matrix.  Row strides in elements.
+struct MuonTensor {
+  const void* in;
+  float* m;
+  void* out;
+  uint16_t* pb;
+  int32_t rows, cols;
+  int32_t ldi, ldm, ldo, ldb;
+  float scale;        // of a step: lr times the shape's factor
+  int32_t bf16;       // type of `in` (and of `out` without a step)
+  int32_t wg, slice;  // its first workgroup in the call, long indices of each
+  uint32_t part, q;   // its partial products and polynomial, in tiles of 256 doubles
+};
+constexpr int kMuonBatch = 48;   // per launch: 3.8 KB of kernel arguments
+struct MuonBatch {
+  int count, first;              // index of t[0] in the call
+  MuonTensor t[kMuonBatch];
+};
+struct MuonHyper {
+  float mu, one_minus_mu, decay;
+  int nesterov, step, steps;     // step: update parameters; else write the matrix
+  double a, b, c, eps;
+};
+struct MuonScratch {
+  MuonTensor* t;                 // [tensors]
+  int32_t* owner;                // [workgroups] tensor of each
+  double* part;
+  double* q;
+};
+
+// Padded short side (16, 32, 64 or 128), long indices of a chunk, and 16 x 16 tiles of
+// the products' upper triangle.
+inline __host__ __device__ int muon_pad(int s) {
+  return s <= 16 ? 16 : s <= 32 ? 32 : s <= 64 ? 64 : 128;
+}
+inline __host__ __device__ int muon_chunk(int sp) { return 4096 / sp; }
+inline __host__ __device__ int muon_tiles(int sp) { return (sp / 16) * (sp / 16 + 1) / 2; }
+// Long indices of a workgroup, for a call of `total` elements.
+int muon_slice(int sp, int64_t total);
+
+// m, and the slices' products of a batch's tensors whose padded short side is sp;
+// the table of these goes to the scratch
+hipError_t launch_muon_gram(const MuonBatch& b, int sp, int wgs, const MuonHyper& h,
+                            const MuonScratch& s, hipStream_t st);
+// polynomials, then the update, of the call's tensors of that padded short side
+hipError_t launch_muon_poly(int count, int sp, const MuonHyper& h, const MuonScratch& s,
+                            hipStream_t st);
+hipError_t launch_muon_apply(int sp, int wgs, const MuonHyper& h, const MuonScratch& s,
+                             hipStream_t st);
+
+}  // namespace qnf4

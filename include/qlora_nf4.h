@@ -460,6 +460,72 @@ typedef struct {
 qlora_status qlora_adamw8_step(const qlora_adamw_hparams* h, int64_t step,
                                const qlora_adamw8_tensor* tensors, int32_t count, void* stream);
 
+/* The orthogonalised update (as the Muon optimiser takes it): the momentum of a
+ * gradient moved towards the nearest matrix of singular values 1 by Newton-Schulz
+ * steps
+ *     X_0 = U / max(|U|_F, eps),   X <- a X + b (X X^T) X + c (X X^T)^2 X
+ * (the products on the shorter side).  An adapter's shorter side is its rank,
+ * <= 128: the steps run on its product matrix, in float64, and U is read once
+ * more to be multiplied by their polynomial, also in float64.  The result is
+ * rounded once (to float32 in a step).  Orders are fixed: results are identical
+ * run to run.  A NaN or an infinity in U makes the whole result NaN. */
+typedef struct {
+  double a, b, c;      /* 3.4445, -4.7750, 2.0315 are the usual ones */
+  double eps;          /* > 0; usually 1e-7 */
+  int32_t steps;       /* 1 .. 32; usually 5 */
+  int32_t reserved;    /* must be 0 */
+} qlora_newton_schulz;
+
+/* Bytes of workspace the two calls below need for matrices of these shapes; 0 for
+ * shapes they refuse: the shorter side above 128, a side or a row stride of 2^30
+ * or more, or 2^24 or more slices of 4096 to 65536 elements. */
+size_t qlora_muon_workspace_bytes(const int64_t* rows, const int64_t* cols, int32_t count);
+
+typedef struct {
+  const void* in;      /* [rows] x ld_in */
+  void* out;           /* [rows] x ld_out; may be `in` (then ld_out == ld_in) */
+  int64_t rows, cols, ld_in, ld_out;
+  qlora_dtype dtype;   /* of both */
+  int32_t reserved;    /* must be 0 */
+} qlora_ortho_matrix;
+/* Orthogonalises `count` matrices, in 3 launches for up to 48 of one rank.  A
+ * matrix without elements is skipped; a zero matrix gives zeros. */
+qlora_status qlora_orthogonalize(const qlora_newton_schulz* ns, const qlora_ortho_matrix* m,
+                                 int32_t count, void* ws, size_t ws_bytes, void* stream);
+
+/* One step on adapter matrices (float32 masters, momentum in float32):
+ *     m <- mu m + (1 - mu) g,    U = m, or mu m + (1 - mu) g with nesterov
+ *     p <- p (1 - lr weight_decay) - lr f O(U),   bf16(p) to param_bf16
+ * with f = 1 (QLORA_MUON_PLAIN), sqrt(max(1, rows / cols)) (_SHAPE) or
+ * 0.2 sqrt(max(rows, cols)) (_RMS).  Each float32 coefficient is formed in double
+ * and rounded once.  Rows of any stride, so that one projection's B in a wider
+ * grouped matrix is updated in its place. */
+#define QLORA_MUON_PLAIN 0
+#define QLORA_MUON_SHAPE 1
+#define QLORA_MUON_RMS 2
+typedef struct {
+  float* param;            /* [rows] x ld_param, updated in place */
+  const void* grad;        /* [rows] x ld_grad, of grad_dtype */
+  float* momentum;         /* [rows] x ld_momentum, updated in place */
+  qlora_bf16* param_bf16;  /* nullable, [rows] x ld_bf16 */
+  int64_t rows, cols;
+  int64_t ld_param, ld_grad, ld_momentum, ld_bf16;
+  qlora_dtype grad_dtype;
+  int32_t reserved;        /* must be 0 */
+} qlora_muon_tensor;
+typedef struct {
+  double lr;               /* >= 0 */
+  double momentum;         /* mu, in [0, 1) */
+  double weight_decay;     /* >= 0 */
+  qlora_newton_schulz ns;
+  int32_t nesterov;        /* 0 or 1 */
+  int32_t adjust;          /* QLORA_MUON_* */
+} qlora_muon_hparams;
+/* Pointers are aligned to their types (16 bytes and strides that are multiples
+ * of 4 take the vector path); tensors must not overlap. */
+qlora_status qlora_muon_step(const qlora_muon_hparams* h, const qlora_muon_tensor* tensors,
+                             int32_t count, void* ws, size_t ws_bytes, void* stream);
+
 /* Optimiser state kept in host memory ("QLoRA: Fine-Tuning a 70B on One
  * GPU", section "Paged Optimizers": host RAM serves as an extension of device
  * memory for the optimiser statistics).  Allocates `bytes` of pinned,
