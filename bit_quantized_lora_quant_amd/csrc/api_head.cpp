@@ -74,7 +74,7 @@ HeadWs head_layout(const qlora_head* h, bool dh, bool dw) {
   L.h = take(all * h->dim * 2);
   L.src = take(all * 4);
   L.y = take(all * 4);
-  L.n = take(4);
+  L.n = take(8);
   L.stat = take(grad ? all * sizeof(HeadStat) : 0);
   L.w = take(grad ? all * 4 : 0);
   L.lp = take(all * 8);
@@ -102,14 +102,23 @@ HeadPanel panel(const qlora_head* h, void* ws, const HeadWs& L) {
   p.vocab = h->vocab;
   p.part = at<HeadPart>(ws, L.part);
   p.zy = at<float>(ws, L.zy);
+  p.splits = head_dh_splits(p.rows, p.dim, p.vocab, head_tile(h->rows));
   p.e = at<uint16_t>(ws, L.e);
   return p;
 }
 
 HeadPackArgs pack_args(const qlora_head* h, const HeadPanel& p) {
-  return HeadPackArgs{h->hidden, h->ld_hidden, h->rows, (int)h->dim, h->vocab, h->labels,
-                      nullptr,   nullptr,      nullptr, p.r,         nullptr,  nullptr,
-                      nullptr,   0};
+  HeadPackArgs a = {};
+  a.hidden = h->hidden;
+  a.ldh = h->ld_hidden;
+  a.rows = h->rows;
+  a.dim = (int)h->dim;
+  a.vocab = h->vocab;
+  a.labels = h->labels;
+  a.to = p.r;
+  a.panel = p.rows;
+  a.tile = head_tile(h->rows);
+  return a;
 }
 
 // dh and dW of a panel whose e holds dz
@@ -178,6 +187,7 @@ qlora_status qlora_head_logprobs_bwd(const qlora_head* h, const float* stats, co
   a.stat = reinterpret_cast<const HeadStat*>(stats);
   a.dh = dhidden;
   a.ldd = ldd;
+  a.pad = dweight != nullptr;
   const int tile = head_tile(h->rows);
   hipError_t e = launch_head_pack(a, s);
   do {
@@ -206,6 +216,7 @@ qlora_status qlora_head_cross_entropy(const qlora_head* h, int32_t reduction, fl
   a.logp = logp;
   a.dh = dhidden;
   a.ldd = ldd;
+  a.pad = dweight != nullptr;
   const int tile = head_tile(h->rows), mean = reduction == QLORA_HEAD_MEAN;
   const bool grad = dhidden || dweight;
   hipError_t e = launch_head_pack(a, s);

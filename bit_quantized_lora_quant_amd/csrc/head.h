@@ -23,7 +23,7 @@ struct HeadRows {
   uint16_t* h;
   int32_t* src;
   int32_t* y;
-  int32_t* n;         // [1] how many
+  int32_t* n;         // [2] how many, and the slices of dh in a panel they do not fill
   HeadStat* stat;
   float* w;
 };
@@ -38,6 +38,8 @@ struct HeadPackArgs {
   const float* w_scale;    // nullable, [1]
   const HeadStat* stat;    // with w
   HeadRows to;
+  int panel, tile;         // rows of a panel and of a tile
+  int pad;                 // zero rows behind the last, for dW
   // rows without a target, each nullable
   float* logp;
   HeadStat* stat_out;
@@ -57,10 +59,12 @@ struct HeadPanel {
   int64_t ldw, vocab;
   HeadPart* part;      // [vocab tiles * 2][rows]
   float* zy;           // [rows] the target's logit
+  int splits;          // slices of dh in a full panel
   uint16_t* e;         // [rows][head_cols(vocab)] exponentials (fp16), then dz (bf16)
 };
 // Columns of a panel's row.
 __host__ __device__ inline int64_t head_cols(int64_t vocab) { return ceil_div(vocab, 256) * 256; }
+int head_dh_splits(int64_t rows, int dim, int64_t vocab, int tile);
 // Rows of tokens per workgroup tile (64, 128 or 256) for a call of this many rows.
 int head_tile(int64_t rows);
 

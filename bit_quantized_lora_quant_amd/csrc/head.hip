@@ -17,16 +17,18 @@
 // All three products share one tile loop, bound by the matrix cores: 256 values of
 // the output's contiguous index (MFMA rows: a lane then holds eight
 // neighbours of one output row, a 16-byte store) x 64 to 256 of its rows, 64 inner
-// indices a step, four waves of 128 x half the rows.  Accumulators stay in AGPRs;
-// both tiles stream into LDS by DMA while the step before them is multiplied, and
-// operands are read half a step ahead.  Operands whose inner index is not
+// indices a step, eight waves of 128 x a quarter of the rows.  Accumulators stay in AGPRs;
+// both tiles stream into LDS by DMA, and operands are read half a step ahead.  Operands whose inner index is not
 // contiguous (W in dh, both in dW) are transposed by the LDS reads themselves.
 #include "head.h"
+
+#include <type_traits>
 
 namespace qnf4 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;           // of the streaming kernels
+constexpr int kWavesB = 4, kWaves = 2 * kWavesB, kGemmThreads = 64 * kWaves;
 constexpr int kStep = 64;               // inner indices per step
 constexpr int kTileA = 256;             // values of the output's contiguous index
 constexpr int kMaxSlots = 1024;         // partial tiles of dh
@@ -39,6 +41,35 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float exp_diff(float z, float m) {
   return __builtin_amdgcn_exp2f((z - m) * kLog2e);
+}
+
+// ----------------------------------------------------------------- slices of dh
+// The inner index is the vocabulary, long: with fewer tiles than CUs it is cut
+// into the number of slices that fills whole rounds best, which hangs on how
+// many rows there are and so is found here.  A slice's epilogue and its part of
+// the sum that follows cost about as much as 24 steps.
+__host__ __device__ inline uint32_t dh_cost(uint32_t tiles, uint32_t steps, uint32_t splits) {
+  const uint32_t each = (steps + splits - 1) / splits;
+  if (splits > 1 && (each < 6 || tiles * splits > kMaxSlots)) return UINT32_MAX;
+  return (tiles * splits + 255) / 256 * (each + (splits > 1 ? 24 : 4));
+}
+int dh_splits(int64_t tiles, int64_t steps) {
+  if (tiles > kMaxSlots) return 1;
+  int best = 1;
+  for (int s = 2; s <= kMaxSplits; ++s)
+    if (dh_cost(tiles, steps, s) < dh_cost(tiles, steps, best)) best = s;
+  return best;
+}
+// the same by a wave, a candidate a lane
+__device__ __forceinline__ int dh_splits_wave(int64_t tiles, int64_t steps, int lane) {
+  if (tiles > kMaxSlots) return 1;
+  uint64_t c = (uint64_t)dh_cost((uint32_t)tiles, (uint32_t)steps, lane + 1) << 8 | (lane + 1);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    const uint64_t o = __shfl_xor(c, d);
+    c = o < c ? o : c;
+  }
+  return (int)(c & 255);
 }
 
 // ---------------------------------------------------------------- packing rows
@@ -102,7 +133,17 @@ __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t 
     at += wave_count[0] + wave_count[1] + wave_count[2] + wave_count[3];
   }
   if (blockIdx.x != gridDim.x - 1) return;
-  if (tid == 0) *a.to.n = at;
+  // how many, and the slices of dh over a last panel that they do not fill
+  if (wv == 0) {
+    const int rest = at % a.panel;
+    const int sp = dh_splits_wave(ceil_div(a.dim, kTileA) * ceil_div(rest, a.tile),
+                                  ceil_div(a.vocab, kStep), lane);
+    if (lane == 0) {
+      a.to.n[0] = at;
+      a.to.n[1] = sp;
+    }
+  }
+  if (!a.pad) return;
   // zeros up to a whole step: inner indices of dW
   for (int64_t q = at + wv; q < ceil_div(at, kStep) * kStep; q += 4) {
     uint4* out = reinterpret_cast<uint4*>(a.to.h + q * a.dim);
@@ -117,6 +158,17 @@ __device__ __forceinline__ void mfma_acc(f32x4_t& acc, const u32x4_t& a, const u
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 __device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7"); }
+
+// f(I), ..., f(N - 1) with constants (the unroller gives up on the step's body)
+template <int I, int N, typename F>
+__device__ __forceinline__ void static_for(const F& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<I + 1, N>(f);
+  }
+}
+
+constexpr int min_of(int a, int b) { return a < b ? a : b; }
 
 template <int N>
 __device__ __forceinline__ void wait_vmem() {
@@ -142,13 +194,13 @@ struct Operand {
 
 // LDS of a step.  TR false: [R][64] values, 128 bytes a row, 16-byte chunk c of row
 // r at c ^ hash(r); TR true: [64][R], 2 R bytes an inner index k, chunk c at
-// c ^ hash(k).  The hashes put the addresses that a read's lanes use together on
-// different banks: A's MFMA row 4 q + v of tile (i, h) is index 32 i + 8 q + 4 h + v
-// (so that a lane's results of h = 0, 1 are neighbours), B's is in order.
+// c ^ hash(k).  The hashes spread what the lanes of a read use together over all 64
+// banks: A's MFMA row 4 q + v of tile (i, h) is index 32 i + 8 q + 4 h + v (so that
+// a lane's results of h = 0, 1 are neighbours), B's is in order.
 template <int R, bool TR, bool IS_A>
 struct Tile {
   static constexpr int kBytes = R * kStep * 2;
-  static constexpr int kLoads = kBytes / 1024 / 4;     // per wave and step
+  static constexpr int kLoads = kBytes / 1024 / kWaves;     // per wave and step
   static constexpr int kRowChunks = TR ? R / 8 : 8;
   uint32_t off[kLoads];
   uint32_t krow[TR ? kLoads : 1];
@@ -157,7 +209,7 @@ struct Tile {
   int64_t inner;
 
   __device__ static __forceinline__ int hash(int r) {
-    if (TR) return IS_A ? (r & 1) | ((r & 2) << 1) : (r & 3) << 1;
+    if (TR) return (IS_A ? (r & 1) | ((r & 2) << 1) : (r & 3) << 1) | (r & 8);
     return IS_A ? (r & 3) | (((r >> 3) & 1) << 2) : r & 7;
   }
   __device__ __forceinline__ void init(const Operand& o, int64_t first, int lane, int wv) {
@@ -191,9 +243,9 @@ struct Tile {
       dma16_at(base + k0, off[q], to);
     }
   }
-  // Lane's addresses within a stage: kBases of them, a tile's at one of them plus a
-  // constant.
-  static constexpr int kBases = TR ? 4 : 2;
+  // A lane's addresses within a stage: kBases of them, a tile's at one of them (plus a
+  // constant where the tile's bits are none that the hash reaches).
+  static constexpr int kBases = TR ? 8 : 2;
   __device__ static __forceinline__ void bases(uint32_t (&b)[kBases], int first, int lane) {
     const int j = lane & 15, g = lane >> 4;
     if (!TR) {
@@ -204,55 +256,50 @@ struct Tile {
     } else {
       // this lane hands in 8 bytes of inner index 8 g + j / 4, piece j % 4 of 16 columns
       const int k = 8 * g + (j >> 2), p = j & 3;
-      const uint32_t row = k * R * 2;
-      if (IS_A) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {   // u = (i & 1) * 2 + h
-          const int i = u >> 1, h = u & 1;
-          b[u] = row + (((first / 8 + 4 * i + p) ^ hash(k)) << 4) + 8 * (h ^ (p & 1));
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)     // u = tile & 3
-          b[u] = row + (((first / 8 + 2 * u + (p >> 1)) ^ hash(k)) << 4) + 8 * (p & 1);
+      for (int t = 0; t < kBases; ++t) {
+        const int c = IS_A ? 4 * (t >> 1) + p : 2 * t + (p >> 1);
+        const int half = IS_A ? (t & 1) ^ (p & 1) : p & 1;
+        b[t] = k * R * 2 + (((first / 8 + c) ^ hash(k)) << 4) + 8 * half;
       }
     }
   }
-  // MFMA operand of tile t (A: t = 2 i + h), inner half s of the stage at `lds`
+  // MFMA operand of tile t (A: t = 2 i + h), half s of the step
   __device__ static __forceinline__ u32x4_t read(const char* lds, const uint32_t (&b)[kBases],
                                                  int t, int s) {
-    if (!TR) {
+    if constexpr (!TR) {
       const int c = IS_A ? (t >> 1) * 4096 + (t & 1) * 512 : t * 2048;
       return *reinterpret_cast<const u32x4_t*>(lds + b[s] + c);
+    } else {
+      const char* at = lds + b[t] + s * 32 * R * 2;
+      const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)at);
+      const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(at + 4 * R * 2));
+      const uint2 l = __builtin_bit_cast(uint2, lo), u = __builtin_bit_cast(uint2, hi);
+      return u32x4_t{l.x, l.y, u.x, u.y};
     }
-    // (tile t + 4 is 64 columns on: the hash does not reach that bit of the chunk)
-    const uint32_t at = b[t & 3] + (t >> 2) * 128 + s * 32 * R * 2;
-    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds + at));
-    const i16x4_t hi =
-        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds + at + 4 * R * 2));
-    const uint2 l = __builtin_bit_cast(uint2, lo), u = __builtin_bit_cast(uint2, hi);
-    return u32x4_t{l.x, l.y, u.x, u.y};
   }
 };
 
 template <int TN>
 struct Shape {
   static constexpr int kStages = TN == 256 ? 2 : 3;
-  static constexpr int kTilesB = TN / 32;          // MFMA tiles of a wave's half
+  static constexpr int kTilesB = TN / 16 / kWavesB;   // MFMA tiles of a wave
   static constexpr int kStageBytes = (kTileA + TN) * kStep * 2;
   static constexpr int kLds = kStages * kStageBytes;
 };
 
 // acc[ta][tb] += A . B^T over steps [s0, s1) (s0 < s1).  Wave (wm, wn): A's values
-// 128 wm .. and B's rows TN / 2 wn ...  Step k's DMA was issued stages - 1 / 2 steps
-// ahead; one barrier a step, in its middle: by then every wave has read the
-// step's second half, so its stage takes the DMA of step k + stages, and step
-// k + 1's tiles have landed (an exact vmcnt: every wave issues the same loads
-// each step, past the end the last step's again).
+// 128 wm .. and B's rows TN / 4 wn ...  While a half step is multiplied from
+// registers, the next half's operands are read.  One barrier a step, in its
+// middle: by then every wave has read the step's second half, so its stage takes the
+// DMA of step k + stages, and step k + 1's tiles have landed (an exact vmcnt: every
+// wave issues the same loads each step, past the end the last step's again).  The
+// loads are spread over the half step: their path takes 64 bytes a cycle, and a burst
+// of them holds up the wave (in a quarter of the step, 7% slower).
 template <int TN, bool ATR, bool BTR>
-__device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 32], char* lds, const Operand& A,
-                                          int64_t a0, const Operand& B, int64_t b0, int64_t s0,
-                                          int64_t s1) {
+__device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], char* lds,
+                                          const Operand& A, int64_t a0, const Operand& B,
+                                          int64_t b0, int64_t s0, int64_t s1) {
   using S = Shape<TN>;
   using TA = Tile<kTileA, ATR, true>;
   using TB = Tile<TN, BTR, false>;
@@ -267,7 +314,7 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 32], char* lds,
   tb.init(B, b0, lane, wv);
   uint32_t ab[TA::kBases], bb[TB::kBases];
   TA::bases(ab, 128 * wm, lane);
-  TB::bases(bb, TN / 2 * wn, lane);
+  TB::bases(bb, 16 * NB * wn, lane);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void_t*)lds;
 
 #pragma unroll
@@ -279,7 +326,7 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 32], char* lds,
     }
   mfma_settle();
 
-  auto load = [&](int q, int64_t step, uint32_t stage) {
+  auto load = [&](int q, int64_t step, uint32_t stage) __attribute__((always_inline)) {
     const int64_t k0 = (step < s1 ? step : s1 - 1) * kStep;
     if (q < TA::kLoads) ta.load(q, k0, lds0 + stage, wv);
     else tb.load(q - TA::kLoads, k0, lds0 + stage + TA::kBytes, wv);
@@ -292,37 +339,37 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 32], char* lds,
   __syncthreads();
 
   u32x4_t fa[2][8], fb[2][NB];
-  auto fetch = [&](int r, const char* stage, int s) {   // operand r of half s
-    if (r < 8) fa[s][r] = TA::read(stage, ab, r, s);
+  auto fetch = [&](int r, const char* stage, int s) __attribute__((always_inline)) {
+    if (r < 8) fa[s][r] = TA::read(stage, ab, r, s);    // operand r of half s
     else fb[s][r - 8] = TB::read(stage + TA::kBytes, bb, r - 8, s);
   };
 #pragma unroll
   for (int r = 0; r < 8 + NB; ++r) fetch(r, lds, 0);
 
+  constexpr int M = 8 * NB, R = 8 + NB, RM = M * 3 / 4;
   uint32_t cur = 0;
-  constexpr int M = 8 * NB, R = 8 + NB, RM = M * 3 / 4, DM = M / 2;
   for (int64_t k = s0; k < s1; ++k) {
     const uint32_t nxt = cur + S::kStageBytes < S::kLds ? cur + S::kStageBytes : 0;
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
+    static_for<0, M>([&](auto c) __attribute__((always_inline)) {
+      constexpr int i = c;
       mfma_acc(acc[i & 7][i >> 3], fa[0][i & 7], fb[0][i >> 3]);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int r = i * R / RM; r < (i + 1) * R / RM && r < R; ++r) fetch(r, lds + cur, 1);
+      static_for<min_of(i * R / RM, R), min_of((i + 1) * R / RM, R)>(
+          [&](auto r) __attribute__((always_inline)) { fetch(r, lds + cur, 1); });
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
     wait_vmem<(NS - 2) * kDma>();
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
+    static_for<0, M>([&](auto c) __attribute__((always_inline)) {
+      constexpr int i = c;
       mfma_acc(acc[i & 7][i >> 3], fa[1][i & 7], fb[1][i >> 3]);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int q = i * kDma / DM; q < (i + 1) * kDma / DM && q < kDma; ++q) load(q, k + NS, cur);
-#pragma unroll
-      for (int r = i * R / RM; r < (i + 1) * R / RM && r < R; ++r) fetch(r, lds + nxt, 0);
+      static_for<i * kDma / M, (i + 1) * kDma / M>(
+          [&](auto q) __attribute__((always_inline)) { load(q, k + NS, cur); });
+      static_for<min_of(i * R / RM, R), min_of((i + 1) * R / RM, R)>(
+          [&](auto r) __attribute__((always_inline)) { fetch(r, lds + nxt, 0); });
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
     cur = nxt;
   }
   wait_vmem<0>();   // nothing left in flight into LDS at exit
@@ -349,15 +396,19 @@ __device__ __forceinline__ int panel_rows(const HeadPanel& p) {
   return n < 0 ? 0 : n < p.rows ? (int)n : p.rows;
 }
 
+__device__ __forceinline__ int panel_splits(const HeadPanel& p, int n) {
+  return n == p.rows ? p.splits : __builtin_amdgcn_readfirstlane(p.r.n[1]);
+}
+
 // -------------------------------------------------------------------- logits
 // A = W (the vocabulary along a lane's registers: a row's statistics are sums in the
 // lane, then over the four lanes of its column), B = rows.
 template <int TN, int MODE>
-__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
-                          amdgpu_waves_per_eu(1, 1)))
+__global__ __attribute__((amdgpu_flat_work_group_size(kGemmThreads, kGemmThreads),
+                          amdgpu_waves_per_eu(kWaves / 4, kWaves / 4)))
 void k_head_logits(HeadPanel p) {
   __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
-  constexpr int NB = TN / 32;
+  constexpr int NB = Shape<TN>::kTilesB;
   const int n = panel_rows(p);
   int64_t tv, tt;
   if (!tile_of(blockIdx.x, ceil_div(p.vocab, kTileA), ceil_div(n, TN), tv, tt)) return;
@@ -373,7 +424,7 @@ void k_head_logits(HeadPanel p) {
   const int64_t cols = head_cols(p.vocab);
 #pragma unroll
   for (int t = 0; t < NB; ++t) {
-    const int row = (int)(tt * TN) + TN / 2 * wn + 16 * t + j;
+    const int row = (int)(tt * TN) + 16 * (NB * wn + t) + j;
     const bool valid = row < n;
     const int64_t q = p.row0 + (valid ? row : 0);
     const int64_t rel = valid ? (int64_t)p.r.y[q] - v0 - 8 * g : -1;   // in this lane: 32 i + 4 h + v
@@ -448,42 +499,47 @@ void k_head_logits(HeadPanel p) {
 }
 
 // ---------------------------------------------------------------------- join
-// A workgroup joins the slices of 64 rows (a lane each), 16 waves every sixteenth
-// slice: the maximum first, then the sums in float64.
-constexpr int kJoinWaves = 16;
+// A workgroup joins the slices of 16 rows, 64 of its threads a row: the maximum
+// first, then the sums in float64.
+constexpr int kJoinRows = 16, kJoinWaves = 16;
 __global__ __launch_bounds__(64 * kJoinWaves)
 void k_head_join(HeadPanel p, int kind, double* lp, float* logp, HeadStat* stat) {
-  __shared__ float ms[kJoinWaves][64];
-  __shared__ double ss[kJoinWaves][64];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  __shared__ float ms[kJoinWaves][kJoinRows];
+  __shared__ double ss[kJoinWaves][kJoinRows];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, r = lane & 15;
   const int n = panel_rows(p);
-  const int row = blockIdx.x * 64 + lane;
-  if ((int)blockIdx.x * 64 >= n) return;
+  const int row = blockIdx.x * kJoinRows + r;
+  if ((int)blockIdx.x * kJoinRows >= n) return;
   const int rr = row < n ? row : n - 1;
   const int64_t slices = 2 * ceil_div(p.vocab, kTileA);
   const HeadPart* part = p.part + rr;
+  const int first = 4 * wv + (lane >> 4);
   float m = -INFINITY;
-#pragma unroll 4
-  for (int64_t k = wv; k < slices; k += kJoinWaves) m = fmaxf(m, part[k * p.rows].m);
-  ms[wv][lane] = m;
-  __syncthreads();
+#pragma unroll 8
+  for (int64_t k = first; k < slices; k += 4 * kJoinWaves) m = fmaxf(m, part[k * p.rows].m);
+  m = fmaxf(m, __shfl_xor(m, 16));
+  m = fmaxf(m, __shfl_xor(m, 32));
+  if (lane < 16) ms[wv][r] = m;
   const int32_t y = p.r.y[p.row0 + rr];
   const float zy = y >= 0 ? p.zy[rr] : NAN;
+  __syncthreads();
   m = zy;
 #pragma unroll
-  for (int k = 0; k < kJoinWaves; ++k) m = fmaxf(m, ms[k][lane]);
+  for (int k = 0; k < kJoinWaves; ++k) m = fmaxf(m, ms[k][r]);
   double s = 0;
-#pragma unroll 4
-  for (int64_t k = wv; k < slices; k += kJoinWaves) {
+#pragma unroll 8
+  for (int64_t k = first; k < slices; k += 4 * kJoinWaves) {
     const HeadPart e = part[k * p.rows];
     if (e.m != -INFINITY || !(e.s == 0.f)) s += (double)e.s * exp_diff(e.m, m);
   }
-  ss[wv][lane] = s;
+  s += __shfl_xor(s, 16);
+  s += __shfl_xor(s, 32);
+  if (lane < 16) ss[wv][r] = s;
   __syncthreads();
-  if (wv != 0 || row >= n) return;
+  if (threadIdx.x >= kJoinRows || row >= n) return;
   s = 0;
 #pragma unroll
-  for (int k = 0; k < kJoinWaves; ++k) s += ss[k][lane];
+  for (int k = 0; k < kJoinWaves; ++k) s += ss[k][r];
   const double ey = exp((double)zy - (double)m);
   const double all = s + ey, lg = log(all);
   double l = (double)zy - (double)m - lg;
@@ -565,32 +621,6 @@ __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
 }
 
 // ------------------------------------------------------------------------ dh
-// The inner index is the vocabulary, long: with fewer tiles than CUs it is cut
-// into the number of slices that fills whole rounds best, which hangs on how
-// many rows there are and so is found here.  A slice's epilogue and its part of
-// the sum that follows cost about as much as 24 steps.
-__host__ __device__ inline int dh_splits(int64_t tiles, int64_t steps) {
-  int best = 1;
-  int64_t least = -1;
-  for (int s = 1; s <= kMaxSplits && tiles * s <= kMaxSlots; ++s) {
-    const int64_t each = ceil_div(steps, s);
-    if (s > 1 && each < 6) break;
-    const int64_t cost = ceil_div(tiles * s, 256) * (each + (s > 1 ? 24 : 4));
-    if (least < 0 || cost < least) {
-      least = cost;
-      best = s;
-    }
-  }
-  return best;
-}
-
-__device__ __forceinline__ void dh_plan(const HeadPanel& p, int n, int TN, int64_t& ta, int64_t& tb,
-                                        int& splits) {
-  ta = ceil_div(p.dim, kTileA);
-  tb = ceil_div(n, TN);
-  splits = dh_splits(ta * tb, ceil_div(p.vocab, kStep));
-}
-
 // Eight neighbouring values of a lane: tiles (i, 0) and (i, 1), in the order the
 // transposing read has them (odd lane groups the other way round).
 template <int NB>
@@ -609,15 +639,14 @@ __device__ __forceinline__ uint4 pack8(const float (&o)[8]) {
 }
 
 template <int TN>
-__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
-                          amdgpu_waves_per_eu(1, 1)))
+__global__ __attribute__((amdgpu_flat_work_group_size(kGemmThreads, kGemmThreads),
+                          amdgpu_waves_per_eu(kWaves / 4, kWaves / 4)))
 void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
   __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
-  constexpr int NB = TN / 32;
-  const int n = panel_rows(p);
-  int64_t na, nb, td, tt;
-  int splits;
-  dh_plan(p, n, TN, na, nb, splits);
+  constexpr int NB = Shape<TN>::kTilesB;
+  const int n = panel_rows(p), splits = panel_splits(p, n);
+  const int64_t na = ceil_div(p.dim, kTileA), nb = ceil_div(n, TN);
+  int64_t td, tt;
   const int64_t slot = blockIdx.x;       // tiles of a slice together
   const int64_t per8 = ceil_div(na * nb, 8) * 8;
   const int64_t sl = per8 ? slot / per8 : 0;
@@ -636,7 +665,7 @@ void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
   const int wm = wv & 1, wn = wv >> 1;
 #pragma unroll
   for (int t = 0; t < NB; ++t) {
-    const int in = TN / 2 * wn + 16 * t + j, row = (int)(tt * TN) + in;
+    const int in = 16 * (NB * wn + t) + j, row = (int)(tt * TN) + in;
     if (row >= n) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -662,10 +691,8 @@ void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
 // Adds the slices in order and rounds once; a thread 8 values of a row.
 __global__ __launch_bounds__(kThreads) void k_head_dh_sum(HeadPanel p, int TN, const float* part,
                                                           uint16_t* dh, int64_t ldd) {
-  const int n = panel_rows(p);
-  int64_t na, nb;
-  int splits;
-  dh_plan(p, n, TN, na, nb, splits);
+  const int n = panel_rows(p), splits = panel_splits(p, n);
+  const int64_t na = ceil_div(p.dim, kTileA), nb = ceil_div(n, TN);
   const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int per = p.dim / 8;
   const int64_t row = k / per;
@@ -687,10 +714,10 @@ __global__ __launch_bounds__(kThreads) void k_head_dh_sum(HeadPanel p, int TN, c
 
 // ------------------------------------------------------------------------ dW
 // A = h (transposed by the reads), B = dz (likewise); inner index the rows.
-__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
-                          amdgpu_waves_per_eu(1, 1)))
+__global__ __attribute__((amdgpu_flat_work_group_size(kGemmThreads, kGemmThreads),
+                          amdgpu_waves_per_eu(kWaves / 4, kWaves / 4)))
 void k_head_dw(HeadPanel p, float* sum, int first, int last, uint16_t* dw, int64_t ldo) {
-  constexpr int TN = 256, NB = TN / 32;
+  constexpr int TN = 256, NB = Shape<TN>::kTilesB;
   __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
   const int n = panel_rows(p);
   int64_t td, tv;
@@ -716,7 +743,7 @@ void k_head_dw(HeadPanel p, float* sum, int first, int last, uint16_t* dw, int64
   const int wm = wv & 1, wn = wv >> 1;
 #pragma unroll
   for (int t = 0; t < NB; ++t) {
-    const int64_t v = tv * TN + TN / 2 * wn + 16 * t + j;
+    const int64_t v = tv * TN + 16 * (NB * wn + t) + j;
     if (v >= p.vocab) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -747,9 +774,9 @@ template <int TN>
 hipError_t launch_logits(const HeadPanel& p, int mode, hipStream_t s) {
   const dim3 grid(grid8(ceil_div(p.vocab, kTileA) * ceil_div(p.rows, TN)));
   if (mode == HEAD_STATS)
-    return launch_kernel(k_head_logits<TN, HEAD_STATS>, grid, dim3(kThreads), s, p);
-  if (mode == HEAD_EXP) return launch_kernel(k_head_logits<TN, HEAD_EXP>, grid, dim3(kThreads), s, p);
-  return launch_kernel(k_head_logits<TN, HEAD_DZ>, grid, dim3(kThreads), s, p);
+    return launch_kernel(k_head_logits<TN, HEAD_STATS>, grid, dim3(kGemmThreads), s, p);
+  if (mode == HEAD_EXP) return launch_kernel(k_head_logits<TN, HEAD_EXP>, grid, dim3(kGemmThreads), s, p);
+  return launch_kernel(k_head_logits<TN, HEAD_DZ>, grid, dim3(kGemmThreads), s, p);
 }
 
 // Workgroups of dh, and tiles of its partial sums, that any number of rows up to
@@ -771,6 +798,10 @@ DhSize dh_size(int64_t rows, int dim, int64_t vocab, int tile) {
 
 }  // namespace
 
+int head_dh_splits(int64_t rows, int dim, int64_t vocab, int tile) {
+  return dh_splits(ceil_div(dim, kTileA) * ceil_div(rows, tile), ceil_div(vocab, kStep));
+}
+
 int head_tile(int64_t rows) { return rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
 
 hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t s) {
@@ -787,7 +818,8 @@ hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, hipStream_
 
 hipError_t launch_head_join(const HeadPanel& p, int kind, double* lp, float* logp, HeadStat* stat,
                             hipStream_t s) {
-  return launch_kernel(k_head_join, dim3((unsigned)ceil_div(p.rows, 64)), dim3(64 * kJoinWaves), s,
+  return launch_kernel(k_head_join, dim3((unsigned)ceil_div(p.rows, kJoinRows)),
+                       dim3(64 * kJoinWaves), s,
                        p, kind, lp, logp, stat);
 }
 
@@ -810,10 +842,10 @@ hipError_t launch_head_dh(const HeadPanel& p, int tile, float* part, uint16_t* d
                           hipStream_t s) {
   const DhSize d = dh_size(p.rows, p.dim, p.vocab, tile);
   const dim3 grid((unsigned)d.grid);
-  hipError_t e = tile == 64 ? launch_kernel(k_head_dh<64>, grid, dim3(kThreads), s, p, part, dh, ldd)
+  hipError_t e = tile == 64 ? launch_kernel(k_head_dh<64>, grid, dim3(kGemmThreads), s, p, part, dh, ldd)
                  : tile == 128
-                     ? launch_kernel(k_head_dh<128>, grid, dim3(kThreads), s, p, part, dh, ldd)
-                     : launch_kernel(k_head_dh<256>, grid, dim3(kThreads), s, p, part, dh, ldd);
+                     ? launch_kernel(k_head_dh<128>, grid, dim3(kGemmThreads), s, p, part, dh, ldd)
+                     : launch_kernel(k_head_dh<256>, grid, dim3(kGemmThreads), s, p, part, dh, ldd);
   if (e != hipSuccess || d.slots == 0) return e;
   return launch_kernel(k_head_dh_sum, dim3((unsigned)ceil_div((int64_t)p.rows * p.dim / 8, kThreads)),
                        dim3(kThreads), s, p, tile, part, dh, ldd);
@@ -822,7 +854,7 @@ hipError_t launch_head_dh(const HeadPanel& p, int tile, float* part, uint16_t* d
 hipError_t launch_head_dw(const HeadPanel& p, float* acc, int first, int last, uint16_t* dw,
                           int64_t ldo, hipStream_t s) {
   const dim3 grid(grid8(ceil_div(p.dim, kTileA) * ceil_div(p.vocab, 256)));
-  return launch_kernel(k_head_dw, grid, dim3(kThreads), s, p, acc, first, last, dw, ldo);
+  return launch_kernel(k_head_dw, grid, dim3(kGemmThreads), s, p, acc, first, last, dw, ldo);
 }
 
 }  // namespace qnf4
