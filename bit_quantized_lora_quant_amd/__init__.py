@@ -896,7 +896,7 @@ class MuonPlan:
             if any(t[1] is not g for t, g in zip(self.tensors, grads)):
                 self.tensors = [(t[0], g, *t[2:]) for t, g in zip(self.tensors, grads)]
                 self._collect()
-        at = [x.data_ptr() for x in self._flat]
+        at = list(map(torch.Tensor.data_ptr, self._flat))
         if at == self._at:
             return
         for x, kept in zip(self._flat, self._layout):

@@ -43,7 +43,7 @@ bool valid_ns(const qlora_newton_schulz* n) {
 // pointers and strides); workgroups, parts and polynomials follow one another.
 struct Sizes {
   int64_t total = 0;                    // elements
-  int64_t count = 0, wgs = 0, part = 0, q = 0;
+  int64_t count = 0, wgs = 0, chunks = 0, part = 0, q = 0;
   uint32_t ranks = 0;                   // bit sp / 16 of each padded short side
 };
 bool empty(const MuonTensor& t) { return t.rows == 0 || t.cols == 0; }
@@ -52,11 +52,13 @@ void place(MuonTensor& t, Sizes& z) {
   const int sp = muon_pad((int)s);
   t.slice = muon_slice(sp, z.total);
   t.wg = (int32_t)z.wgs;
+  t.chunk = (int32_t)z.chunks;
   t.part = (uint32_t)z.part;
   t.q = (uint32_t)z.q;
   const int64_t wgs = ceil_div(n, t.slice);
   z.count += 1;
   z.wgs += wgs;
+  z.chunks += ceil_div(n, muon_chunk(sp));
   z.part += wgs * muon_tiles(sp);
   z.q += sp * sp / 256;
   z.ranks |= 1u << (sp / 16);
@@ -76,17 +78,19 @@ Sizes sizes(int32_t count, Get get) {
 }
 bool fits(const Sizes& z) {
   const int64_t most = (int64_t)1 << 32;
-  return z.wgs < kMaxGroups256 && z.part < most && z.q < most;
+  return z.chunks < kMaxGroups256 && z.count < 65536 && z.part < most && z.q < most;
 }
 
 struct MuonWs {
-  size_t t, owner, part, q, total;
+  size_t t, owner, owner_wg, part, q, total;
 };
 MuonWs muon_layout(const Sizes& z) {
   MuonWs L;
   size_t off = 0;
   L.t = off;      off = align_up(off + z.count * sizeof(MuonTensor));
-  L.owner = off;  off = align_up(off + z.wgs * sizeof(int32_t));
+  L.owner = off;  off = align_up(off + z.chunks * sizeof(int32_t));
+  L.owner_wg = off;
+  off = align_up(off + z.wgs * sizeof(int32_t));
   L.part = off;   off = align_up(off + z.part * 256 * sizeof(double));
   L.q = off;      off = align_up(off + z.q * 256 * sizeof(double));
   L.total = off;
@@ -104,8 +108,11 @@ qlora_status run(int32_t count, Get get, const MuonHyper& h, void* ws, size_t ws
   char* base = static_cast<char*>(ws);
   const MuonScratch s{reinterpret_cast<MuonTensor*>(base + L.t),
                       reinterpret_cast<int32_t*>(base + L.owner),
+                      reinterpret_cast<int32_t*>(base + L.owner_wg),
                       reinterpret_cast<double*>(base + L.part),
                       reinterpret_cast<double*>(base + L.q)};
+  // one batch travels in the first launch's arguments, more through the table
+  const bool whole = z.count <= kMuonBatch;
   Sizes at;
   at.total = z.total;
   MuonBatch b;
@@ -113,22 +120,23 @@ qlora_status run(int32_t count, Get get, const MuonHyper& h, void* ws, size_t ws
   for (int32_t i = 0; i < count && e == hipSuccess;) {
     b.count = 0;
     b.first = (int)at.count;
-    at.ranks = 0;
-    const int64_t wg0 = at.wgs;
     for (; i < count && b.count < kMuonBatch; ++i) {
       MuonTensor t = get(i);
       if (empty(t)) continue;
       place(t, at);
       b.t[b.count++] = t;
     }
-    for (int sp = 16; sp <= kMaxRank && b.count > 0 && e == hipSuccess; sp *= 2)
-      if (at.ranks >> (sp / 16) & 1) e = launch_muon_gram(b, sp, (int)(at.wgs - wg0), h, s, st);
+    if (whole) i = count;   // (what is left is empty)
+    else if (b.count > 0) e = launch_muon_table(b, s, st);
   }
-  for (int sp = 16; sp <= kMaxRank && e == hipSuccess; sp *= 2) {
-    if (!(z.ranks >> (sp / 16) & 1)) continue;
-    e = launch_muon_poly((int)z.count, sp, h, s, st);
-    if (e == hipSuccess) e = launch_muon_apply(sp, (int)z.wgs, h, s, st);
-  }
+  // (the first launches of all ranks write the table that the others read)
+  auto each = [&](auto launch) {
+    for (int sp = 16; sp <= kMaxRank && e == hipSuccess; sp *= 2)
+      if (z.ranks >> (sp / 16) & 1) e = launch(sp);
+  };
+  each([&](int sp) { return launch_muon_gram(whole ? &b : nullptr, sp, (int)z.wgs, h, s, st); });
+  each([&](int sp) { return launch_muon_poly((int)z.count, sp, h, s, st); });
+  each([&](int sp) { return launch_muon_apply(sp, (int)z.chunks, h, s, st); });
   return hip_status(e);
 }
 

@@ -17,10 +17,12 @@ struct MuonTensor {
   int32_t ldi, ldm, ldo, ldb;
   float scale;        // of a step: lr times the shape's factor
   int32_t bf16;       // type of `in` (and of `out` without a step)
-  int32_t wg, slice;  // its first workgroup in the call, long indices of each
+  int32_t wg, slice;  // its first slice in the call, long indices of each
+  int32_t chunk;      // its first chunk in the call
   uint32_t part, q;   // its partial products and polynomial, in tiles of 256 doubles
+  int32_t reserved;
 };
-constexpr int kMuonBatch = 48;   // per launch: 3.8 KB of kernel arguments
+constexpr int kMuonBatch = 45;   // per launch: 3.9 KB of kernel arguments
 struct MuonBatch {
   int count, first;              // index of t[0] in the call
   MuonTensor t[kMuonBatch];
@@ -32,7 +34,8 @@ struct MuonHyper {
 };
 struct MuonScratch {
   MuonTensor* t;                 // [tensors]
-  int32_t* owner;                // [workgroups] tensor of each
+  int32_t* owner;                // [chunks] tensor of each
+  int32_t* owner_wg;             // [slices] likewise
   double* part;
   double* q;
 };
@@ -47,14 +50,16 @@ inline __host__ __device__ int muon_tiles(int sp) { return (sp / 16) * (sp / 16 
 // Long indices of a workgroup, for a call of `total` elements.
 int muon_slice(int sp, int64_t total);
 
-// m, and the slices' products of a batch's tensors whose padded short side is sp;
-// the table of these goes to the scratch
-hipError_t launch_muon_gram(const MuonBatch& b, int sp, int wgs, const MuonHyper& h,
+// Tensors of a batch to the scratch's table.
+hipError_t launch_muon_table(const MuonBatch& b, const MuonScratch& s, hipStream_t st);
+// m, and the slices' products of the tensors whose padded short side is sp: those of
+// the table (b null), or of a batch that is the whole call, which goes to the table
+hipError_t launch_muon_gram(const MuonBatch* b, int sp, int wgs, const MuonHyper& h,
                             const MuonScratch& s, hipStream_t st);
 // polynomials, then the update, of the call's tensors of that padded short side
 hipError_t launch_muon_poly(int count, int sp, const MuonHyper& h, const MuonScratch& s,
                             hipStream_t st);
-hipError_t launch_muon_apply(int sp, int wgs, const MuonHyper& h, const MuonScratch& s,
+hipError_t launch_muon_apply(int sp, int chunks, const MuonHyper& h, const MuonScratch& s,
                              hipStream_t st);
 
 }  // namespace qnf4

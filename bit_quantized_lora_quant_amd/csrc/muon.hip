@@ -21,11 +21,14 @@
 //   k_muon_gram   workgroup per slice of the long side: m <- mu m + (1 - mu) g, and its
 //                 part of U U^T on v_mfma_f64_16x16x4 (upper triangle of tiles)
 //   k_muon_poly   workgroup per tensor: the parts in order, |U|^2 as the trace, Q / |U|
-//   k_muon_apply  workgroup per slice: O = Q U, then the parameter's update
+//   k_muon_apply  workgroup per chunk of 4096 elements: O = Q U, then the parameter's
+//                 update
 //
 // Bound: HBM for rank up to 64 (a step moves 30 bytes a parameter, 22 of them
 // unavoidable: gradient and momentum are read again); the f64 matrix cores at 128.
 #include "muon.h"
+
+#include <type_traits>
 
 namespace qnf4 {
 namespace {
@@ -40,8 +43,8 @@ __device__ __forceinline__ f64x4_t mfma64(double a, double b, f64x4_t c) {
   return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
 }
 
-// The workgroup's tensor seen along its short side s (index i) and long side n
-// (index l): element (i, l) lies at i ld + l of a wide matrix, l ld + i of a tall one.
+// A tensor seen along its short side s (index i) and long side n (index l): element
+// (i, l) lies at i ld + l of a wide matrix, l ld + i of a tall one.
 struct View {
   bool tall;
   int s, n, sp, chunk;
@@ -58,32 +61,6 @@ __device__ __forceinline__ View view(const MuonTensor& t) {
 
 __device__ __forceinline__ bool fits16(const void* p, int ld, int bytes) {
   return ((uintptr_t)p % (4 * bytes)) == 0 && ld % 4 == 0;
-}
-
-// Units of a chunk: 4 neighbours in memory, wide (C / 4 a row of s), tall
-// (ceil(s / 4) a long index).  Unit u: short index, long index within the chunk.
-struct Unit {
-  int i, l;
-};
-__device__ __forceinline__ Unit unit_at(const View& v, int u) {
-  if (v.tall) {
-    const int per = (v.s + 3) / 4;
-    return Unit{4 * (u % per), u / per};
-  }
-  const int per = v.chunk / 4;
-  return Unit{u / per, 4 * (u % per)};
-}
-__device__ __forceinline__ int units(const View& v) {
-  return v.tall ? v.chunk * ((v.s + 3) / 4) : v.s * (v.chunk / 4);
-}
-// How many of a unit's four elements there are.
-__device__ __forceinline__ int unit_valid(const View& v, const Unit& a, int l0) {
-  if (v.tall) return l0 + a.l < v.n ? (v.s - a.i < 4 ? v.s - a.i : 4) : 0;
-  const int left = v.n - l0 - a.l;
-  return left < 0 ? 0 : left < 4 ? left : 4;
-}
-__device__ __forceinline__ int64_t unit_off(const View& v, const Unit& a, int l0, int ld) {
-  return v.tall ? (int64_t)(l0 + a.l) * ld + a.i : (int64_t)a.i * ld + l0 + a.l;
 }
 
 __device__ __forceinline__ void load4(float (&x)[4], const float* p, int valid, bool vec) {
@@ -130,33 +107,48 @@ __device__ __forceinline__ void load_in(float (&x)[4], const MuonTensor& t, int6
   else load4(x, static_cast<const float*>(t.in) + off, valid, vec);
 }
 
-// A chunk of U lies in LDS as [short][long] with C + 4 floats a row: the 16 x 4
-// operand reads and both kinds of writes meet each bank evenly.
-__device__ __forceinline__ void put(float* u, const View& v, const Unit& a, const float (&x)[4]) {
-  const int pitch = v.chunk + 4;
-  if (v.tall) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (a.i + e < v.s) u[(a.i + e) * pitch + a.l] = x[e];
-  } else {
-    *reinterpret_cast<float4*>(u + a.i * pitch + a.l) = make_float4(x[0], x[1], x[2], x[3]);
+// A thread's four units of a chunk, 4 neighbours in memory each: wide C / 4 of them a
+// short index, tall 4 NT a long index (past the short side or the end they hold
+// nothing).  In LDS a chunk of U lies as [short][long], C + 4 floats a row: the
+// 16 x 4 operand reads and both kinds of writes spread over the banks.
+template <int NT, bool TALL>
+struct Chunk {
+  static constexpr int C = 4096 / (16 * NT), pitch = C + 4;
+  int i0, l0, s, n;     // of unit 0; sides
+  __device__ __forceinline__ Chunk(const View& v) : s(v.s), n(v.n) {
+    const int tid = threadIdx.x;
+    i0 = TALL ? 4 * (tid % (4 * NT)) : tid / (C / 4);
+    l0 = TALL ? tid / (4 * NT) : 4 * (tid % (C / 4));
   }
-}
-__device__ __forceinline__ void get(float (&x)[4], const float* u, const View& v, const Unit& a) {
-  const int pitch = v.chunk + 4;
-  if (v.tall) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = a.i + e < v.s ? u[(a.i + e) * pitch + a.l] : 0.f;
-  } else {
-    const float4 f = *reinterpret_cast<const float4*>(u + a.i * pitch + a.l);
-    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+  __device__ __forceinline__ int i(int k) const { return TALL ? i0 : i0 + 4 * NT * k; }
+  __device__ __forceinline__ int l(int k) const { return TALL ? l0 + 64 / NT * k : l0; }
+  // how many of unit k's elements there are in the chunk that starts at `at`
+  __device__ __forceinline__ int valid(int k, int at) const {
+    const int left = TALL ? s - i0 : n - at - l0;
+    const bool in = TALL ? at + l(k) < n : i(k) < s;
+    return in ? (left < 0 ? 0 : left < 4 ? left : 4) : 0;
   }
-}
-// rows past the short side: read by the matrix cores, never written after
-__device__ __forceinline__ void clear_pad(float* u, const View& v) {
-  const int pitch = v.chunk + 4;
-  for (int k = v.s * pitch + threadIdx.x; k < v.sp * pitch; k += kThreads) u[k] = 0.f;
-}
+  __device__ __forceinline__ int64_t off(int k, int at, int ld) const {
+    return TALL ? (int64_t)(at + l(k)) * ld + i0 : (int64_t)i(k) * ld + at + l0;
+  }
+  __device__ __forceinline__ void put(float* u, int k, const float (&x)[4]) const {
+    if (TALL) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[(i0 + e) * pitch + l(k)] = x[e];
+    } else {
+      *reinterpret_cast<float4*>(u + i(k) * pitch + l0) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[4], const float* u, int k) const {
+    if (TALL) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = u[(i0 + e) * pitch + l(k)];
+    } else {
+      const float4 f = *reinterpret_cast<const float4*>(u + i(k) * pitch + l0);
+      x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+    }
+  }
+};
 
 __device__ __forceinline__ float momentum(float m, float g, const MuonHyper& h) {
   return h.mu * m + h.one_minus_mu * g;
@@ -169,21 +161,37 @@ __device__ __forceinline__ float update(float m, float g, const MuonHyper& h) {
 // ---------------------------------------------------------------------- gram
 // Products of a chunk over this workgroup's waves.  Up to two tiles of rank (one or
 // three products) a wave takes every fourth 4-long step and all of them; beyond, a
-// wave takes every fourth product and all steps.
+// wave takes every fourth product and all steps, which ones known to the compiler
+// (a test of the wave in the loop costs as much as the products).
 template <int NT>
 struct Gram {
   static constexpr int kTiles = NT * (NT + 1) / 2;
   static constexpr bool kByStep = NT <= 2;
   static constexpr int kMine = kByStep ? kTiles : (kTiles + 3) / 4;
+  static constexpr int C = 4096 / (16 * NT), pitch = C + 4;
   f64x4_t acc[kMine];
   __device__ __forceinline__ void init() {
 #pragma unroll
     for (int k = 0; k < kMine; ++k) acc[k] = f64x4_t{0., 0., 0., 0.};
   }
+  template <int WV>
+  __device__ __forceinline__ void add_products(const float* at) {
+#pragma unroll 2
+    for (int l = 0; l < C; l += 4) {
+      double x[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) x[i] = (double)at[i * 16 * pitch + l];
+      int k = 0;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = i; j < NT; ++j, ++k)
+          if ((k & 3) == WV) acc[k >> 2] = mfma64(x[i], x[j], acc[k >> 2]);
+    }
+  }
   __device__ __forceinline__ void add(const float* u, int lane, int wv) {
-    constexpr int C = 4096 / (16 * NT), pitch = C + 4;
     const float* at = u + (lane & 15) * pitch + (lane >> 4);
-    if (kByStep) {
+    if constexpr (kByStep) {
 #pragma unroll 4
       for (int l = 4 * wv; l < C; l += 16) {
         double x[NT];
@@ -196,18 +204,11 @@ struct Gram {
           for (int j = i; j < NT; ++j, ++k) acc[k] = mfma64(x[i], x[j], acc[k]);
       }
     } else {
-#pragma unroll 2
-      for (int l = 0; l < C; l += 4) {
-        double x[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) x[i] = (double)at[i * 16 * pitch + l];
-        // product k is wave k % 4's
-        int k = 0;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int j = i; j < NT; ++j, ++k)
-            if ((k & 3) == wv) acc[k >> 2] = mfma64(x[i], x[j], acc[k >> 2]);
+      switch (wv) {
+        case 0: add_products<0>(at); break;
+        case 1: add_products<1>(at); break;
+        case 2: add_products<2>(at); break;
+        default: add_products<3>(at); break;
       }
     }
   }
@@ -237,73 +238,114 @@ struct Gram {
   }
 };
 
-template <int NT>
+template <int NT, bool TALL>
 __device__ __forceinline__ void gram(const MuonTensor& t, const View& v, const MuonHyper& h,
                                      int slice, double* out, float* u, double* buf) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = slice * t.slice, end = first + t.slice < v.n ? first + t.slice : v.n;
-  const int count = units(v);
   const bool vi = fits16(t.in, t.ldi, t.bf16 ? 2 : 4), vm = fits16(t.m, t.ldm, 4);
+  const Chunk<NT, TALL> c(v);
   float g[kUnits][4], m[kUnits][4];
-  auto load = [&](int l0) {
+  auto load = [&](int at) {
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      const int id = threadIdx.x + k * kThreads;
-      if (id >= count) break;
-      const Unit a = unit_at(v, id);
-      const int valid = unit_valid(v, a, l0);
-      load_in(g[k], t, unit_off(v, a, l0, t.ldi), valid, vi);
-      if (t.m) load4(m[k], t.m + unit_off(v, a, l0, t.ldm), valid, vm);
+      const int valid = c.valid(k, at);
+      load_in(g[k], t, c.off(k, at, t.ldi), valid, vi);
+      if (t.m) load4(m[k], t.m + c.off(k, at, t.ldm), valid, vm);
     }
   };
   Gram<NT> G;
   G.init();
-  clear_pad(u, v);
   load(first);
-  for (int l0 = first; l0 < end; l0 += v.chunk) {
+  for (int at = first; at < end; at += v.chunk) {
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      const int id = threadIdx.x + k * kThreads;
-      if (id >= count) break;
-      const Unit a = unit_at(v, id);
       if (t.m) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) m[k][e] = momentum(m[k][e], g[k][e], h);
-        store4(t.m + unit_off(v, a, l0, t.ldm), m[k], unit_valid(v, a, l0), vm);
+        store4(t.m + c.off(k, at, t.ldm), m[k], c.valid(k, at), vm);
 #pragma unroll
         for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
       }
-      put(u, v, a, g[k]);
+      c.put(u, k, g[k]);
     }
     __syncthreads();
-    if (l0 + v.chunk < end) load(l0 + v.chunk);   // in flight under the products
+    if (at + v.chunk < end) load(at + v.chunk);   // in flight under the products
     G.add(u, lane, wv);
     __syncthreads();
   }
   G.store(out, buf, lane, wv);
 }
 
-// (a launch per padded rank that the batch has: workgroups of another return)
-template <int NT>
-__global__ __launch_bounds__(kThreads) void k_muon_gram(const MuonBatch bt, MuonHyper h,
-                                                        MuonScratch s) {
+// Fills the call's table from a batch of it: which tensor each slice and chunk is of.
+__device__ __forceinline__ void note(const MuonTensor& t, const View& v, int index, int c0, int c1,
+                                     const MuonScratch& s) {
+  const int per = t.slice / v.chunk;
+  for (int c = c0 + threadIdx.x; c < c1; c += kThreads) {
+    s.owner[t.chunk + c] = index;
+    if (c % per == 0) s.owner_wg[t.wg + c / per] = index;
+  }
+  if (threadIdx.x == 0 && c0 == 0) s.t[index] = t;
+}
+__global__ __launch_bounds__(kThreads) void k_muon_table(const MuonBatch bt, MuonScratch s) {
+  const MuonTensor t = bt.t[blockIdx.x];
+  const View v = view(t);
+  note(t, v, bt.first + blockIdx.x, 0, (int)ceil_div(v.n, v.chunk), s);
+}
+
+// TABLE: the call's tensors are in the scratch, all of them in one launch; else
+// they are this batch's, the call's only one, and go to the scratch from here.
+// (A launch per padded rank that there is: workgroups of another return.)
+template <int NT, bool TABLE>
+__global__ __launch_bounds__(kThreads, NT <= 2 ? 5 : NT == 4 ? 4 : 2)
+void k_muon_gram(const std::conditional_t<TABLE, int, MuonBatch> bt, MuonHyper h, MuonScratch s) {
   __shared__ __attribute__((aligned(16))) float u[kBuf];
   __shared__ __attribute__((aligned(32))) double buf[NT <= 2 ? 3 * Gram<NT>::kTiles * 256 : 1];
-  const int lane = threadIdx.x & 63;
-  const int wg = bt.t[0].wg + blockIdx.x;
-  const uint64_t before =
-      __builtin_amdgcn_ballot_w64(lane < bt.count && bt.t[lane < bt.count ? lane : 0].wg <= wg);
-  const int i = __builtin_amdgcn_readfirstlane(__popcll(before)) - 1;
-  const MuonTensor t = bt.t[i];
+  const int lane = threadIdx.x & 63, wg = blockIdx.x;
+  MuonTensor t;
+  int i = 0;
+  if constexpr (TABLE) {
+    t = s.t[__builtin_amdgcn_readfirstlane(s.owner_wg[wg])];
+  } else {
+    const uint64_t before =
+        __builtin_amdgcn_ballot_w64(lane < bt.count && bt.t[lane < bt.count ? lane : 0].wg <= wg);
+    i = __builtin_amdgcn_readfirstlane(__popcll(before)) - 1;
+    t = bt.t[i];
+  }
   const View v = view(t);
   if (v.sp != 16 * NT) return;
   const int slice = wg - t.wg;
-  if (threadIdx.x == 0) {
-    s.owner[wg] = bt.first + i;
-    if (slice == 0) s.t[bt.first + i] = t;
+  if constexpr (!TABLE) {
+    const int per = t.slice / v.chunk, all = (int)ceil_div(v.n, v.chunk);
+    note(t, v, i, slice * per, (slice + 1) * per < all ? (slice + 1) * per : all, s);
   }
-  gram<NT>(t, v, h, slice, s.part + ((size_t)t.part + (size_t)slice * Gram<NT>::kTiles) * 256, u,
-           buf);
+  double* out = s.part + ((size_t)t.part + (size_t)slice * Gram<NT>::kTiles) * 256;
+  if (v.tall) gram<NT, true>(t, v, h, slice, out, u, buf);
+  else gram<NT, false>(t, v, h, slice, out, u, buf);
+}
+
+// ----------------------------------------------------------------------- sum
+// From a rank of 33 on the slices' parts are megabytes, more than k_muon_poly's one
+// workgroup per tensor should read: a workgroup per tile and tensor adds them into
+// the first slice's place (64 x 22016: 2 us in place of 15).
+template <int NT>
+__global__ __launch_bounds__(kThreads) void k_muon_sum(MuonScratch s) {
+  __shared__ __attribute__((aligned(32))) f64x4_t buf[3 * 64];
+  const MuonTensor t = s.t[blockIdx.y];
+  const View v = view(t);
+  if (v.sp != 16 * NT) return;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int slices = (int)ceil_div(v.n, t.slice);
+  f64x4_t* at = reinterpret_cast<f64x4_t*>(s.part + ((size_t)t.part + blockIdx.x) * 256) + lane;
+  f64x4_t g = f64x4_t{0., 0., 0., 0.};
+#pragma unroll 8
+  for (int p = wv; p < slices; p += 4) g += at[(size_t)p * Gram<NT>::kTiles * 64];
+  if (wv > 0) buf[(wv - 1) * 64 + lane] = g;
+  __syncthreads();
+  if (wv > 0) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) g += buf[w * 64 + lane];
+  *at = g;
 }
 
 // ---------------------------------------------------------------------- poly
@@ -334,37 +376,61 @@ __device__ __forceinline__ Panel<NT> times(const double* x, const Panel<NT>& b, 
   return r;
 }
 template <int NT>
-__device__ __forceinline__ void put_panel(double* x, const Panel<NT>& p, int lane, int wv) {
+__device__ __forceinline__ void put_panel(double* x, const Panel<NT>& p, int lane, int pan,
+                                          bool own) {
   constexpr int pitch = 16 * NT + 2;
-  double* at = x + (lane >> 4) * pitch + 16 * wv + (lane & 15);
+  double* at = x + (lane >> 4) * pitch + 16 * pan + (lane & 15);
   __syncthreads();
+  if (own) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) at[(16 * i + 4 * v) * pitch] = p.t[i][v];
+      for (int v = 0; v < 4; ++v) at[(16 * i + 4 * v) * pitch] = p.t[i][v];
+  }
   __syncthreads();
 }
 
+constexpr int poly_waves(int nt) { return nt < 4 ? 4 : nt; }
 template <int NT>
-__global__ __launch_bounds__(64 * NT) void k_muon_poly(MuonHyper h, MuonScratch s) {
+__global__ __launch_bounds__(64 * poly_waves(NT)) void k_muon_poly(MuonHyper h, MuonScratch s) {
   constexpr int pitch = 16 * NT + 2;
   __shared__ __attribute__((aligned(16))) double x[16 * NT * pitch];
+  __shared__ __attribute__((aligned(32))) f64x4_t buf[NT < 4 ? 4 * Gram<NT>::kTiles * 64 : 1];
   const MuonTensor t = s.t[blockIdx.x];
   const View vw = view(t);
   if (vw.sp != 16 * NT) return;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slices = (int)ceil_div(vw.n, t.slice), tiles = muon_tiles(vw.sp);
-  // the slices' parts in order, both halves of the matrix
+  const f64x4_t* from = reinterpret_cast<const f64x4_t*>(s.part + (size_t)t.part * 256) + lane;
+  if constexpr (NT < 4) {
+    // every fourth slice a wave, then the four in order
+    const int slices = (int)ceil_div(vw.n, t.slice);
+    f64x4_t g[Gram<NT>::kTiles];
+#pragma unroll
+    for (int k = 0; k < Gram<NT>::kTiles; ++k) g[k] = f64x4_t{0., 0., 0., 0.};
+#pragma unroll 8
+    for (int p = wv; p < slices; p += 4)
+#pragma unroll
+      for (int k = 0; k < Gram<NT>::kTiles; ++k)
+        g[k] += from[((size_t)p * Gram<NT>::kTiles + k) * 64];
+#pragma unroll
+    for (int k = 0; k < Gram<NT>::kTiles; ++k) buf[(wv * Gram<NT>::kTiles + k) * 64 + lane] = g[k];
+    __syncthreads();
+  }
+  // both halves of the matrix
   int k = 0;
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = i; j < NT; ++j, ++k) {
-      if (k % NT != wv) continue;
-      const f64x4_t* from = reinterpret_cast<const f64x4_t*>(s.part + ((size_t)t.part + k) * 256) + lane;
-      f64x4_t g = f64x4_t{0., 0., 0., 0.};
-#pragma unroll 8
-      for (int p = 0; p < slices; ++p) g += from[(size_t)p * tiles * 64];
+      if (k % poly_waves(NT) != wv) continue;
+      f64x4_t g;
+      if constexpr (NT < 4) {
+        g = buf[k * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) g += buf[(w * Gram<NT>::kTiles + k) * 64 + lane];
+      } else {
+        g = from[k * 64];
+      }
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int r = 16 * i + 4 * v + (lane >> 4), c = 16 * j + (lane & 15);
@@ -373,6 +439,9 @@ __global__ __launch_bounds__(64 * NT) void k_muon_poly(MuonHyper h, MuonScratch 
       }
     }
   __syncthreads();
+  // (waves past the panels, there for the sum, repeat panel 0 and keep to the barriers)
+  const bool own = wv < NT;
+  const int pan = own ? wv : 0;
   double tr = 0;
   for (int r = lane; r < 16 * NT; r += 64) tr += x[r * (pitch + 1)];
 #pragma unroll
@@ -384,8 +453,8 @@ __global__ __launch_bounds__(64 * NT) void k_muon_poly(MuonHyper h, MuonScratch 
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-      G.t[i][v] = x[(16 * i + 4 * v + (lane >> 4)) * pitch + 16 * wv + (lane & 15)] * inv * inv;
-  put_panel<NT>(x, G, lane, wv);
+      G.t[i][v] = x[(16 * i + 4 * v + (lane >> 4)) * pitch + 16 * pan + (lane & 15)] * inv * inv;
+  put_panel<NT>(x, G, lane, pan, own);
   for (int n = 0; n < h.steps; ++n) {
     Panel<NT> P = times<NT>(x, G, lane);
 #pragma unroll
@@ -393,172 +462,176 @@ __global__ __launch_bounds__(64 * NT) void k_muon_poly(MuonHyper h, MuonScratch 
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         P.t[i][v] = h.b * G.t[i][v] + h.c * P.t[i][v];
-        if (i == wv && 4 * v + (lane >> 4) == (lane & 15)) P.t[i][v] += h.a;
+        if (i == pan && 4 * v + (lane >> 4) == (lane & 15)) P.t[i][v] += h.a;
       }
     const bool last = n + 1 == h.steps;
     Panel<NT> U;
     if (!last) U = times<NT>(x, P, lane);          // G P
-    put_panel<NT>(x, P, lane, wv);
+    put_panel<NT>(x, P, lane, pan, own);
     if (n == 0) Q = P;
     else Q = times<NT>(x, Q, lane);                // P Q
     if (!last) {
       G = times<NT>(x, U, lane);                   // P G P
-      put_panel<NT>(x, G, lane, wv);
+      put_panel<NT>(x, G, lane, pan, own);
     }
   }
-  double* out = s.q + (size_t)t.q * 256 + (lane >> 4) * 16 * NT + 16 * wv + (lane & 15);
+  // as k_muon_apply's left operands: (Q symmetric) row tile `pan`, inner indices
+  // 16 i + 4 v .., a line a load
+  if (!own) return;
+  double* out = s.q + (size_t)t.q * 256 + pan * 256 * NT + lane;
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) out[(16 * i + 4 * v) * 16 * NT] = Q.t[i][v] * inv;
+    for (int v = 0; v < 4; ++v) out[(4 * i + v) * 64] = Q.t[i][v] * inv;
 }
 
 // --------------------------------------------------------------------- apply
-// O = Q U of a chunk: wave w takes row tiles and columns so that its part of Q stays
-// in registers over the whole slice.
-template <int NT>
+// O = Q U of one chunk: wave w takes row tiles and columns of it.  The chunk's loads are
+// in flight before those of Q; several workgroups a CU hide one another's phases.
+template <int NT, bool TALL>
 __device__ __forceinline__ void apply(const MuonTensor& t, const View& v, const MuonHyper& h,
-                                      int slice, const double* q, float* u) {
-  constexpr int SP = 16 * NT, C = 4096 / SP, pitch = C + 4;
+                                      int start, const double* q, float* u) {
+  constexpr int C = 4096 / (16 * NT), pitch = C + 4;
   constexpr int RW = NT < 4 ? NT : 4;         // waves along the short side
   constexpr int MI = NT / RW;                 // row tiles of a wave
   constexpr int CW = 4 / RW;                  // waves along the long side
   constexpr int MJ = C / 16 / CW;             // column tiles of a wave
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wv % RW, wc = wv / RW;
-  const int first = slice * t.slice, end = first + t.slice < v.n ? first + t.slice : v.n;
-  const int count = units(v);
   const bool vi = fits16(t.in, t.ldi, t.bf16 ? 2 : 4), vm = fits16(t.m, t.ldm, 4);
   const bool vo = fits16(t.out, t.ldo, !h.step && t.bf16 ? 2 : 4), vb = fits16(t.pb, t.ldb, 2);
   const bool need_in = !t.m || h.nesterov;
-  double a[MI][4 * NT];
+  const Chunk<NT, TALL> c(v);
+  float g[kUnits][4], m[kUnits][4], p[kUnits][4];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const int valid = c.valid(k, start);
+    if (need_in) load_in(g[k], t, c.off(k, start, t.ldi), valid, vi);
+    if (t.m) load4(m[k], t.m + c.off(k, start, t.ldm), valid, vm);
+    if (h.step) load4(p[k], static_cast<const float*>(t.out) + c.off(k, start, t.ldo), valid, vo);
+  }
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    if (t.m) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
+    }
+    c.put(u, k, g[k]);
+  }
+  __syncthreads();
+  f64x4_t o[MI][MJ];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int k = 0; k < 4 * NT; ++k)
-      a[i][k] = q[(16 * (wr * MI + i) + (lane & 15)) * SP + 4 * k + (lane >> 4)];
-  float g[kUnits][4], m[kUnits][4], p[kUnits][4];
-  auto load = [&](int l0) {
+    for (int j = 0; j < MJ; ++j) o[i][j] = f64x4_t{0., 0., 0., 0.};
+  const float* at = u + (lane >> 4) * pitch + 16 * wc * MJ + (lane & 15);
+  const double* aq = q + wr * MI * 256 * NT + lane;
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const int id = threadIdx.x + k * kThreads;
-      if (id >= count) break;
-      const Unit b = unit_at(v, id);
-      const int valid = unit_valid(v, b, l0);
-      if (need_in) load_in(g[k], t, unit_off(v, b, l0, t.ldi), valid, vi);
-      if (t.m) load4(m[k], t.m + unit_off(v, b, l0, t.ldm), valid, vm);
-      if (h.step) load4(p[k], static_cast<const float*>(t.out) + unit_off(v, b, l0, t.ldo), valid, vo);
-    }
-  };
-  clear_pad(u, v);
-  for (int l0 = first; l0 < end; l0 += v.chunk) {
-    load(l0);
+  for (int k = 0; k < 4 * NT; ++k) {
+    double a[MI];
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const int id = threadIdx.x + k * kThreads;
-      if (id >= count) break;
-      if (t.m) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
-      }
-      put(u, v, unit_at(v, id), g[k]);
-    }
-    __syncthreads();
-    f64x4_t o[MI][MJ];
+    for (int i = 0; i < MI; ++i) a[i] = aq[i * 256 * NT + 64 * k];
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
-      const float* at = u + (lane >> 4) * pitch + 16 * (wc * MJ + j) + (lane & 15);
+      const double x = (double)at[4 * k * pitch + 16 * j];
 #pragma unroll
-      for (int i = 0; i < MI; ++i) o[i][j] = f64x4_t{0., 0., 0., 0.};
-#pragma unroll
-      for (int k = 0; k < 4 * NT; ++k) {
-        const double x = (double)at[4 * k * pitch];
-#pragma unroll
-        for (int i = 0; i < MI; ++i) o[i][j] = mfma64(a[i][k], x, o[i][j]);
-      }
+      for (int i = 0; i < MI; ++i) o[i][j] = mfma64(a[i], x, o[i][j]);
     }
-    __syncthreads();
+  }
+  __syncthreads();
 #pragma unroll
-    for (int j = 0; j < MJ; ++j)
+  for (int j = 0; j < MJ; ++j)
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * (wr * MI + i) + 4 * r + (lane >> 4);
-          if (row < v.s) u[row * pitch + 16 * (wc * MJ + j) + (lane & 15)] = (float)o[i][j][r];
-        }
-    __syncthreads();
+      for (int r = 0; r < 4; ++r)
+        u[(16 * (wr * MI + i) + 4 * r + (lane >> 4)) * pitch + 16 * (wc * MJ + j) + (lane & 15)] =
+            (float)o[i][j][r];
+  __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const int id = threadIdx.x + k * kThreads;
-      if (id >= count) break;
-      const Unit b = unit_at(v, id);
-      const int valid = unit_valid(v, b, l0);
-      const int64_t off = unit_off(v, b, l0, t.ldo);
-      float x[4];
-      get(x, u, v, b);
-      if (!h.step) {
-        if (t.bf16) store4(static_cast<uint16_t*>(t.out) + off, x, valid, vo);
-        else store4(static_cast<float*>(t.out) + off, x, valid, vo);
-        continue;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = p[k][e] * h.decay - t.scale * x[e];
-      store4(static_cast<float*>(t.out) + off, x, valid, vo);
-      if (t.pb) store4(t.pb + unit_off(v, b, l0, t.ldb), x, valid, vb);
+  for (int k = 0; k < kUnits; ++k) {
+    const int valid = c.valid(k, start);
+    const int64_t off = c.off(k, start, t.ldo);
+    float x[4];
+    c.get(x, u, k);
+    if (!h.step) {
+      if (t.bf16) store4(static_cast<uint16_t*>(t.out) + off, x, valid, vo);
+      else store4(static_cast<float*>(t.out) + off, x, valid, vo);
+      continue;
     }
-    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = p[k][e] * h.decay - t.scale * x[e];
+    store4(static_cast<float*>(t.out) + off, x, valid, vo);
+    if (t.pb) store4(t.pb + c.off(k, start, t.ldb), x, valid, vb);
   }
 }
 
-// Last workgroups first: what the first launches read last is still in the
-// Infinity Cache.
+// Last chunks first: what the first launches read last is still in the Infinity
+// Cache.
 template <int NT>
-__global__ __launch_bounds__(kThreads) void k_muon_apply(MuonHyper h, MuonScratch s) {
+__global__ __launch_bounds__(kThreads, 4) void k_muon_apply(MuonHyper h, MuonScratch s) {
   __shared__ __attribute__((aligned(16))) float u[kBuf];
-  const int wg = gridDim.x - 1 - blockIdx.x;
-  const MuonTensor t = s.t[__builtin_amdgcn_readfirstlane(s.owner[wg])];
+  const int c = gridDim.x - 1 - blockIdx.x;
+  const MuonTensor t = s.t[__builtin_amdgcn_readfirstlane(s.owner[c])];
   const View v = view(t);
   if (v.sp != 16 * NT) return;
-  apply<NT>(t, v, h, wg - t.wg, s.q + (size_t)t.q * 256, u);
+  const double* q = s.q + (size_t)t.q * 256;
+  const int start = (c - t.chunk) * v.chunk;
+  if (v.tall) apply<NT, true>(t, v, h, start, q, u);
+  else apply<NT, false>(t, v, h, start, q, u);
 }
 
 }  // namespace
 
 int muon_slice(int sp, int64_t total) {
-  // at least 512 workgroups where there is work for them, at most 16 chunks (the
-  // parts of a rank of 128 are as large as 4.5 chunks of it)
-  const int64_t most = sp <= 32 ? 4 : sp == 64 ? 8 : 16;
-  int64_t chunks = ceil_div(total, 512 * 4096);
+  // A rank of 16 leaves 2 KB of parts a slice (a chunk moves 48 KB), one of 64 20 KB and
+  // of 128 72 KB: there as many chunks as leave 1536 workgroups, six a CU.
+  const int64_t most = sp <= 32 ? 1 : sp == 64 ? 8 : 16;
+  int64_t chunks = ceil_div(total, 1536 * 4096);
   chunks = chunks < 1 ? 1 : chunks > most ? most : chunks;
   return (int)chunks * muon_chunk(sp);
 }
 
-hipError_t launch_muon_gram(const MuonBatch& b, int sp, int wgs, const MuonHyper& h,
+hipError_t launch_muon_table(const MuonBatch& b, const MuonScratch& s, hipStream_t st) {
+  return launch_kernel(k_muon_table, dim3((unsigned)b.count), dim3(kThreads), st, b, s);
+}
+
+template <int NT>
+hipError_t launch_gram(const MuonBatch* b, dim3 grid, const MuonHyper& h, const MuonScratch& s,
+                       hipStream_t st) {
+  return b ? launch_kernel(k_muon_gram<NT, false>, grid, dim3(kThreads), st, *b, h, s)
+           : launch_kernel(k_muon_gram<NT, true>, grid, dim3(kThreads), st, 0, h, s);
+}
+hipError_t launch_muon_gram(const MuonBatch* b, int sp, int wgs, const MuonHyper& h,
                             const MuonScratch& s, hipStream_t st) {
-  const dim3 grid((unsigned)wgs), block(kThreads);
+  const dim3 grid((unsigned)wgs);
   switch (sp) {
-    case 16: return launch_kernel(k_muon_gram<1>, grid, block, st, b, h, s);
-    case 32: return launch_kernel(k_muon_gram<2>, grid, block, st, b, h, s);
-    case 64: return launch_kernel(k_muon_gram<4>, grid, block, st, b, h, s);
-    default: return launch_kernel(k_muon_gram<8>, grid, block, st, b, h, s);
+    case 16: return launch_gram<1>(b, grid, h, s, st);
+    case 32: return launch_gram<2>(b, grid, h, s, st);
+    case 64: return launch_gram<4>(b, grid, h, s, st);
+    default: return launch_gram<8>(b, grid, h, s, st);
   }
 }
 
 hipError_t launch_muon_poly(int count, int sp, const MuonHyper& h, const MuonScratch& s,
                             hipStream_t st) {
   const dim3 grid((unsigned)count);
+  hipError_t e = hipSuccess;
   switch (sp) {
-    case 16: return launch_kernel(k_muon_poly<1>, grid, dim3(64), st, h, s);
-    case 32: return launch_kernel(k_muon_poly<2>, grid, dim3(128), st, h, s);
-    case 64: return launch_kernel(k_muon_poly<4>, grid, dim3(256), st, h, s);
-    default: return launch_kernel(k_muon_poly<8>, grid, dim3(512), st, h, s);
+    case 16: return launch_kernel(k_muon_poly<1>, grid, dim3(64 * poly_waves(1)), st, h, s);
+    case 32: return launch_kernel(k_muon_poly<2>, grid, dim3(64 * poly_waves(2)), st, h, s);
+    case 64:
+      e = launch_kernel(k_muon_sum<4>, dim3(10, (unsigned)count), dim3(kThreads), st, s);
+      return e != hipSuccess ? e : launch_kernel(k_muon_poly<4>, grid, dim3(64 * poly_waves(4)), st, h, s);
+    default:
+      e = launch_kernel(k_muon_sum<8>, dim3(36, (unsigned)count), dim3(kThreads), st, s);
+      return e != hipSuccess ? e : launch_kernel(k_muon_poly<8>, grid, dim3(64 * poly_waves(8)), st, h, s);
   }
 }
 
-hipError_t launch_muon_apply(int sp, int wgs, const MuonHyper& h, const MuonScratch& s,
+hipError_t launch_muon_apply(int sp, int chunks, const MuonHyper& h, const MuonScratch& s,
                              hipStream_t st) {
-  const dim3 grid((unsigned)wgs), block(kThreads);
+  const dim3 grid((unsigned)chunks), block(kThreads);
   switch (sp) {
     case 16: return launch_kernel(k_muon_apply<1>, grid, block, st, h, s);
     case 32: return launch_kernel(k_muon_apply<2>, grid, block, st, h, s);

@@ -478,7 +478,7 @@ typedef struct {
 
 /* Bytes of workspace the two calls below need for matrices of these shapes; 0 for
  * shapes they refuse: the shorter side above 128, a side or a row stride of 2^30
- * or more, or 2^24 or more slices of 4096 to 65536 elements. */
+ * or more, 65536 or more matrices, or 2^24 or more chunks of 4096 elements. */
 size_t qlora_muon_workspace_bytes(const int64_t* rows, const int64_t* cols, int32_t count);
 
 typedef struct {
@@ -488,8 +488,8 @@ typedef struct {
   qlora_dtype dtype;   /* of both */
   int32_t reserved;    /* must be 0 */
 } qlora_ortho_matrix;
-/* Orthogonalises `count` matrices, in 3 launches for up to 48 of one rank.  A
- * matrix without elements is skipped; a zero matrix gives zeros. */
+/* Orthogonalises `count` matrices, in 3 launches for up to 45 of a rank up to 32
+ * (4 above).  A matrix without elements is skipped; a zero matrix gives zeros. */
 qlora_status qlora_orthogonalize(const qlora_newton_schulz* ns, const qlora_ortho_matrix* m,
                                  int32_t count, void* ws, size_t ws_bytes, void* stream);
 
