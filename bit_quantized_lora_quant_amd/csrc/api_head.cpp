@@ -49,7 +49,7 @@ bool valid_grad(const qlora_head* h, const void* d, int64_t ld) {
 }
 
 int64_t panel_rows(const qlora_head* h) {
-  const int tile = head_tile(h->rows);
+  const int tile = head_tile(h->rows, h->vocab);
   const int64_t all = ceil_div(h->rows > 0 ? h->rows : 1, tile) * tile;
   int64_t rows = kPanel / head_cols(h->vocab) / 256 * 256;
   if (rows < 256) rows = 256;
@@ -57,7 +57,7 @@ int64_t panel_rows(const qlora_head* h) {
 }
 
 struct HeadWs {
-  size_t h, src, y, n, stat, w, lp, part, zy, e, split, acc, total;
+  size_t h, src, y, n, stat, w, scale, lp, part, zy, shift, e, split, acc, total;
 };
 HeadWs head_layout(const qlora_head* h, bool dh, bool dw) {
   HeadWs L;
@@ -77,11 +77,13 @@ HeadWs head_layout(const qlora_head* h, bool dh, bool dw) {
   L.n = take(8);
   L.stat = take(grad ? all * sizeof(HeadStat) : 0);
   L.w = take(grad ? all * 4 : 0);
+  L.scale = take(grad ? all * sizeof(HeadScale) : 0);
   L.lp = take(all * 8);
   L.part = take(cols / 128 * panel * sizeof(HeadPart));
   L.zy = take(panel * 4);
+  L.shift = take(dh && !dw ? cols / 128 * panel * 4 : 0);
   L.e = take(grad ? panel * cols * 2 : 0);
-  L.split = take(dh ? head_dh_floats(panel, (int)h->dim, h->vocab, head_tile(h->rows)) * 4 : 0);
+  L.split = take(dh ? head_dh_floats(panel, (int)h->dim, h->vocab, head_tile(h->rows, h->vocab)) * 4 : 0);
   L.acc = take(dw && h->rows > panel ? (size_t)h->vocab * h->dim * 4 : 0);
   L.total = off;
   return L;
@@ -93,7 +95,8 @@ T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws)
 HeadPanel panel(const qlora_head* h, void* ws, const HeadWs& L) {
   HeadPanel p;
   p.r = HeadRows{at<uint16_t>(ws, L.h), at<int32_t>(ws, L.src), at<int32_t>(ws, L.y),
-                 at<int32_t>(ws, L.n), at<HeadStat>(ws, L.stat), at<float>(ws, L.w)};
+                 at<int32_t>(ws, L.n), at<HeadStat>(ws, L.stat), at<float>(ws, L.w),
+                 at<HeadScale>(ws, L.scale)};
   p.row0 = 0;
   p.rows = (int)panel_rows(h);
   p.dim = (int)h->dim;
@@ -102,7 +105,8 @@ HeadPanel panel(const qlora_head* h, void* ws, const HeadWs& L) {
   p.vocab = h->vocab;
   p.part = at<HeadPart>(ws, L.part);
   p.zy = at<float>(ws, L.zy);
-  p.splits = head_dh_splits(p.rows, p.dim, p.vocab, head_tile(h->rows));
+  p.shift = at<uint32_t>(ws, L.shift);
+  p.splits = head_dh_splits(p.rows, p.dim, p.vocab, head_tile(h->rows, h->vocab));
   p.e = at<uint16_t>(ws, L.e);
   return p;
 }
@@ -117,15 +121,15 @@ HeadPackArgs pack_args(const qlora_head* h, const HeadPanel& p) {
   a.labels = h->labels;
   a.to = p.r;
   a.panel = p.rows;
-  a.tile = head_tile(h->rows);
+  a.tile = head_tile(h->rows, h->vocab);
   return a;
 }
 
-// dh and dW of a panel whose e holds dz
+// dh and dW of a panel whose e holds dz, or (pow, without dW) the powers of two
 hipError_t panel_grads(const qlora_head* h, const HeadPanel& p, void* ws, const HeadWs& L, int tile,
-                       uint16_t* dh, int64_t ldd, uint16_t* dw, int64_t ldo, hipStream_t s) {
+                       int pow, uint16_t* dh, int64_t ldd, uint16_t* dw, int64_t ldo, hipStream_t s) {
   hipError_t e = hipSuccess;
-  if (dh) e = launch_head_dh(p, tile, at<float>(ws, L.split), dh, ldd, s);
+  if (dh) e = launch_head_dh(p, tile, pow, at<float>(ws, L.split), dh, ldd, s);
   if (e == hipSuccess && dw)
     e = launch_head_dw(p, h->rows > p.rows ? at<float>(ws, L.acc) : nullptr, p.row0 == 0,
                        p.row0 + p.rows >= h->rows, dw, ldo, s);
@@ -156,12 +160,12 @@ qlora_status qlora_head_logprobs(const qlora_head* h, float* logp, float* stats,
   HeadPackArgs a = pack_args(h, p);
   a.logp = logp;
   a.stat_out = reinterpret_cast<HeadStat*>(stats);
-  const int tile = head_tile(h->rows);
+  const int tile = head_tile(h->rows, h->vocab);
   hipError_t e = launch_head_pack(a, s);
   for (; e == hipSuccess && p.row0 < h->rows; p.row0 += p.rows) {
     e = launch_head_logits(p, tile, HEAD_STATS, s);
     if (e == hipSuccess)
-      e = launch_head_join(p, HEAD_SCORE, nullptr, logp, a.stat_out, s);
+      e = launch_head_join(p, HEAD_SCORE, 0, nullptr, logp, a.stat_out, s);
   }
   return hip_status(e);
 }
@@ -188,11 +192,11 @@ qlora_status qlora_head_logprobs_bwd(const qlora_head* h, const float* stats, co
   a.dh = dhidden;
   a.ldd = ldd;
   a.pad = dweight != nullptr;
-  const int tile = head_tile(h->rows);
+  const int tile = head_tile(h->rows, h->vocab);
   hipError_t e = launch_head_pack(a, s);
   do {
     if (e == hipSuccess) e = launch_head_logits(p, tile, HEAD_DZ, s);
-    if (e == hipSuccess) e = panel_grads(h, p, ws, L, tile, dhidden, ldd, dweight, ldo, s);
+    if (e == hipSuccess) e = panel_grads(h, p, ws, L, tile, 0, dhidden, ldd, dweight, ldo, s);
     p.row0 += p.rows;
   } while (e == hipSuccess && p.row0 < h->rows);
   return hip_status(e);
@@ -217,16 +221,16 @@ qlora_status qlora_head_cross_entropy(const qlora_head* h, int32_t reduction, fl
   a.dh = dhidden;
   a.ldd = ldd;
   a.pad = dweight != nullptr;
-  const int tile = head_tile(h->rows), mean = reduction == QLORA_HEAD_MEAN;
-  const bool grad = dhidden || dweight;
+  const int tile = head_tile(h->rows, h->vocab), mean = reduction == QLORA_HEAD_MEAN;
+  const bool grad = dhidden || dweight, pow = grad && !dweight;
   hipError_t e = launch_head_pack(a, s);
   do {
-    if (e == hipSuccess) e = launch_head_logits(p, tile, grad ? HEAD_EXP : HEAD_STATS, s);
+    if (e == hipSuccess) e = launch_head_logits(p, tile, pow ? HEAD_POW : grad ? HEAD_EXP : HEAD_STATS, s);
     if (e == hipSuccess)
       e = launch_head_join(p, !grad ? HEAD_LOSS : mean ? HEAD_GRAD_MEAN : HEAD_GRAD_SUM,
-                           at<double>(ws, L.lp), logp, nullptr, s);
-    if (e == hipSuccess && grad) e = launch_head_dz(p, s);
-    if (e == hipSuccess && grad) e = panel_grads(h, p, ws, L, tile, dhidden, ldd, dweight, ldo, s);
+                           pow, at<double>(ws, L.lp), logp, nullptr, s);
+    if (e == hipSuccess && dweight) e = launch_head_dz(p, s);
+    if (e == hipSuccess && grad) e = panel_grads(h, p, ws, L, tile, pow, dhidden, ldd, dweight, ldo, s);
     p.row0 += p.rows;
   } while (e == hipSuccess && p.row0 < h->rows);
   if (e == hipSuccess) e = launch_head_loss(p.r.n, at<double>(ws, L.lp), mean, loss, s);

@@ -12,9 +12,15 @@ namespace qnf4 {
 struct HeadStat {
   float lse, rest;
 };
-// A slice's maximum and sum of exp(z - m), the target left out of both.
+// A slice's largest exponent M = ceil(max z log2 e), a whole number, and sum of
+// 2^(z log2 e - M), the target left out of both.
 struct HeadPart {
   float m, s;
+};
+// A row after the join: R, the largest M of its slices; f and c with
+// dz_v = f 2^(z_v log2 e - R), at the target c = w (1 - p).
+struct HeadScale {
+  float r, f, c;
 };
 
 // Rows with a target, packed: hidden [up to a tile's rows][D], their source rows and
@@ -26,6 +32,7 @@ struct HeadRows {
   int32_t* n;         // [2] how many, and the slices of dh in a panel they do not fill
   HeadStat* stat;
   float* w;
+  HeadScale* scale;
 };
 
 struct HeadPackArgs {
@@ -59,31 +66,34 @@ struct HeadPanel {
   int64_t ldw, vocab;
   HeadPart* part;      // [vocab tiles * 2][rows]
   float* zy;           // [rows] the target's logit
+  uint32_t* shift;     // [vocab tiles * 2][rows] R - M, in both halves as bf16's exponent
   int splits;          // slices of dh in a full panel
   uint16_t* e;         // [rows][head_cols(vocab)] exponentials (fp16), then dz (bf16)
 };
 // Columns of a panel's row.
 __host__ __device__ inline int64_t head_cols(int64_t vocab) { return ceil_div(vocab, 256) * 256; }
 int head_dh_splits(int64_t rows, int dim, int64_t vocab, int tile);
-// Rows of tokens per workgroup tile (64, 128 or 256) for a call of this many rows.
-int head_tile(int64_t rows);
+// Rows of tokens per workgroup tile (64, 128 or 256) of a call.
+int head_tile(int64_t rows, int64_t vocab);
 
-// HEAD_STATS: part and zy; HEAD_EXP: these and e; HEAD_DZ: dz from r.stat and r.w
-enum { HEAD_STATS = 0, HEAD_EXP = 1, HEAD_DZ = 2 };
+// HEAD_STATS: part and zy; HEAD_EXP: these and e; HEAD_DZ: dz from r.stat and r.w;
+// HEAD_POW: as HEAD_EXP with e in bf16, which dh takes as it is
+enum { HEAD_STATS = 0, HEAD_EXP = 1, HEAD_DZ = 2, HEAD_POW = 3 };
 hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, hipStream_t s);
 // Joins the slices: logp and stat of the rows (nullable, by source row).
-// From HEAD_LOSS on the packed rows' logp in lp; with HEAD_GRAD_* also r.stat and
-// r.w = -1 (sum) or -1 / n (mean).
+// From HEAD_LOSS on the packed rows' logp in lp; with HEAD_GRAD_* also r.scale for
+// w = -1 (sum) or -1 / n (mean), and p.shift where `shift`.
 enum { HEAD_SCORE = 0, HEAD_LOSS = 1, HEAD_GRAD_SUM = 2, HEAD_GRAD_MEAN = 3 };
-hipError_t launch_head_join(const HeadPanel& p, int kind, double* lp, float* logp, HeadStat* stat,
-                            hipStream_t s);
+hipError_t launch_head_join(const HeadPanel& p, int kind, int shift, double* lp, float* logp,
+                            HeadStat* stat, hipStream_t s);
 hipError_t launch_head_loss(const int32_t* n, const double* lp, int mean, float* loss,
                             hipStream_t s);
 // e -> dz in place
 hipError_t launch_head_dz(const HeadPanel& p, hipStream_t s);
-// dh = dz . W by source row; part: head_dh_floats floats
+// dh = dz . W by source row, from e's dz, or (pow) from HEAD_POW's e, p.shift and
+// r.scale; part: head_dh_floats floats
 size_t head_dh_floats(int64_t rows, int dim, int64_t vocab, int tile);
-hipError_t launch_head_dh(const HeadPanel& p, int tile, float* part, uint16_t* dh, int64_t ldd,
+hipError_t launch_head_dh(const HeadPanel& p, int tile, int pow, float* part, uint16_t* dh, int64_t ldd,
                           hipStream_t s);
 // dw = dz^T . h (bf16, row stride ldo), or with acc [vocab][dim] over several
 // panels: added to it (stored where first), and only the last writes dw.

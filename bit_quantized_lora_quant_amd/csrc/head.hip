@@ -38,9 +38,17 @@ constexpr float kLog2e = 1.4426950408889634f;
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2eLo = 1.925963033500e-08f;   // log2 e - kLog2e
 
 __device__ __forceinline__ float exp_diff(float z, float m) {
   return __builtin_amdgcn_exp2f((z - m) * kLog2e);
+}
+// 2^(z log2 e - m), m a whole number: the difference is rounded once
+__device__ __forceinline__ float pow2_diff(float z, float m) {
+  return __builtin_amdgcn_exp2f(
+      __builtin_fmaf(z, kLog2eLo, __builtin_fmaf(z, kLog2e, -m)));
 }
 
 // ----------------------------------------------------------------- slices of dh
@@ -182,6 +190,11 @@ __device__ __forceinline__ void dma16_at(const void* base, uint32_t off, uint32_
                :: "v"(off), "s"(base), "s"(lds) : "m0", "memory");
 }
 
+__device__ __forceinline__ void dma4_at(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "m0", "memory");
+}
+
 // An operand: element (index, inner) at p[index * ld + inner] (TR false) or
 // p[inner * ld + index] (TR true); indices past `count` repeat the last ones
 // (their outputs are not stored), inner indices past `inner` the last one (the
@@ -280,11 +293,19 @@ struct Tile {
   }
 };
 
-template <int TN>
+// Exponents that a B operand's bf16 values are lowered by before they are multiplied:
+// rows' words (the same in both halves) p[(inner / 128) * ld + row].
+struct Shift {
+  const uint32_t* p;
+  int64_t ld;
+};
+
+template <int TN, bool SHIFT = false>
 struct Shape {
   static constexpr int kStages = TN == 256 ? 2 : 3;
   static constexpr int kTilesB = TN / 16 / kWavesB;   // MFMA tiles of a wave
-  static constexpr int kStageBytes = (kTileA + TN) * kStep * 2;
+  static constexpr int kTileBytes = (kTileA + TN) * kStep * 2;
+  static constexpr int kStageBytes = kTileBytes + (SHIFT ? TN * 4 : 0);
   static constexpr int kLds = kStages * kStageBytes;
 };
 
@@ -296,15 +317,16 @@ struct Shape {
 // wave issues the same loads each step, past the end the last step's again).  The
 // loads are spread over the half step: their path takes 64 bytes a cycle, and a burst
 // of them holds up the wave (in a quarter of the step, 7% slower).
-template <int TN, bool ATR, bool BTR>
+template <int TN, bool ATR, bool BTR, bool SHIFT = false>
 __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], char* lds,
                                           const Operand& A, int64_t a0, const Operand& B,
-                                          int64_t b0, int64_t s0, int64_t s1) {
-  using S = Shape<TN>;
+                                          int64_t b0, int64_t s0, int64_t s1,
+                                          const Shift& sh = Shift{nullptr, 0}) {
+  using S = Shape<TN, SHIFT>;
   using TA = Tile<kTileA, ATR, true>;
   using TB = Tile<TN, BTR, false>;
   constexpr int NB = S::kTilesB, NS = S::kStages;
-  constexpr int kDma = TA::kLoads + TB::kLoads;
+  constexpr int kDma = TA::kLoads + TB::kLoads + SHIFT;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 1, wn = wv >> 1;
@@ -329,7 +351,11 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], 
   auto load = [&](int q, int64_t step, uint32_t stage) __attribute__((always_inline)) {
     const int64_t k0 = (step < s1 ? step : s1 - 1) * kStep;
     if (q < TA::kLoads) ta.load(q, k0, lds0 + stage, wv);
-    else tb.load(q - TA::kLoads, k0, lds0 + stage + TA::kBytes, wv);
+    else if (q < TA::kLoads + TB::kLoads)
+      tb.load(q - TA::kLoads, k0, lds0 + stage + TA::kBytes, wv);
+    else   // (with fewer than 512 rows several waves fetch the same words)
+      dma4_at(sh.p + k0 / 128 * sh.ld + b0 + 64 * (wv % (TN / 64)), 4 * lane,
+              lds0 + stage + S::kTileBytes + 256 * (wv % (TN / 64)));
   };
 #pragma unroll
   for (int st = 0; st < NS; ++st)
@@ -346,9 +372,32 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], 
 #pragma unroll
   for (int r = 0; r < 8 + NB; ++r) fetch(r, lds, 0);
 
+  // The exponents of bf16 values by whole numbers: exact, and 0 where one would leave the
+  // range.  A tile's words are changed at least two instructions before the first
+  // product that reads them (which the compiler does not see inside the asm).
+  uint32_t sv[NB];
+  auto words = [&](int t, const char* stage) __attribute__((always_inline)) {
+    if constexpr (SHIFT)
+      sv[t] = *reinterpret_cast<const uint32_t*>(stage + S::kTileBytes +
+                                                 4 * (16 * (NB * wn + t) + (lane & 15)));
+  };
+  auto lower = [&](int t, int s) __attribute__((always_inline)) {
+    if constexpr (SHIFT) {
+      const u16x2_t by = __builtin_bit_cast(u16x2_t, sv[t]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        fb[s][t][q] = __builtin_bit_cast(
+            uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2_t, (uint32_t)fb[s][t][q]), by));
+    }
+  };
+#pragma unroll
+  for (int t = 0; t < NB; ++t) words(t, lds);
+  lower(0, 0);
+
   constexpr int M = 8 * NB, R = 8 + NB, RM = M * 3 / 4;
   uint32_t cur = 0;
   for (int64_t k = s0; k < s1; ++k) {
+    if constexpr (SHIFT) asm volatile("s_nop 1");
     const uint32_t nxt = cur + S::kStageBytes < S::kLds ? cur + S::kStageBytes : 0;
     static_for<0, M>([&](auto c) __attribute__((always_inline)) {
       constexpr int i = c;
@@ -356,6 +405,8 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], 
       __builtin_amdgcn_sched_barrier(0);
       static_for<min_of(i * R / RM, R), min_of((i + 1) * R / RM, R)>(
           [&](auto r) __attribute__((always_inline)) { fetch(r, lds + cur, 1); });
+      if constexpr (i % 8 == 4 && i / 8 + 1 < NB) lower(i / 8 + 1, 0);
+      if constexpr (i == M - 1) lower(0, 1);
       __builtin_amdgcn_sched_barrier(0);
     });
     wait_vmem<(NS - 2) * kDma>();
@@ -368,6 +419,10 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], 
           [&](auto q) __attribute__((always_inline)) { load(q, k + NS, cur); });
       static_for<min_of(i * R / RM, R), min_of((i + 1) * R / RM, R)>(
           [&](auto r) __attribute__((always_inline)) { fetch(r, lds + nxt, 0); });
+      if constexpr (i % 8 == 4 && i / 8 + 1 < NB) lower(i / 8 + 1, 1);
+      // (the last tile's words are used by then)
+      if constexpr (i >= RM && i < RM + NB) words(i - RM, lds + nxt);
+      if constexpr (i == M - 1) lower(0, 0);
       __builtin_amdgcn_sched_barrier(0);
     });
     cur = nxt;
@@ -379,11 +434,17 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], 
 // Tile of workgroup `id` among na x nb (A tiles, B tiles): workgroups go to the
 // eight XCDs in turn, so each XCD takes a contiguous run of the order "eight A
 // tiles, then the next B tile", where 32 neighbours (its CUs) share 8 + 4 tiles.
+// With slices of the inner index, all tiles of one, then the next.
 __device__ __forceinline__ bool tile_of(int64_t id, int64_t na, int64_t nb, int64_t& ta,
-                                        int64_t& tb) {
-  const int64_t total = na * nb, per = ceil_div(total, 8);
-  const int64_t loc = id >> 3, l = (id & 7) * per + loc;
+                                        int64_t& tb, int slices = 1, int* slice = nullptr) {
+  const int64_t tiles = na * nb, total = tiles * slices, per = ceil_div(total, 8);
+  const int64_t loc = id >> 3;
+  int64_t l = (id & 7) * per + loc;
   if (loc >= per || l >= total) return false;
+  if (slice) {
+    *slice = (int)(l / tiles);
+    l -= *slice * tiles;
+  }
   const int64_t grp = l / (8 * nb), left = na - 8 * grp;
   const int64_t rem = l - grp * 8 * nb, ga = left < 8 ? left : 8;
   tb = rem / ga;
@@ -474,24 +535,27 @@ void k_head_logits(HeadPanel p) {
     for (int i = 1; i < 32; ++i) m = fmaxf(m, z[i]);
     m = fmaxf(m, __shfl_xor(m, 16));
     m = fmaxf(m, __shfl_xor(m, 32));
+    m = ceilf(m * kLog2e);
     const float from = m == -INFINITY ? 0.f : m;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      z[i] = exp_diff(z[i], from);
+      z[i] = pow2_diff(z[i], from);
       s += z[i];
     }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
     if (valid && g == 0) p.part[(2 * tv + wm) * p.rows + row] = HeadPart{m, s};
-    if (MODE == HEAD_EXP && valid) {
+    if ((MODE == HEAD_EXP || MODE == HEAD_POW) && valid) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[k] = __builtin_bit_cast(uint32_t, half2_t{(_Float16)z[8 * i + 2 * k],
-                                                      (_Float16)z[8 * i + 2 * k + 1]});
+          o[k] = MODE == HEAD_POW
+                     ? pack_bf16x2(z[8 * i + 2 * k], z[8 * i + 2 * k + 1])
+                     : __builtin_bit_cast(uint32_t, half2_t{(_Float16)z[8 * i + 2 * k],
+                                                            (_Float16)z[8 * i + 2 * k + 1]});
         *reinterpret_cast<uint4*>(out + 32 * i) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
@@ -503,7 +567,7 @@ void k_head_logits(HeadPanel p) {
 // first, then the sums in float64.
 constexpr int kJoinRows = 16, kJoinWaves = 16;
 __global__ __launch_bounds__(64 * kJoinWaves)
-void k_head_join(HeadPanel p, int kind, double* lp, float* logp, HeadStat* stat) {
+void k_head_join(HeadPanel p, int kind, int shift, double* lp, float* logp, HeadStat* stat) {
   __shared__ float ms[kJoinWaves][kJoinRows];
   __shared__ double ss[kJoinWaves][kJoinRows];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, r = lane & 15;
@@ -523,14 +587,20 @@ void k_head_join(HeadPanel p, int kind, double* lp, float* logp, HeadStat* stat)
   const int32_t y = p.r.y[p.row0 + rr];
   const float zy = y >= 0 ? p.zy[rr] : NAN;
   __syncthreads();
-  m = zy;
+  m = ms[0][r];
 #pragma unroll
-  for (int k = 0; k < kJoinWaves; ++k) m = fmaxf(m, ms[k][r]);
+  for (int k = 1; k < kJoinWaves; ++k) m = fmaxf(m, ms[k][r]);
+  // sums relative to 2^m: every factor is a power of two
   double s = 0;
 #pragma unroll 8
   for (int64_t k = first; k < slices; k += 4 * kJoinWaves) {
     const HeadPart e = part[k * p.rows];
-    if (e.m != -INFINITY || !(e.s == 0.f)) s += (double)e.s * exp_diff(e.m, m);
+    const int down = (int)fmaxf(e.m - m, -2000.f);   // (0 for a NaN: the sum shows it)
+    s += ldexp((double)e.s, down);
+    if (shift && row < n) {
+      const uint32_t d = down < -511 ? 511 : -down;
+      p.shift[k * p.rows + row] = e.s == 0.f ? 0u : d << 7 | d << 23;
+    }
   }
   s += __shfl_xor(s, 16);
   s += __shfl_xor(s, 32);
@@ -540,23 +610,26 @@ void k_head_join(HeadPanel p, int kind, double* lp, float* logp, HeadStat* stat)
   s = 0;
 #pragma unroll
   for (int k = 0; k < kJoinWaves; ++k) s += ss[k][r];
-  const double ey = exp((double)zy - (double)m);
-  const double all = s + ey, lg = log(all);
-  double l = (double)zy - (double)m - lg;
-  HeadStat st{(float)((double)m + lg), (float)(s / all)};
+  // the target joins: both relative to 2^top
+  const double ty = (double)zy * 1.4426950408889634074, top = fmax((double)m, ceil(ty));
+  const double out = m == -INFINITY ? 0.0 : exp2((double)m - top);
+  const double rest = m == -INFINITY ? 0.0 : s * out, all = rest + exp2(ty - top);
+  const double lse = (top + log2(all)) * 0.69314718055994530942;
+  double l = (double)zy - lse;
+  HeadStat st{(float)lse, (float)(rest / all)};
+  const double w = kind == HEAD_GRAD_MEAN ? -1.0 / *p.r.n : -1.0;
+  HeadScale sc{m, (float)(-w * out / all), (float)(w * rest / all)};
   if (y < 0) {
     l = NAN;
     st = HeadStat{NAN, NAN};
+    sc = HeadScale{0.f, NAN, NAN};
   }
   const int64_t q = p.row0 + row;
   const int32_t src = p.r.src[q];
   if (logp) logp[src] = (float)l;
   if (stat) stat[src] = st;
   if (kind >= HEAD_LOSS) lp[q] = l;
-  if (kind >= HEAD_GRAD_SUM) {
-    p.r.stat[q] = st;
-    p.r.w[q] = kind == HEAD_GRAD_MEAN ? (float)(-1.0 / *p.r.n) : -1.f;
-  }
+  if (kind >= HEAD_GRAD_SUM) p.r.scale[q] = sc;
 }
 
 // loss = -(sum of logp), over the number of targets
@@ -578,8 +651,8 @@ __global__ __launch_bounds__(1024) void k_head_loss(const int32_t* n, const doub
 }
 
 // ------------------------------------------------------------------------ dz
-// In place, a thread 8 columns of 8 rows: HBM-bound.  dz = -w exp(m - lse) e, the
-// target's w (1 - p); zeros in the rows up to a whole step of dW.
+// In place, a thread 8 columns of 8 rows: HBM-bound.  dz = f 2^(M - R) e, the target's
+// c; zeros in the rows up to a whole step of dW.
 constexpr int kDzRows = 8;
 __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
   const int n = panel_rows(p);
@@ -597,9 +670,9 @@ __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
     uint4 o = make_uint4(0u, 0u, 0u, 0u);
     if (r0 + r < n) {
       const int64_t q = p.row0 + r0 + r;
-      const HeadStat st = p.r.stat[q];
-      const float w = p.r.w[q], m = p.part[(c >> 7) * p.rows + r0 + r].m;
-      const float f = m == -INFINITY ? 0.f : -w * exp_diff(m, st.lse);
+      const HeadScale sc = p.r.scale[q];
+      const float m = p.part[(c >> 7) * p.rows + r0 + r].m;
+      const float f = m == -INFINITY ? 0.f : sc.f * __builtin_amdgcn_exp2f(m - sc.r);
       float d[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -611,7 +684,7 @@ __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
       if (rel >= 0 && rel < 8) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (rel == k) d[k] = w * st.rest;
+          if (rel == k) d[k] = sc.c;
       }
       o = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
                      pack_bf16x2(d[6], d[7]));
@@ -638,19 +711,31 @@ __device__ __forceinline__ uint4 pack8(const float (&o)[8]) {
                     pack_bf16x2(o[6], o[7]));
 }
 
-template <int TN>
+// POW: e holds 2^(z log2 e - M) of each slice: the tile loop lowers its exponents to
+// the row's R, and what is left is a factor of the whole row and the target's term,
+// c times its row of W, in float32 at the end.  So dz is rounded to bf16 once, e is
+// written once and read once, and the target's cancellation stays out of the sums.
+__device__ __forceinline__ void finish_row(const HeadPanel& p, int64_t q, int64_t col,
+                                           float (&o)[8]) {
+  const HeadScale sc = p.r.scale[q];
+  const int y = p.r.y[q];
+  const uint4 w = *reinterpret_cast<const uint4*>(p.weight + (y < 0 ? 0 : y) * p.ldw + col);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    o[k] = sc.f * o[k] + sc.c * bf16_to_f32((uint16_t)((&w.x)[k >> 1] >> (16 * (k & 1))));
+}
+
+template <int TN, bool POW>
 __global__ __attribute__((amdgpu_flat_work_group_size(kGemmThreads, kGemmThreads),
                           amdgpu_waves_per_eu(kWaves / 4, kWaves / 4)))
 void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
-  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN, POW>::kLds];
   constexpr int NB = Shape<TN>::kTilesB;
   const int n = panel_rows(p), splits = panel_splits(p, n);
   const int64_t na = ceil_div(p.dim, kTileA), nb = ceil_div(n, TN);
   int64_t td, tt;
-  const int64_t slot = blockIdx.x;       // tiles of a slice together
-  const int64_t per8 = ceil_div(na * nb, 8) * 8;
-  const int64_t sl = per8 ? slot / per8 : 0;
-  if (sl >= splits || !tile_of(slot - sl * per8, na, nb, td, tt)) return;
+  int sl;
+  if (!tile_of(blockIdx.x, na, nb, td, tt, splits, &sl)) return;
   const int64_t steps = ceil_div(p.vocab, kStep), each = ceil_div(steps, splits);
   const int64_t s0 = sl * each, s1 = s0 + each < steps ? s0 + each : steps;
   const int64_t cols = head_cols(p.vocab);
@@ -658,7 +743,8 @@ void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
   const Operand B{p.e, cols, n, cols};
   f32x4_t acc[8][NB];
   // (a cut that leaves the last slice empty is left out by the rows above: each >= 1)
-  tile_loop<TN, true, false>(acc, lds, A, td * kTileA, B, tt * TN, s0 < steps ? s0 : steps - 1, s1);
+  tile_loop<TN, true, false, POW>(acc, lds, A, td * kTileA, B, tt * TN,
+                                  s0 < steps ? s0 : steps - 1, s1, Shift{p.shift, p.rows});
 
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -682,33 +768,50 @@ void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
         to[0] = make_float4(o[0], o[1], o[2], o[3]);
         to[1] = make_float4(o[4], o[5], o[6], o[7]);
       } else if (col < p.dim) {
+        if (POW) finish_row(p, p.row0 + row, col, o);
         *reinterpret_cast<uint4*>(dh + p.r.src[p.row0 + row] * ldd + col) = pack8(o);
       }
     }
   }
 }
 
-// Adds the slices in order and rounds once; a thread 8 values of a row.
-__global__ __launch_bounds__(kThreads) void k_head_dh_sum(HeadPanel p, int TN, const float* part,
-                                                          uint16_t* dh, int64_t ldd) {
+// Adds the slices and rounds once: a wave 64 x 8 values of the rows, every fourth
+// slice a wave and then the four in order.
+__global__ __launch_bounds__(kThreads) void k_head_dh_sum(HeadPanel p, int TN, int pow,
+                                                          const float* part, uint16_t* dh,
+                                                          int64_t ldd) {
+  __shared__ float4 buf[3][2][64];
   const int n = panel_rows(p), splits = panel_splits(p, n);
   const int64_t na = ceil_div(p.dim, kTileA), nb = ceil_div(n, TN);
-  const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int per = p.dim / 8;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, per = p.dim / 8;
+  const int64_t k = (int64_t)blockIdx.x * 64 + lane;
+  if (splits == 1 || (int64_t)blockIdx.x * 64 >= (int64_t)n * per) return;
   const int64_t row = k / per;
   const int col = (int)(k - row * per) * 8;
-  if (splits == 1 || row >= n) return;
-  const float* from = part + ((col / kTileA) * nb + row / TN) * (TN * kTileA) +
-                      (row % TN) * kTileA + col % kTileA;
-  const int64_t step = na * nb * (TN * kTileA);
+  const bool in = row < n;
   float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float4 a = *reinterpret_cast<const float4*>(from + s * step);
-    const float4 b = *reinterpret_cast<const float4*>(from + s * step + 4);
+  auto add = [&](const float4& a, const float4& b) {
     o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
     o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
+  };
+  if (in) {
+    const float* from = part + ((col / kTileA) * nb + row / TN) * (TN * kTileA) +
+                        (row % TN) * kTileA + col % kTileA;
+    const int64_t step = na * nb * (TN * kTileA);
+#pragma unroll 8
+    for (int s = wv; s < splits; s += 4)
+      add(*reinterpret_cast<const float4*>(from + s * step),
+          *reinterpret_cast<const float4*>(from + s * step + 4));
   }
+  if (wv > 0) {
+    buf[wv - 1][0][lane] = make_float4(o[0], o[1], o[2], o[3]);
+    buf[wv - 1][1][lane] = make_float4(o[4], o[5], o[6], o[7]);
+  }
+  __syncthreads();
+  if (wv > 0 || !in) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) add(buf[w][0][lane], buf[w][1][lane]);
+  if (pow) finish_row(p, p.row0 + row, col, o);
   *reinterpret_cast<uint4*>(dh + p.r.src[p.row0 + row] * ldd + col) = pack8(o);
 }
 
@@ -775,6 +878,7 @@ hipError_t launch_logits(const HeadPanel& p, int mode, hipStream_t s) {
   const dim3 grid(grid8(ceil_div(p.vocab, kTileA) * ceil_div(p.rows, TN)));
   if (mode == HEAD_STATS)
     return launch_kernel(k_head_logits<TN, HEAD_STATS>, grid, dim3(kGemmThreads), s, p);
+  if (mode == HEAD_POW) return launch_kernel(k_head_logits<TN, HEAD_POW>, grid, dim3(kGemmThreads), s, p);
   if (mode == HEAD_EXP) return launch_kernel(k_head_logits<TN, HEAD_EXP>, grid, dim3(kGemmThreads), s, p);
   return launch_kernel(k_head_logits<TN, HEAD_DZ>, grid, dim3(kGemmThreads), s, p);
 }
@@ -790,7 +894,7 @@ DhSize dh_size(int64_t rows, int dim, int64_t vocab, int tile) {
   DhSize d{ceil_div(na * all, 8) * 8, 0};   // uncut
   for (int64_t nb = 1; nb <= all && na * nb <= kMaxSlots; ++nb) {
     const int64_t sp = dh_splits(na * nb, steps);
-    if (ceil_div(na * nb, 8) * 8 * sp > d.grid) d.grid = ceil_div(na * nb, 8) * 8 * sp;
+    if (ceil_div(na * nb * sp, 8) * 8 > d.grid) d.grid = ceil_div(na * nb * sp, 8) * 8;
     if (sp > 1 && na * nb * sp > d.slots) d.slots = na * nb * sp;
   }
   return d;
@@ -802,7 +906,25 @@ int head_dh_splits(int64_t rows, int dim, int64_t vocab, int tile) {
   return dh_splits(ceil_div(dim, kTileA) * ceil_div(rows, tile), ceil_div(vocab, kStep));
 }
 
-int head_tile(int64_t rows) { return rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+int head_tile(int64_t rows, int64_t vocab) {
+  // The least time of the logits' rounds: a round of 256 workgroups takes about 45, 65
+  // and 118 us at 4096 inner indices with tiles of 64, 128 and 256 rows.  (331 rows
+  // of a vocabulary of 128256: 555, 393 and 474 us; 512 rows: 698, 510 and 476; 96
+  // rows of 32000 at 1024: 25, 26 and 34.)
+  const int unit[3] = {45, 65, 118};
+  int best = 64;
+  int64_t least = -1;
+  for (int i = 0; i < 3; ++i) {
+    const int tile = 64 << i;
+    const int64_t cost =
+        ceil_div(ceil_div(rows > 0 ? rows : 1, tile) * ceil_div(vocab, kTileA), 256) * unit[i];
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = tile;
+    }
+  }
+  return best;
+}
 
 hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t s) {
   // (a workgroup also without rows: it writes how many there are)
@@ -816,11 +938,11 @@ hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, hipStream_
                     : tile == 128 ? launch_logits<128>(p, mode, s) : launch_logits<256>(p, mode, s);
 }
 
-hipError_t launch_head_join(const HeadPanel& p, int kind, double* lp, float* logp, HeadStat* stat,
-                            hipStream_t s) {
+hipError_t launch_head_join(const HeadPanel& p, int kind, int shift, double* lp, float* logp,
+                            HeadStat* stat, hipStream_t s) {
   return launch_kernel(k_head_join, dim3((unsigned)ceil_div(p.rows, kJoinRows)),
                        dim3(64 * kJoinWaves), s,
-                       p, kind, lp, logp, stat);
+                       p, kind, shift, lp, logp, stat);
 }
 
 hipError_t launch_head_loss(const int32_t* n, const double* lp, int mean, float* loss,
@@ -838,17 +960,23 @@ size_t head_dh_floats(int64_t rows, int dim, int64_t vocab, int tile) {
   return (size_t)dh_size(rows, dim, vocab, tile).slots * tile * kTileA;
 }
 
-hipError_t launch_head_dh(const HeadPanel& p, int tile, float* part, uint16_t* dh, int64_t ldd,
-                          hipStream_t s) {
+template <bool POW>
+hipError_t launch_dh(const HeadPanel& p, int tile, dim3 grid, float* part, uint16_t* dh,
+                     int64_t ldd, hipStream_t s) {
+  const dim3 block(kGemmThreads);
+  return tile == 64    ? launch_kernel(k_head_dh<64, POW>, grid, block, s, p, part, dh, ldd)
+         : tile == 128 ? launch_kernel(k_head_dh<128, POW>, grid, block, s, p, part, dh, ldd)
+                       : launch_kernel(k_head_dh<256, POW>, grid, block, s, p, part, dh, ldd);
+}
+hipError_t launch_head_dh(const HeadPanel& p, int tile, int pow, float* part, uint16_t* dh,
+                          int64_t ldd, hipStream_t s) {
   const DhSize d = dh_size(p.rows, p.dim, p.vocab, tile);
   const dim3 grid((unsigned)d.grid);
-  hipError_t e = tile == 64 ? launch_kernel(k_head_dh<64>, grid, dim3(kGemmThreads), s, p, part, dh, ldd)
-                 : tile == 128
-                     ? launch_kernel(k_head_dh<128>, grid, dim3(kGemmThreads), s, p, part, dh, ldd)
-                     : launch_kernel(k_head_dh<256>, grid, dim3(kGemmThreads), s, p, part, dh, ldd);
+  const hipError_t e = pow ? launch_dh<true>(p, tile, grid, part, dh, ldd, s)
+                           : launch_dh<false>(p, tile, grid, part, dh, ldd, s);
   if (e != hipSuccess || d.slots == 0) return e;
-  return launch_kernel(k_head_dh_sum, dim3((unsigned)ceil_div((int64_t)p.rows * p.dim / 8, kThreads)),
-                       dim3(kThreads), s, p, tile, part, dh, ldd);
+  return launch_kernel(k_head_dh_sum, dim3((unsigned)ceil_div((int64_t)p.rows * p.dim / 8, 64)),
+                       dim3(kThreads), s, p, tile, pow, part, dh, ldd);
 }
 
 hipError_t launch_head_dw(const HeadPanel& p, float* acc, int first, int last, uint16_t* dw,
