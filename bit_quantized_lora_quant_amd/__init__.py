@@ -1542,13 +1542,19 @@ def _scaled(d, g):
 class HeadCrossEntropyFn(torch.autograd.Function):
     """autograd wrapper of qlora_head_cross_entropy: the loss, and (without
     gradients) logp.  The gradients are formed in the forward, beside the loss,
-    where any is needed; the backward multiplies them by the upstream gradient."""
+    where autograd will ask for them; the backward multiplies them by the upstream
+    gradient."""
+
+    @classmethod
+    def apply(cls, hidden, weight, labels, reduction="mean"):
+        # (the mode is off inside forward, whose needs_input_grad does not know it)
+        return super().apply(hidden, weight, labels, reduction, torch.is_grad_enabled())
 
     @staticmethod
-    def forward(ctx, hidden, weight, labels, reduction="mean"):
+    def forward(ctx, hidden, weight, labels, reduction, grad):
         o = qlora_head_cross_entropy(hidden, weight, labels, reduction,
-                                     return_grad=ctx.needs_input_grad[0],
-                                     need_dweight=ctx.needs_input_grad[1])
+                                     return_grad=grad and ctx.needs_input_grad[0],
+                                     need_dweight=grad and ctx.needs_input_grad[1])
         # (the inputs only so that a second derivative hangs on them)
         ctx.save_for_backward(o.dhidden, o.dweight, hidden, weight)
         ctx.mark_non_differentiable(o.logp)
@@ -1557,4 +1563,4 @@ class HeadCrossEntropyFn(torch.autograd.Function):
     @staticmethod
     @_first_order
     def backward(ctx, saved, g, _):
-        return tuple(_scaled(d, g) if d is not None else None for d in saved[:2]) + (None, None)
+        return tuple(_scaled(d, g) if d is not None else None for d in saved[:2]) + (None,) * 3

@@ -81,7 +81,8 @@ HeadWs head_layout(const qlora_head* h, bool dh, bool dw) {
   L.lp = take(all * 8);
   L.part = take(cols / 128 * panel * sizeof(HeadPart));
   L.zy = take(panel * 4);
-  L.shift = take(dh && !dw ? cols / 128 * panel * 4 : 0);
+  // (also where dW's path does not use it: more gradients need no less)
+  L.shift = take(dh ? cols / 128 * panel * 4 : 0);
   L.e = take(grad ? panel * cols * 2 : 0);
   L.split = take(dh ? head_dh_floats(panel, (int)h->dim, h->vocab, head_tile(h->rows, h->vocab)) * 4 : 0);
   L.acc = take(dw && h->rows > panel ? (size_t)h->vocab * h->dim * 4 : 0);

@@ -45,10 +45,12 @@ constexpr float kLog2eLo = 1.925963033500e-08f;   // log2 e - kLog2e
 __device__ __forceinline__ float exp_diff(float z, float m) {
   return __builtin_amdgcn_exp2f((z - m) * kLog2e);
 }
-// 2^(z log2 e - m), m a whole number: the difference is rounded once
-__device__ __forceinline__ float pow2_diff(float z, float m) {
-  return __builtin_amdgcn_exp2f(
-      __builtin_fmaf(z, kLog2eLo, __builtin_fmaf(z, kLog2e, -m)));
+// A slice's whole exponent for its largest logit m, and what 2^(z log2 e - M) has beside
+// (z - m) log2 e: m log2 e - M, to float32's last bit while M is exact, and never
+// out of [-1, 0] for logits beyond that.
+__device__ __forceinline__ float slice_exponent(float m) { return ceilf(m * kLog2e); }
+__device__ __forceinline__ float slice_offset(float m, float M) {
+  return fminf(fmaxf(__builtin_fmaf(m, kLog2eLo, __builtin_fmaf(m, kLog2e, -M)), -1.f), 0.f);
 }
 
 // ----------------------------------------------------------------- slices of dh
@@ -535,17 +537,16 @@ void k_head_logits(HeadPanel p) {
     for (int i = 1; i < 32; ++i) m = fmaxf(m, z[i]);
     m = fmaxf(m, __shfl_xor(m, 16));
     m = fmaxf(m, __shfl_xor(m, 32));
-    m = ceilf(m * kLog2e);
-    const float from = m == -INFINITY ? 0.f : m;
+    const float M = slice_exponent(m), off = slice_offset(m, M), from = m == -INFINITY ? 0.f : m;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      z[i] = pow2_diff(z[i], from);
+      z[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i] - from, kLog2e, off));
       s += z[i];
     }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (valid && g == 0) p.part[(2 * tv + wm) * p.rows + row] = HeadPart{m, s};
+    if (valid && g == 0) p.part[(2 * tv + wm) * p.rows + row] = HeadPart{M, s};
     if ((MODE == HEAD_EXP || MODE == HEAD_POW) && valid) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

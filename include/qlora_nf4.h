@@ -752,8 +752,8 @@ typedef struct {
 #define QLORA_HEAD_SUM 1
 
 /* Bytes of workspace the calls below need; grads: the gradients the call
- * returns, QLORA_HEAD_DHIDDEN | QLORA_HEAD_DWEIGHT (0: none).  0 for sizes they
- * refuse. */
+ * returns, QLORA_HEAD_DHIDDEN | QLORA_HEAD_DWEIGHT (0: none); what serves more
+ * gradients serves fewer.  0 for sizes they refuse. */
 size_t qlora_head_workspace_bytes(const qlora_head* h, int32_t grads);
 
 /* Log-probabilities of the targets: logp float32 [rows].  stats (nullable)
