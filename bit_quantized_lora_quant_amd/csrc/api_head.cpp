@@ -57,7 +57,7 @@ int64_t panel_rows(const qlora_head* h) {
 }
 
 struct HeadWs {
-  size_t h, src, y, n, stat, w, scale, lp, part, zy, shift, e, split, acc, total;
+  size_t h, src, y, n, stat, w, scale, zy, lp, part, shift, e, split, acc, total;
 };
 HeadWs head_layout(const qlora_head* h, bool dh, bool dw) {
   HeadWs L;
@@ -78,9 +78,9 @@ HeadWs head_layout(const qlora_head* h, bool dh, bool dw) {
   L.stat = take(grad ? all * sizeof(HeadStat) : 0);
   L.w = take(grad ? all * 4 : 0);
   L.scale = take(grad ? all * sizeof(HeadScale) : 0);
+  L.zy = take(all * 8);
   L.lp = take(all * 8);
   L.part = take(cols / 128 * panel * sizeof(HeadPart));
-  L.zy = take(panel * 4);
   // (also where dW's path does not use it: more gradients need no less)
   L.shift = take(dh ? cols / 128 * panel * 4 : 0);
   L.e = take(grad ? panel * cols * 2 : 0);
@@ -97,7 +97,7 @@ HeadPanel panel(const qlora_head* h, void* ws, const HeadWs& L) {
   HeadPanel p;
   p.r = HeadRows{at<uint16_t>(ws, L.h), at<int32_t>(ws, L.src), at<int32_t>(ws, L.y),
                  at<int32_t>(ws, L.n), at<HeadStat>(ws, L.stat), at<float>(ws, L.w),
-                 at<HeadScale>(ws, L.scale)};
+                 at<HeadScale>(ws, L.scale), at<double>(ws, L.zy)};
   p.row0 = 0;
   p.rows = (int)panel_rows(h);
   p.dim = (int)h->dim;
@@ -105,7 +105,6 @@ HeadPanel panel(const qlora_head* h, void* ws, const HeadWs& L) {
   p.ldw = h->ld_weight;
   p.vocab = h->vocab;
   p.part = at<HeadPart>(ws, L.part);
-  p.zy = at<float>(ws, L.zy);
   p.shift = at<uint32_t>(ws, L.shift);
   p.splits = head_dh_splits(p.rows, p.dim, p.vocab, head_tile(h->rows, h->vocab));
   p.e = at<uint16_t>(ws, L.e);
@@ -119,6 +118,8 @@ HeadPackArgs pack_args(const qlora_head* h, const HeadPanel& p) {
   a.rows = h->rows;
   a.dim = (int)h->dim;
   a.vocab = h->vocab;
+  a.weight = h->weight;
+  a.ldw = h->ld_weight;
   a.labels = h->labels;
   a.to = p.r;
   a.panel = p.rows;
@@ -187,6 +188,7 @@ qlora_status qlora_head_logprobs_bwd(const qlora_head* h, const float* stats, co
   hipStream_t s = static_cast<hipStream_t>(stream);
   HeadPanel p = panel(h, ws, L);
   HeadPackArgs a = pack_args(h, p);
+  a.weight = nullptr;   // (the statistics are the caller's)
   a.w = w;
   a.w_scale = grad_scale;
   a.stat = reinterpret_cast<const HeadStat*>(stats);

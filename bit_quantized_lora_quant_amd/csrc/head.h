@@ -17,8 +17,8 @@ struct HeadStat {
 struct HeadPart {
   float m, s;
 };
-// A row after the join: R, the largest M of its slices; f and c with
-// dz_v = f 2^(z_v log2 e - R), at the target c = w (1 - p).
+// A row's gradient: R, the largest M of its slices; f and c with
+// dz_v = f 2^(z_v log2 e - R), at the target c = w (1 - p).  (The backward: c alone.)
 struct HeadScale {
   float r, f, c;
 };
@@ -33,6 +33,7 @@ struct HeadRows {
   HeadStat* stat;
   float* w;
   HeadScale* scale;
+  double* zy;         // the target's logit
 };
 
 struct HeadPackArgs {
@@ -40,6 +41,8 @@ struct HeadPackArgs {
   int64_t ldh, rows;
   int dim;
   int64_t vocab;
+  const uint16_t* weight;  // nullable: no target's logit
+  int64_t ldw;
   const int64_t* labels;
   const float* w;          // nullable: rows of weight 0 count as without target
   const float* w_scale;    // nullable, [1]
@@ -65,7 +68,6 @@ struct HeadPanel {
   const uint16_t* weight;
   int64_t ldw, vocab;
   HeadPart* part;      // [vocab tiles * 2][rows]
-  float* zy;           // [rows] the target's logit
   uint32_t* shift;     // [vocab tiles * 2][rows] R - M, in both halves as bf16's exponent
   int splits;          // slices of dh in a full panel
   uint16_t* e;         // [rows][head_cols(vocab)] exponentials (fp16), then dz (bf16)
@@ -76,7 +78,7 @@ int head_dh_splits(int64_t rows, int dim, int64_t vocab, int tile);
 // Rows of tokens per workgroup tile (64, 128 or 256) of a call.
 int head_tile(int64_t rows, int64_t vocab);
 
-// HEAD_STATS: part and zy; HEAD_EXP: these and e; HEAD_DZ: dz from r.stat and r.w;
+// HEAD_STATS: part; HEAD_EXP: part and e; HEAD_DZ: dz from r.stat and r.w;
 // HEAD_POW: as HEAD_EXP with e in bf16, which dh takes as it is
 enum { HEAD_STATS = 0, HEAD_EXP = 1, HEAD_DZ = 2, HEAD_POW = 3 };
 hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, hipStream_t s);

@@ -119,8 +119,10 @@ __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t 
       a.to.src[p] = (int32_t)t;
       a.to.y[p] = y < a.vocab ? (int32_t)y : -1;
       if (a.w) {
-        a.to.w[p] = scale * a.w[t];
+        const float w = scale * a.w[t];
+        a.to.w[p] = w;
         a.to.stat[p] = a.stat[t];
+        a.to.scale[p] = HeadScale{0.f, 0.f, y < a.vocab ? w * a.stat[t].rest : NAN};
       }
     } else if (t < end) {
       if (a.logp) a.logp[t] = 0.f;
@@ -133,8 +135,31 @@ __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t 
       const uint4* in = reinterpret_cast<const uint4*>(a.hidden + (t0 + i) * a.ldh);
       if (q >= 0) {
         uint4* out = reinterpret_cast<uint4*>(a.to.h + (int64_t)q * a.dim);
+        const int64_t y = a.labels[t0 + i];
+        if (!a.weight || y >= a.vocab) {
 #pragma unroll 4
-        for (int k = lane; k < chunks; k += 64) out[k] = in[k];
+          for (int k = lane; k < chunks; k += 64) out[k] = in[k];
+          continue;
+        }
+        // the target's logit, in float64: logp and 1 - p of a likely target hang on its
+        // last bits (from the product's float32 sum logp of one row at D = 4096 was
+        // off by 6e-6 of itself, and torch's by 5e-7)
+        const uint4* with = reinterpret_cast<const uint4*>(a.weight + y * a.ldw);
+        double z = 0;
+#pragma unroll 4
+        for (int k = lane; k < chunks; k += 64) {
+          const uint4 x = in[k], w = with[k];
+          out[k] = x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t u = (&x.x)[e], v = (&w.x)[e];
+            z += (double)(bf16_to_f32((uint16_t)u) * bf16_to_f32((uint16_t)v)) +
+                 (double)(bf16_to_f32((uint16_t)(u >> 16)) * bf16_to_f32((uint16_t)(v >> 16)));
+          }
+        }
+#pragma unroll
+        for (int d = 32; d; d >>= 1) z += __shfl_xor(z, d);
+        if (lane == 0) a.to.zy[q] = z;
       } else if (a.dh) {
         uint4* out = reinterpret_cast<uint4*>(a.dh + (t0 + i) * a.ldd);
         for (int k = lane; k < chunks; k += 64) out[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -527,10 +552,7 @@ void k_head_logits(HeadPanel p) {
     if (__builtin_amdgcn_ballot_w64(rel >= 0 && rel < 128)) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (rel == 32 * (i >> 3) + (i & 7)) {
-          p.zy[row] = z[i];
-          z[i] = -INFINITY;
-        }
+        if (rel == 32 * (i >> 3) + (i & 7)) z[i] = -INFINITY;
     }
     float m = z[0];
 #pragma unroll
@@ -586,7 +608,7 @@ void k_head_join(HeadPanel p, int kind, int shift, double* lp, float* logp, Head
   m = fmaxf(m, __shfl_xor(m, 32));
   if (lane < 16) ms[wv][r] = m;
   const int32_t y = p.r.y[p.row0 + rr];
-  const float zy = y >= 0 ? p.zy[rr] : NAN;
+  const double zy = y >= 0 ? p.r.zy[p.row0 + rr] : NAN;
   __syncthreads();
   m = ms[0][r];
 #pragma unroll
@@ -612,11 +634,11 @@ void k_head_join(HeadPanel p, int kind, int shift, double* lp, float* logp, Head
 #pragma unroll
   for (int k = 0; k < kJoinWaves; ++k) s += ss[k][r];
   // the target joins: both relative to 2^top
-  const double ty = (double)zy * 1.4426950408889634074, top = fmax((double)m, ceil(ty));
+  const double ty = zy * 1.4426950408889634074, top = fmax((double)m, ceil(ty));
   const double out = m == -INFINITY ? 0.0 : exp2((double)m - top);
   const double rest = m == -INFINITY ? 0.0 : s * out, all = rest + exp2(ty - top);
   const double lse = (top + log2(all)) * 0.69314718055994530942;
-  double l = (double)zy - lse;
+  double l = zy - lse;
   HeadStat st{(float)lse, (float)(rest / all)};
   const double w = kind == HEAD_GRAD_MEAN ? -1.0 / *p.r.n : -1.0;
   HeadScale sc{m, (float)(-w * out / all), (float)(w * rest / all)};
@@ -716,14 +738,18 @@ __device__ __forceinline__ uint4 pack8(const float (&o)[8]) {
 // the row's R, and what is left is a factor of the whole row and the target's term,
 // c times its row of W, in float32 at the end.  So dz is rounded to bf16 once, e is
 // written once and read once, and the target's cancellation stays out of the sums.
-__device__ __forceinline__ void finish_row(const HeadPanel& p, int64_t q, int64_t col,
+// From dz, the target's own rounding is put right the same way: it is the largest
+// of its row, half of the gradient's error (2.4e-3 of its norm against 1.7e-3).
+__device__ __forceinline__ void finish_row(const HeadPanel& p, bool pow, int64_t q, int64_t col,
                                            float (&o)[8]) {
   const HeadScale sc = p.r.scale[q];
   const int y = p.r.y[q];
   const uint4 w = *reinterpret_cast<const uint4*>(p.weight + (y < 0 ? 0 : y) * p.ldw + col);
+  const float f = pow ? sc.f : 1.f;
+  const float c = pow ? sc.c : sc.c - bf16_to_f32((uint16_t)pack_bf16x2(sc.c, 0.f));
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    o[k] = sc.f * o[k] + sc.c * bf16_to_f32((uint16_t)((&w.x)[k >> 1] >> (16 * (k & 1))));
+    o[k] = f * o[k] + c * bf16_to_f32((uint16_t)((&w.x)[k >> 1] >> (16 * (k & 1))));
 }
 
 template <int TN, bool POW>
@@ -769,7 +795,7 @@ void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
         to[0] = make_float4(o[0], o[1], o[2], o[3]);
         to[1] = make_float4(o[4], o[5], o[6], o[7]);
       } else if (col < p.dim) {
-        if (POW) finish_row(p, p.row0 + row, col, o);
+        finish_row(p, POW, p.row0 + row, col, o);
         *reinterpret_cast<uint4*>(dh + p.r.src[p.row0 + row] * ldd + col) = pack8(o);
       }
     }
@@ -812,7 +838,7 @@ __global__ __launch_bounds__(kThreads) void k_head_dh_sum(HeadPanel p, int TN, i
   if (wv > 0 || !in) return;
 #pragma unroll
   for (int w = 0; w < 3; ++w) add(buf[w][0][lane], buf[w][1][lane]);
-  if (pow) finish_row(p, p.row0 + row, col, o);
+  finish_row(p, pow, p.row0 + row, col, o);
   *reinterpret_cast<uint4*>(dh + p.r.src[p.row0 + row] * ldd + col) = pack8(o);
 }
 
