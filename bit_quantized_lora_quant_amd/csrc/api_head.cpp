@@ -3,6 +3,7 @@
 // call, as in api.cpp.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/qlora_nf4.h"
@@ -57,7 +58,8 @@ int64_t panel_rows(const qlora_head* h) {
 }
 
 struct HeadWs {
-  size_t h, src, y, n, stat, w, scale, zy, lp, part, shift, e, split, acc, total;
+  size_t h, src, y, n, stat, w, scale, zy, last, lp, part, shift, e, split, rest, acc,
+      total;
 };
 HeadWs head_layout(const qlora_head* h, bool dh, bool dw) {
   HeadWs L;
@@ -79,12 +81,19 @@ HeadWs head_layout(const qlora_head* h, bool dh, bool dw) {
   L.w = take(grad ? all * 4 : 0);
   L.scale = take(grad ? all * sizeof(HeadScale) : 0);
   L.zy = take(all * 8);
+  L.last = take(dw ? (size_t)h->vocab * 4 : 0);
   L.lp = take(all * 8);
   L.part = take(cols / 128 * panel * sizeof(HeadPart));
   // (also where dW's path does not use it: more gradients need no less)
   L.shift = take(dh ? cols / 128 * panel * 4 : 0);
   L.e = take(grad ? panel * cols * 2 : 0);
-  L.split = take(dh ? head_dh_floats(panel, (int)h->dim, h->vocab, head_tile(h->rows, h->vocab)) * 4 : 0);
+  // parts of whichever product's inner index is cut, one after the other
+  const int tile = head_tile(h->rows, h->vocab), dim = (int)h->dim;
+  size_t split = head_logits_floats(panel, dim, h->vocab, tile);
+  if (dh) split = std::max(split, head_dh_floats(panel, dim, h->vocab, tile));
+  if (dw) split = std::max(split, head_dw_floats(panel, dim, h->vocab));
+  L.split = take(split * 4);
+  L.rest = take(dw ? (size_t)head_slots(panel, h->vocab) * h->dim * 4 : 0);
   L.acc = take(dw && h->rows > panel ? (size_t)h->vocab * h->dim * 4 : 0);
   L.total = off;
   return L;
@@ -93,11 +102,11 @@ HeadWs head_layout(const qlora_head* h, bool dh, bool dw) {
 template <typename T>
 T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
 
-HeadPanel panel(const qlora_head* h, void* ws, const HeadWs& L) {
+HeadPanel panel(const qlora_head* h, void* ws, const HeadWs& L, bool dw) {
   HeadPanel p;
   p.r = HeadRows{at<uint16_t>(ws, L.h), at<int32_t>(ws, L.src), at<int32_t>(ws, L.y),
                  at<int32_t>(ws, L.n), at<HeadStat>(ws, L.stat), at<float>(ws, L.w),
-                 at<HeadScale>(ws, L.scale), at<double>(ws, L.zy)};
+                 at<HeadScale>(ws, L.scale), at<double>(ws, L.zy), at<int32_t>(ws, L.last)};
   p.row0 = 0;
   p.rows = (int)panel_rows(h);
   p.dim = (int)h->dim;
@@ -105,6 +114,7 @@ HeadPanel panel(const qlora_head* h, void* ws, const HeadWs& L) {
   p.ldw = h->ld_weight;
   p.vocab = h->vocab;
   p.part = at<HeadPart>(ws, L.part);
+  p.want_last = dw;
   p.shift = at<uint32_t>(ws, L.shift);
   p.splits = head_dh_splits(p.rows, p.dim, p.vocab, head_tile(h->rows, h->vocab));
   p.e = at<uint16_t>(ws, L.e);
@@ -132,8 +142,10 @@ hipError_t panel_grads(const qlora_head* h, const HeadPanel& p, void* ws, const 
                        int pow, uint16_t* dh, int64_t ldd, uint16_t* dw, int64_t ldo, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (dh) e = launch_head_dh(p, tile, pow, at<float>(ws, L.split), dh, ldd, s);
+  if (e == hipSuccess && dw) e = launch_head_rest(p, at<float>(ws, L.rest), s);
   if (e == hipSuccess && dw)
-    e = launch_head_dw(p, h->rows > p.rows ? at<float>(ws, L.acc) : nullptr, p.row0 == 0,
+    e = launch_head_dw(p, at<float>(ws, L.rest), at<float>(ws, L.split),
+                       h->rows > p.rows ? at<float>(ws, L.acc) : nullptr, p.row0 == 0,
                        p.row0 + p.rows >= h->rows, dw, ldo, s);
   return e;
 }
@@ -158,14 +170,14 @@ qlora_status qlora_head_logprobs(const qlora_head* h, float* logp, float* stats,
   const HeadWs L = head_layout(h, false, false);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  HeadPanel p = panel(h, ws, L);
+  HeadPanel p = panel(h, ws, L, false);
   HeadPackArgs a = pack_args(h, p);
   a.logp = logp;
   a.stat_out = reinterpret_cast<HeadStat*>(stats);
   const int tile = head_tile(h->rows, h->vocab);
   hipError_t e = launch_head_pack(a, s);
   for (; e == hipSuccess && p.row0 < h->rows; p.row0 += p.rows) {
-    e = launch_head_logits(p, tile, HEAD_STATS, s);
+    e = launch_head_logits(p, tile, HEAD_STATS, at<float>(ws, L.split), s);
     if (e == hipSuccess)
       e = launch_head_join(p, HEAD_SCORE, 0, nullptr, logp, a.stat_out, s);
   }
@@ -186,7 +198,7 @@ qlora_status qlora_head_logprobs_bwd(const qlora_head* h, const float* stats, co
   const HeadWs L = head_layout(h, dhidden, dweight);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  HeadPanel p = panel(h, ws, L);
+  HeadPanel p = panel(h, ws, L, dweight);
   HeadPackArgs a = pack_args(h, p);
   a.weight = nullptr;   // (the statistics are the caller's)
   a.w = w;
@@ -198,7 +210,7 @@ qlora_status qlora_head_logprobs_bwd(const qlora_head* h, const float* stats, co
   const int tile = head_tile(h->rows, h->vocab);
   hipError_t e = launch_head_pack(a, s);
   do {
-    if (e == hipSuccess) e = launch_head_logits(p, tile, HEAD_DZ, s);
+    if (e == hipSuccess) e = launch_head_logits(p, tile, HEAD_DZ, at<float>(ws, L.split), s);
     if (e == hipSuccess) e = panel_grads(h, p, ws, L, tile, 0, dhidden, ldd, dweight, ldo, s);
     p.row0 += p.rows;
   } while (e == hipSuccess && p.row0 < h->rows);
@@ -218,7 +230,7 @@ qlora_status qlora_head_cross_entropy(const qlora_head* h, int32_t reduction, fl
   const HeadWs L = head_layout(h, dhidden, dweight);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  HeadPanel p = panel(h, ws, L);
+  HeadPanel p = panel(h, ws, L, dweight);
   HeadPackArgs a = pack_args(h, p);
   a.logp = logp;
   a.dh = dhidden;
@@ -228,7 +240,9 @@ qlora_status qlora_head_cross_entropy(const qlora_head* h, int32_t reduction, fl
   const bool grad = dhidden || dweight, pow = grad && !dweight;
   hipError_t e = launch_head_pack(a, s);
   do {
-    if (e == hipSuccess) e = launch_head_logits(p, tile, pow ? HEAD_POW : grad ? HEAD_EXP : HEAD_STATS, s);
+    if (e == hipSuccess)
+      e = launch_head_logits(p, tile, pow ? HEAD_POW : grad ? HEAD_EXP : HEAD_STATS,
+                             at<float>(ws, L.split), s);
     if (e == hipSuccess)
       e = launch_head_join(p, !grad ? HEAD_LOSS : mean ? HEAD_GRAD_MEAN : HEAD_GRAD_SUM,
                            pow, at<double>(ws, L.lp), logp, nullptr, s);

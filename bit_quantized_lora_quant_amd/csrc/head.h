@@ -34,6 +34,7 @@ struct HeadRows {
   float* w;
   HeadScale* scale;
   double* zy;         // the target's logit
+  int32_t* last;      // [vocab] the last packed row with that target, -1 none (for dW)
 };
 
 struct HeadPackArgs {
@@ -49,7 +50,7 @@ struct HeadPackArgs {
   const HeadStat* stat;    // with w
   HeadRows to;
   int panel, tile;         // rows of a panel and of a tile
-  int pad;                 // zero rows behind the last, for dW
+  int pad;                 // for dW: zero rows behind the last, and to.last
   // rows without a target, each nullable
   float* logp;
   HeadStat* stat_out;
@@ -70,6 +71,7 @@ struct HeadPanel {
   HeadPart* part;      // [vocab tiles * 2][rows]
   uint32_t* shift;     // [vocab tiles * 2][rows] R - M, in both halves as bf16's exponent
   int splits;          // slices of dh in a full panel
+  int want_last;       // r.last is needed (dW)
   uint16_t* e;         // [rows][head_cols(vocab)] exponentials (fp16), then dz (bf16)
 };
 // Columns of a panel's row.
@@ -81,7 +83,9 @@ int head_tile(int64_t rows, int64_t vocab);
 // HEAD_STATS: part; HEAD_EXP: part and e; HEAD_DZ: dz from r.stat and r.w;
 // HEAD_POW: as HEAD_EXP with e in bf16, which dh takes as it is
 enum { HEAD_STATS = 0, HEAD_EXP = 1, HEAD_DZ = 2, HEAD_POW = 3 };
-hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, hipStream_t s);
+// part: head_logits_floats floats (of partial logits, where the inner index is cut)
+size_t head_logits_floats(int64_t rows, int dim, int64_t vocab, int tile);
+hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, float* part, hipStream_t s);
 // Joins the slices: logp and stat of the rows (nullable, by source row).
 // From HEAD_LOSS on the packed rows' logp in lp; with HEAD_GRAD_* also r.scale for
 // w = -1 (sum) or -1 / n (mean), and p.shift where `shift`.
@@ -97,9 +101,17 @@ hipError_t launch_head_dz(const HeadPanel& p, hipStream_t s);
 size_t head_dh_floats(int64_t rows, int dim, int64_t vocab, int tile);
 hipError_t launch_head_dh(const HeadPanel& p, int tile, int pow, float* part, uint16_t* dh, int64_t ldd,
                           hipStream_t s);
-// dw = dz^T . h (bf16, row stride ldo), or with acc [vocab][dim] over several
+// What rounding the targets' dz leaves of dW, in float32: rest[head_slot] = sum over the
+// panel's rows with that target of (c - bf16(c)) h.
+__host__ __device__ inline int64_t head_slots(int64_t rows, int64_t vocab) {
+  return rows < vocab ? rows : vocab;
+}
+hipError_t launch_head_rest(const HeadPanel& p, float* rest, hipStream_t s);
+// dw = dz^T . h + rest (bf16, row stride ldo), or with acc [vocab][dim] over several
 // panels: added to it (stored where first), and only the last writes dw.
-hipError_t launch_head_dw(const HeadPanel& p, float* acc, int first, int last, uint16_t* dw,
-                          int64_t ldo, hipStream_t s);
+// part: head_dw_floats floats
+size_t head_dw_floats(int64_t rows, int dim, int64_t vocab);
+hipError_t launch_head_dw(const HeadPanel& p, const float* rest, float* part, float* acc, int first,
+                          int last, uint16_t* dw, int64_t ldo, hipStream_t s);
 
 }  // namespace qnf4

@@ -102,6 +102,10 @@ __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t 
   if (lane == 0) wave_count[wv] = c;
   __syncthreads();
   int at = wave_count[0] + wave_count[1] + wave_count[2] + wave_count[3];
+  if (a.pad)
+    for (int64_t v = (int64_t)blockIdx.x * kThreads + tid; v < a.vocab;
+         v += (int64_t)gridDim.x * kThreads)
+      a.to.last[v] = -1;
   const float scale = a.w && a.w_scale ? a.w_scale[0] : 1.f;
   const int chunks = a.dim / 8;
   for (int64_t t0 = first; t0 < end; t0 += kThreads) {
@@ -491,19 +495,25 @@ __device__ __forceinline__ int panel_splits(const HeadPanel& p, int n) {
 // -------------------------------------------------------------------- logits
 // A = W (the vocabulary along a lane's registers: a row's statistics are sums in the
 // lane, then over the four lanes of its column), B = rows.
+constexpr int HEAD_RAW = 4;    // partial logits of a slice of the inner index
 template <int TN, int MODE>
 __global__ __attribute__((amdgpu_flat_work_group_size(kGemmThreads, kGemmThreads),
                           amdgpu_waves_per_eu(kWaves / 4, kWaves / 4)))
-void k_head_logits(HeadPanel p) {
+void k_head_logits(HeadPanel p, int splits, float* part) {
   __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
   constexpr int NB = Shape<TN>::kTilesB;
   const int n = panel_rows(p);
+  const int64_t na = ceil_div(p.vocab, kTileA), nb = ceil_div(n, TN);
   int64_t tv, tt;
-  if (!tile_of(blockIdx.x, ceil_div(p.vocab, kTileA), ceil_div(n, TN), tv, tt)) return;
+  int sl;
+  if (!tile_of(blockIdx.x, na, nb, tv, tt, MODE == HEAD_RAW ? splits : 1, &sl)) return;
+  const int64_t steps = p.dim / kStep, each = MODE == HEAD_RAW ? ceil_div(steps, splits) : steps;
   const Operand A{p.weight, p.ldw, p.vocab, p.dim};
   const Operand B{p.r.h + p.row0 * p.dim, p.dim, n, p.dim};
   f32x4_t acc[8][NB];
-  tile_loop<TN, false, false>(acc, lds, A, tv * kTileA, B, tt * TN, 0, p.dim / kStep);
+  // (no slice is empty: logits_splits)
+  tile_loop<TN, false, false>(acc, lds, A, tv * kTileA, B, tt * TN, sl * each,
+                              (sl + 1) * each < steps ? (sl + 1) * each : steps);
 
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -514,6 +524,14 @@ void k_head_logits(HeadPanel p) {
   for (int t = 0; t < NB; ++t) {
     const int row = (int)(tt * TN) + 16 * (NB * wn + t) + j;
     const bool valid = row < n;
+    if constexpr (MODE == HEAD_RAW) {
+      float* to = part + ((sl * na + tv) * nb + tt) * (TN * kTileA) +
+                  (row - tt * TN) * kTileA + 128 * wm + 8 * g;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<f32x4_t*>(to + 32 * (i >> 1) + 4 * (i & 1)) = acc[i][t];
+      continue;
+    }
     const int64_t q = p.row0 + (valid ? row : 0);
     const int64_t rel = valid ? (int64_t)p.r.y[q] - v0 - 8 * g : -1;   // in this lane: 32 i + 4 h + v
     float z[32];
@@ -535,7 +553,10 @@ void k_head_logits(HeadPanel p) {
       if (__builtin_amdgcn_ballot_w64(rel >= 0 && rel < 128)) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (rel == 32 * (i >> 3) + (i & 7)) z[i] = w * st.rest;
+          if (rel == 32 * (i >> 3) + (i & 7)) {
+            z[i] = w * st.rest;
+            if (p.want_last) atomicMax(p.r.last + p.r.y[q], (int)q);
+          }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -552,7 +573,10 @@ void k_head_logits(HeadPanel p) {
     if (__builtin_amdgcn_ballot_w64(rel >= 0 && rel < 128)) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (rel == 32 * (i >> 3) + (i & 7)) z[i] = -INFINITY;
+        if (rel == 32 * (i >> 3) + (i & 7)) {
+          z[i] = -INFINITY;
+          if (MODE == HEAD_EXP) atomicMax(p.r.last + p.r.y[q], (int)q);
+        }
     }
     float m = z[0];
 #pragma unroll
@@ -583,6 +607,75 @@ void k_head_logits(HeadPanel p) {
       }
     }
   }
+}
+
+// With few tiles (a small vocabulary, few rows) the logits' inner index is cut over
+// the CUs and this kernel adds the parts and does what the tile's epilogue does
+// otherwise: a wave per row and slice of 128 vocabulary entries, two a lane.
+template <int MODE>
+__global__ __launch_bounds__(kThreads) void k_head_slices(HeadPanel p, int TN, int splits,
+                                                          const float* part) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int n = panel_rows(p);
+  const int row = blockIdx.x * 4 + wv, sl = blockIdx.y;
+  // (rows behind the last: zeros for dW's inner index)
+  const int rows = MODE == HEAD_DZ ? (int)ceil_div(n, kStep) * kStep : n;
+  if (row >= rows) return;
+  const int64_t na = ceil_div(p.vocab, kTileA), nb = ceil_div(n, TN), cols = head_cols(p.vocab);
+  const int64_t v = 128 * (int64_t)sl + 2 * lane;
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.e + row * cols + v);
+  if (MODE == HEAD_DZ && row >= n) {
+    *out = 0u;
+    return;
+  }
+  const float* from = part + ((sl >> 1) * nb + row / TN) * (TN * kTileA) + (row % TN) * kTileA +
+                      128 * (sl & 1) + 2 * lane;
+  float z[2] = {0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float2 x = *reinterpret_cast<const float2*>(from + s * (na * nb * (TN * kTileA)));
+    z[0] += x.x;
+    z[1] += x.y;
+  }
+  const int64_t q = p.row0 + row;
+  const int y = p.r.y[q];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (v + e >= p.vocab) z[e] = -INFINITY;
+  if (MODE == HEAD_DZ) {
+    const HeadStat st = p.r.stat[q];
+    const float w = p.r.w[q];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      z[e] = -w * exp_diff(z[e], st.lse);
+      if (v + e == y) {
+        z[e] = w * st.rest;
+        if (p.want_last) atomicMax(p.r.last + y, (int)q);
+      }
+    }
+    *out = pack_bf16x2(z[0], z[1]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (v + e == y) {
+      z[e] = -INFINITY;
+      if (MODE == HEAD_EXP) atomicMax(p.r.last + y, (int)q);
+    }
+  float m = fmaxf(z[0], z[1]);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float M = slice_exponent(m), off = slice_offset(m, M), at = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    z[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e] - at, kLog2e, off));
+  float s = z[0] + z[1];
+#pragma unroll
+  for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+  if (lane == 0) p.part[(int64_t)sl * p.rows + row] = HeadPart{M, s};
+  if (MODE == HEAD_POW) *out = pack_bf16x2(z[0], z[1]);
+  if (MODE == HEAD_EXP)
+    *out = __builtin_bit_cast(uint32_t, half2_t{(_Float16)z[0], (_Float16)z[1]});
 }
 
 // ---------------------------------------------------------------------- join
@@ -843,21 +936,81 @@ __global__ __launch_bounds__(kThreads) void k_head_dh_sum(HeadPanel p, int TN, i
 }
 
 // ------------------------------------------------------------------------ dW
+// A vocabulary row's gradient is often one row's target and little else, so its dz's
+// rounding to bf16 would be as large as the output's own (2.6e-3 of dW's norm against
+// 1.7e-3).  What it leaves out is added in float32.  A workgroup per packed row, at
+// work where that row is its target's last: it looks through the panel's labels and
+// adds the rows in order.  Of more than 256 rows the roundings, which have no bias,
+// add up to less than a sixteenth of one's: there nothing is added.
+__device__ __forceinline__ int64_t rest_slot(const HeadPanel& p, int64_t v, int64_t q) {
+  return p.rows < p.vocab ? q - p.row0 : v;
+}
+constexpr int kFound = 256;
+__global__ __launch_bounds__(kThreads) void k_head_rest(HeadPanel p, float* rest) {
+  __shared__ int found[kFound];
+  __shared__ float off[kFound];
+  __shared__ int wave_count[4];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int n = panel_rows(p), self = blockIdx.x;
+  if (self >= n) return;
+  const int y = p.r.y[p.row0 + self];
+  if (y < 0 || p.r.last[y] != p.row0 + self) return;
+  int have = 0;
+  for (int t0 = 0; t0 <= self && have <= kFound; t0 += kThreads) {
+    const int t = t0 + tid;
+    const bool hit = t <= self && p.r.y[p.row0 + t] == y;
+    const uint64_t m = __builtin_amdgcn_ballot_w64(hit);
+    if (lane == 0) wave_count[wv] = __popcll(m);
+    __syncthreads();
+    int at = have + __popcll(m & ((1ull << lane) - 1));
+    for (int w = 0; w < wv; ++w) at += wave_count[w];
+    if (hit && at < kFound) {
+      const float c = p.r.scale[p.row0 + t].c;
+      found[at] = t;
+      off[at] = c - bf16_to_f32((uint16_t)pack_bf16x2(c, 0.f));
+    }
+    have += wave_count[0] + wave_count[1] + wave_count[2] + wave_count[3];
+    __syncthreads();
+  }
+  if (have > kFound) have = 0;
+  float* out = rest + rest_slot(p, y, p.row0 + self) * p.dim;
+  for (int col = 8 * tid; col < p.dim; col += kThreads * 8) {
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int k = 0; k < have; ++k) {
+      const uint4 h =
+          *reinterpret_cast<const uint4*>(p.r.h + (p.row0 + found[k]) * p.dim + col);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o[e] += off[k] * bf16_to_f32((uint16_t)((&h.x)[e >> 1] >> (16 * (e & 1))));
+    }
+    float4* to = reinterpret_cast<float4*>(out + col);
+    to[0] = make_float4(o[0], o[1], o[2], o[3]);
+    to[1] = make_float4(o[4], o[5], o[6], o[7]);
+  }
+}
+
 // A = h (transposed by the reads), B = dz (likewise); inner index the rows.
 __global__ __attribute__((amdgpu_flat_work_group_size(kGemmThreads, kGemmThreads),
                           amdgpu_waves_per_eu(kWaves / 4, kWaves / 4)))
-void k_head_dw(HeadPanel p, float* sum, int first, int last, uint16_t* dw, int64_t ldo) {
+void k_head_dw(HeadPanel p, const float* rest, int splits, float* part, float* sum, int first,
+               int last, uint16_t* dw, int64_t ldo) {
   constexpr int TN = 256, NB = Shape<TN>::kTilesB;
   __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
   const int n = panel_rows(p);
+  const int64_t na = ceil_div(p.dim, kTileA), nb = ceil_div(p.vocab, TN);
   int64_t td, tv;
-  if (!tile_of(blockIdx.x, ceil_div(p.dim, kTileA), ceil_div(p.vocab, TN), td, tv)) return;
+  int sl;
+  if (!tile_of(blockIdx.x, na, nb, td, tv, splits, &sl)) return;
   const int64_t cols = head_cols(p.vocab), steps = ceil_div(n, kStep);
+  const int64_t each = ceil_div(steps, splits), s0 = sl * each;
+  const int64_t s1 = s0 + each < steps ? s0 + each : steps;
+  if (splits > 1 && s0 >= s1) return;      // (k_head_dw_sum leaves it out)
   const Operand A{p.r.h + p.row0 * p.dim, p.dim, p.dim, steps * kStep};
   const Operand B{p.e, cols, cols, steps * kStep};
   f32x4_t acc[8][NB];
   if (steps > 0) {
-    tile_loop<TN, true, true>(acc, lds, A, td * kTileA, B, tv * TN, 0, steps);
+    tile_loop<TN, true, true>(acc, lds, A, td * kTileA, B, tv * TN, s0, s1);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -875,12 +1028,32 @@ void k_head_dw(HeadPanel p, float* sum, int first, int last, uint16_t* dw, int64
   for (int t = 0; t < NB; ++t) {
     const int64_t v = tv * TN + 16 * (NB * wn + t) + j;
     if (v >= p.vocab) continue;
+    if (splits > 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float o[8];
+        eight<NB>(acc, i, t, g, o);
+        float4* to = reinterpret_cast<float4*>(part + ((sl * na + td) * nb + tv) * (TN * kTileA) +
+                                               (v - tv * TN) * kTileA + 128 * wm + 32 * i + 8 * g);
+        to[0] = make_float4(o[0], o[1], o[2], o[3]);
+        to[1] = make_float4(o[4], o[5], o[6], o[7]);
+      }
+      continue;
+    }
+    const int row = p.r.last[v];         // (of an earlier panel: none here)
+    const float* add = row < p.row0 ? nullptr : rest + rest_slot(p, v, row) * p.dim;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t col = td * kTileA + 128 * wm + 32 * i + 8 * g;
       if (col >= p.dim) continue;
       float o[8];
       eight<NB>(acc, i, t, g, o);
+      if (add) {
+        const float4 a = *reinterpret_cast<const float4*>(add + col);
+        const float4 b = *reinterpret_cast<const float4*>(add + col + 4);
+        o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
+        o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
+      }
       if (sum) {
         float4* at = reinterpret_cast<float4*>(sum + v * p.dim + col);
         if (!first) {
@@ -898,16 +1071,75 @@ void k_head_dw(HeadPanel p, float* sum, int first, int last, uint16_t* dw, int64
   }
 }
 
+// Few tiles of dW: its rows were cut over the CUs; a thread 8 values.
+__global__ __launch_bounds__(kThreads) void k_head_dw_sum(HeadPanel p, const float* rest, int splits,
+                                                          const float* part, uint16_t* dw,
+                                                          int64_t ldo) {
+  const int n = panel_rows(p);
+  const int64_t na = ceil_div(p.dim, kTileA), nb = ceil_div(p.vocab, kTileA);
+  const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int per = p.dim / 8;
+  const int64_t v = k / per;
+  const int col = (int)(k - v * per) * 8;
+  if (v >= p.vocab) return;
+  const int64_t steps = ceil_div(n, kStep), each = ceil_div(steps, splits);
+  const int used = each > 0 ? (int)ceil_div(steps, each) : 0;
+  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  auto add = [&](const float* x) {
+    const float4 a = *reinterpret_cast<const float4*>(x);
+    const float4 b = *reinterpret_cast<const float4*>(x + 4);
+    o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
+    o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
+  };
+  const float* from = part + ((col / kTileA) * nb + v / kTileA) * (kTileA * kTileA) +
+                      (v % kTileA) * kTileA + col % kTileA;
+#pragma unroll 4
+  for (int s = 0; s < used; ++s) add(from + s * (na * nb * (kTileA * kTileA)));
+  const int row = p.r.last[v];
+  if (row >= p.row0) add(rest + rest_slot(p, v, row) * p.dim + col);
+  *reinterpret_cast<uint4*>(dw + v * ldo + col) = pack8(o);
+}
+
+// Slices of an inner index of `steps` where `tiles` tiles leave CUs without one, none
+// of them empty, each of four steps or more: the parts cost about as much.
+int few_tiles_splits(int64_t tiles, int64_t steps) {
+  int64_t s = 256 / (tiles > 0 ? tiles : 1);
+  s = s < steps / 4 ? s : steps / 4;
+  s = s < 32 ? s : 32;
+  if (s < 2) return 1;
+  return (int)ceil_div(steps, ceil_div(steps, s));
+}
+int logits_splits(int64_t rows, int dim, int64_t vocab, int tile) {
+  return few_tiles_splits(ceil_div(vocab, kTileA) * ceil_div(rows, tile), dim / kStep);
+}
+int dw_splits(int64_t rows, int dim, int64_t vocab) {
+  return few_tiles_splits(ceil_div(dim, kTileA) * ceil_div(vocab, kTileA), ceil_div(rows, kStep));
+}
+
 unsigned grid8(int64_t tiles) { return (unsigned)(ceil_div(tiles, 8) * 8); }
 
 template <int TN>
-hipError_t launch_logits(const HeadPanel& p, int mode, hipStream_t s) {
-  const dim3 grid(grid8(ceil_div(p.vocab, kTileA) * ceil_div(p.rows, TN)));
-  if (mode == HEAD_STATS)
-    return launch_kernel(k_head_logits<TN, HEAD_STATS>, grid, dim3(kGemmThreads), s, p);
-  if (mode == HEAD_POW) return launch_kernel(k_head_logits<TN, HEAD_POW>, grid, dim3(kGemmThreads), s, p);
-  if (mode == HEAD_EXP) return launch_kernel(k_head_logits<TN, HEAD_EXP>, grid, dim3(kGemmThreads), s, p);
-  return launch_kernel(k_head_logits<TN, HEAD_DZ>, grid, dim3(kGemmThreads), s, p);
+hipError_t launch_logits(const HeadPanel& p, int mode, int splits, float* part, hipStream_t s) {
+  const dim3 grid(grid8(ceil_div(p.vocab, kTileA) * ceil_div(p.rows, TN) * splits));
+  const dim3 block(kGemmThreads);
+  switch (splits > 1 ? HEAD_RAW : mode) {
+    case HEAD_STATS: return launch_kernel(k_head_logits<TN, HEAD_STATS>, grid, block, s, p, 1, part);
+    case HEAD_EXP: return launch_kernel(k_head_logits<TN, HEAD_EXP>, grid, block, s, p, 1, part);
+    case HEAD_DZ: return launch_kernel(k_head_logits<TN, HEAD_DZ>, grid, block, s, p, 1, part);
+    case HEAD_POW: return launch_kernel(k_head_logits<TN, HEAD_POW>, grid, block, s, p, 1, part);
+    default: break;
+  }
+  const hipError_t e =
+      launch_kernel(k_head_logits<TN, HEAD_RAW>, grid, block, s, p, splits, part);
+  if (e != hipSuccess) return e;
+  const dim3 g2((unsigned)ceil_div(p.rows, 4), (unsigned)(2 * ceil_div(p.vocab, kTileA)));
+  const dim3 b2(kThreads);
+  switch (mode) {
+    case HEAD_STATS: return launch_kernel(k_head_slices<HEAD_STATS>, g2, b2, s, p, TN, splits, part);
+    case HEAD_EXP: return launch_kernel(k_head_slices<HEAD_EXP>, g2, b2, s, p, TN, splits, part);
+    case HEAD_DZ: return launch_kernel(k_head_slices<HEAD_DZ>, g2, b2, s, p, TN, splits, part);
+    default: return launch_kernel(k_head_slices<HEAD_POW>, g2, b2, s, p, TN, splits, part);
+  }
 }
 
 // Workgroups of dh, and tiles of its partial sums, that any number of rows up to
@@ -960,9 +1192,16 @@ hipError_t launch_head_pack(const HeadPackArgs& a, hipStream_t s) {
   return launch_kernel(k_head_pack, dim3((unsigned)groups), dim3(kThreads), s, a, per);
 }
 
-hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, hipStream_t s) {
-  return tile == 64 ? launch_logits<64>(p, mode, s)
-                    : tile == 128 ? launch_logits<128>(p, mode, s) : launch_logits<256>(p, mode, s);
+size_t head_logits_floats(int64_t rows, int dim, int64_t vocab, int tile) {
+  const int sp = logits_splits(rows, dim, vocab, tile);
+  return sp > 1 ? (size_t)sp * ceil_div(vocab, kTileA) * ceil_div(rows, tile) * tile * kTileA : 0;
+}
+
+hipError_t launch_head_logits(const HeadPanel& p, int tile, int mode, float* part, hipStream_t s) {
+  const int splits = logits_splits(p.rows, p.dim, p.vocab, tile);
+  return tile == 64    ? launch_logits<64>(p, mode, splits, part, s)
+         : tile == 128 ? launch_logits<128>(p, mode, splits, part, s)
+                       : launch_logits<256>(p, mode, splits, part, s);
 }
 
 hipError_t launch_head_join(const HeadPanel& p, int kind, int shift, double* lp, float* logp,
@@ -1006,10 +1245,24 @@ hipError_t launch_head_dh(const HeadPanel& p, int tile, int pow, float* part, ui
                        dim3(kThreads), s, p, tile, pow, part, dh, ldd);
 }
 
-hipError_t launch_head_dw(const HeadPanel& p, float* acc, int first, int last, uint16_t* dw,
-                          int64_t ldo, hipStream_t s) {
-  const dim3 grid(grid8(ceil_div(p.dim, kTileA) * ceil_div(p.vocab, 256)));
-  return launch_kernel(k_head_dw, grid, dim3(kGemmThreads), s, p, acc, first, last, dw, ldo);
+hipError_t launch_head_rest(const HeadPanel& p, float* rest, hipStream_t s) {
+  return launch_kernel(k_head_rest, dim3((unsigned)p.rows), dim3(kThreads), s, p, rest);
+}
+
+size_t head_dw_floats(int64_t rows, int dim, int64_t vocab) {
+  const int sp = dw_splits(rows, dim, vocab);
+  return sp > 1 ? (size_t)sp * ceil_div(dim, kTileA) * ceil_div(vocab, kTileA) * kTileA * kTileA : 0;
+}
+
+hipError_t launch_head_dw(const HeadPanel& p, const float* rest, float* part, float* acc, int first,
+                          int last, uint16_t* dw, int64_t ldo, hipStream_t s) {
+  const int splits = acc ? 1 : dw_splits(p.rows, p.dim, p.vocab);
+  const dim3 grid(grid8(ceil_div(p.dim, kTileA) * ceil_div(p.vocab, kTileA) * splits));
+  const hipError_t e = launch_kernel(k_head_dw, grid, dim3(kGemmThreads), s, p, rest, splits, part,
+                                     acc, first, last, dw, ldo);
+  if (e != hipSuccess || splits == 1) return e;
+  return launch_kernel(k_head_dw_sum, dim3((unsigned)ceil_div(p.vocab * p.dim / 8, kThreads)),
+                       dim3(kThreads), s, p, rest, splits, part, dw, ldo);
 }
 
 }  // namespace qnf4

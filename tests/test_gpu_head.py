@@ -91,6 +91,9 @@ SHAPES = [  # T, D, V, row padding
     (33, 1024, 1000, 0), (200, 512, 4099, 8), (256, 256, 256, 0), (257, 320, 513, 0),
     (700, 576, 2000, 0), (1, 4096, 32000, 0), (16, 1024, 32003, 0), (331, 1024, 5003, 0),
     (1500, 128, 777, 0), (2, 8192, 1003, 0), (40, 64, 128256, 0),
+    # few tiles: the inner index is cut
+    (38, 6848, 1652, 0), (71, 2880, 2662, 0), (2481, 1024, 700, 0), (9, 384, 12004, 0),
+    (300, 4096, 600, 8), (3000, 128, 300, 0), (1000, 2048, 130, 0), (130, 1024, 1, 0),
 ]
 
 
