@@ -828,21 +828,32 @@ def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_
     matrices = list(matrices)
     ns = _newton_schulz(what, coefficients, steps, eps)
     if out is None:
-        out = [torch.empty(m.shape, dtype=m.dtype, device=m.device) for m in matrices]
+        out = [torch.empty_like(m, memory_format=torch.contiguous_format) for m in matrices]
     out = list(out)
     _require(len(out) == len(matrices), what, "as many outputs as matrices")
     if not matrices:
         return out
-    arr = (OrthoMatrix * len(matrices))()
-    for a, m, o in zip(arr, matrices, out):
-        ld = _matrix(what, m, (torch.float32, torch.bfloat16), None, "each")
-        a.ld_in, a.ld_out = ld, _matrix(what, o, (m.dtype,), m.shape, "its output")
-        a.input, a.out, (a.rows, a.cols) = m.data_ptr(), o.data_ptr(), m.shape
-        a.dtype = QLORA_BF16 if m.dtype == torch.bfloat16 else QLORA_F32
-    dev = matrices[0].device
+    # qlora_ortho_matrix as seven int64 (a step of many small adapters is as long as
+    # this loop)
+    flat, shapes, code = [], [], {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+    for m, o in zip(matrices, out):
+        _require(m.dim() == 2 and m.dtype in code, what, "each must be a float32 or bf16 matrix")
+        (rows, cols), (ld, one), (ldo, oneo) = m.shape, m.stride(), o.stride()
+        _require((one == 1 or cols <= 1) and (oneo == 1 or cols <= 1), what,
+                 "each must have dense rows")
+        _require(o.dtype == m.dtype and o.shape == m.shape, what,
+                 "an output must be of its matrix's type and shape")
+        if rows <= 1:
+            ld = ldo = max(1, cols)
+        flat += (m.data_ptr(), o.data_ptr(), rows, cols, ld, ldo, code[m.dtype])
+        shapes.append((rows, cols))
     if ws is None:
-        ws = workspace(qlora_muon_workspace_bytes([m.shape for m in matrices]), dev)
-    with _on(what, matrices[0], ws, *matrices[1:], *out):
+        ws = workspace(qlora_muon_workspace_bytes(shapes), matrices[0].device)
+    with _on(what, matrices[0], ws):
+        d = ws.get_device()
+        _require(all(t.get_device() == d for t in matrices) and
+                 all(t.get_device() == d for t in out), what, "tensors on different devices")
+        arr = (ctypes.c_int64 * len(flat))(*flat)
         _check(lib().qlora_orthogonalize(ctypes.byref(ns), arr, len(matrices), _ptr(ws),
                                          ws.numel(), _stream()), what)
     return out

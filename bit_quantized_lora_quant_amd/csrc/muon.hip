@@ -254,10 +254,7 @@ __device__ __forceinline__ void gram(const MuonTensor& t, const View& v, const M
       if (t.m) load4(m[k], t.m + c.off(k, at, t.ldm), valid, vm);
     }
   };
-  Gram<NT> G;
-  G.init();
-  load(first);
-  for (int at = first; at < end; at += v.chunk) {
+  auto process = [&](int at, float* to) {
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
       if (t.m) {
@@ -267,11 +264,25 @@ __device__ __forceinline__ void gram(const MuonTensor& t, const View& v, const M
 #pragma unroll
         for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
       }
-      c.put(u, k, g[k]);
+      c.put(to, k, g[k]);
     }
-    __syncthreads();
-    if (at + v.chunk < end) load(at + v.chunk);   // in flight under the products
-    G.add(u, lane, wv);
+  };
+  Gram<NT> G;
+  G.init();
+  load(first);
+  process(first, u);
+  __syncthreads();
+  // a chunk's loads fly under the products of the one before, and no barrier stands
+  // between these and its momentum, so that waves are in different phases
+  int cur = 0;
+  for (int at = first; at < end; at += v.chunk) {
+    const bool more = at + v.chunk < end;
+    if (more) load(at + v.chunk);
+    G.add(u + cur, lane, wv);
+    if (more) {
+      cur = kBuf - cur;
+      process(at + v.chunk, u + cur);
+    }
     __syncthreads();
   }
   G.store(out, buf, lane, wv);
@@ -299,7 +310,8 @@ __global__ __launch_bounds__(kThreads) void k_muon_table(const MuonBatch bt, Muo
 template <int NT, bool TABLE>
 __global__ __launch_bounds__(kThreads, NT <= 2 ? 5 : NT == 4 ? 4 : 2)
 void k_muon_gram(const std::conditional_t<TABLE, int, MuonBatch> bt, MuonHyper h, MuonScratch s) {
-  __shared__ __attribute__((aligned(16))) float u[kBuf];
+  // (slices of a rank up to 32 are a single chunk)
+  __shared__ __attribute__((aligned(16))) float u[NT <= 2 ? kBuf : 2 * kBuf];
   __shared__ __attribute__((aligned(32))) double buf[NT <= 2 ? 3 * Gram<NT>::kTiles * 256 : 1];
   const int lane = threadIdx.x & 63, wg = blockIdx.x;
   MuonTensor t;
@@ -485,6 +497,134 @@ __global__ __launch_bounds__(64 * poly_waves(NT)) void k_muon_poly(MuonHyper h, 
     for (int v = 0; v < 4; ++v) out[(4 * i + v) * 64] = Q.t[i][v] * inv;
 }
 
+// Rank 33 to 64: all matrices fit LDS, so a product is taken by its tiles on and above
+// the diagonal alone (three, three, two and two a wave in place of four each) and
+// written to both sides, which also keeps every matrix exactly symmetric: operands are
+// read along rows, 512 bytes a read.  34 us in place of 43.  (The waves meet at
+// barriers in code of their own, the same number in each.)
+constexpr int kSide = 64, kPitch = kSide + 2;
+struct Tri {
+  int i, j;
+};
+template <int WV>
+struct Mine {
+  static constexpr Tri t[3] = {
+      WV == 0 ? Tri{0, 0} : WV == 1 ? Tri{1, 1} : WV == 2 ? Tri{2, 2} : Tri{3, 3},
+      WV == 0 ? Tri{0, 1} : WV == 1 ? Tri{1, 2} : WV == 2 ? Tri{2, 3} : Tri{0, 3},
+      WV == 0 ? Tri{0, 2} : Tri{1, 3}};
+  static constexpr int n = WV < 2 ? 3 : 2;
+};
+template <int WV>
+struct Tri3 {
+  using M = Mine<WV>;
+  f64x4_t c[3];
+  // a b, both symmetric and commuting
+  __device__ __forceinline__ void product(const double* a, const double* b, int lane) {
+    const int at = (lane >> 4) * kPitch + (lane & 15);
+#pragma unroll
+    for (int k = 0; k < M::n; ++k) c[k] = f64x4_t{0., 0., 0., 0.};
+#pragma unroll
+    for (int s = 0; s < kSide; s += 4)
+#pragma unroll
+      for (int k = 0; k < M::n; ++k)
+        c[k] = mfma64(a[at + s * kPitch + 16 * M::t[k].i], b[at + s * kPitch + 16 * M::t[k].j], c[k]);
+  }
+  __device__ __forceinline__ void put(double* x, int lane) const {
+#pragma unroll
+    for (int k = 0; k < M::n; ++k)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = 16 * M::t[k].i + 4 * v + (lane >> 4), q = 16 * M::t[k].j + (lane & 15);
+        x[r * kPitch + q] = c[k][v];
+        if (M::t[k].i != M::t[k].j) x[q * kPitch + r] = c[k][v];
+      }
+  }
+  // a + b g + c times what it holds
+  __device__ __forceinline__ void polynomial(const double* g, const MuonHyper& h, int lane) {
+#pragma unroll
+    for (int k = 0; k < M::n; ++k)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = 16 * M::t[k].i + 4 * v + (lane >> 4), q = 16 * M::t[k].j + (lane & 15);
+        c[k][v] = h.b * g[r * kPitch + q] + h.c * c[k][v];
+        if (r == q) c[k][v] += h.a;
+      }
+  }
+};
+template <int WV>
+__device__ __forceinline__ void poly64(const MuonHyper& h, double* g, double* p, double* u,
+                                       double* q, int lane) {
+  Tri3<WV> x, y;
+  for (int n = 0; n < h.steps; ++n) {
+    const bool last = n + 1 == h.steps;
+    x.product(g, g, lane);
+    x.polynomial(g, h, lane);
+    x.put(n == 0 ? q : p, lane);          // P; the first is Q as well
+    __syncthreads();
+    const double* pn = n == 0 ? q : p;
+    if (!last) {
+      x.product(pn, g, lane);
+      x.put(u, lane);                     // G P
+    }
+    if (n > 0) {
+      y.product(p, q, lane);
+      __syncthreads();
+      y.put(q, lane);                     // P Q
+    }
+    __syncthreads();
+    if (!last) {
+      x.product(pn, u, lane);
+      // (with n == 0 only: the next step writes P elsewhere, so Q stays)
+      x.put(g, lane);                     // P G P
+      __syncthreads();
+    }
+  }
+}
+__global__ __launch_bounds__(kThreads) void k_muon_poly64(MuonHyper h, MuonScratch s) {
+  __shared__ __attribute__((aligned(16))) double x[4][kSide * kPitch];
+  const MuonTensor t = s.t[blockIdx.x];
+  if (view(t).sp != kSide) return;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  double* g = x[0];
+  // (the slices' parts are summed by then)
+  const f64x4_t* from = reinterpret_cast<const f64x4_t*>(s.part + (size_t)t.part * 256) + lane;
+  int k = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = i; j < 4; ++j, ++k) {
+      if ((k & 3) != wv) continue;
+      const f64x4_t c = from[k * 64];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = 16 * i + 4 * v + (lane >> 4), q = 16 * j + (lane & 15);
+        g[r * kPitch + q] = c[v];
+        g[q * kPitch + r] = c[v];
+      }
+    }
+  __syncthreads();
+  double tr = g[lane * (kPitch + 1)];
+#pragma unroll
+  for (int d = 32; d; d >>= 1) tr += __shfl_xor(tr, d);
+  const double norm = fmax(sqrt(tr), h.eps), inv = 1.0 / norm;
+  // (fmax drops a NaN: then every product shows it)
+  __syncthreads();
+  for (int e = threadIdx.x; e < kSide * kSide; e += kThreads)
+    g[(e >> 6) * kPitch + (e & 63)] *= inv * inv;
+  __syncthreads();
+  switch (wv) {
+    case 0: poly64<0>(h, x[0], x[1], x[2], x[3], lane); break;
+    case 1: poly64<1>(h, x[0], x[1], x[2], x[3], lane); break;
+    case 2: poly64<2>(h, x[0], x[1], x[2], x[3], lane); break;
+    default: poly64<3>(h, x[0], x[1], x[2], x[3], lane); break;
+  }
+  // as k_muon_apply's left operands, a line a load (Q symmetric: its row tile wv)
+  double* out = s.q + (size_t)t.q * 256 + wv * 256 * 4 + lane;
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    out[e * 64] = x[3][(4 * e + (lane >> 4)) * kPitch + 16 * wv + (lane & 15)] * inv;
+}
+
 // --------------------------------------------------------------------- apply
 // O = Q U of one chunk: wave w takes row tiles and columns of it.  The chunk's loads are
 // in flight before those of Q; several workgroups a CU hide one another's phases.
@@ -585,9 +725,10 @@ __global__ __launch_bounds__(kThreads, 4) void k_muon_apply(MuonHyper h, MuonScr
 
 int muon_slice(int sp, int64_t total) {
   // A rank of 16 leaves 2 KB of parts a slice (a chunk moves 48 KB), one of 64 20 KB and
-  // of 128 72 KB: there as many chunks as leave 1536 workgroups, six a CU.
+  // of 128 72 KB: there as many chunks as leave 960 workgroups, about what runs at once
+  // (two 65B layers of rank 64: 176 us for the whole step, with 1536 of them 187).
   const int64_t most = sp <= 32 ? 1 : sp == 64 ? 8 : 16;
-  int64_t chunks = ceil_div(total, 1536 * 4096);
+  int64_t chunks = ceil_div(total, 960 * 4096);
   chunks = chunks < 1 ? 1 : chunks > most ? most : chunks;
   return (int)chunks * muon_chunk(sp);
 }
@@ -622,7 +763,7 @@ hipError_t launch_muon_poly(int count, int sp, const MuonHyper& h, const MuonScr
     case 32: return launch_kernel(k_muon_poly<2>, grid, dim3(64 * poly_waves(2)), st, h, s);
     case 64:
       e = launch_kernel(k_muon_sum<4>, dim3(10, (unsigned)count), dim3(kThreads), st, s);
-      return e != hipSuccess ? e : launch_kernel(k_muon_poly<4>, grid, dim3(64 * poly_waves(4)), st, h, s);
+      return e != hipSuccess ? e : launch_kernel(k_muon_poly64, grid, dim3(kThreads), st, h, s);
     default:
       e = launch_kernel(k_muon_sum<8>, dim3(36, (unsigned)count), dim3(kThreads), st, s);
       return e != hipSuccess ? e : launch_kernel(k_muon_poly<8>, grid, dim3(64 * poly_waves(8)), st, h, s);
