@@ -46,7 +46,8 @@ qlora_status check_head(const qlora_head* h) {
 
 // A gradient of `dim` columns and its row stride; NULL is not asked for.
 bool valid_grad(const qlora_head* h, const void* d, int64_t ld) {
-  return !d || (aligned(d, 16) && ld >= h->dim && ld % 8 == 0 && ld < kMaxLd);
+  return !d || (aligned(d, 16) && ld >= h->dim && ld % 8 == 0 && ld < kMaxLd &&
+                (d != h->hidden || ld == h->ld_hidden || h->rows < 2));
 }
 
 int64_t panel_rows(const qlora_head* h) {

@@ -90,6 +90,7 @@ __device__ __forceinline__ int dh_splits_wave(int64_t tiles, int64_t steps, int 
 __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t per) {
   __shared__ int wave_count[4];
   __shared__ int place[kThreads];
+  __shared__ double wave_sum[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int64_t first = blockIdx.x * per;
   const int64_t end = first + per < a.rows ? first + per : a.rows;
@@ -108,6 +109,8 @@ __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t 
       a.to.last[v] = -1;
   const float scale = a.w && a.w_scale ? a.w_scale[0] : 1.f;
   const int chunks = a.dim / 8;
+  // with one row a workgroup its four waves share the row's chunks
+  const int ways = per == 1 ? 4 : 1, from = ways == 4 ? tid : lane, stride = 64 * ways;
   for (int64_t t0 = first; t0 < end; t0 += kThreads) {
     const int64_t t = t0 + tid;
     const bool mine = t < end && has(t);
@@ -134,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t 
     }
     __syncthreads();
     const int n = end - t0 < kThreads ? (int)(end - t0) : kThreads;
-    for (int i = wv; i < n; i += 4) {
+    for (int i = ways == 4 ? 0 : wv; i < n; i += 4 / ways) {
       const int q = place[i];
       const uint4* in = reinterpret_cast<const uint4*>(a.hidden + (t0 + i) * a.ldh);
       if (q >= 0) {
@@ -142,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t 
         const int64_t y = a.labels[t0 + i];
         if (!a.weight || y >= a.vocab) {
 #pragma unroll 4
-          for (int k = lane; k < chunks; k += 64) out[k] = in[k];
+          for (int k = from; k < chunks; k += stride) out[k] = in[k];
           continue;
         }
         // the target's logit, in float64: logp and 1 - p of a likely target hang on its
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t 
         const uint4* with = reinterpret_cast<const uint4*>(a.weight + y * a.ldw);
         double z = 0;
 #pragma unroll 4
-        for (int k = lane; k < chunks; k += 64) {
+        for (int k = from; k < chunks; k += stride) {
           const uint4 x = in[k], w = with[k];
           out[k] = x;
 #pragma unroll
@@ -163,10 +166,15 @@ __global__ __launch_bounds__(kThreads) void k_head_pack(HeadPackArgs a, int64_t 
         }
 #pragma unroll
         for (int d = 32; d; d >>= 1) z += __shfl_xor(z, d);
-        if (lane == 0) a.to.zy[q] = z;
+        if (ways == 4) {
+          if (lane == 0) wave_sum[wv] = z;
+          __syncthreads();
+          z = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+        }
+        if (lane == 0 && (ways == 1 || wv == 0)) a.to.zy[q] = z;
       } else if (a.dh) {
         uint4* out = reinterpret_cast<uint4*>(a.dh + (t0 + i) * a.ldd);
-        for (int k = lane; k < chunks; k += 64) out[k] = make_uint4(0u, 0u, 0u, 0u);
+        for (int k = from; k < chunks; k += stride) out[k] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
     at += wave_count[0] + wave_count[1] + wave_count[2] + wave_count[3];
@@ -694,9 +702,20 @@ void k_head_join(HeadPanel p, int kind, int shift, double* lp, float* logp, Head
   const int64_t slices = 2 * ceil_div(p.vocab, kTileA);
   const HeadPart* part = p.part + rr;
   const int first = 4 * wv + (lane >> 4);
+  // (a thread's first 16 slices stay in registers: a vocabulary of 131072)
+  constexpr int kHeld = 16, kStride = 4 * kJoinWaves;
+  HeadPart held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int64_t sl = first + k * kStride;
+    held[k] = sl < slices ? part[sl * p.rows] : HeadPart{-INFINITY, 0.f};
+  }
   float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) m = fmaxf(m, held[k].m);
 #pragma unroll 8
-  for (int64_t k = first; k < slices; k += 4 * kJoinWaves) m = fmaxf(m, part[k * p.rows].m);
+  for (int64_t k = first + kHeld * kStride; k < slices; k += kStride)
+    m = fmaxf(m, part[k * p.rows].m);
   m = fmaxf(m, __shfl_xor(m, 16));
   m = fmaxf(m, __shfl_xor(m, 32));
   if (lane < 16) ms[wv][r] = m;
@@ -708,16 +727,19 @@ void k_head_join(HeadPanel p, int kind, int shift, double* lp, float* logp, Head
   for (int k = 1; k < kJoinWaves; ++k) m = fmaxf(m, ms[k][r]);
   // sums relative to 2^m: every factor is a power of two
   double s = 0;
-#pragma unroll 8
-  for (int64_t k = first; k < slices; k += 4 * kJoinWaves) {
-    const HeadPart e = part[k * p.rows];
-    const int down = (int)fmaxf(e.m - m, -2000.f);   // (0 for a NaN: the sum shows it)
+  auto add = [&](const HeadPart& e, int64_t k) {
+    const int down = (int)fmaxf(e.m - m, -2000.f);   // (-2000 for a NaN: the sum shows it)
     s += ldexp((double)e.s, down);
     if (shift && row < n) {
       const uint32_t d = down < -511 ? 511 : -down;
       p.shift[k * p.rows + row] = e.s == 0.f ? 0u : d << 7 | d << 23;
     }
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (first + k * kStride < slices) add(held[k], first + k * kStride);
+#pragma unroll 8
+  for (int64_t k = first + kHeld * kStride; k < slices; k += kStride) add(part[k * p.rows], k);
   s += __shfl_xor(s, 16);
   s += __shfl_xor(s, 32);
   if (lane < 16) ss[wv][r] = s;
@@ -1168,15 +1190,18 @@ int head_dh_splits(int64_t rows, int dim, int64_t vocab, int tile) {
 int head_tile(int64_t rows, int64_t vocab) {
   // The least time of the logits' rounds: a round of 256 workgroups takes about 45, 65
   // and 118 us at 4096 inner indices with tiles of 64, 128 and 256 rows.  (331 rows
-  // of a vocabulary of 128256: 555, 393 and 474 us; 512 rows: 698, 510 and 476; 96
-  // rows of 32000 at 1024: 25, 26 and 34.)
+  // of a vocabulary of 128256: 555, 393 and 474 us; 700 rows: 1162, 726 and 663; 96
+  // rows of 32000 at 1024: 25, 26 and 34.)  How many rows have a target only the GPU
+  // knows: the mean over all of them and five in eight.
   const int unit[3] = {45, 65, 118};
+  const int64_t all = rows > 0 ? rows : 1, some = ceil_div(5 * all, 8);
   int best = 64;
   int64_t least = -1;
   for (int i = 0; i < 3; ++i) {
     const int tile = 64 << i;
-    const int64_t cost =
-        ceil_div(ceil_div(rows > 0 ? rows : 1, tile) * ceil_div(vocab, kTileA), 256) * unit[i];
+    const int64_t nv = ceil_div(vocab, kTileA);
+    const int64_t cost = unit[i] * (ceil_div(ceil_div(all, tile) * nv, 256) +
+                                    ceil_div(ceil_div(some, tile) * nv, 256));
     if (least < 0 || cost < least) {
       least = cost;
       best = tile;
@@ -1241,7 +1266,10 @@ hipError_t launch_head_dh(const HeadPanel& p, int tile, int pow, float* part, ui
   const hipError_t e = pow ? launch_dh<true>(p, tile, grid, part, dh, ldd, s)
                            : launch_dh<false>(p, tile, grid, part, dh, ldd, s);
   if (e != hipSuccess || d.slots == 0) return e;
-  return launch_kernel(k_head_dh_sum, dim3((unsigned)ceil_div((int64_t)p.rows * p.dim / 8, 64)),
+  // (rows of more tiles than kMaxSlots are not cut)
+  const int64_t most = kMaxSlots / ceil_div(p.dim, kTileA) * tile;
+  const int64_t rows = p.rows < most ? p.rows : most;
+  return launch_kernel(k_head_dh_sum, dim3((unsigned)ceil_div(rows * p.dim / 8, 64)),
                        dim3(kThreads), s, p, tile, pow, part, dh, ldd);
 }
 

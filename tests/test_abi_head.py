@@ -70,6 +70,9 @@ def test_refusals():
                dict(logp=FAKE + 1), dict(dh=FAKE + 4), dict(dh=FAKE, ldd=129),
                dict(dw=FAKE, ldo=1 << 22)):
         assert _ce(h, **kw) == bad, kw
+    # in place needs the same stride
+    assert _back(_h(ldh=136), dh=FAKE, ldd=128) == bad
+    assert _ce(_h(ldh=136), dh=FAKE, ldd=144) == bad
     none = _h(rows=0, hidden=0, labels=0)
     assert _score(none, logp=None, ws=None) == q.QLORA_OK
     assert _back(none, stats=None, w=None, dh=None, ws=None) == q.QLORA_OK
