@@ -6,20 +6,30 @@
 //
 // Rows with a target are packed first, so prompts and padding cost nothing and
 // whatever they hold reaches no sum.  The packed rows go through in panels of at
-// most 2^29 row x vocabulary elements: the product's tiles leave a maximum and a
-// sum per row and 128 vocabulary entries and, where a gradient follows in the
-// same call, exp(z - m) of the slice in fp16 (11 bits below the slice's own
-// maximum; the next kernel rounds dz to bf16, the matrix cores' type, once).  The
-// target is left out of its slice: its exponential is kept apart, so that
-// 1 - p of a nearly certain target is a sum of what is left and not 1 minus
-// something rounded.
+// most 2^29 row x vocabulary elements.  The product's tiles leave, per row and slice
+// of 128 vocabulary entries, a whole exponent M = ceil(max z log2 e) and the sum of
+// 2^(z log2 e - M).  The target is left out of its slice: its logit is a float64 dot
+// product of the packing, and 1 - p of a nearly certain target is a sum of what is
+// left, not 1 minus something rounded.  The slices are joined in float64, by powers
+// of two only.
 //
-// All three products share one tile loop, bound by the matrix cores: 256 values of
-// the output's contiguous index (MFMA rows: a lane then holds eight
+// A gradient in the same call has the slices' values written in 16 bits.  dh alone
+// takes them as bf16, the matrix cores' type: its tile loop lowers their exponents
+// by R - M to the row's R, and the row's factor and its target's term come in float32
+// at the end, so they are written once and read once.  With dW they are fp16 (11 bits
+// below the slice's largest) and become dz = bf16 in place, which both products
+// read.  Either way a value is rounded to bf16 once.  A backward call from stored
+// statistics multiplies the logits again and writes dz at once.
+//
+// All three products share one tile loop, bound by the matrix cores' power: 256
+// values of the output's contiguous index (MFMA rows: a lane then holds eight
 // neighbours of one output row, a 16-byte store) x 64 to 256 of its rows, 64 inner
-// indices a step, eight waves of 128 x a quarter of the rows.  Accumulators stay in AGPRs;
-// both tiles stream into LDS by DMA, and operands are read half a step ahead.  Operands whose inner index is not
-// contiguous (W in dh, both in dW) are transposed by the LDS reads themselves.
+// indices a step.  Accumulators stay in AGPRs, both tiles stream into LDS by DMA and
+// operands are read half a step ahead.  Operands whose inner index is not contiguous
+// (W in dh, both in dW) are transposed by the LDS reads themselves.  At V = 128256,
+// D = 4096 the logits of 2048 rows take 1.4 to 1.65 ms (1300 to 1540 TF, by the card;
+// the card's largest library products reach 1240 to 1390) and 4096 rows' loss and dh
+// 5.1 ms.
 #include "head.h"
 
 #include <type_traits>
@@ -28,7 +38,6 @@ namespace qnf4 {
 namespace {
 
 constexpr int kThreads = 256;           // of the streaming kernels
-constexpr int kWavesB = 4, kWaves = 2 * kWavesB, kGemmThreads = 64 * kWaves;
 constexpr int kStep = 64;               // inner indices per step
 constexpr int kTileA = 256;             // values of the output's contiguous index
 constexpr int kMaxSlots = 1024;         // partial tiles of dh
@@ -249,10 +258,10 @@ struct Operand {
 // c ^ hash(k).  The hashes spread what the lanes of a read use together over all 64
 // banks: A's MFMA row 4 q + v of tile (i, h) is index 32 i + 8 q + 4 h + v (so that
 // a lane's results of h = 0, 1 are neighbours), B's is in order.
-template <int R, bool TR, bool IS_A>
+template <int R, bool TR, bool IS_A, int WAVES>
 struct Tile {
   static constexpr int kBytes = R * kStep * 2;
-  static constexpr int kLoads = kBytes / 1024 / kWaves;     // per wave and step
+  static constexpr int kLoads = kBytes / 1024 / WAVES;     // per wave and step
   static constexpr int kRowChunks = TR ? R / 8 : 8;
   uint32_t off[kLoads];
   uint32_t krow[TR ? kLoads : 1];
@@ -339,33 +348,47 @@ struct Shift {
   int64_t ld;
 };
 
-template <int TN, bool SHIFT = false>
+// TN rows of B, WB waves along them (and two along A).
+template <int TN, int WB, bool SHIFT = false>
 struct Shape {
-  static constexpr int kStages = TN == 256 ? 2 : 3;
-  static constexpr int kTilesB = TN / 16 / kWavesB;   // MFMA tiles of a wave
-  static constexpr int kTileBytes = (kTileA + TN) * kStep * 2;
-  static constexpr int kStageBytes = kTileBytes + (SHIFT ? TN * 4 : 0);
-  static constexpr int kLds = kStages * kStageBytes;
+  static constexpr int kWaves = 2 * WB;
+  static constexpr int kTilesB = TN / 16 / WB;     // MFMA tiles of a wave
+  // 256 rows: A in three buffers and B in two fill LDS (the words of SHIFT leave A two)
+  static constexpr bool kA3 = TN == 256 && !SHIFT;
+  static constexpr int kStages = TN == 256 ? 2 : 3;        // of B
+  static constexpr int kStagesA = kA3 ? 3 : kStages;
+  static constexpr int kA = kTileA * kStep * 2, kB = TN * kStep * 2, kWords = SHIFT ? TN * 4 : 0;
+  // a step's A, B and words side by side, or A's buffers and then B's
+  static constexpr int kStage = kA + kB + kWords;
+  static constexpr uint32_t kNextA = kA3 ? kA : kStage, kNextB = kA3 ? kB : kStage;
+  static constexpr uint32_t kEndA = kStagesA * kNextA, kEndB = kStages * kNextB;
+  static constexpr int kAtB = kA3 ? kEndA : kA, kAtWords = kAtB + kB;
+  static constexpr int kLds = kA3 ? kEndA + kEndB : kEndB;
 };
 
 // acc[ta][tb] += A . B^T over steps [s0, s1) (s0 < s1).  Wave (wm, wn): A's values
-// 128 wm .. and B's rows TN / 4 wn ...  While a half step is multiplied from
+// 128 wm .. and B's rows TN / WB wn ...  While a half step is multiplied from
 // registers, the next half's operands are read.  One barrier a step, in its
-// middle: by then every wave has read the step's second half, so its stage takes the
-// DMA of step k + stages, and step k + 1's tiles have landed (an exact vmcnt: every
-// wave issues the same loads each step, past the end the last step's again).  The
-// loads are spread over the half step: their path takes 64 bytes a cycle, and a burst
-// of them holds up the wave (in a quarter of the step, 7% slower).
-template <int TN, bool ATR, bool BTR, bool SHIFT = false>
-__device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], char* lds,
+// middle: by then every wave has read the step's second half, so its buffers are
+// free, and step k + 1's tiles have landed (an exact vmcnt: every wave issues the
+// same loads each step, past the end the last step's again).
+//
+// The loads' path takes 64 bytes a cycle, half of a step's time at 256 rows, and what
+// comes faster holds up the wave: bunched in a quarter of the step the products ran
+// 7% slower than over half of it.  So A has a third buffer where LDS has room: its
+// tile of step k + 2 goes there in the first half of step k, B's in the second
+// half, to the buffer that step k leaves (V = 128256, D = 4096: 2048 rows' loss, dh and
+// dW 5550 -> 5385 us; logits of 2048 rows at V = 32000, D = 8192: 849 -> 825).
+template <int TN, int WB, bool ATR, bool BTR, bool SHIFT = false>
+__device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / WB], char* lds,
                                           const Operand& A, int64_t a0, const Operand& B,
                                           int64_t b0, int64_t s0, int64_t s1,
                                           const Shift& sh = Shift{nullptr, 0}) {
-  using S = Shape<TN, SHIFT>;
-  using TA = Tile<kTileA, ATR, true>;
-  using TB = Tile<TN, BTR, false>;
+  using S = Shape<TN, WB, SHIFT>;
+  using TA = Tile<kTileA, ATR, true, S::kWaves>;
+  using TB = Tile<TN, BTR, false, S::kWaves>;
   constexpr int NB = S::kTilesB, NS = S::kStages;
-  constexpr int kDma = TA::kLoads + TB::kLoads + SHIFT;
+  constexpr int LA = TA::kLoads, LB = TB::kLoads + SHIFT;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 1, wn = wv >> 1;
@@ -387,37 +410,45 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], 
     }
   mfma_settle();
 
-  auto load = [&](int q, int64_t step, uint32_t stage) __attribute__((always_inline)) {
-    const int64_t k0 = (step < s1 ? step : s1 - 1) * kStep;
-    if (q < TA::kLoads) ta.load(q, k0, lds0 + stage, wv);
-    else if (q < TA::kLoads + TB::kLoads)
-      tb.load(q - TA::kLoads, k0, lds0 + stage + TA::kBytes, wv);
-    else   // (with fewer than 512 rows several waves fetch the same words)
-      dma4_at(sh.p + k0 / 128 * sh.ld + b0 + 64 * (wv % (TN / 64)), 4 * lane,
-              lds0 + stage + S::kTileBytes + 256 * (wv % (TN / 64)));
+  // buffers by where they are behind the first: A's, B's (and its words')
+  auto inner = [&](int64_t step) __attribute__((always_inline)) {
+    return (step < s1 ? step : s1 - 1) * kStep;
+  };
+  auto load_a = [&](int q, int64_t step, uint32_t buf) __attribute__((always_inline)) {
+    ta.load(q, inner(step), lds0 + buf, wv);
+  };
+  auto load_b = [&](int q, int64_t step, uint32_t buf) __attribute__((always_inline)) {
+    if (q < TB::kLoads) tb.load(q, inner(step), lds0 + S::kAtB + buf, wv);
+    else   // (several waves fetch the same words where there are more waves than those)
+      dma4_at(sh.p + inner(step) / 128 * sh.ld + b0 + 64 * (wv % (TN / 64)), 4 * lane,
+              lds0 + S::kAtWords + buf + 256 * (wv % (TN / 64)));
   };
 #pragma unroll
-  for (int st = 0; st < NS; ++st)
+  for (int st = 0; st < NS; ++st) {
 #pragma unroll
-    for (int q = 0; q < kDma; ++q) load(q, s0 + st, st * S::kStageBytes);
-  wait_vmem<(NS - 1) * kDma>();
+    for (int q = 0; q < LA; ++q) load_a(q, s0 + st, st * S::kNextA);
+#pragma unroll
+    for (int q = 0; q < LB; ++q) load_b(q, s0 + st, st * S::kNextB);
+  }
+  wait_vmem<(NS - 1) * (LA + LB)>();
   __syncthreads();
 
   u32x4_t fa[2][8], fb[2][NB];
-  auto fetch = [&](int r, const char* stage, int s) __attribute__((always_inline)) {
-    if (r < 8) fa[s][r] = TA::read(stage, ab, r, s);    // operand r of half s
-    else fb[s][r - 8] = TB::read(stage + TA::kBytes, bb, r - 8, s);
+  // operand r of half s
+  auto fetch = [&](int r, uint32_t ba, uint32_t bb0, int s) __attribute__((always_inline)) {
+    if (r < 8) fa[s][r] = TA::read(lds + ba, ab, r, s);
+    else fb[s][r - 8] = TB::read(lds + S::kAtB + bb0, bb, r - 8, s);
   };
 #pragma unroll
-  for (int r = 0; r < 8 + NB; ++r) fetch(r, lds, 0);
+  for (int r = 0; r < 8 + NB; ++r) fetch(r, 0, 0, 0);
 
   // The exponents of bf16 values by whole numbers: exact, and 0 where one would leave the
   // range.  A tile's words are changed at least two instructions before the first
   // product that reads them (which the compiler does not see inside the asm).
   uint32_t sv[NB];
-  auto words = [&](int t, const char* stage) __attribute__((always_inline)) {
+  auto words = [&](int t, uint32_t buf) __attribute__((always_inline)) {
     if constexpr (SHIFT)
-      sv[t] = *reinterpret_cast<const uint32_t*>(stage + S::kTileBytes +
+      sv[t] = *reinterpret_cast<const uint32_t*>(lds + S::kAtWords + buf +
                                                  4 * (16 * (NB * wn + t) + (lane & 15)));
   };
   auto lower = [&](int t, int s) __attribute__((always_inline)) {
@@ -430,41 +461,55 @@ __device__ __forceinline__ void tile_loop(f32x4_t (&acc)[8][TN / 16 / kWavesB], 
     }
   };
 #pragma unroll
-  for (int t = 0; t < NB; ++t) words(t, lds);
+  for (int t = 0; t < NB; ++t) words(t, 0);
   lower(0, 0);
 
   constexpr int M = 8 * NB, R = 8 + NB, RM = M * 3 / 4;
-  uint32_t cur = 0;
+  // loads of the second half: B's, and A's where it has no buffer of its own
+  constexpr int L1 = S::kA3 ? LB : LA + LB;
+  uint32_t ca = 0, cb3 = 0;                       // this step's buffers
   for (int64_t k = s0; k < s1; ++k) {
+    const uint32_t cb = S::kA3 ? cb3 : ca;
+    auto after = [](uint32_t at, uint32_t next, uint32_t end) __attribute__((always_inline)) {
+      return at + next == end ? 0u : at + next;
+    };
+    const uint32_t na = after(ca, S::kNextA, S::kEndA);
+    const uint32_t nb = S::kA3 ? after(cb, S::kNextB, S::kEndB) : na;
+    const uint32_t free_a = S::kA3 ? after(na, S::kNextA, S::kEndA) : ca;
     if constexpr (SHIFT) asm volatile("s_nop 1");
-    const uint32_t nxt = cur + S::kStageBytes < S::kLds ? cur + S::kStageBytes : 0;
     static_for<0, M>([&](auto c) __attribute__((always_inline)) {
       constexpr int i = c;
       mfma_acc(acc[i & 7][i >> 3], fa[0][i & 7], fb[0][i >> 3]);
       __builtin_amdgcn_sched_barrier(0);
+      if constexpr (S::kA3)
+        static_for<i * LA / M, (i + 1) * LA / M>(
+            [&](auto q) __attribute__((always_inline)) { load_a(q, k + 2, free_a); });
       static_for<min_of(i * R / RM, R), min_of((i + 1) * R / RM, R)>(
-          [&](auto r) __attribute__((always_inline)) { fetch(r, lds + cur, 1); });
+          [&](auto r) __attribute__((always_inline)) { fetch(r, ca, cb, 1); });
       if constexpr (i % 8 == 4 && i / 8 + 1 < NB) lower(i / 8 + 1, 0);
       if constexpr (i == M - 1) lower(0, 1);
       __builtin_amdgcn_sched_barrier(0);
     });
-    wait_vmem<(NS - 2) * kDma>();
+    wait_vmem<S::kA3 ? LA : (NS - 2) * (LA + LB)>();
     __syncthreads();
     static_for<0, M>([&](auto c) __attribute__((always_inline)) {
       constexpr int i = c;
       mfma_acc(acc[i & 7][i >> 3], fa[1][i & 7], fb[1][i >> 3]);
       __builtin_amdgcn_sched_barrier(0);
-      static_for<i * kDma / M, (i + 1) * kDma / M>(
-          [&](auto q) __attribute__((always_inline)) { load(q, k + NS, cur); });
+      static_for<i * L1 / M, (i + 1) * L1 / M>([&](auto q) __attribute__((always_inline)) {
+        if constexpr (q < L1 - LB) load_a(q, k + NS, free_a);
+        else load_b(q - (L1 - LB), k + NS, cb);
+      });
       static_for<min_of(i * R / RM, R), min_of((i + 1) * R / RM, R)>(
-          [&](auto r) __attribute__((always_inline)) { fetch(r, lds + nxt, 0); });
+          [&](auto r) __attribute__((always_inline)) { fetch(r, na, nb, 0); });
       if constexpr (i % 8 == 4 && i / 8 + 1 < NB) lower(i / 8 + 1, 1);
       // (the last tile's words are used by then)
-      if constexpr (i >= RM && i < RM + NB) words(i - RM, lds + nxt);
+      if constexpr (i >= RM && i < RM + NB) words(i - RM, nb);
       if constexpr (i == M - 1) lower(0, 0);
       __builtin_amdgcn_sched_barrier(0);
     });
-    cur = nxt;
+    ca = na;
+    cb3 = nb;
   }
   wait_vmem<0>();   // nothing left in flight into LDS at exit
   mfma_settle();
@@ -504,12 +549,22 @@ __device__ __forceinline__ int panel_splits(const HeadPanel& p, int n) {
 // A = W (the vocabulary along a lane's registers: a row's statistics are sums in the
 // lane, then over the four lanes of its column), B = rows.
 constexpr int HEAD_RAW = 4;    // partial logits of a slice of the inner index
-template <int TN, int MODE>
-__global__ __attribute__((amdgpu_flat_work_group_size(kGemmThreads, kGemmThreads),
-                          amdgpu_waves_per_eu(kWaves / 4, kWaves / 4)))
+// Waves along the rows.  Of 256 rows, two of 128 each read half as much from LDS as
+// four of 64 do, for one wave a SIMD: 2048 rows at D = 8192, V = 32000 take 813 us for
+// 825.  Where powers for dh are written the wave's epilogue costs more than that (4096
+// rows at V = 128256, D = 4096, loss and dh: 6835 us for 6789), and the products that
+// transpose lose as well (2048 rows' loss, dh and dW: 5650 with two waves in dh and
+// 5861 with two in dW, for 5561).
+constexpr int kWavesB = 4;
+constexpr int logits_waves(int tn, int mode) {
+  return tn == 256 && mode != HEAD_POW ? 2 : kWavesB;
+}
+template <int TN, int MODE, int WB>
+__global__ __attribute__((amdgpu_flat_work_group_size(128 * WB, 128 * WB),
+                          amdgpu_waves_per_eu(WB / 2, WB / 2)))
 void k_head_logits(HeadPanel p, int splits, float* part) {
-  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
-  constexpr int NB = Shape<TN>::kTilesB;
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN, WB>::kLds];
+  constexpr int NB = Shape<TN, WB>::kTilesB;
   const int n = panel_rows(p);
   const int64_t na = ceil_div(p.vocab, kTileA), nb = ceil_div(n, TN);
   int64_t tv, tt;
@@ -520,8 +575,8 @@ void k_head_logits(HeadPanel p, int splits, float* part) {
   const Operand B{p.r.h + p.row0 * p.dim, p.dim, n, p.dim};
   f32x4_t acc[8][NB];
   // (no slice is empty: logits_splits)
-  tile_loop<TN, false, false>(acc, lds, A, tv * kTileA, B, tt * TN, sl * each,
-                              (sl + 1) * each < steps ? (sl + 1) * each : steps);
+  tile_loop<TN, WB, false, false>(acc, lds, A, tv * kTileA, B, tt * TN, sl * each,
+                                  (sl + 1) * each < steps ? (sl + 1) * each : steps);
 
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -868,11 +923,11 @@ __device__ __forceinline__ void finish_row(const HeadPanel& p, bool pow, int64_t
 }
 
 template <int TN, bool POW>
-__global__ __attribute__((amdgpu_flat_work_group_size(kGemmThreads, kGemmThreads),
-                          amdgpu_waves_per_eu(kWaves / 4, kWaves / 4)))
+__global__ __attribute__((amdgpu_flat_work_group_size(128 * kWavesB, 128 * kWavesB),
+                          amdgpu_waves_per_eu(kWavesB / 2, kWavesB / 2)))
 void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
-  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN, POW>::kLds];
-  constexpr int NB = Shape<TN>::kTilesB;
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN, kWavesB, POW>::kLds];
+  constexpr int NB = Shape<TN, kWavesB>::kTilesB;
   const int n = panel_rows(p), splits = panel_splits(p, n);
   const int64_t na = ceil_div(p.dim, kTileA), nb = ceil_div(n, TN);
   int64_t td, tt;
@@ -885,8 +940,9 @@ void k_head_dh(HeadPanel p, float* part, uint16_t* dh, int64_t ldd) {
   const Operand B{p.e, cols, n, cols};
   f32x4_t acc[8][NB];
   // (a cut that leaves the last slice empty is left out by the rows above: each >= 1)
-  tile_loop<TN, true, false, POW>(acc, lds, A, td * kTileA, B, tt * TN,
-                                  s0 < steps ? s0 : steps - 1, s1, Shift{p.shift, p.rows});
+  tile_loop<TN, kWavesB, true, false, POW>(acc, lds, A, td * kTileA, B, tt * TN,
+                                           s0 < steps ? s0 : steps - 1, s1,
+                                           Shift{p.shift, p.rows});
 
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1013,12 +1069,12 @@ __global__ __launch_bounds__(kThreads) void k_head_rest(HeadPanel p, float* rest
 }
 
 // A = h (transposed by the reads), B = dz (likewise); inner index the rows.
-__global__ __attribute__((amdgpu_flat_work_group_size(kGemmThreads, kGemmThreads),
-                          amdgpu_waves_per_eu(kWaves / 4, kWaves / 4)))
+__global__ __attribute__((amdgpu_flat_work_group_size(128 * kWavesB, 128 * kWavesB),
+                          amdgpu_waves_per_eu(kWavesB / 2, kWavesB / 2)))
 void k_head_dw(HeadPanel p, const float* rest, int splits, float* part, float* sum, int first,
                int last, uint16_t* dw, int64_t ldo) {
-  constexpr int TN = 256, NB = Shape<TN>::kTilesB;
-  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN>::kLds];
+  constexpr int TN = 256, NB = Shape<TN, kWavesB>::kTilesB;
+  __shared__ __attribute__((aligned(1024))) char lds[Shape<TN, kWavesB>::kLds];
   const int n = panel_rows(p);
   const int64_t na = ceil_div(p.dim, kTileA), nb = ceil_div(p.vocab, TN);
   int64_t td, tv;
@@ -1032,7 +1088,7 @@ void k_head_dw(HeadPanel p, const float* rest, int splits, float* part, float* s
   const Operand B{p.e, cols, cols, steps * kStep};
   f32x4_t acc[8][NB];
   if (steps > 0) {
-    tile_loop<TN, true, true>(acc, lds, A, td * kTileA, B, tv * TN, s0, s1);
+    tile_loop<TN, kWavesB, true, true>(acc, lds, A, td * kTileA, B, tv * TN, s0, s1);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -1140,19 +1196,23 @@ int dw_splits(int64_t rows, int dim, int64_t vocab) {
 
 unsigned grid8(int64_t tiles) { return (unsigned)(ceil_div(tiles, 8) * 8); }
 
+template <int TN, int MODE>
+hipError_t start_logits(const HeadPanel& p, dim3 grid, int splits, float* part, hipStream_t s) {
+  constexpr int WB = logits_waves(TN, MODE);
+  return launch_kernel(k_head_logits<TN, MODE, WB>, grid, dim3(128 * WB), s, p, splits, part);
+}
+
 template <int TN>
 hipError_t launch_logits(const HeadPanel& p, int mode, int splits, float* part, hipStream_t s) {
   const dim3 grid(grid8(ceil_div(p.vocab, kTileA) * ceil_div(p.rows, TN) * splits));
-  const dim3 block(kGemmThreads);
   switch (splits > 1 ? HEAD_RAW : mode) {
-    case HEAD_STATS: return launch_kernel(k_head_logits<TN, HEAD_STATS>, grid, block, s, p, 1, part);
-    case HEAD_EXP: return launch_kernel(k_head_logits<TN, HEAD_EXP>, grid, block, s, p, 1, part);
-    case HEAD_DZ: return launch_kernel(k_head_logits<TN, HEAD_DZ>, grid, block, s, p, 1, part);
-    case HEAD_POW: return launch_kernel(k_head_logits<TN, HEAD_POW>, grid, block, s, p, 1, part);
+    case HEAD_STATS: return start_logits<TN, HEAD_STATS>(p, grid, 1, part, s);
+    case HEAD_EXP: return start_logits<TN, HEAD_EXP>(p, grid, 1, part, s);
+    case HEAD_DZ: return start_logits<TN, HEAD_DZ>(p, grid, 1, part, s);
+    case HEAD_POW: return start_logits<TN, HEAD_POW>(p, grid, 1, part, s);
     default: break;
   }
-  const hipError_t e =
-      launch_kernel(k_head_logits<TN, HEAD_RAW>, grid, block, s, p, splits, part);
+  const hipError_t e = start_logits<TN, HEAD_RAW>(p, grid, splits, part, s);
   if (e != hipSuccess) return e;
   const dim3 g2((unsigned)ceil_div(p.rows, 4), (unsigned)(2 * ceil_div(p.vocab, kTileA)));
   const dim3 b2(kThreads);
@@ -1254,7 +1314,7 @@ size_t head_dh_floats(int64_t rows, int dim, int64_t vocab, int tile) {
 template <bool POW>
 hipError_t launch_dh(const HeadPanel& p, int tile, dim3 grid, float* part, uint16_t* dh,
                      int64_t ldd, hipStream_t s) {
-  const dim3 block(kGemmThreads);
+  const dim3 block(128 * kWavesB);
   return tile == 64    ? launch_kernel(k_head_dh<64, POW>, grid, block, s, p, part, dh, ldd)
          : tile == 128 ? launch_kernel(k_head_dh<128, POW>, grid, block, s, p, part, dh, ldd)
                        : launch_kernel(k_head_dh<256, POW>, grid, block, s, p, part, dh, ldd);
@@ -1286,8 +1346,8 @@ hipError_t launch_head_dw(const HeadPanel& p, const float* rest, float* part, fl
                           int last, uint16_t* dw, int64_t ldo, hipStream_t s) {
   const int splits = acc ? 1 : dw_splits(p.rows, p.dim, p.vocab);
   const dim3 grid(grid8(ceil_div(p.dim, kTileA) * ceil_div(p.vocab, kTileA) * splits));
-  const hipError_t e = launch_kernel(k_head_dw, grid, dim3(kGemmThreads), s, p, rest, splits, part,
-                                     acc, first, last, dw, ldo);
+  const hipError_t e = launch_kernel(k_head_dw, grid, dim3(128 * kWavesB), s, p, rest, splits,
+                                     part, acc, first, last, dw, ldo);
   if (e != hipSuccess || splits == 1) return e;
   return launch_kernel(k_head_dw_sum, dim3((unsigned)ceil_div(p.vocab * p.dim / 8, kThreads)),
                        dim3(kThreads), s, p, rest, splits, part, dw, ldo);
