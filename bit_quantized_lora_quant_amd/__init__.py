@@ -819,6 +819,12 @@ def _newton_schulz(what, coefficients, steps, eps):
     return NewtonSchulz(*coefficients, eps, steps, 0)
 
 
+def _distinct(what, name, tensors):
+    """No two of the tensors begin at one place: workgroups of both would write it."""
+    at = [t.data_ptr() for t in tensors if t.numel()]
+    _require(len(set(at)) == len(at), what, "%s is given twice", name)
+
+
 def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_SCHULZ,
                         eps: float = 1e-7, ws=None):
     """Each float32 or bf16 matrix (shorter side <= 128, rows of any stride) moved
@@ -847,6 +853,7 @@ def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_
             ld = ldo = max(1, cols)
         flat += (m.data_ptr(), o.data_ptr(), rows, cols, ld, ldo, code[m.dtype])
         shapes.append((rows, cols))
+    _distinct(what, "an output", out)
     if ws is None:
         ws = workspace(qlora_muon_workspace_bytes(shapes), matrices[0].device)
     with _on(what, matrices[0], ws):
@@ -863,9 +870,10 @@ class MuonPlan:
     """The tensors of a qlora_muon_step and its workspace, checked and laid out
     once: a list of (param, grad, momentum, param_bf16 or None), matrices whose
     shorter side is <= 128, rows of any stride; param and momentum float32, grad
-    float32 or bf16.  The plan holds the tensors and finds their memory anew each
-    step; gradients that are other tensors every time go to the step itself.  Steps
-    that share a plan must be ordered on one stream."""
+    float32 or bf16; no tensor but a grad twice.  The plan holds the tensors and
+    finds their memory anew each step; gradients that are other tensors every time
+    go to the step itself.  Steps that share a plan must be ordered on one stream,
+    and a graph that captured one needs the plan kept."""
 
     def __init__(self, tensors):
         what = "MuonPlan"
@@ -886,7 +894,8 @@ class MuonPlan:
             shapes.append(tuple(p.shape))
         self._collect()
         self._layout = [(x.dtype, x.shape, x.stride(), x.device) for x in self._flat]
-        self.ws = None
+        self._separate(what)
+        self.ws, self._streams = None, set()
         if self._flat:
             with _on(what, *self._flat):
                 pass
@@ -898,6 +907,10 @@ class MuonPlan:
     def _collect(self):
         self._flat = [x for t in self.tensors for x in t if x is not None]
         self._at = None
+
+    def _separate(self, what):
+        _distinct(what, "a tensor to be written",
+                  [x for p, _, m, pb in self.tensors for x in (p, m, pb) if x is not None])
 
     def _bind(self, what, grads):
         """The tensors' addresses as they are now."""
@@ -913,6 +926,7 @@ class MuonPlan:
         for x, kept in zip(self._flat, self._layout):
             _require((x.dtype, x.shape, x.stride(), x.device) == kept, what,
                      "a tensor of another type, shape, stride or device than the plan's")
+        self._separate(what)
         for a, (p, g, m, pb) in zip(self.array, self.tensors):
             a.param, a.grad, a.momentum = p.data_ptr(), g.data_ptr(), m.data_ptr()
             a.param_bf16 = None if pb is None else pb.data_ptr()
@@ -924,8 +938,8 @@ def qlora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool =
                     coefficients=NEWTON_SCHULZ, eps: float = 1e-7, grads=None):
     """One step of the orthogonalised update on a MuonPlan (or the list it is made
     of).  grads: this step's gradients in place of the plan's, of the same types,
-    shapes and strides (kept until others come).  adjust: the step's factor, "shape" sqrt(max(1, rows / cols)), "rms"
-    0.2 sqrt(max(rows, cols)) or None."""
+    shapes and strides (kept until others come).  adjust: the step's factor, "shape"
+    sqrt(max(1, rows / cols)), "rms" 0.2 sqrt(max(rows, cols)) or None."""
     what = "qlora_muon_step"
     plan = tensors if isinstance(tensors, MuonPlan) else MuonPlan(tensors)
     _require(adjust in MUON_ADJUST, what, "unknown adjust")
@@ -935,8 +949,12 @@ def qlora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool =
         return
     plan._bind(what, grads)
     with _on(what, plan.ws):
+        s = _stream()
+        if s.value not in plan._streams:   # (its memory is not another's while this one runs)
+            plan.ws.record_stream(torch.cuda.current_stream())
+            plan._streams.add(s.value)
         _check(lib().qlora_muon_step(ctypes.byref(h), plan.array, len(plan.tensors),
-                                     _ptr(plan.ws), plan.ws.numel(), _stream()), what)
+                                     _ptr(plan.ws), plan.ws.numel(), s), what)
 
 
 class Act8Tensor:

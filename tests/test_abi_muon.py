@@ -124,3 +124,23 @@ def test_binding_refusals():
     _raises(q.qlora_muon_step, [], 0.1, adjust="other")
     assert q.qlora_muon_step([], 0.1) is None
     assert q.qlora_orthogonalize([]) == []
+
+
+def test_nothing_is_written_twice():
+    """Two tensors of a call that begin at one place would be written by workgroups of
+    both; a gradient, which is only read, may serve two."""
+    x, y, z, w = (torch.zeros(4, 50) for _ in range(4))
+    b = x.bfloat16()
+    for bad in ([(x, y, z, None), (x, y, w, None)],                  # a parameter
+                [(x, y, z, None), (w, y, z, None)],                  # a momentum
+                [(x, y, x, None)],
+                [(x, y, z, b), (w, y, y.clone(), b)]):
+        with pytest.raises(q.QloraError, match="twice"):
+            q.MuonPlan(bad)
+    with pytest.raises(q.QloraError, match="twice"):
+        q.qlora_orthogonalize([x, y], out=[z, z])
+    e = torch.zeros(0, 5)
+    for fine in ([(x, y, z, None), (w, y, y.clone(), None)],         # refused for the host only
+                 [(x, y, z, None), (e, e, e, None), (e, e, e, None)]):
+        with pytest.raises(q.QloraError, match="GPU"):
+            q.MuonPlan(fine)

@@ -238,3 +238,28 @@ def test_other_stream_and_graph():
         torch.ones(1000, device=DEV).sum()
     for a, b in zip(base, ref):
         assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2]) and torch.equal(a[3], b[3])
+
+
+def test_plan_dropped_while_another_stream_runs():
+    """The workspace of a plan is not handed out again while a step of it on another
+    stream than the one it was made on still runs."""
+    say("muon plan dropped behind a step on another stream")
+    base = _tensors([(64, 4000)] * 3)
+    ref = [tuple(x.clone() for x in t) for t in base]
+    q.qlora_muon_step(ref, 0.05)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    plan = q.MuonPlan(base)
+    n = plan.ws.numel()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        x = torch.ones((4096, 4096), device=DEV)
+        for _ in range(40):                      # the step waits its turn behind these
+            x = x @ x * 2.0 ** -12
+        q.qlora_muon_step(plan, 0.05)
+    del plan
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    for a, b in zip(base, ref):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
+    del junk
