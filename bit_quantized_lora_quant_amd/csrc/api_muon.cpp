@@ -2,6 +2,7 @@
 // launch sequence of each call, as in api.cpp.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -44,6 +45,7 @@ bool valid_ns(const qlora_newton_schulz* n) {
 struct Sizes {
   int64_t total = 0;                    // elements
   int64_t count = 0, wgs = 0, chunks = 0, part = 0, q = 0;
+  int64_t longest = 0;                  // chunks of a tensor
   uint32_t ranks = 0;                   // bit sp / 16 of each padded short side
 };
 bool empty(const MuonTensor& t) { return t.rows == 0 || t.cols == 0; }
@@ -59,6 +61,7 @@ void place(MuonTensor& t, Sizes& z) {
   z.count += 1;
   z.wgs += wgs;
   z.chunks += ceil_div(n, muon_chunk(sp));
+  z.longest = std::max(z.longest, ceil_div(n, muon_chunk(sp)));
   z.part += wgs * muon_tiles(sp);
   z.q += sp * sp / 256;
   z.ranks |= 1u << (sp / 16);
@@ -113,6 +116,7 @@ qlora_status run(int32_t count, Get get, const MuonHyper& h, void* ws, size_t ws
                       reinterpret_cast<double*>(base + L.q)};
   // one batch travels in the first launch's arguments, more through the table
   const bool whole = z.count <= kMuonBatch;
+  const bool small = whole && z.longest <= kMuonSmall && z.ranks < 1u << (64 / 16);
   Sizes at;
   at.total = z.total;
   MuonBatch b;
@@ -134,6 +138,10 @@ qlora_status run(int32_t count, Get get, const MuonHyper& h, void* ws, size_t ws
     for (int sp = 16; sp <= kMaxRank && e == hipSuccess; sp *= 2)
       if (z.ranks >> (sp / 16) & 1) e = launch(sp);
   };
+  if (small) {
+    each([&](int sp) { return launch_muon_small(b, sp, h, st); });
+    return hip_status(e);
+  }
   each([&](int sp) { return launch_muon_gram(whole ? &b : nullptr, sp, (int)z.wgs, h, s, st); });
   each([&](int sp) { return launch_muon_poly((int)z.count, sp, h, s, st); });
   each([&](int sp) { return launch_muon_apply(sp, (int)z.chunks, h, s, st); });

@@ -50,6 +50,10 @@ inline __host__ __device__ int muon_tiles(int sp) { return (sp / 16) * (sp / 16 
 // Long indices of a workgroup, for a call of `total` elements.
 int muon_slice(int sp, int64_t total);
 
+// Chunks of a matrix that one workgroup can take whole, where its padded short side is
+// 32 or less, and the update of a batch of nothing else (those of that short side).
+constexpr int kMuonSmall = 4;
+hipError_t launch_muon_small(const MuonBatch& b, int sp, const MuonHyper& h, hipStream_t st);
 // Tensors of a batch to the scratch's table.
 hipError_t launch_muon_table(const MuonBatch& b, const MuonScratch& s, hipStream_t st);
 // m, and the slices' products of the tensors whose padded short side is sp: those of

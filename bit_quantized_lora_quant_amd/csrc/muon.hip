@@ -23,9 +23,16 @@
 //   k_muon_poly   workgroup per tensor: the parts in order, |U|^2 as the trace, Q / |U|
 //   k_muon_apply  workgroup per chunk of 4096 elements: O = Q U, then the parameter's
 //                 update
+//   k_muon_small  all three for a call of small matrices
 //
-// Bound: HBM for rank up to 64 (a step moves 30 bytes a parameter, 22 of them
-// unavoidable: gradient and momentum are read again); the f64 matrix cores at 128.
+// Bound: HBM for rank up to 32 (a step moves 30 bytes a parameter, 22 of them
+// unavoidable: gradient and momentum are read again).  448 adapters of rank 16, 42
+// million parameters: gram 101 us and apply 152 us, 5.0 TB/s both, where a large copy
+// reaches 5.2; polynomials 14 us, ten launches of the table 27 us.  From a rank of 64
+// the f64 matrix cores join in (70 TF: 2 s flops a value each for the product and Q U),
+// and the polynomial of a few matrices, a chain of products on a CU each, weighs more:
+// two 65B layers of rank 64 take 70 us for gram, 7.5 us for the sum, 34 us for the
+// polynomial and 80 us for apply.
 #include "muon.h"
 
 #include <type_traits>
@@ -116,7 +123,7 @@ struct Chunk {
   static constexpr int C = 4096 / (16 * NT), pitch = C + 4;
   int i0, l0, s, n;     // of unit 0; sides
   __device__ __forceinline__ Chunk(const View& v) : s(v.s), n(v.n) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x % kThreads;
     i0 = TALL ? 4 * (tid % (4 * NT)) : tid / (C / 4);
     l0 = TALL ? tid / (4 * NT) : 4 * (tid % (C / 4));
   }
@@ -404,30 +411,21 @@ __device__ __forceinline__ void put_panel(double* x, const Panel<NT>& p, int lan
 
 constexpr int poly_waves(int nt) { return nt < 4 ? 4 : nt; }
 template <int NT>
-__global__ __launch_bounds__(64 * poly_waves(NT)) void k_muon_poly(MuonHyper h, MuonScratch s) {
-  constexpr int pitch = 16 * NT + 2;
-  __shared__ __attribute__((aligned(16))) double x[16 * NT * pitch];
-  __shared__ __attribute__((aligned(32))) f64x4_t buf[NT < 4 ? 4 * Gram<NT>::kTiles * 64 : 1];
-  const MuonTensor t = s.t[blockIdx.x];
-  const View vw = view(t);
-  if (vw.sp != 16 * NT) return;
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const f64x4_t* from = reinterpret_cast<const f64x4_t*>(s.part + (size_t)t.part * 256) + lane;
-  if constexpr (NT < 4) {
-    // every fourth slice a wave, then the four in order
-    const int slices = (int)ceil_div(vw.n, t.slice);
-    f64x4_t g[Gram<NT>::kTiles];
-#pragma unroll
-    for (int k = 0; k < Gram<NT>::kTiles; ++k) g[k] = f64x4_t{0., 0., 0., 0.};
-#pragma unroll 8
-    for (int p = wv; p < slices; p += 4)
-#pragma unroll
-      for (int k = 0; k < Gram<NT>::kTiles; ++k)
-        g[k] += from[((size_t)p * Gram<NT>::kTiles + k) * 64];
-#pragma unroll
-    for (int k = 0; k < Gram<NT>::kTiles; ++k) buf[(wv * Gram<NT>::kTiles + k) * 64 + lane] = g[k];
-    __syncthreads();
-  }
+struct PolyLds {
+  static constexpr int pitch = 16 * NT + 2;
+  __attribute__((aligned(16))) double x[16 * NT * pitch];
+  __attribute__((aligned(32))) f64x4_t buf[NT < 4 ? 4 * Gram<NT>::kTiles * 64 : 1];
+};
+// Barriers of polynomial(): after the matrix, two of G, two of each P and of each next G.
+__device__ __forceinline__ int poly_barriers(int steps) { return 1 + 2 + 2 * steps + 2 * (steps - 1); }
+// Q / |U| of the product matrix whose upper triangle is (NT < 4) the sum over the
+// waves of l.buf, else at `from`: to `out`, as k_muon_apply's left operands.
+template <int NT>
+__device__ __forceinline__ void polynomial(const MuonHyper& h, PolyLds<NT>& l, const f64x4_t* from,
+                                           double* out, int lane, int wv) {
+  constexpr int pitch = PolyLds<NT>::pitch;
+  double* x = l.x;
+  const f64x4_t* buf = l.buf;
   // both halves of the matrix
   int k = 0;
 #pragma unroll
@@ -487,14 +485,39 @@ __global__ __launch_bounds__(64 * poly_waves(NT)) void k_muon_poly(MuonHyper h, 
       put_panel<NT>(x, G, lane, pan, own);
     }
   }
-  // as k_muon_apply's left operands: (Q symmetric) row tile `pan`, inner indices
-  // 16 i + 4 v .., a line a load
+  // (Q symmetric) row tile `pan`, inner indices 16 i + 4 v .., a line a load
   if (!own) return;
-  double* out = s.q + (size_t)t.q * 256 + pan * 256 * NT + lane;
+  out += pan * 256 * NT + lane;
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v) out[(4 * i + v) * 64] = Q.t[i][v] * inv;
+}
+
+template <int NT>
+__global__ __launch_bounds__(64 * poly_waves(NT)) void k_muon_poly(MuonHyper h, MuonScratch s) {
+  __shared__ PolyLds<NT> l;
+  const MuonTensor t = s.t[blockIdx.x];
+  const View vw = view(t);
+  if (vw.sp != 16 * NT) return;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const f64x4_t* from = reinterpret_cast<const f64x4_t*>(s.part + (size_t)t.part * 256) + lane;
+  if constexpr (NT < 4) {
+    // every fourth slice a wave, then the four in order
+    const int slices = (int)ceil_div(vw.n, t.slice);
+    f64x4_t g[Gram<NT>::kTiles];
+#pragma unroll
+    for (int k = 0; k < Gram<NT>::kTiles; ++k) g[k] = f64x4_t{0., 0., 0., 0.};
+#pragma unroll 8
+    for (int p = wv; p < slices; p += 4)
+#pragma unroll
+      for (int k = 0; k < Gram<NT>::kTiles; ++k)
+        g[k] += from[((size_t)p * Gram<NT>::kTiles + k) * 64];
+#pragma unroll
+    for (int k = 0; k < Gram<NT>::kTiles; ++k) l.buf[(wv * Gram<NT>::kTiles + k) * 64 + lane] = g[k];
+    __syncthreads();
+  }
+  polynomial<NT>(h, l, from, s.q + (size_t)t.q * 256, lane, wv);
 }
 
 // Rank 33 to 64: all matrices fit LDS, so a product is taken by its tiles on and above
@@ -626,39 +649,17 @@ __global__ __launch_bounds__(kThreads) void k_muon_poly64(MuonHyper h, MuonScrat
 }
 
 // --------------------------------------------------------------------- apply
-// O = Q U of one chunk: wave w takes row tiles and columns of it.  The chunk's loads are
-// in flight before those of Q; several workgroups a CU hide one another's phases.
-template <int NT, bool TALL>
-__device__ __forceinline__ void apply(const MuonTensor& t, const View& v, const MuonHyper& h,
-                                      int start, const double* q, float* u) {
+// U <- Q U of one chunk in LDS: wave w takes row tiles and columns of it.
+template <int NT>
+__device__ __forceinline__ void product(const double* q, float* u) {
   constexpr int C = 4096 / (16 * NT), pitch = C + 4;
   constexpr int RW = NT < 4 ? NT : 4;         // waves along the short side
   constexpr int MI = NT / RW;                 // row tiles of a wave
   constexpr int CW = 4 / RW;                  // waves along the long side
   constexpr int MJ = C / 16 / CW;             // column tiles of a wave
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x % kThreads >> 6);
   const int wr = wv % RW, wc = wv / RW;
-  const bool vi = fits16(t.in, t.ldi, t.bf16 ? 2 : 4), vm = fits16(t.m, t.ldm, 4);
-  const bool vo = fits16(t.out, t.ldo, !h.step && t.bf16 ? 2 : 4), vb = fits16(t.pb, t.ldb, 2);
-  const bool need_in = !t.m || h.nesterov;
-  const Chunk<NT, TALL> c(v);
-  float g[kUnits][4], m[kUnits][4], p[kUnits][4];
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    const int valid = c.valid(k, start);
-    if (need_in) load_in(g[k], t, c.off(k, start, t.ldi), valid, vi);
-    if (t.m) load4(m[k], t.m + c.off(k, start, t.ldm), valid, vm);
-    if (h.step) load4(p[k], static_cast<const float*>(t.out) + c.off(k, start, t.ldo), valid, vo);
-  }
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    if (t.m) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
-    }
-    c.put(u, k, g[k]);
-  }
-  __syncthreads();
   f64x4_t o[MI][MJ];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
@@ -688,6 +689,14 @@ __device__ __forceinline__ void apply(const MuonTensor& t, const View& v, const 
         u[(16 * (wr * MI + i) + 4 * r + (lane >> 4)) * pitch + 16 * (wc * MJ + j) + (lane & 15)] =
             (float)o[i][j][r];
   __syncthreads();
+}
+
+// What becomes of a chunk of O in LDS; p: the parameters' values of a step.
+template <int NT, bool TALL>
+__device__ __forceinline__ void finish(const MuonTensor& t, const MuonHyper& h,
+                                       const Chunk<NT, TALL>& c, int start, const float* u,
+                                       const float (&p)[kUnits][4]) {
+  const bool vo = fits16(t.out, t.ldo, !h.step && t.bf16 ? 2 : 4), vb = fits16(t.pb, t.ldb, 2);
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
     const int valid = c.valid(k, start);
@@ -706,6 +715,44 @@ __device__ __forceinline__ void apply(const MuonTensor& t, const View& v, const 
   }
 }
 
+template <int NT, bool TALL>
+__device__ __forceinline__ void load_param(float (&p)[kUnits][4], const MuonTensor& t,
+                                           const Chunk<NT, TALL>& c, int start) {
+  const bool vo = fits16(t.out, t.ldo, 4);
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k)
+    load4(p[k], static_cast<const float*>(t.out) + c.off(k, start, t.ldo), c.valid(k, start), vo);
+}
+
+// The chunk's loads are in flight before those of Q; several workgroups a CU hide one
+// another's phases.
+template <int NT, bool TALL>
+__device__ __forceinline__ void apply(const MuonTensor& t, const View& v, const MuonHyper& h,
+                                      int start, const double* q, float* u) {
+  const bool vi = fits16(t.in, t.ldi, t.bf16 ? 2 : 4), vm = fits16(t.m, t.ldm, 4);
+  const bool need_in = !t.m || h.nesterov;
+  const Chunk<NT, TALL> c(v);
+  float g[kUnits][4], m[kUnits][4], p[kUnits][4];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const int valid = c.valid(k, start);
+    if (need_in) load_in(g[k], t, c.off(k, start, t.ldi), valid, vi);
+    if (t.m) load4(m[k], t.m + c.off(k, start, t.ldm), valid, vm);
+  }
+  if (h.step) load_param(p, t, c, start);
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    if (t.m) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
+    }
+    c.put(u, k, g[k]);
+  }
+  __syncthreads();
+  product<NT>(q, u);
+  finish(t, h, c, start, u, p);
+}
+
 // Last chunks first: what the first launches read last is still in the Infinity
 // Cache.
 template <int NT>
@@ -719,6 +766,81 @@ __global__ __launch_bounds__(kThreads, 4) void k_muon_apply(MuonHyper h, MuonScr
   const int start = (c - t.chunk) * v.chunk;
   if (v.tall) apply<NT, true>(t, v, h, start, q, u);
   else apply<NT, false>(t, v, h, start, q, u);
+}
+
+// --------------------------------------------------------------------- small
+// A call of small matrices: a workgroup takes one from its gradient to its update, in
+// one launch, U and Q in LDS all the while, four waves a chunk: latency is all there is
+// (8 x 1024 and 1024 x 8, a step 16.6 us in place of 20.2 with three launches; with four
+// waves for all chunks 30).
+template <int NT, bool TALL>
+__device__ __forceinline__ void small(const MuonTensor& t, const View& v, const MuonHyper& h,
+                                      float* u, PolyLds<NT>& l, double* q) {
+  constexpr int kTiles = Gram<NT>::kTiles;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+  const int at = group * Chunk<NT, TALL>::C;
+  const bool vi = fits16(t.in, t.ldi, t.bf16 ? 2 : 4), vm = fits16(t.m, t.ldm, 4);
+  const Chunk<NT, TALL> c(v);
+  u += group * kBuf;
+  float g[kUnits][4], m[kUnits][4], p[kUnits][4];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const int valid = c.valid(k, at);
+    load_in(g[k], t, c.off(k, at, t.ldi), valid, vi);
+    if (t.m) load4(m[k], t.m + c.off(k, at, t.ldm), valid, vm);
+  }
+  if (h.step) load_param(p, t, c, at);
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    if (t.m) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[k][e] = momentum(m[k][e], g[k][e], h);
+      store4(t.m + c.off(k, at, t.ldm), m[k], c.valid(k, at), vm);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
+    }
+    c.put(u, k, g[k]);
+  }
+  __syncthreads();
+  Gram<NT> G;
+  G.init();
+  G.add(u, lane, wv);
+  // the chunks' products, from the last on
+  f64x4_t* buf = l.buf + wv * kTiles * 64 + lane;
+  for (int from = kMuonSmall - 1; from >= 0; --from) {
+    if (group == from) {
+#pragma unroll
+      for (int k = 0; k < kTiles; ++k) buf[k * 64] = G.acc[k];
+    }
+    __syncthreads();
+    if (group == from - 1) {
+#pragma unroll
+      for (int k = 0; k < kTiles; ++k) G.acc[k] += buf[k * 64];
+    }
+    __syncthreads();
+  }
+  if (group == 0) {
+    polynomial<NT>(h, l, nullptr, q, lane, wv);
+  } else {
+    // (the barriers of the waves that do)
+    for (int k = 0; k < poly_barriers(h.steps); ++k) __syncthreads();
+  }
+  __syncthreads();
+  product<NT>(q, u);
+  finish(t, h, c, at, u, p);
+}
+template <int NT>
+__global__ __launch_bounds__(kMuonSmall * kThreads) void k_muon_small(const MuonBatch bt,
+                                                                      MuonHyper h) {
+  __shared__ __attribute__((aligned(16))) float u[kMuonSmall * kBuf];
+  __shared__ PolyLds<NT> l;
+  __shared__ __attribute__((aligned(16))) double q[256 * NT * NT];
+  const MuonTensor t = bt.t[blockIdx.x];
+  const View v = view(t);
+  if (v.sp != 16 * NT) return;
+  if (v.tall) small<NT, true>(t, v, h, u, l, q);
+  else small<NT, false>(t, v, h, u, l, q);
 }
 
 }  // namespace
@@ -752,6 +874,12 @@ hipError_t launch_muon_gram(const MuonBatch* b, int sp, int wgs, const MuonHyper
     case 64: return launch_gram<4>(b, grid, h, s, st);
     default: return launch_gram<8>(b, grid, h, s, st);
   }
+}
+
+hipError_t launch_muon_small(const MuonBatch& b, int sp, const MuonHyper& h, hipStream_t st) {
+  const dim3 grid((unsigned)b.count), block(kMuonSmall * kThreads);
+  return sp == 16 ? launch_kernel(k_muon_small<1>, grid, block, st, b, h)
+                  : launch_kernel(k_muon_small<2>, grid, block, st, b, h);
 }
 
 hipError_t launch_muon_poly(int count, int sp, const MuonHyper& h, const MuonScratch& s,

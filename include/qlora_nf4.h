@@ -489,7 +489,8 @@ typedef struct {
   int32_t reserved;    /* must be 0 */
 } qlora_ortho_matrix;
 /* Orthogonalises `count` matrices, in 3 launches for up to 45 of a rank up to 32
- * (4 above).  A matrix without elements is skipped; a zero matrix gives zeros.
+ * (4 above), in one for as many of at most 16384 elements and a rank up to 16 (or 32),
+ * the short side taken as 16 (32).  A matrix without elements is skipped; a zero matrix gives zeros.
  * No output may overlap another matrix of the call. */
 qlora_status qlora_orthogonalize(const qlora_newton_schulz* ns, const qlora_ortho_matrix* m,
                                  int32_t count, void* ws, size_t ws_bytes, void* stream);

@@ -263,3 +263,35 @@ def test_plan_dropped_while_another_stream_runs():
     for a, b in zip(base, ref):
         assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
     del junk
+
+
+# up to four chunks of 4096 padded elements, where a workgroup takes a matrix whole, and
+# one more long index, where none does
+SMALL = [(16, 1024), (1024, 16), (32, 512), (511, 32), (3, 257), (769, 5), (1, 1), (20, 129)]
+
+
+@pytest.mark.parametrize("count", [1, 8, 45, 46])
+@pytest.mark.parametrize("more", [0, 1])
+def test_small_matrices(count, more):
+    say("%d small matrices, %d more" % (count, more))
+    shapes = [SMALL[i % 8] for i in range(count)]
+    if more:
+        shapes[0] = (16, 1025)
+    ts = _tensors(shapes, pads=[0, 4, 1])
+    us = [_matrix(7 + i, *s, pad=i % 3, dtype=BF if i % 2 else F32) for i, s in enumerate(shapes)]
+    ref = [_expect(p, g, m, 0.3, 0.9, True, 0.1, "rms") for p, g, m, _ in ts]
+    for u, o in zip(us, q.qlora_orthogonalize(us)):
+        _check(o, omuon.orthogonalize(_np(u)), u.dtype)
+    q.qlora_muon_step(ts, 0.3, 0.9, weight_decay=0.1, adjust="rms")
+    for (p, _, m, pb), (m_ref, p_ref, tol) in zip(ts, ref):
+        assert np.array_equal(host(m).numpy(), m_ref)
+        assert np.all(np.abs(_np(p) - p_ref) <= tol)
+        assert torch.equal(pb, p.to(BF))
+    for (p, _, _, _), (rows, cols) in zip(ts, shapes):
+        pad = p.stride(0) - cols
+        if rows > 1 and pad > 0:     # (the values were drawn as 7 and multiplied by 20)
+            between = torch.as_strided(p, (rows - 1, pad), (p.stride(0), 1), cols)
+            assert (between == 7).all()
+    again = q.qlora_orthogonalize(us)
+    q.qlora_orthogonalize(us, out=us)
+    assert all(torch.equal(a, b) for a, b in zip(us, again))
