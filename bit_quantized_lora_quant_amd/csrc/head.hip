@@ -27,9 +27,9 @@
 // indices a step.  Accumulators stay in AGPRs, both tiles stream into LDS by DMA and
 // operands are read half a step ahead.  Operands whose inner index is not contiguous
 // (W in dh, both in dW) are transposed by the LDS reads themselves.  At V = 128256,
-// D = 4096 the logits of 2048 rows take 1.4 to 1.65 ms (1300 to 1540 TF, by the card;
-// the card's largest library products reach 1240 to 1390) and 4096 rows' loss and dh
-// 5.1 ms.
+// D = 4096 the log-probabilities of 2048 rows take 1.59 to 1.67 ms (1290 to 1350 TF, by
+// the card; torch's products of such sizes reach 1240 to 1390) and 4096 rows' loss and dh
+// 6.6 to 6.8 ms, both products at 1270 to 1310 TF.
 #include "head.h"
 
 #include <type_traits>
@@ -92,6 +92,8 @@ __device__ __forceinline__ int dh_splits_wave(int64_t tiles, int64_t steps, int 
 }
 
 // ---------------------------------------------------------------- packing rows
+// Bound by HBM where rows are many (3055 of 4096 rows at D = 4096: 27 us, 75 MB with the
+// targets' rows of W, each of which a wave waits for), by latency below (5 us).
 // Workgroup b looks after rows [b R, (b + 1) R): it counts the targets before
 // them, copies its rows that have one to their places and clears what the call
 // returns for the others.  Labels are few (8 bytes a row, against 2 D), so
@@ -547,7 +549,8 @@ __device__ __forceinline__ int panel_splits(const HeadPanel& p, int n) {
 
 // -------------------------------------------------------------------- logits
 // A = W (the vocabulary along a lane's registers: a row's statistics are sums in the
-// lane, then over the four lanes of its column), B = rows.
+// lane, then over the four lanes of its column), B = rows.  One row of 4096 reads a
+// weight of 128256 rows in 171 us, 6.1 TB/s; many rows are bound by the matrix cores.
 constexpr int HEAD_RAW = 4;    // partial logits of a slice of the inner index
 // Waves along the rows.  Of 256 rows, two of 128 each read half as much from LDS as
 // four of 64 do, for one wave a SIMD: 2048 rows at D = 8192, V = 32000 take 813 us for
@@ -743,7 +746,8 @@ __global__ __launch_bounds__(kThreads) void k_head_slices(HeadPanel p, int TN, i
 
 // ---------------------------------------------------------------------- join
 // A workgroup joins the slices of 16 rows, 64 of its threads a row: the maximum
-// first, then the sums in float64.
+// first, then the sums in float64.  Latency: 5 us for 250 slices a row, 11 for 1002
+// (16 loads in flight a thread, kept for the second pass).
 constexpr int kJoinRows = 16, kJoinWaves = 16;
 __global__ __launch_bounds__(64 * kJoinWaves)
 void k_head_join(HeadPanel p, int kind, int shift, double* lp, float* logp, HeadStat* stat) {
@@ -844,7 +848,8 @@ __global__ __launch_bounds__(1024) void k_head_loss(const int32_t* n, const doub
 }
 
 // ------------------------------------------------------------------------ dz
-// In place, a thread 8 columns of 8 rows: HBM-bound.  dz = f 2^(M - R) e, the target's
+// In place, a thread 8 columns of 8 rows: HBM-bound (2048 x 128256: 224 us, 1.05 GB at
+// 4.7 TB/s).  dz = f 2^(M - R) e, the target's
 // c; zeros in the rows up to a whole step of dW.
 constexpr int kDzRows = 8;
 __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
@@ -904,6 +909,9 @@ __device__ __forceinline__ uint4 pack8(const float (&o)[8]) {
                     pack_bf16x2(o[6], o[7]));
 }
 
+// A = W (transposed by the reads), B = e; inner index the vocabulary.  2048 rows at
+// V = 128256, D = 4096 1.5 ms, 1400 TF, from dz; from powers, whose exponents the
+// loop lowers on the vector unit, 3055 rows 2.6 ms, 1230 TF (192 tiles: cut in slices).
 // POW: e holds 2^(z log2 e - M) of each slice: the tile loop lowers its exponents to
 // the row's R, and what is left is a factor of the whole row and the target's term,
 // c times its row of W, in float32 at the end.  So dz is rounded to bf16 once, e is
@@ -1068,7 +1076,9 @@ __global__ __launch_bounds__(kThreads) void k_head_rest(HeadPanel p, float* rest
   }
 }
 
-// A = h (transposed by the reads), B = dz (likewise); inner index the rows.
+// A = h (transposed by the reads), B = dz (likewise); inner index the rows.  Bound by
+// the matrix cores, and by 1 GB of writes at V = 128256, D = 4096: 2048 rows 1.91 to 2.0 ms,
+// 1080 to 1130 TF (torch's product of that layout reaches 1059).
 __global__ __attribute__((amdgpu_flat_work_group_size(128 * kWavesB, 128 * kWavesB),
                           amdgpu_waves_per_eu(kWavesB / 2, kWavesB / 2)))
 void k_head_dw(HeadPanel p, const float* rest, int splits, float* part, float* sum, int first,

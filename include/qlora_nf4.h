@@ -489,9 +489,10 @@ typedef struct {
   int32_t reserved;    /* must be 0 */
 } qlora_ortho_matrix;
 /* Orthogonalises `count` matrices, in 3 launches for up to 45 of a rank up to 32
- * (4 above), in one for as many of at most 16384 elements and a rank up to 16 (or 32),
- * the short side taken as 16 (32).  A matrix without elements is skipped; a zero matrix gives zeros.
- * No output may overlap another matrix of the call. */
+ * (4 above); in one if each is small, of a long side up to 1024 for a rank up to 16
+ * or up to 512 for 32 (one for each of the two).  A matrix without elements is
+ * skipped; a zero matrix gives zeros.  No output may overlap another matrix of the
+ * call. */
 qlora_status qlora_orthogonalize(const qlora_newton_schulz* ns, const qlora_ortho_matrix* m,
                                  int32_t count, void* ws, size_t ws_bytes, void* stream);
 
@@ -731,10 +732,14 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
  * no target (logp 0, gradient row zero; whatever the hidden row holds, NaN
  * included, reaches nothing, and the row costs no product), a label >= vocab
  * gives logp NaN, which reaches the loss, the row's gradient and all of dW.
- * Sums over the vocabulary are float32 in a tile and float64 between tiles and
- * after the logarithm.  dz is rounded to bf16 (the matrix cores' type) once
- * before the products that give dh and dW, whose sums are float32 and rounded
- * once to bf16.  Results are identical run to run. */
+ * The target's logit is a float64 sum.  Sums over the rest of the vocabulary are
+ * float32 over 128 entries and float64 between those and after the logarithm.  dz
+ * is rounded to bf16 (the matrix cores' type) once before the products that give
+ * dh and dW, whose sums are float32 and rounded once to bf16; what the rounding
+ * leaves of the targets' dz, the largest of their rows, is added in float32 (to dW
+ * for labels of up to 256 rows at a time).  Results are identical run to run, but
+ * dh is formed otherwise beside dW than alone: within the same bounds, not the same
+ * bits. */
 typedef struct {
   const qlora_bf16* hidden;  /* device, [rows] x ld_hidden; may be NULL when rows == 0 */
   int64_t rows;              /* < 2^24 */
