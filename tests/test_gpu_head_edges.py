@@ -418,3 +418,64 @@ def test_a_supervised_step_from_end_to_end():
     for p, leaf, ref in zip(masters, (a, b), want):
         assert np.max(np.abs(_np(p) - ref)) <= 1e-6 * np.max(np.abs(ref))
         assert torch.equal(leaf.detach(), p.to(BF))
+
+
+@pytest.mark.parametrize("T,D,V", [(1500, 64, 9000), (2300, 128, 20001), (900, 192, 16128),
+                                   (3000, 256, 5000)])
+def test_tall_tiles_of_few_steps(T, D, V):
+    """Tiles of 256 rows whose inner index is one to four steps long."""
+    say("tall tiles T=%d D=%d V=%d" % (T, D, V))
+    h, W, y = _inputs(T, T, D, V, ignored=0.05)
+    w = torch.linspace(-1, 1, T, device=DEV)
+    ref, d, dh_ref, dw_ref = _exact(h, W, y, w)
+    masked = torch.where((y >= 0)[:, None], h.double(), 0.0)
+    logp, stats = q.qlora_head_logprobs(h, W, y, return_stats=True)
+    assert float((logp.double() - ref).abs().max()) <= _logp_tol(D, V)
+    dh, dw = q.qlora_head_logprobs_bwd(h, W, y, stats, w, need_dweight=True)
+    _check_grad(dh, d, W.double(), dh_ref, V)
+    _check_grad(dw, d.T.contiguous(), masked, dw_ref, T)
+    n = int((y >= 0).sum())
+    _, d, dh_ref, dw_ref = _exact(h, W, y, torch.full((T,), -1.0 / n, device=DEV))
+    o = q.qlora_head_cross_entropy(h, W, y, return_grad=True, need_dweight=True)
+    assert torch.equal(o.logp, logp)
+    _check_grad(o.dhidden, d, W.double(), dh_ref, V)
+    _check_grad(o.dweight, d.T.contiguous(), masked, dw_ref, T)
+    only = q.qlora_head_cross_entropy(h, W, y, return_grad=True)
+    assert torch.equal(only.logp, logp)
+    _check_grad(only.dhidden, d, W.double(), dh_ref, V)
+
+
+@pytest.mark.parametrize("times", [1, 2, 255, 256, 257, 700])
+@pytest.mark.parametrize("V", [90, 700, 9000])
+def test_one_label_many_times(times, V):
+    """The same target in many rows, up to where their roundings are left to average."""
+    say("one label %d times, V=%d" % (times, V))
+    h, W, y = _inputs(41, 720, 128, V, ignored=0.1, sharp=0.3)
+    y[torch.randperm(720, generator=torch.Generator().manual_seed(times))[:times].to(DEV)] = 7
+    n = int((y >= 0).sum())
+    _, d, _, dw_ref = _exact(h, W, y, torch.full((720,), -1.0 / n, device=DEV))
+    masked = torch.where((y >= 0)[:, None], h.double(), 0.0)
+    o = q.qlora_head_cross_entropy(h, W, y, need_dweight=True)
+    _check_grad(o.dweight, d.T.contiguous(), masked, dw_ref, 720)
+    _, stats = q.qlora_head_logprobs(h, W, y, return_stats=True)
+    w = torch.full((720,), -1.0 / n, device=DEV)
+    dw = q.qlora_head_logprobs_bwd(h, W, y, stats, w, need_dhidden=False, need_dweight=True)[1]
+    _check_grad(dw, d.T.contiguous(), masked, dw_ref, 720)
+
+
+def test_labels_and_weights_of_one_call_in_another():
+    """A workspace that held another call's rows, slices and labels leaves nothing in
+    the next one's results."""
+    say("one workspace for calls of several sizes")
+    cases = [_inputs(50, 900, 256, 9000), _inputs(51, 3, 64, 300), _inputs(52, 300, 128, 2000)]
+    ws = torch.full((max(q.qlora_head_workspace_bytes(*x, True, True) for x in cases),), 255,
+                    dtype=torch.uint8, device=DEV)
+    for h, W, y in cases + cases[::-1]:
+        a = q.qlora_head_cross_entropy(h, W, y, return_grad=True, need_dweight=True)
+        b = q.qlora_head_cross_entropy(h, W, y, return_grad=True, need_dweight=True, ws=ws)
+        c = q.qlora_head_cross_entropy(h, W, y, return_grad=True)
+        d = q.qlora_head_cross_entropy(h, W, y, return_grad=True, ws=ws)
+        for x, z in ((a, b), (c, d)):
+            assert torch.equal(x.loss, z.loss) and torch.equal(x.logp, z.logp)
+            assert torch.equal(x.dhidden, z.dhidden)
+        assert torch.equal(a.dweight, b.dweight)
