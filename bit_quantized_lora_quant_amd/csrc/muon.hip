@@ -116,11 +116,11 @@ __device__ __forceinline__ void load_in(float (&x)[4], const MuonTensor& t, int6
 
 // A thread's four units of a chunk, 4 neighbours in memory each: wide C / 4 of them a
 // short index, tall 4 NT a long index (past the short side or the end they hold
-// nothing).  In LDS a chunk of U lies as [short][long], C + 4 floats a row: the
-// 16 x 4 operand reads and both kinds of writes spread over the banks.
+// nothing).  In LDS element (i, l) of a chunk lies at i SI + l SL floats, with one of
+// the strides 1.
 template <int NT, bool TALL>
 struct Chunk {
-  static constexpr int C = 4096 / (16 * NT), pitch = C + 4;
+  static constexpr int C = 4096 / (16 * NT);
   int i0, l0, s, n;     // of unit 0; sides
   __device__ __forceinline__ Chunk(const View& v) : s(v.s), n(v.n) {
     const int tid = threadIdx.x % kThreads;
@@ -138,21 +138,25 @@ struct Chunk {
   __device__ __forceinline__ int64_t off(int k, int at, int ld) const {
     return TALL ? (int64_t)(at + l(k)) * ld + i0 : (int64_t)i(k) * ld + at + l0;
   }
+  template <int SI, int SL>
   __device__ __forceinline__ void put(float* u, int k, const float (&x)[4]) const {
-    if (TALL) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[(i0 + e) * pitch + l(k)] = x[e];
+    float* at = u + i(k) * SI + l(k) * SL;
+    if constexpr ((TALL ? SI : SL) == 1) {
+      *reinterpret_cast<float4*>(at) = make_float4(x[0], x[1], x[2], x[3]);
     } else {
-      *reinterpret_cast<float4*>(u + i(k) * pitch + l0) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) at[e * (TALL ? SI : SL)] = x[e];
     }
   }
+  template <int SI, int SL>
   __device__ __forceinline__ void get(float (&x)[4], const float* u, int k) const {
-    if (TALL) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = u[(i0 + e) * pitch + l(k)];
-    } else {
-      const float4 f = *reinterpret_cast<const float4*>(u + i(k) * pitch + l0);
+    const float* at = u + i(k) * SI + l(k) * SL;
+    if constexpr ((TALL ? SI : SL) == 1) {
+      const float4 f = *reinterpret_cast<const float4*>(at);
       x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = at[e * (TALL ? SI : SL)];
     }
   }
 };
@@ -248,7 +252,9 @@ struct Gram {
 template <int NT, bool TALL>
 __device__ __forceinline__ void gram(const MuonTensor& t, const View& v, const MuonHyper& h,
                                      int slice, double* out, float* u, double* buf) {
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // (of ten products two waves have three: not the same two in neighbouring workgroups)
+  const int lane = threadIdx.x & 63;
+  const int wv = (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + 2 * (slice & 1)) & 3;
   const int first = slice * t.slice, end = first + t.slice < v.n ? first + t.slice : v.n;
   const bool vi = fits16(t.in, t.ldi, t.bf16 ? 2 : 4), vm = fits16(t.m, t.ldm, 4);
   const Chunk<NT, TALL> c(v);
@@ -271,7 +277,7 @@ __device__ __forceinline__ void gram(const MuonTensor& t, const View& v, const M
 #pragma unroll
         for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
       }
-      c.put(to, k, g[k]);
+      c.template put<Gram<NT>::pitch, 1>(to, k, g[k]);
     }
   };
   Gram<NT> G;
@@ -650,9 +656,9 @@ __global__ __launch_bounds__(kThreads) void k_muon_poly64(MuonHyper h, MuonScrat
 
 // --------------------------------------------------------------------- apply
 // U <- Q U of one chunk in LDS: wave w takes row tiles and columns of it.
-template <int NT>
+template <int NT, int SI, int SL>
 __device__ __forceinline__ void product(const double* q, float* u) {
-  constexpr int C = 4096 / (16 * NT), pitch = C + 4;
+  constexpr int C = 4096 / (16 * NT);
   constexpr int RW = NT < 4 ? NT : 4;         // waves along the short side
   constexpr int MI = NT / RW;                 // row tiles of a wave
   constexpr int CW = 4 / RW;                  // waves along the long side
@@ -665,7 +671,7 @@ __device__ __forceinline__ void product(const double* q, float* u) {
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < MJ; ++j) o[i][j] = f64x4_t{0., 0., 0., 0.};
-  const float* at = u + (lane >> 4) * pitch + 16 * wc * MJ + (lane & 15);
+  const float* at = u + (lane >> 4) * SI + (16 * wc * MJ + (lane & 15)) * SL;
   const double* aq = q + wr * MI * 256 * NT + lane;
 #pragma unroll
   for (int k = 0; k < 4 * NT; ++k) {
@@ -674,7 +680,7 @@ __device__ __forceinline__ void product(const double* q, float* u) {
     for (int i = 0; i < MI; ++i) a[i] = aq[i * 256 * NT + 64 * k];
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
-      const double x = (double)at[4 * k * pitch + 16 * j];
+      const double x = (double)at[4 * k * SI + 16 * j * SL];
 #pragma unroll
       for (int i = 0; i < MI; ++i) o[i][j] = mfma64(a[i], x, o[i][j]);
     }
@@ -686,13 +692,13 @@ __device__ __forceinline__ void product(const double* q, float* u) {
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        u[(16 * (wr * MI + i) + 4 * r + (lane >> 4)) * pitch + 16 * (wc * MJ + j) + (lane & 15)] =
-            (float)o[i][j][r];
+        u[(16 * (wr * MI + i) + 4 * r + (lane >> 4)) * SI +
+          (16 * (wc * MJ + j) + (lane & 15)) * SL] = (float)o[i][j][r];
   __syncthreads();
 }
 
 // What becomes of a chunk of O in LDS; p: the parameters' values of a step.
-template <int NT, bool TALL>
+template <int NT, bool TALL, int SI, int SL>
 __device__ __forceinline__ void finish(const MuonTensor& t, const MuonHyper& h,
                                        const Chunk<NT, TALL>& c, int start, const float* u,
                                        const float (&p)[kUnits][4]) {
@@ -702,7 +708,7 @@ __device__ __forceinline__ void finish(const MuonTensor& t, const MuonHyper& h,
     const int valid = c.valid(k, start);
     const int64_t off = c.off(k, start, t.ldo);
     float x[4];
-    c.get(x, u, k);
+    c.template get<SI, SL>(x, u, k);
     if (!h.step) {
       if (t.bf16) store4(static_cast<uint16_t*>(t.out) + off, x, valid, vo);
       else store4(static_cast<float*>(t.out) + off, x, valid, vo);
@@ -724,11 +730,21 @@ __device__ __forceinline__ void load_param(float (&p)[kUnits][4], const MuonTens
     load4(p[k], static_cast<const float*>(t.out) + c.off(k, start, t.ldo), c.valid(k, start), vo);
 }
 
+// A chunk's place in LDS for the product alone: the four units' values of a thread side
+// by side, and an operand (four short indices of 16 long ones) on 64 banks.
+template <int NT, bool TALL>
+struct ApplyLds {
+  static constexpr int C = 4096 / (16 * NT);
+  static constexpr int SI = TALL ? 1 : C + 16, SL = TALL ? 16 * NT + 4 : 1;
+  static constexpr int kFloats = TALL ? C * SL : 16 * NT * SI;
+};
+
 // The chunk's loads are in flight before those of Q; several workgroups a CU hide one
 // another's phases.
 template <int NT, bool TALL>
 __device__ __forceinline__ void apply(const MuonTensor& t, const View& v, const MuonHyper& h,
                                       int start, const double* q, float* u) {
+  using A = ApplyLds<NT, TALL>;
   const bool vi = fits16(t.in, t.ldi, t.bf16 ? 2 : 4), vm = fits16(t.m, t.ldm, 4);
   const bool need_in = !t.m || h.nesterov;
   const Chunk<NT, TALL> c(v);
@@ -746,18 +762,19 @@ __device__ __forceinline__ void apply(const MuonTensor& t, const View& v, const 
 #pragma unroll
       for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
     }
-    c.put(u, k, g[k]);
+    c.template put<A::SI, A::SL>(u, k, g[k]);
   }
   __syncthreads();
-  product<NT>(q, u);
-  finish(t, h, c, start, u, p);
+  product<NT, A::SI, A::SL>(q, u);
+  finish<NT, TALL, A::SI, A::SL>(t, h, c, start, u, p);
 }
 
 // Last chunks first: what the first launches read last is still in the Infinity
 // Cache.
 template <int NT>
 __global__ __launch_bounds__(kThreads, 4) void k_muon_apply(MuonHyper h, MuonScratch s) {
-  __shared__ __attribute__((aligned(16))) float u[kBuf];
+  constexpr int kWide = ApplyLds<NT, false>::kFloats, kTall = ApplyLds<NT, true>::kFloats;
+  __shared__ __attribute__((aligned(16))) float u[kWide > kTall ? kWide : kTall];
   const int c = gridDim.x - 1 - blockIdx.x;
   const MuonTensor t = s.t[__builtin_amdgcn_readfirstlane(s.owner[c])];
   const View v = view(t);
@@ -776,7 +793,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_muon_apply(MuonHyper h, MuonScr
 template <int NT, bool TALL>
 __device__ __forceinline__ void small(const MuonTensor& t, const View& v, const MuonHyper& h,
                                       float* u, PolyLds<NT>& l, double* q) {
-  constexpr int kTiles = Gram<NT>::kTiles;
+  constexpr int kTiles = Gram<NT>::kTiles, SI = Gram<NT>::pitch;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
   const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
   const int at = group * Chunk<NT, TALL>::C;
@@ -800,7 +817,7 @@ __device__ __forceinline__ void small(const MuonTensor& t, const View& v, const 
 #pragma unroll
       for (int e = 0; e < 4; ++e) g[k][e] = update(m[k][e], g[k][e], h);
     }
-    c.put(u, k, g[k]);
+    c.template put<SI, 1>(u, k, g[k]);
   }
   __syncthreads();
   Gram<NT> G;
@@ -827,8 +844,8 @@ __device__ __forceinline__ void small(const MuonTensor& t, const View& v, const 
     for (int k = 0; k < poly_barriers(h.steps); ++k) __syncthreads();
   }
   __syncthreads();
-  product<NT>(q, u);
-  finish(t, h, c, at, u, p);
+  product<NT, SI, 1>(q, u);
+  finish<NT, TALL, SI, 1>(t, h, c, at, u, p);
 }
 template <int NT>
 __global__ __launch_bounds__(kMuonSmall * kThreads) void k_muon_small(const MuonBatch bt,
