@@ -9,6 +9,7 @@ every call raises.
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 from typing import NamedTuple, Optional
 
@@ -877,11 +878,11 @@ class MuonPlan:
 
     def __init__(self, tensors):
         what = "MuonPlan"
-        self.tensors = [tuple(t) for t in tensors]
-        self.array = (MuonTensor * max(len(self.tensors), 1))()
+        tensors = [tuple(t) for t in tensors]
+        self.array = (MuonTensor * max(len(tensors), 1))()
         f32 = (torch.float32,)
         shapes = []
-        for a, t in zip(self.array, self.tensors):
+        for a, t in zip(self.array, tensors):
             _require(len(t) == 4, what, "(param, grad, momentum, param_bf16) tuples")
             p, g, m, pb = t
             a.ld_param = _matrix(what, p, f32, None, "param")
@@ -892,45 +893,61 @@ class MuonPlan:
             a.rows, a.cols = p.shape
             a.grad_dtype = QLORA_BF16 if g.dtype == torch.bfloat16 else QLORA_F32
             shapes.append(tuple(p.shape))
-        self._collect()
-        self._layout = [(x.dtype, x.shape, x.stride(), x.device) for x in self._flat]
+        self._written = [(p, m, pb) for p, _, m, pb in tensors]
+        self._own = [x for t in self._written for x in t if x is not None]
+        self._grads = [t[1] for t in tensors]
+        self._own_at = self._grads_at = None
+        self._own_layout, self._grads_layout = self._layout(self._own), self._layout(self._grads)
         self._separate(what)
         self.ws, self._streams = None, set()
-        if self._flat:
-            with _on(what, *self._flat):
+        if tensors:
+            with _on(what, *self._own, *self._grads):
                 pass
             need = qlora_muon_workspace_bytes(shapes)
             _require(need > 0 or all(0 in s for s in shapes), what,
                      "a matrix's shorter side is above %d", MAX_RANK)
-            self.ws = workspace(need, self._flat[0].device)
+            self.ws = workspace(need, self._own[0].device)
 
-    def _collect(self):
-        self._flat = [x for t in self.tensors for x in t if x is not None]
-        self._at = None
+    @property
+    def tensors(self):
+        """(param, grad, momentum, param_bf16) of each, with the last gradients."""
+        return [(p, g, m, pb) for (p, m, pb), g in zip(self._written, self._grads)]
+
+    @staticmethod
+    def _layout(tensors):
+        # (whole lists at a time: a step whose gradients are new is as long as this)
+        return ([x.dtype for x in tensors], [x.shape for x in tensors],
+                list(map(torch.Tensor.stride, tensors)),
+                list(map(torch.Tensor.get_device, tensors)))
 
     def _separate(self, what):
-        _distinct(what, "a tensor to be written",
-                  [x for p, _, m, pb in self.tensors for x in (p, m, pb) if x is not None])
+        _distinct(what, "a tensor to be written", self._own)
 
     def _bind(self, what, grads):
         """The tensors' addresses as they are now."""
         if grads is not None:
             grads = list(grads)
-            _require(len(grads) == len(self.tensors), what, "as many gradients as tensors")
-            if any(t[1] is not g for t, g in zip(self.tensors, grads)):
-                self.tensors = [(t[0], g, *t[2:]) for t, g in zip(self.tensors, grads)]
-                self._collect()
-        at = list(map(torch.Tensor.data_ptr, self._flat))
-        if at == self._at:
-            return
-        for x, kept in zip(self._flat, self._layout):
-            _require((x.dtype, x.shape, x.stride(), x.device) == kept, what,
-                     "a tensor of another type, shape, stride or device than the plan's")
-        self._separate(what)
-        for a, (p, g, m, pb) in zip(self.array, self.tensors):
-            a.param, a.grad, a.momentum = p.data_ptr(), g.data_ptr(), m.data_ptr()
-            a.param_bf16 = None if pb is None else pb.data_ptr()
-        self._at = at
+            _require(len(grads) == len(self._grads), what, "as many gradients as tensors")
+        other = "a tensor of another type, shape, stride or device than the plan's"
+        at = list(map(torch.Tensor.data_ptr, self._own))
+        if at != self._own_at:
+            _require(self._layout(self._own) == self._own_layout, what, other)
+            self._separate(what)
+            for a, (p, m, pb) in zip(self.array, self._written):
+                a.param, a.momentum = p.data_ptr(), m.data_ptr()
+                a.param_bf16 = None if pb is None else pb.data_ptr()
+            self._own_at = at
+        # (other tensors may lie where the last ones did)
+        new = grads is not None and any(map(operator.is_not, grads, self._grads))
+        at = list(map(torch.Tensor.data_ptr, grads if new else self._grads))
+        if new or at != self._grads_at:
+            _require(self._layout(grads if new else self._grads) == self._grads_layout, what,
+                     other)
+            words = torch.frombuffer(self.array, dtype=torch.int64).view(len(self.array), -1)
+            words[:, MuonTensor.grad.offset // 8] = torch.tensor(at, dtype=torch.int64)
+            self._grads_at = at
+            if new:
+                self._grads = grads
 
 
 def qlora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool = True,
@@ -945,7 +962,7 @@ def qlora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool =
     _require(adjust in MUON_ADJUST, what, "unknown adjust")
     h = MuonHparams(lr, momentum, weight_decay, _newton_schulz(what, coefficients, steps, eps),
                     int(nesterov), MUON_ADJUST[adjust])
-    if not plan._flat:
+    if not plan._own:
         return
     plan._bind(what, grads)
     with _on(what, plan.ws):
@@ -953,7 +970,7 @@ def qlora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool =
         if s.value not in plan._streams:   # (its memory is not another's while this one runs)
             plan.ws.record_stream(torch.cuda.current_stream())
             plan._streams.add(s.value)
-        _check(lib().qlora_muon_step(ctypes.byref(h), plan.array, len(plan.tensors),
+        _check(lib().qlora_muon_step(ctypes.byref(h), plan.array, len(plan._grads),
                                      _ptr(plan.ws), plan.ws.numel(), s), what)
 
 

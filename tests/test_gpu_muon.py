@@ -295,3 +295,27 @@ def test_small_matrices(count, more):
     again = q.qlora_orthogonalize(us)
     q.qlora_orthogonalize(us, out=us)
     assert all(torch.equal(a, b) for a, b in zip(us, again))
+
+
+def test_new_gradients_where_the_last_ones_lay():
+    """Gradients of another type or shape are refused also at the last ones' addresses,
+    and a refusal leaves the plan as it was."""
+    say("muon gradients at one address")
+    ts = _tensors([(8, 100), (60, 16)])
+    ref = [tuple(x.clone() for x in t) for t in ts]
+    plan = q.MuonPlan(ts)
+    flat = [torch.zeros(4000, device=DEV) for _ in ts]
+    good = [f[:t[1].numel()].view(t[1].shape) for f, t in zip(flat, ts)]
+    for k in range(3):
+        new = [_matrix(90 + 2 * k + i, *t[1].shape) for i, t in enumerate(ts)]
+        for f, g in zip(good, new):
+            f.copy_(g)
+        # (new tensor objects at one place each step)
+        q.qlora_muon_step(plan, 0.1, grads=[x.view(x.shape) for x in good])
+        q.qlora_muon_step([(t[0], g, t[2], t[3]) for t, g in zip(ref, new)], 0.1)
+        for bad in (flat[0].view(BF)[:800].view(8, 100), flat[0][:1600].view(8, 200)[:, :100]):
+            with pytest.raises(q.QloraError):
+                q.qlora_muon_step(plan, 0.1, grads=[bad, good[1]])
+        for a, b in zip(ts, ref):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
+    assert [g.data_ptr() for _, g, _, _ in plan.tensors] == [g.data_ptr() for g in good]
