@@ -31,8 +31,9 @@
 // reaches 5.2; polynomials 14 us, ten launches of the table 27 us.  From a rank of 64
 // the f64 matrix cores join in (70 TF: 2 s flops a value each for the product and Q U),
 // and the polynomial of a few matrices, a chain of products on a CU each, weighs more:
-// two 65B layers of rank 64 take 70 us for gram, 7.5 us for the sum, 34 us for the
-// polynomial and 80 us for apply.
+// two 65B layers of rank 64 take 64 us for gram, 6 us for the sum, 31 us for the
+// polynomial and 76 us for apply (strips of several chunks to a workgroup, loading the
+// next chunk under a product, took 105: fewer waves in flight).
 #include "muon.h"
 
 #include <type_traits>
@@ -526,27 +527,29 @@ __global__ __launch_bounds__(64 * poly_waves(NT)) void k_muon_poly(MuonHyper h, 
   polynomial<NT>(h, l, from, s.q + (size_t)t.q * 256, lane, wv);
 }
 
-// Rank 33 to 64: all matrices fit LDS, so a product is taken by its tiles on and above
-// the diagonal alone (three, three, two and two a wave in place of four each) and
-// written to both sides, which also keeps every matrix exactly symmetric: operands are
-// read along rows, 512 bytes a read.  34 us in place of 43.  (The waves meet at
-// barriers in code of their own, the same number in each.)
-constexpr int kSide = 64, kPitch = kSide + 2;
+// Rank 33 to 64: all matrices fit LDS, so a product is taken by its ten tiles on and above
+// the diagonal alone and written to both sides, which also keeps every matrix exactly
+// symmetric: operands are read along rows, 512 bytes a read.  Eight waves, two a SIMD
+// (which has three, three, two and two tiles), so that one's reads, polynomial and
+// stores run beside the other's products: 31 us (33 with four waves; 43 with whole
+// matrices; the products of the fullest SIMD alone are 22).  G P and P Q in one loop,
+// with their left factor read once, took 32.  (The waves meet at barriers in code of
+// their own, the same number in each.)
+constexpr int kSide = 64, kPitch = kSide + 2, kPoly64 = 512;
 struct Tri {
   int i, j;
 };
 template <int WV>
 struct Mine {
-  static constexpr Tri t[3] = {
-      WV == 0 ? Tri{0, 0} : WV == 1 ? Tri{1, 1} : WV == 2 ? Tri{2, 2} : Tri{3, 3},
-      WV == 0 ? Tri{0, 1} : WV == 1 ? Tri{1, 2} : WV == 2 ? Tri{2, 3} : Tri{0, 3},
-      WV == 0 ? Tri{0, 2} : Tri{1, 3}};
-  static constexpr int n = WV < 2 ? 3 : 2;
+  static constexpr Tri all[8][2] = {{{0, 0}, {0, 1}}, {{1, 1}, {1, 2}}, {{2, 2}}, {{3, 3}},
+                                    {{0, 2}},         {{1, 3}},         {{2, 3}}, {{0, 3}}};
+  static constexpr Tri t[2] = {all[WV][0], all[WV][1]};
+  static constexpr int n = WV < 2 ? 2 : 1;
 };
 template <int WV>
 struct Tri3 {
   using M = Mine<WV>;
-  f64x4_t c[3];
+  f64x4_t c[M::n];
   // a b, both symmetric and commuting
   __device__ __forceinline__ void product(const double* a, const double* b, int lane) {
     const int at = (lane >> 4) * kPitch + (lane & 15);
@@ -609,7 +612,7 @@ __device__ __forceinline__ void poly64(const MuonHyper& h, double* g, double* p,
     }
   }
 }
-__global__ __launch_bounds__(kThreads) void k_muon_poly64(MuonHyper h, MuonScratch s) {
+__global__ __launch_bounds__(kPoly64) void k_muon_poly64(MuonHyper h, MuonScratch s) {
   __shared__ __attribute__((aligned(16))) double x[4][kSide * kPitch];
   const MuonTensor t = s.t[blockIdx.x];
   if (view(t).sp != kSide) return;
@@ -622,7 +625,7 @@ __global__ __launch_bounds__(kThreads) void k_muon_poly64(MuonHyper h, MuonScrat
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = i; j < 4; ++j, ++k) {
-      if ((k & 3) != wv) continue;
+      if ((k & 7) != wv) continue;
       const f64x4_t c = from[k * 64];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -638,20 +641,25 @@ __global__ __launch_bounds__(kThreads) void k_muon_poly64(MuonHyper h, MuonScrat
   const double norm = fmax(sqrt(tr), h.eps), inv = 1.0 / norm;
   // (fmax drops a NaN: then every product shows it)
   __syncthreads();
-  for (int e = threadIdx.x; e < kSide * kSide; e += kThreads)
+  for (int e = threadIdx.x; e < kSide * kSide; e += kPoly64)
     g[(e >> 6) * kPitch + (e & 63)] *= inv * inv;
   __syncthreads();
   switch (wv) {
     case 0: poly64<0>(h, x[0], x[1], x[2], x[3], lane); break;
     case 1: poly64<1>(h, x[0], x[1], x[2], x[3], lane); break;
     case 2: poly64<2>(h, x[0], x[1], x[2], x[3], lane); break;
-    default: poly64<3>(h, x[0], x[1], x[2], x[3], lane); break;
+    case 3: poly64<3>(h, x[0], x[1], x[2], x[3], lane); break;
+    case 4: poly64<4>(h, x[0], x[1], x[2], x[3], lane); break;
+    case 5: poly64<5>(h, x[0], x[1], x[2], x[3], lane); break;
+    case 6: poly64<6>(h, x[0], x[1], x[2], x[3], lane); break;
+    default: poly64<7>(h, x[0], x[1], x[2], x[3], lane); break;
   }
-  // as k_muon_apply's left operands, a line a load (Q symmetric: its row tile wv)
-  double* out = s.q + (size_t)t.q * 256 + wv * 256 * 4 + lane;
+  // as k_muon_apply's left operands, a line a load (Q symmetric: half its row tile wv / 2)
+  double* out = s.q + (size_t)t.q * 256 + wv * 256 * 2 + lane;
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-    out[e * 64] = x[3][(4 * e + (lane >> 4)) * kPitch + 16 * wv + (lane & 15)] * inv;
+  for (int e = 0; e < 8; ++e)
+    out[e * 64] = x[3][(4 * (8 * (wv & 1) + e) + (lane >> 4)) * kPitch + 16 * (wv >> 1) +
+                       (lane & 15)] * inv;
 }
 
 // --------------------------------------------------------------------- apply
@@ -908,7 +916,7 @@ hipError_t launch_muon_poly(int count, int sp, const MuonHyper& h, const MuonScr
     case 32: return launch_kernel(k_muon_poly<2>, grid, dim3(64 * poly_waves(2)), st, h, s);
     case 64:
       e = launch_kernel(k_muon_sum<4>, dim3(10, (unsigned)count), dim3(kThreads), st, s);
-      return e != hipSuccess ? e : launch_kernel(k_muon_poly64, grid, dim3(kThreads), st, h, s);
+      return e != hipSuccess ? e : launch_kernel(k_muon_poly64, grid, dim3(kPoly64), st, h, s);
     default:
       e = launch_kernel(k_muon_sum<8>, dim3(36, (unsigned)count), dim3(kThreads), st, s);
       return e != hipSuccess ? e : launch_kernel(k_muon_poly<8>, grid, dim3(64 * poly_waves(8)), st, h, s);
