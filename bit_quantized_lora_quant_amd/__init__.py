@@ -9,7 +9,6 @@ every call raises.
 import contextlib
 import ctypes
 import functools
-import operator
 import os
 from typing import NamedTuple, Optional
 
@@ -872,8 +871,9 @@ class MuonPlan:
     once: a list of (param, grad, momentum, param_bf16 or None), matrices whose
     shorter side is <= 128, rows of any stride; param and momentum float32, grad
     float32 or bf16; no tensor but a grad twice.  The plan holds the tensors and
-    finds their memory anew each step; gradients that are other tensors every time
-    go to the step itself.  Steps that share a plan must be ordered on one stream,
+    finds their memory anew each step, and refuses one whose type, shape or stride
+    is no longer what it was; gradients that are other tensors every time go to the
+    step itself.  Steps that share a plan must be ordered on one stream,
     and a graph that captured one needs the plan kept."""
 
     def __init__(self, tensors):
@@ -898,6 +898,7 @@ class MuonPlan:
         self._grads = [t[1] for t in tensors]
         self._own_at = self._grads_at = None
         self._own_layout, self._grads_layout = self._layout(self._own), self._layout(self._grads)
+        self._own_devices, self._grads_devices = self._devices(self._own), self._devices(self._grads)
         self._separate(what)
         self.ws, self._streams = None, set()
         if tensors:
@@ -915,39 +916,44 @@ class MuonPlan:
 
     @staticmethod
     def _layout(tensors):
-        # (whole lists at a time: a step whose gradients are new is as long as this)
+        # (whole lists at a time: a step's host time is as long as this)
         return ([x.dtype for x in tensors], [x.shape for x in tensors],
-                list(map(torch.Tensor.stride, tensors)),
-                list(map(torch.Tensor.get_device, tensors)))
+                list(map(torch.Tensor.stride, tensors)))
+
+    @staticmethod
+    def _devices(tensors):
+        return list(map(torch.Tensor.get_device, tensors))
 
     def _separate(self, what):
         _distinct(what, "a tensor to be written", self._own)
 
     def _bind(self, what, grads):
-        """The tensors' addresses as they are now."""
-        if grads is not None:
+        """The tensors' addresses as they are now.  Their layouts are looked at every step:
+        a tensor that was laid out otherwise in its place (`.data` of another view or type)
+        has the address it had."""
+        if grads is None:
+            grads = self._grads
+        else:
             grads = list(grads)
             _require(len(grads) == len(self._grads), what, "as many gradients as tensors")
         other = "a tensor of another type, shape, stride or device than the plan's"
+        _require(self._layout(self._own) == self._own_layout, what, other)
         at = list(map(torch.Tensor.data_ptr, self._own))
         if at != self._own_at:
-            _require(self._layout(self._own) == self._own_layout, what, other)
+            _require(self._devices(self._own) == self._own_devices, what, other)
             self._separate(what)
             for a, (p, m, pb) in zip(self.array, self._written):
                 a.param, a.momentum = p.data_ptr(), m.data_ptr()
                 a.param_bf16 = None if pb is None else pb.data_ptr()
             self._own_at = at
-        # (other tensors may lie where the last ones did)
-        new = grads is not None and any(map(operator.is_not, grads, self._grads))
-        at = list(map(torch.Tensor.data_ptr, grads if new else self._grads))
-        if new or at != self._grads_at:
-            _require(self._layout(grads if new else self._grads) == self._grads_layout, what,
-                     other)
+        _require(self._layout(grads) == self._grads_layout, what, other)
+        at = list(map(torch.Tensor.data_ptr, grads))
+        if at != self._grads_at:
+            _require(self._devices(grads) == self._grads_devices, what, other)
             words = torch.frombuffer(self.array, dtype=torch.int64).view(len(self.array), -1)
             words[:, MuonTensor.grad.offset // 8] = torch.tensor(at, dtype=torch.int64)
             self._grads_at = at
-            if new:
-                self._grads = grads
+        self._grads = grads
 
 
 def qlora_muon_step(tensors, lr: float, momentum: float = 0.95, nesterov: bool = True,
