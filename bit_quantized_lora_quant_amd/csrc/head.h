@@ -72,7 +72,7 @@ struct HeadPanel {
   uint32_t* shift;     // [vocab tiles * 2][rows] R - M, in both halves as bf16's exponent
   int splits;          // slices of dh in a full panel
   int want_last;       // r.last is needed (dW)
-  uint16_t* e;         // [rows][head_cols(vocab)] exponentials (fp16), then dz (bf16)
+  uint16_t* e;         // [rows][head_cols(vocab)] exponents in 16 bits, then dz (bf16)
 };
 // Columns of a panel's row.
 __host__ __device__ inline int64_t head_cols(int64_t vocab) { return ceil_div(vocab, 256) * 256; }
@@ -80,8 +80,8 @@ int head_dh_splits(int64_t rows, int dim, int64_t vocab, int tile);
 // Rows of tokens per workgroup tile (64, 128 or 256) of a call.
 int head_tile(int64_t rows, int64_t vocab);
 
-// HEAD_STATS: part; HEAD_EXP: part and e; HEAD_DZ: dz from r.stat and r.w;
-// HEAD_POW: as HEAD_EXP with e in bf16, which dh takes as it is
+// HEAD_STATS: part; HEAD_EXP: part and e's exponents; HEAD_DZ: dz from r.stat and r.w;
+// HEAD_POW: as HEAD_EXP with powers in bf16, which dh takes as they are
 enum { HEAD_STATS = 0, HEAD_EXP = 1, HEAD_DZ = 2, HEAD_POW = 3 };
 // part: head_logits_floats floats (of partial logits, where the inner index is cut)
 size_t head_logits_floats(int64_t rows, int dim, int64_t vocab, int tile);

@@ -16,10 +16,11 @@
 // A gradient in the same call has the slices' values written in 16 bits.  dh alone
 // takes them as bf16, the matrix cores' type: its tile loop lowers their exponents
 // by R - M to the row's R, and the row's factor and its target's term come in float32
-// at the end, so they are written once and read once.  With dW they are fp16 (11 bits
-// below the slice's largest) and become dz = bf16 in place, which both products
-// read.  Either way a value is rounded to bf16 once.  A backward call from stored
-// statistics multiplies the logits again and writes dz at once.
+// at the end, so they are written once and read once.  With dW their exponents are
+// written (pack_exponents) and become dz = bf16 in place, which both products read.
+// Either way a value is rounded to bf16 once, and is as exact beside a far likelier
+// neighbour as alone.  A backward call from stored statistics multiplies the logits
+// again and writes dz at once.
 //
 // All three products share one tile loop, bound by the matrix cores' power: 256
 // values of the output's contiguous index (MFMA rows: a lane then holds eight
@@ -46,10 +47,27 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
-typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2eLo = 1.925963033500e-08f;   // log2 e - kLog2e
+
+// 2^t, t <= 0, kept in 16 bits: t as a whole number of steps of 90.5 / 65535, rounded to
+// nearest, so 2^t is off by ln 2 / 2 steps, 2^-11 of itself, all the way down to 2^-90
+// (63 nats); the last code is 0.  fp16 is as exact down to 2^-14 only and holds nothing
+// below 2^-25: vocabulary entries 10 to 17 nats under the likeliest of their slice would
+// lose their gradient, rows of dW that the norm of all does not show.  It costs what fp16
+// does (2048 rows' loss, dh and dW at V = 128256, D = 4096: 5465 us, with fp16 5485).
+// (A NaN leaves its whole row's factor NaN, whatever becomes of it here.)
+constexpr float kExponents = 90.5f;
+__device__ __forceinline__ uint32_t pack_exponents(float t, float u) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(t * (-1.f / kExponents),
+                                                                      u * (-1.f / kExponents)));
+}
+// 2^(by + t) of a code
+__device__ __forceinline__ float unpack_power(uint32_t code, float by) {
+  const float e = __builtin_fmaf((float)code, -kExponents / 65535.f, by);
+  return code == 65535u ? 0.f : __builtin_amdgcn_exp2f(e);
+}
 
 __device__ __forceinline__ float exp_diff(float z, float m) {
   return __builtin_amdgcn_exp2f((z - m) * kLog2e);
@@ -653,8 +671,9 @@ void k_head_logits(HeadPanel p, int splits, float* part) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      z[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i] - from, kLog2e, off));
-      s += z[i];
+      const float t = __builtin_fmaf(z[i] - from, kLog2e, off), e = __builtin_amdgcn_exp2f(t);
+      z[i] = MODE == HEAD_EXP ? t : e;
+      s += e;
     }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
@@ -667,8 +686,7 @@ void k_head_logits(HeadPanel p, int splits, float* part) {
         for (int k = 0; k < 4; ++k)
           o[k] = MODE == HEAD_POW
                      ? pack_bf16x2(z[8 * i + 2 * k], z[8 * i + 2 * k + 1])
-                     : __builtin_bit_cast(uint32_t, half2_t{(_Float16)z[8 * i + 2 * k],
-                                                            (_Float16)z[8 * i + 2 * k + 1]});
+                     : pack_exponents(z[8 * i + 2 * k], z[8 * i + 2 * k + 1]);
         *reinterpret_cast<uint4*>(out + 32 * i) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
@@ -732,16 +750,18 @@ __global__ __launch_bounds__(kThreads) void k_head_slices(HeadPanel p, int TN, i
 #pragma unroll
   for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
   const float M = slice_exponent(m), off = slice_offset(m, M), at = m == -INFINITY ? 0.f : m;
+  float t[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    z[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e] - at, kLog2e, off));
+  for (int e = 0; e < 2; ++e) {
+    t[e] = __builtin_fmaf(z[e] - at, kLog2e, off);
+    z[e] = __builtin_amdgcn_exp2f(t[e]);
+  }
   float s = z[0] + z[1];
 #pragma unroll
   for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
   if (lane == 0) p.part[(int64_t)sl * p.rows + row] = HeadPart{M, s};
   if (MODE == HEAD_POW) *out = pack_bf16x2(z[0], z[1]);
-  if (MODE == HEAD_EXP)
-    *out = __builtin_bit_cast(uint32_t, half2_t{(_Float16)z[0], (_Float16)z[1]});
+  if (MODE == HEAD_EXP) *out = pack_exponents(t[0], t[1]);
 }
 
 // ---------------------------------------------------------------------- join
@@ -849,8 +869,8 @@ __global__ __launch_bounds__(1024) void k_head_loss(const int32_t* n, const doub
 
 // ------------------------------------------------------------------------ dz
 // In place, a thread 8 columns of 8 rows: HBM-bound (2048 x 128256: 224 us, 1.05 GB at
-// 4.7 TB/s).  dz = f 2^(M - R) e, the target's
-// c; zeros in the rows up to a whole step of dW.
+// 4.7 TB/s).  dz = f 2^(M - R + t), the target's c; zeros in the rows up to a whole step
+// of dW.
 constexpr int kDzRows = 8;
 __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
   const int n = panel_rows(p);
@@ -870,13 +890,13 @@ __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
       const int64_t q = p.row0 + r0 + r;
       const HeadScale sc = p.r.scale[q];
       const float m = p.part[(c >> 7) * p.rows + r0 + r].m;
-      const float f = m == -INFINITY ? 0.f : sc.f * __builtin_amdgcn_exp2f(m - sc.r);
+      const float f = m == -INFINITY ? 0.f : sc.f, by = m == -INFINITY ? 0.f : m - sc.r;
       float d[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const half2_t h = __builtin_bit_cast(half2_t, (&e[r].x)[k]);
-        d[2 * k] = f * (float)h[0];
-        d[2 * k + 1] = f * (float)h[1];
+        const uint32_t two = (&e[r].x)[k];
+        d[2 * k] = f * unpack_power(two & 0xffffu, by);
+        d[2 * k + 1] = f * unpack_power(two >> 16, by);
       }
       const int64_t rel = p.r.y[q] - c;
       if (rel >= 0 && rel < 8) {

@@ -726,7 +726,7 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
  * head's weight W [vocab, dim] (both bf16), z_t = W h_t in float32.  The logits
  * of a step are its largest tensor; here they are never written.  At most
  * 2^29 row x vocabulary elements (at least 256 rows) are in work at a time,
- * and of those a call that returns gradients keeps 16-bit exponentials.
+ * and of those a call that returns gradients keeps 16 bits each.
  *
  * Rows, labels and their refusals follow qlora_logits: a negative label means
  * no target (logp 0, gradient row zero; whatever the hidden row holds, NaN
@@ -735,7 +735,9 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
  * The target's logit is a float64 sum.  Sums over the rest of the vocabulary are
  * float32 over 128 entries and float64 between those and after the logarithm.  dz
  * is rounded to bf16 (the matrix cores' type) once before the products that give
- * dh and dW, whose sums are float32 and rounded once to bf16; what the rounding
+ * dh and dW, whose sums are float32 and rounded once to bf16 (cross entropy with
+ * dweight forms it from powers kept to 2^-11 of themselves, and to 0 below 2^-90 of
+ * the largest of their 128 entries); what the rounding
  * leaves of the targets' dz, the largest of their rows, is added in float32 (to dW
  * for labels of up to 256 rows at a time).  Results are identical run to run, but
  * dh is formed otherwise beside dW than alone: within the same bounds, not the same

@@ -1,0 +1,61 @@
+"""Every row of the head's weight gradient for itself, where a slice of the vocabulary has
+one entry that is far likelier than its neighbours in every row: their gradients are
+small, and as exact as any other."""
+import pytest
+import torch
+
+from gpu_common import DEV, say
+from test_gpu_head import BF, _exact, _inputs, _logp_tol
+
+import bit_quantized_lora_quant_amd as q
+
+pytestmark = pytest.mark.gpu
+
+
+def _dominated(seed, T, D, V, margin, every=128):
+    """One entry of each `every` about `margin` nats above the others; never a target."""
+    h, W, y = _inputs(seed, T, D, V, ignored=0.2, sharp=0.2)
+    g = torch.Generator().manual_seed(seed + 1)
+    u = torch.randn(D, generator=g).to(DEV)
+    u = u / u.norm()
+    likely = torch.arange(every // 3, V, every, device=DEV)
+    Wf, hf = W.float(), h.float()
+    Wf[likely] += margin / 4 * u
+    Wf -= (Wf @ u)[:, None] * u * (~torch.isin(torch.arange(V, device=DEV), likely))[:, None]
+    hf += (4 - hf @ u)[:, None] * u
+    y = torch.where(torch.isin(y, likely), y + 1, y)
+    return hf.to(BF), Wf.to(BF), y
+
+
+def _check_rows(got, d, h, ref, slack):
+    """A value of dz is off by 2^-11 (the value in 16 bits), 2^-8 (bf16) and what its float32
+    logit leaves, all relative to itself however small it is; products with h are exact in
+    float32 and their sum off by 2^-24 a term; then the output's rounding."""
+    T = d.shape[0]
+    bound = (d.abs().T @ h.abs()) * (2.0 ** -8 + 2.0 ** -11 + slack + T * 2.0 ** -24)
+    bound = bound + ref.abs() * 2.0 ** -8 + 2.0 ** -126
+    err = (got.double() - ref).abs()
+    assert bool((err <= bound).all()), (float((err / bound).max()),
+                                        int((err > bound).any(1).sum()), "rows")
+
+
+@pytest.mark.parametrize("T,D,V", [(300, 128, 1000), (256, 1024, 1000), (40, 64, 9000),
+                                   (2300, 128, 20001)])
+@pytest.mark.parametrize("margin", [12.0, 18.0, 24.0, 40.0])
+def test_neighbours_of_a_likely_entry(T, D, V, margin):
+    say("one likely entry a slice, T=%d D=%d V=%d margin=%g" % (T, D, V, margin))
+    h, W, y = _dominated(T + V, T, D, V, margin)
+    n = int((y >= 0).sum())
+    w = torch.full((T,), -1.0 / n, device=DEV)
+    _, d, dh_ref, dw_ref = _exact(h, W, y, w)
+    masked = torch.where((y >= 0)[:, None], h.double(), 0.0)
+    slack = _logp_tol(D, V, 2 * margin + 30)
+    o = q.qlora_head_cross_entropy(h, W, y, return_grad=True, need_dweight=True)
+    _check_rows(o.dweight, d, masked, dw_ref, slack)
+    only = q.qlora_head_cross_entropy(h, W, y, need_dweight=True)
+    assert torch.equal(only.dweight, o.dweight)
+    _, stats = q.qlora_head_logprobs(h, W, y, return_stats=True)
+    dh, dw = q.qlora_head_logprobs_bwd(h, W, y, stats, w, need_dweight=True)
+    _check_rows(dw, d, masked, dw_ref, slack)
+    for x in (o.dhidden, dh):
+        assert float((x.double() - dh_ref).norm() / dh_ref.norm()) < 4e-3
