@@ -1042,16 +1042,18 @@ __global__ __launch_bounds__(kThreads) void k_head_dh_sum(HeadPanel p, int TN, i
 }
 
 // ------------------------------------------------------------------------ dW
-// A vocabulary row's gradient is often one row's target and little else, so its dz's
+// A vocabulary row's gradient is often its targets' and little else, so its dz's
 // rounding to bf16 would be as large as the output's own (2.6e-3 of dW's norm against
-// 1.7e-3).  What it leaves out is added in float32.  A workgroup per packed row, at
-// work where that row is its target's last: it looks through the panel's labels and
-// adds the rows in order.  Of more than 256 rows the roundings, which have no bias,
-// add up to less than a sixteenth of one's: there nothing is added.
+// 1.7e-3), and targets of one weight and small p all round to the same side (of 1020
+// rows' mean by 2^-8).  What it leaves out is added in float32, rows in order.  A
+// workgroup per packed row and 2048 columns, at work where that row is its target's
+// last: it looks through the panel's labels for the others, and adds what it has found
+// where its list has no room for the next 256.  (A chain of loads for a label of very
+// many rows: 1000 and 2048 rows of one at D = 4096 take 100 and 200 us.)
 __device__ __forceinline__ int64_t rest_slot(const HeadPanel& p, int64_t v, int64_t q) {
   return p.rows < p.vocab ? q - p.row0 : v;
 }
-constexpr int kFound = 256;
+constexpr int kFound = 512;
 __global__ __launch_bounds__(kThreads) void k_head_rest(HeadPanel p, float* rest) {
   __shared__ int found[kFound];
   __shared__ float off[kFound];
@@ -1061,8 +1063,10 @@ __global__ __launch_bounds__(kThreads) void k_head_rest(HeadPanel p, float* rest
   if (self >= n) return;
   const int y = p.r.y[p.row0 + self];
   if (y < 0 || p.r.last[y] != p.row0 + self) return;
+  const int col = (int)(blockIdx.y * kThreads + tid) * 8;
+  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   int have = 0;
-  for (int t0 = 0; t0 <= self && have <= kFound; t0 += kThreads) {
+  for (int t0 = 0; t0 <= self; t0 += kThreads) {
     const int t = t0 + tid;
     const bool hit = t <= self && p.r.y[p.row0 + t] == y;
     const uint64_t m = __builtin_amdgcn_ballot_w64(hit);
@@ -1070,30 +1074,32 @@ __global__ __launch_bounds__(kThreads) void k_head_rest(HeadPanel p, float* rest
     __syncthreads();
     int at = have + __popcll(m & ((1ull << lane) - 1));
     for (int w = 0; w < wv; ++w) at += wave_count[w];
-    if (hit && at < kFound) {
+    if (hit) {
       const float c = p.r.scale[p.row0 + t].c;
       found[at] = t;
       off[at] = c - bf16_to_f32((uint16_t)pack_bf16x2(c, 0.f));
     }
     have += wave_count[0] + wave_count[1] + wave_count[2] + wave_count[3];
     __syncthreads();
-  }
-  if (have > kFound) have = 0;
-  float* out = rest + rest_slot(p, y, p.row0 + self) * p.dim;
-  for (int col = 8 * tid; col < p.dim; col += kThreads * 8) {
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int k = 0; k < have; ++k) {
-      const uint4 h =
-          *reinterpret_cast<const uint4*>(p.r.h + (p.row0 + found[k]) * p.dim + col);
+    if (have + kThreads <= kFound && t0 + kThreads <= self) continue;
+    if (col < p.dim) {
+#pragma unroll 8
+      for (int k = 0; k < have; ++k) {
+        const uint4 h =
+            *reinterpret_cast<const uint4*>(p.r.h + (p.row0 + found[k]) * p.dim + col);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[e] += off[k] * bf16_to_f32((uint16_t)((&h.x)[e >> 1] >> (16 * (e & 1))));
+        for (int e = 0; e < 8; ++e)
+          o[e] += off[k] * bf16_to_f32((uint16_t)((&h.x)[e >> 1] >> (16 * (e & 1))));
+      }
     }
-    float4* to = reinterpret_cast<float4*>(out + col);
-    to[0] = make_float4(o[0], o[1], o[2], o[3]);
-    to[1] = make_float4(o[4], o[5], o[6], o[7]);
+    have = 0;
+    __syncthreads();
   }
+  if (col >= p.dim) return;
+  float4* to =
+      reinterpret_cast<float4*>(rest + rest_slot(p, y, p.row0 + self) * p.dim + col);
+  to[0] = make_float4(o[0], o[1], o[2], o[3]);
+  to[1] = make_float4(o[4], o[5], o[6], o[7]);
 }
 
 // A = h (transposed by the reads), B = dz (likewise); inner index the rows.  Bound by
@@ -1364,7 +1370,8 @@ hipError_t launch_head_dh(const HeadPanel& p, int tile, int pow, float* part, ui
 }
 
 hipError_t launch_head_rest(const HeadPanel& p, float* rest, hipStream_t s) {
-  return launch_kernel(k_head_rest, dim3((unsigned)p.rows), dim3(kThreads), s, p, rest);
+  const dim3 grid((unsigned)p.rows, (unsigned)ceil_div(p.dim, kThreads * 8));
+  return launch_kernel(k_head_rest, grid, dim3(kThreads), s, p, rest);
 }
 
 size_t head_dw_floats(int64_t rows, int dim, int64_t vocab) {

@@ -737,10 +737,9 @@ qlora_status qlora_policy_loss(const qlora_logits* z, int32_t sequences,
  * is rounded to bf16 (the matrix cores' type) once before the products that give
  * dh and dW, whose sums are float32 and rounded once to bf16 (cross entropy with
  * dweight forms it from powers kept to 2^-11 of themselves, and to 0 below 2^-90 of
- * the largest of their 128 entries); what the rounding
- * leaves of the targets' dz, the largest of their rows, is added in float32 (to dW
- * for labels of up to 256 rows at a time).  Results are identical run to run, but
- * dh is formed otherwise beside dW than alone: within the same bounds, not the same
+ * the largest of their 128 entries); what the rounding leaves of the targets' dz, the
+ * largest of their rows, is added in float32.  Results are identical run to run, but dh
+ * is formed otherwise beside dW than alone: within the same bounds, not the same
  * bits. */
 typedef struct {
   const qlora_bf16* hidden;  /* device, [rows] x ld_hidden; may be NULL when rows == 0 */

@@ -59,3 +59,61 @@ def test_neighbours_of_a_likely_entry(T, D, V, margin):
     _check_rows(dw, d, masked, dw_ref, slack)
     for x in (o.dhidden, dh):
         assert float((x.double() - dh_ref).norm() / dh_ref.norm()) < 4e-3
+
+
+def _row_of_dw(h, W, y, w, v):
+    """Row v of dW in 64 bits, and the parts of its sum: |dz h| over its targets' rows and
+    over the others."""
+    ref, own, other = 0, 0, 0
+    for i in range(0, len(y), 512):
+        s = slice(i, i + 512)
+        _, d, _, _ = _exact(h[s], W, y[s], w[s])
+        hd = torch.where((y[s] >= 0)[:, None], h[s].double(), 0.0)
+        ref = ref + d[:, v] @ hd
+        mine = (y[s] == v).double()
+        own = own + (mine * d[:, v].abs()) @ hd.abs()
+        other = other + ((1 - mine) * d[:, v].abs()) @ hd.abs()
+        del d
+    return ref, own, other
+
+
+@pytest.mark.parametrize("times", [1, 256, 257, 511, 512, 513, 769, 1020])
+@pytest.mark.parametrize("V", [700, 9000])
+def test_targets_that_round_alike(times, V):
+    """The mean over 1020 targets: 1 / 1020 lies halfway between two bf16 values, and with
+    p near 0 every target's dz is off to the same side by 2^-8.  What the roundings
+    leave is added however many they are, so that the row is off by its own rounding."""
+    say("%d targets that round alike, V=%d" % (times, V))
+    T, D = 1020, 192
+    h, W, y = _inputs(times, T, D, V, ignored=0.0, sharp=0.0)
+    h = (h.float() + torch.linspace(-3, 3, D, device=DEV)).to(BF)
+    W[7] = 0
+    y = torch.where(y == 7, 8, y)
+    y[torch.randperm(T, generator=torch.Generator().manual_seed(1))[:times].to(DEV)] = 7
+    w = torch.full((T,), -1.0 / T, device=DEV)
+    ref, own, other = _row_of_dw(h, W, y, w, 7)
+    # (own: float32 sums of exact products and of what is left of each; statistics)
+    bound = ref.abs() * 2.0 ** -8 + own * (T * 2.0 ** -23 + _logp_tol(D, V)) + \
+        other * (2.0 ** -8 + 2.0 ** -11 + T * 2.0 ** -24 + _logp_tol(D, V))
+    o = q.qlora_head_cross_entropy(h, W, y, need_dweight=True)
+    _, stats = q.qlora_head_logprobs(h, W, y, return_stats=True)
+    dw = q.qlora_head_logprobs_bwd(h, W, y, stats, w, need_dhidden=False, need_dweight=True)[1]
+    for name, got in (("cross entropy", o.dweight), ("backward", dw)):
+        err = (got[7].double() - ref).abs()
+        assert bool((err <= bound).all()), (name, float((err / bound).max()))
+
+
+def test_targets_that_round_alike_over_panels():
+    say("3000 targets that round alike in two panels")
+    T, D, V = 4080, 64, 262144
+    h, W, y = _inputs(5, T, D, V, ignored=0.0, sharp=0.0)
+    h = (h.float() + torch.linspace(-3, 3, D, device=DEV)).to(BF)
+    W[7] = 0
+    y = torch.where(y == 7, 8, y)
+    y[torch.randperm(T, generator=torch.Generator().manual_seed(1))[:3000].to(DEV)] = 7
+    ref, own, other = _row_of_dw(h, W, y, torch.full((T,), -1.0 / T, device=DEV), 7)
+    bound = ref.abs() * 2.0 ** -8 + own * (T * 2.0 ** -23 + _logp_tol(D, V)) + \
+        other * (2.0 ** -8 + 2.0 ** -11 + T * 2.0 ** -24 + _logp_tol(D, V))
+    o = q.qlora_head_cross_entropy(h, W, y, need_dweight=True)
+    err = (o.dweight[7].double() - ref).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
