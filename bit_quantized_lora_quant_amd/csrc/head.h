@@ -12,15 +12,15 @@ namespace qnf4 {
 struct HeadStat {
   float lse, rest;
 };
-// A slice's largest exponent M = ceil(max z log2 e), a whole number, and sum of
+// A slice's largest logit m and, with M = ceil(m log2 e), a whole number, its sum of
 // 2^(z log2 e - M), the target left out of both.
 struct HeadPart {
   float m, s;
 };
-// A row's gradient: R, the largest M of its slices; f and c with
+// A row's gradient: the largest m of its slices, whose M is R; f and c with
 // dz_v = f 2^(z_v log2 e - R), at the target c = w (1 - p).  (The backward: c alone.)
 struct HeadScale {
-  float r, f, c;
+  float m, f, c;
 };
 
 // Rows with a target, packed: hidden [up to a tile's rows][D], their source rows and

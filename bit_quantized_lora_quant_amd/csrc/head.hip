@@ -7,8 +7,9 @@
 // Rows with a target are packed first, so prompts and padding cost nothing and
 // whatever they hold reaches no sum.  The packed rows go through in panels of at
 // most 2^29 row x vocabulary elements.  The product's tiles leave, per row and slice
-// of 128 vocabulary entries, a whole exponent M = ceil(max z log2 e) and the sum of
-// 2^(z log2 e - M).  The target is left out of its slice: its logit is a float64 dot
+// of 128 vocabulary entries, the largest logit m and, with the whole exponent
+// M = ceil(m log2 e), the sum of 2^(z log2 e - M).  The target is left out of its
+// slice: its logit is a float64 dot
 // product of the packing, and 1 - p of a nearly certain target is a sum of what is
 // left, not 1 minus something rounded.  The slices are joined in float64, by powers
 // of two only.
@@ -33,6 +34,7 @@
 // 6.6 to 6.8 ms, both products at 1270 to 1310 TF.
 #include "head.h"
 
+#include <cfloat>
 #include <type_traits>
 
 namespace qnf4 {
@@ -72,12 +74,23 @@ __device__ __forceinline__ float unpack_power(uint32_t code, float by) {
 __device__ __forceinline__ float exp_diff(float z, float m) {
   return __builtin_amdgcn_exp2f((z - m) * kLog2e);
 }
-// A slice's whole exponent for its largest logit m, and what 2^(z log2 e - M) has beside
-// (z - m) log2 e: m log2 e - M, to float32's last bit while M is exact, and never
-// out of [-1, 0] for logits beyond that.
-__device__ __forceinline__ float slice_exponent(float m) { return ceilf(m * kLog2e); }
+// A slice's whole exponent for its largest logit m (finite also where m log2 e is not), and
+// what 2^(z log2 e - M) has beside (z - m) log2 e: m log2 e - M, to float32's last bit
+// while M is exact, and never out of [-1, 0] for logits beyond that (2^23).
+__device__ __forceinline__ float slice_exponent(float m) {
+  return fminf(fmaxf(ceilf(m * kLog2e), -FLT_MAX), FLT_MAX);
+}
 __device__ __forceinline__ float slice_offset(float m, float M) {
   return fminf(fmaxf(__builtin_fmaf(m, kLog2eLo, __builtin_fmaf(m, kLog2e, -M)), -1.f), 0.f);
+}
+
+// A slice's exponent relative to that of the row's largest logit, a whole number from -2000
+// to 0.  (Where exponents are no longer exact their difference may be off by more than
+// the logits': never above these.  -2000 too for a slice without entries or of NaN,
+// whose sum shows it.)
+__device__ __forceinline__ float relative_exponent(float slice, float row) {
+  const float d = slice_exponent(slice) - slice_exponent(row);
+  return fmaxf(fminf(d, ceilf((slice - row) * kLog2e) + 1.f), -2000.f);
 }
 
 // ----------------------------------------------------------------- slices of dh
@@ -677,7 +690,7 @@ void k_head_logits(HeadPanel p, int splits, float* part) {
     }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (valid && g == 0) p.part[(2 * tv + wm) * p.rows + row] = HeadPart{M, s};
+    if (valid && g == 0) p.part[(2 * tv + wm) * p.rows + row] = HeadPart{m, s};
     if ((MODE == HEAD_EXP || MODE == HEAD_POW) && valid) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -759,7 +772,7 @@ __global__ __launch_bounds__(kThreads) void k_head_slices(HeadPanel p, int TN, i
   float s = z[0] + z[1];
 #pragma unroll
   for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
-  if (lane == 0) p.part[(int64_t)sl * p.rows + row] = HeadPart{M, s};
+  if (lane == 0) p.part[(int64_t)sl * p.rows + row] = HeadPart{m, s};
   if (MODE == HEAD_POW) *out = pack_bf16x2(z[0], z[1]);
   if (MODE == HEAD_EXP) *out = pack_exponents(t[0], t[1]);
 }
@@ -804,10 +817,10 @@ void k_head_join(HeadPanel p, int kind, int shift, double* lp, float* logp, Head
   m = ms[0][r];
 #pragma unroll
   for (int k = 1; k < kJoinWaves; ++k) m = fmaxf(m, ms[k][r]);
-  // sums relative to 2^m: every factor is a power of two
+  // sums relative to 2^M of the row: every factor is a power of two
   double s = 0;
   auto add = [&](const HeadPart& e, int64_t k) {
-    const int down = (int)fmaxf(e.m - m, -2000.f);   // (-2000 for a NaN: the sum shows it)
+    const int down = (int)relative_exponent(e.m, m);
     s += ldexp((double)e.s, down);
     if (shift && row < n) {
       const uint32_t d = down < -511 ? 511 : -down;
@@ -827,11 +840,14 @@ void k_head_join(HeadPanel p, int kind, int shift, double* lp, float* logp, Head
   s = 0;
 #pragma unroll
   for (int k = 0; k < kJoinWaves; ++k) s += ss[k][r];
-  // the target joins: both relative to 2^top
-  const double ty = zy * 1.4426950408889634074, top = fmax((double)m, ceil(ty));
-  const double out = m == -INFINITY ? 0.0 : exp2((double)m - top);
-  const double rest = m == -INFINITY ? 0.0 : s * out, all = rest + exp2(ty - top);
-  const double lse = (top + log2(all)) * 0.69314718055994530942;
+  // the target joins: both relative to the larger logit's exponential.  (From that logit
+  // itself, not from its exponent: lse of a far larger one is that float32, and the
+  // backward's exp(z - lse) is 1 there.)
+  const double top = fmax((double)m, zy);
+  const float off = slice_offset(m, slice_exponent(m));
+  const double out = m == -INFINITY ? 0.0 : exp((double)m - top) * exp2(-(double)off);
+  const double rest = m == -INFINITY ? 0.0 : s * out, all = rest + exp(zy - top);
+  const double lse = top + log(all);
   double l = zy - lse;
   HeadStat st{(float)lse, (float)(rest / all)};
   const double w = kind == HEAD_GRAD_MEAN ? -1.0 / *p.r.n : -1.0;
@@ -869,8 +885,8 @@ __global__ __launch_bounds__(1024) void k_head_loss(const int32_t* n, const doub
 
 // ------------------------------------------------------------------------ dz
 // In place, a thread 8 columns of 8 rows: HBM-bound (2048 x 128256: 224 us, 1.05 GB at
-// 4.7 TB/s).  dz = f 2^(M - R + t), the target's c; zeros in the rows up to a whole step
-// of dW.
+// 4.7 TB/s).  dz = f 2^(M - R + t), the target's c; zeros in the rows up to a whole step of
+// dW.
 constexpr int kDzRows = 8;
 __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
   const int n = panel_rows(p);
@@ -890,13 +906,13 @@ __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {
       const int64_t q = p.row0 + r0 + r;
       const HeadScale sc = p.r.scale[q];
       const float m = p.part[(c >> 7) * p.rows + r0 + r].m;
-      const float f = m == -INFINITY ? 0.f : sc.f, by = m == -INFINITY ? 0.f : m - sc.r;
+      const float by = relative_exponent(m, sc.m);
       float d[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t two = (&e[r].x)[k];
-        d[2 * k] = f * unpack_power(two & 0xffffu, by);
-        d[2 * k + 1] = f * unpack_power(two >> 16, by);
+        d[2 * k] = sc.f * unpack_power(two & 0xffffu, by);
+        d[2 * k + 1] = sc.f * unpack_power(two >> 16, by);
       }
       const int64_t rel = p.r.y[q] - c;
       if (rel >= 0 && rel < 8) {

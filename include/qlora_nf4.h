@@ -766,7 +766,8 @@ size_t qlora_head_workspace_bytes(const qlora_head* h, int32_t grads);
 
 /* Log-probabilities of the targets: logp float32 [rows].  stats (nullable)
  * float32 [rows][2] receives each row's log sum_v exp(z_v) and the target's
- * 1 - p (0, 0 without target) for the backward. */
+ * 1 - p (0, 0 without target) for the backward, whose p = exp(z - that) is as exact as
+ * its float32 step (2^-24 of it). */
 qlora_status qlora_head_logprobs(const qlora_head* h, float* logp, float* stats, void* ws,
                                  size_t ws_bytes, void* stream);
 
