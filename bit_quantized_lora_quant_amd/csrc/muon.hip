@@ -416,6 +416,18 @@ __device__ __forceinline__ void put_panel(double* x, const Panel<NT>& p, int lan
   __syncthreads();
 }
 
+// What U is multiplied by, from the trace of U U^T.  No square of a float32 value other
+// than 0 is lost in float64, so a trace of 0 is a zero matrix, whose result is 0 under
+// any eps (whose reciprocal need not be finite); else this is below 2^149.
+__device__ __forceinline__ double inverse_norm(double trace, double eps) {
+  // (fmax drops a NaN: then every product shows it)
+  return trace == 0. ? 0. : 1. / fmax(sqrt(trace), eps);
+}
+// Q / |U|; of a zero matrix 0, also where Q, powers of a then, is not finite.
+__device__ __forceinline__ double scaled(double q, double inv, double trace) {
+  return trace == 0. ? 0. : q * inv;
+}
+
 constexpr int poly_waves(int nt) { return nt < 4 ? 4 : nt; }
 template <int NT>
 struct PolyLds {
@@ -463,8 +475,7 @@ __device__ __forceinline__ void polynomial(const MuonHyper& h, PolyLds<NT>& l, c
   for (int r = lane; r < 16 * NT; r += 64) tr += x[r * (pitch + 1)];
 #pragma unroll
   for (int d = 32; d; d >>= 1) tr += __shfl_xor(tr, d);
-  const double norm = fmax(sqrt(tr), h.eps), inv = 1.0 / norm;
-  // (fmax drops a NaN: then every product shows it)
+  const double inv = inverse_norm(tr, h.eps);
   Panel<NT> G, Q;
 #pragma unroll
   for (int i = 0; i < NT; ++i)
@@ -498,7 +509,7 @@ __device__ __forceinline__ void polynomial(const MuonHyper& h, PolyLds<NT>& l, c
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) out[(4 * i + v) * 64] = Q.t[i][v] * inv;
+    for (int v = 0; v < 4; ++v) out[(4 * i + v) * 64] = scaled(Q.t[i][v], inv, tr);
 }
 
 template <int NT>
@@ -638,8 +649,7 @@ __global__ __launch_bounds__(kPoly64) void k_muon_poly64(MuonHyper h, MuonScratc
   double tr = g[lane * (kPitch + 1)];
 #pragma unroll
   for (int d = 32; d; d >>= 1) tr += __shfl_xor(tr, d);
-  const double norm = fmax(sqrt(tr), h.eps), inv = 1.0 / norm;
-  // (fmax drops a NaN: then every product shows it)
+  const double inv = inverse_norm(tr, h.eps);
   __syncthreads();
   for (int e = threadIdx.x; e < kSide * kSide; e += kPoly64)
     g[(e >> 6) * kPitch + (e & 63)] *= inv * inv;
@@ -658,8 +668,8 @@ __global__ __launch_bounds__(kPoly64) void k_muon_poly64(MuonHyper h, MuonScratc
   double* out = s.q + (size_t)t.q * 256 + wv * 256 * 2 + lane;
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    out[e * 64] = x[3][(4 * (8 * (wv & 1) + e) + (lane >> 4)) * kPitch + 16 * (wv >> 1) +
-                       (lane & 15)] * inv;
+    out[e * 64] = scaled(x[3][(4 * (8 * (wv & 1) + e) + (lane >> 4)) * kPitch + 16 * (wv >> 1) +
+                              (lane & 15)], inv, tr);
 }
 
 // --------------------------------------------------------------------- apply
