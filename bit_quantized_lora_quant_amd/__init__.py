@@ -6,6 +6,7 @@ memory and the current HIP stream, every step of the computation runs in the
 library's HIP kernels.  There is no CPU fallback: if the library is missing,
 every call raises.
 """
+import array
 import contextlib
 import ctypes
 import functools
@@ -866,6 +867,48 @@ def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_
     return out
 
 
+@functools.lru_cache(None)
+def _exchange():
+    """(function, table): the library's look at many tensors through the table of C
+    functions that this torch publishes (a DLPack exchange capsule), or None where it
+    publishes none."""
+    capsule = getattr(torch.Tensor, "__dlpack_c_exchange_api__", None)
+    if capsule is None:
+        return None
+    P, I64 = ctypes.c_void_p, ctypes.c_int64
+    pointer = ctypes.pythonapi.PyCapsule_GetPointer
+    pointer.restype, pointer.argtypes = P, [ctypes.py_object, ctypes.c_char_p]
+    table = pointer(capsule, b"dlpack_exchange_api")
+    lib()
+    look = ctypes.PyDLL(LIB_PATH).qlora_binding_layouts     # (keeps the interpreter's lock)
+    look.argtypes = [P, P, I64, P, P]
+    return (look, table) if look(table, None, 0, None, None) == 0 else None
+
+
+def _layouts(what, tensors, ids=None):
+    """The tensors' addresses as the bytes of int64's, and their types, devices, shapes
+    and strides as something to compare.  ids: array of their id()s."""
+    for t in set(map(type, tensors)):
+        _require(issubclass(t, torch.Tensor), what, "%s is no tensor", t.__name__)
+    n, exchange = len(tensors), _exchange()
+    if exchange is None:
+        return (array.array("q", map(torch.Tensor.data_ptr, tensors)).tobytes(),
+                [(x.dtype, x.get_device(), x.shape, x.stride()) for x in tensors])
+    if n == 0:
+        return b"", b""
+    if ids is None:
+        ids = array.array("q", map(id, tensors))
+    at, layout = bytearray(8 * n), bytearray(48 * n)
+    word = ctypes.c_char
+    look, table = exchange
+    try:
+        look(table, ids.buffer_info()[0], n, ctypes.addressof(word.from_buffer(at)),
+             ctypes.addressof(word.from_buffer(layout)))
+    except Exception as e:
+        raise QloraError(QLORA_ERR_INVALID_ARG, "%s: %s" % (what, e)) from e
+    return at, layout
+
+
 class MuonPlan:
     """The tensors of a qlora_muon_step and its workspace, checked and laid out
     once: a list of (param, grad, momentum, param_bf16 or None), matrices whose
@@ -897,8 +940,9 @@ class MuonPlan:
         self._own = [x for t in self._written for x in t if x is not None]
         self._grads = [t[1] for t in tensors]
         self._own_at = self._grads_at = None
-        self._own_layout, self._grads_layout = self._layout(self._own), self._layout(self._grads)
-        self._own_devices, self._grads_devices = self._devices(self._own), self._devices(self._grads)
+        self._own_ids = array.array("q", map(id, self._own))
+        self._own_layout = _layouts(what, self._own)[1]
+        self._grads_layout = _layouts(what, self._grads)[1]
         self._separate(what)
         self.ws, self._streams = None, set()
         if tensors:
@@ -914,16 +958,6 @@ class MuonPlan:
         """(param, grad, momentum, param_bf16) of each, with the last gradients."""
         return [(p, g, m, pb) for (p, m, pb), g in zip(self._written, self._grads)]
 
-    @staticmethod
-    def _layout(tensors):
-        # (whole lists at a time: a step's host time is as long as this)
-        return ([x.dtype for x in tensors], [x.shape for x in tensors],
-                list(map(torch.Tensor.stride, tensors)))
-
-    @staticmethod
-    def _devices(tensors):
-        return list(map(torch.Tensor.get_device, tensors))
-
     def _separate(self, what):
         _distinct(what, "a tensor to be written", self._own)
 
@@ -937,21 +971,20 @@ class MuonPlan:
             grads = list(grads)
             _require(len(grads) == len(self._grads), what, "as many gradients as tensors")
         other = "a tensor of another type, shape, stride or device than the plan's"
-        _require(self._layout(self._own) == self._own_layout, what, other)
-        at = list(map(torch.Tensor.data_ptr, self._own))
+        at, layout = _layouts(what, self._own, self._own_ids)
+        _require(layout == self._own_layout, what, other)
         if at != self._own_at:
-            _require(self._devices(self._own) == self._own_devices, what, other)
             self._separate(what)
             for a, (p, m, pb) in zip(self.array, self._written):
                 a.param, a.momentum = p.data_ptr(), m.data_ptr()
                 a.param_bf16 = None if pb is None else pb.data_ptr()
             self._own_at = at
-        _require(self._layout(grads) == self._grads_layout, what, other)
-        at = list(map(torch.Tensor.data_ptr, grads))
+        at, layout = _layouts(what, grads)
+        _require(layout == self._grads_layout, what, other)
         if at != self._grads_at:
-            _require(self._devices(grads) == self._grads_devices, what, other)
             words = torch.frombuffer(self.array, dtype=torch.int64).view(len(self.array), -1)
-            words[:, MuonTensor.grad.offset // 8] = torch.tensor(at, dtype=torch.int64)
+            words[:, MuonTensor.grad.offset // 8] = torch.frombuffer(bytearray(at),
+                                                                     dtype=torch.int64)
             self._grads_at = at
         self._grads = grads
 

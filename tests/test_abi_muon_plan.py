@@ -10,9 +10,12 @@ import bit_quantized_lora_quant_amd as q
 BF = torch.bfloat16
 
 
-@pytest.fixture
-def plan(monkeypatch):
-    """A plan of a wide and a tall matrix whose rows lie in wider ones, bound once."""
+@pytest.fixture(params=["torch's table", "one by one"])
+def plan(request, monkeypatch):
+    """A plan of a wide and a tall matrix whose rows lie in wider ones, bound once; its
+    tensors looked at through torch's table of functions or from Python."""
+    if request.param == "one by one":
+        monkeypatch.setattr(q, "_exchange", lambda: None)
     monkeypatch.setattr(q, "_on", lambda *a: contextlib.nullcontext())
     bufs = [torch.zeros(4096) for _ in range(6)] + [torch.zeros(4096, dtype=BF) for _ in range(2)]
     wide, tall = [(b[:16 * 40].view(16, 40)[:8, :20]) for b in bufs[0:6:2] + bufs[6:7]], \
@@ -68,3 +71,31 @@ def test_moved_memory_is_followed(plan):
         for a, (p, g, m, pb) in zip(plan.array, plan.tensors):
             assert (a.param, a.grad, a.momentum, a.param_bf16) == tuple(
                 t.data_ptr() for t in (p, g, m, pb))
+
+
+def test_what_is_no_matrix_is_refused(plan):
+    good = [t[1] for t in plan.tensors]
+    for bad in (None, 3, [1.0], good[0].unsqueeze(0), good[0][0], good[0].new_zeros(()),
+                good[0].to("meta"), torch.zeros((8, 20)).to_sparse()):
+        with pytest.raises((q.QloraError, NotImplementedError, RuntimeError)):
+            plan._bind("bind", [bad, good[1]])
+    plan._bind("bind", good)
+    assert [g.data_ptr() for g in good] == [a.grad for a in plan.array]
+
+
+def test_the_two_looks_agree():
+    """Both tell apart what is laid out differently, and nothing else."""
+    assert q._exchange() is not None
+    x = torch.zeros((12, 20))
+    some = [x, x.clone(), x[:, :10], x[:6], x.t(), x.double(), x.bool(), x.to(BF), x[::2], x[:, ::2],
+            torch.nn.Parameter(x.clone()), x[:0], x[:, :0]]
+    fast = [q._layouts("t", [t]) for t in some]
+    assert [int.from_bytes(a, "little") for a, _ in fast] == [t.data_ptr() for t in some]
+    key = [(t.dtype, t.device, t.shape, t.stride()) for t in some]
+    for i in range(len(some)):
+        for j in range(len(some)):
+            assert (fast[i][1] == fast[j][1]) == (key[i] == key[j]), (i, j)
+    at, layout = q._layouts("t", some)
+    assert at == b"".join(a for a, _ in fast) and layout == b"".join(b for _, b in fast)
+    with pytest.raises(q.QloraError):
+        q._layouts("t", [x, "no tensor"])
