@@ -887,13 +887,16 @@ def _exchange():
 
 def _layouts(what, tensors, ids=None):
     """The tensors' addresses as the bytes of int64's, and their types, devices, shapes
-    and strides as something to compare.  ids: array of their id()s."""
+    and strides (of dimensions longer than 1) as something to compare.  ids: array of
+    their id()s."""
     for t in set(map(type, tensors)):
         _require(issubclass(t, torch.Tensor), what, "%s is no tensor", t.__name__)
     n, exchange = len(tensors), _exchange()
     if exchange is None:
         return (array.array("q", map(torch.Tensor.data_ptr, tensors)).tobytes(),
-                [(x.dtype, x.get_device(), x.shape, x.stride()) for x in tensors])
+                [(x.dtype, x.get_device(), x.shape) +
+                 tuple(s if n > 1 and x.numel() else 0 for n, s in zip(x.shape, x.stride()))
+                 for x in tensors])
     if n == 0:
         return b"", b""
     if ids is None:

@@ -29,8 +29,8 @@ struct Table {                // DLPackExchangeAPI
 
 }  // namespace
 
-// at[i]: tensor i's address; layout[6 i ..]: its type, device, rows, columns, row and
-// column stride (-1 of all but a matrix).  table is torch's; with n == 0 whether it can
+// at[i]: tensor i's address; layout[6 i ..]: its type, device, rows, columns (-1 of all but
+// a matrix), row and column stride (0 where no two elements are that far apart).  table is torch's; with n == 0 whether it can
 // be used.  Called with the interpreter's lock held.  Returns 0 or -1 (exception set).
 extern "C" int qlora_binding_layouts(const void* table, void* const* objects, int64_t n,
                                      int64_t* at, int64_t* layout) {
@@ -47,6 +47,8 @@ extern "C" int qlora_binding_layouts(const void* table, void* const* objects, in
       l[2 + k] = v.ndim == 2 ? v.shape[k] : -1;
       l[4 + k] = v.ndim == 2 ? v.strides[k] : -1;
     }
+    if (l[2] <= 1 || l[3] == 0) l[4] = 0;   // of no meaning, and whatever it was given
+    if (l[3] <= 1 || l[2] == 0) l[5] = 0;
   }
   return 0;
 }

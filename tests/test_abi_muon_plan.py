@@ -99,3 +99,23 @@ def test_the_two_looks_agree():
     assert at == b"".join(a for a, _ in fast) and layout == b"".join(b for _, b in fast)
     with pytest.raises(q.QloraError):
         q._layouts("t", [x, "no tensor"])
+
+
+@pytest.mark.parametrize("shape,strides", [((1, 30), [(30, 1), (1, 1), (64, 1), (0, 1)]),
+                                           ((30, 1), [(1, 1), (1, 30), (1, 64), (1, 0)]),
+                                           ((1, 1), [(1, 1), (9, 5), (0, 0)]),
+                                           ((30, 1), [(4, 1), (4, 7)]),
+                                           ((0, 30), [(30, 1), (1, 1), (7, 3)]),
+                                           ((30, 0), [(1, 1), (30, 5), (0, 0)])])
+def test_strides_of_single_rows_and_columns(plan, shape, strides):
+    """The stride of a dimension of one (or no) element is no part of a layout."""
+    buf = torch.arange(256.)
+    of = lambda s: torch.as_strided(buf, shape, s)  # noqa: E731
+    p, m = torch.zeros(shape), torch.zeros(shape)
+    one = q.MuonPlan([(p, of(strides[0]), m, None)])
+    for s in strides[::-1]:
+        one._bind("bind", [of(s)])
+        assert one.array[0].grad == of(s).data_ptr()
+    if shape[0] > 1 and shape[1] == 1:          # this one's row stride counts
+        with pytest.raises(q.QloraError, match="stride"):
+            one._bind("bind", [of((strides[0][0] + 1, 1))])
