@@ -115,7 +115,7 @@ def test_strides_of_single_rows_and_columns(plan, shape, strides):
     one = q.MuonPlan([(p, of(strides[0]), m, None)])
     for s in strides[::-1]:
         one._bind("bind", [of(s)])
-        assert one.array[0].grad == of(s).data_ptr()
+        assert (one.array[0].grad or 0) == of(s).data_ptr()       # (0 reads as None)
     if shape[0] > 1 and shape[1] == 1:          # this one's row stride counts
         with pytest.raises(q.QloraError, match="stride"):
             one._bind("bind", [of((strides[0][0] + 1, 1))])
