@@ -845,11 +845,11 @@ def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_
     flat, shapes, code = [], [], {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
     for m, o in zip(matrices, out):
         _require(m.dim() == 2 and m.dtype in code, what, "each must be a float32 or bf16 matrix")
+        _require(o.dtype == m.dtype and o.shape == m.shape, what,
+                 "an output must be of its matrix's type and shape")
         (rows, cols), (ld, one), (ldo, oneo) = m.shape, m.stride(), o.stride()
         _require((one == 1 or cols <= 1) and (oneo == 1 or cols <= 1), what,
                  "each must have dense rows")
-        _require(o.dtype == m.dtype and o.shape == m.shape, what,
-                 "an output must be of its matrix's type and shape")
         if rows <= 1:
             ld = ldo = max(1, cols)
         flat += (m.data_ptr(), o.data_ptr(), rows, cols, ld, ldo, code[m.dtype])
