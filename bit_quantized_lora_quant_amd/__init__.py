@@ -7,6 +7,7 @@ library's HIP kernels.  There is no CPU fallback: if the library is missing,
 every call raises.
 """
 import array
+import collections
 import contextlib
 import ctypes
 import functools
@@ -830,7 +831,7 @@ def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_
                         eps: float = 1e-7, ws=None):
     """Each float32 or bf16 matrix (shorter side <= 128, rows of any stride) moved
     towards singular values of 1 by Newton-Schulz steps.  Returns the list of
-    results, in `out` (which may be the matrices) or new tensors."""
+    results, in `out` (which may be the matrices, each its own) or new tensors."""
     what = "qlora_orthogonalize"
     matrices = list(matrices)
     ns = _newton_schulz(what, coefficients, steps, eps)
@@ -855,6 +856,12 @@ def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_
         flat += (m.data_ptr(), o.data_ptr(), rows, cols, ld, ldo, code[m.dtype])
         shapes.append((rows, cols))
     _distinct(what, "an output", out)
+    # (an output may be its own matrix: no other is read where it is written)
+    at, to = [m.data_ptr() for m in matrices], [o.data_ptr() for o in out]
+    if not set(at).isdisjoint(to):
+        reads = collections.Counter(at)
+        for m, i, o in zip(matrices, at, to):
+            _require(not m.numel() or reads[o] == (i == o), what, "an output is another matrix")
     if ws is None:
         ws = workspace(qlora_muon_workspace_bytes(shapes), matrices[0].device)
     with _on(what, matrices[0], ws):
