@@ -923,7 +923,7 @@ class MuonPlan:
     """The tensors of a qlora_muon_step and its workspace, checked and laid out
     once: a list of (param, grad, momentum, param_bf16 or None), matrices whose
     shorter side is <= 128, rows of any stride; param and momentum float32, grad
-    float32 or bf16; no tensor but a grad twice.  The plan holds the tensors and
+    float32 or bf16; no tensor twice but a grad among the grads.  The plan holds the tensors and
     finds their memory anew each step, and refuses one whose type, shape or stride
     is no longer what it was; gradients that are other tensors every time go to the
     step itself.  Steps that share a plan must be ordered on one stream,
@@ -953,7 +953,7 @@ class MuonPlan:
         self._own_ids = array.array("q", map(id, self._own))
         self._own_layout = _layouts(what, self._own)[1]
         self._grads_layout = _layouts(what, self._grads)[1]
-        self._separate(what)
+        self._separate(what, *(_layouts(what, x)[0] for x in (self._own, self._grads)))
         self.ws, self._streams = None, set()
         if tensors:
             with _on(what, *self._own, *self._grads):
@@ -968,8 +968,15 @@ class MuonPlan:
         """(param, grad, momentum, param_bf16) of each, with the last gradients."""
         return [(p, g, m, pb) for (p, m, pb), g in zip(self._written, self._grads)]
 
-    def _separate(self, what):
-        _distinct(what, "a tensor to be written", self._own)
+    @staticmethod
+    def _separate(what, own_at, grads_at):
+        own, grads = array.array("q"), array.array("q")
+        own.frombytes(own_at)
+        grads.frombytes(grads_at)
+        own = [a for a in own if a]                # (without elements: nowhere)
+        places = set(own)
+        _require(len(places) == len(own), what, "a tensor to be written is given twice")
+        _require(places.isdisjoint(grads), what, "a gradient is a tensor to be written")
 
     def _bind(self, what, grads):
         """The tensors' addresses as they are now.  Their layouts are looked at every step:
@@ -981,16 +988,17 @@ class MuonPlan:
             grads = list(grads)
             _require(len(grads) == len(self._grads), what, "as many gradients as tensors")
         other = "a tensor of another type, shape, stride or device than the plan's"
-        at, layout = _layouts(what, self._own, self._own_ids)
+        own_at, layout = _layouts(what, self._own, self._own_ids)
         _require(layout == self._own_layout, what, other)
-        if at != self._own_at:
-            self._separate(what)
+        at, layout = _layouts(what, grads)
+        _require(layout == self._grads_layout, what, other)
+        if own_at != self._own_at or at != self._grads_at:
+            self._separate(what, own_at, at)
+        if own_at != self._own_at:
             for a, (p, m, pb) in zip(self.array, self._written):
                 a.param, a.momentum = p.data_ptr(), m.data_ptr()
                 a.param_bf16 = None if pb is None else pb.data_ptr()
-            self._own_at = at
-        at, layout = _layouts(what, grads)
-        _require(layout == self._grads_layout, what, other)
+            self._own_at = own_at
         if at != self._grads_at:
             words = torch.frombuffer(self.array, dtype=torch.int64).view(len(self.array), -1)
             words[:, MuonTensor.grad.offset // 8] = torch.frombuffer(bytearray(at),
