@@ -884,8 +884,8 @@ __global__ __launch_bounds__(1024) void k_head_loss(const int32_t* n, const doub
 }
 
 // ------------------------------------------------------------------------ dz
-// In place, a thread 8 columns of 8 rows: HBM-bound (2048 x 128256: 224 us, 1.05 GB at
-// 4.7 TB/s).  dz = f 2^(M - R + t), the target's c; zeros in the rows up to a whole step of
+// In place, a thread 8 columns of 8 rows: HBM-bound (2048 x 128256: 192 us, 1.05 GB at
+// 5.5 TB/s).  dz = f 2^(M - R + t), the target's c; zeros in the rows up to a whole step of
 // dW.
 constexpr int kDzRows = 8;
 __global__ __launch_bounds__(kThreads) void k_head_dz(HeadPanel p) {

@@ -467,8 +467,9 @@ qlora_status qlora_adamw8_step(const qlora_adamw_hparams* h, int64_t step,
  * (the products on the shorter side).  An adapter's shorter side is its rank,
  * <= 128: the steps run on its product matrix, in float64, and U is read once
  * more to be multiplied by their polynomial, also in float64.  The result is
- * rounded once (to float32 in a step).  Orders are fixed: results are identical
- * run to run.  A NaN or an infinity in U makes the whole result NaN. */
+ * rounded to float32, and to bf16 from there for a bf16 matrix.  Orders are fixed:
+ * results are identical run to run.  A NaN or an infinity in U makes the whole
+ * result NaN. */
 typedef struct {
   double a, b, c;      /* 3.4445, -4.7750, 2.0315 are the usual ones */
   double eps;          /* > 0; usually 1e-7 */
