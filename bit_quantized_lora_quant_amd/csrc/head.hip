@@ -1061,46 +1061,63 @@ __global__ __launch_bounds__(kThreads) void k_head_dh_sum(HeadPanel p, int TN, i
 // A vocabulary row's gradient is often its targets' and little else, so its dz's
 // rounding to bf16 would be as large as the output's own (2.6e-3 of dW's norm against
 // 1.7e-3), and targets of one weight and small p all round to the same side (of 1020
-// rows' mean by 2^-8).  What it leaves out is added in float32, rows in order.  A
-// workgroup per packed row and 2048 columns, at work where that row is its target's
-// last: it looks through the panel's labels for the others, and adds what it has found
-// where its list has no room for the next 256.  (A chain of loads for a label of very
-// many rows: 1000 and 2048 rows of one at D = 4096 take 100 and 200 us.)
+// rows' mean by 2^-8).  What it leaves out is added in float32.  A workgroup per packed
+// row (at work where that row is its target's last) or, if those are fewer, per
+// vocabulary entry, and some columns: it looks through the panel's labels for the
+// target's rows, and adds what it has found where its list has no room for as many
+// labels as it has threads.  A wave adds 512 columns of every WAYS-th row of the list:
+// of all, where labels have few rows (200 rows of one of 32000 cost nothing that shows;
+// 2048 of one, a chain of loads, 200 us at D = 4096); of every sixteenth, where the panel
+// has kRestMany rows a vocabulary entry or more (8192 rows' whole call at D = 4096: 2
+// entries 312 us, 686 with all; 30 entries 232 and 268; 100 entries 246 and 236).
 __device__ __forceinline__ int64_t rest_slot(const HeadPanel& p, int64_t v, int64_t q) {
   return p.rows < p.vocab ? q - p.row0 : v;
 }
-constexpr int kFound = 512;
-__global__ __launch_bounds__(kThreads) void k_head_rest(HeadPanel p, float* rest) {
-  __shared__ int found[kFound];
-  __shared__ float off[kFound];
-  __shared__ int wave_count[4];
+constexpr int kRestMany = 128;
+template <int WAYS, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_head_rest(HeadPanel p, float* rest) {
+  constexpr int kWaves = THREADS / 64, kList = 2 * THREADS, kColumns = kWaves / WAYS * 512;
+  __shared__ int found[kList];
+  __shared__ float off[kList];
+  __shared__ int wave_count[kWaves];
+  __shared__ __attribute__((aligned(16))) float sums[WAYS > 1 ? kWaves : 1][WAYS > 1 ? 512 : 1];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int n = panel_rows(p), self = blockIdx.x;
-  if (self >= n) return;
-  const int y = p.r.y[p.row0 + self];
-  if (y < 0 || p.r.last[y] != p.row0 + self) return;
-  const int col = (int)(blockIdx.y * kThreads + tid) * 8;
+  const int n = panel_rows(p);
+  int self, y;                           // the target and the last row with it
+  if (p.rows < p.vocab) {
+    self = blockIdx.x;
+    if (self >= n) return;
+    y = p.r.y[p.row0 + self];
+    if (y < 0 || p.r.last[y] != p.row0 + self) return;
+  } else {
+    y = blockIdx.x;
+    self = (int)(p.r.last[y] - p.row0);
+    if (self < 0) return;                // (of an earlier panel, or none)
+  }
+  const int way = wv % WAYS, col = (int)blockIdx.y * kColumns + wv / WAYS * 512 + lane * 8;
   float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   int have = 0;
-  for (int t0 = 0; t0 <= self; t0 += kThreads) {
+  for (int t0 = 0; t0 <= self; t0 += THREADS) {
     const int t = t0 + tid;
     const bool hit = t <= self && p.r.y[p.row0 + t] == y;
     const uint64_t m = __builtin_amdgcn_ballot_w64(hit);
     if (lane == 0) wave_count[wv] = __popcll(m);
     __syncthreads();
     int at = have + __popcll(m & ((1ull << lane) - 1));
-    for (int w = 0; w < wv; ++w) at += wave_count[w];
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wv) at += wave_count[w];
+      have += wave_count[w];
+    }
     if (hit) {
       const float c = p.r.scale[p.row0 + t].c;
       found[at] = t;
       off[at] = c - bf16_to_f32((uint16_t)pack_bf16x2(c, 0.f));
     }
-    have += wave_count[0] + wave_count[1] + wave_count[2] + wave_count[3];
     __syncthreads();
-    if (have + kThreads <= kFound && t0 + kThreads <= self) continue;
+    if (have + THREADS <= kList && t0 + THREADS <= self) continue;
     if (col < p.dim) {
 #pragma unroll 8
-      for (int k = 0; k < have; ++k) {
+      for (int k = way; k < have; k += WAYS) {
         const uint4 h =
             *reinterpret_cast<const uint4*>(p.r.h + (p.row0 + found[k]) * p.dim + col);
 #pragma unroll
@@ -1110,6 +1127,16 @@ __global__ __launch_bounds__(kThreads) void k_head_rest(HeadPanel p, float* rest
     }
     have = 0;
     __syncthreads();
+  }
+  if constexpr (WAYS > 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[wv][lane + 64 * e] = o[e];
+    __syncthreads();
+    if (way > 0) return;
+#pragma unroll
+    for (int w = 1; w < WAYS; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += sums[wv + w][lane + 64 * e];
   }
   if (col >= p.dim) return;
   float4* to =
@@ -1386,8 +1413,12 @@ hipError_t launch_head_dh(const HeadPanel& p, int tile, int pow, float* part, ui
 }
 
 hipError_t launch_head_rest(const HeadPanel& p, float* rest, hipStream_t s) {
-  const dim3 grid((unsigned)p.rows, (unsigned)ceil_div(p.dim, kThreads * 8));
-  return launch_kernel(k_head_rest, grid, dim3(kThreads), s, p, rest);
+  const unsigned slots = (unsigned)head_slots(p.rows, p.vocab);
+  return p.rows >= kRestMany * p.vocab
+             ? launch_kernel(k_head_rest<16, 1024>, dim3(slots, (unsigned)ceil_div(p.dim, 512)),
+                             dim3(1024), s, p, rest)
+             : launch_kernel(k_head_rest<1, kThreads>, dim3(slots, (unsigned)ceil_div(p.dim, 2048)),
+                             dim3(kThreads), s, p, rest);
 }
 
 size_t head_dw_floats(int64_t rows, int dim, int64_t vocab) {

@@ -117,3 +117,27 @@ def test_targets_that_round_alike_over_panels():
     o = q.qlora_head_cross_entropy(h, W, y, need_dweight=True)
     err = (o.dweight[7].double() - ref).abs()
     assert bool((err <= bound).all()), float((err / bound).max())
+
+
+@pytest.mark.parametrize("T,D,V", [(130, 64, 2), (1020, 192, 12), (1500, 576, 16), (1020, 1088, 40),
+                                   (5000, 128, 3), (4200, 2112, 2)])
+@pytest.mark.parametrize("ignored", [0.0, 0.6])
+def test_few_entries_of_many_rows(T, D, V, ignored):
+    """A target's rows by the thousand, of which every one's rounding is made up for."""
+    say("few entries T=%d D=%d V=%d ignored=%g" % (T, D, V, ignored))
+    h, W, y = _inputs(T + V, T, D, V, ignored=ignored, sharp=0.2)
+    h = torch.where((y >= 0)[:, None], h, float("nan"))
+    n = int((y >= 0).sum())
+    w = torch.full((T,), -1.0 / n, device=DEV)
+    o = q.qlora_head_cross_entropy(h, W, y, need_dweight=True)
+    _, stats = q.qlora_head_logprobs(h, W, y, return_stats=True)
+    dw = q.qlora_head_logprobs_bwd(h, W, y, stats, w, need_dhidden=False, need_dweight=True)[1]
+    for v in range(0, V, max(1, V // 5)):
+        ref, own, other = _row_of_dw(h, W, y, w, v)
+        bound = ref.abs() * 2.0 ** -8 + own * (T * 2.0 ** -23 + _logp_tol(D, V)) + \
+            other * (2.0 ** -8 + 2.0 ** -11 + T * 2.0 ** -24 + _logp_tol(D, V))
+        for got in (o.dweight, dw):
+            err = (got[v].double() - ref).abs()
+            assert bool((err <= bound).all()), (v, float((err / bound).max()))
+    again = q.qlora_head_cross_entropy(h, W, y, need_dweight=True)
+    assert torch.equal(again.dweight, o.dweight)
