@@ -883,8 +883,8 @@ def _exchange():
     if capsule is None:
         return None
     P, I64 = ctypes.c_void_p, ctypes.c_int64
-    pointer = ctypes.pythonapi.PyCapsule_GetPointer
-    pointer.restype, pointer.argtypes = P, [ctypes.py_object, ctypes.c_char_p]
+    pointer = ctypes.PYFUNCTYPE(P, ctypes.py_object, ctypes.c_char_p)(
+        ("PyCapsule_GetPointer", ctypes.pythonapi))
     table = pointer(capsule, b"dlpack_exchange_api")
     lib()
     look = ctypes.PyDLL(LIB_PATH).qlora_binding_layouts     # (keeps the interpreter's lock)
