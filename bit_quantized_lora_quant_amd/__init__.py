@@ -821,12 +821,6 @@ def _newton_schulz(what, coefficients, steps, eps):
     return NewtonSchulz(*coefficients, eps, steps, 0)
 
 
-def _distinct(what, name, tensors):
-    """No two of the tensors begin at one place: workgroups of both would write it."""
-    at = [t.data_ptr() for t in tensors if t.numel()]
-    _require(len(set(at)) == len(at), what, "%s is given twice", name)
-
-
 def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_SCHULZ,
                         eps: float = 1e-7, ws=None):
     """Each float32 or bf16 matrix (shorter side <= 128, rows of any stride) moved
@@ -843,7 +837,8 @@ def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_
         return out
     # qlora_ortho_matrix as seven int64 (a step of many small adapters is as long as
     # this loop)
-    flat, shapes, code = [], [], {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+    flat, shapes, read, written = [], [], [], []
+    code = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
     for m, o in zip(matrices, out):
         _require(m.dim() == 2 and m.dtype in code, what, "each must be a float32 or bf16 matrix")
         _require(o.dtype == m.dtype and o.shape == m.shape, what,
@@ -853,15 +848,19 @@ def qlora_orthogonalize(matrices, out=None, steps: int = 5, coefficients=NEWTON_
                  "each must have dense rows")
         if rows <= 1:
             ld = ldo = max(1, cols)
-        flat += (m.data_ptr(), o.data_ptr(), rows, cols, ld, ldo, code[m.dtype])
+        i, to = m.data_ptr(), o.data_ptr()
+        flat += (i, to, rows, cols, ld, ldo, code[m.dtype])
+        if rows and cols:
+            read.append(i)
+            written.append(to)
         shapes.append((rows, cols))
-    _distinct(what, "an output", out)
-    # (an output may be its own matrix: no other is read where it is written)
-    at, to = [m.data_ptr() for m in matrices], [o.data_ptr() for o in out]
-    if not set(at).isdisjoint(to):
-        reads = collections.Counter(at)
-        for m, i, o in zip(matrices, at, to):
-            _require(not m.numel() or reads[o] == (i == o), what, "an output is another matrix")
+    places = set(written)
+    _require(len(places) == len(written), what, "an output is given twice")
+    if not places.isdisjoint(read):
+        # (an output may be its own matrix: no other is read where it is written)
+        reads = collections.Counter(read)
+        _require(all(reads[o] == (i == o) for i, o in zip(read, written)), what,
+                 "an output is another matrix")
     if ws is None:
         ws = workspace(qlora_muon_workspace_bytes(shapes), matrices[0].device)
     with _on(what, matrices[0], ws):
